@@ -419,6 +419,139 @@ int dsa_forward_host(const dsa_problem *p, const dsa_seqs *seqs, const dsa_host_
                      size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Speculative decoding over a served latent cache (the pages have no
+ * counterpart to these four entry points): the heads' norm and rotation at a
+ * draft tree's positions, the cache written (and quantised) and read back by
+ * token position, and the attention of the tree's nodes over it.
+ * ---------------------------------------------------------------------- */
+
+/* Where a sequence's tokens sit in a cache cut into pages of page_size rows:
+ * token s of sequence b is row block_table[b * ld_table + s / page_size] *
+ * page_size + s % page_size.  Wherever an entry point takes a `pages` pointer,
+ * NULL means a contiguous cache: token s of sequence b is row cu_k[b] + s.
+ * With pages, cu_k gives only the sequences' lengths.  Entries of tokens that
+ * a call does not touch are not read.  An entry outside 0 .. n_pages - 1 (e.g.
+ * -1) names no page: nothing is written there, it reads as zeros, and the
+ * attention masks its tokens. */
+typedef struct dsa_pages {
+    const int32_t *block_table;   /* device [B, ld_table] */
+    int64_t ld_table;             /* entries per sequence */
+    int32_t page_size;            /* rows of a page: a multiple of 16 */
+    int32_t n_pages;              /* pages of the cache: n_pages * page_size <= rows */
+} dsa_pages;
+
+/* A latent cache.  The storage type is DSA_F32 or DSA_BF16 values, or DSA_E4M3:
+ * codes with one power-of-two scale per 128 values (the block recipe of
+ * dsa_quant_e4m3_ue8m0) and bf16 rotary keys.  Rows start 16-byte aligned
+ * (base and stride). */
+typedef struct dsa_latent_cache {
+    void *kv;                     /* [rows, ld_kv]: d_c values or codes per row */
+    int64_t ld_kv;                /* elements (bytes for E4M3) */
+    float *kv_scale;              /* E4M3: [rows, d_c / 128]; else NULL */
+    void *k_pe;                   /* [rows, ld_pe]: d_r rotary key values per row (may lie inside kv's rows) */
+    int64_t ld_pe;                /* elements */
+    int32_t dtype;                /* DSA_F32, DSA_BF16 or DSA_E4M3 */
+    int64_t rows;                 /* rows of every array, < 2^31 - 64 */
+} dsa_latent_cache;
+
+/* Writes the new tokens' latent rows and rotary keys into the cache, quantising
+ * them on the way when it holds E4M3.  Row r = cu_q[b] + t of c_kv and k_pe
+ * becomes token start_pos[b] + t of sequence b; every other row of the cache
+ * stays as it was.
+ *   c_kv   [sum T, ld_c] of x_dtype (DSA_F32 or DSA_BF16), d_c values per row
+ *   k_pe   [sum T, ld_x] of x_dtype, d_r values per row (NULL when d_r = 0)
+ * Values are rounded once, to nearest even; a DSA_F32 cache holds bf16 inputs
+ * exactly.  E4M3 codes and scales are those that dsa_quant_e4m3_ue8m0 gives for
+ * the same values; Inf and NaN are not supported there.  Inputs must not
+ * overlap the cache.  Tokens that share a row (two sequences with one page)
+ * leave that row unspecified.
+ * Errors: DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED (d_c > 1024, d_r > 128, E4M3
+ * with d_c not a multiple of 128), DSA_ERR_CUDA. */
+int dsa_latent_cache_write(const void *c_kv, int64_t ld_c, const void *k_pe, int64_t ld_x, int x_dtype, int d_c, int d_r,
+                           const dsa_latent_cache *cache, const dsa_seqs *seqs, const dsa_pages *pages, void *stream);
+
+/* Reads tokens of the cache back as dense rows, dequantised.  Row r = cu_q[b] + t
+ * is token pos[r] of sequence b, or start_pos[b] + t when pos is NULL; a pos
+ * outside 0 .. S_b - 1 gives a row of zeros.  The same token may be read more
+ * than once.
+ *   pos    device [sum T] int32, or NULL
+ *   c_kv   out [sum T, ld_c] of out_dtype (DSA_F32 or DSA_BF16), d_c values per row
+ *   k_pe   out [sum T, ld_x] of out_dtype, d_r values per row (NULL when d_r = 0)
+ * code * scale is exact in both types unless it leaves the type's normal range.
+ * Outputs must not overlap the cache.
+ * Errors: as dsa_latent_cache_write. */
+int dsa_latent_cache_read(const dsa_latent_cache *cache, int d_c, int d_r, const dsa_seqs *seqs, const dsa_pages *pages,
+                          const int32_t *pos, void *c_kv, int64_t ld_c, void *k_pe, int64_t ld_x, int out_dtype,
+                          void *stream);
+
+/* Attention of drafted tokens over the cache, in absorbed form.  The T_b query
+ * rows of sequence b are the nodes of a tree whose root is token start_pos[b] - 1;
+ * node j's key is token start_pos[b] + j of the cache (written there
+ * beforehand).  A node sees every token before start_pos[b] and the nodes whose
+ * bit its mask sets (its ancestors and itself):
+ *   z[r,h,s] = softmax_scale (q~[r,h] . c[s] + q_pe[r,h] . k_pe[s]),  q~ = q_nope W_UK
+ *   out[r,h] = (sum_s softmax_s(z) c[s]) W_UV,  lse = log sum_s exp(z)
+ *   q_nope, q_pe, W_UK, W_UV, out, lse   as in dsa_sparse_mla_fwd (dense, dtype)
+ *   tree_mask   device [sum T, mask_words] 64-bit words: bit j % 64 of word j / 64
+ *               of a row is node j of the row's own sequence (bits of nodes >= T_b
+ *               are ignored; T_b <= 64 mask_words); NULL: node t sees nodes 0 .. t
+ *               (a chain: one token, or a prompt chunk)
+ * A row that sees nothing gets out = 0, lse = -inf.  What a row does not see never
+ * reaches it, whatever its bits (stale rows, Inf, NaN); visible Inf and NaN are
+ * not supported.  Contiguous or paged cache (`pages`), of dtype's own type, or
+ * E4M3 with dtype DSA_BF16.
+ * Two kernels: tensor cores for bf16 at d_n = 128, d_r = 64, d_c = 512, d_v = 128
+ * and any H; a generic one for everything else within the limits of
+ * dsa_sparse_mla_fwd (E4M3: d_c a multiple of 128).
+ * All pointers 16-byte aligned; workspace as in dsa_sparse_mla_fwd, its size
+ * depends on the sequences (calls captured in graphs that may run at the same
+ * time need workspaces of their own).
+ * Errors: DSA_ERR_INVALID_ARG, DSA_ERR_WORKSPACE, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA. */
+size_t dsa_tree_mla_workspace_size(int dtype, int H, int d_n, int d_r, int d_c, int d_v, const dsa_seqs *seqs);
+int dsa_tree_mla_fwd(const void *q_nope, const void *q_pe, int dtype, const dsa_latent_cache *cache, const void *W_UK,
+                     const void *W_UV, int H, int d_n, int d_r, int d_c, int d_v, const uint64_t *tree_mask,
+                     int mask_words, const dsa_seqs *seqs, const dsa_pages *pages, float softmax_scale, void *out,
+                     float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/* The heads of one tensor for dsa_head_norm_rope: head h of row r starts at
+ * x + r * ld_x + h * hd_x (elements), and likewise for y and y_pe. */
+typedef struct dsa_heads {
+    const void *x;
+    int64_t ld_x, hd_x;
+    int32_t n_heads;              /* 0: none (everything else is then ignored) */
+    int32_t norm;                 /* DSA_NORM_* */
+    const float *gain, *bias;     /* [D] fp32, NULL: 1 and 0 */
+    void *y;                      /* all D dims, or with y_pe the D - d_r unrotated ones */
+    int64_t ld_y, hd_y;
+    void *y_pe;                   /* the d_r rotated dims, or NULL: they stay in their place in y */
+    int64_t ld_pe, hd_pe;
+} dsa_heads;
+#define DSA_NORM_NONE  0
+#define DSA_NORM_RMS   1          /* x / sqrt(mean x^2 + eps) * gain */
+#define DSA_NORM_LAYER 2          /* (x - mean) / sqrt(var + eps) * gain + bias (biased variance) */
+#define DSA_ROPE_PAIRS  0         /* pair (2i, 2i+1) -> dims i and d_r/2 + i (the order the caches hold) */
+#define DSA_ROPE_HALVES 1         /* pair (i, d_r/2 + i) stays in place */
+
+/* Norms every head of the queries q and keys k and rotates its d_r rotary dims to
+ * the row's position, in one pass: (a, b) -> (a cos_i - b sin_i, a sin_i + b cos_i)
+ * for pair i.  The rotary dims are the last d_r of the D, or the first with
+ * rope_first.  Norm and rotation in fp32, rounded once to y_dtype.
+ *   q, k        either may be NULL (or have n_heads 0)
+ *   x_dtype, y_dtype   DSA_F32 or DSA_BF16
+ *   rope_cos, rope_sin [n_pos, d_r / 2] fp32
+ *   pos         device [sum T] int32 positions (a draft node's start + depth), or
+ *               NULL: start_pos[b] + t.  An entry outside 0 .. n_pos - 1 leaves
+ *               its row unrotated (padding)
+ * y may be x itself (same address, strides and type, y_pe NULL); otherwise
+ * outputs overlap neither inputs nor each other.
+ * Errors: DSA_ERR_INVALID_ARG (odd d_r, d_r > D, a position that start_pos gives
+ * outside the tables, y_pe with d_r = 0), DSA_ERR_UNSUPPORTED (D > 512, dtype,
+ * norm or rope of another kind), DSA_ERR_CUDA. */
+int dsa_head_norm_rope(const dsa_heads *q, const dsa_heads *k, int x_dtype, int y_dtype, int D, int d_r, int rope_first,
+                       int rope, float eps, const float *rope_cos, const float *rope_sin, int n_pos,
+                       const int32_t *pos, const dsa_seqs *seqs, void *stream);
+
+/* ------------------------------------------------------------------------
  * Status and diagnostics.
  * ---------------------------------------------------------------------- */
 /* Human-readable name of a dsa_status. */
@@ -498,6 +631,12 @@ int dsa_set_stage_events(void *const *events, int n_events);
 #define DSA_KERNEL_PROLOGUE     (1u << 13)
 #define DSA_KERNEL_INDEXER_TOPK (1u << 14)  /* the indexer launch also selected the top-k (fused) */
 #define DSA_KERNEL_APPEND       (1u << 15)  /* dsa_forward_host put staged cache rows in place */
+#define DSA_KERNEL_CACHE_WRITE  (1u << 16)
+#define DSA_KERNEL_CACHE_READ   (1u << 17)
+#define DSA_KERNEL_TREE_SIMT    (1u << 18)
+#define DSA_KERNEL_TREE_TC      (1u << 19)
+#define DSA_KERNEL_TREE_COMBINE (1u << 20)
+#define DSA_KERNEL_HEAD_NORM    (1u << 21)
 
 #ifdef __cplusplus
 }

@@ -16,8 +16,11 @@ KERNEL_BITS = {
     "quant": 1 << 0, "indexer_simt": 1 << 1, "indexer_tc": 1 << 2, "indexer_fp8": 1 << 3, "topk": 1 << 4,
     "absorb_simt": 1 << 5, "absorb_tc": 1 << 6, "mla_simt": 1 << 7, "mla_tc": 1 << 8, "combine": 1 << 9,
     "selftest": 1 << 10, "dense_idx": 1 << 11, "gemm_tc": 1 << 12, "prologue": 1 << 13,
-    "indexer_topk": 1 << 14, "append": 1 << 15,
+    "indexer_topk": 1 << 14, "append": 1 << 15, "cache_write": 1 << 16, "cache_read": 1 << 17, "tree_simt": 1 << 18,
+    "tree_tc": 1 << 19, "tree_combine": 1 << 20, "head_norm": 1 << 21,
 }
+DSA_NORM_NONE, DSA_NORM_RMS, DSA_NORM_LAYER = range(3)
+DSA_ROPE_PAIRS, DSA_ROPE_HALVES = range(2)
 
 
 class dsa_seqs(ctypes.Structure):
@@ -52,10 +55,32 @@ class dsa_host_io(ctypes.Structure):
     ]
 
 
+class dsa_pages(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32)]
+
+
+class dsa_latent_cache(ctypes.Structure):
+    _fields_ = [
+        ("kv", ctypes.c_void_p), ("ld_kv", ctypes.c_int64), ("kv_scale", ctypes.c_void_p), ("k_pe", ctypes.c_void_p),
+        ("ld_pe", ctypes.c_int64), ("dtype", ctypes.c_int32), ("rows", ctypes.c_int64),
+    ]
+
+
+class dsa_heads(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("hd_x", ctypes.c_int64), ("n_heads", ctypes.c_int32),
+        ("norm", ctypes.c_int32), ("gain", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64), ("hd_y", ctypes.c_int64),
+        ("y_pe", ctypes.c_void_p), ("ld_pe", ctypes.c_int64), ("hd_pe", ctypes.c_int64),
+    ]
+
+
 # (name, restype, argtypes) of every exported function
 P, I, I64, F, SZ, U32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint32
 SEQS = ctypes.POINTER(dsa_seqs)
 PROB = ctypes.POINTER(dsa_problem)
+CACHE, PAGES, HEADS = ctypes.POINTER(dsa_latent_cache), ctypes.POINTER(dsa_pages), ctypes.POINTER(dsa_heads)
 SIGNATURES = [
     ("dsa_quant_e4m3_ue8m0", I, [P, I, I64, P, P, P]),
     ("dsa_indexer_scores", I, [P, P, P, P, I, P, I, I, SEQS, P, I64, P]),
@@ -70,6 +95,11 @@ SIGNATURES = [
     ("dsa_forward_workspace_size", SZ, [PROB, SEQS]),
     ("dsa_forward", I, [PROB, SEQS, P, SZ, P]),
     ("dsa_forward_host", I, [PROB, SEQS, ctypes.POINTER(dsa_host_io), P, SZ, P]),
+    ("dsa_latent_cache_write", I, [P, I64, P, I64, I, I, I, CACHE, SEQS, PAGES, P]),
+    ("dsa_latent_cache_read", I, [CACHE, I, I, SEQS, PAGES, P, P, I64, P, I64, I, P]),
+    ("dsa_tree_mla_workspace_size", SZ, [I, I, I, I, I, I, SEQS]),
+    ("dsa_tree_mla_fwd", I, [P, P, I, CACHE, P, P, I, I, I, I, I, P, I, SEQS, PAGES, F, P, P, P, SZ, P]),
+    ("dsa_head_norm_rope", I, [HEADS, HEADS, I, I, I, I, I, I, F, P, P, I, P, SEQS, P]),
     ("dsa_status_string", ctypes.c_char_p, [I]),
     ("dsa_last_cuda_error", I, []),
     ("dsa_check_device_error", I, [P, ctypes.POINTER(ctypes.c_int)]),

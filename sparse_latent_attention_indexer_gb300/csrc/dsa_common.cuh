@@ -218,6 +218,33 @@ cudaError_t launch_gemm_tc(const void *A, int64_t lda, const void *B, int64_t ld
                            int M, int N, int K, cudaStream_t s);
 int gemm_tc_read_error(int *site);
 
+// ---------------------------------------------------------------------------
+// Paged latent caches (latent_cache.cu, tree_mla.cu, tree_mla_tc.cu)
+// ---------------------------------------------------------------------------
+// A block table as the kernels take it; table null: sequences lie contiguously at k_base.
+struct PageTab {
+    const int32_t *table;
+    int64_t ld;
+    int page, n_pages;
+};
+
+// Cache row of token `s` of sequence `b` (-1: its table entry names no page).  The caller has checked
+// that the table has an entry for s.
+__device__ __forceinline__ int64_t cache_row(const PageTab &pt, int b, int kbase, int s) {
+    if (!pt.table) return (int64_t)kbase + s;
+    const int pg = s / pt.page, e = __ldg(pt.table + (int64_t)b * pt.ld + pg);
+    return (unsigned)e < (unsigned)pt.n_pages ? (int64_t)e * pt.page + (s - pg * pt.page) : -1;
+}
+
+// Host checks of a cache and of a block table that covers tokens 0 .. last[b] - 1 of every sequence
+// with query rows (start_pos + T, or the whole sequence); fills the kernel's table.
+int check_latent_cache(const dsa_latent_cache *c, int d_c, int d_r);
+int check_pages(const dsa_pages *pages, const dsa_latent_cache *c, const Batch &bt, bool whole, PageTab &pt);
+
+// tcgen05 tree attention (bf16 queries, d_c = 512, d_r = 64, any H): q~ rows [N, H, 512] and q_pe rows
+// [N, H, 64] -> olat [N, H, 512] bf16 and lse; long contexts are split and joined through part_ws.
+bool tree_tc_supported(int dtype, int H, int d_n, int d_r, int d_c, int d_v);
+
 // Bounded-wait self-test (selftest.cu): one CTA whose first wait runs out after limit_cycles.
 cudaError_t launch_bounded_wait_selftest(long long limit_cycles, int *completed_ok, cudaStream_t s);
 int selftest_read_error(int *site);

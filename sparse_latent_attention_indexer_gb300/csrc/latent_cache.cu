@@ -1,0 +1,339 @@
+// Writing the latent cache by token position (quantising on the way) and
+// reading it back.
+//
+//   write: token t of sequence b -> row of position start_pos[b] + t:
+//          bf16 / fp32 rows as they are, or per 128 values e4m3 codes
+//          rne(x 2^-e) and the scale 2^e, e the smallest integer with
+//          amax <= 448 * 2^e (config_671B_v3.2.json excerpt, "DeepSeek-V3.2-Exp
+//          - Block input" page: dtype fp8, scale_fmt ue8m0);
+//   read:  code * scale, by position.
+//
+// Both only move bytes (1152 or 2304 in and 656 out per token, or back), so
+// each is one pass, one warp per token with everything it loads in flight
+// before the first use.  A lane takes 16 consecutive values: eight lanes make a
+// 128-block, whose maximum is three shuffles away, and the codes leave as one
+// 16-byte store a lane.  Rows that do not start on 16 bytes, or whose width is no
+// multiple of 16, go value by value.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "dsa_common.cuh"
+
+namespace dsa {
+namespace {
+
+struct MoveParams {
+    SeqTab st;
+    PageTab pt;
+    int n;              // tokens
+    int d_c, d_r;
+    int64_t ld_c, ld_x;     // dense rows
+    int64_t ld_kv, ld_pe;   // cache rows
+};
+static_assert(sizeof(MoveParams) + 256 <= 32764, "launch parameters");
+
+constexpr int PER = 16;  // values of a lane
+
+__device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[PER]) {
+    const uint4 a = __ldg((const uint4 *)p), b = __ldg((const uint4 *)p + 1);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void load16(const float *p, float (&v)[PER]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 a = __ldg((const float4 *)p + i);
+        v[4 * i] = a.x;
+        v[4 * i + 1] = a.y;
+        v[4 * i + 2] = a.z;
+        v[4 * i + 3] = a.w;
+    }
+}
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&v)[PER]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *(const uint32_t *)&t;
+    }
+    ((uint4 *)p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    ((uint4 *)p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void store16(float *p, const float (&v)[PER]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ((float4 *)p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// 16 e4m3 codes -> values times the block's scale.
+__device__ __forceinline__ void decode16(const uint4 &c, float sc, float (&v)[PER]) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w[i >> 1] >> (16 * (i & 1))) & 0xffffu),
+                                                         __NV_E4M3);
+        const float2 f = __half22float2(*(const __half2 *)&h);
+        v[2 * i] = f.x * sc;
+        v[2 * i + 1] = f.y * sc;
+    }
+}
+
+// One row of d values between the dense side and the cache.  VEC: both start on 16 bytes and d is a
+// multiple of 16.
+template <typename TI, typename TO, bool VEC>
+__device__ __forceinline__ void move_row(const TI *__restrict__ src, TO *__restrict__ dst, int d, int lane) {
+    if constexpr (VEC) {
+        for (int i = lane * PER; i < d; i += 32 * PER) {
+            float v[PER];
+            load16(src + i, v);
+            store16(dst + i, v);
+        }
+    } else {
+        for (int i = lane; i < d; i += 32) dst[i] = from_f32<TO>(to_f32(src[i]));
+    }
+}
+
+// TC: uint8_t = e4m3 codes, else the value type of the cache; rotary keys of an e4m3 cache are bf16.
+template <typename TC> struct PeOf { using T = TC; };
+template <> struct PeOf<uint8_t> { using T = __nv_bfloat16; };
+
+template <typename TX, typename TC, bool VEC, bool VEC_PE>
+__global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant__ MoveParams P,
+                                                          const TX *__restrict__ c_kv, const TX *__restrict__ k_pe,
+                                                          TC *__restrict__ kv, float *__restrict__ kv_scale,
+                                                          typename PeOf<TC>::T *__restrict__ pe) {
+    const int lane = threadIdx.x & 31;
+    const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= P.n) return;
+    const RowInfo ri = row_info(P.st, r);
+    const int64_t row = cache_row(P.pt, ri.b, ri.kbase, ri.p);
+    if (row < 0) return;
+    const TX *x = c_kv + (int64_t)r * P.ld_c;
+    TC *out = kv + row * P.ld_kv;
+    if constexpr (sizeof(TC) == 1) {
+        const int nb = P.d_c / 128;
+        for (int g0 = 0; g0 < nb; g0 += 4) {  // four blocks a pass, eight lanes each (warp-uniform)
+            const int g = g0 + (lane >> 3), j = g * 128 + (lane & 7) * PER;
+            float v[PER];
+            if (g < nb) {
+                if constexpr (VEC) {
+                    load16(x + j, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) v[i] = to_f32(x[j + i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) v[i] = 0.0f;
+            }
+            float amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const int e = ue8m0_exponent(amax);
+            const float inv = ldexpf(1.0f, -e);  // exact power of two
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i] * inv, v[4 * i + 1] * inv),
+                                                             __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2] * inv, v[4 * i + 3] * inv),
+                                                             __NV_SATFINITE, __NV_E4M3);
+                w[i] = lo | hi << 16;
+            }
+            if (g < nb) {
+                *(uint4 *)(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                if ((lane & 7) == 0) kv_scale[row * nb + g] = ldexpf(1.0f, e);
+            }
+        }
+    } else {
+        move_row<TX, TC, VEC>(x, out, P.d_c, lane);
+    }
+    if (P.d_r)
+        move_row<TX, typename PeOf<TC>::T, VEC_PE>(k_pe + (int64_t)r * P.ld_x, pe + row * P.ld_pe, P.d_r, lane);
+}
+
+template <typename TC, typename TO, bool VEC, bool VEC_PE>
+__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ MoveParams P,
+                                                         const int32_t *__restrict__ pos, const TC *__restrict__ kv,
+                                                         const float *__restrict__ kv_scale,
+                                                         const typename PeOf<TC>::T *__restrict__ pe,
+                                                         TO *__restrict__ c_kv, TO *__restrict__ k_pe) {
+    const int lane = threadIdx.x & 31;
+    const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= P.n) return;
+    const RowInfo ri = row_info(P.st, r);
+    const int p = pos ? __ldg(pos + r) : ri.p;
+    const int64_t row = (unsigned)p < (unsigned)ri.S ? cache_row(P.pt, ri.b, ri.kbase, p) : -1;
+    TO *out = c_kv + (int64_t)r * P.ld_c, *ope = k_pe + (int64_t)r * P.ld_x;
+    if (row < 0) {
+        for (int i = lane; i < P.d_c; i += 32) out[i] = from_f32<TO>(0.0f);
+        for (int i = lane; i < P.d_r; i += 32) ope[i] = from_f32<TO>(0.0f);
+        return;
+    }
+    const TC *x = kv + row * P.ld_kv;
+    if constexpr (sizeof(TC) == 1) {
+        const int nb = P.d_c / 128;
+        for (int j = lane * PER; j < P.d_c; j += 32 * PER) {
+            const uint4 c = __ldg((const uint4 *)(x + j));
+            float v[PER];
+            decode16(c, __ldg(kv_scale + row * nb + j / 128), v);
+            if constexpr (VEC) {
+                store16(out + j, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) out[j + i] = from_f32<TO>(v[i]);
+            }
+        }
+    } else {
+        move_row<TC, TO, VEC>(x, out, P.d_c, lane);
+    }
+    if (P.d_r) move_row<typename PeOf<TC>::T, TO, VEC_PE>(pe + row * P.ld_pe, ope, P.d_r, lane);
+}
+
+inline bool on16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+inline size_t esz(int dtype) { return dtype == DSA_F32 ? 4 : (dtype == DSA_BF16 ? 2 : 1); }
+// Whether rows of d values at p with stride ld take the 16-value path (the cache's rows always start on
+// 16 bytes).
+inline bool vec_rows(const void *p, int64_t ld, int dtype, int d) {
+    return on16(p) && ld * esz(dtype) % 16 == 0 && d % PER == 0;
+}
+
+template <typename F>
+auto by_bools(bool a, bool b, F f) {
+    if (a) return b ? f(std::true_type(), std::true_type()) : f(std::true_type(), std::false_type());
+    return b ? f(std::false_type(), std::true_type()) : f(std::false_type(), std::false_type());
+}
+
+template <typename TX, typename TC>
+cudaError_t launch_write(const MoveParams &P, const void *c_kv, const void *k_pe, const dsa_latent_cache *c, bool vec,
+                         bool vec_pe, cudaStream_t s) {
+    by_bools(vec, vec_pe, [&](auto v, auto vp) {
+        cache_write_kernel<TX, TC, decltype(v)::value, decltype(vp)::value><<<(P.n + 7) / 8, 256, 0, s>>>(
+            P, (const TX *)c_kv, (const TX *)k_pe, (TC *)c->kv, c->kv_scale, (typename PeOf<TC>::T *)c->k_pe);
+    });
+    return cudaGetLastError();
+}
+template <typename TC, typename TO>
+cudaError_t launch_read(const MoveParams &P, const int32_t *pos, const dsa_latent_cache *c, void *c_kv, void *k_pe,
+                        bool vec, bool vec_pe, cudaStream_t s) {
+    by_bools(vec, vec_pe, [&](auto v, auto vp) {
+        cache_read_kernel<TC, TO, decltype(v)::value, decltype(vp)::value><<<(P.n + 7) / 8, 256, 0, s>>>(
+            P, pos, (const TC *)c->kv, c->kv_scale, (const typename PeOf<TC>::T *)c->k_pe, (TO *)c_kv, (TO *)k_pe);
+    });
+    return cudaGetLastError();
+}
+
+// What a write and a read check alike; fills P.
+int check_move(int dense_dtype, int d_c, int d_r, const dsa_latent_cache *cache, const dsa_seqs *seqs,
+               const dsa_pages *pages, bool whole, const void *c_kv, int64_t ld_c, const void *k_pe, int64_t ld_x,
+               MoveParams &P) {
+    if (dense_dtype != DSA_F32 && dense_dtype != DSA_BF16) return DSA_ERR_UNSUPPORTED;
+    int rc = check_latent_cache(cache, d_c, d_r);
+    if (rc) return rc;
+    Batch bt;
+    if ((rc = build_batch(seqs, bt))) return rc;
+    if ((rc = check_pages(pages, cache, bt, whole, P.pt))) return rc;
+    if (ld_c < d_c || (d_r > 0 && ld_x < d_r)) return DSA_ERR_INVALID_ARG;
+    P.st = bt.st;
+    P.n = bt.total_q;
+    if (P.n == 0) return DSA_OK;
+    if (!c_kv || (d_r > 0 && !k_pe)) return DSA_ERR_INVALID_ARG;
+    const size_t a = esz(dense_dtype);
+    if ((uintptr_t)c_kv % a || (uintptr_t)k_pe % a) return DSA_ERR_INVALID_ARG;
+    P.d_c = d_c;
+    P.d_r = d_r;
+    P.ld_c = ld_c;
+    P.ld_x = ld_x;
+    P.ld_kv = cache->ld_kv;
+    P.ld_pe = cache->ld_pe;
+    return DSA_OK;
+}
+
+}  // namespace
+
+int check_latent_cache(const dsa_latent_cache *c, int d_c, int d_r) {
+    if (!c || d_c < 1 || d_r < 0) return DSA_ERR_INVALID_ARG;
+    if (c->dtype != DSA_F32 && c->dtype != DSA_BF16 && c->dtype != DSA_E4M3) return DSA_ERR_UNSUPPORTED;
+    if (d_c > 1024 || d_r > 128 || (c->dtype == DSA_E4M3 && d_c % 128)) return DSA_ERR_UNSUPPORTED;
+    const int pe_dtype = c->dtype == DSA_E4M3 ? DSA_BF16 : c->dtype;
+    if (!c->kv || c->ld_kv < d_c || c->ld_kv * esz(c->dtype) % 16 || !on16(c->kv)) return DSA_ERR_INVALID_ARG;
+    if (d_r > 0 && (!c->k_pe || c->ld_pe < d_r || c->ld_pe * esz(pe_dtype) % 16 || !on16(c->k_pe)))
+        return DSA_ERR_INVALID_ARG;
+    if (c->dtype == DSA_E4M3 && (!c->kv_scale || (uintptr_t)c->kv_scale % 4)) return DSA_ERR_INVALID_ARG;
+    if (c->rows < 0 || c->rows >= (int64_t(1) << 31) - 64) return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+int check_pages(const dsa_pages *pages, const dsa_latent_cache *c, const Batch &bt, bool whole, PageTab &pt) {
+    pt = PageTab{nullptr, 0, 1, 0};
+    if (!pages) return bt.total_k <= c->rows ? DSA_OK : DSA_ERR_INVALID_ARG;
+    if (pages->page_size < 16 || pages->page_size % 16 || pages->n_pages < 0 || pages->ld_table < 0)
+        return DSA_ERR_INVALID_ARG;
+    if ((int64_t)pages->n_pages * pages->page_size > c->rows) return DSA_ERR_INVALID_ARG;
+    int64_t most = 0;
+    for (int b = 0; b < bt.st.B; ++b) {
+        const int64_t T = bt.st.q_off[b + 1] - bt.st.q_off[b];
+        if (T > 0) most = std::max<int64_t>(most, whole ? bt.st.k_len[b] : bt.st.start_pos[b] + T);
+    }
+    if (most > pages->ld_table * pages->page_size) return DSA_ERR_INVALID_ARG;
+    if (most > 0 && (!pages->block_table || (uintptr_t)pages->block_table % 4)) return DSA_ERR_INVALID_ARG;
+    pt = PageTab{pages->block_table, pages->ld_table, pages->page_size, pages->n_pages};
+    return DSA_OK;
+}
+
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" {
+
+int dsa_latent_cache_write(const void *c_kv, int64_t ld_c, const void *k_pe, int64_t ld_x, int x_dtype, int d_c, int d_r,
+                           const dsa_latent_cache *cache, const dsa_seqs *seqs, const dsa_pages *pages, void *stream) {
+    reset_trace();
+    static thread_local MoveParams P;  // 16 KB: keep it off the host stack
+    const int rc = check_move(x_dtype, d_c, d_r, cache, seqs, pages, false, c_kv, ld_c, k_pe, ld_x, P);
+    if (rc || P.n == 0) return rc;
+    const bool vec = vec_rows(c_kv, ld_c, x_dtype, d_c), vec_pe = vec_rows(k_pe, ld_x, x_dtype, d_r);
+    const cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    auto go = [&](auto x) {
+        using TX = decltype(x);
+        if (cache->dtype == DSA_E4M3) return launch_write<TX, uint8_t>(P, c_kv, k_pe, cache, vec, vec_pe, s);
+        if (cache->dtype == DSA_BF16) return launch_write<TX, __nv_bfloat16>(P, c_kv, k_pe, cache, vec, vec_pe, s);
+        return launch_write<TX, float>(P, c_kv, k_pe, cache, vec, vec_pe, s);
+    };
+    e = x_dtype == DSA_F32 ? go(float()) : go(__nv_bfloat16());
+    note_launch(DSA_KERNEL_CACHE_WRITE);
+    return e == cudaSuccess ? DSA_OK : fail_cuda(e);
+}
+
+int dsa_latent_cache_read(const dsa_latent_cache *cache, int d_c, int d_r, const dsa_seqs *seqs, const dsa_pages *pages,
+                          const int32_t *pos, void *c_kv, int64_t ld_c, void *k_pe, int64_t ld_x, int out_dtype,
+                          void *stream) {
+    reset_trace();
+    static thread_local MoveParams P;
+    const int rc = check_move(out_dtype, d_c, d_r, cache, seqs, pages, pos != nullptr, c_kv, ld_c, k_pe, ld_x, P);
+    if (rc || P.n == 0) return rc;
+    if ((uintptr_t)pos % 4) return DSA_ERR_INVALID_ARG;
+    const bool vec = vec_rows(c_kv, ld_c, out_dtype, d_c), vec_pe = vec_rows(k_pe, ld_x, out_dtype, d_r);
+    const cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    auto go = [&](auto o) {
+        using TO = decltype(o);
+        if (cache->dtype == DSA_E4M3) return launch_read<uint8_t, TO>(P, pos, cache, c_kv, k_pe, vec, vec_pe, s);
+        if (cache->dtype == DSA_BF16) return launch_read<__nv_bfloat16, TO>(P, pos, cache, c_kv, k_pe, vec, vec_pe, s);
+        return launch_read<float, TO>(P, pos, cache, c_kv, k_pe, vec, vec_pe, s);
+    };
+    e = out_dtype == DSA_F32 ? go(float()) : go(__nv_bfloat16());
+    note_launch(DSA_KERNEL_CACHE_READ);
+    return e == cudaSuccess ? DSA_OK : fail_cuda(e);
+}
+
+}  // extern "C"
