@@ -242,8 +242,14 @@ int check_latent_cache(const dsa_latent_cache *c, int d_c, int d_r);
 int check_pages(const dsa_pages *pages, const dsa_latent_cache *c, const Batch &bt, bool whole, PageTab &pt);
 
 // tcgen05 tree attention (bf16 queries, d_c = 512, d_r = 64, any H): q~ rows [N, H, 512] and q_pe rows
-// [N, H, 64] -> olat [N, H, 512] bf16 and lse; long contexts are split and joined through part_ws.
+// [N, H, 64] -> olat [N, H, 512] bf16 and lse.  Long contexts are split and joined through part_ws
+// (tree_tc_partial_bytes).
 bool tree_tc_supported(int dtype, int H, int d_n, int d_r, int d_c, int d_v);
+size_t tree_tc_partial_bytes(int H, const Batch &bt);
+cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cache *c, const uint64_t *mask, int words,
+                           const Batch &bt, const PageTab &pt, int H, float scale, void *olat, float *lse,
+                           void *part_ws, cudaStream_t s);
+int tree_tc_read_error(int *site);
 
 // Bounded-wait self-test (selftest.cu): one CTA whose first wait runs out after limit_cycles.
 cudaError_t launch_bounded_wait_selftest(long long limit_cycles, int *completed_ok, cudaStream_t s);

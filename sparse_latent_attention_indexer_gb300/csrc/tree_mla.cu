@@ -15,6 +15,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "dsa_common.cuh"
 
@@ -183,11 +184,17 @@ inline bool on16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 // Scratch of a call: q~ and the latent context [N, H, d_c] (bf16 for the tensor-core kernel, fp32 for the
 // generic one), and the partial contexts of split rows.
 struct TreeWs {
+    bool tc;
     size_t olat, part, total;
 };
 TreeWs tree_ws(int dtype, int H, int d_n, int d_r, int d_c, int d_v, const Batch &bt) {
-    const size_t per = align256((size_t)bt.total_q * H * d_c * 4);
-    return TreeWs{per, 2 * per, 2 * per};
+    TreeWs w;
+    w.tc = !force_generic() && tree_tc_supported(dtype, H, d_n, d_r, d_c, d_v);
+    const size_t per = align256((size_t)bt.total_q * H * d_c * (w.tc ? 2 : 4));
+    w.olat = per;
+    w.part = 2 * per;
+    w.total = w.part + (w.tc ? tree_tc_partial_bytes(H, bt) : 0);
+    return w;
 }
 
 int check_tree_shape(int dtype, int H, int d_n, int d_r, int d_c, int d_v) {
@@ -219,6 +226,8 @@ int dsa_tree_mla_fwd(const void *q_nope, const void *q_pe, int dtype, const dsa_
         (rc = check_pages(pages, cache, bt, false, pt)))
         return rc;
     if (dtype == DSA_F32 ? cache->dtype != DSA_F32 : cache->dtype == DSA_F32) return DSA_ERR_UNSUPPORTED;
+    if (!std::isfinite(softmax_scale)) return DSA_ERR_INVALID_ARG;
+    if ((int64_t)bt.total_q * H >= (int64_t(1) << 31) - 256) return DSA_ERR_UNSUPPORTED;
     if (bt.total_q == 0) return DSA_OK;
     if (!q_nope || (d_r > 0 && !q_pe) || !W_UK || !W_UV || !out) return DSA_ERR_INVALID_ARG;
     if (!on16(q_nope) || !on16(q_pe) || !on16(W_UK) || !on16(W_UV) || !on16(out) || (uintptr_t)lse % 4)
@@ -233,8 +242,18 @@ int dsa_tree_mla_fwd(const void *q_nope, const void *q_pe, int dtype, const dsa_
     const cudaStream_t s = (cudaStream_t)stream;
     char *ws = (char *)workspace;
     const int N = bt.total_q;
+    cudaError_t e;
+    if (L.tc) {
+        void *qt = ws, *olat = ws + L.olat;
+        e = launch_absorb_q_tc(q_nope, W_UK, qt, N, H, s);
+        if (e != cudaSuccess) return fail_cuda(e);
+        e = launch_tree_tc(qt, q_pe, cache, tree_mask, mask_words, bt, pt, H, softmax_scale, olat, lse, ws + L.part, s);
+        if (e != cudaSuccess) return fail_cuda(e);
+        e = launch_absorb_v_tc(olat, W_UV, out, N, H, s);
+        return e == cudaSuccess ? DSA_OK : fail_cuda(e);
+    }
     float *qt = (float *)ws, *olat = (float *)(ws + L.olat);
-    cudaError_t e = launch_absorb_simt(q_nope, dtype, (int64_t)H * d_n, W_UK, dtype, qt, DSA_F32, (int64_t)H * d_c, N, H,
+    e = launch_absorb_simt(q_nope, dtype, (int64_t)H * d_n, W_UK, dtype, qt, DSA_F32, (int64_t)H * d_c, N, H,
                                        d_n, d_c, s);
     if (e != cudaSuccess) return fail_cuda(e);
     e = launch_tree_simt(qt, q_pe, dtype, cache, tree_mask, mask_words, bt, pt, H, d_r, d_c, softmax_scale, olat, lse, s);
