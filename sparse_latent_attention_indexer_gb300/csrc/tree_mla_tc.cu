@@ -158,16 +158,17 @@ __device__ __forceinline__ void dequant16(const uint4 &c, const Scale2 &s, uint4
     o[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// The softmax warps arrive; returns the AND of `v` over them.
-__device__ __forceinline__ bool soft_bar_and(bool v) {
+// Four warps (1: softmax, 2: loading) arrive at barrier ID; returns the AND of `v` over them.
+template <int ID>
+__device__ __forceinline__ bool bar_and(bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.and.pred p, 1, 128, q;\n\t"
+        "bar.red.and.pred p, %2, 128, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "n"(ID)
         : "memory");
     return r != 0;
 }
@@ -179,17 +180,19 @@ __device__ __forceinline__ int v_pos(int t, int n) { return K_SLOTS * min(t + AH
 template <bool KV8>
 struct Cfg {
     static constexpr int NLOAD = KV8 ? 8 : 4;  // loading warps
+    static constexpr int ARRIVE = KV8 ? 8 : 1; // arrivals of a CTA on a full slot
     static constexpr int THREADS = 32 * (6 + NLOAD);
 };
 
 template <bool KV8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qpe,
-                   const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_pe, int box,
+                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_pe, int run,
                    const void *__restrict__ kv, const float *__restrict__ kv_scale,
                    const __grid_constant__ TreeParams P, __nv_bfloat16 *__restrict__ olat, float *__restrict__ lse,
                    float *__restrict__ opart, float *__restrict__ lpart) {
-    constexpr int NLOAD = Cfg<KV8>::NLOAD;
+    constexpr int ARRIVE = Cfg<KV8>::ARRIVE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *Q = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *Pb = Q + NQ * SLAB;
@@ -231,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
     if (threadIdx.x == 0) {
         tc::mbar_init(&bar->q_full, 2);
         for (int i = 0; i < NSLOT; ++i) {
-            tc::mbar_init(&bar->full[i], 2 * NLOAD);  // the loading warps of both CTAs, or as many producer lanes
+            tc::mbar_init(&bar->full[i], 2 * ARRIVE);
             tc::mbar_init(&bar->empty[i], 1);
             tc::mbar_init(&bar->go[i], 1);
         }
@@ -265,8 +268,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
     // Cache row of token s, or -1 (behind the last token, or on no page).
     const auto row_of = [&](int s) -> int64_t { return s < tokens ? cache_row(P.pt, b, kbase, s) : -1; };
 
+    // ---- one warp's work: TMA copies of the cache ----
+    // Rows of a tile's eight runs of 16 tokens, a run a lane: its cache row, -1 behind the last token, or the row past
+    // the cache (read as zeros) where there is no page.
+    const auto runs_of = [&](int t) {
+        const int s = (t0 + t) * TK + (lane & 7) * 16;
+        const int64_t r = row_of(s);
+        return t >= n || s >= tokens ? -1 : r >= 0 ? (int)r : P.oob;
+    };
+    // `ntok` tokens from run r0 on, `parts` slabs of 64 columns from column slab x0 on.  A copy takes `run` tokens;
+    // where that is all of them it takes all slabs at once.
+    const auto slot_copy = [&](int pos, const CUtensorMap *map, int parts, int slab_bytes, int ntok, int rows, int r0,
+                               int x0) {
+        const int st = pos % NSLOT;
+        const uint32_t fb = leader(&bar->full[st]), dst = tc::smem_u32(Ring + st * SLOT);
+        const int each = min(run, ntok), at_once = run >= ntok ? parts : 1;
+        const int copies = (ntok / each) * (parts / at_once);
+        const int k = lane / (parts / at_once), j = lane - k * (parts / at_once);  // this lane's copy: tokens, slab
+        const int row = __shfl_sync(0xffffffffu, rows, (r0 + k * (each / 16)) & 7);
+        const bool go = lane < copies && row >= 0;
+        const int some = __popc(__ballot_sync(0xffffffffu, go));
+        if (lane == 0) tc::mbar_arrive_expect_tx_remote(fb, (uint32_t)(some * each * at_once * 128));
+        __syncwarp();
+        if (go) tc::tma_load_3d_pair(dst + j * slab_bytes + k * each * 128, map, fb, 0, row, x0 + j);
+    };
+    // Publishes which of tile t's tokens have a page.
+    const auto put_mask = [&](int t, int rows) {
+        if (!P.pt.table) return;
+        const unsigned have = __ballot_sync(0xffffffffu, rows >= 0 && rows != P.oob);
+        if (lane < 2) {
+            uint64_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (have >> (4 * lane + i) & 1) m |= 0xffffull << 16 * i;
+            live[2 * (t % NMASK) + lane] = m;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar->mask_full[t % NMASK]);
+    };
+
     if (warp == 4 && n > 0) {
-        // ---------------- producer: Q, the live-token masks, TMA copies of K and V (e4m3: of the rotary keys) ------------
+        // ---------------- producer: Q; of a bf16 cache K and V ----------------
         if (lane == 0) {
             const uint32_t qb = leader(&bar->q_full);
             tc::mbar_arrive_expect_tx_remote(qb, NQ * SLAB);
@@ -275,103 +317,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             tc::tma_load_2d_pair(tc::smem_u32(Q + (NQ - 1) * SLAB), &tm_qpe, qb, 0, y);
         }
         __syncwarp();
-        bool ok = true;
-        // The producer waits for every slot in turn (a barrier's phase can be told from its neighbour only, so nobody may
-        // skip one) and hands the slots that the loading warps fill on to them.
+        // Who waits for slots waits for every one in turn: a barrier's phase can be told from its neighbours only.  So the
+        // producer also waits for the slots that the loading warps fill, and hands them on.
         const auto slot_wait = [&](int pos) {
             return __all_sync(0xffffffffu, tc::mbar_wait(&bar->empty[pos % NSLOT], ((pos / NSLOT) & 1) ^ 1, abort_flag,
                                                          err, 101, P.wait_limit));
         };
-        const auto slot_pass = [&](int pos) {
-            if (!slot_wait(pos)) return false;
-            if (lane == 0) tc::mbar_arrive(&bar->go[pos % NSLOT]);
-            return true;
-        };
-        // Boxes of `box` tokens: `parts` slabs of `ntok` tokens from token s0 on, slab j from column x0 + 64 j.
-        const auto slot_tma = [&](int pos, const CUtensorMap *map, int parts, int slab_bytes, int ntok, int s0, int x0) {
-            if (!slot_wait(pos)) return false;
-            const int st = pos % NSLOT;
-            const int runs = ntok / box, mine = lane / parts, j = lane - mine * parts;
-            const int s = s0 + mine * box;
-            const bool go = mine < runs && s < tokens;
-            int row = P.oob;
-            if (go) {
-                const int64_t r = row_of(s);
-                if (r >= 0) row = (int)r;
-            }
-            const int boxes = __popc(__ballot_sync(0xffffffffu, go));
-            const uint32_t fb = leader(&bar->full[st]);
-            if (lane == 0) tc::mbar_arrive_expect_tx_remote(fb, (uint32_t)boxes * box * 128);
-            else if (lane < NLOAD) tc::mbar_arrive_remote(fb);
-            __syncwarp();
-            if (go)
-                tc::tma_load_2d_pair(tc::smem_u32(Ring + st * SLOT + j * slab_bytes + mine * box * 128), map, fb,
-                                     x0 + j * 64, row);
-            return true;
-        };
-        for (int s = 0; ok && s < n + AHEAD; ++s) {
-            if (s < n) {
-                const int k0 = (t0 + s) * TK;
-                // which of the tile's 128 tokens have a page (lane: four tokens of one page)
-                uint64_t m0 = ~0ull, m1 = ~0ull;
-                if (P.pt.table) {
-                    const unsigned ok16 = __ballot_sync(0xffffffffu, row_of(k0 + 4 * lane) >= 0);
-                    m0 = m1 = 0;
+        bool ok = true;
+        int rows[AHEAD + 2];  // of tiles s - AHEAD .. s + 1
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (ok16 >> i & 1) m0 |= 0xfull << 4 * i;
-                        if (ok16 >> (16 + i) & 1) m1 |= 0xfull << 4 * i;
-                    }
+        for (int i = 0; i < AHEAD; ++i) rows[i] = -1;
+        rows[AHEAD] = runs_of(0);
+        for (int s = 0; !KV8 && ok && s < n + AHEAD; ++s) {
+            rows[AHEAD + 1] = runs_of(s + 1);
+            if (s < n) {
+                put_mask(s, rows[AHEAD]);
+                for (int j = 0; ok && j < K_SLOTS; ++j) {
+                    if (!(ok = slot_wait(k_pos(s) + j))) break;
+                    if (j < K_SLOTS - 1) slot_copy(k_pos(s) + j, &tm_k, 2, SLAB, HR, rows[AHEAD], rank * 4, 2 * j);
+                    else slot_copy(k_pos(s) + j, &tm_pe, 1, SLAB, HR, rows[AHEAD], rank * 4, 0);
                 }
-                if (lane == 0) {
-                    live[2 * (s % NMASK)] = m0;
-                    live[2 * (s % NMASK) + 1] = m1;
-                    tc::mbar_arrive(&bar->mask_full[s % NMASK]);
-                }
-                __syncwarp();
-                const int own = k0 + rank * HR;
-                for (int j = 0; ok && j < K_SLOTS - 1; ++j)
-                    ok = KV8 ? slot_pass(k_pos(s) + j) : slot_tma(k_pos(s) + j, &tm_kv, 2, SLAB, HR, own, j * 128);
-                if (ok) ok = slot_tma(k_pos(s) + K_SLOTS - 1, &tm_pe, 1, SLAB, HR, own, 0);
             }
             if (s >= AHEAD) {
-                const int t = s - AHEAD, k0 = (t0 + t) * TK;
-                const bool pass = KV8 || k0 + TK > safe;  // tiles with hidden tokens: the loading warps
-                for (int j = 0; ok && j < V_SLOTS; ++j)
-                    ok = pass ? slot_pass(v_pos(t, n) + j)
-                              : slot_tma(v_pos(t, n) + j, &tm_kv, 4, VSLAB, VCH, k0 + j * VCH, rank * 256);
+                const int t = s - AHEAD;
+                const bool pass = (t0 + t + 1) * TK > safe;  // tiles with hidden tokens: the loading warps
+                for (int j = 0; ok && j < V_SLOTS; ++j) {
+                    const int pos = v_pos(t, n) + j;
+                    if (!(ok = slot_wait(pos))) break;
+                    if (!pass) slot_copy(pos, &tm_v, 4, VSLAB, VCH, rows[0], 2 * j, rank * 4);
+                    else if (lane == 0) tc::mbar_arrive(&bar->go[pos % NSLOT]);
+                }
             }
+#pragma unroll
+            for (int i = 0; i <= AHEAD; ++i) rows[i] = rows[i + 1];
         }
     } else if (warp == 5 && rank == 0 && lane == 0 && n > 0) {
         // ---------------- MMA issuer (of the pair) ----------------
-        const uint32_t q0 = tc::smem_u32(Q), p0 = tc::smem_u32(Pb), r0 = tc::smem_u32(Ring);
+        // Descriptors are a base plus (bytes >> 4): the issuing thread has little time between MMAs.
+        const uint64_t qd = tc::smem_desc(tc::smem_u32(Q), 16, 1024), pd = tc::smem_desc(tc::smem_u32(Pb), 16, 1024);
+        const uint64_t kd = tc::smem_desc(tc::smem_u32(Ring), 16, 1024), vd = tc::smem_desc(tc::smem_u32(Ring), VSLAB, 1024);
         const uint16_t both = 3;
         bool ok = tc::mbar_wait(&bar->q_full, 0, abort_flag, err, 102, P.wait_limit);
-        int pos = 0;
-        const auto slot_ready = [&](int &st) {
-            st = pos % NSLOT;
-            const bool r = tc::mbar_wait(&bar->full[st], (pos / NSLOT) & 1, abort_flag, err, 103, P.wait_limit);
+        int st = 0;
+        uint32_t ring_ph = 0;
+        const auto slot_ready = [&]() {
+            const bool r = tc::mbar_wait(&bar->full[st], ring_ph, abort_flag, err, 103, P.wait_limit);
             tc::tc_fence_after();
-            ++pos;
             return r;
         };
+        const auto slot_used = [&]() {
+            tc::mma_commit_pair(&bar->empty[st], both);
+            if (++st == NSLOT) {
+                st = 0;
+                ring_ph ^= 1;
+            }
+        };
         for (int s = 0; ok && s < n + AHEAD; ++s) {
-            int st;
             if (s < n) {
                 const int sb = s % NS;
                 if (s >= NS && !(ok = tc::mbar_wait(&bar->s_empty[sb], ((s / NS) - 1) & 1, abort_flag, err, 104, P.wait_limit))) break;
                 const uint32_t d = tmem + COL_S + sb * (TK / 2);
-                for (int j = 0; j < K_SLOTS; ++j) {
-                    if (!(ok = slot_ready(st))) break;
-                    const int slabs = j < K_SLOTS - 1 ? 2 : 1;
-                    for (int h = 0; h < slabs; ++h)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t ad = tc::smem_desc(q0 + (2 * j + h) * SLAB + kk * 32, 16, 1024);
-                            const uint64_t bd = tc::smem_desc(r0 + st * SLOT + h * SLAB + kk * 32, 16, 1024);
-                            tc::mma_f16_pair(d, ad, bd, IDESC_QK, (j | h | kk) != 0);
-                        }
-                    tc::mma_commit_pair(&bar->empty[st], both);
+                for (int j = 0; j < K_SLOTS; ++j) {
+                    if (!(ok = slot_ready())) break;
+                    const uint64_t b0 = kd + (uint64_t)(uint32_t)(st * (SLOT / 16));
+#pragma unroll
+                    for (int i = 0; i < (j < K_SLOTS - 1 ? 8 : 4); ++i)  // slab i / 4, 16 columns each
+                        tc::mma_f16_pair(d, qd + ((2 * j + (i >> 2)) * SLAB + (i & 3) * 32) / 16,
+                                         b0 + ((i >> 2) * SLAB + (i & 3) * 32) / 16, IDESC_QK, (j | i) != 0);
+                    slot_used();
                 }
                 if (!ok) break;
                 tc::mma_commit_pair(&bar->s_full[sb], both);
@@ -380,19 +394,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                 const int t = s - AHEAD, pb = t & 1;
                 if (!(ok = tc::mbar_wait(&bar->p_full[pb], (t >> 1) & 1, abort_flag, err, 105, P.wait_limit))) break;
                 tc::tc_fence_after();
+                const uint64_t a0 = pd + (uint64_t)(uint32_t)(pb * (P_BYTES / 16));
+#pragma unroll
                 for (int j = 0; j < V_SLOTS; ++j) {
-                    if (!(ok = slot_ready(st))) break;
+                    if (!(ok = slot_ready())) break;
+                    const uint64_t b0 = vd + (uint64_t)(uint32_t)(st * (SLOT / 16));
 #pragma unroll
-                    for (int kk = 0; kk < VCH / 16; ++kk) {
-                        const int key = j * VCH + kk * 16;  // of the tile
-                        const uint64_t ad = tc::smem_desc(p0 + pb * P_BYTES + (key >> 6) * SLAB + (key & 63) * 2, 16, 1024);
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint64_t bd = tc::smem_desc(r0 + st * SLOT + half * 2 * VSLAB + kk * 16 * 128, VSLAB, 1024);
-                            tc::mma_f16_pair(tmem + COL_O + half * 128, ad, bd, IDESC_PV, (t | j | kk) != 0);
-                        }
+                    for (int i = 0; i < 2 * (VCH / 16); ++i) {  // 16 tokens i / 2, columns of half i % 2
+                        const int key = j * VCH + (i >> 1) * 16;
+                        tc::mma_f16_pair(tmem + COL_O + (i & 1) * 128, a0 + ((key >> 6) * SLAB + (key & 63) * 2) / 16,
+                                         b0 + ((i & 1) * 2 * VSLAB + (i >> 1) * 16 * 128) / 16, IDESC_PV,
+                                         (t | j | (i >> 1)) != 0);
                     }
-                    tc::mma_commit_pair(&bar->empty[st], both);
+                    slot_used();
                 }
                 if (!ok) break;
                 tc::mma_commit_pair(&bar->p_empty[pb], both);
@@ -406,17 +420,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         // ---------------- loading warps ----------------
         const int tid = threadIdx.x - 6 * 32;
         bool ok = true;
-        uint32_t turn = 0;  // phase of every slot's `go`
+        uint32_t turn = 0;  // bf16: phase of every slot's `go`
         const auto slot_free = [&](int pos) {
             const int st = pos % NSLOT;
-            const uint32_t ph = (turn >> st) & 1u;
+            const uint32_t ph = KV8 ? ((pos / NSLOT) & 1) ^ 1 : (turn >> st) & 1u;
             turn ^= 1u << st;
-            return ok = __all_sync(0xffffffffu, tc::mbar_wait(&bar->go[st], ph, abort_flag, err, 107, P.wait_limit));
-        };
-        const auto slot_done = [&](int pos) {
-            tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_remote(leader(&bar->full[pos % NSLOT]));
+            return ok = __all_sync(0xffffffffu, tc::mbar_wait(KV8 ? &bar->empty[st] : &bar->go[st], ph, abort_flag, err, 107,
+                                                              P.wait_limit));
         };
         if constexpr (KV8) {
             // Thread (K): 32 columns of one of the CTA's 64 tokens; (V): 32 of its columns of one of the chunk's
@@ -425,6 +435,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             const int k_tok = tid >> 2, k_col = (tid & 3) * 32, v_tok = tid >> 3, v_col = (tid & 7) * 32;
             uint4 kc[K_SLOTS - 1][2], vc[V_SLOTS][2];
             float ks[K_SLOTS - 1], vs[V_SLOTS];
+            const auto slot_done = [&](int pos) {
+                tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_remote(leader(&bar->full[pos % NSLOT]));
+            };
             const auto fetch = [&](uint4 (&c)[2], float &sc, int64_t row, int col) {
                 c[0] = c[1] = make_uint4(0, 0, 0, 0);
                 sc = 0.0f;
@@ -448,14 +463,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                         *(uint4 *)(dst + tok * 128 + (((c0 + 2 * i + e) ^ (tok & 7)) << 4)) = o[e];
                 }
             };
-            const auto fetch_k = [&](int t, int j) {
-                fetch(kc[j], ks[j], row_of((t0 + t) * TK + rank * HR + k_tok), j * 128 + k_col);
-            };
-            const auto fetch_v = [&](int t, int j) {
-                fetch(vc[j], vs[j], row_of((t0 + t) * TK + j * VCH + v_tok), rank * 256 + v_col);
-            };
+            // All loads of a tile's K (or V) together: the wait for one batch must not include a younger load's.
+            const auto fetch_k = [&](int t) {
+                const int64_t row = row_of((t0 + t) * TK + rank * HR + k_tok);
 #pragma unroll
-            for (int j = 0; j < K_SLOTS - 1; ++j) fetch_k(0, j);
+                for (int j = 0; j < K_SLOTS - 1; ++j) fetch(kc[j], ks[j], row, j * 128 + k_col);
+            };
+            const auto fetch_v = [&](int t) {
+#pragma unroll
+                for (int j = 0; j < V_SLOTS; ++j)
+                    fetch(vc[j], vs[j], row_of((t0 + t) * TK + j * VCH + v_tok), rank * 256 + v_col);
+            };
+            fetch_k(0);
             for (int s = 0; ok && s < n + AHEAD; ++s) {
                 if (s < n) {
 #pragma unroll
@@ -464,13 +483,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                         if (!slot_free(pos)) break;
                         put(kc[j], ks[j], Ring + (pos % NSLOT) * SLOT + (k_col >> 6) * SLAB, k_tok, k_col, false);
                         slot_done(pos);
-                        if (s + 1 < n) fetch_k(s + 1, j);
                     }
-                    if (s == AHEAD - 1 || n <= AHEAD && s == n - 1) {
-#pragma unroll
-                        for (int j = 0; j < V_SLOTS; ++j) fetch_v(0, j);
+                    // the rotary slab is bf16: one of the warps copies it
+                    if (ok && slot_free(k_pos(s) + K_SLOTS - 1)) {
+                        const int pos = k_pos(s) + K_SLOTS - 1;
+                        if (warp == 6) {
+                            const int rows = runs_of(s);
+                            put_mask(s, rows);
+                            slot_copy(pos, &tm_pe, 1, SLAB, HR, rows, rank * 4, 0);
+                        } else if (lane == 0) {
+                            tc::mbar_arrive_remote(leader(&bar->full[pos % NSLOT]));
+                        }
                     }
+                    if (s + 1 < n) fetch_k(s + 1);
                 }
+                if (s == AHEAD - 1) fetch_v(0);
                 if (ok && s >= AHEAD) {
                     const int t = s - AHEAD;
                     const bool scrub = (t0 + t + 1) * TK > safe;
@@ -480,8 +507,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                         if (!slot_free(pos)) break;
                         put(vc[j], vs[j], Ring + (pos % NSLOT) * SLOT + (v_col >> 6) * VSLAB, v_tok, v_col, scrub);
                         slot_done(pos);
-                        if (t + 1 < n) fetch_v(t + 1, j);
                     }
+                    if (t + 1 < n) fetch_v(t + 1);
                 }
             }
         } else {
@@ -498,13 +525,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                     for (int e = 0; e < 8; ++e)
                         w[e] = row >= 0 ? __ldg((const uint4 *)(lat + row * P.ld_kv + rank * 256 + q * 64) + e)
                                         : make_uint4(0, 0, 0, 0);
-                    if (!slot_free(pos)) break;
-                    uint8_t *dst = Ring + (pos % NSLOT) * SLOT + q * VSLAB + tok * 128;
+                    // a warp whose wait gave up comes to the barrier all the same, and they stop together
+                    if (slot_free(pos)) {
+                        uint8_t *dst = Ring + (pos % NSLOT) * SLOT + q * VSLAB + tok * 128;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        *(uint4 *)(dst + ((e ^ (tok & 7)) << 4)) =
-                            make_uint4(finite2(w[e].x), finite2(w[e].y), finite2(w[e].z), finite2(w[e].w));
-                    slot_done(pos);
+                        for (int e = 0; e < 8; ++e)
+                            *(uint4 *)(dst + ((e ^ (tok & 7)) << 4)) =
+                                make_uint4(finite2(w[e].x), finite2(w[e].y), finite2(w[e].z), finite2(w[e].w));
+                        tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
+                    }
+                    if (!(ok = bar_and<2>(ok))) break;
+                    if (tid == 0) tc::mbar_arrive_remote(leader(&bar->full[pos % NSLOT]));
                 }
         }
     } else if (warp < 4) {
@@ -589,7 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             }
             float *ex = mx + (t & 1) * 128;
             ex[threadIdx.x] = mt;
-            if (!(ok = soft_bar_and(ok))) break;
+            if (!(ok = bar_and<1>(ok))) break;
             mt = fmaxf(mt, ex[threadIdx.x ^ 64]) * sl2;
             float m_new = m;
             bool rescale = false;
@@ -889,24 +920,33 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
     const uint64_t rows = (uint64_t)std::max<int64_t>(c->rows, 1);
     P.oob = (int)rows;
     const bool kv8 = c->dtype == DSA_E4M3;
-    const int box = pt.table && pt.page % 32 ? 16 : 32;
-    CUtensorMap tq, tqpe, tkv, tpe;
-    const auto map2 = [](CUtensorMap *m, const void *base, int cols, uint64_t n_rows, int64_t ld, int box_rows) {
-        const uint64_t dims[2] = {(uint64_t)cols, n_rows}, strides[1] = {(uint64_t)ld * 2};
-        const uint32_t bx[2] = {64, (uint32_t)box_rows};
+    // Tokens that lie together: all of a K slot's 64 (contiguous caches, pages of 64), or fewer.
+    const int run = !pt.table || pt.page % 64 == 0 ? 64 : pt.page % 32 == 0 ? 32 : 16;
+    CUtensorMap tq, tqpe, tk, tv, tpe;
+    const auto map2 = [](CUtensorMap *m, const void *base, int cols, uint64_t n_rows) {
+        const uint64_t dims[2] = {(uint64_t)cols, n_rows}, strides[1] = {(uint64_t)cols * 2};
+        const uint32_t bx[2] = {64, HR};
         return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, bx);
     };
-    if (!map2(&tq, qt, DC, (uint64_t)N * H, DC, HR) || !map2(&tqpe, qpe, DR, (uint64_t)N * H, DR, HR) ||
-        !map2(&tpe, c->k_pe, DR, rows, c->ld_pe, box))
+    // Cache rows as slabs of 64 columns: (column, row, slab).
+    const auto map3 = [&](CUtensorMap *m, const void *base, int cols, int64_t ld, int box_rows, int box_slabs) {
+        const uint64_t dims[3] = {64, rows, (uint64_t)cols / 64}, strides[2] = {(uint64_t)ld * 2, 128};
+        const uint32_t bx[3] = {64, (uint32_t)box_rows, (uint32_t)box_slabs};
+        return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, bx);
+    };
+    if (!map2(&tq, qt, DC, (uint64_t)N * H) || !map2(&tqpe, qpe, DR, (uint64_t)N * H) ||
+        !map3(&tpe, c->k_pe, DR, c->ld_pe, run, 1))
         return cudaErrorInvalidValue;
-    if (kv8) tkv = tpe;  // not used
-    else if (!map2(&tkv, c->kv, DC, rows, c->ld_kv, box)) return cudaErrorInvalidValue;
+    if (kv8) tk = tv = tpe;  // not used
+    else if (!map3(&tk, c->kv, DC, c->ld_kv, run, run == HR ? 2 : 1) ||
+             !map3(&tv, c->kv, DC, c->ld_kv, std::min(run, VCH), run >= VCH ? 4 : 1))
+        return cudaErrorInvalidValue;
     float *opart = (float *)part_ws, *lpart = (float *)((char *)part_ws + part_bytes(plan));
     auto kern = kv8 ? tree_tc_kernel<true> : tree_tc_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)(2 * unit)), dim3(kv8 ? Cfg<true>::THREADS : Cfg<false>::THREADS), SMEM, s, tq,
-                   tqpe, tkv, tpe, box, (const void *)c->kv, (const float *)c->kv_scale, P, (__nv_bfloat16 *)olat, lse,
+                   tqpe, tk, tv, tpe, run, (const void *)c->kv, (const float *)c->kv_scale, P, (__nv_bfloat16 *)olat, lse,
                    opart, lpart);
     if (e != cudaSuccess) return e;
     note_launch(DSA_KERNEL_TREE_TC);
