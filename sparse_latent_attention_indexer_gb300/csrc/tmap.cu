@@ -25,7 +25,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }  // namespace
 
 bool make_tmap(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const uint64_t *dims,
-               const uint64_t *strides_bytes, const uint32_t *box) {
+               const uint64_t *strides_bytes, const uint32_t *box, CUtensorMapSwizzle swizzle) {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t gdim[5], gstride[4];
@@ -37,7 +37,7 @@ bool make_tmap(CUtensorMap *map, CUtensorMapDataType type, int rank, const void 
     }
     for (int i = 0; i < rank - 1; ++i) gstride[i] = strides_bytes[i];
     CUresult r = fn(map, type, (cuuint32_t)rank, const_cast<void *>(base), gdim, gstride, bdim, estride,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }

@@ -8,33 +8,33 @@
 // the mask is the tree's.)
 //
 // Work unit: 128 rows of one sequence (nodes x heads are rows of one matrix: every
-// head reads the same latent) times a range of its tokens, on a pair of SMs.
-// The context of 128 x 512 fp32 values would fill one SM's tensor memory, so
-// the pair runs every MMA together (cta_group::2, M = 128): CTA c holds rows
-// 64c .. 64c+63 and leaves half of its tensor memory to three score buffers.  A row
-// then lives in one SM: its softmax needs nothing from the other one.
-//   * QK^T (N = 128 tokens): CTA c brings the 64 tokens 64c.. of the tile, all 576
-//     columns, in 64-column slabs.
-//   * PV (N = 256 columns, twice): CTA c brings columns 256c.. of all 128 tokens, in
-//     chunks of 32 tokens.
-//   The quarter of the tile that a CTA needs in both forms is loaded twice: L2
-//   delivers 73 B/clk/SM (measured), the copy costs 16 of the 45 that the kernel
-//   takes, and in exchange slabs and chunks pass through one ring of 16 KB slots in
-//   the order the MMAs use them, so no operand waits in shared memory for a softmax.
-//   * The MMA thread issues QK^T two tiles ahead of PV, which hides a whole
-//     softmax; P (bf16) goes through two shared-memory buffers.
-//   * Softmax: four warps, lane l of the tensor memory is row l % 64 and tokens
-//     64 (l / 64) ..; the two halves of a row meet once per tile for its maximum.  The
-//     running maximum moves (and the context is rescaled) only when a tile exceeds
-//     it by more than 2^8.
-//   * bf16 caches arrive by TMA; e4m3 caches are read by eight warps that hold a whole
-//     tile of codes in registers, dequantise (exact in bf16) and store it swizzled.
-//   * A token that some row does not see may hold anything, and 0 x NaN is NaN: the
-//     V chunks of tiles with hidden tokens are loaded through registers, where
-//     Inf and NaN become 0.  Scores of hidden tokens are replaced after the MMA.
-// Bound by shared memory: per 128 tokens a CTA's MMAs read 240 KB (A again for every 64
-// columns), copies write 139 KB and P 16 KB, 3.1K cycles at 128 B/clk against 2.2K
-// of MMA.
+// head reads the same latent) times a range of its tokens.  The context of
+// 128 x 512 fp32 values would fill an SM's tensor memory, so two CTAs on two
+// SMs share a unit by columns: CTA c owns latent columns 256c.. and rotary columns
+// 32c.. of every row and token.  A tile is 64 tokens.
+//   * Each CTA multiplies its columns: a partial score tile (q~ slice resident in
+//     tensor memory as the A operand, so QK^T reads only the tokens from shared
+//     memory).  CTA c finishes rows 64c .. 64c+63: the other CTA sends it its partial
+//     scores of those rows (fp16 of the log2-scaled values, 8 KB), it adds its own in
+//     fp32, runs the softmax and sends the probabilities (bf16, 8 KB) back, which both
+//     need for PV.  Nothing is computed twice, and a row's maximum and sum live in
+//     one place.
+//   * Eight softmax warps in two groups that take alternate tiles.  Tensor-memory
+//     lanes are rows, so in each group two warps finish the CTA's own rows (a thread
+//     a row) and two send the other rows' partial scores and then watch for the
+//     probabilities that come back.
+//   * Lazy rescaling: a row's reference maximum moves only when a tile exceeds it by
+//     more than 2^8; the factor travels with the probabilities, and both CTAs rescale
+//     their half of the context.
+//   * bf16 caches arrive by TMA (two copies a tile where 64 tokens lie together); of e4m3
+//     caches four warps keep the next tile's codes in registers, dequantise (exact in
+//     bf16) and store them swizzled.
+//   * A token that some row does not see may hold anything, and 0 x NaN is NaN: tiles
+//     with hidden tokens are loaded through registers, where Inf and NaN become 0.
+//     Scores of hidden tokens are replaced after the MMA.
+// Bound by shared memory and by the length of a tile's chain (score, exchange, softmax,
+// exchange) over four stages of tokens: per tile a CTA's MMAs take 1088 cycles and its
+// shared-memory traffic (MMA operands 92 KB, copies 37, scores and probabilities 64) 1.5K.
 //
 // Waits are bounded; a timeout records its site in the device error word and
 // both CTAs drain and exit.
@@ -48,39 +48,52 @@ __device__ int g_tree_tc_error = 0;
 
 namespace {
 
-constexpr int ROWS = 128;               // rows of a unit (MMA M, 64 per CTA)
-constexpr int HR = 64;                  // rows of a CTA
+constexpr int ROWS = 128;               // rows of a unit (MMA M)
+constexpr int HR = 64;                  // rows that a CTA finishes
 constexpr int DC = 512, DR = 64;
-constexpr int TK = 128;                 // tokens of a tile
-constexpr int SLAB = HR * 128;          // 64 rows or tokens x 64 columns, 128-byte swizzle: 8 KB
-constexpr int NQ = (DC + DR) / 64;      // slabs of a row
-constexpr int SLOT = 16384;             // two K slabs, the rotary slab (half a slot), or 32 tokens x 256 columns of V
-constexpr int K_SLOTS = 5, V_SLOTS = 4; // slots of a tile
-constexpr int VCH = TK / V_SLOTS;       // tokens of a V chunk
-constexpr int VSLAB = VCH * 128;        // 64 columns of a V chunk
-constexpr int NSLOT = 7;
-constexpr int P_BYTES = HR * TK * 2;
-constexpr int AHEAD = 2;                // tiles that QK^T runs ahead of PV
-constexpr int NS = AHEAD + 1;           // score buffers
+constexpr int TK = 64;                  // tokens of a tile
+constexpr int SLAB = TK * 128;          // 64 tokens x 64 columns, 128-byte swizzle: 8 KB
+constexpr int ROPE = TK * 64;           // 64 tokens x 32 rotary columns, 64-byte swizzle: 4 KB
+constexpr int STAGE = 4 * SLAB + ROPE;  // a CTA's columns of a tile
+constexpr int NSTAGE = 4;
+constexpr int P_BYTES = ROWS * TK * 2;  // probabilities of all rows
+constexpr int X_BYTES = HR * TK * 2;    // fp16 partial scores of half of the rows
+constexpr int Q_BOX = ROWS * 128;       // 128 rows x 64 columns of q~ (staged in the exchange buffers)
+constexpr int QR_BYTES = ROWS * 64;     // rotary slice of the queries, 64-byte swizzle
 constexpr int NMASK = 8;
-constexpr uint32_t COL_O = 0, COL_S = 256;
+constexpr uint32_t COL_S = 0, COL_Q = 128, COL_O = 256;
 constexpr uint32_t IDESC_QK = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, ROWS, TK, 0, 0);
 constexpr uint32_t IDESC_PV = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, ROWS, 256, 0, 1);
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr long long kAbortQuietCycles = 1LL << 18;
 constexpr int PAIRS = 76;               // 152 SMs
+// warp 0: TMA; 1: QK^T; 2: tensor memory, PV; 4-7, 8-11: softmax groups (warp % 4 = lane quarter); 12-15: loading
+constexpr int THREADS = 512;
 
+// [g]: softmax group = tile parity.
 struct Bars {
-    uint64_t q_full, full[NSLOT], empty[NSLOT], go[NSLOT], s_full[NS], s_empty[NS], p_full[2], p_empty[2], mask_full[NMASK], o_done,
-        drain;
+    uint64_t q_stage, q_ready, peer_ready, kv_full[NSTAGE], kv_empty[NSTAGE], go[NSTAGE], s_full[2], s_empty[2];
+    uint64_t x_full[2], x_free[2];    // the other CTA's partial scores are here; it has read ours
+    uint64_t p_in[2], pv_peer[2];     // the other CTA's probabilities are here; its PV product is done with ours
+    uint64_t p_full[2], p_empty[2], hand[2][2], mask_full[NMASK], qk_done, o_done;
 };
-constexpr int MISC = 2 * 128 * 4 + NMASK * 16 + (int)sizeof(Bars) + 16;
-constexpr int SMEM = 1024 + NQ * SLAB + 2 * P_BYTES + NSLOT * SLOT + MISC;
+struct Misc {
+    float m_pub[2][HR];               // reference maximum that a group used, for the other group
+    float alpha_out[2][HR], alpha_in[2][HR];  // context factors of a tile, of this CTA's rows and of the other's
+    float sum[2][HR], ref[2][HR];     // a group's share of the row sum and its reference
+    float inv[ROWS];                  // 1 / row sum
+    uint64_t live[NMASK];             // tokens of a tile whose page exists
+    Bars bar;
+    uint32_t tmem_slot;
+    int abort_flag, never;
+};
+constexpr int SMEM = 1024 + NSTAGE * STAGE + 2 * P_BYTES + 4 * X_BYTES + QR_BYTES + (int)sizeof(Misc);
 static_assert(SMEM <= 232448, "shared memory per CTA");
-// The epilogue stages 64 rows of the context, 16 bytes apart from a power of two, where P and the ring were.
-constexpr int OUT_LD_F32 = DC * 4 + 16, OUT_LD_BF16 = DC * 2 + 16;
-static_assert(HR * OUT_LD_F32 <= 2 * P_BYTES + NSLOT * SLOT, "staged context");
+static_assert(4 * Q_BOX <= 2 * P_BYTES + 4 * X_BYTES, "the q~ slice is staged in the exchange buffers");
+// The epilogue stages a CTA's 256 columns, rows 16 bytes apart from a power of two, in the token stages.
+constexpr int OUT_LD_F32 = 256 * 4 + 16, OUT_LD_BF16 = 256 * 2 + 16;
+static_assert(ROWS * OUT_LD_F32 <= NSTAGE * STAGE, "staged context");
 
 // Sequences in the order of the units (the longest units first).
 struct TreeParams {
@@ -96,11 +109,11 @@ struct TreeParams {
     const uint64_t *mask;
     int words, H;
     int oob;                     // a cache row past the last one
-    int64_t ld_kv;
+    int64_t ld_kv, ld_pe;
     float scale_log2;
     long long wait_limit;
 };
-static_assert(sizeof(TreeParams) + 5 * 128 + 128 <= 32764, "launch parameters");
+static_assert(sizeof(TreeParams) + 3 * 128 + 128 <= 32764, "launch parameters");
 
 // One 16-bit pair per word: bf16 Inf and NaN become 0.
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
@@ -158,56 +171,72 @@ __device__ __forceinline__ void dequant16(const uint4 &c, const Scale2 &s, uint4
     o[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// Four warps (1: softmax, 2: loading) arrive at barrier ID; returns the AND of `v` over them.
-template <int ID>
+// COUNT threads arrive at barrier ID; returns the AND of `v` over them.
+template <int ID, int COUNT>
 __device__ __forceinline__ bool bar_and(bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.and.pred p, %2, 128, q;\n\t"
+        "bar.red.and.pred p, %2, %3, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v), "n"(ID)
+        : "r"((uint32_t)v), "n"(ID), "n"(COUNT)
         : "memory");
     return r != 0;
 }
 
-// Position of a tile's first slot in the unit's sequence of slots: step s brings K(s), then V(s - AHEAD).
-__device__ __forceinline__ int k_pos(int t) { return K_SLOTS * t + V_SLOTS * max(0, t - AHEAD); }
-__device__ __forceinline__ int v_pos(int t, int n) { return K_SLOTS * min(t + AHEAD + 1, n) + V_SLOTS * t; }
+// O[rows of this warp] *= alpha (tcgen05.ld/st are warp-wide: rows that stay take a factor of 1).
+__device__ __forceinline__ void rescale_rows(uint32_t lanes, float alpha) {
+    tc::tc_fence_after();
+#pragma unroll 1
+    for (int cc = 0; cc < 8; ++cc) {
+        float o[32];
+        uint32_t ob[32];
+        tc::tmem_ld32(lanes + COL_O + cc * 32, o);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) ob[j] = __float_as_uint(o[j] * alpha);
+        tc::tmem_st32(lanes + COL_O + cc * 32, ob);
+    }
+    tc::tmem_st_wait();
+    tc::tc_fence_before();
+}
+
+// Maximum of 64 values as a tree (depth 4).
+__device__ __forceinline__ float max64(const float (&v)[64]) {
+    float a[22], b[8];
+#pragma unroll
+    for (int i = 0; i < 21; ++i) a[i] = tc::max3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+    a[21] = v[63];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) b[i] = tc::max3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
+    b[7] = a[21];
+    return tc::max3(tc::max3(b[0], b[1], b[2]), tc::max3(b[3], b[4], b[5]), fmaxf(b[6], b[7]));
+}
 
 template <bool KV8>
-struct Cfg {
-    static constexpr int NLOAD = KV8 ? 8 : 4;  // loading warps
-    static constexpr int ARRIVE = KV8 ? 8 : 1; // arrivals of a CTA on a full slot
-    static constexpr int THREADS = 32 * (6 + NLOAD);
-};
-
-template <bool KV8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1)
-    tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qpe,
-                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const __grid_constant__ CUtensorMap tm_pe, int run,
-                   const void *__restrict__ kv, const float *__restrict__ kv_scale,
-                   const __grid_constant__ TreeParams P, __nv_bfloat16 *__restrict__ olat, float *__restrict__ lse,
-                   float *__restrict__ opart, float *__restrict__ lpart) {
-    constexpr int ARRIVE = Cfg<KV8>::ARRIVE;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                   const __grid_constant__ CUtensorMap tm_pe, int run, const void *__restrict__ kv,
+                   const float *__restrict__ kv_scale, const __nv_bfloat16 *__restrict__ kpe,
+                   const __nv_bfloat16 *__restrict__ qpe, const __grid_constant__ TreeParams P,
+                   __nv_bfloat16 *__restrict__ olat, float *__restrict__ lse, float *__restrict__ opart,
+                   float *__restrict__ lpart) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *Q = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t *Pb = Q + NQ * SLAB;
-    uint8_t *Ring = Pb + 2 * P_BYTES;
-    float *mx = (float *)(Ring + NSLOT * SLOT);              // [2][128] tile maxima, then row sums
-    uint64_t *live = (uint64_t *)(mx + 256);                 // [NMASK][2] tokens whose page exists
-    Bars *bar = (Bars *)(live + 2 * NMASK);
-    uint32_t *tmem_slot = (uint32_t *)(bar + 1);
-    volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
-    __shared__ int never;
-    volatile int *nv = (volatile int *)&never;
+    uint8_t *KV = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *Pb = KV + NSTAGE * STAGE;   // [g] probabilities: rows x 64 tokens, 128-byte swizzle
+    uint8_t *X = Pb + 2 * P_BYTES;       // [g] the other CTA's partial scores of this CTA's rows
+    uint8_t *Y = X + 2 * X_BYTES;        // [g] this CTA's partial scores of the other's rows, sent from here
+    uint8_t *QR = Y + 2 * X_BYTES;       // rotary slice of the queries
+    Misc *ms = (Misc *)(QR + QR_BYTES);
+    Bars *bar = &ms->bar;
+    volatile int *abort_flag = (volatile int *)&ms->abort_flag, *nv = (volatile int *)&ms->never;
     int *err = &g_tree_tc_error;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = tc::cluster_rank();
+    const unsigned FULL = 0xffffffffu;
+    const uint32_t rank = tc::cluster_rank(), peer = rank ^ 1u;
 
     // ---- the unit: rows row0 .. of a sequence, tiles t0 .. t0 + n - 1 of its tokens ----
     const int u = (int)(blockIdx.x >> 1);
@@ -232,476 +261,503 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
     const int n = max(0, min((tokens + TK - 1) / TK, t0 + per) - t0);
 
     if (threadIdx.x == 0) {
-        tc::mbar_init(&bar->q_full, 2);
-        for (int i = 0; i < NSLOT; ++i) {
-            tc::mbar_init(&bar->full[i], 2 * ARRIVE);
-            tc::mbar_init(&bar->empty[i], 1);
+        tc::mbar_init(&bar->q_stage, 1);
+        tc::mbar_init(&bar->q_ready, 8);
+        tc::mbar_init(&bar->peer_ready, 1);
+        for (int i = 0; i < NSTAGE; ++i) {
+            tc::mbar_init(&bar->kv_full[i], KV8 ? 4 : 1);
+            tc::mbar_init(&bar->kv_empty[i], 1);
             tc::mbar_init(&bar->go[i], 1);
         }
-        for (int i = 0; i < NS; ++i) {
-            tc::mbar_init(&bar->s_full[i], 1);
-            tc::mbar_init(&bar->s_empty[i], 8);       // the softmax warps of both CTAs
-        }
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bar->p_full[i], 8);
-            tc::mbar_init(&bar->p_empty[i], 1);
+        for (int g = 0; g < 2; ++g) {
+            tc::mbar_init(&bar->s_full[g], 1);
+            tc::mbar_init(&bar->s_empty[g], 4);  // the group's warps have read the scores
+            tc::mbar_init(&bar->x_full[g], 1);   // armed here with what the other CTA sends
+            tc::mbar_init(&bar->x_free[g], 2);   // its two finishing warps
+            tc::mbar_init(&bar->p_in[g], 1);
+            tc::mbar_init(&bar->pv_peer[g], 1);
+            tc::mbar_init(&bar->p_full[g], 4);
+            tc::mbar_init(&bar->p_empty[g], 1);
+            tc::mbar_init(&bar->hand[0][g], 1);
+            tc::mbar_init(&bar->hand[1][g], 1);
         }
         for (int i = 0; i < NMASK; ++i) tc::mbar_init(&bar->mask_full[i], 1);
+        tc::mbar_init(&bar->qk_done, 1);
         tc::mbar_init(&bar->o_done, 1);
-        tc::mbar_init(&bar->drain, 1);
         *abort_flag = 0;
-        never = 0;
+        ms->never = 0;
         tc::fence_mbar_init();
     }
-    if (warp == 5) {
-        tc::tmem_alloc_pair(tmem_slot, 512);
-        tc::tmem_relinquish_pair();
+    if (warp == 2) {
+        tc::tmem_alloc(&ms->tmem_slot, 512);
+        tc::tmem_relinquish();
     }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     tc::cluster_sync();  // both CTAs' barriers exist before any remote arrive
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = ms->tmem_slot;
     pdl_wait();  // the set-up above overlapped the previous kernel; global memory only from here
 
-    const auto leader = [&](uint64_t *p) { return tc::map_peer(tc::smem_u32(p), 0); };
     // Cache row of token s, or -1 (behind the last token, or on no page).
     const auto row_of = [&](int s) -> int64_t { return s < tokens ? cache_row(P.pt, b, kbase, s) : -1; };
-
-    // ---- one warp's work: TMA copies of the cache ----
-    // Rows of a tile's eight runs of 16 tokens, a run a lane: its cache row, -1 behind the last token, or the row past
+    // Rows of a tile's four runs of 16 tokens, a run a lane: its cache row, -1 behind the last token, or the row past
     // the cache (read as zeros) where there is no page.
     const auto runs_of = [&](int t) {
-        const int s = (t0 + t) * TK + (lane & 7) * 16;
+        const int s = (t0 + t) * TK + (lane & 3) * 16;
         const int64_t r = row_of(s);
         return t >= n || s >= tokens ? -1 : r >= 0 ? (int)r : P.oob;
     };
-    // `ntok` tokens from run r0 on, `parts` slabs of 64 columns from column slab x0 on.  A copy takes `run` tokens;
-    // where that is all of them it takes all slabs at once.
-    const auto slot_copy = [&](int pos, const CUtensorMap *map, int parts, int slab_bytes, int ntok, int rows, int r0,
-                               int x0) {
-        const int st = pos % NSLOT;
-        const uint32_t fb = leader(&bar->full[st]), dst = tc::smem_u32(Ring + st * SLOT);
-        const int each = min(run, ntok), at_once = run >= ntok ? parts : 1;
-        const int copies = (ntok / each) * (parts / at_once);
-        const int k = lane / (parts / at_once), j = lane - k * (parts / at_once);  // this lane's copy: tokens, slab
-        const int row = __shfl_sync(0xffffffffu, rows, (r0 + k * (each / 16)) & 7);
-        const bool go = lane < copies && row >= 0;
-        const int some = __popc(__ballot_sync(0xffffffffu, go));
-        if (lane == 0) tc::mbar_arrive_expect_tx_remote(fb, (uint32_t)(some * each * at_once * 128));
-        __syncwarp();
-        if (go) tc::tma_load_3d_pair(dst + j * slab_bytes + k * each * 128, map, fb, 0, row, x0 + j);
-    };
-    // Publishes which of tile t's tokens have a page.
+    // Publishes which of tile t's tokens have a page (one warp).
     const auto put_mask = [&](int t, int rows) {
         if (!P.pt.table) return;
-        const unsigned have = __ballot_sync(0xffffffffu, rows >= 0 && rows != P.oob);
-        if (lane < 2) {
+        const unsigned have = __ballot_sync(FULL, rows >= 0 && rows != P.oob);
+        if (lane == 0) {
             uint64_t m = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (have >> (4 * lane + i) & 1) m |= 0xffffull << 16 * i;
-            live[2 * (t % NMASK) + lane] = m;
+                if (have >> i & 1) m |= 0xffffull << 16 * i;
+            ms->live[t % NMASK] = m;
+            tc::mbar_arrive(&bar->mask_full[t % NMASK]);
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar->mask_full[t % NMASK]);
     };
 
-    if (warp == 4 && n > 0) {
-        // ---------------- producer: Q; of a bf16 cache K and V ----------------
+    if (warp == 0 && n > 0) {
+        // ---------------- TMA: the q~ slice (staged in the exchange buffers), then a bf16 cache's tiles ----------------
         if (lane == 0) {
-            const uint32_t qb = leader(&bar->q_full);
-            tc::mbar_arrive_expect_tx_remote(qb, NQ * SLAB);
-            const int y = (int)(seq_row0 + lrow + rank * HR);
-            for (int j = 0; j < DC / 64; ++j) tc::tma_load_2d_pair(tc::smem_u32(Q + j * SLAB), &tm_q, qb, j * 64, y);
-            tc::tma_load_2d_pair(tc::smem_u32(Q + (NQ - 1) * SLAB), &tm_qpe, qb, 0, y);
+            tc::mbar_arrive_expect_tx(&bar->q_stage, 4 * Q_BOX);
+            for (int j = 0; j < 4; ++j)
+                tc::tma_load_2d(Pb + j * Q_BOX, &tm_q, &bar->q_stage, rank * 256 + j * 64, (int)(seq_row0 + lrow));
         }
         __syncwarp();
-        // Who waits for slots waits for every one in turn: a barrier's phase can be told from its neighbours only.  So the
-        // producer also waits for the slots that the loading warps fill, and hands them on.
-        const auto slot_wait = [&](int pos) {
-            return __all_sync(0xffffffffu, tc::mbar_wait(&bar->empty[pos % NSLOT], ((pos / NSLOT) & 1) ^ 1, abort_flag,
-                                                         err, 101, P.wait_limit));
-        };
-        bool ok = true;
-        int rows[AHEAD + 2];  // of tiles s - AHEAD .. s + 1
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) rows[i] = -1;
-        rows[AHEAD] = runs_of(0);
-        for (int s = 0; !KV8 && ok && s < n + AHEAD; ++s) {
-            rows[AHEAD + 1] = runs_of(s + 1);
-            if (s < n) {
-                put_mask(s, rows[AHEAD]);
-                for (int j = 0; ok && j < K_SLOTS; ++j) {
-                    if (!(ok = slot_wait(k_pos(s) + j))) break;
-                    if (j < K_SLOTS - 1) slot_copy(k_pos(s) + j, &tm_k, 2, SLAB, HR, rows[AHEAD], rank * 4, 2 * j);
-                    else slot_copy(k_pos(s) + j, &tm_pe, 1, SLAB, HR, rows[AHEAD], rank * 4, 0);
+        if constexpr (!KV8) {
+            // Lane's copy: latents of run k (all four slabs at once where 64 tokens lie together), or rotary columns.
+            const int runs = TK / run, nlat = runs == 1 ? 1 : 4 * runs;
+            const bool lat = lane < nlat;
+            const int k = lat ? (runs == 1 ? 0 : lane >> 2) : lane - nlat, j = lat && runs > 1 ? lane & 3 : 0;
+            int rows = runs_of(0);
+            bool ok = true;
+            for (int t = 0; ok && t < n; ++t) {
+                const int st = t % NSTAGE;
+                // Who waits for stages waits for every one in turn (a barrier's phase can be told from its neighbours only):
+                // the stages that the loading warps fill are handed on to them.
+                ok = __all_sync(FULL, tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 101, P.wait_limit));
+                if (!ok) break;
+                put_mask(t, rows);
+                if ((t0 + t + 1) * TK > safe) {
+                    if (lane == 0) tc::mbar_arrive(&bar->go[st]);
+                } else {
+                    // every token of the tile exists
+                    const int row = __shfl_sync(FULL, rows, (k * (run / 16)) & 3);
+                    if (lane == 0) tc::mbar_arrive_expect_tx(&bar->kv_full[st], STAGE);
+                    __syncwarp();
+                    uint8_t *dst = KV + st * STAGE;
+                    if (lat) tc::tma_load_3d(dst + j * SLAB + k * run * 128, &tm_kv, &bar->kv_full[st], 0, row, rank * 4 + j);
+                    else if (k < runs) tc::tma_load_2d(dst + 4 * SLAB + k * run * 64, &tm_pe, &bar->kv_full[st], rank * 32, row);
                 }
+                rows = runs_of(t + 1);
             }
-            if (s >= AHEAD) {
-                const int t = s - AHEAD;
-                const bool pass = (t0 + t + 1) * TK > safe;  // tiles with hidden tokens: the loading warps
-                for (int j = 0; ok && j < V_SLOTS; ++j) {
-                    const int pos = v_pos(t, n) + j;
-                    if (!(ok = slot_wait(pos))) break;
-                    if (!pass) slot_copy(pos, &tm_v, 4, VSLAB, VCH, rows[0], 2 * j, rank * 4);
-                    else if (lane == 0) tc::mbar_arrive(&bar->go[pos % NSLOT]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i <= AHEAD; ++i) rows[i] = rows[i + 1];
         }
-    } else if (warp == 5 && rank == 0 && lane == 0 && n > 0) {
-        // ---------------- MMA issuer (of the pair) ----------------
-        // Descriptors are a base plus (bytes >> 4): the issuing thread has little time between MMAs.
-        const uint64_t qd = tc::smem_desc(tc::smem_u32(Q), 16, 1024), pd = tc::smem_desc(tc::smem_u32(Pb), 16, 1024);
-        const uint64_t kd = tc::smem_desc(tc::smem_u32(Ring), 16, 1024), vd = tc::smem_desc(tc::smem_u32(Ring), VSLAB, 1024);
-        const uint16_t both = 3;
-        bool ok = tc::mbar_wait(&bar->q_full, 0, abort_flag, err, 102, P.wait_limit);
-        int st = 0;
-        uint32_t ring_ph = 0;
-        const auto slot_ready = [&]() {
-            const bool r = tc::mbar_wait(&bar->full[st], ring_ph, abort_flag, err, 103, P.wait_limit);
+    } else if (warp == 1 && lane == 0 && n > 0) {
+        // ---------------- QK^T issuer: tile t into score buffer t % 2 once its tokens are here ----------------
+        // (PV comes from another thread: an issue blocks while the tensor pipe is busy.)
+        const uint64_t kd = tc::smem_desc(tc::smem_u32(KV), 16, 1024);
+        const uint64_t rd = tc::smem_desc(tc::smem_u32(KV) + 4 * SLAB, 16, 512, tc::kSwizzle64B);
+        const uint64_t qd = tc::smem_desc(tc::smem_u32(QR), 16, 512, tc::kSwizzle64B);
+        bool ok = tc::mbar_wait(&bar->q_ready, 0, abort_flag, err, 102, P.wait_limit);
+        for (int t = 0; ok && t < n; ++t) {
+            const int st = t % NSTAGE;
+            if (t >= 2 && !(ok = tc::mbar_wait(&bar->s_empty[t & 1], ((t >> 1) - 1) & 1, abort_flag, err, 103, P.wait_limit))) break;
+            if (!(ok = tc::mbar_wait(&bar->kv_full[st], (t / NSTAGE) & 1, abort_flag, err, 104, P.wait_limit))) break;
             tc::tc_fence_after();
-            return r;
-        };
-        const auto slot_used = [&]() {
-            tc::mma_commit_pair(&bar->empty[st], both);
-            if (++st == NSLOT) {
-                st = 0;
-                ring_ph ^= 1;
-            }
-        };
-        for (int s = 0; ok && s < n + AHEAD; ++s) {
-            if (s < n) {
-                const int sb = s % NS;
-                if (s >= NS && !(ok = tc::mbar_wait(&bar->s_empty[sb], ((s / NS) - 1) & 1, abort_flag, err, 104, P.wait_limit))) break;
-                const uint32_t d = tmem + COL_S + sb * (TK / 2);
+            const uint32_t d = tmem + COL_S + (t & 1) * TK;
+            const uint64_t off = (uint64_t)(uint32_t)(st * (STAGE / 16));
 #pragma unroll
-                for (int j = 0; j < K_SLOTS; ++j) {
-                    if (!(ok = slot_ready())) break;
-                    const uint64_t b0 = kd + (uint64_t)(uint32_t)(st * (SLOT / 16));
+            for (int i = 0; i < 16; ++i)
+                tc::mma_f16_ts(d, tmem + COL_Q + i * 8, kd + off + ((i >> 2) * SLAB + (i & 3) * 32) / 16, IDESC_QK, i != 0);
 #pragma unroll
-                    for (int i = 0; i < (j < K_SLOTS - 1 ? 8 : 4); ++i)  // slab i / 4, 16 columns each
-                        tc::mma_f16_pair(d, qd + ((2 * j + (i >> 2)) * SLAB + (i & 3) * 32) / 16,
-                                         b0 + ((i >> 2) * SLAB + (i & 3) * 32) / 16, IDESC_QK, (j | i) != 0);
-                    slot_used();
-                }
-                if (!ok) break;
-                tc::mma_commit_pair(&bar->s_full[sb], both);
-            }
-            if (s >= AHEAD) {
-                const int t = s - AHEAD, pb = t & 1;
-                if (!(ok = tc::mbar_wait(&bar->p_full[pb], (t >> 1) & 1, abort_flag, err, 105, P.wait_limit))) break;
-                tc::tc_fence_after();
-                const uint64_t a0 = pd + (uint64_t)(uint32_t)(pb * (P_BYTES / 16));
-#pragma unroll
-                for (int j = 0; j < V_SLOTS; ++j) {
-                    if (!(ok = slot_ready())) break;
-                    const uint64_t b0 = vd + (uint64_t)(uint32_t)(st * (SLOT / 16));
-#pragma unroll
-                    for (int i = 0; i < 2 * (VCH / 16); ++i) {  // 16 tokens i / 2, columns of half i % 2
-                        const int key = j * VCH + (i >> 1) * 16;
-                        tc::mma_f16_pair(tmem + COL_O + (i & 1) * 128, a0 + ((key >> 6) * SLAB + (key & 63) * 2) / 16,
-                                         b0 + ((i & 1) * 2 * VSLAB + (i >> 1) * 16 * 128) / 16, IDESC_PV,
-                                         (t | j | (i >> 1)) != 0);
-                    }
-                    slot_used();
-                }
-                if (!ok) break;
-                tc::mma_commit_pair(&bar->p_empty[pb], both);
-            }
+            for (int i = 0; i < 2; ++i) tc::mma_f16(d, qd + i * 2, rd + off + i * 2, IDESC_QK, 1);
+            tc::mma_commit(&bar->s_full[t & 1]);
         }
-        // No MMA may still be running when the tensor memory is released, whatever stopped the loop.
-        if (ok) tc::mma_commit_pair(&bar->o_done, both);
-        tc::mma_commit_pair(&bar->drain, 1);
-        tc::mbar_wait(&bar->drain, 0, nv, err, 106);
-    } else if (warp >= 6 && n > 0) {
-        // ---------------- loading warps ----------------
-        const int tid = threadIdx.x - 6 * 32;
-        bool ok = true;
-        uint32_t turn = 0;  // bf16: phase of every slot's `go`
-        const auto slot_free = [&](int pos) {
-            const int st = pos % NSLOT;
-            const uint32_t ph = KV8 ? ((pos / NSLOT) & 1) ^ 1 : (turn >> st) & 1u;
-            turn ^= 1u << st;
-            return ok = __all_sync(0xffffffffu, tc::mbar_wait(KV8 ? &bar->empty[st] : &bar->go[st], ph, abort_flag, err, 107,
-                                                              P.wait_limit));
-        };
-        if constexpr (KV8) {
-            // Thread (K): 32 columns of one of the CTA's 64 tokens; (V): 32 of its columns of one of the chunk's
-            // 32 tokens.  Codes are loaded a whole tile before they are needed.
-            const uint8_t *codes = (const uint8_t *)kv;
-            const int k_tok = tid >> 2, k_col = (tid & 3) * 32, v_tok = tid >> 3, v_col = (tid & 7) * 32;
-            uint4 kc[K_SLOTS - 1][2], vc[V_SLOTS][2];
-            float ks[K_SLOTS - 1], vs[V_SLOTS];
-            const auto slot_done = [&](int pos) {
-                tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive_remote(leader(&bar->full[pos % NSLOT]));
-            };
-            const auto fetch = [&](uint4 (&c)[2], float &sc, int64_t row, int col) {
-                c[0] = c[1] = make_uint4(0, 0, 0, 0);
-                sc = 0.0f;
-                if (row >= 0) {
-                    const uint4 *p = (const uint4 *)(codes + row * P.ld_kv + col);
-                    c[0] = __ldg(p);
-                    c[1] = __ldg(p + 1);
-                    sc = __ldg(kv_scale + row * (DC / 128) + (col >> 7));
-                }
-            };
-            const auto put = [&](const uint4 (&c)[2], float sc, uint8_t *dst, int tok, int col, bool scrub) {
-                // columns col .. col + 31 of a slab's 64: chunks c0 .. c0 + 3 of the token's 128-byte row
-                const Scale2 s2 = scale2(sc);
-                const int c0 = (col & 63) >> 3;
+        // No MMA of this thread may still be running when the tensor memory is released.
+        tc::mma_commit(&bar->qk_done);
+        tc::mbar_wait(&bar->qk_done, 0, nv, err, 105);
+    } else if (warp == 2 && lane == 0 && n > 0) {
+        // ---------------- PV issuer: frees the stage, the probabilities here and (the other CTA's copy) there ----------------
+        const uint64_t pd = tc::smem_desc(tc::smem_u32(Pb), 16, 1024), vd = tc::smem_desc(tc::smem_u32(KV), SLAB, 1024);
+        const uint16_t peer_mask = (uint16_t)(1u << peer);
+        for (int t = 0; t < n; ++t) {
+            if (!tc::mbar_wait(&bar->p_full[t & 1], (t >> 1) & 1, abort_flag, err, 106, P.wait_limit)) break;
+            tc::tc_fence_after();
+            const int st = t % NSTAGE;
+            const uint64_t a0 = pd + (uint64_t)(uint32_t)((t & 1) * (P_BYTES / 16));
+            const uint64_t b0 = vd + (uint64_t)(uint32_t)(st * (STAGE / 16));
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+            for (int kk = 0; kk < 4; ++kk)
+                tc::mma_f16(tmem + COL_O, a0 + kk * 2, b0 + kk * (16 * 128 / 16), IDESC_PV, (t | kk) != 0);
+            tc::mma_commit(&bar->kv_empty[st]);
+            tc::mma_commit(&bar->p_empty[t & 1]);
+            tc::mma_commit_multicast(&bar->pv_peer[t & 1], peer_mask);
+        }
+        tc::mma_commit(&bar->o_done);
+        tc::mbar_wait(&bar->o_done, 0, nv, err, 107);
+        tc::mbar_wait(&bar->q_stage, 0, nv, err, 108);  // after an abort nobody else may have waited for it
+    } else if (warp >= 12 && n > 0) {
+        // ---------------- loading warps ----------------
+        // Thread: one token, 128 of the CTA's 256 columns (two slabs), half of its rotary columns.
+        const int tid = threadIdx.x - 12 * 32, tok = tid >> 1, part = tid & 1;
+        const auto put_rope = [&](uint8_t *stage, const uint4 (&w)[2]) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *(uint4 *)(stage + 4 * SLAB + tok * 64 + (((2 * part + e) ^ ((tok >> 1) & 3)) << 4)) = w[e];
+        };
+        const auto get_rope = [&](int64_t row, uint4 (&w)[2]) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                w[e] = row >= 0 ? __ldg((const uint4 *)(kpe + row * P.ld_pe + rank * 32 + part * 16) + e)
+                                : make_uint4(0, 0, 0, 0);
+        };
+        bool ok = true;
+        if constexpr (KV8) {
+            const uint8_t *codes = (const uint8_t *)kv;
+            uint4 c[8], rp[2];
+            float sc;
+            int runs = 0;
+            const auto fetch = [&](int t) {
+                const int64_t row = row_of((t0 + t) * TK + tok);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    c[i] = row >= 0 ? __ldg((const uint4 *)(codes + row * P.ld_kv + rank * 256 + part * 128) + i)
+                                    : make_uint4(0, 0, 0, 0);
+                sc = row >= 0 ? __ldg(kv_scale + row * (DC / 128) + rank * 2 + part) : 0.0f;
+                get_rope(row, rp);
+                if (warp == 12) runs = runs_of(t);
+            };
+            fetch(0);
+            for (int t = 0; t < n; ++t) {
+                const int st = t % NSTAGE;
+                ok = __all_sync(FULL, tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 109, P.wait_limit));
+                if (!ok) break;
+                if (warp == 12) put_mask(t, runs);
+                uint8_t *stage = KV + st * STAGE;
+                const bool scrub = (t0 + t + 1) * TK > safe;
+                const Scale2 s2 = scale2(sc);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {  // 16 columns: chunks 2i, 2i+1 of the token's two 128-byte rows
                     uint4 o[2];
                     if (scrub) dequant16<true>(c[i], s2, o); else dequant16<false>(c[i], s2, o);
+                    uint8_t *dst = stage + (2 * part + (i >> 2)) * SLAB + tok * 128;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *(uint4 *)(dst + tok * 128 + (((c0 + 2 * i + e) ^ (tok & 7)) << 4)) = o[e];
+                    for (int e = 0; e < 2; ++e) *(uint4 *)(dst + (((2 * (i & 3) + e) ^ (tok & 7)) << 4)) = o[e];
                 }
-            };
-            // All loads of a tile's K (or V) together: the wait for one batch must not include a younger load's.
-            const auto fetch_k = [&](int t) {
-                const int64_t row = row_of((t0 + t) * TK + rank * HR + k_tok);
-#pragma unroll
-                for (int j = 0; j < K_SLOTS - 1; ++j) fetch(kc[j], ks[j], row, j * 128 + k_col);
-            };
-            const auto fetch_v = [&](int t) {
-#pragma unroll
-                for (int j = 0; j < V_SLOTS; ++j)
-                    fetch(vc[j], vs[j], row_of((t0 + t) * TK + j * VCH + v_tok), rank * 256 + v_col);
-            };
-            fetch_k(0);
-            for (int s = 0; ok && s < n + AHEAD; ++s) {
-                if (s < n) {
-#pragma unroll
-                    for (int j = 0; j < K_SLOTS - 1; ++j) {
-                        const int pos = k_pos(s) + j;
-                        if (!slot_free(pos)) break;
-                        put(kc[j], ks[j], Ring + (pos % NSLOT) * SLOT + (k_col >> 6) * SLAB, k_tok, k_col, false);
-                        slot_done(pos);
-                    }
-                    // the rotary slab is bf16: one of the warps copies it
-                    if (ok && slot_free(k_pos(s) + K_SLOTS - 1)) {
-                        const int pos = k_pos(s) + K_SLOTS - 1;
-                        if (warp == 6) {
-                            const int rows = runs_of(s);
-                            put_mask(s, rows);
-                            slot_copy(pos, &tm_pe, 1, SLAB, HR, rows, rank * 4, 0);
-                        } else if (lane == 0) {
-                            tc::mbar_arrive_remote(leader(&bar->full[pos % NSLOT]));
-                        }
-                    }
-                    if (s + 1 < n) fetch_k(s + 1);
-                }
-                if (s == AHEAD - 1) fetch_v(0);
-                if (ok && s >= AHEAD) {
-                    const int t = s - AHEAD;
-                    const bool scrub = (t0 + t + 1) * TK > safe;
-#pragma unroll
-                    for (int j = 0; j < V_SLOTS; ++j) {
-                        const int pos = v_pos(t, n) + j;
-                        if (!slot_free(pos)) break;
-                        put(vc[j], vs[j], Ring + (pos % NSLOT) * SLOT + (v_col >> 6) * VSLAB, v_tok, v_col, scrub);
-                        slot_done(pos);
-                    }
-                    if (t + 1 < n) fetch_v(t + 1);
-                }
+                put_rope(stage, rp);
+                tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar->kv_full[st]);
+                if (t + 1 < n) fetch(t + 1);
             }
         } else {
-            // V chunks of the tiles with hidden tokens: thread = one token, 64 of the CTA's columns.
+            // Tiles with hidden tokens.
             const __nv_bfloat16 *lat = (const __nv_bfloat16 *)kv;
-            const int tok = tid >> 2, q = tid & 3;
-            const int t_first = max(0, (safe / TK) - t0);  // the first tile that ends behind `safe`
-            for (int t = t_first; ok && t < n; ++t)
-                for (int j = 0; j < V_SLOTS; ++j) {
-                    const int pos = v_pos(t, n) + j;
-                    const int64_t row = row_of((t0 + t) * TK + j * VCH + tok);
-                    uint4 w[8];
+            uint32_t turn = 0;  // phase of every stage's `go`
+            for (int t = max(0, safe / TK - t0); t < n; ++t) {
+                const int st = t % NSTAGE;
+                const int64_t row = row_of((t0 + t) * TK + tok);
+                uint4 w[8], rp[2];
+                const auto get = [&](int half) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        w[e] = row >= 0 ? __ldg((const uint4 *)(lat + row * P.ld_kv + rank * 256 + q * 64) + e)
+                        w[e] = row >= 0 ? __ldg((const uint4 *)(lat + row * P.ld_kv + rank * 256 + part * 128 + half * 64) + e)
                                         : make_uint4(0, 0, 0, 0);
-                    // a warp whose wait gave up comes to the barrier all the same, and they stop together
-                    if (slot_free(pos)) {
-                        uint8_t *dst = Ring + (pos % NSLOT) * SLOT + q * VSLAB + tok * 128;
+                };
+                get(0);
+                get_rope(row, rp);
+                ok = tc::mbar_wait(&bar->go[st], (turn >> st) & 1u, abort_flag, err, 110, P.wait_limit);
+                turn ^= 1u << st;
+                uint8_t *stage = KV + st * STAGE;
+                if (ok) {
+                    for (int half = 0; half < 2; ++half) {
+                        if (half) get(1);
+                        uint8_t *dst = stage + (2 * part + half) * SLAB + tok * 128;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             *(uint4 *)(dst + ((e ^ (tok & 7)) << 4)) =
                                 make_uint4(finite2(w[e].x), finite2(w[e].y), finite2(w[e].z), finite2(w[e].w));
-                        tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
                     }
-                    if (!(ok = bar_and<2>(ok))) break;
-                    if (tid == 0) tc::mbar_arrive_remote(leader(&bar->full[pos % NSLOT]));
+                    put_rope(stage, rp);
+                    tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
                 }
+                // a warp whose wait gave up comes to the barrier all the same, and they stop together
+                if (!bar_and<2, 128>(ok)) break;
+                if (tid == 0) tc::mbar_arrive(&bar->kv_full[st]);
+            }
         }
-    } else if (warp < 4) {
-        // ---------------- softmax: thread = row r of the CTA's 64, tokens 64 hh .. of the tile's 128 ----------------
-        const unsigned FULL = 0xffffffffu;
-        const int r = threadIdx.x & 63, hh = threadIdx.x >> 6;
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        const int li = lrow + (int)rank * HR + r;      // row within the sequence
-        const bool mine = li < seq_rows;               // else a row of the next sequence, or none
-        const int node = mine ? li / P.H : 0;
-        const uint64_t *bits = P.mask ? P.mask + (int64_t)(P.q0[lo] + node) * P.words : nullptr;
-        const float sl2 = fabsf(P.scale_log2);         // not 0
-        const bool negative = P.scale_log2 < 0.0f;
-        float m = -INFINITY, l = 0.0f;
+    } else if (warp >= 4 && warp < 12) {
+        // ---------------- softmax groups: group g takes tiles g, g + 2, ..; thread = row h ----------------
+        const int q = warp & 3, g = (warp >> 2) - 1, h = q * 32 + lane;
+        const bool own = (uint32_t)(q >> 1) == rank;      // rows that this CTA finishes
+        const int r = h & 63;                             // row within its half
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         bool ok = true;
-        for (int t = 0; t < n; ++t) {
-            const int sb = t % NS;
-            const int kb = (t0 + t) * TK + hh * 64;    // this thread's first token
-            // --- which of its 64 tokens the row sees ---
-            uint64_t see = ~0ull;
-            if ((t0 + t + 1) * TK > safe) {
-                const int rel = kb - first;            // node number of the first token (negative: before the tree)
-                if (!bits) {
-                    const int left = node + 1 - rel;
-                    see = left >= 64 ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1;
-                } else if (rel + 64 > 0) {
-                    const int w = rel >> 6, sh = rel & 63;
-                    const uint64_t w0 = w < 0 ? ~0ull : w < P.words ? __ldg(bits + w) : 0ull;
-                    const uint64_t w1 = w + 1 < P.words ? __ldg(bits + w + 1) : 0ull;
-                    see = sh ? (w0 >> sh) | (w1 << (64 - sh)) : w0;
-                    const int left = T - rel;
-                    if (left < 64) see &= left <= 0 ? 0ull : (1ull << left) - 1;
-                }
-                if (!mine) see &= 1;                   // any row will do that is computed and not stored
-            }
-            // A warp whose wait gave up goes on to the barrier below, where all four warps stop together.
-            if (P.pt.table) {
-                ok = ok && tc::mbar_wait(&bar->mask_full[t % NMASK], (t / NMASK) & 1, abort_flag, err, 108, P.wait_limit);
-                see &= live[2 * (t % NMASK) + hh];
-            }
-            ok = ok && tc::mbar_wait(&bar->s_full[sb], (t / NS) & 1, abort_flag, err, 109, P.wait_limit);
-            ok = __all_sync(FULL, ok);
-            tc::tc_fence_after();
-            float v[64];
-            {
-                float a[32], c[32];
-                tc::tmem_ld32(lanes + COL_S + sb * (TK / 2), a);
-                tc::tmem_ld32(lanes + COL_S + sb * (TK / 2) + 32, c);
-                tc::tmem_ld_wait();
+        if (n > 0) {
+            // The q~ slice moves to tensor memory (A operand of QK^T): four slabs of 32 packed columns, two a group; group 1
+            // puts the rotary slice of the queries into shared memory.
+            uint4 rq[4];
+            if (g) {
+                const int64_t row = seq_row0 + lrow + h;
+                const bool there = lrow + h < seq_rows;
+                const uint4 *src = (const uint4 *)(qpe + row * DR + rank * 32);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    v[j] = a[j];
-                    v[32 + j] = c[j];
+                for (int e = 0; e < 4; ++e) rq[e] = there ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
+            }
+            ok = __all_sync(FULL, tc::mbar_wait(&bar->q_stage, 0, abort_flag, err, 111, P.wait_limit));
+            for (int js = g * 2; ok && js < g * 2 + 2; ++js) {
+                const uint8_t *srow = Pb + js * Q_BOX + h * 128;
+                uint32_t qv[32];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint4 t4 = *(const uint4 *)(srow + ((e ^ (h & 7)) << 4));
+                    qv[4 * e] = t4.x;
+                    qv[4 * e + 1] = t4.y;
+                    qv[4 * e + 2] = t4.z;
+                    qv[4 * e + 3] = t4.w;
                 }
+                tc::tmem_st32(lanes + COL_Q + js * 32, qv);
+            }
+            tc::tmem_st_wait();
+            if (g) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) *(uint4 *)(QR + h * 64 + ((e ^ ((h >> 1) & 3)) << 4)) = rq[e];
+                tc::fence_proxy_async_smem();  // read by the rotary MMAs (async proxy)
+            }
+            tc::tc_fence_before();
+            // Every warp has read its part of the staging: the buffers may carry scores, here and from the other CTA.
+            ok = bar_and<1, 256>(ok);
+            if (lane == 0) tc::mbar_arrive(&bar->q_ready);
+            if (threadIdx.x == 4 * 32) tc::mbar_arrive_remote(tc::map_peer(tc::smem_u32(&bar->peer_ready), peer));
+            ok = ok && __all_sync(FULL, tc::mbar_wait(&bar->peer_ready, 0, abort_flag, err, 112, P.wait_limit));
+        }
+        const float sl2 = P.scale_log2;
+        uint8_t *Xg = X + g * X_BYTES, *Yg = Y + g * X_BYTES, *Pg = Pb + g * P_BYTES;
+        const auto sw = [&](uint8_t *rowp, int c) { return rowp + ((c ^ (h & 7)) << 4); };
+        // this warp's scores of its tile
+        const auto load_scores = [&](float (&v)[64]) {
+            tc::tc_fence_after();
+            float a[32], c[32];
+            tc::tmem_ld32(lanes + COL_S + g * TK, a);
+            tc::tmem_ld32(lanes + COL_S + g * TK + 32, c);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                v[j] = a[j];
+                v[32 + j] = c[j];
             }
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_remote(leader(&bar->s_empty[sb]));
-            if (negative) {
+            if (lane == 0) tc::mbar_arrive(&bar->s_empty[g]);
+        };
+#define TREE_WAIT(bar_, parity_, site_)                                                                                  \
+    if (!(ok = __all_sync(FULL, tc::mbar_wait(bar_, parity_, abort_flag, err, site_, P.wait_limit)))) break
+        if (own) {
+            const int li = lrow + h;                      // row within the sequence
+            const bool mine = li < seq_rows;              // else a row of the next sequence, or none
+            const int node = mine ? li / P.H : 0;
+            const uint64_t *bits = P.mask ? P.mask + (int64_t)(P.q0[lo] + node) * P.words : nullptr;
+            float m_g = -INFINITY, l_g = 0.0f;            // this group's reference and its share of the row sum
+            for (int t = g, k = 0; ok && t < n; t += 2, ++k) {
+                const uint32_t ph = (uint32_t)k & 1u;
+                if (lane == 0 && !(q & 1)) tc::mbar_arrive_expect_tx(&bar->x_full[g], X_BYTES);
+                // --- which of the 64 tokens the row sees ---
+                uint64_t see = ~0ull;
+                if ((t0 + t + 1) * TK > safe) {
+                    const int rel = (t0 + t) * TK - first;  // node number of the first token (negative: before the tree)
+                    if (!bits) {
+                        const int left = node + 1 - rel;
+                        see = left >= 64 ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1;
+                    } else if (rel + 64 > 0) {
+                        const int w = rel >> 6, sh = rel & 63;
+                        const uint64_t w0 = w < 0 ? ~0ull : w < P.words ? __ldg(bits + w) : 0ull;
+                        const uint64_t w1 = w + 1 < P.words ? __ldg(bits + w + 1) : 0ull;
+                        see = sh ? (w0 >> sh) | (w1 << (64 - sh)) : w0;
+                        const int left = T - rel;
+                        if (left < 64) see &= left <= 0 ? 0ull : (1ull << left) - 1;
+                    }
+                }
+                if (P.pt.table) {
+                    TREE_WAIT(&bar->mask_full[t % NMASK], (t / NMASK) & 1, 113);
+                    see &= ms->live[t % NMASK];
+                }
+                TREE_WAIT(&bar->s_full[g], ph, 114);
+                float v[64];
+                load_scores(v);
+                // --- + the other CTA's half, in log2 units ---
+                TREE_WAIT(&bar->x_full[g], ph, 115);
 #pragma unroll
-                for (int j = 0; j < 64; ++j) v[j] = -v[j];
-            }
-            if (!__all_sync(FULL, see == ~0ull)) {
-                const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 x = *(const uint4 *)sw(Xg + r * 128, c);
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[8 * c + 2 * e] = fmaf(v[8 * c + 2 * e], sl2, tc::f16_to_f32((uint16_t)(xs[e] & 0xffffu)));
+                        v[8 * c + 2 * e + 1] = fmaf(v[8 * c + 2 * e + 1], sl2, tc::f16_to_f32((uint16_t)(xs[e] >> 16)));
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(tc::smem_u32(&bar->x_free[g]), peer));
+                if (!__all_sync(FULL, see == ~0ull)) {
+                    const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (!(s0 >> j & 1)) v[j] = -INFINITY;
+                        if (!(s1 >> j & 1)) v[32 + j] = -INFINITY;
+                    }
+                }
+                const float mt = max64(v);
+                // --- running reference: the one used for tile t-1 comes from the other group ---
+                float m_prev = -INFINITY;
+                if (t > 0) {
+                    TREE_WAIT(&bar->hand[q & 1][1 - g], ((t - 1) >> 1) & 1, 116);
+                    m_prev = ms->m_pub[1 - g][r];
+                }
+                float m_now = m_prev, alpha = 1.0f;
+                if (mt != -INFINITY) {
+                    if (m_prev == -INFINITY) {
+                        m_now = mt;
+                    } else if (mt > m_prev + RESCALE_LOG2) {
+                        m_now = mt;
+                        alpha = tc::ex2_approx(m_prev - m_now);
+                    }
+                }
+                if (t + 1 < n) {
+                    ms->m_pub[g][r] = m_now;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar->hand[q & 1][g]);
+                }
+                if (m_now != m_g) {
+                    if (m_g != -INFINITY) l_g *= tc::ex2_approx(m_g - m_now);
+                    m_g = m_now;
+                }
+                // --- probabilities, rounded to bf16 for the PV product; the row sum takes the rounded ones ---
+                const float neg = m_now == -INFINITY ? 0.0f : -m_now;
+                uint32_t pk[32];
+                float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    if (!(s0 >> j & 1)) v[j] = -INFINITY;
-                    if (!(s1 >> j & 1)) v[32 + j] = -INFINITY;
+                    const float p0 = tc::ex2_approx(v[2 * j] + neg), p1 = tc::ex2_approx(v[2 * j + 1] + neg);
+                    const __nv_bfloat162 t2 = __floats2bfloat162_rn(p0, p1);
+                    pk[j] = *(const uint32_t *)&t2;
+                    sum0 = tc::add_bf16_f32((uint16_t)(pk[j] & 0xffffu), sum0);
+                    sum1 = tc::add_bf16_f32((uint16_t)(pk[j] >> 16), sum1);
+                }
+                l_g += sum0 + sum1;
+                // --- P(t) here and to the other CTA, once both PV(t-2) are done with the buffer ---
+                if (k > 0) {
+                    TREE_WAIT(&bar->p_empty[g], (k - 1) & 1, 117);
+                    TREE_WAIT(&bar->pv_peer[g], (k - 1) & 1, 118);
+                }
+                // --- the context moves after PV(t-1) and before PV(t) (PV(t-2) is done: the phase is the next one) ---
+                if (__any_sync(FULL, alpha != 1.0f)) {
+                    TREE_WAIT(&bar->p_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, 119);
+                    rescale_rows(lanes, alpha);
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *(uint4 *)sw(Pg + h * 128, c) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                ms->alpha_out[g][r] = alpha;
+                tc::fence_proxy_async_smem();  // read by the PV product and by the copies (async proxy)
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t in = tc::map_peer(tc::smem_u32(&bar->p_in[g]), peer);
+                    uint8_t *rows32 = Pg + q * 32 * 128;
+                    tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(rows32), peer), rows32, 32 * 128, in);
+                    tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(&ms->alpha_in[g][(q & 1) * 32]), peer),
+                                          &ms->alpha_out[g][(q & 1) * 32], 32 * 4, in);
+                    tc::mbar_arrive(&bar->p_full[g]);
                 }
             }
-            // --- the row's maximum: a tree over the 64 values, then the other half's ---
-            float mt;
-            {
-                float a[22], b8[8];
-#pragma unroll
-                for (int i = 0; i < 21; ++i) a[i] = tc::max3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
-                a[21] = v[63];
-#pragma unroll
-                for (int i = 0; i < 7; ++i) b8[i] = tc::max3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
-                b8[7] = a[21];
-                mt = tc::max3(tc::max3(b8[0], b8[1], b8[2]), tc::max3(b8[3], b8[4], b8[5]), fmaxf(b8[6], b8[7]));
+            // The other CTA's last PV products are done: its copies from here have been read, and its commits that arrive
+            // here have arrived.
+            if (ok && n > 0) {
+                for (int t = max(0, n - 2); t < n; ++t)
+                    if ((t & 1) == g)
+                        ok = __all_sync(FULL, tc::mbar_wait(&bar->pv_peer[g], (t >> 1) & 1, abort_flag, err, 120, P.wait_limit));
             }
-            float *ex = mx + (t & 1) * 128;
-            ex[threadIdx.x] = mt;
-            if (!(ok = bar_and<1>(ok))) break;
-            mt = fmaxf(mt, ex[threadIdx.x ^ 64]) * sl2;
-            float m_new = m;
-            bool rescale = false;
-            if (mt != -INFINITY) {
-                if (m == -INFINITY) {
-                    m_new = mt;
-                } else if (mt > m + RESCALE_LOG2) {
-                    m_new = mt;
-                    rescale = true;
+            ms->sum[g][r] = l_g;
+            ms->ref[g][r] = m_g;
+        } else {
+            for (int t = g, k = 0; ok && t < n; t += 2, ++k) {
+                const uint32_t ph = (uint32_t)k & 1u;
+                if (lane == 0 && !(q & 1)) tc::mbar_arrive_expect_tx(&bar->p_in[g], X_BYTES + HR * 4);
+                TREE_WAIT(&bar->s_full[g], ph, 121);
+                float v[64];
+                load_scores(v);
+                uint32_t w[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) w[j] = tc::f16x2_satfinite(v[2 * j] * sl2, v[2 * j + 1] * sl2);
+                // the other CTA has read this group's previous tile, from there and so from here
+                if (k > 0) TREE_WAIT(&bar->x_free[g], (k - 1) & 1, 122);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *(uint4 *)sw(Yg + r * 128, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                tc::fence_proxy_async_smem();  // read by the copy (async proxy)
+                __syncwarp();
+                if (lane == 0)
+                    tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(Xg + (q & 1) * 32 * 128), peer), Yg + (q & 1) * 32 * 128,
+                                          32 * 128, tc::map_peer(tc::smem_u32(&bar->x_full[g]), peer));
+                // --- the probabilities of these rows, and their context factors ---
+                TREE_WAIT(&bar->p_in[g], ph, 123);
+                const float alpha = ms->alpha_in[g][r];
+                if (__any_sync(FULL, alpha != 1.0f)) {
+                    TREE_WAIT(&bar->p_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, 124);
+                    rescale_rows(lanes, alpha);
                 }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar->p_full[g]);
             }
-            if (__any_sync(FULL, rescale)) {
-                // after PV(t-1), before PV(t); tcgen05.ld/st are warp-wide: rows that stay take a factor of 1
-                const float alpha = rescale ? tc::ex2_approx(m - m_new) : 1.0f;
-                l *= alpha;
-                ok = __all_sync(FULL, tc::mbar_wait(&bar->p_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag, err,
-                                                            110, P.wait_limit));
-                if (!ok) continue;
-                tc::tc_fence_after();
-#pragma unroll 1
-                for (int cc = 0; cc < 8; ++cc) {
-                    float o[32];
-                    uint32_t ob[32];
-                    tc::tmem_ld32(lanes + COL_O + cc * 32, o);
-                    tc::tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) ob[j] = __float_as_uint(o[j] * alpha);
-                    tc::tmem_st32(lanes + COL_O + cc * 32, ob);
-                }
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-            }
-            m = m_new;
-            // --- probabilities, rounded to bf16 for the PV product; the row sum takes the rounded ones ---
-            const float neg = m == -INFINITY ? 0.0f : -m;
-            uint32_t pk[32];
-            float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float p0 = tc::ex2_approx(fmaf(v[2 * j], sl2, neg));
-                const float p1 = tc::ex2_approx(fmaf(v[2 * j + 1], sl2, neg));
-                const __nv_bfloat162 t2 = __floats2bfloat162_rn(p0, p1);
-                pk[j] = *(const uint32_t *)&t2;
-                sum0 = tc::add_bf16_f32((uint16_t)(pk[j] & 0xffffu), sum0);
-                sum1 = tc::add_bf16_f32((uint16_t)(pk[j] >> 16), sum1);
-            }
-            l += sum0 + sum1;
-            if (t >= 2) {
-                ok = __all_sync(FULL, tc::mbar_wait(&bar->p_empty[t & 1], ((t >> 1) - 1) & 1, abort_flag, err, 111,
-                                                            P.wait_limit));
-                if (!ok) continue;
-            }
-            uint8_t *prow = Pb + (t & 1) * P_BYTES + hh * SLAB + r * 128;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                *(uint4 *)(prow + ((c ^ (r & 7)) << 4)) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-            tc::fence_proxy_async_smem();  // read by the PV product (async proxy)
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_remote(leader(&bar->p_full[t & 1]));
         }
-        // ---------------- epilogue: normalise, stage rows in shared memory, write whole rows ----------------
-        const bool have = __all_sync(FULL, n > 0 && ok && tc::mbar_wait(&bar->o_done, 0, abort_flag, err, 112, P.wait_limit));
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        mx[threadIdx.x] = l;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const float sum = have ? l + mx[threadIdx.x ^ 64] : 0.0f;
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        const float row_lse = sum > 0.0f ? (m + log2f(sum)) * LN2 : -INFINITY;
-        if (have) tc::tc_fence_after();
-        const bool whole = splits == 1;
-        const int ld = whole ? OUT_LD_BF16 : OUT_LD_F32;
-        uint8_t *srow = Pb + r * ld + hh * 256 * (whole ? 2 : 4);
-#pragma unroll 1
-        for (int cc = 0; cc < 8; ++cc) {
-            float o[32];
-            if (have) {
-                tc::tmem_ld32(lanes + COL_O + cc * 32, o);
-                tc::tmem_ld_wait();
+#undef TREE_WAIT
+        // ---------------- row sums: the finishing warps' results, to both CTAs ----------------
+        bar_and<1, 256>(ok);
+        if (own && g == 0) {
+            const float la = ms->sum[0][r], ma = ms->ref[0][r], lb = ms->sum[1][r], mb = ms->ref[1][r];
+            const float m = fmaxf(ma, mb);
+            const float sum = (ma == -INFINITY ? 0.0f : la * tc::ex2_approx(ma - m)) +
+                              (mb == -INFINITY ? 0.0f : lb * tc::ex2_approx(mb - m));
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            ms->inv[h] = inv;
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::map_peer(tc::smem_u32(&ms->inv[h]), peer)), "f"(inv)
+                         : "memory");
+            if (lrow + h < seq_rows) {
+                const float row_lse = sum > 0.0f ? (m + log2f(sum)) * LN2 : -INFINITY;
+                if (splits > 1) lpart[((int64_t)P.part0[lo] + rem) * ROWS + h] = row_lse;
+                else if (lse) lse[seq_row0 + lrow + h] = row_lse;
             }
+        }
+    }
+    __syncthreads();
+    if (*abort_flag) {
+        // Copies that nobody waits for any more land within microseconds.
+        const long long c0 = clock64();
+        while (clock64() - c0 < kAbortQuietCycles) {
+        }
+    }
+    tc::cluster_sync();  // both CTAs have every row's sum, and send each other nothing more
+    if (warp >= 4 && warp < 12) {
+        // ---------------- epilogue: normalise, stage rows in the token stages, write whole rows ----------------
+        const int q = warp & 3, g = (warp >> 2) - 1, h = q * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        const float inv = ms->inv[h];
+        const bool have = n > 0 && !*abort_flag, whole = splits == 1;
+        tc::tc_fence_after();
+        const int ld = whole ? OUT_LD_BF16 : OUT_LD_F32;
+        uint8_t *srow = KV + h * ld;
+#pragma unroll 1
+        for (int cc = g * 4; cc < g * 4 + 4; ++cc) {
+            float o[32];
+            tc::tmem_ld32(lanes + COL_O + cc * 32, o);
+            tc::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = have && sum > 0.0f ? o[j] * inv : 0.0f;
+            for (int j = 0; j < 32; ++j) o[j] = have && inv > 0.0f ? o[j] * inv : 0.0f;
             if (whole) {
                 uint4 *d = (uint4 *)(srow + cc * 64);
 #pragma unroll
@@ -720,31 +776,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                 for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const int64_t part = splits == 1 ? 0 : (int64_t)P.part0[lo] + rem;
-        const int rows = min(HR, seq_rows - lrow - (int)rank * HR);  // of this CTA; may be <= 0
-        for (int i = warp; i < rows; i += 4) {
-            const uint4 *src = (const uint4 *)(Pb + i * ld);
-            uint4 *dst = whole ? (uint4 *)(olat + (seq_row0 + lrow + rank * HR + i) * DC)
-                               : (uint4 *)(opart + (part * ROWS + rank * HR + i) * DC);
-            for (int c = lane; c < (whole ? DC / 8 : DC / 4); c += 32) dst[c] = src[c];
+        bar_and<1, 256>(true);
+        const int64_t part = whole ? 0 : (int64_t)P.part0[lo] + rem;
+        const int rows = min(ROWS, seq_rows - lrow);
+        for (int i = warp - 4; i < rows; i += 8) {
+            const uint4 *src = (const uint4 *)(KV + i * ld);
+            uint4 *dst = whole ? (uint4 *)(olat + (seq_row0 + lrow + i) * DC + rank * 256)
+                               : (uint4 *)(opart + (part * ROWS + i) * DC + rank * 256);
+            for (int c = lane; c < (whole ? 32 : 64); c += 32) dst[c] = src[c];
         }
-        if (hh == 0 && mine) {
-            if (!whole) lpart[part * ROWS + rank * HR + r] = row_lse;
-            else if (lse) lse[seq_row0 + li] = row_lse;
-        }
+        tc::tc_fence_before();
     }
     __syncthreads();
-    if (*abort_flag) {
-        // copies that nobody waits for any more land within microseconds
-        const long long c0 = clock64();
-        while (clock64() - c0 < kAbortQuietCycles) {
-        }
-    }
-    tc::cluster_sync();  // the other CTA's MMAs, copies and arrivals are done with this CTA's memory
-    if (warp == 5) {
+    if (warp == 2) {
         tc::tc_fence_after();
-        tc::tmem_dealloc_pair(tmem, 512);
+        tc::tmem_dealloc(tmem, 512);
     }
 }
 
@@ -816,7 +862,7 @@ Shape shape_of(const Batch &bt, int H, int b) {
 // One pair of SMs works on a unit at a time, so units come in waves of 76.  A unit costs its tiles and about
 // kUnitCost tiles to start and end.  Of the chunk sizes that fill one, two, .. waves the cheapest is
 // taken; no split at all competes with them.
-constexpr int kUnitCost = 3, kMinChunk = 2, kMaxWaves = 4, kMaxSplits = 76;
+constexpr int kUnitCost = 6, kMinChunk = 4, kMaxWaves = 4, kMaxSplits = 76;
 int split_of(const Shape &s, int chunk) { return std::min(kMaxSplits, (s.tiles + chunk - 1) / chunk); }
 void make_plan(const Batch &bt, int H, Plan &plan) {
     const int B = bt.st.B;
@@ -915,39 +961,38 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
     P.words = words;
     P.H = H;
     P.ld_kv = c->ld_kv;
+    P.ld_pe = c->ld_pe;
     P.scale_log2 = scale == 0.0f ? 1e-30f : scale * 1.4426950408889634f;  // 0: so small that every score counts alike
     P.wait_limit = wait_limit_cycles();
     const uint64_t rows = (uint64_t)std::max<int64_t>(c->rows, 1);
     P.oob = (int)rows;
     const bool kv8 = c->dtype == DSA_E4M3;
-    // Tokens that lie together: all of a K slot's 64 (contiguous caches, pages of 64), or fewer.
-    const int run = !pt.table || pt.page % 64 == 0 ? 64 : pt.page % 32 == 0 ? 32 : 16;
-    CUtensorMap tq, tqpe, tk, tv, tpe;
-    const auto map2 = [](CUtensorMap *m, const void *base, int cols, uint64_t n_rows) {
-        const uint64_t dims[2] = {(uint64_t)cols, n_rows}, strides[1] = {(uint64_t)cols * 2};
-        const uint32_t bx[2] = {64, HR};
-        return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, bx);
-    };
-    // Cache rows as slabs of 64 columns: (column, row, slab).
-    const auto map3 = [&](CUtensorMap *m, const void *base, int cols, int64_t ld, int box_rows, int box_slabs) {
-        const uint64_t dims[3] = {64, rows, (uint64_t)cols / 64}, strides[2] = {(uint64_t)ld * 2, 128};
-        const uint32_t bx[3] = {64, (uint32_t)box_rows, (uint32_t)box_slabs};
-        return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, bx);
-    };
-    if (!map2(&tq, qt, DC, (uint64_t)N * H) || !map2(&tqpe, qpe, DR, (uint64_t)N * H) ||
-        !map3(&tpe, c->k_pe, DR, c->ld_pe, run, 1))
-        return cudaErrorInvalidValue;
-    if (kv8) tk = tv = tpe;  // not used
-    else if (!map3(&tk, c->kv, DC, c->ld_kv, run, run == HR ? 2 : 1) ||
-             !map3(&tv, c->kv, DC, c->ld_kv, std::min(run, VCH), run >= VCH ? 4 : 1))
-        return cudaErrorInvalidValue;
+    // Tokens that lie together: a whole tile (contiguous caches, pages of 64), or less.
+    const int run = !pt.table || pt.page % TK == 0 ? TK : pt.page % 32 == 0 ? 32 : 16;
+    CUtensorMap tq, tkv, tpe;
+    {
+        const uint64_t dims[2] = {DC, (uint64_t)N * H}, strides[1] = {DC * 2};
+        const uint32_t box[2] = {64, ROWS};
+        if (!make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, qt, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    tkv = tpe = tq;  // e4m3: not used
+    if (!kv8) {
+        // latents as slabs of 64 columns (column, row, slab); rotary keys in halves of 32 columns
+        const uint64_t dims[3] = {64, rows, DC / 64}, strides[2] = {(uint64_t)c->ld_kv * 2, 128};
+        const uint32_t box[3] = {64, (uint32_t)run, run == TK ? 4u : 1u};
+        const uint64_t pdims[2] = {DR, rows}, pstrides[1] = {(uint64_t)c->ld_pe * 2};
+        const uint32_t pbox[2] = {32, (uint32_t)run};
+        if (!make_tmap(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c->kv, dims, strides, box) ||
+            !make_tmap(&tpe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c->k_pe, pdims, pstrides, pbox, CU_TENSOR_MAP_SWIZZLE_64B))
+            return cudaErrorInvalidValue;
+    }
     float *opart = (float *)part_ws, *lpart = (float *)((char *)part_ws + part_bytes(plan));
     auto kern = kv8 ? tree_tc_kernel<true> : tree_tc_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3((unsigned)(2 * unit)), dim3(kv8 ? Cfg<true>::THREADS : Cfg<false>::THREADS), SMEM, s, tq,
-                   tqpe, tk, tv, tpe, run, (const void *)c->kv, (const float *)c->kv_scale, P, (__nv_bfloat16 *)olat, lse,
-                   opart, lpart);
+    e = launch_pdl(kern, dim3((unsigned)(2 * unit)), dim3(THREADS), SMEM, s, tq, tkv, tpe, run, (const void *)c->kv,
+                   (const float *)c->kv_scale, (const __nv_bfloat16 *)c->k_pe, (const __nv_bfloat16 *)qpe, P,
+                   (__nv_bfloat16 *)olat, lse, opart, lpart);
     if (e != cudaSuccess) return e;
     note_launch(DSA_KERNEL_TREE_TC);
     if (!plan.parts) return cudaSuccess;
