@@ -15,7 +15,7 @@
 //   * Each CTA multiplies its columns: a partial score tile (q~ slice resident in
 //     tensor memory as the A operand, so QK^T reads only the tokens from shared
 //     memory).  CTA c finishes rows 64c .. 64c+63: the other CTA sends it its partial
-//     scores of those rows (fp16 of the log2-scaled values, 8 KB), it adds its own in
+//     scores of those rows (fp16, 8 KB), it adds its own in
 //     fp32, runs the softmax and sends the probabilities (bf16, 8 KB) back, which both
 //     need for PV.  Nothing is computed twice, and a row's maximum and sum live in
 //     one place.
@@ -60,7 +60,8 @@ constexpr int P_BYTES = ROWS * TK * 2;  // probabilities of all rows
 constexpr int X_BYTES = HR * TK * 2;    // fp16 partial scores of half of the rows
 constexpr int Q_BOX = ROWS * 128;       // 128 rows x 64 columns of q~ (staged in the exchange buffers)
 constexpr int QR_BYTES = ROWS * 64;     // rotary slice of the queries, 64-byte swizzle
-constexpr int NMASK = 8;
+constexpr int NB = 6;                   // barriers of a kind: tile t uses number t % 6, which belongs to one softmax group and one
+                                        // buffer whether there are two groups or three
 constexpr uint32_t COL_S = 0, COL_Q = 128, COL_O = 256;
 constexpr uint32_t IDESC_QK = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, ROWS, TK, 0, 0);
 constexpr uint32_t IDESC_PV = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, ROWS, 256, 0, 1);
@@ -68,22 +69,24 @@ constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr long long kAbortQuietCycles = 1LL << 18;
 constexpr int PAIRS = 76;               // 152 SMs
-// warp 0: TMA; 1: QK^T; 2: tensor memory, PV; 4-7, 8-11: softmax groups (warp % 4 = lane quarter); 12-15: loading
+// warp 0: TMA; 1: QK^T; 2: tensor memory, PV; 3: bf16 tiles with hidden tokens; from 4 on the softmax groups of four
+// (warp % 4 = lane quarter): three, or for e4m3 two, and 12-15 load
 constexpr int THREADS = 512;
+constexpr int MAX_G = 3;
 
-// [g]: softmax group = tile parity.
 struct Bars {
-    uint64_t q_stage, q_ready, peer_ready, kv_full[NSTAGE], kv_empty[NSTAGE], go[NSTAGE], s_full[2], s_empty[2];
-    uint64_t x_full[2], x_free[2];    // the other CTA's partial scores are here; it has read ours
-    uint64_t p_in[2], pv_peer[2];     // the other CTA's probabilities are here; its PV product is done with ours
-    uint64_t p_full[2], p_empty[2], hand[2][2], mask_full[NMASK], qk_done, o_done;
+    uint64_t q_stage, q_ready, peer_ready, kv_full[NSTAGE], kv_empty[NSTAGE], raw[NSTAGE], s_full[NB], s_empty[NB];
+    uint64_t x_full[NB], x_free[NB];  // the other CTA's partial scores are here; it has read ours
+    uint64_t p_in[NB], p_full[NB];    // the other CTA's probabilities are here; all are, and the context is ready for them
+    uint64_t p_free[NB];              // the PV products of both CTAs are done
+    uint64_t hand[2][NB], mask_full[NB], qk_done, o_done;
 };
 struct Misc {
-    float m_pub[2][HR];               // reference maximum that a group used, for the other group
+    float m_pub[MAX_G][HR];           // reference maximum that a group used, for the next tile's group
     float alpha_out[2][HR], alpha_in[2][HR];  // context factors of a tile, of this CTA's rows and of the other's
-    float sum[2][HR], ref[2][HR];     // a group's share of the row sum and its reference
+    float sum[MAX_G][HR], ref[MAX_G][HR];     // a group's share of the row sum and its reference
     float inv[ROWS];                  // 1 / row sum
-    uint64_t live[NMASK];             // tokens of a tile whose page exists
+    uint64_t live[NB];                // tokens of a tile whose page exists
     Bars bar;
     uint32_t tmem_slot;
     int abort_flag, never;
@@ -134,41 +137,27 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     return *(const uint32_t *)&r;
 }
 
-// 16 codes x scale -> 16 bf16 (two 16-byte chunks).  `up` is 2^120 * scale / `rest`, a bf16 pair each: the scale
-// goes in one factor unless 2^120 times it leaves bf16's range.
-struct Scale2 {
-    uint32_t up, rest;
-    bool two;
-};
-__device__ __forceinline__ Scale2 scale2(float s) {
-    Scale2 r;
-    r.two = !(s <= 128.0f);  // Inf and NaN included
-    const float up = r.two ? 0x1p120f : 0x1p120f * s;
-    const __nv_bfloat162 u = __float2bfloat162_rn(up), v = __float2bfloat162_rn(s);
-    r.up = *(const uint32_t *)&u;
-    r.rest = *(const uint32_t *)&v;
-    return r;
-}
-template <bool SCRUB>
-__device__ __forceinline__ void dequant16(const uint4 &c, const Scale2 &s, uint4 (&o)[2]) {
+// 16 codes x 2^120 scale -> 16 bf16 (two 16-byte chunks).
+__device__ __forceinline__ void dequant16(const uint4 &c, uint32_t up, uint4 (&o)[2]) {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     uint32_t r[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         spread4(w[i], r[2 * i], r[2 * i + 1]);
-        r[2 * i] = mul2(r[2 * i], s.up);
-        r[2 * i + 1] = mul2(r[2 * i + 1], s.up);
-    }
-    if (s.two) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = mul2(r[i], s.rest);
-    }
-    if (SCRUB) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = finite2(r[i]);
+        r[2 * i] = mul2(r[2 * i], up);
+        r[2 * i + 1] = mul2(r[2 * i + 1], up);
     }
     o[0] = make_uint4(r[0], r[1], r[2], r[3]);
     o[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float x) {
+    const __nv_bfloat162 v = __float2bfloat162_rn(x);
+    return *(const uint32_t *)&v;
+}
+// 2^d of a whole number d (0 below the normal range).
+__device__ __forceinline__ float pow2(float d) {
+    const int e = (int)fmaxf(d, -127.0f) + 127;
+    return e > 0 ? __int_as_float(min(e, 254) << 23) : 0.0f;
 }
 
 // COUNT threads arrive at barrier ID; returns the AND of `v` over them.
@@ -216,6 +205,11 @@ __device__ __forceinline__ float max64(const float (&v)[64]) {
 }
 
 template <bool KV8>
+struct Cfg {
+    static constexpr int G = KV8 ? 2 : 3;  // softmax groups
+};
+
+template <bool KV8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                    const __grid_constant__ CUtensorMap tm_pe, int run, const void *__restrict__ kv,
@@ -225,17 +219,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                    float *__restrict__ lpart) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *KV = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t *Pb = KV + NSTAGE * STAGE;   // [g] probabilities: rows x 64 tokens, 128-byte swizzle
-    uint8_t *X = Pb + 2 * P_BYTES;       // [g] the other CTA's partial scores of this CTA's rows
-    uint8_t *Y = X + 2 * X_BYTES;        // [g] this CTA's partial scores of the other's rows, sent from here
+    constexpr int G = Cfg<KV8>::G, SOFT = 4 * G;
+    uint8_t *Pb = KV + NSTAGE * STAGE;   // [t % 2] probabilities: rows x 64 tokens, 128-byte swizzle
+    uint8_t *X = Pb + 2 * P_BYTES;       // [t % 2] the other CTA's partial scores of this CTA's rows
+    uint8_t *Y = X + 2 * X_BYTES;        // [t % 2] this CTA's partial scores of the other's rows, sent from here
     uint8_t *QR = Y + 2 * X_BYTES;       // rotary slice of the queries
     Misc *ms = (Misc *)(QR + QR_BYTES);
     Bars *bar = &ms->bar;
     volatile int *abort_flag = (volatile int *)&ms->abort_flag, *nv = (volatile int *)&ms->never;
     int *err = &g_tree_tc_error;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned FULL = 0xffffffffu;
+    const int warp = __shfl_sync(FULL, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank(), peer = rank ^ 1u;
 
     // ---- the unit: rows row0 .. of a sequence, tiles t0 .. t0 + n - 1 of its tokens ----
@@ -262,26 +257,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
     if (threadIdx.x == 0) {
         tc::mbar_init(&bar->q_stage, 1);
-        tc::mbar_init(&bar->q_ready, 8);
+        tc::mbar_init(&bar->q_ready, SOFT);
         tc::mbar_init(&bar->peer_ready, 1);
         for (int i = 0; i < NSTAGE; ++i) {
             tc::mbar_init(&bar->kv_full[i], KV8 ? 4 : 1);
             tc::mbar_init(&bar->kv_empty[i], 1);
-            tc::mbar_init(&bar->go[i], 1);
+            tc::mbar_init(&bar->raw[i], 1);
         }
-        for (int g = 0; g < 2; ++g) {
-            tc::mbar_init(&bar->s_full[g], 1);
-            tc::mbar_init(&bar->s_empty[g], 4);  // the group's warps have read the scores
-            tc::mbar_init(&bar->x_full[g], 1);   // armed here with what the other CTA sends
-            tc::mbar_init(&bar->x_free[g], 2);   // its two finishing warps
-            tc::mbar_init(&bar->p_in[g], 1);
-            tc::mbar_init(&bar->pv_peer[g], 1);
-            tc::mbar_init(&bar->p_full[g], 4);
-            tc::mbar_init(&bar->p_empty[g], 1);
-            tc::mbar_init(&bar->hand[0][g], 1);
-            tc::mbar_init(&bar->hand[1][g], 1);
+        for (int i = 0; i < NB; ++i) {
+            tc::mbar_init(&bar->s_full[i], 1);
+            tc::mbar_init(&bar->s_empty[i], 4);  // the group's warps have read the scores
+            tc::mbar_init(&bar->x_full[i], 1);   // armed here with what the other CTA sends
+            tc::mbar_init(&bar->x_free[i], 2);   // its two finishing warps
+            tc::mbar_init(&bar->p_in[i], 1);
+            tc::mbar_init(&bar->p_full[i], 4);
+            tc::mbar_init(&bar->p_free[i], 2);
+            tc::mbar_init(&bar->hand[0][i], 1);
+            tc::mbar_init(&bar->hand[1][i], 1);
+            tc::mbar_init(&bar->mask_full[i], 1);
         }
-        for (int i = 0; i < NMASK; ++i) tc::mbar_init(&bar->mask_full[i], 1);
         tc::mbar_init(&bar->qk_done, 1);
         tc::mbar_init(&bar->o_done, 1);
         *abort_flag = 0;
@@ -296,7 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc::tc_fence_after();
     tc::cluster_sync();  // both CTAs' barriers exist before any remote arrive
-    const uint32_t tmem = ms->tmem_slot;
+    const uint32_t tmem = __shfl_sync(FULL, ms->tmem_slot, 0);
     pdl_wait();  // the set-up above overlapped the previous kernel; global memory only from here
 
     // Cache row of token s, or -1 (behind the last token, or on no page).
@@ -317,8 +311,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (have >> i & 1) m |= 0xffffull << 16 * i;
-            ms->live[t % NMASK] = m;
-            tc::mbar_arrive(&bar->mask_full[t % NMASK]);
+            ms->live[t % NB] = m;
+            tc::mbar_arrive(&bar->mask_full[t % NB]);
         }
     };
 
@@ -339,171 +333,199 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             bool ok = true;
             for (int t = 0; ok && t < n; ++t) {
                 const int st = t % NSTAGE;
-                // Who waits for stages waits for every one in turn (a barrier's phase can be told from its neighbours only):
-                // the stages that the loading warps fill are handed on to them.
                 ok = __all_sync(FULL, tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 101, P.wait_limit));
                 if (!ok) break;
                 put_mask(t, rows);
-                if ((t0 + t + 1) * TK > safe) {
-                    if (lane == 0) tc::mbar_arrive(&bar->go[st]);
-                } else {
-                    // every token of the tile exists
-                    const int row = __shfl_sync(FULL, rows, (k * (run / 16)) & 3);
-                    if (lane == 0) tc::mbar_arrive_expect_tx(&bar->kv_full[st], STAGE);
-                    __syncwarp();
-                    uint8_t *dst = KV + st * STAGE;
-                    if (lat) tc::tma_load_3d(dst + j * SLAB + k * run * 128, &tm_kv, &bar->kv_full[st], 0, row, rank * 4 + j);
-                    else if (k < runs) tc::tma_load_2d(dst + 4 * SLAB + k * run * 64, &tm_pe, &bar->kv_full[st], rank * 32, row);
-                }
+                // Tiles with hidden tokens pass through warp 3; of runs behind the last token nothing is read.
+                uint64_t *full = (t0 + t + 1) * TK > safe ? &bar->raw[st] : &bar->kv_full[st];
+                const int row = __shfl_sync(FULL, rows, (k * (run / 16)) & 3);
+                const bool go = (lat || k < runs) && row >= 0;
+                const int n_lat = __popc(__ballot_sync(FULL, go && lat)), n_pe = __popc(__ballot_sync(FULL, go && !lat));
+                if (lane == 0)
+                    tc::mbar_arrive_expect_tx(full, (uint32_t)(run * (n_lat * (runs == 1 ? 512 : 128) + n_pe * 64)));
+                __syncwarp();
+                uint8_t *dst = KV + st * STAGE;
+                if (go && lat) tc::tma_load_3d(dst + j * SLAB + k * run * 128, &tm_kv, full, 0, row, rank * 4 + j);
+                else if (go) tc::tma_load_2d(dst + 4 * SLAB + k * run * 64, &tm_pe, full, rank * 32, row);
                 rows = runs_of(t + 1);
             }
         }
-    } else if (warp == 1 && lane == 0 && n > 0) {
+    } else if (warp == 1 && n > 0) {
         // ---------------- QK^T issuer: tile t into score buffer t % 2 once its tokens are here ----------------
-        // (PV comes from another thread: an issue blocks while the tensor pipe is busy.)
-        const uint64_t kd = tc::smem_desc(tc::smem_u32(KV), 16, 1024);
-        const uint64_t rd = tc::smem_desc(tc::smem_u32(KV) + 4 * SLAB, 16, 512, tc::kSwizzle64B);
-        const uint64_t qd = tc::smem_desc(tc::smem_u32(QR), 16, 512, tc::kSwizzle64B);
-        bool ok = tc::mbar_wait(&bar->q_ready, 0, abort_flag, err, 102, P.wait_limit);
+        // (PV comes from another warp: an issue blocks while the tensor pipe is busy.)
+        const uint32_t issue = tc::elect_one();
+        const uint32_t kv0 = __shfl_sync(FULL, tc::smem_u32(KV), 0), qr0 = __shfl_sync(FULL, tc::smem_u32(QR), 0);
+        const uint64_t kd = tc::smem_desc(kv0, 16, 1024);
+        const uint64_t rd = tc::smem_desc(kv0 + 4 * SLAB, 16, 512, tc::kSwizzle64B);
+        const uint64_t qd = tc::smem_desc(qr0, 16, 512, tc::kSwizzle64B);
+        bool ok = __all_sync(FULL, tc::mbar_wait(&bar->q_ready, 0, abort_flag, err, 102, P.wait_limit));
         for (int t = 0; ok && t < n; ++t) {
             const int st = t % NSTAGE;
-            if (t >= 2 && !(ok = tc::mbar_wait(&bar->s_empty[t & 1], ((t >> 1) - 1) & 1, abort_flag, err, 103, P.wait_limit))) break;
-            if (!(ok = tc::mbar_wait(&bar->kv_full[st], (t / NSTAGE) & 1, abort_flag, err, 104, P.wait_limit))) break;
+            if (t >= 2) ok = tc::mbar_wait(&bar->s_empty[(t - 2) % NB], ((t - 2) / NB) & 1, abort_flag, err, 103, P.wait_limit);
+            ok = tc::mbar_wait(&bar->kv_full[st], (t / NSTAGE) & 1, abort_flag, err, 104, P.wait_limit) && ok;
+            if (!(ok = __all_sync(FULL, ok))) break;
             tc::tc_fence_after();
             const uint32_t d = tmem + COL_S + (t & 1) * TK;
             const uint64_t off = (uint64_t)(uint32_t)(st * (STAGE / 16));
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                tc::mma_f16_ts(d, tmem + COL_Q + i * 8, kd + off + ((i >> 2) * SLAB + (i & 3) * 32) / 16, IDESC_QK, i != 0);
+                tc::mma_f16_ts_if(issue, d, tmem + COL_Q + i * 8, kd + off + ((i >> 2) * SLAB + (i & 3) * 32) / 16, IDESC_QK,
+                                  i != 0);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) tc::mma_f16(d, qd + i * 2, rd + off + i * 2, IDESC_QK, 1);
-            tc::mma_commit(&bar->s_full[t & 1]);
+            for (int i = 0; i < 2; ++i) tc::mma_f16_if(issue, d, qd + i * 2, rd + off + i * 2, IDESC_QK, 1);
+            if (issue) tc::mma_commit(&bar->s_full[t % NB]);
+            __syncwarp();
         }
-        // No MMA of this thread may still be running when the tensor memory is released.
-        tc::mma_commit(&bar->qk_done);
+        // No MMA of this warp may still be running when the tensor memory is released.
+        if (issue) tc::mma_commit(&bar->qk_done);
         tc::mbar_wait(&bar->qk_done, 0, nv, err, 105);
-    } else if (warp == 2 && lane == 0 && n > 0) {
-        // ---------------- PV issuer: frees the stage, the probabilities here and (the other CTA's copy) there ----------------
-        const uint64_t pd = tc::smem_desc(tc::smem_u32(Pb), 16, 1024), vd = tc::smem_desc(tc::smem_u32(KV), SLAB, 1024);
-        const uint16_t peer_mask = (uint16_t)(1u << peer);
+    } else if (warp == 2 && n > 0) {
+        // ---------------- PV issuer: frees the stage and the probabilities (which both CTAs hold) ----------------
+        const uint32_t issue = tc::elect_one();
+        const uint32_t kv0 = __shfl_sync(FULL, tc::smem_u32(KV), 0), p0 = __shfl_sync(FULL, tc::smem_u32(Pb), 0);
+        const uint64_t pd = tc::smem_desc(p0, 16, 1024), vd = tc::smem_desc(kv0, SLAB, 1024);
         for (int t = 0; t < n; ++t) {
-            if (!tc::mbar_wait(&bar->p_full[t & 1], (t >> 1) & 1, abort_flag, err, 106, P.wait_limit)) break;
+            if (!__all_sync(FULL, tc::mbar_wait(&bar->p_full[t % NB], (t / NB) & 1, abort_flag, err, 106, P.wait_limit))) break;
             tc::tc_fence_after();
             const int st = t % NSTAGE;
             const uint64_t a0 = pd + (uint64_t)(uint32_t)((t & 1) * (P_BYTES / 16));
             const uint64_t b0 = vd + (uint64_t)(uint32_t)(st * (STAGE / 16));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                tc::mma_f16(tmem + COL_O, a0 + kk * 2, b0 + kk * (16 * 128 / 16), IDESC_PV, (t | kk) != 0);
-            tc::mma_commit(&bar->kv_empty[st]);
-            tc::mma_commit(&bar->p_empty[t & 1]);
-            tc::mma_commit_multicast(&bar->pv_peer[t & 1], peer_mask);
+                tc::mma_f16_if(issue, tmem + COL_O, a0 + kk * 2, b0 + kk * (16 * 128 / 16), IDESC_PV, (t | kk) != 0);
+            if (issue) {
+                tc::mma_commit(&bar->kv_empty[st]);
+                tc::mma_commit_multicast(&bar->p_free[t % NB], 3);
+            }
+            __syncwarp();
         }
-        tc::mma_commit(&bar->o_done);
+        if (issue) tc::mma_commit(&bar->o_done);
         tc::mbar_wait(&bar->o_done, 0, nv, err, 107);
         tc::mbar_wait(&bar->q_stage, 0, nv, err, 108);  // after an abort nobody else may have waited for it
-    } else if (warp >= 12 && n > 0) {
-        // ---------------- loading warps ----------------
-        // Thread: one token, 128 of the CTA's 256 columns (two slabs), half of its rotary columns.
-        const int tid = threadIdx.x - 12 * 32, tok = tid >> 1, part = tid & 1;
-        const auto put_rope = [&](uint8_t *stage, const uint4 (&w)[2]) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                *(uint4 *)(stage + 4 * SLAB + tok * 64 + (((2 * part + e) ^ ((tok >> 1) & 3)) << 4)) = w[e];
+    } else if (!KV8 && warp == 3 && n > 0) {
+        // ---------------- bf16 tiles with hidden tokens: Inf and NaN of the latents (V) become 0 ----------------
+        for (int t = max(0, safe / TK - t0); t < n; ++t) {
+            const int st = t % NSTAGE;
+            // the stage's first such tile is number t % NSTAGE + a multiple: every phase of `raw` is this warp's
+            const int use = (t - max(0, safe / TK - t0)) / NSTAGE;
+            if (!__all_sync(FULL, tc::mbar_wait(&bar->raw[st], use & 1, abort_flag, err, 110, P.wait_limit))) break;
+            uint4 *p = (uint4 *)(KV + st * STAGE) + lane;
+#pragma unroll 8
+            for (int i = 0; i < 4 * SLAB / 512; ++i) {
+                const uint4 v = p[i * 32];
+                const uint4 f = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+                if ((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) p[i * 32] = f;
+            }
+            tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar->kv_full[st]);
+        }
+    } else if (KV8 && warp >= 12 && n > 0) {
+        // ---------------- loading warps (e4m3) ----------------
+        // Warp w brings 16 tokens, which lie together: one look at the block table a tile.
+        const int w = warp - 12;
+        int64_t row = -1;   // of its first token
+        int count = 0;      // tokens that exist
+        const auto locate = [&](int t) {
+            const int s = (t0 + t) * TK + w * 16;
+            row = row_of(s);
+            count = row >= 0 ? min(16, tokens - s) : 0;
         };
-        const auto get_rope = [&](int64_t row, uint4 (&w)[2]) {
+        // Rotary columns: eight tokens x four 16-byte chunks an instruction.
+        uint4 rp[2];
+        const auto get_rope = [&]() {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                w[e] = row >= 0 ? __ldg((const uint4 *)(kpe + row * P.ld_pe + rank * 32 + part * 16) + e)
-                                : make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 2; ++e) {
+                const int tok = e * 8 + (lane >> 2);
+                rp[e] = tok < count ? __ldg((const uint4 *)(kpe + (row + tok) * P.ld_pe + rank * 32) + (lane & 3))
+                                    : make_uint4(0, 0, 0, 0);
+            }
+        };
+        const auto put_rope = [&](uint8_t *stage) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int tok = w * 16 + e * 8 + (lane >> 2);
+                *(uint4 *)(stage + 4 * SLAB + tok * 64 + (((lane & 3) ^ ((tok >> 1) & 3)) << 4)) = rp[e];
+            }
         };
         bool ok = true;
-        if constexpr (KV8) {
-            const uint8_t *codes = (const uint8_t *)kv;
-            uint4 c[8], rp[2];
-            float sc;
+        {
+            // Pass i: tokens 4 (i / 2) .., block i % 2 of the CTA's two; a token's 128 codes are eight lanes' 16 bytes.
+            // The next tile's codes wait in registers.
+            const uint8_t *codes = (const uint8_t *)kv + rank * 256 + (lane & 7) * 16;
+            uint4 c[8];
+            float sc = 0.0f;   // scale of token lane / 2, block lane % 2
             int runs = 0;
             const auto fetch = [&](int t) {
-                const int64_t row = row_of((t0 + t) * TK + tok);
+                locate(t);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    c[i] = row >= 0 ? __ldg((const uint4 *)(codes + row * P.ld_kv + rank * 256 + part * 128) + i)
-                                    : make_uint4(0, 0, 0, 0);
-                sc = row >= 0 ? __ldg(kv_scale + row * (DC / 128) + rank * 2 + part) : 0.0f;
-                get_rope(row, rp);
-                if (warp == 12) runs = runs_of(t);
+                for (int i = 0; i < 8; ++i) {
+                    const int tok = (i >> 1) * 4 + (lane >> 3);
+                    c[i] = tok < count ? __ldg((const uint4 *)(codes + (row + tok) * P.ld_kv + (i & 1) * 128))
+                                       : make_uint4(0, 0, 0, 0);
+                }
+                sc = (lane >> 1) < count ? __ldg(kv_scale + (row + (lane >> 1)) * (DC / 128) + rank * 2 + (lane & 1)) : 0.0f;
+                get_rope();
+                if (w == 0) runs = runs_of(t);
             };
+            const int slab = (lane >> 2) & 1, chunk = (lane & 3) * 2;
             fetch(0);
             for (int t = 0; t < n; ++t) {
                 const int st = t % NSTAGE;
                 ok = __all_sync(FULL, tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 109, P.wait_limit));
                 if (!ok) break;
-                if (warp == 12) put_mask(t, runs);
+                if (w == 0) put_mask(t, runs);
                 uint8_t *stage = KV + st * STAGE;
-                const bool scrub = (t0 + t + 1) * TK > safe;
-                const Scale2 s2 = scale2(sc);
+                // A hidden token's scale may be anything: past what a finite product allows it counts as 0 (the codes
+                // themselves become finite numbers, whatever they are).
+                if ((t0 + t + 1) * TK > safe && !(fabsf(sc) <= 0x1p118f)) sc = 0.0f;
+                // 2^120 scale is one factor while it stays in bf16's range
+                const bool big = __any_sync(FULL, sc > 128.0f);
+                const float up = big ? 0x1p120f : 0x1p120f * sc;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {  // 16 columns: chunks 2i, 2i+1 of the token's two 128-byte rows
+                for (int i = 0; i < 8; ++i) {
+                    const int tok = (i >> 1) * 4 + (lane >> 3);
+                    const float f = __shfl_sync(FULL, up, tok * 2 + (i & 1));
                     uint4 o[2];
-                    if (scrub) dequant16<true>(c[i], s2, o); else dequant16<false>(c[i], s2, o);
-                    uint8_t *dst = stage + (2 * part + (i >> 2)) * SLAB + tok * 128;
+                    dequant16(c[i], bf16_pair(f), o);
+                    uint8_t *dst = stage + ((i & 1) * 2 + slab) * SLAB + (w * 16 + tok) * 128;
+                    const int x = (w * 16 + tok) & 7;
+                    // the two slabs' lanes store their chunks in opposite order: eight lanes cover all banks
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) *(uint4 *)(dst + (((2 * (i & 3) + e) ^ (tok & 7)) << 4)) = o[e];
+                    for (int e = 0; e < 2; ++e)
+                        *(uint4 *)(dst + (((chunk + (e ^ slab)) ^ x) << 4)) = (e ^ slab) ? o[1] : o[0];
                 }
-                put_rope(stage, rp);
+                if (big) {  // the second factor, over the stored values
+#pragma unroll 1
+                    for (int i = 0; i < 16; ++i) {
+                        const int tok = i, lane_slab = lane >> 3;
+                        const float f = __shfl_sync(FULL, sc, tok * 2 + (lane_slab >> 1));
+                        uint4 *p = (uint4 *)(stage + lane_slab * SLAB + (w * 16 + tok) * 128 + (lane & 7) * 16);
+                        __syncwarp();
+                        uint4 v = *p;
+                        const uint32_t m = bf16_pair(f);
+                        *p = make_uint4(mul2(v.x, m), mul2(v.y, m), mul2(v.z, m), mul2(v.w, m));
+                    }
+                }
+                put_rope(stage);
                 tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bar->kv_full[st]);
                 if (t + 1 < n) fetch(t + 1);
             }
-        } else {
-            // Tiles with hidden tokens.
-            const __nv_bfloat16 *lat = (const __nv_bfloat16 *)kv;
-            uint32_t turn = 0;  // phase of every stage's `go`
-            for (int t = max(0, safe / TK - t0); t < n; ++t) {
-                const int st = t % NSTAGE;
-                const int64_t row = row_of((t0 + t) * TK + tok);
-                uint4 w[8], rp[2];
-                const auto get = [&](int half) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e] = row >= 0 ? __ldg((const uint4 *)(lat + row * P.ld_kv + rank * 256 + part * 128 + half * 64) + e)
-                                        : make_uint4(0, 0, 0, 0);
-                };
-                get(0);
-                get_rope(row, rp);
-                ok = tc::mbar_wait(&bar->go[st], (turn >> st) & 1u, abort_flag, err, 110, P.wait_limit);
-                turn ^= 1u << st;
-                uint8_t *stage = KV + st * STAGE;
-                if (ok) {
-                    for (int half = 0; half < 2; ++half) {
-                        if (half) get(1);
-                        uint8_t *dst = stage + (2 * part + half) * SLAB + tok * 128;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *(uint4 *)(dst + ((e ^ (tok & 7)) << 4)) =
-                                make_uint4(finite2(w[e].x), finite2(w[e].y), finite2(w[e].z), finite2(w[e].w));
-                    }
-                    put_rope(stage, rp);
-                    tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
-                }
-                // a warp whose wait gave up comes to the barrier all the same, and they stop together
-                if (!bar_and<2, 128>(ok)) break;
-                if (tid == 0) tc::mbar_arrive(&bar->kv_full[st]);
-            }
         }
-    } else if (warp >= 4 && warp < 12) {
-        // ---------------- softmax groups: group g takes tiles g, g + 2, ..; thread = row h ----------------
+    } else if (warp >= 4 && warp < 4 + SOFT) {
+        // ---------------- softmax groups: group g takes tiles g, g + G, ..; thread = row h ----------------
         const int q = warp & 3, g = (warp >> 2) - 1, h = q * 32 + lane;
         const bool own = (uint32_t)(q >> 1) == rank;      // rows that this CTA finishes
         const int r = h & 63;                             // row within its half
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         bool ok = true;
         if (n > 0) {
-            // The q~ slice moves to tensor memory (A operand of QK^T): four slabs of 32 packed columns, two a group; group 1
-            // puts the rotary slice of the queries into shared memory.
+            // The q~ slice moves to tensor memory (A operand of QK^T): four slabs of 32 packed columns, two each of the first
+            // groups; the last one puts the rotary slice of the queries into shared memory.
             uint4 rq[4];
-            if (g) {
+            if (g == G - 1) {
                 const int64_t row = seq_row0 + lrow + h;
                 const bool there = lrow + h < seq_rows;
                 const uint4 *src = (const uint4 *)(qpe + row * DR + rank * 32);
@@ -511,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 for (int e = 0; e < 4; ++e) rq[e] = there ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
             }
             ok = __all_sync(FULL, tc::mbar_wait(&bar->q_stage, 0, abort_flag, err, 111, P.wait_limit));
-            for (int js = g * 2; ok && js < g * 2 + 2; ++js) {
+            for (int js = g * 2; ok && g < 2 && js < g * 2 + 2; ++js) {
                 const uint8_t *srow = Pb + js * Q_BOX + h * 128;
                 uint32_t qv[32];
 #pragma unroll
@@ -525,27 +547,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 tc::tmem_st32(lanes + COL_Q + js * 32, qv);
             }
             tc::tmem_st_wait();
-            if (g) {
+            if (g == G - 1) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) *(uint4 *)(QR + h * 64 + ((e ^ ((h >> 1) & 3)) << 4)) = rq[e];
                 tc::fence_proxy_async_smem();  // read by the rotary MMAs (async proxy)
             }
             tc::tc_fence_before();
             // Every warp has read its part of the staging: the buffers may carry scores, here and from the other CTA.
-            ok = bar_and<1, 256>(ok);
+            ok = bar_and<1, 32 * SOFT>(ok);
             if (lane == 0) tc::mbar_arrive(&bar->q_ready);
             if (threadIdx.x == 4 * 32) tc::mbar_arrive_remote(tc::map_peer(tc::smem_u32(&bar->peer_ready), peer));
             ok = ok && __all_sync(FULL, tc::mbar_wait(&bar->peer_ready, 0, abort_flag, err, 112, P.wait_limit));
         }
-        const float sl2 = P.scale_log2;
-        uint8_t *Xg = X + g * X_BYTES, *Yg = Y + g * X_BYTES, *Pg = Pb + g * P_BYTES;
+        const float sl2 = fabsf(P.scale_log2);            // not 0
+        const bool negative = P.scale_log2 < 0.0f;
         const auto sw = [&](uint8_t *rowp, int c) { return rowp + ((c ^ (h & 7)) << 4); };
-        // this warp's scores of its tile
-        const auto load_scores = [&](float (&v)[64]) {
+        // this warp's scores of tile t
+        const auto load_scores = [&](int t, float (&v)[64]) {
             tc::tc_fence_after();
             float a[32], c[32];
-            tc::tmem_ld32(lanes + COL_S + g * TK, a);
-            tc::tmem_ld32(lanes + COL_S + g * TK + 32, c);
+            tc::tmem_ld32(lanes + COL_S + (t & 1) * TK, a);
+            tc::tmem_ld32(lanes + COL_S + (t & 1) * TK + 32, c);
             tc::tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -554,19 +576,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bar->s_empty[g]);
+            if (lane == 0) tc::mbar_arrive(&bar->s_empty[t % NB]);
+            if (negative) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) v[j] = -v[j];
+            }
         };
-#define TREE_WAIT(bar_, parity_, site_)                                                                                  \
-    if (!(ok = __all_sync(FULL, tc::mbar_wait(bar_, parity_, abort_flag, err, site_, P.wait_limit)))) break
+        // A lane's waits only note a failure; the warp stops together at the end of the tile.
+        const auto wait = [&](uint64_t *bars, int t, int site) {
+            ok = tc::mbar_wait(&bars[t % NB], (t / NB) & 1, abort_flag, err, site, P.wait_limit) && ok;
+        };
         if (own) {
             const int li = lrow + h;                      // row within the sequence
             const bool mine = li < seq_rows;              // else a row of the next sequence, or none
             const int node = mine ? li / P.H : 0;
             const uint64_t *bits = P.mask ? P.mask + (int64_t)(P.q0[lo] + node) * P.words : nullptr;
             float m_g = -INFINITY, l_g = 0.0f;            // this group's reference and its share of the row sum
-            for (int t = g, k = 0; ok && t < n; t += 2, ++k) {
-                const uint32_t ph = (uint32_t)k & 1u;
-                if (lane == 0 && !(q & 1)) tc::mbar_arrive_expect_tx(&bar->x_full[g], X_BYTES);
+            for (int t = g; ok && t < n; t += G) {
+                uint8_t *Xb = X + (t & 1) * X_BYTES, *Pt = Pb + (t & 1) * P_BYTES;
+                if (lane == 0 && !(q & 1)) tc::mbar_arrive_expect_tx(&bar->x_full[t % NB], X_BYTES);
                 // --- which of the 64 tokens the row sees ---
                 uint64_t see = ~0ull;
                 if ((t0 + t + 1) * TK > safe) {
@@ -584,26 +612,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     }
                 }
                 if (P.pt.table) {
-                    TREE_WAIT(&bar->mask_full[t % NMASK], (t / NMASK) & 1, 113);
-                    see &= ms->live[t % NMASK];
+                    wait(bar->mask_full, t, 113);
+                    see &= ms->live[t % NB];
                 }
-                TREE_WAIT(&bar->s_full[g], ph, 114);
+                wait(bar->s_full, t, 114);
+                __syncwarp();
                 float v[64];
-                load_scores(v);
-                // --- + the other CTA's half, in log2 units ---
-                TREE_WAIT(&bar->x_full[g], ph, 115);
+                load_scores(t, v);
+                // --- + the other CTA's half ---
+                wait(bar->x_full, t, 115);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    const uint4 x = *(const uint4 *)sw(Xg + r * 128, c);
+                    const uint4 x = *(const uint4 *)sw(Xb + r * 128, c);
                     const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        v[8 * c + 2 * e] = fmaf(v[8 * c + 2 * e], sl2, tc::f16_to_f32((uint16_t)(xs[e] & 0xffffu)));
-                        v[8 * c + 2 * e + 1] = fmaf(v[8 * c + 2 * e + 1], sl2, tc::f16_to_f32((uint16_t)(xs[e] >> 16)));
+                        v[8 * c + 2 * e] = tc::add_f16_f32((uint16_t)(xs[e] & 0xffffu), v[8 * c + 2 * e]);
+                        v[8 * c + 2 * e + 1] = tc::add_f16_f32((uint16_t)(xs[e] >> 16), v[8 * c + 2 * e + 1]);
                     }
                 }
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(tc::smem_u32(&bar->x_free[g]), peer));
+                if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(tc::smem_u32(&bar->x_free[t % NB]), peer));
                 if (!__all_sync(FULL, see == ~0ull)) {
                     const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
 #pragma unroll
@@ -612,117 +641,155 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         if (!(s1 >> j & 1)) v[32 + j] = -INFINITY;
                     }
                 }
-                const float mt = max64(v);
-                // --- running reference: the one used for tile t-1 comes from the other group ---
-                float m_prev = -INFINITY;
-                if (t > 0) {
-                    TREE_WAIT(&bar->hand[q & 1][1 - g], ((t - 1) >> 1) & 1, 116);
-                    m_prev = ms->m_pub[1 - g][r];
-                }
-                float m_now = m_prev, alpha = 1.0f;
-                if (mt != -INFINITY) {
-                    if (m_prev == -INFINITY) {
-                        m_now = mt;
-                    } else if (mt > m_prev + RESCALE_LOG2) {
-                        m_now = mt;
-                        alpha = tc::ex2_approx(m_prev - m_now);
-                    }
-                }
-                if (t + 1 < n) {
-                    ms->m_pub[g][r] = m_now;
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bar->hand[q & 1][g]);
-                }
-                if (m_now != m_g) {
-                    if (m_g != -INFINITY) l_g *= tc::ex2_approx(m_g - m_now);
-                    m_g = m_now;
-                }
+                const float mt = max64(v) * sl2;
+                // --- The row's reference (a whole number, in log2 units) moves up when a tile exceeds it by more than 8.  The
+                // one that tile t-1 used comes from the other group; rather than wait for it the probabilities are taken
+                // against this group's last one, and corrected by a power of two in the rare case that it has moved. ---
+                const auto moved = [&](float from) {
+                    return mt != -INFINITY && !(mt <= from + RESCALE_LOG2) ? ceilf(mt) : from;
+                };
+                float m_prev = m_g, m_used;
+                const bool ahead = __all_sync(FULL, m_g != -INFINITY);
+                const auto handed = [&]() {
+                    wait(bar->hand[q & 1], t - 1, 116);
+                    m_prev = ms->m_pub[(t + G - 1) % G][r];
+                };
+                if (!ahead && t > 0) handed();
+                m_used = moved(m_prev);
                 // --- probabilities, rounded to bf16 for the PV product; the row sum takes the rounded ones ---
-                const float neg = m_now == -INFINITY ? 0.0f : -m_now;
+                const float neg = m_used == -INFINITY ? 0.0f : -m_used;
                 uint32_t pk[32];
                 float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    const float p0 = tc::ex2_approx(v[2 * j] + neg), p1 = tc::ex2_approx(v[2 * j + 1] + neg);
+                    const float p0 = tc::ex2_approx(fmaf(v[2 * j], sl2, neg)), p1 = tc::ex2_approx(fmaf(v[2 * j + 1], sl2, neg));
                     const __nv_bfloat162 t2 = __floats2bfloat162_rn(p0, p1);
                     pk[j] = *(const uint32_t *)&t2;
                     sum0 = tc::add_bf16_f32((uint16_t)(pk[j] & 0xffffu), sum0);
                     sum1 = tc::add_bf16_f32((uint16_t)(pk[j] >> 16), sum1);
                 }
-                l_g += sum0 + sum1;
-                // --- P(t) here and to the other CTA, once both PV(t-2) are done with the buffer ---
-                if (k > 0) {
-                    TREE_WAIT(&bar->p_empty[g], (k - 1) & 1, 117);
-                    TREE_WAIT(&bar->pv_peer[g], (k - 1) & 1, 118);
+                float sum = sum0 + sum1, m_now = m_used;
+                if (ahead) {
+                    handed();
+                    m_now = moved(m_prev);
+                    if (__any_sync(FULL, m_now != m_used)) {
+                        const float f = pow2(m_used - m_now);
+                        const uint32_t f2 = bf16_pair(f);
+                        sum *= f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) pk[j] = mul2(pk[j], f2);
+                    }
                 }
-                // --- the context moves after PV(t-1) and before PV(t) (PV(t-2) is done: the phase is the next one) ---
+                if (t + 1 < n) {
+                    ms->m_pub[g][r] = m_now;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar->hand[q & 1][t % NB]);
+                }
+                float alpha = 1.0f;
+                if (__any_sync(FULL, m_now != m_prev || m_now != m_g)) {
+                    if (m_prev != -INFINITY) alpha = pow2(m_prev - m_now);
+                    if (m_g != -INFINITY) l_g *= pow2(m_g - m_now);
+                    m_g = m_now;
+                }
+                l_g += sum;
+                // --- the buffer that P(t) goes to is free once both PV(t-2) are done ---
+                if (t >= 2) wait(bar->p_free, t - 2, 117);
+                // --- the context moves after PV(t-1) and before PV(t) ---
                 if (__any_sync(FULL, alpha != 1.0f)) {
-                    TREE_WAIT(&bar->p_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, 119);
+                    wait(bar->p_free, t - 1, 118);
+                    __syncwarp();
                     rescale_rows(lanes, alpha);
                 }
+                // --- P(t), here and to the other CTA ---
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    *(uint4 *)sw(Pg + h * 128, c) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-                ms->alpha_out[g][r] = alpha;
+                    *(uint4 *)sw(Pt + h * 128, c) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                ms->alpha_out[t & 1][r] = alpha;
                 tc::fence_proxy_async_smem();  // read by the PV product and by the copies (async proxy)
-                __syncwarp();
+                ok = __all_sync(FULL, ok);
                 if (lane == 0) {
-                    const uint32_t in = tc::map_peer(tc::smem_u32(&bar->p_in[g]), peer);
-                    uint8_t *rows32 = Pg + q * 32 * 128;
+                    const uint32_t in = tc::map_peer(tc::smem_u32(&bar->p_in[t % NB]), peer);
+                    uint8_t *rows32 = Pt + q * 32 * 128;
                     tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(rows32), peer), rows32, 32 * 128, in);
-                    tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(&ms->alpha_in[g][(q & 1) * 32]), peer),
-                                          &ms->alpha_out[g][(q & 1) * 32], 32 * 4, in);
-                    tc::mbar_arrive(&bar->p_full[g]);
+                    tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(&ms->alpha_in[t & 1][(q & 1) * 32]), peer),
+                                          &ms->alpha_out[t & 1][(q & 1) * 32], 32 * 4, in);
+                    tc::mbar_arrive(&bar->p_full[t % NB]);
                 }
             }
-            // The other CTA's last PV products are done: its copies from here have been read, and its commits that arrive
-            // here have arrived.
-            if (ok && n > 0) {
-                for (int t = max(0, n - 2); t < n; ++t)
-                    if ((t & 1) == g)
-                        ok = __all_sync(FULL, tc::mbar_wait(&bar->pv_peer[g], (t >> 1) & 1, abort_flag, err, 120, P.wait_limit));
-            }
+            // The PV products of the group's last tile are done in both CTAs: copies from here have been read, and the
+            // commits that arrive here have arrived.
+            if (ok && g < n) wait(bar->p_free, (n - 1 - g) / G * G + g, 119);
             ms->sum[g][r] = l_g;
             ms->ref[g][r] = m_g;
         } else {
-            for (int t = g, k = 0; ok && t < n; t += 2, ++k) {
-                const uint32_t ph = (uint32_t)k & 1u;
-                if (lane == 0 && !(q & 1)) tc::mbar_arrive_expect_tx(&bar->p_in[g], X_BYTES + HR * 4);
-                TREE_WAIT(&bar->s_full[g], ph, 121);
+            // The probabilities of these rows and their context factors, when they come back: tile t is ready for PV here.
+            const auto take = [&](int t) {
+                const float alpha = ms->alpha_in[t & 1][r];
+                if (__any_sync(FULL, alpha != 1.0f)) {
+                    wait(bar->p_free, t - 1, 120);
+                    __syncwarp();
+                    rescale_rows(lanes, alpha);
+                }
+                ok = __all_sync(FULL, ok);
+                if (lane == 0) tc::mbar_arrive(&bar->p_full[t % NB]);
+            };
+            bool owed = false;  // the previous tile's probabilities have not been taken yet
+            for (int t = g; ok && t < n; t += G) {
+                uint8_t *Yb = Y + (t & 1) * X_BYTES;
+                if (lane == 0 && !(q & 1)) tc::mbar_arrive_expect_tx(&bar->p_in[t % NB], X_BYTES + HR * 4);
+                // Whichever is first: this tile's scores, or the previous one's probabilities.
+                if (owed) {
+                    const long long c0 = clock64();
+                    while (!__all_sync(FULL, tc::mbar_test(&bar->s_full[t % NB], (t / NB) & 1))) {
+                        if (__all_sync(FULL, tc::mbar_test(&bar->p_in[(t - G) % NB], ((t - G) / NB) & 1))) {
+                            take(t - G);
+                            owed = false;
+                            break;
+                        }
+                        // the wait below reports it
+                        if (__any_sync(FULL, *abort_flag || clock64() - c0 > P.wait_limit)) break;
+                    }
+                }
+                // the other CTA has read tile t - 2 from its buffer, and so from the one here
+                if (t >= 2) wait(bar->x_free, t - 2, 121);
+                wait(bar->s_full, t, 122);
+                __syncwarp();
                 float v[64];
-                load_scores(v);
+                load_scores(t, v);
                 uint32_t w[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) w[j] = tc::f16x2_satfinite(v[2 * j] * sl2, v[2 * j + 1] * sl2);
-                // the other CTA has read this group's previous tile, from there and so from here
-                if (k > 0) TREE_WAIT(&bar->x_free[g], (k - 1) & 1, 122);
+                for (int j = 0; j < 32; ++j) w[j] = tc::f16x2_satfinite(v[2 * j], v[2 * j + 1]);
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    *(uint4 *)sw(Yg + r * 128, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                    *(uint4 *)sw(Yb + r * 128, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
                 tc::fence_proxy_async_smem();  // read by the copy (async proxy)
                 __syncwarp();
                 if (lane == 0)
-                    tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(Xg + (q & 1) * 32 * 128), peer), Yg + (q & 1) * 32 * 128,
-                                          32 * 128, tc::map_peer(tc::smem_u32(&bar->x_full[g]), peer));
-                // --- the probabilities of these rows, and their context factors ---
-                TREE_WAIT(&bar->p_in[g], ph, 123);
-                const float alpha = ms->alpha_in[g][r];
-                if (__any_sync(FULL, alpha != 1.0f)) {
-                    TREE_WAIT(&bar->p_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, 124);
-                    rescale_rows(lanes, alpha);
+                    tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(X + (t & 1) * X_BYTES + (q & 1) * 32 * 128), peer),
+                                          Yb + (q & 1) * 32 * 128, 32 * 128,
+                                          tc::map_peer(tc::smem_u32(&bar->x_full[t % NB]), peer));
+                if (owed) {
+                    wait(bar->p_in, t - G, 123);
+                    take(t - G);
                 }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar->p_full[g]);
+                ok = __all_sync(FULL, ok);
+                owed = true;
+            }
+            if (ok && owed) {
+                const int t = (n - 1 - g) / G * G + g;  // the group's last tile
+                wait(bar->p_in, t, 124);
+                take(t);
             }
         }
-#undef TREE_WAIT
         // ---------------- row sums: the finishing warps' results, to both CTAs ----------------
-        bar_and<1, 256>(ok);
+        bar_and<1, 32 * SOFT>(ok);
         if (own && g == 0) {
-            const float la = ms->sum[0][r], ma = ms->ref[0][r], lb = ms->sum[1][r], mb = ms->ref[1][r];
-            const float m = fmaxf(ma, mb);
-            const float sum = (ma == -INFINITY ? 0.0f : la * tc::ex2_approx(ma - m)) +
-                              (mb == -INFINITY ? 0.0f : lb * tc::ex2_approx(mb - m));
+            float m = ms->ref[0][r], sum = 0.0f;
+#pragma unroll
+            for (int i = 1; i < G; ++i) m = fmaxf(m, ms->ref[i][r]);
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (ms->ref[i][r] != -INFINITY) sum += ms->sum[i][r] * pow2(ms->ref[i][r] - m);
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
             ms->inv[h] = inv;
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::map_peer(tc::smem_u32(&ms->inv[h]), peer)), "f"(inv)
@@ -742,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     }
     tc::cluster_sync();  // both CTAs have every row's sum, and send each other nothing more
-    if (warp >= 4 && warp < 12) {
+    if (warp >= 4 && warp < 12) {  // two warps a lane quarter
         // ---------------- epilogue: normalise, stage rows in the token stages, write whole rows ----------------
         const int q = warp & 3, g = (warp >> 2) - 1, h = q * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
@@ -776,7 +843,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
         }
-        bar_and<1, 256>(true);
+        bar_and<2, 256>(true);
         const int64_t part = whole ? 0 : (int64_t)P.part0[lo] + rem;
         const int rows = min(ROWS, seq_rows - lrow);
         for (int i = warp - 4; i < rows; i += 8) {
