@@ -55,13 +55,16 @@ constexpr int TK = 64;                  // tokens of a tile
 constexpr int SLAB = TK * 128;          // 64 tokens x 64 columns, 128-byte swizzle: 8 KB
 constexpr int ROPE = TK * 64;           // 64 tokens x 32 rotary columns, 64-byte swizzle: 4 KB
 constexpr int STAGE = 4 * SLAB + ROPE;  // a CTA's columns of a tile
-constexpr int NSTAGE = 4;
+constexpr int NSTAGE = 4;               // e4m3 caches: four stages that serve K and V
+// bf16 caches: two stages of K, free after QK^T, and two of V (the latents again), loaded when PV comes near: no operand
+// waits in shared memory for a softmax.
+constexpr int VSTAGE = 4 * SLAB;
+static_assert(2 * STAGE + 2 * VSTAGE <= NSTAGE * STAGE, "stages");
 constexpr int P_BYTES = ROWS * TK * 2;  // probabilities of all rows
 constexpr int X_BYTES = HR * TK * 2;    // fp16 partial scores of half of the rows
 constexpr int Q_BOX = ROWS * 128;       // 128 rows x 64 columns of q~ (staged in the exchange buffers)
 constexpr int QR_BYTES = ROWS * 64;     // rotary slice of the queries, 64-byte swizzle
-constexpr int NB = 6;                   // barriers of a kind: tile t uses number t % 6, which belongs to one softmax group and one
-                                        // buffer whether there are two groups or three
+constexpr int NB = 6;                   // barriers of a kind: tile t uses number t % 6, which belongs to one group and one buffer
 constexpr uint32_t COL_S = 0, COL_Q = 128, COL_O = 256;
 constexpr uint32_t IDESC_QK = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, ROWS, TK, 0, 0);
 constexpr uint32_t IDESC_PV = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, ROWS, 256, 0, 1);
@@ -69,22 +72,23 @@ constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr long long kAbortQuietCycles = 1LL << 18;
 constexpr int PAIRS = 76;               // 152 SMs
-// warp 0: TMA; 1: QK^T; 2: tensor memory, PV; 3: bf16 tiles with hidden tokens; from 4 on the softmax groups of four
-// (warp % 4 = lane quarter): three, or for e4m3 two, and 12-15 load
-constexpr int THREADS = 512;
-constexpr int MAX_G = 3;
+// warp 0: TMA (Q, bf16 K); 1: QK^T; 2: tensor memory, PV; 3: TMA (bf16 V); from 4 on the softmax groups of four
+// (warp % 4 = lane quarter); of an e4m3 cache four more load
+constexpr int G = 3;                    // softmax groups
+constexpr int SOFT = 4 * G;
+constexpr int FIRST_LOAD = 4 + SOFT;
 
 struct Bars {
-    uint64_t q_stage, q_ready, peer_ready, kv_full[NSTAGE], kv_empty[NSTAGE], raw[NSTAGE], s_full[NB], s_empty[NB];
+    uint64_t q_stage, q_ready, peer_ready, kv_full[NSTAGE], kv_empty[NSTAGE], raw[2], s_full[NB], s_empty[NB];
     uint64_t x_full[NB], x_free[NB];  // the other CTA's partial scores are here; it has read ours
     uint64_t p_in[NB], p_full[NB];    // the other CTA's probabilities are here; all are, and the context is ready for them
     uint64_t p_free[NB];              // the PV products of both CTAs are done
-    uint64_t hand[2][NB], mask_full[NB], qk_done, o_done;
+    uint64_t hand[4][NB], mask_full[NB], qk_done, o_done;
 };
 struct Misc {
-    float m_pub[MAX_G][HR];           // reference maximum that a group used, for the next tile's group
+    float m_pub[G][HR];           // reference maximum that a group used, for the next tile's group
     float alpha_out[2][HR], alpha_in[2][HR];  // context factors of a tile, of this CTA's rows and of the other's
-    float sum[MAX_G][HR], ref[MAX_G][HR];     // a group's share of the row sum and its reference
+    float sum[G][HR], ref[G][HR];     // a group's share of the row sum and its reference
     float inv[ROWS];                  // 1 / row sum
     uint64_t live[NB];                // tokens of a tile whose page exists
     Bars bar;
@@ -192,25 +196,36 @@ __device__ __forceinline__ void rescale_rows(uint32_t lanes, float alpha) {
     tc::tc_fence_before();
 }
 
-// Maximum of 64 values as a tree (depth 4).
-__device__ __forceinline__ float max64(const float (&v)[64]) {
-    float a[22], b[8];
+// 16 lanes x 64 fp32 columns: thread i gets of rows i / 4 (v[4j], v[4j + 1]) and i / 4 + 8 (v[4j + 2], v[4j + 3]) the
+// columns 8j + 2 (i % 4) and the next.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
 #pragma unroll
-    for (int i = 0; i < 21; ++i) a[i] = tc::max3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
-    a[21] = v[63];
-#pragma unroll
-    for (int i = 0; i < 7; ++i) b[i] = tc::max3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
-    b[7] = a[21];
-    return tc::max3(tc::max3(b[0], b[1], b[2]), tc::max3(b[3], b[4], b[5]), fmaxf(b[6], b[7]));
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Four 8 x 8 tiles of 16-bit values in that layout -> shared memory rows (lane i: row i % 8 of tile i / 8).
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
 }
 
 template <bool KV8>
 struct Cfg {
-    static constexpr int G = KV8 ? 2 : 3;  // softmax groups
+    static constexpr int THREADS = 32 * (FIRST_LOAD + (KV8 ? 4 : 0));
 };
 
 template <bool KV8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                    const __grid_constant__ CUtensorMap tm_pe, int run, const void *__restrict__ kv,
                    const float *__restrict__ kv_scale, const __nv_bfloat16 *__restrict__ kpe,
@@ -219,7 +234,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                    float *__restrict__ lpart) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *KV = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    constexpr int G = Cfg<KV8>::G, SOFT = 4 * G;
     uint8_t *Pb = KV + NSTAGE * STAGE;   // [t % 2] probabilities: rows x 64 tokens, 128-byte swizzle
     uint8_t *X = Pb + 2 * P_BYTES;       // [t % 2] the other CTA's partial scores of this CTA's rows
     uint8_t *Y = X + 2 * X_BYTES;        // [t % 2] this CTA's partial scores of the other's rows, sent from here
@@ -262,20 +276,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int i = 0; i < NSTAGE; ++i) {
             tc::mbar_init(&bar->kv_full[i], KV8 ? 4 : 1);
             tc::mbar_init(&bar->kv_empty[i], 1);
-            tc::mbar_init(&bar->raw[i], 1);
         }
         for (int i = 0; i < NB; ++i) {
             tc::mbar_init(&bar->s_full[i], 1);
             tc::mbar_init(&bar->s_empty[i], 4);  // the group's warps have read the scores
             tc::mbar_init(&bar->x_full[i], 1);   // armed here with what the other CTA sends
-            tc::mbar_init(&bar->x_free[i], 2);   // its two finishing warps
+            tc::mbar_init(&bar->x_free[i], 4);   // its warps
             tc::mbar_init(&bar->p_in[i], 1);
             tc::mbar_init(&bar->p_full[i], 4);
             tc::mbar_init(&bar->p_free[i], 2);
-            tc::mbar_init(&bar->hand[0][i], 1);
-            tc::mbar_init(&bar->hand[1][i], 1);
+            for (int k = 0; k < 4; ++k) tc::mbar_init(&bar->hand[k][i], 1);
             tc::mbar_init(&bar->mask_full[i], 1);
         }
+        tc::mbar_init(&bar->raw[0], 1);
+        tc::mbar_init(&bar->raw[1], 1);
         tc::mbar_init(&bar->qk_done, 1);
         tc::mbar_init(&bar->o_done, 1);
         *abort_flag = 0;
@@ -317,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     };
 
     if (warp == 0 && n > 0) {
-        // ---------------- TMA: the q~ slice (staged in the exchange buffers), then a bf16 cache's tiles ----------------
+        // ---------------- TMA: the q~ slice (staged in the exchange buffers), then K of a bf16 cache ----------------
         if (lane == 0) {
             tc::mbar_arrive_expect_tx(&bar->q_stage, 4 * Q_BOX);
             for (int j = 0; j < 4; ++j)
@@ -330,23 +344,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const bool lat = lane < nlat;
             const int k = lat ? (runs == 1 ? 0 : lane >> 2) : lane - nlat, j = lat && runs > 1 ? lane & 3 : 0;
             int rows = runs_of(0);
-            bool ok = true;
-            for (int t = 0; ok && t < n; ++t) {
-                const int st = t % NSTAGE;
-                ok = __all_sync(FULL, tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 101, P.wait_limit));
-                if (!ok) break;
+            for (int t = 0; t < n; ++t) {
+                const int st = t & 1;
+                if (!__all_sync(FULL, tc::mbar_wait(&bar->kv_empty[st], ((t >> 1) & 1) ^ 1, abort_flag, err, 101, P.wait_limit))) break;
                 put_mask(t, rows);
-                // Tiles with hidden tokens pass through warp 3; of runs behind the last token nothing is read.
-                uint64_t *full = (t0 + t + 1) * TK > safe ? &bar->raw[st] : &bar->kv_full[st];
+                // of runs behind the last token nothing is read
                 const int row = __shfl_sync(FULL, rows, (k * (run / 16)) & 3);
                 const bool go = (lat || k < runs) && row >= 0;
                 const int n_lat = __popc(__ballot_sync(FULL, go && lat)), n_pe = __popc(__ballot_sync(FULL, go && !lat));
                 if (lane == 0)
-                    tc::mbar_arrive_expect_tx(full, (uint32_t)(run * (n_lat * (runs == 1 ? 512 : 128) + n_pe * 64)));
+                    tc::mbar_arrive_expect_tx(&bar->kv_full[st], (uint32_t)(run * (n_lat * (runs == 1 ? 512 : 128) + n_pe * 64)));
                 __syncwarp();
                 uint8_t *dst = KV + st * STAGE;
-                if (go && lat) tc::tma_load_3d(dst + j * SLAB + k * run * 128, &tm_kv, full, 0, row, rank * 4 + j);
-                else if (go) tc::tma_load_2d(dst + 4 * SLAB + k * run * 64, &tm_pe, full, rank * 32, row);
+                if (go && lat) tc::tma_load_3d(dst + j * SLAB + k * run * 128, &tm_kv, &bar->kv_full[st], 0, row, rank * 4 + j);
+                else if (go) tc::tma_load_2d(dst + 4 * SLAB + k * run * 64, &tm_pe, &bar->kv_full[st], rank * 32, row);
                 rows = runs_of(t + 1);
             }
         }
@@ -360,9 +371,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint64_t qd = tc::smem_desc(qr0, 16, 512, tc::kSwizzle64B);
         bool ok = __all_sync(FULL, tc::mbar_wait(&bar->q_ready, 0, abort_flag, err, 102, P.wait_limit));
         for (int t = 0; ok && t < n; ++t) {
-            const int st = t % NSTAGE;
+            const int st = KV8 ? t % NSTAGE : t & 1;
             if (t >= 2) ok = tc::mbar_wait(&bar->s_empty[(t - 2) % NB], ((t - 2) / NB) & 1, abort_flag, err, 103, P.wait_limit);
-            ok = tc::mbar_wait(&bar->kv_full[st], (t / NSTAGE) & 1, abort_flag, err, 104, P.wait_limit) && ok;
+            ok = tc::mbar_wait(&bar->kv_full[st], (KV8 ? t / NSTAGE : t >> 1) & 1, abort_flag, err, 104, P.wait_limit) && ok;
             if (!(ok = __all_sync(FULL, ok))) break;
             tc::tc_fence_after();
             const uint32_t d = tmem + COL_S + (t & 1) * TK;
@@ -373,7 +384,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                   i != 0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) tc::mma_f16_if(issue, d, qd + i * 2, rd + off + i * 2, IDESC_QK, 1);
-            if (issue) tc::mma_commit(&bar->s_full[t % NB]);
+            if (issue) {
+                tc::mma_commit(&bar->s_full[t % NB]);
+                if (!KV8) tc::mma_commit(&bar->kv_empty[st]);
+            }
             __syncwarp();
         }
         // No MMA of this warp may still be running when the tensor memory is released.
@@ -383,18 +397,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // ---------------- PV issuer: frees the stage and the probabilities (which both CTAs hold) ----------------
         const uint32_t issue = tc::elect_one();
         const uint32_t kv0 = __shfl_sync(FULL, tc::smem_u32(KV), 0), p0 = __shfl_sync(FULL, tc::smem_u32(Pb), 0);
-        const uint64_t pd = tc::smem_desc(p0, 16, 1024), vd = tc::smem_desc(kv0, SLAB, 1024);
+        const uint64_t pd = tc::smem_desc(p0, 16, 1024), vd = tc::smem_desc(kv0 + (KV8 ? 0 : 2 * STAGE), SLAB, 1024);
         for (int t = 0; t < n; ++t) {
-            if (!__all_sync(FULL, tc::mbar_wait(&bar->p_full[t % NB], (t / NB) & 1, abort_flag, err, 106, P.wait_limit))) break;
+            bool ok = KV8 || tc::mbar_wait(&bar->kv_full[2 + (t & 1)], (t >> 1) & 1, abort_flag, err, 109, P.wait_limit);
+            ok = tc::mbar_wait(&bar->p_full[t % NB], (t / NB) & 1, abort_flag, err, 106, P.wait_limit) && ok;
+            if (!__all_sync(FULL, ok)) break;
             tc::tc_fence_after();
-            const int st = t % NSTAGE;
+            const int st = KV8 ? t % NSTAGE : t & 1;
             const uint64_t a0 = pd + (uint64_t)(uint32_t)((t & 1) * (P_BYTES / 16));
-            const uint64_t b0 = vd + (uint64_t)(uint32_t)(st * (STAGE / 16));
+            const uint64_t b0 = vd + (uint64_t)(uint32_t)(st * ((KV8 ? STAGE : VSTAGE) / 16));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
                 tc::mma_f16_if(issue, tmem + COL_O, a0 + kk * 2, b0 + kk * (16 * 128 / 16), IDESC_PV, (t | kk) != 0);
             if (issue) {
-                tc::mma_commit(&bar->kv_empty[st]);
+                tc::mma_commit(&bar->kv_empty[KV8 ? st : 2 + st]);
                 tc::mma_commit_multicast(&bar->p_free[t % NB], 3);
             }
             __syncwarp();
@@ -403,27 +419,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc::mbar_wait(&bar->o_done, 0, nv, err, 107);
         tc::mbar_wait(&bar->q_stage, 0, nv, err, 108);  // after an abort nobody else may have waited for it
     } else if (!KV8 && warp == 3 && n > 0) {
-        // ---------------- bf16 tiles with hidden tokens: Inf and NaN of the latents (V) become 0 ----------------
-        for (int t = max(0, safe / TK - t0); t < n; ++t) {
-            const int st = t % NSTAGE;
-            // the stage's first such tile is number t % NSTAGE + a multiple: every phase of `raw` is this warp's
-            const int use = (t - max(0, safe / TK - t0)) / NSTAGE;
-            if (!__all_sync(FULL, tc::mbar_wait(&bar->raw[st], use & 1, abort_flag, err, 110, P.wait_limit))) break;
-            uint4 *p = (uint4 *)(KV + st * STAGE) + lane;
-#pragma unroll 8
-            for (int i = 0; i < 4 * SLAB / 512; ++i) {
-                const uint4 v = p[i * 32];
-                const uint4 f = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
-                if ((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) p[i * 32] = f;
-            }
-            tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
+        // ---------------- TMA: V of a bf16 cache; of tiles with hidden tokens Inf and NaN become 0 ----------------
+        const int runs = TK / run, copies = runs == 1 ? 1 : 4 * runs;
+        const int k = runs == 1 ? 0 : lane >> 2, j = runs == 1 ? 0 : lane & 3;
+        int rows = runs_of(0);
+        uint32_t turn = 0;  // phase of each stage's `raw`
+        for (int t = 0; t < n; ++t) {
+            const int st = t & 1;
+            if (!__all_sync(FULL, tc::mbar_wait(&bar->kv_empty[2 + st], ((t >> 1) & 1) ^ 1, abort_flag, err, 110, P.wait_limit))) break;
+            const bool scrub = (t0 + t + 1) * TK > safe;
+            uint64_t *full = scrub ? &bar->raw[st] : &bar->kv_full[2 + st];
+            const int row = __shfl_sync(FULL, rows, (k * (run / 16)) & 3);
+            const bool go = lane < copies && row >= 0;
+            const int some = __popc(__ballot_sync(FULL, go));
+            if (lane == 0) tc::mbar_arrive_expect_tx(full, (uint32_t)(run * some * (runs == 1 ? 512 : 128)));
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bar->kv_full[st]);
+            uint8_t *stage = KV + 2 * STAGE + st * VSTAGE;
+            if (go) tc::tma_load_3d(stage + j * SLAB + k * run * 128, &tm_kv, full, 0, row, rank * 4 + j);
+            rows = runs_of(t + 1);
+            if (scrub) {
+                if (!__all_sync(FULL, tc::mbar_wait(full, (turn >> st) & 1u, abort_flag, err, 125, P.wait_limit))) break;
+                turn ^= 1u << st;
+                uint4 *p = (uint4 *)stage + lane;
+#pragma unroll 8
+                for (int i = 0; i < VSTAGE / 512; ++i) {
+                    const uint4 v = p[i * 32];
+                    const uint4 f = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+                    if ((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) p[i * 32] = f;
+                }
+                tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar->kv_full[2 + st]);
+            }
         }
-    } else if (KV8 && warp >= 12 && n > 0) {
+    } else if (KV8 && warp >= FIRST_LOAD && n > 0) {
         // ---------------- loading warps (e4m3) ----------------
         // Warp w brings 16 tokens, which lie together: one look at the block table a tile.
-        const int w = warp - 12;
+        const int w = warp - FIRST_LOAD;
         int64_t row = -1;   // of its first token
         int count = 0;      // tokens that exist
         const auto locate = [&](int t) {
@@ -514,16 +546,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (t + 1 < n) fetch(t + 1);
             }
         }
-    } else if (warp >= 4 && warp < 4 + SOFT) {
-        // ---------------- softmax groups: group g takes tiles g, g + G, ..; thread = row h ----------------
-        const int q = warp & 3, g = (warp >> 2) - 1, h = q * 32 + lane;
-        const bool own = (uint32_t)(q >> 1) == rank;      // rows that this CTA finishes
-        const int r = h & 63;                             // row within its half
+    } else if (warp >= 4 && warp < FIRST_LOAD) {
+        // ---------------- softmax groups: group g takes tiles g, g + G, .. ----------------
+        // Of its lane quarter's 32 rows a warp finishes 16 and sends the partial scores of the other 16.
+        const int q = warp & 3, g = (warp >> 2) - 1;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        const uint32_t own_lanes = lanes + (rank * 16u << 16), other_lanes = lanes + (peer * 16u << 16);
+        const float sl2 = fabsf(P.scale_log2);            // not 0; the queries carry its sign
         bool ok = true;
         if (n > 0) {
             // The q~ slice moves to tensor memory (A operand of QK^T): four slabs of 32 packed columns, two each of the first
             // groups; the last one puts the rotary slice of the queries into shared memory.
+            const int h = q * 32 + lane;
+            const uint32_t flip = P.scale_log2 < 0.0f ? 0x80008000u : 0u;
             uint4 rq[4];
             if (g == G - 1) {
                 const int64_t row = seq_row0 + lrow + h;
@@ -533,23 +568,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 for (int e = 0; e < 4; ++e) rq[e] = there ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
             }
             ok = __all_sync(FULL, tc::mbar_wait(&bar->q_stage, 0, abort_flag, err, 111, P.wait_limit));
+#pragma unroll 1
             for (int js = g * 2; ok && g < 2 && js < g * 2 + 2; ++js) {
                 const uint8_t *srow = Pb + js * Q_BOX + h * 128;
                 uint32_t qv[32];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const uint4 t4 = *(const uint4 *)(srow + ((e ^ (h & 7)) << 4));
-                    qv[4 * e] = t4.x;
-                    qv[4 * e + 1] = t4.y;
-                    qv[4 * e + 2] = t4.z;
-                    qv[4 * e + 3] = t4.w;
+                    qv[4 * e] = t4.x ^ flip;
+                    qv[4 * e + 1] = t4.y ^ flip;
+                    qv[4 * e + 2] = t4.z ^ flip;
+                    qv[4 * e + 3] = t4.w ^ flip;
                 }
                 tc::tmem_st32(lanes + COL_Q + js * 32, qv);
             }
             tc::tmem_st_wait();
             if (g == G - 1) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) *(uint4 *)(QR + h * 64 + ((e ^ ((h >> 1) & 3)) << 4)) = rq[e];
+                for (int e = 0; e < 4; ++e)
+                    *(uint4 *)(QR + h * 64 + ((e ^ ((h >> 1) & 3)) << 4)) =
+                        make_uint4(rq[e].x ^ flip, rq[e].y ^ flip, rq[e].z ^ flip, rq[e].w ^ flip);
                 tc::fence_proxy_async_smem();  // read by the rotary MMAs (async proxy)
             }
             tc::tc_fence_before();
@@ -559,231 +597,238 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (threadIdx.x == 4 * 32) tc::mbar_arrive_remote(tc::map_peer(tc::smem_u32(&bar->peer_ready), peer));
             ok = ok && __all_sync(FULL, tc::mbar_wait(&bar->peer_ready, 0, abort_flag, err, 112, P.wait_limit));
         }
-        const float sl2 = fabsf(P.scale_log2);            // not 0
-        const bool negative = P.scale_log2 < 0.0f;
-        const auto sw = [&](uint8_t *rowp, int c) { return rowp + ((c ^ (h & 7)) << 4); };
-        // this warp's scores of tile t
-        const auto load_scores = [&](int t, float (&v)[64]) {
-            tc::tc_fence_after();
-            float a[32], c[32];
-            tc::tmem_ld32(lanes + COL_S + (t & 1) * TK, a);
-            tc::tmem_ld32(lanes + COL_S + (t & 1) * TK + 32, c);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                v[j] = a[j];
-                v[32 + j] = c[j];
-            }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bar->s_empty[t % NB]);
-            if (negative) {
-#pragma unroll
-                for (int j = 0; j < 64; ++j) v[j] = -v[j];
-            }
-        };
         // A lane's waits only note a failure; the warp stops together at the end of the tile.
         const auto wait = [&](uint64_t *bars, int t, int site) {
             ok = tc::mbar_wait(&bars[t % NB], (t / NB) & 1, abort_flag, err, site, P.wait_limit) && ok;
         };
-        if (own) {
-            const int li = lrow + h;                      // row within the sequence
-            const bool mine = li < seq_rows;              // else a row of the next sequence, or none
-            const int node = mine ? li / P.H : 0;
-            const uint64_t *bits = P.mask ? P.mask + (int64_t)(P.q0[lo] + node) * P.words : nullptr;
-            float m_g = -INFINITY, l_g = 0.0f;            // this group's reference and its share of the row sum
-            for (int t = g; ok && t < n; t += G) {
-                uint8_t *Xb = X + (t & 1) * X_BYTES, *Pt = Pb + (t & 1) * P_BYTES;
-                if (lane == 0 && !(q & 1)) tc::mbar_arrive_expect_tx(&bar->x_full[t % NB], X_BYTES);
-                // --- which of the 64 tokens the row sees ---
-                uint64_t see = ~0ull;
-                if ((t0 + t + 1) * TK > safe) {
-                    const int rel = (t0 + t) * TK - first;  // node number of the first token (negative: before the tree)
-                    if (!bits) {
-                        const int left = node + 1 - rel;
-                        see = left >= 64 ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1;
-                    } else if (rel + 64 > 0) {
-                        const int w = rel >> 6, sh = rel & 63;
-                        const uint64_t w0 = w < 0 ? ~0ull : w < P.words ? __ldg(bits + w) : 0ull;
-                        const uint64_t w1 = w + 1 < P.words ? __ldg(bits + w + 1) : 0ull;
-                        see = sh ? (w0 >> sh) | (w1 << (64 - sh)) : w0;
-                        const int left = T - rel;
-                        if (left < 64) see &= left <= 0 ? 0ull : (1ull << left) - 1;
-                    }
-                }
-                if (P.pt.table) {
-                    wait(bar->mask_full, t, 113);
-                    see &= ms->live[t % NB];
-                }
-                wait(bar->s_full, t, 114);
-                __syncwarp();
-                float v[64];
-                load_scores(t, v);
-                // --- + the other CTA's half ---
-                wait(bar->x_full, t, 115);
+        // This thread's two rows (eight apart) and columns 8j + 2 (lane % 4) and the next of each eight.
+        const int ra = q * 16 + (lane >> 2), c0 = 2 * (lane & 3);   // ra: among the CTA's 64 rows
+        const int la = lrow + q * 32 + (int)rank * 16 + (lane >> 2);  // row within the sequence; may be past its end
+        float ref_a = -INFINITY, ref_b = -INFINITY;                 // this group's references
+        float sum_a = 0.0f, sum_b = 0.0f;                           // its share of the row sums, of this thread's columns
+        // Which of tile t's 64 tokens row li sees, from this thread's first column on.
+        const auto sees = [&](int t, int li) {
+            const int rel = (t0 + t) * TK - first;  // node number of the tile's first token (negative: before the tree)
+            const int node = li < seq_rows ? li / P.H : 0;
+            uint64_t see = ~0ull;
+            if (!P.mask) {
+                const int left = node + 1 - rel;
+                see = left >= 64 ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1;
+            } else if (rel + 64 > 0) {
+                const uint64_t *bits = P.mask + (int64_t)(P.q0[lo] + node) * P.words;
+                const int w = rel >> 6, sh = rel & 63;
+                const uint64_t w0 = w < 0 ? ~0ull : w < P.words ? __ldg(bits + w) : 0ull;
+                const uint64_t w1 = w + 1 < P.words ? __ldg(bits + w + 1) : 0ull;
+                see = sh ? (w0 >> sh) | (w1 << (64 - sh)) : w0;
+                const int left = T - rel;
+                if (left < 64) see &= left <= 0 ? 0ull : (1ull << left) - 1;
+            }
+            return see;
+        };
+        const uint32_t p_row = (uint32_t)(q * 32 + rank * 16 + (lane & 15));  // the row this lane addresses in stmatrix
+#pragma unroll 1
+        for (int t = g; ok && t < n; t += G) {
+            const int buf = t & 1;
+            uint8_t *Xw = X + buf * X_BYTES + q * 2048, *Yw = Y + buf * X_BYTES + q * 2048, *Pt = Pb + buf * P_BYTES;
+            if (lane == 0 && q == 0) {
+                tc::mbar_arrive_expect_tx(&bar->x_full[t % NB], X_BYTES);
+                tc::mbar_arrive_expect_tx(&bar->p_in[t % NB], X_BYTES + HR * 4);
+            }
+            uint64_t see_a = ~0ull, see_b = ~0ull;
+            if ((t0 + t + 1) * TK > safe) {
+                see_a = sees(t, la);
+                see_b = sees(t, la + 8);
+            }
+            if (P.pt.table) {
+                wait(bar->mask_full, t, 113);
+                const uint64_t m = ms->live[t % NB];
+                see_a &= m;
+                see_b &= m;
+            }
+            // --- the other CTA's rows: partial scores in fp16, in this layout (the receiving thread has the same); the
+            // buffers are free once the other CTA has read tile t-2 ---
+            if (t >= 2) wait(bar->x_free, t - 2, 114);
+            wait(bar->s_full, t, 115);
+            __syncwarp();
+            tc::tc_fence_after();
+            float v[32];
+            {
+                tmem_ld_16x64(other_lanes + COL_S + buf * TK, v);
+                tc::tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 x = *(const uint4 *)sw(Xb + r * 128, c);
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                for (int i = 0; i < 4; ++i)
+                    *(uint4 *)(Yw + i * 512 + lane * 16) =
+                        make_uint4(tc::f16x2_satfinite(v[8 * i], v[8 * i + 1]), tc::f16x2_satfinite(v[8 * i + 2], v[8 * i + 3]),
+                                   tc::f16x2_satfinite(v[8 * i + 4], v[8 * i + 5]),
+                                   tc::f16x2_satfinite(v[8 * i + 6], v[8 * i + 7]));
+            }
+            tc::fence_proxy_async_smem();  // read by the copy (async proxy)
+            __syncwarp();
+            if (lane == 0)
+                tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(Xw), peer), Yw, 2048,
+                                      tc::map_peer(tc::smem_u32(&bar->x_full[t % NB]), peer));
+            // --- this CTA's rows: its own half in fp32, and the other one's ---
+            tmem_ld_16x64(own_lanes + COL_S + buf * TK, v);
+            tc::tmem_ld_wait();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar->s_empty[t % NB]);
+            wait(bar->x_full, t, 116);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[8 * c + 2 * e] = tc::add_f16_f32((uint16_t)(xs[e] & 0xffffu), v[8 * c + 2 * e]);
-                        v[8 * c + 2 * e + 1] = tc::add_f16_f32((uint16_t)(xs[e] >> 16), v[8 * c + 2 * e + 1]);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(tc::smem_u32(&bar->x_free[t % NB]), peer));
-                if (!__all_sync(FULL, see == ~0ull)) {
-                    const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+            for (int i = 0; i < 4; ++i) {
+                const uint4 x = *(const uint4 *)(Xw + i * 512 + lane * 16);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (!(s0 >> j & 1)) v[j] = -INFINITY;
-                        if (!(s1 >> j & 1)) v[32 + j] = -INFINITY;
-                    }
-                }
-                const float mt = max64(v) * sl2;
-                // --- The row's reference (a whole number, in log2 units) moves up when a tile exceeds it by more than 8.  The
-                // one that tile t-1 used comes from the other group; rather than wait for it the probabilities are taken
-                // against this group's last one, and corrected by a power of two in the rare case that it has moved. ---
-                const auto moved = [&](float from) {
-                    return mt != -INFINITY && !(mt <= from + RESCALE_LOG2) ? ceilf(mt) : from;
-                };
-                float m_prev = m_g, m_used;
-                const bool ahead = __all_sync(FULL, m_g != -INFINITY);
-                const auto handed = [&]() {
-                    wait(bar->hand[q & 1], t - 1, 116);
-                    m_prev = ms->m_pub[(t + G - 1) % G][r];
-                };
-                if (!ahead && t > 0) handed();
-                m_used = moved(m_prev);
-                // --- probabilities, rounded to bf16 for the PV product; the row sum takes the rounded ones ---
-                const float neg = m_used == -INFINITY ? 0.0f : -m_used;
-                uint32_t pk[32];
-                float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float p0 = tc::ex2_approx(fmaf(v[2 * j], sl2, neg)), p1 = tc::ex2_approx(fmaf(v[2 * j + 1], sl2, neg));
-                    const __nv_bfloat162 t2 = __floats2bfloat162_rn(p0, p1);
-                    pk[j] = *(const uint32_t *)&t2;
-                    sum0 = tc::add_bf16_f32((uint16_t)(pk[j] & 0xffffu), sum0);
-                    sum1 = tc::add_bf16_f32((uint16_t)(pk[j] >> 16), sum1);
-                }
-                float sum = sum0 + sum1, m_now = m_used;
-                if (ahead) {
-                    handed();
-                    m_now = moved(m_prev);
-                    if (__any_sync(FULL, m_now != m_used)) {
-                        const float f = pow2(m_used - m_now);
-                        const uint32_t f2 = bf16_pair(f);
-                        sum *= f;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) pk[j] = mul2(pk[j], f2);
-                    }
-                }
-                if (t + 1 < n) {
-                    ms->m_pub[g][r] = m_now;
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bar->hand[q & 1][t % NB]);
-                }
-                float alpha = 1.0f;
-                if (__any_sync(FULL, m_now != m_prev || m_now != m_g)) {
-                    if (m_prev != -INFINITY) alpha = pow2(m_prev - m_now);
-                    if (m_g != -INFINITY) l_g *= pow2(m_g - m_now);
-                    m_g = m_now;
-                }
-                l_g += sum;
-                // --- the buffer that P(t) goes to is free once both PV(t-2) are done ---
-                if (t >= 2) wait(bar->p_free, t - 2, 117);
-                // --- the context moves after PV(t-1) and before PV(t) ---
-                if (__any_sync(FULL, alpha != 1.0f)) {
-                    wait(bar->p_free, t - 1, 118);
-                    __syncwarp();
-                    rescale_rows(lanes, alpha);
-                }
-                // --- P(t), here and to the other CTA ---
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *(uint4 *)sw(Pt + h * 128, c) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-                ms->alpha_out[t & 1][r] = alpha;
-                tc::fence_proxy_async_smem();  // read by the PV product and by the copies (async proxy)
-                ok = __all_sync(FULL, ok);
-                if (lane == 0) {
-                    const uint32_t in = tc::map_peer(tc::smem_u32(&bar->p_in[t % NB]), peer);
-                    uint8_t *rows32 = Pt + q * 32 * 128;
-                    tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(rows32), peer), rows32, 32 * 128, in);
-                    tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(&ms->alpha_in[t & 1][(q & 1) * 32]), peer),
-                                          &ms->alpha_out[t & 1][(q & 1) * 32], 32 * 4, in);
-                    tc::mbar_arrive(&bar->p_full[t % NB]);
+                for (int e = 0; e < 4; ++e) {
+                    v[8 * i + 2 * e] = tc::add_f16_f32((uint16_t)(xs[e] & 0xffffu), v[8 * i + 2 * e]);
+                    v[8 * i + 2 * e + 1] = tc::add_f16_f32((uint16_t)(xs[e] >> 16), v[8 * i + 2 * e + 1]);
                 }
             }
-            // The PV products of the group's last tile are done in both CTAs: copies from here have been read, and the
-            // commits that arrive here have arrived.
-            if (ok && g < n) wait(bar->p_free, (n - 1 - g) / G * G + g, 119);
-            ms->sum[g][r] = l_g;
-            ms->ref[g][r] = m_g;
-        } else {
-            // The probabilities of these rows and their context factors, when they come back: tile t is ready for PV here.
-            const auto take = [&](int t) {
-                const float alpha = ms->alpha_in[t & 1][r];
-                if (__any_sync(FULL, alpha != 1.0f)) {
-                    wait(bar->p_free, t - 1, 120);
-                    __syncwarp();
-                    rescale_rows(lanes, alpha);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(tc::smem_u32(&bar->x_free[t % NB]), peer));
+            if (!__all_sync(FULL, (see_a & see_b) == ~0ull)) {
+                const uint64_t sa = see_a >> c0, sb = see_b >> c0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (!(sa >> (8 * j) & 1)) v[4 * j] = -INFINITY;
+                    if (!(sa >> (8 * j + 1) & 1)) v[4 * j + 1] = -INFINITY;
+                    if (!(sb >> (8 * j) & 1)) v[4 * j + 2] = -INFINITY;
+                    if (!(sb >> (8 * j + 1) & 1)) v[4 * j + 3] = -INFINITY;
                 }
-                ok = __all_sync(FULL, ok);
-                if (lane == 0) tc::mbar_arrive(&bar->p_full[t % NB]);
+            }
+            float ma = fmaxf(v[0], v[1]), mb = fmaxf(v[2], v[3]);
+#pragma unroll
+            for (int j = 1; j < 8; ++j) {
+                ma = tc::max3(ma, v[4 * j], v[4 * j + 1]);
+                mb = tc::max3(mb, v[4 * j + 2], v[4 * j + 3]);
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                ma = fmaxf(ma, __shfl_xor_sync(FULL, ma, o));
+                mb = fmaxf(mb, __shfl_xor_sync(FULL, mb, o));
+            }
+            ma *= sl2;
+            mb *= sl2;
+            // --- A row's reference (a whole number, in log2 units) moves up when a tile exceeds it by more than 8.  The one
+            // that tile t-1 used comes from another group; rather than wait for it the probabilities are taken against this
+            // group's last one, and corrected by a power of two in the rare case that it has moved. ---
+            const auto moved = [&](float m, float from) {
+                return m != -INFINITY && !(m <= from + RESCALE_LOG2) ? ceilf(m) : from;
             };
-            bool owed = false;  // the previous tile's probabilities have not been taken yet
-            for (int t = g; ok && t < n; t += G) {
-                uint8_t *Yb = Y + (t & 1) * X_BYTES;
-                if (lane == 0 && !(q & 1)) tc::mbar_arrive_expect_tx(&bar->p_in[t % NB], X_BYTES + HR * 4);
-                // Whichever is first: this tile's scores, or the previous one's probabilities.
-                if (owed) {
-                    const long long c0 = clock64();
-                    while (!__all_sync(FULL, tc::mbar_test(&bar->s_full[t % NB], (t / NB) & 1))) {
-                        if (__all_sync(FULL, tc::mbar_test(&bar->p_in[(t - G) % NB], ((t - G) / NB) & 1))) {
-                            take(t - G);
-                            owed = false;
-                            break;
-                        }
-                        // the wait below reports it
-                        if (__any_sync(FULL, *abort_flag || clock64() - c0 > P.wait_limit)) break;
+            float prev_a = ref_a, prev_b = ref_b;
+            const bool ahead = __all_sync(FULL, ref_a != -INFINITY && ref_b != -INFINITY);
+            const auto handed = [&]() {
+                wait(bar->hand[q], t - 1, 117);
+                prev_a = ms->m_pub[(t + G - 1) % G][ra];
+                prev_b = ms->m_pub[(t + G - 1) % G][ra + 8];
+            };
+            if (!ahead && t > 0) handed();
+            const float used_a = moved(ma, prev_a), used_b = moved(mb, prev_b);
+            // --- probabilities, rounded to bf16 for the PV product; the row sums take the rounded ones ---
+            const float neg_a = used_a == -INFINITY ? 0.0f : -used_a, neg_b = used_b == -INFINITY ? 0.0f : -used_b;
+            uint32_t pk[16];
+            float sa = 0.0f, sb = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(tc::ex2_approx(fmaf(v[4 * j], sl2, neg_a)),
+                                                               tc::ex2_approx(fmaf(v[4 * j + 1], sl2, neg_a)));
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(tc::ex2_approx(fmaf(v[4 * j + 2], sl2, neg_b)),
+                                                                tc::ex2_approx(fmaf(v[4 * j + 3], sl2, neg_b)));
+                pk[2 * j] = *(const uint32_t *)&a;
+                pk[2 * j + 1] = *(const uint32_t *)&b2;
+                sa = tc::add_bf16_f32((uint16_t)(pk[2 * j] & 0xffffu), sa);
+                sb = tc::add_bf16_f32((uint16_t)(pk[2 * j + 1] & 0xffffu), sb);
+                sa = tc::add_bf16_f32((uint16_t)(pk[2 * j] >> 16), sa);
+                sb = tc::add_bf16_f32((uint16_t)(pk[2 * j + 1] >> 16), sb);
+            }
+            float now_a = used_a, now_b = used_b;
+            if (ahead) {
+                handed();
+                now_a = moved(ma, prev_a);
+                now_b = moved(mb, prev_b);
+                if (__any_sync(FULL, now_a != used_a || now_b != used_b)) {
+                    const float fa = pow2(used_a - now_a), fb = pow2(used_b - now_b);
+                    const uint32_t fa2 = bf16_pair(fa), fb2 = bf16_pair(fb);
+                    sa *= fa;
+                    sb *= fb;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        pk[2 * j] = mul2(pk[2 * j], fa2);
+                        pk[2 * j + 1] = mul2(pk[2 * j + 1], fb2);
                     }
                 }
-                // the other CTA has read tile t - 2 from its buffer, and so from the one here
-                if (t >= 2) wait(bar->x_free, t - 2, 121);
-                wait(bar->s_full, t, 122);
-                __syncwarp();
-                float v[64];
-                load_scores(t, v);
-                uint32_t w[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) w[j] = tc::f16x2_satfinite(v[2 * j], v[2 * j + 1]);
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *(uint4 *)sw(Yb + r * 128, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-                tc::fence_proxy_async_smem();  // read by the copy (async proxy)
-                __syncwarp();
-                if (lane == 0)
-                    tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(X + (t & 1) * X_BYTES + (q & 1) * 32 * 128), peer),
-                                          Yb + (q & 1) * 32 * 128, 32 * 128,
-                                          tc::map_peer(tc::smem_u32(&bar->x_full[t % NB]), peer));
-                if (owed) {
-                    wait(bar->p_in, t - G, 123);
-                    take(t - G);
+            }
+            if (t + 1 < n) {
+                if (c0 == 0) {
+                    ms->m_pub[g][ra] = now_a;
+                    ms->m_pub[g][ra + 8] = now_b;
                 }
-                ok = __all_sync(FULL, ok);
-                owed = true;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar->hand[q][t % NB]);
             }
-            if (ok && owed) {
-                const int t = (n - 1 - g) / G * G + g;  // the group's last tile
-                wait(bar->p_in, t, 124);
-                take(t);
+            float alpha_a = 1.0f, alpha_b = 1.0f;  // what the context is multiplied by before PV(t)
+            if (__any_sync(FULL, now_a != prev_a || now_b != prev_b || now_a != ref_a || now_b != ref_b)) {
+                if (prev_a != -INFINITY) alpha_a = pow2(prev_a - now_a);
+                if (prev_b != -INFINITY) alpha_b = pow2(prev_b - now_b);
+                if (ref_a != -INFINITY) sum_a *= pow2(ref_a - now_a);
+                if (ref_b != -INFINITY) sum_b *= pow2(ref_b - now_b);
+                ref_a = now_a;
+                ref_b = now_b;
             }
+            sum_a += sa;
+            sum_b += sb;
+            // --- P(t), here and to the other CTA, into the buffer that both PV(t-2) are done with ---
+            if (t >= 2) wait(bar->p_free, t - 2, 118);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; j += 2)
+                stmatrix4(tc::smem_u32(Pt) + p_row * 128 + (((j + (lane >> 4)) ^ (lane & 7)) << 4), pk[2 * j], pk[2 * j + 1],
+                          pk[2 * j + 2], pk[2 * j + 3]);
+            if (c0 == 0) {
+                ms->alpha_out[buf][ra] = alpha_a;
+                ms->alpha_out[buf][ra + 8] = alpha_b;
+            }
+            tc::fence_proxy_async_smem();  // read by the PV product and by the copies (async proxy)
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t in = tc::map_peer(tc::smem_u32(&bar->p_in[t % NB]), peer);
+                uint8_t *rows16 = Pt + (q * 32 + rank * 16) * 128;
+                tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(rows16), peer), rows16, 2048, in);
+                tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(&ms->alpha_in[buf][q * 16]), peer), &ms->alpha_out[buf][q * 16],
+                                      64, in);
+            }
+            // --- the other CTA's rows have come back: the context moves after PV(t-1) and before PV(t) ---
+            wait(bar->p_in, t, 119);
+            __syncwarp();
+            const float alpha = ((uint32_t)lane >> 4) == rank ? ms->alpha_out[buf][q * 16 + (lane & 15)]
+                                                              : ms->alpha_in[buf][q * 16 + (lane & 15)];
+            if (__any_sync(FULL, alpha != 1.0f)) {
+                wait(bar->p_free, t - 1, 120);
+                __syncwarp();
+                rescale_rows(lanes, alpha);
+            }
+            ok = __all_sync(FULL, ok);
+            if (lane == 0) tc::mbar_arrive(&bar->p_full[t % NB]);
         }
-        // ---------------- row sums: the finishing warps' results, to both CTAs ----------------
+        // The PV products of the group's last tile are done in both CTAs: copies from here have been read, and the commits
+        // that arrive here have arrived.
+        if (ok && g < n) wait(bar->p_free, (n - 1 - g) / G * G + g, 121);
+        __syncwarp();
+        // ---------------- row sums, to both CTAs ----------------
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            sum_a += __shfl_xor_sync(FULL, sum_a, o);
+            sum_b += __shfl_xor_sync(FULL, sum_b, o);
+        }
+        if (c0 == 0) {
+            ms->sum[g][ra] = sum_a;
+            ms->sum[g][ra + 8] = sum_b;
+            ms->ref[g][ra] = ref_a;
+            ms->ref[g][ra + 8] = ref_b;
+        }
         bar_and<1, 32 * SOFT>(ok);
-        if (own && g == 0) {
+        if (g == 0 && lane < 16) {
+            const int r = q * 16 + lane, h = q * 32 + (int)rank * 16 + lane;
             float m = ms->ref[0][r], sum = 0.0f;
 #pragma unroll
             for (int i = 1; i < G; ++i) m = fmaxf(m, ms->ref[i][r]);
@@ -1057,7 +1102,7 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
     auto kern = kv8 ? tree_tc_kernel<true> : tree_tc_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3((unsigned)(2 * unit)), dim3(THREADS), SMEM, s, tq, tkv, tpe, run, (const void *)c->kv,
+    e = launch_pdl(kern, dim3((unsigned)(2 * unit)), dim3(kv8 ? Cfg<true>::THREADS : Cfg<false>::THREADS), SMEM, s, tq, tkv, tpe, run, (const void *)c->kv,
                    (const float *)c->kv_scale, (const __nv_bfloat16 *)c->k_pe, (const __nv_bfloat16 *)qpe, P,
                    (__nv_bfloat16 *)olat, lse, opart, lpart);
     if (e != cudaSuccess) return e;
