@@ -26,12 +26,11 @@
 //   * Lazy rescaling: a row's reference maximum moves only when a tile exceeds it by
 //     more than 2^8; the factor travels with the probabilities, and both CTAs rescale
 //     their half of the context.
-//   * bf16 caches arrive by TMA (two copies a tile where 64 tokens lie together); of e4m3
-//     caches four warps keep the next tile's codes in registers, dequantise (exact in
-//     bf16) and store them swizzled.
-//   * A token that some row does not see may hold anything, and 0 x NaN is NaN: tiles
-//     with hidden tokens are loaded through registers, where Inf and NaN become 0.
-//     Scores of hidden tokens are replaced after the MMA.
+//   * Tokens arrive by TMA (two copies a tile where 64 lie together); four more warps
+//     dequantise e4m3 codes (exact in bf16) from where they landed into the stages.
+//   * A token that some row does not see may hold anything, and 0 x NaN is NaN: in the V
+//     of tiles with hidden tokens Inf and NaN become 0.  Scores of hidden tokens are
+//     replaced after the MMA.
 // Bound by shared memory and by the length of a tile's chain (score, exchange, softmax,
 // exchange) over four stages of tokens: per tile a CTA's MMAs take 1088 cycles and its
 // shared-memory traffic (MMA operands 92 KB, copies 37, scores and probabilities 64) 1.5K.
@@ -55,11 +54,13 @@ constexpr int TK = 64;                  // tokens of a tile
 constexpr int SLAB = TK * 128;          // 64 tokens x 64 columns, 128-byte swizzle: 8 KB
 constexpr int ROPE = TK * 64;           // 64 tokens x 32 rotary columns, 64-byte swizzle: 4 KB
 constexpr int STAGE = 4 * SLAB + ROPE;  // a CTA's columns of a tile
-constexpr int NSTAGE = 4;               // e4m3 caches: four stages that serve K and V
 // bf16 caches: two stages of K, free after QK^T, and two of V (the latents again), loaded when PV comes near: no operand
 // waits in shared memory for a softmax.
 constexpr int VSTAGE = 4 * SLAB;
-static_assert(2 * STAGE + 2 * VSTAGE <= NSTAGE * STAGE, "stages");
+// e4m3 caches: three stages that serve K and V, and two of raw codes and rotary keys.
+constexpr int NSTAGE = 3;
+constexpr int RAW_LD = 256, RAW = TK * RAW_LD + ROPE;
+constexpr int KV_BYTES = std::max(2 * STAGE + 2 * VSTAGE, NSTAGE * STAGE + 2 * RAW);
 constexpr int P_BYTES = ROWS * TK * 2;  // probabilities of all rows
 constexpr int X_BYTES = HR * TK * 2;    // fp16 partial scores of half of the rows
 constexpr int Q_BOX = ROWS * 128;       // 128 rows x 64 columns of q~ (staged in the exchange buffers)
@@ -79,7 +80,7 @@ constexpr int SOFT = 4 * G;
 constexpr int FIRST_LOAD = 4 + SOFT;
 
 struct Bars {
-    uint64_t q_stage, q_ready, peer_ready, kv_full[NSTAGE], kv_empty[NSTAGE], raw[2], s_full[NB], s_empty[NB];
+    uint64_t q_stage, q_ready, peer_ready, kv_full[4], kv_empty[4], raw[2], raw_free[2], s_full[NB], s_empty[NB];
     uint64_t x_full[NB], x_free[NB];  // the other CTA's partial scores are here; it has read ours
     uint64_t p_in[NB], p_full[NB];    // the other CTA's probabilities are here; all are, and the context is ready for them
     uint64_t p_free[NB];              // the PV products of both CTAs are done
@@ -95,12 +96,12 @@ struct Misc {
     uint32_t tmem_slot;
     int abort_flag, never;
 };
-constexpr int SMEM = 1024 + NSTAGE * STAGE + 2 * P_BYTES + 4 * X_BYTES + QR_BYTES + (int)sizeof(Misc);
+constexpr int SMEM = 1024 + KV_BYTES + 2 * P_BYTES + 4 * X_BYTES + QR_BYTES + (int)sizeof(Misc);
 static_assert(SMEM <= 232448, "shared memory per CTA");
 static_assert(4 * Q_BOX <= 2 * P_BYTES + 4 * X_BYTES, "the q~ slice is staged in the exchange buffers");
 // The epilogue stages a CTA's 256 columns, rows 16 bytes apart from a power of two, in the token stages.
 constexpr int OUT_LD_F32 = 256 * 4 + 16, OUT_LD_BF16 = 256 * 2 + 16;
-static_assert(ROWS * OUT_LD_F32 <= NSTAGE * STAGE, "staged context");
+static_assert(ROWS * OUT_LD_F32 <= KV_BYTES, "staged context");
 
 // Sequences in the order of the units (the longest units first).
 struct TreeParams {
@@ -116,7 +117,6 @@ struct TreeParams {
     const uint64_t *mask;
     int words, H;
     int oob;                     // a cache row past the last one
-    int64_t ld_kv, ld_pe;
     float scale_log2;
     long long wait_limit;
 };
@@ -227,14 +227,14 @@ struct Cfg {
 template <bool KV8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
-                   const __grid_constant__ CUtensorMap tm_pe, int run, const void *__restrict__ kv,
-                   const float *__restrict__ kv_scale, const __nv_bfloat16 *__restrict__ kpe,
+                   const __grid_constant__ CUtensorMap tm_pe, int run,
+                   const float *__restrict__ kv_scale,
                    const __nv_bfloat16 *__restrict__ qpe, const __grid_constant__ TreeParams P,
                    __nv_bfloat16 *__restrict__ olat, float *__restrict__ lse, float *__restrict__ opart,
                    float *__restrict__ lpart) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *KV = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t *Pb = KV + NSTAGE * STAGE;   // [t % 2] probabilities: rows x 64 tokens, 128-byte swizzle
+    uint8_t *Pb = KV + KV_BYTES;   // [t % 2] probabilities: rows x 64 tokens, 128-byte swizzle
     uint8_t *X = Pb + 2 * P_BYTES;       // [t % 2] the other CTA's partial scores of this CTA's rows
     uint8_t *Y = X + 2 * X_BYTES;        // [t % 2] this CTA's partial scores of the other's rows, sent from here
     uint8_t *QR = Y + 2 * X_BYTES;       // rotary slice of the queries
@@ -273,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         tc::mbar_init(&bar->q_stage, 1);
         tc::mbar_init(&bar->q_ready, SOFT);
         tc::mbar_init(&bar->peer_ready, 1);
-        for (int i = 0; i < NSTAGE; ++i) {
+        for (int i = 0; i < 4; ++i) {
             tc::mbar_init(&bar->kv_full[i], KV8 ? 4 : 1);
             tc::mbar_init(&bar->kv_empty[i], 1);
         }
@@ -288,8 +288,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             for (int k = 0; k < 4; ++k) tc::mbar_init(&bar->hand[k][i], 1);
             tc::mbar_init(&bar->mask_full[i], 1);
         }
-        tc::mbar_init(&bar->raw[0], 1);
-        tc::mbar_init(&bar->raw[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bar->raw[i], 1);
+            tc::mbar_init(&bar->raw_free[i], 4);
+        }
         tc::mbar_init(&bar->qk_done, 1);
         tc::mbar_init(&bar->o_done, 1);
         *abort_flag = 0;
@@ -331,35 +333,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
     };
 
     if (warp == 0 && n > 0) {
-        // ---------------- TMA: the q~ slice (staged in the exchange buffers), then K of a bf16 cache ----------------
+        // ---------------- TMA: the q~ slice (staged in the exchange buffers), then K of a bf16 cache, or raw codes ----------------
         if (lane == 0) {
             tc::mbar_arrive_expect_tx(&bar->q_stage, 4 * Q_BOX);
             for (int j = 0; j < 4; ++j)
                 tc::tma_load_2d(Pb + j * Q_BOX, &tm_q, &bar->q_stage, rank * 256 + j * 64, (int)(seq_row0 + lrow));
         }
         __syncwarp();
-        if constexpr (!KV8) {
-            // Lane's copy: latents of run k (all four slabs at once where 64 tokens lie together), or rotary columns.
-            const int runs = TK / run, nlat = runs == 1 ? 1 : 4 * runs;
-            const bool lat = lane < nlat;
-            const int k = lat ? (runs == 1 ? 0 : lane >> 2) : lane - nlat, j = lat && runs > 1 ? lane & 3 : 0;
-            int rows = runs_of(0);
-            for (int t = 0; t < n; ++t) {
-                const int st = t & 1;
-                if (!__all_sync(FULL, tc::mbar_wait(&bar->kv_empty[st], ((t >> 1) & 1) ^ 1, abort_flag, err, 101, P.wait_limit))) break;
-                put_mask(t, rows);
-                // of runs behind the last token nothing is read
-                const int row = __shfl_sync(FULL, rows, (k * (run / 16)) & 3);
-                const bool go = (lat || k < runs) && row >= 0;
-                const int n_lat = __popc(__ballot_sync(FULL, go && lat)), n_pe = __popc(__ballot_sync(FULL, go && !lat));
-                if (lane == 0)
-                    tc::mbar_arrive_expect_tx(&bar->kv_full[st], (uint32_t)(run * (n_lat * (runs == 1 ? 512 : 128) + n_pe * 64)));
-                __syncwarp();
-                uint8_t *dst = KV + st * STAGE;
-                if (go && lat) tc::tma_load_3d(dst + j * SLAB + k * run * 128, &tm_kv, &bar->kv_full[st], 0, row, rank * 4 + j);
-                else if (go) tc::tma_load_2d(dst + 4 * SLAB + k * run * 64, &tm_pe, &bar->kv_full[st], rank * 32, row);
-                rows = runs_of(t + 1);
+        // Lane's copy: latents of run k (bf16: all four slabs at once where 64 tokens lie together), or rotary columns.
+        const int runs = TK / run, per_run = KV8 || runs == 1 ? 1 : 4, nlat = per_run * runs;
+        const bool lat = lane < nlat;
+        const int k = lat ? lane / per_run : lane - nlat, j = lat ? lane % per_run : 0;
+        int rows = runs_of(0);
+        for (int t = 0; t < n; ++t) {
+            const int st = t & 1;
+            if (!__all_sync(FULL, tc::mbar_wait(KV8 ? &bar->raw_free[st] : &bar->kv_empty[st], ((t >> 1) & 1) ^ 1, abort_flag,
+                                                err, 101, P.wait_limit)))
+                break;
+            put_mask(t, rows);
+            uint64_t *full = KV8 ? &bar->raw[st] : &bar->kv_full[st];
+            // of runs behind the last token nothing is read
+            const int row = __shfl_sync(FULL, rows, (k * (run / 16)) & 3);
+            const bool go = (lat || k < runs) && row >= 0;
+            const int n_lat = __popc(__ballot_sync(FULL, go && lat)), n_pe = __popc(__ballot_sync(FULL, go && !lat));
+            if (lane == 0)
+                tc::mbar_arrive_expect_tx(full, (uint32_t)(run * (n_lat * (KV8 ? RAW_LD : 512 / per_run) + n_pe * 64)));
+            __syncwarp();
+            uint8_t *dst = KV8 ? KV + NSTAGE * STAGE + st * RAW : KV + st * STAGE;
+            if (go && lat) {
+                if (KV8) tc::tma_load_2d(dst + k * run * RAW_LD, &tm_kv, full, rank * 256, row);
+                else tc::tma_load_3d(dst + j * SLAB + k * run * 128, &tm_kv, full, 0, row, rank * 4 + j);
+            } else if (go) {
+                tc::tma_load_2d(dst + (KV8 ? TK * RAW_LD : 4 * SLAB) + k * run * 64, &tm_pe, full, rank * 32, row);
             }
+            rows = runs_of(t + 1);
         }
     } else if (warp == 1 && n > 0) {
         // ---------------- QK^T issuer: tile t into score buffer t % 2 once its tokens are here ----------------
@@ -454,96 +461,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         }
     } else if (KV8 && warp >= FIRST_LOAD && n > 0) {
         // ---------------- loading warps (e4m3) ----------------
-        // Warp w brings 16 tokens, which lie together: one look at the block table a tile.
-        const int w = warp - FIRST_LOAD;
-        int64_t row = -1;   // of its first token
-        int count = 0;      // tokens that exist
-        const auto locate = [&](int t) {
+        // Warp w: 16 tokens of the tile, which lie together.  A pass takes four tokens' 128 codes of one block, eight lanes'
+        // 16 bytes each.  (The loop is kept rolled: unrolled, with the codes in registers, it and the softmax evict one
+        // another from the instruction cache, at 2.2 times the time a tile.)
+        const int w = warp - FIRST_LOAD, slab = (lane >> 2) & 1, chunk = (lane & 3) * 2;
+        float next = 0.0f;  // scale of token lane / 2, block lane % 2, of the next tile
+        const auto fetch = [&](int t) {
             const int s = (t0 + t) * TK + w * 16;
-            row = row_of(s);
-            count = row >= 0 ? min(16, tokens - s) : 0;
+            const int64_t row = t < n ? row_of(s) : -1;
+            next = row >= 0 && s + (lane >> 1) < tokens
+                       ? __ldg(kv_scale + (row + (lane >> 1)) * (DC / 128) + rank * 2 + (lane & 1)) : 0.0f;
         };
-        // Rotary columns: eight tokens x four 16-byte chunks an instruction.
-        uint4 rp[2];
-        const auto get_rope = [&]() {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int tok = e * 8 + (lane >> 2);
-                rp[e] = tok < count ? __ldg((const uint4 *)(kpe + (row + tok) * P.ld_pe + rank * 32) + (lane & 3))
-                                    : make_uint4(0, 0, 0, 0);
-            }
-        };
-        const auto put_rope = [&](uint8_t *stage) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int tok = w * 16 + e * 8 + (lane >> 2);
-                *(uint4 *)(stage + 4 * SLAB + tok * 64 + (((lane & 3) ^ ((tok >> 1) & 3)) << 4)) = rp[e];
-            }
-        };
-        bool ok = true;
-        {
-            // Pass i: tokens 4 (i / 2) .., block i % 2 of the CTA's two; a token's 128 codes are eight lanes' 16 bytes.
-            // The next tile's codes wait in registers.
-            const uint8_t *codes = (const uint8_t *)kv + rank * 256 + (lane & 7) * 16;
-            uint4 c[8];
-            float sc = 0.0f;   // scale of token lane / 2, block lane % 2
-            int runs = 0;
-            const auto fetch = [&](int t) {
-                locate(t);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int tok = (i >> 1) * 4 + (lane >> 3);
-                    c[i] = tok < count ? __ldg((const uint4 *)(codes + (row + tok) * P.ld_kv + (i & 1) * 128))
-                                       : make_uint4(0, 0, 0, 0);
-                }
-                sc = (lane >> 1) < count ? __ldg(kv_scale + (row + (lane >> 1)) * (DC / 128) + rank * 2 + (lane & 1)) : 0.0f;
-                get_rope();
-                if (w == 0) runs = runs_of(t);
-            };
-            const int slab = (lane >> 2) & 1, chunk = (lane & 3) * 2;
-            fetch(0);
-            for (int t = 0; t < n; ++t) {
-                const int st = t % NSTAGE;
-                ok = __all_sync(FULL, tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 109, P.wait_limit));
-                if (!ok) break;
-                if (w == 0) put_mask(t, runs);
-                uint8_t *stage = KV + st * STAGE;
-                // A hidden token's scale may be anything: past what a finite product allows it counts as 0 (the codes
-                // themselves become finite numbers, whatever they are).
-                if ((t0 + t + 1) * TK > safe && !(fabsf(sc) <= 0x1p118f)) sc = 0.0f;
-                // 2^120 scale is one factor while it stays in bf16's range
-                const bool big = __any_sync(FULL, sc > 128.0f);
-                const float up = big ? 0x1p120f : 0x1p120f * sc;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int tok = (i >> 1) * 4 + (lane >> 3);
-                    const float f = __shfl_sync(FULL, up, tok * 2 + (i & 1));
-                    uint4 o[2];
-                    dequant16(c[i], bf16_pair(f), o);
-                    uint8_t *dst = stage + ((i & 1) * 2 + slab) * SLAB + (w * 16 + tok) * 128;
-                    const int x = (w * 16 + tok) & 7;
-                    // the two slabs' lanes store their chunks in opposite order: eight lanes cover all banks
+        fetch(0);
+        for (int t = 0; t < n; ++t) {
+            const int st = t % NSTAGE;
+            float sc = next;
+            fetch(t + 1);
+            bool ok = tc::mbar_wait(&bar->raw[t & 1], (t >> 1) & 1, abort_flag, err, 109, P.wait_limit);
+            ok = tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 110, P.wait_limit) && ok;
+            if (!__all_sync(FULL, ok)) break;
+            uint8_t *stage = KV + st * STAGE;
+            const uint8_t *raw = KV + NSTAGE * STAGE + (t & 1) * RAW;
+            // A hidden token's scale may be anything: past what a finite product allows it counts as 0 (the codes
+            // themselves become finite numbers, whatever they are).
+            if ((t0 + t + 1) * TK > safe && !(fabsf(sc) <= 0x1p118f)) sc = 0.0f;
+            // 2^120 scale is one factor while it stays in bf16's range
+            const bool big = __any_sync(FULL, sc > 128.0f);
+            const float up = big ? 0x1p120f : 0x1p120f * sc;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const int tok = (i >> 1) * 4 + (lane >> 3), x = tok & 7;
+                const uint4 c = *(const uint4 *)(raw + (w * 16 + tok) * RAW_LD + (i & 1) * 128 + (lane & 7) * 16);
+                const float f = __shfl_sync(FULL, up, tok * 2 + (i & 1));
+                uint4 o[2];
+                dequant16(c, bf16_pair(f), o);
+                if (big) {
+                    const uint32_t f2 = bf16_pair(__shfl_sync(FULL, sc, tok * 2 + (i & 1)));
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        *(uint4 *)(dst + (((chunk + (e ^ slab)) ^ x) << 4)) = (e ^ slab) ? o[1] : o[0];
+                        o[e] = make_uint4(mul2(o[e].x, f2), mul2(o[e].y, f2), mul2(o[e].z, f2), mul2(o[e].w, f2));
                 }
-                if (big) {  // the second factor, over the stored values
-#pragma unroll 1
-                    for (int i = 0; i < 16; ++i) {
-                        const int tok = i, lane_slab = lane >> 3;
-                        const float f = __shfl_sync(FULL, sc, tok * 2 + (lane_slab >> 1));
-                        uint4 *p = (uint4 *)(stage + lane_slab * SLAB + (w * 16 + tok) * 128 + (lane & 7) * 16);
-                        __syncwarp();
-                        uint4 v = *p;
-                        const uint32_t m = bf16_pair(f);
-                        *p = make_uint4(mul2(v.x, m), mul2(v.y, m), mul2(v.z, m), mul2(v.w, m));
-                    }
-                }
-                put_rope(stage);
-                tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar->kv_full[st]);
-                if (t + 1 < n) fetch(t + 1);
+                uint8_t *dst = stage + ((i & 1) * 2 + slab) * SLAB + (w * 16 + tok) * 128;
+                // the two slabs' lanes store their chunks in opposite order: eight lanes cover all banks
+                *(uint4 *)(dst + (((chunk + slab) ^ x) << 4)) = slab ? o[1] : o[0];
+                *(uint4 *)(dst + (((chunk + 1 - slab) ^ x) << 4)) = slab ? o[0] : o[1];
+            }
+            // the rotary columns as they are (both sides in the same 64-byte swizzle)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int at = w * 1024 + e * 512 + lane * 16;
+                *(uint4 *)(stage + 4 * SLAB + at) = *(const uint4 *)(raw + TK * RAW_LD + at);
+            }
+            tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
+            __syncwarp();
+            if (lane == 0) {
+                tc::mbar_arrive(&bar->kv_full[st]);
+                tc::mbar_arrive(&bar->raw_free[t & 1]);
             }
         }
     } else if (warp >= 4 && warp < FIRST_LOAD) {
@@ -1072,8 +1045,6 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
     P.mask = mask;
     P.words = words;
     P.H = H;
-    P.ld_kv = c->ld_kv;
-    P.ld_pe = c->ld_pe;
     P.scale_log2 = scale == 0.0f ? 1e-30f : scale * 1.4426950408889634f;  // 0: so small that every score counts alike
     P.wait_limit = wait_limit_cycles();
     const uint64_t rows = (uint64_t)std::max<int64_t>(c->rows, 1);
@@ -1087,23 +1058,29 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
         const uint32_t box[2] = {64, ROWS};
         if (!make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, qt, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    tkv = tpe = tq;  // e4m3: not used
-    if (!kv8) {
-        // latents as slabs of 64 columns (column, row, slab); rotary keys in halves of 32 columns
+    {
+        const uint64_t pdims[2] = {DR, rows}, pstrides[1] = {(uint64_t)c->ld_pe * 2};
+        const uint32_t pbox[2] = {32, (uint32_t)run};  // half of the rotary columns
+        if (!make_tmap(&tpe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c->k_pe, pdims, pstrides, pbox, CU_TENSOR_MAP_SWIZZLE_64B))
+            return cudaErrorInvalidValue;
+    }
+    if (kv8) {
+        const uint64_t dims[2] = {DC, rows}, strides[1] = {(uint64_t)c->ld_kv};
+        const uint32_t box[2] = {RAW_LD, (uint32_t)run};
+        if (!make_tmap(&tkv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c->kv, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
+    } else {
+        // latents as slabs of 64 columns: (column, row, slab)
         const uint64_t dims[3] = {64, rows, DC / 64}, strides[2] = {(uint64_t)c->ld_kv * 2, 128};
         const uint32_t box[3] = {64, (uint32_t)run, run == TK ? 4u : 1u};
-        const uint64_t pdims[2] = {DR, rows}, pstrides[1] = {(uint64_t)c->ld_pe * 2};
-        const uint32_t pbox[2] = {32, (uint32_t)run};
-        if (!make_tmap(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c->kv, dims, strides, box) ||
-            !make_tmap(&tpe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c->k_pe, pdims, pstrides, pbox, CU_TENSOR_MAP_SWIZZLE_64B))
-            return cudaErrorInvalidValue;
+        if (!make_tmap(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c->kv, dims, strides, box)) return cudaErrorInvalidValue;
     }
     float *opart = (float *)part_ws, *lpart = (float *)((char *)part_ws + part_bytes(plan));
     auto kern = kv8 ? tree_tc_kernel<true> : tree_tc_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3((unsigned)(2 * unit)), dim3(kv8 ? Cfg<true>::THREADS : Cfg<false>::THREADS), SMEM, s, tq, tkv, tpe, run, (const void *)c->kv,
-                   (const float *)c->kv_scale, (const __nv_bfloat16 *)c->k_pe, (const __nv_bfloat16 *)qpe, P,
+    e = launch_pdl(kern, dim3((unsigned)(2 * unit)), dim3(kv8 ? Cfg<true>::THREADS : Cfg<false>::THREADS), SMEM, s, tq, tkv, tpe, run,
+                   (const float *)c->kv_scale, (const __nv_bfloat16 *)qpe, P,
                    (__nv_bfloat16 *)olat, lse, opart, lpart);
     if (e != cudaSuccess) return e;
     note_launch(DSA_KERNEL_TREE_TC);
