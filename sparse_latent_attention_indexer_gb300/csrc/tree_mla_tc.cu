@@ -38,6 +38,7 @@
 // Waits are bounded; a timeout records its site in the device error word and
 // both CTAs drain and exit.
 #include <algorithm>
+#include <type_traits>
 
 #include "tc_common.cuh"
 
@@ -462,15 +463,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
     } else if (KV8 && warp >= FIRST_LOAD && n > 0) {
         // ---------------- loading warps (e4m3) ----------------
         // Warp w: 16 tokens of the tile, which lie together.  A pass takes four tokens' 128 codes of one block, eight lanes'
-        // 16 bytes each.  (The loop is kept rolled: unrolled, with the codes in registers, it and the softmax evict one
-        // another from the instruction cache, at 2.2 times the time a tile.)
+        // 16 bytes each.  (Eight unrolled passes with the codes in registers, loaded a tile ahead, were slower: that loop and
+        // the softmax evict one another from the instruction cache.)
         const int w = warp - FIRST_LOAD, slab = (lane >> 2) & 1, chunk = (lane & 3) * 2;
         float next = 0.0f;  // scale of token lane / 2, block lane % 2, of the next tile
+        int64_t row = row_of(t0 * TK + w * 16);  // of the warp's first token of that tile
         const auto fetch = [&](int t) {
             const int s = (t0 + t) * TK + w * 16;
-            const int64_t row = t < n ? row_of(s) : -1;
-            next = row >= 0 && s + (lane >> 1) < tokens
+            next = t < n && row >= 0 && s + (lane >> 1) < tokens
                        ? __ldg(kv_scale + (row + (lane >> 1)) * (DC / 128) + rank * 2 + (lane & 1)) : 0.0f;
+            row = row_of(s + TK);  // looked up a tile before it is needed
         };
         fetch(0);
         for (int t = 0; t < n; ++t) {
@@ -485,26 +487,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             // A hidden token's scale may be anything: past what a finite product allows it counts as 0 (the codes
             // themselves become finite numbers, whatever they are).
             if ((t0 + t + 1) * TK > safe && !(fabsf(sc) <= 0x1p118f)) sc = 0.0f;
-            // 2^120 scale is one factor while it stays in bf16's range
-            const bool big = __any_sync(FULL, sc > 128.0f);
-            const float up = big ? 0x1p120f : 0x1p120f * sc;
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
+            // 2^120 scale is one factor while it stays in bf16's range; scales above 128 go in two.
+            const auto load = [&](int i) {
+                return *(const uint4 *)(raw + (w * 16 + (i >> 1) * 4 + (lane >> 3)) * RAW_LD + (i & 1) * 128 + (lane & 7) * 16);
+            };
+            const auto pass = [&](int i, const uint4 &c, float up, auto more) {
                 const int tok = (i >> 1) * 4 + (lane >> 3), x = tok & 7;
-                const uint4 c = *(const uint4 *)(raw + (w * 16 + tok) * RAW_LD + (i & 1) * 128 + (lane & 7) * 16);
-                const float f = __shfl_sync(FULL, up, tok * 2 + (i & 1));
                 uint4 o[2];
-                dequant16(c, bf16_pair(f), o);
-                if (big) {
-                    const uint32_t f2 = bf16_pair(__shfl_sync(FULL, sc, tok * 2 + (i & 1)));
+                dequant16(c, bf16_pair(__shfl_sync(FULL, up, tok * 2 + (i & 1))), o);
+                if constexpr (decltype(more)::value) {
+                    const uint32_t f = bf16_pair(__shfl_sync(FULL, sc, tok * 2 + (i & 1)));
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        o[e] = make_uint4(mul2(o[e].x, f2), mul2(o[e].y, f2), mul2(o[e].z, f2), mul2(o[e].w, f2));
+                        o[e] = make_uint4(mul2(o[e].x, f), mul2(o[e].y, f), mul2(o[e].z, f), mul2(o[e].w, f));
                 }
                 uint8_t *dst = stage + ((i & 1) * 2 + slab) * SLAB + (w * 16 + tok) * 128;
                 // the two slabs' lanes store their chunks in opposite order: eight lanes cover all banks
                 *(uint4 *)(dst + (((chunk + slab) ^ x) << 4)) = slab ? o[1] : o[0];
                 *(uint4 *)(dst + (((chunk + 1 - slab) ^ x) << 4)) = slab ? o[0] : o[1];
+            };
+            if (!__any_sync(FULL, sc > 128.0f)) {
+#pragma unroll 1
+                for (int i0 = 0; i0 < 8; i0 += 4) {  // the loads first: they could not pass the stores
+                    uint4 c[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c[i] = load(i0 + i);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) pass(i0 + i, c[i], 0x1p120f * sc, std::false_type());
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) pass(i, load(i), 0x1p120f, std::true_type());
             }
             // the rotary columns as they are (both sides in the same 64-byte swizzle)
 #pragma unroll
