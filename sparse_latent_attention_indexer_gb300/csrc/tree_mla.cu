@@ -230,7 +230,8 @@ int dsa_tree_mla_fwd(const void *q_nope, const void *q_pe, int dtype, const dsa_
     if ((int64_t)bt.total_q * H >= (int64_t(1) << 31) - 256) return DSA_ERR_UNSUPPORTED;
     if (bt.total_q == 0) return DSA_OK;
     if (!q_nope || (d_r > 0 && !q_pe) || !W_UK || !W_UV || !out) return DSA_ERR_INVALID_ARG;
-    if (!on16(q_nope) || !on16(q_pe) || !on16(W_UK) || !on16(W_UV) || !on16(out) || (uintptr_t)lse % 4)
+    if (!on16(q_nope) || !on16(q_pe) || !on16(W_UK) || !on16(W_UV) || !on16(out) || (uintptr_t)lse % 4 ||
+        !on16(cache->kv_scale))
         return DSA_ERR_INVALID_ARG;
     if (tree_mask) {
         if (mask_words < 1 || (uintptr_t)tree_mask % 8) return DSA_ERR_INVALID_ARG;

@@ -26,7 +26,7 @@
 //   * Lazy rescaling: a row's reference maximum moves only when a tile exceeds it by
 //     more than 2^8; the factor travels with the probabilities, and both CTAs rescale
 //     their half of the context.
-//   * Tokens arrive by TMA (two copies a tile where 64 lie together); four more warps
+//   * Tokens arrive by TMA (two copies a tile where 64 lie together); eight more warps
 //     dequantise e4m3 codes (exact in bf16) from where they landed into the stages.
 //   * A token that some row does not see may hold anything, and 0 x NaN is NaN: in the V
 //     of tiles with hidden tokens Inf and NaN become 0.  Scores of hidden tokens are
@@ -58,9 +58,9 @@ constexpr int STAGE = 4 * SLAB + ROPE;  // a CTA's columns of a tile
 // bf16 caches: two stages of K, free after QK^T, and two of V (the latents again), loaded when PV comes near: no operand
 // waits in shared memory for a softmax.
 constexpr int VSTAGE = 4 * SLAB;
-// e4m3 caches: three stages that serve K and V, and two of raw codes and rotary keys.
+// e4m3 caches: three stages that serve K and V, and two of raw codes, rotary keys and scales.
 constexpr int NSTAGE = 3;
-constexpr int RAW_LD = 256, RAW = TK * RAW_LD + ROPE;
+constexpr int RAW_LD = 256, RAW_SCALE = TK * RAW_LD + ROPE, RAW = RAW_SCALE + TK * 16;
 constexpr int KV_BYTES = std::max(2 * STAGE + 2 * VSTAGE, NSTAGE * STAGE + 2 * RAW);
 constexpr int P_BYTES = ROWS * TK * 2;  // probabilities of all rows
 constexpr int X_BYTES = HR * TK * 2;    // fp16 partial scores of half of the rows
@@ -75,10 +75,11 @@ constexpr float LN2 = 0.69314718055994530942f;
 constexpr long long kAbortQuietCycles = 1LL << 18;
 constexpr int PAIRS = 76;               // 152 SMs
 // warp 0: TMA (Q, bf16 K); 1: QK^T; 2: tensor memory, PV; 3: TMA (bf16 V); from 4 on the softmax groups of four
-// (warp % 4 = lane quarter); of an e4m3 cache four more load
+// (warp % 4 = lane quarter); of an e4m3 cache eight more load
 constexpr int G = 3;                    // softmax groups
 constexpr int SOFT = 4 * G;
 constexpr int FIRST_LOAD = 4 + SOFT;
+constexpr int LOADERS = 8;
 
 struct Bars {
     uint64_t q_stage, q_ready, peer_ready, kv_full[4], kv_empty[4], raw[2], raw_free[2], s_full[NB], s_empty[NB];
@@ -90,12 +91,14 @@ struct Bars {
 struct Misc {
     float m_pub[G][HR];           // reference maximum that a group used, for the next tile's group
     float alpha_out[2][HR], alpha_in[2][HR];  // context factors of a tile, of this CTA's rows and of the other's
-    float sum[G][HR], ref[G][HR];     // a group's share of the row sum and its reference
     float inv[ROWS];                  // 1 / row sum
     uint64_t live[NB];                // tokens of a tile whose page exists
     Bars bar;
     uint32_t tmem_slot;
     int abort_flag, never;
+};
+struct RowSums {                      // in the exchange buffers, at the end
+    float sum[G][HR], ref[G][HR];     // a group's share of the row sum and its reference
 };
 constexpr int SMEM = 1024 + KV_BYTES + 2 * P_BYTES + 4 * X_BYTES + QR_BYTES + (int)sizeof(Misc);
 static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -121,7 +124,7 @@ struct TreeParams {
     float scale_log2;
     long long wait_limit;
 };
-static_assert(sizeof(TreeParams) + 3 * 128 + 128 <= 32764, "launch parameters");
+static_assert(sizeof(TreeParams) + 4 * 128 + 128 <= 32764, "launch parameters");
 
 // One 16-bit pair per word: bf16 Inf and NaN become 0.
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
@@ -130,12 +133,13 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
     return w;
 }
 
-// Four e4m3 codes -> four bf16 values times 2^120 (exact: the code's exponent and mantissa move to bf16's
-// field, whose bias is 120 larger; subnormal codes become bf16 subnormals).
+// Four e4m3 codes -> four bf16 values times 2^-120 (exact: sign, exponent and mantissa move to bf16's fields, whose
+// exponent bias is 120 larger; subnormal codes become bf16 subnormals).  A code's low nibble is the upper half of the
+// value's low byte, its sign and the three bits behind make the high byte.
 __device__ __forceinline__ void spread4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
-    const uint32_t a = __byte_perm(codes, 0, 0x1404), b = __byte_perm(codes, 0, 0x3424);  // codes in the high bytes
-    lo = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
-    hi = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
+    const uint32_t low = (codes << 4) & 0xf0f0f0f0u, high = ((codes >> 4) & 0x07070707u) | (codes & 0x80808080u);
+    lo = __byte_perm(low, high, 0x5140);
+    hi = __byte_perm(low, high, 0x7362);
 }
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     const __nv_bfloat162 r = __hmul2(*(const __nv_bfloat162 *)&a, *(const __nv_bfloat162 *)&b);
@@ -222,14 +226,13 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b,
 
 template <bool KV8>
 struct Cfg {
-    static constexpr int THREADS = 32 * (FIRST_LOAD + (KV8 ? 4 : 0));
+    static constexpr int THREADS = 32 * (FIRST_LOAD + (KV8 ? LOADERS : 0));
 };
 
 template <bool KV8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
-                   const __grid_constant__ CUtensorMap tm_pe, int run,
-                   const float *__restrict__ kv_scale,
+                   const __grid_constant__ CUtensorMap tm_pe, const __grid_constant__ CUtensorMap tm_sc, int run,
                    const __nv_bfloat16 *__restrict__ qpe, const __grid_constant__ TreeParams P,
                    __nv_bfloat16 *__restrict__ olat, float *__restrict__ lse, float *__restrict__ opart,
                    float *__restrict__ lpart) {
@@ -275,7 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         tc::mbar_init(&bar->q_ready, SOFT);
         tc::mbar_init(&bar->peer_ready, 1);
         for (int i = 0; i < 4; ++i) {
-            tc::mbar_init(&bar->kv_full[i], KV8 ? 4 : 1);
+            tc::mbar_init(&bar->kv_full[i], KV8 ? LOADERS : 1);
             tc::mbar_init(&bar->kv_empty[i], 1);
         }
         for (int i = 0; i < NB; ++i) {
@@ -291,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bar->raw[i], 1);
-            tc::mbar_init(&bar->raw_free[i], 4);
+            tc::mbar_init(&bar->raw_free[i], LOADERS);
         }
         tc::mbar_init(&bar->qk_done, 1);
         tc::mbar_init(&bar->o_done, 1);
@@ -358,12 +361,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             const bool go = (lat || k < runs) && row >= 0;
             const int n_lat = __popc(__ballot_sync(FULL, go && lat)), n_pe = __popc(__ballot_sync(FULL, go && !lat));
             if (lane == 0)
-                tc::mbar_arrive_expect_tx(full, (uint32_t)(run * (n_lat * (KV8 ? RAW_LD : 512 / per_run) + n_pe * 64)));
+                tc::mbar_arrive_expect_tx(full, (uint32_t)(run * (n_lat * (KV8 ? RAW_LD + 16 : 512 / per_run) + n_pe * 64)));
             __syncwarp();
             uint8_t *dst = KV8 ? KV + NSTAGE * STAGE + st * RAW : KV + st * STAGE;
             if (go && lat) {
-                if (KV8) tc::tma_load_2d(dst + k * run * RAW_LD, &tm_kv, full, rank * 256, row);
-                else tc::tma_load_3d(dst + j * SLAB + k * run * 128, &tm_kv, full, 0, row, rank * 4 + j);
+                if (KV8) {
+                    tc::tma_load_2d(dst + k * run * RAW_LD, &tm_kv, full, rank * 256, row);
+                    tc::tma_load_2d(dst + RAW_SCALE + k * run * 16, &tm_sc, full, 0, row);
+                } else tc::tma_load_3d(dst + j * SLAB + k * run * 128, &tm_kv, full, 0, row, rank * 4 + j);
             } else if (go) {
                 tc::tma_load_2d(dst + (KV8 ? TK * RAW_LD : 4 * SLAB) + k * run * 64, &tm_pe, full, rank * 32, row);
             }
@@ -462,37 +467,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         }
     } else if (KV8 && warp >= FIRST_LOAD && n > 0) {
         // ---------------- loading warps (e4m3) ----------------
-        // Warp w: 16 tokens of the tile, which lie together.  A pass takes four tokens' 128 codes of one block, eight lanes'
-        // 16 bytes each.  (Eight unrolled passes with the codes in registers, loaded a tile ahead, were slower: that loop and
-        // the softmax evict one another from the instruction cache.)
-        const int w = warp - FIRST_LOAD, slab = (lane >> 2) & 1, chunk = (lane & 3) * 2;
-        float next = 0.0f;  // scale of token lane / 2, block lane % 2, of the next tile
-        int64_t row = row_of(t0 * TK + w * 16);  // of the warp's first token of that tile
-        const auto fetch = [&](int t) {
-            const int s = (t0 + t) * TK + w * 16;
-            next = t < n && row >= 0 && s + (lane >> 1) < tokens
-                       ? __ldg(kv_scale + (row + (lane >> 1)) * (DC / 128) + rank * 2 + (lane & 1)) : 0.0f;
-            row = row_of(s + TK);  // looked up a tile before it is needed
-        };
-        fetch(0);
+        // Warp w: eight tokens of the tile.  A pass takes four tokens' 128 codes of one block: 16 codes a lane, eight lanes two
+        // tokens' 64 columns of one slab, which are eight different chunks of the swizzled rows.  (Eight unrolled passes with
+        // the codes in registers, loaded a tile ahead, were slower: that loop and the softmax evict one another from the
+        // instruction cache.)
+        const int w = warp - FIRST_LOAD, slab = lane >> 4, chunk = (lane & 3) * 2, sub = (lane >> 2) & 3;
         for (int t = 0; t < n; ++t) {
             const int st = t % NSTAGE;
-            float sc = next;
-            fetch(t + 1);
             bool ok = tc::mbar_wait(&bar->raw[t & 1], (t >> 1) & 1, abort_flag, err, 109, P.wait_limit);
             ok = tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 110, P.wait_limit) && ok;
             if (!__all_sync(FULL, ok)) break;
             uint8_t *stage = KV + st * STAGE;
             const uint8_t *raw = KV + NSTAGE * STAGE + (t & 1) * RAW;
+            // scale of token lane / 2 % 8, block lane % 2
+            float sc = *(const float *)(raw + RAW_SCALE + (w * 8 + (lane >> 1 & 7)) * 16 + (rank * 2 + (lane & 1)) * 4);
             // A hidden token's scale may be anything: past what a finite product allows it counts as 0 (the codes
             // themselves become finite numbers, whatever they are).
             if ((t0 + t + 1) * TK > safe && !(fabsf(sc) <= 0x1p118f)) sc = 0.0f;
             // 2^120 scale is one factor while it stays in bf16's range; scales above 128 go in two.
-            const auto load = [&](int i) {
-                return *(const uint4 *)(raw + (w * 16 + (i >> 1) * 4 + (lane >> 3)) * RAW_LD + (i & 1) * 128 + (lane & 7) * 16);
-            };
+            const uint8_t *from = raw + (w * 8 + sub) * RAW_LD + slab * 64 + (lane & 3) * 16;
+            uint8_t *to = stage + slab * SLAB + (w * 8 + sub) * 128;
+            const auto load = [&](int i) { return *(const uint4 *)(from + (i >> 1) * 4 * RAW_LD + (i & 1) * 128); };
             const auto pass = [&](int i, const uint4 &c, float up, auto more) {
-                const int tok = (i >> 1) * 4 + (lane >> 3), x = tok & 7;
+                const int tok = (i >> 1) * 4 + sub, x = tok & 7;
                 uint4 o[2];
                 dequant16(c, bf16_pair(__shfl_sync(FULL, up, tok * 2 + (i & 1))), o);
                 if constexpr (decltype(more)::value) {
@@ -501,30 +498,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                     for (int e = 0; e < 2; ++e)
                         o[e] = make_uint4(mul2(o[e].x, f), mul2(o[e].y, f), mul2(o[e].z, f), mul2(o[e].w, f));
                 }
-                uint8_t *dst = stage + ((i & 1) * 2 + slab) * SLAB + (w * 16 + tok) * 128;
-                // the two slabs' lanes store their chunks in opposite order: eight lanes cover all banks
-                *(uint4 *)(dst + (((chunk + slab) ^ x) << 4)) = slab ? o[1] : o[0];
-                *(uint4 *)(dst + (((chunk + 1 - slab) ^ x) << 4)) = slab ? o[0] : o[1];
+                uint8_t *dst = to + (i & 1) * 2 * SLAB + (i >> 1) * 512;
+                *(uint4 *)(dst + ((chunk ^ x) << 4)) = o[0];
+                *(uint4 *)(dst + (((chunk + 1) ^ x) << 4)) = o[1];
             };
             if (!__any_sync(FULL, sc > 128.0f)) {
-#pragma unroll 1
-                for (int i0 = 0; i0 < 8; i0 += 4) {  // the loads first: they could not pass the stores
-                    uint4 c[4];
+                uint4 c[4];  // the loads first: they could not pass the stores
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) c[i] = load(i0 + i);
+                for (int i = 0; i < 4; ++i) c[i] = load(i);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) pass(i0 + i, c[i], 0x1p120f * sc, std::false_type());
-                }
+                for (int i = 0; i < 4; ++i) pass(i, c[i], 0x1p120f * sc, std::false_type());
             } else {
 #pragma unroll 1
-                for (int i = 0; i < 8; ++i) pass(i, load(i), 0x1p120f, std::true_type());
+                for (int i = 0; i < 4; ++i) pass(i, load(i), 0x1p120f, std::true_type());
             }
             // the rotary columns as they are (both sides in the same 64-byte swizzle)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int at = w * 1024 + e * 512 + lane * 16;
-                *(uint4 *)(stage + 4 * SLAB + at) = *(const uint4 *)(raw + TK * RAW_LD + at);
-            }
+            const int at = w * 512 + lane * 16;
+            *(uint4 *)(stage + 4 * SLAB + at) = *(const uint4 *)(raw + TK * RAW_LD + at);
             tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
             __syncwarp();
             if (lane == 0) {
@@ -806,21 +796,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             sum_a += __shfl_xor_sync(FULL, sum_a, o);
             sum_b += __shfl_xor_sync(FULL, sum_b, o);
         }
+        bar_and<1, 32 * SOFT>(ok);
+        RowSums *rs = (RowSums *)X;
         if (c0 == 0) {
-            ms->sum[g][ra] = sum_a;
-            ms->sum[g][ra + 8] = sum_b;
-            ms->ref[g][ra] = ref_a;
-            ms->ref[g][ra + 8] = ref_b;
+            rs->sum[g][ra] = sum_a;
+            rs->sum[g][ra + 8] = sum_b;
+            rs->ref[g][ra] = ref_a;
+            rs->ref[g][ra + 8] = ref_b;
         }
         bar_and<1, 32 * SOFT>(ok);
         if (g == 0 && lane < 16) {
             const int r = q * 16 + lane, h = q * 32 + (int)rank * 16 + lane;
-            float m = ms->ref[0][r], sum = 0.0f;
+            float m = rs->ref[0][r], sum = 0.0f;
 #pragma unroll
-            for (int i = 1; i < G; ++i) m = fmaxf(m, ms->ref[i][r]);
+            for (int i = 1; i < G; ++i) m = fmaxf(m, rs->ref[i][r]);
 #pragma unroll
             for (int i = 0; i < G; ++i)
-                if (ms->ref[i][r] != -INFINITY) sum += ms->sum[i][r] * pow2(ms->ref[i][r] - m);
+                if (rs->ref[i][r] != -INFINITY) sum += rs->sum[i][r] * pow2(rs->ref[i][r] - m);
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
             ms->inv[h] = inv;
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::map_peer(tc::smem_u32(&ms->inv[h]), peer)), "f"(inv)
@@ -1065,7 +1057,7 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
     const bool kv8 = c->dtype == DSA_E4M3;
     // Tokens that lie together: a whole tile (contiguous caches, pages of 64), or less.
     const int run = !pt.table || pt.page % TK == 0 ? TK : pt.page % 32 == 0 ? 32 : 16;
-    CUtensorMap tq, tkv, tpe;
+    CUtensorMap tq, tkv, tpe, tsc;
     {
         const uint64_t dims[2] = {DC, (uint64_t)N * H}, strides[1] = {DC * 2};
         const uint32_t box[2] = {64, ROWS};
@@ -1080,20 +1072,25 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
     if (kv8) {
         const uint64_t dims[2] = {DC, rows}, strides[1] = {(uint64_t)c->ld_kv};
         const uint32_t box[2] = {RAW_LD, (uint32_t)run};
-        if (!make_tmap(&tkv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c->kv, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+        const uint64_t sdims[2] = {DC / 128, rows}, sstrides[1] = {DC / 128 * 4};
+        const uint32_t sbox[2] = {DC / 128, (uint32_t)run};
+        if (!make_tmap(&tkv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c->kv, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+            !make_tmap(&tsc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, c->kv_scale, sdims, sstrides, sbox,
+                       CU_TENSOR_MAP_SWIZZLE_NONE))
             return cudaErrorInvalidValue;
     } else {
         // latents as slabs of 64 columns: (column, row, slab)
         const uint64_t dims[3] = {64, rows, DC / 64}, strides[2] = {(uint64_t)c->ld_kv * 2, 128};
         const uint32_t box[3] = {64, (uint32_t)run, run == TK ? 4u : 1u};
         if (!make_tmap(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c->kv, dims, strides, box)) return cudaErrorInvalidValue;
+        tsc = tkv;  // not used
     }
     float *opart = (float *)part_ws, *lpart = (float *)((char *)part_ws + part_bytes(plan));
     auto kern = kv8 ? tree_tc_kernel<true> : tree_tc_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3((unsigned)(2 * unit)), dim3(kv8 ? Cfg<true>::THREADS : Cfg<false>::THREADS), SMEM, s, tq, tkv, tpe, run,
-                   (const float *)c->kv_scale, (const __nv_bfloat16 *)qpe, P,
+    e = launch_pdl(kern, dim3((unsigned)(2 * unit)), dim3(kv8 ? Cfg<true>::THREADS : Cfg<false>::THREADS), SMEM, s, tq, tkv, tpe, tsc, run,
+                   (const __nv_bfloat16 *)qpe, P,
                    (__nv_bfloat16 *)olat, lse, opart, lpart);
     if (e != cudaSuccess) return e;
     note_launch(DSA_KERNEL_TREE_TC);
