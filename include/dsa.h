@@ -435,7 +435,8 @@ int dsa_forward_host(const dsa_problem *p, const dsa_seqs *seqs, const dsa_host_
  * attention masks its tokens. */
 typedef struct dsa_pages {
     const int32_t *block_table;   /* device [B, ld_table] */
-    int64_t ld_table;             /* entries per sequence */
+    int64_t ld_table;             /* row stride in entries, >= width */
+    int64_t width;                /* entries of a sequence */
     int32_t page_size;            /* rows of a page: a multiple of 16 */
     int32_t n_pages;              /* pages of the cache: n_pages * page_size <= rows */
 } dsa_pages;

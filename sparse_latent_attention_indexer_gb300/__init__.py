@@ -9,6 +9,7 @@ missing ``libdsa.so`` raises.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 
@@ -47,20 +48,31 @@ def _check(fn: str, status: int):
         raise DSAError(fn, status)
 
 
+def _int32s(values):
+    """A C array of the values (through ``array``, which takes a list ten times as fast as ctypes does)."""
+    try:
+        a = array.array("i", values)
+    except TypeError:  # tensors of one value and other things that only int() takes
+        a = array.array("i", [int(x) for x in values])
+    return (ctypes.c_int32 * len(a)).from_buffer(a) if a else (ctypes.c_int32 * 1)()
+
+
 class Seqs:
     """A batch description (host arrays): cu_q [B+1], cu_k [B+1], start_pos [B]."""
 
     def __init__(self, cu_q, cu_k, start_pos):
         B = len(start_pos)
         assert len(cu_q) == B + 1 and len(cu_k) == B + 1
-        self._q = (ctypes.c_int32 * (B + 1))(*[int(x) for x in cu_q])
-        self._k = (ctypes.c_int32 * (B + 1))(*[int(x) for x in cu_k])
-        self._p = (ctypes.c_int32 * max(B, 1))(*[int(x) for x in start_pos])
+        self._q, self._k, self._p = _int32s(cu_q), _int32s(cu_k), _int32s(start_pos)
         self.struct = _abi.dsa_seqs(B, self._q, self._k, self._p)
         self.B = B
-        self.total_q = int(cu_q[-1])
-        self.total_k = int(cu_k[-1])
-        self.max_S = max(int(cu_k[b + 1]) - int(cu_k[b]) for b in range(B)) if B else 0
+        self.total_q = self._q[B]
+        self.total_k = self._k[B]
+
+    @property
+    def max_S(self) -> int:
+        k = self._k[:]
+        return max((b - a for a, b in zip(k, k[1:])), default=0)
 
     @classmethod
     def from_lengths(cls, T, S, start_pos):
@@ -383,48 +395,37 @@ def set_stage_events(events):
 # ---------------------------------------------------------------------------------------------------------------
 # Speculative decoding over a served latent cache
 # ---------------------------------------------------------------------------------------------------------------
-def _on_one_device(fn: str, **tensors) -> torch.device:
-    """The CUDA device that every given tensor is on."""
-    dev = None
-    for name, t in tensors.items():
+def _on_one_device(fn: str, tensors) -> int:
+    """The index of the CUDA device that every tensor (of pairs of a name and a tensor or None) is on."""
+    dev = -1
+    for name, t in tensors:
         if t is None:
             continue
-        if t.device.type != "cuda":
+        d = t.get_device()
+        if d < 0:
             raise ValueError(f"{fn}: {name} must be a CUDA tensor, is on {t.device}")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{fn}: {name} is on {t.device}, other arguments on {dev}")
-        dev = t.device
+        if dev >= 0 and d != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, other arguments on cuda:{dev}")
+        dev = d
     return dev
 
 
-@contextlib.contextmanager
-def _launching(dev: torch.device, stream):
-    """Launches go to ``stream`` (default: the current one of ``dev``) with ``dev`` current, and what is
-    allocated meanwhile belongs to that stream."""
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield torch.cuda.current_stream(dev)
-        else:
-            if stream.device != dev:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-            with torch.cuda.stream(stream):
-                yield stream
+_NOTHING = contextlib.nullcontext()
 
 
-def _int32(fn: str, name: str, t, shape=None):
-    if t is None:
-        return
-    if t.dtype != torch.int32 or not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be a contiguous int32 tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _launching(dev: int, stream):
+    """The context of a call on device ``dev``: launches go to ``stream`` (default: the current one) with ``dev``
+    current, and what is allocated meanwhile belongs to that stream."""
+    if stream is None:
+        return _NOTHING if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+    return torch.cuda.stream(stream)
 
 
-def _rows_2d(fn: str, name: str, t: torch.Tensor, width=None, rows=None):
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{fn}: {name} must be 2-D with contiguous rows")
-    if (width is not None and t.shape[1] != width) or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected ({rows}, {width})")
+def _int32(fn: str, name: str, t, n: int):
+    if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous()):
+        raise ValueError(f"{fn}: {name} must be a contiguous int32 tensor [{n}]")
 
 
 class Pages:
@@ -436,21 +437,16 @@ class Pages:
         if block_table.dim() != 2 or block_table.dtype != torch.int32 or \
                 (block_table.shape[1] > 1 and block_table.stride(1) != 1):
             raise ValueError("Pages: block_table must be a 2-D int32 tensor with contiguous rows")
-        self.block_table = block_table
-        ld = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
-        if ld < block_table.shape[1]:
+        rows, width = block_table.shape
+        ld = block_table.stride(0) if rows > 1 else width
+        if ld < width:
             raise ValueError("Pages: the rows of block_table overlap")
-        self.struct = _abi.dsa_pages(block_table.data_ptr(), ld, int(page_size), int(n_pages))
+        self.block_table, self.rows = block_table, rows
+        self.struct = _abi.dsa_pages(block_table.data_ptr(), ld, width, page_size, n_pages)
 
     def ref(self, fn: str, seqs: Seqs):
-        if self.block_table.shape[0] < seqs.B:
-            raise ValueError(f"{fn}: block_table has {self.block_table.shape[0]} rows for {seqs.B} sequences")
-        # the library takes ld_table as the entries a row has; a wider stride only skips
-        need = max((seqs.struct.start_pos[b] + seqs.struct.cu_q[b + 1] - seqs.struct.cu_q[b]
-                    for b in range(seqs.B) if seqs.struct.cu_q[b + 1] > seqs.struct.cu_q[b]), default=0)
-        if need > self.block_table.shape[1] * self.struct.page_size:
-            raise ValueError(f"{fn}: block_table holds {self.block_table.shape[1]} pages of {self.struct.page_size} "
-                             f"tokens a sequence, {need} tokens are asked for")
+        if self.rows < seqs.B:
+            raise ValueError(f"{fn}: block_table has {self.rows} rows for {seqs.B} sequences")
         return ctypes.byref(self.struct)
 
 
@@ -461,26 +457,35 @@ class LatentCache:
 
     def __init__(self, kv: torch.Tensor, k_pe: torch.Tensor, kv_scale: torch.Tensor | None = None):
         dt = _dt(kv)
-        _rows_2d("LatentCache", "kv", kv)
-        _rows_2d("LatentCache", "k_pe", k_pe, rows=kv.shape[0])
+        rows, d_c = _rows_2d("LatentCache", "kv", kv)
+        _, d_r = _rows_2d("LatentCache", "k_pe", k_pe, None, rows)
         if k_pe.dtype != (torch.bfloat16 if dt == DSA_E4M3 else kv.dtype):
             raise ValueError(f"LatentCache: k_pe is {k_pe.dtype} beside {kv.dtype} latents")
         if (kv_scale is not None) != (dt == DSA_E4M3):
             raise ValueError("LatentCache: kv_scale goes with e4m3 codes, and only with them")
         if kv_scale is not None and (kv_scale.dtype != torch.float32 or not kv_scale.is_contiguous() or
-                                     tuple(kv_scale.shape) != (kv.shape[0], kv.shape[1] // 128)):
+                                     kv_scale.shape != (rows, d_c // 128)):
             raise ValueError("LatentCache: kv_scale must be contiguous fp32 [rows, d_c / 128]")
         self.kv, self.k_pe, self.kv_scale = kv, k_pe, kv_scale
-        self.d_c, self.d_r, self.rows = kv.shape[1], k_pe.shape[1], kv.shape[0]
+        self.d_c, self.d_r, self.rows = d_c, d_r, rows
         self.struct = _abi.dsa_latent_cache(
             kv.data_ptr(), _ld(kv), None if kv_scale is None else kv_scale.data_ptr(),
-            k_pe.data_ptr() if self.d_r else None, _ld(k_pe), dt, self.rows)
+            k_pe.data_ptr() if d_r else None, _ld(k_pe), dt, rows)
 
     def ref(self):
         return ctypes.byref(self.struct)
 
     def tensors(self):
-        return {"cache.kv": self.kv, "cache.k_pe": self.k_pe, "cache.kv_scale": self.kv_scale}
+        return ("cache.kv", self.kv), ("cache.k_pe", self.k_pe), ("cache.kv_scale", self.kv_scale)
+
+
+def _rows_2d(fn: str, name: str, t: torch.Tensor, width=None, rows=None):
+    shape = t.shape
+    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{fn}: {name} must be 2-D with contiguous rows")
+    if (width is not None and shape[1] != width) or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{fn}: {name} has shape {tuple(shape)}, expected ({rows}, {width})")
+    return shape
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -491,23 +496,31 @@ def _ld(t: torch.Tensor) -> int:
     return (t.shape[1] + per - 1) // per * per
 
 
-def _pages_ref(fn, pages, seqs):
+def _table(pages):
+    return "block_table", None if pages is None else pages.block_table
+
+
+def _ref_pages(fn, pages, seqs):
     return None if pages is None else pages.ref(fn, seqs)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def dsa_latent_cache_write(c_kv, k_pe, cache: LatentCache, seqs: Seqs, pages: Pages | None = None, stream=None):
     """Write the new tokens' latent rows c_kv [sum T, d_c] and rotary keys k_pe [sum T, d_r] (fp32 or bf16) into the
     cache as tokens start_pos[b] + t of their sequences, quantising them when the cache holds e4m3 codes."""
     fn = "dsa_latent_cache_write"
-    dev = _on_one_device(fn, c_kv=c_kv, k_pe=k_pe, block_table=pages and pages.block_table, **cache.tensors())
+    dev = _on_one_device(fn, (("c_kv", c_kv), ("k_pe", k_pe), _table(pages)) + cache.tensors())
     _rows_2d(fn, "c_kv", c_kv, cache.d_c, seqs.total_q)
     _rows_2d(fn, "k_pe", k_pe, cache.d_r, seqs.total_q)
     if k_pe.dtype != c_kv.dtype:
         raise ValueError(f"{fn}: k_pe is {k_pe.dtype}, c_kv {c_kv.dtype}")
-    with _launching(dev, stream) as s:
+    with _launching(dev, stream):
         _check(fn, _abi.load().dsa_latent_cache_write(
-            _ptr(c_kv), _ld(c_kv), _ptr(k_pe) if cache.d_r else None, _ld(k_pe), _dt(c_kv), cache.d_c, cache.d_r,
-            cache.ref(), seqs.ref(), _pages_ref(fn, pages, seqs), _stream(s)))
+            c_kv.data_ptr(), _ld(c_kv), k_pe.data_ptr() if cache.d_r else None, _ld(k_pe), _dt(c_kv), cache.d_c,
+            cache.d_r, cache.ref(), seqs.ref(), _ref_pages(fn, pages, seqs), torch._C._cuda_getCurrentRawStream(dev)))
 
 
 def dsa_latent_cache_read(cache: LatentCache, seqs: Seqs, pages: Pages | None = None, pos=None, dtype=torch.bfloat16,
@@ -516,25 +529,23 @@ def dsa_latent_cache_read(cache: LatentCache, seqs: Seqs, pages: Pages | None = 
     start_pos[b] + t without pos; zeros where there is no such token.  Returns (c_kv [sum T, d_c],
     k_pe [sum T, d_r]) of ``dtype``."""
     fn = "dsa_latent_cache_read"
-    dev = _on_one_device(fn, pos=pos, c_kv=c_kv, k_pe=k_pe, block_table=pages and pages.block_table, **cache.tensors())
-    _int32(fn, "pos", pos, (seqs.total_q,))
-    if pos is not None and pages is not None and \
-            pages.block_table.shape[1] * pages.struct.page_size < max(
-                (seqs.struct.cu_k[b + 1] - seqs.struct.cu_k[b] for b in range(seqs.B)
-                 if seqs.struct.cu_q[b + 1] > seqs.struct.cu_q[b]), default=0):
-        raise ValueError(f"{fn}: with pos, block_table must cover every token of the sequences")
-    with _launching(dev, stream) as s:
+    dev = _on_one_device(fn, (("pos", pos), ("c_kv", c_kv), ("k_pe", k_pe), _table(pages)) + cache.tensors())
+    _int32(fn, "pos", pos, seqs.total_q)
+    with _launching(dev, stream):
         if c_kv is None:
-            c_kv = torch.empty((seqs.total_q, cache.d_c), dtype=dtype, device=dev)
+            c_kv = cache.kv.new_empty((seqs.total_q, cache.d_c), dtype=dtype)
+        else:
+            _rows_2d(fn, "c_kv", c_kv, cache.d_c, seqs.total_q)
         if k_pe is None:
-            k_pe = torch.empty((seqs.total_q, cache.d_r), dtype=c_kv.dtype, device=dev)
-        _rows_2d(fn, "c_kv", c_kv, cache.d_c, seqs.total_q)
-        _rows_2d(fn, "k_pe", k_pe, cache.d_r, seqs.total_q)
-        if k_pe.dtype != c_kv.dtype:
-            raise ValueError(f"{fn}: k_pe is {k_pe.dtype}, c_kv {c_kv.dtype}")
+            k_pe = cache.kv.new_empty((seqs.total_q, cache.d_r), dtype=c_kv.dtype)
+        else:
+            _rows_2d(fn, "k_pe", k_pe, cache.d_r, seqs.total_q)
+            if k_pe.dtype != c_kv.dtype:
+                raise ValueError(f"{fn}: k_pe is {k_pe.dtype}, c_kv {c_kv.dtype}")
         _check(fn, _abi.load().dsa_latent_cache_read(
-            cache.ref(), cache.d_c, cache.d_r, seqs.ref(), _pages_ref(fn, pages, seqs), _ptr(pos), _ptr(c_kv),
-            _ld(c_kv), _ptr(k_pe) if cache.d_r else None, _ld(k_pe), _dt(c_kv), _stream(s)))
+            cache.ref(), cache.d_c, cache.d_r, seqs.ref(), _ref_pages(fn, pages, seqs), _addr(pos), c_kv.data_ptr(),
+            _ld(c_kv), k_pe.data_ptr() if cache.d_r else None, _ld(k_pe), _dt(c_kv),
+            torch._C._cuda_getCurrentRawStream(dev)))
     return c_kv, k_pe
 
 
@@ -549,36 +560,43 @@ def dsa_tree_mla_fwd(q_nope, q_pe, cache: LatentCache, W_UK, W_UV, seqs: Seqs, s
     [sum T, words] int64 (or uint64): bit j of a row lets it see node j of its sequence (its ancestors and itself);
     None: a chain, node t sees nodes 0 .. t.  Returns (out [sum T, H, d_v], lse [sum T, H] or None)."""
     fn = "dsa_tree_mla_fwd"
-    dev = _on_one_device(fn, q_nope=q_nope, q_pe=q_pe, W_UK=W_UK, W_UV=W_UV, tree_mask=tree_mask, out=out, lse=lse,
-                         workspace=workspace, block_table=pages and pages.block_table, **cache.tensors())
+    dev = _on_one_device(fn, (("q_nope", q_nope), ("q_pe", q_pe), ("W_UK", W_UK), ("W_UV", W_UV),
+                              ("tree_mask", tree_mask), ("out", out), ("lse", lse), ("workspace", workspace),
+                              _table(pages)) + cache.tensors())
     N, H, d_n = q_nope.shape
     d_r, d_c, d_v = q_pe.shape[2], W_UK.shape[2], W_UV.shape[2]
+    dtype = q_nope.dtype
     for name, t, shape in (("q_nope", q_nope, (seqs.total_q, H, d_n)), ("q_pe", q_pe, (N, H, d_r)),
                            ("W_UK", W_UK, (H, d_n, d_c)), ("W_UV", W_UV, (H, d_c, d_v)), ("out", out, (N, H, d_v))):
-        if t is not None and (tuple(t.shape) != shape or t.dtype != q_nope.dtype or not t.is_contiguous()):
-            raise ValueError(f"{fn}: {name} must be contiguous {shape} of {q_nope.dtype}")
+        if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
+            raise ValueError(f"{fn}: {name} must be contiguous {shape} of {dtype}")
     if (cache.d_c, cache.d_r) != (d_c, d_r):
         raise ValueError(f"{fn}: the cache holds {cache.d_c} + {cache.d_r} values a row, expected {d_c} + {d_r}")
-    if tree_mask is not None and (tree_mask.dtype not in (torch.int64, torch.uint64) or tree_mask.dim() != 2 or
-                                  tree_mask.shape[0] != N or not tree_mask.is_contiguous()):
-        raise ValueError(f"{fn}: tree_mask must be contiguous int64 or uint64 [{N}, words]")
-    if lse is not None and (tuple(lse.shape) != (N, H) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dtype not in (torch.int64, torch.uint64) or tree_mask.dim() != 2 or tree_mask.shape[0] != N or \
+                not tree_mask.is_contiguous():
+            raise ValueError(f"{fn}: tree_mask must be contiguous int64 or uint64 [{N}, words]")
+        words = tree_mask.shape[1]
+    if lse is not None and (lse.shape != (N, H) or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError(f"{fn}: lse must be contiguous fp32 [{N}, {H}]")
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise ValueError(f"{fn}: workspace must be a contiguous uint8 tensor")
     dt = _dt(q_nope)
-    with _launching(dev, stream) as s:
+    lib = _abi.load()
+    with _launching(dev, stream):
         if out is None:
-            out = torch.empty((N, H, d_v), dtype=q_nope.dtype, device=dev)
+            out = q_nope.new_empty((N, H, d_v))
         if lse is None and want_lse:
-            lse = torch.empty((N, H), dtype=torch.float32, device=dev)
+            lse = q_nope.new_empty((N, H), dtype=torch.float32)
         if workspace is None:
-            need = dsa_tree_mla_workspace_size(dt, H, d_n, d_r, d_c, d_v, seqs)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        _check(fn, _abi.load().dsa_tree_mla_fwd(
-            _ptr(q_nope), _ptr(q_pe) if d_r else None, dt, cache.ref(), _ptr(W_UK), _ptr(W_UV), H, d_n, d_r, d_c, d_v,
-            _ptr(tree_mask), 0 if tree_mask is None else tree_mask.shape[1], seqs.ref(), _pages_ref(fn, pages, seqs),
-            float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(s)))
+            need = lib.dsa_tree_mla_workspace_size(dt, H, d_n, d_r, d_c, d_v, seqs.ref())
+            workspace = q_nope.new_empty(max(need, 256), dtype=torch.uint8)
+        _check(fn, lib.dsa_tree_mla_fwd(
+            q_nope.data_ptr(), q_pe.data_ptr() if d_r else None, dt, cache.ref(), W_UK.data_ptr(), W_UV.data_ptr(), H,
+            d_n, d_r, d_c, d_v, _addr(tree_mask), words, seqs.ref(), _ref_pages(fn, pages, seqs), softmax_scale,
+            out.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel(),
+            torch._C._cuda_getCurrentRawStream(dev)))
     return out, lse
 
 
@@ -598,6 +616,19 @@ class Heads:
             raise ValueError(f"Heads: norm must be 'rms', 'layer' or 'none', not {norm!r}")
         self.x, self.norm, self.gain, self.bias, self.y, self.y_pe = x, norm, gain, bias, y, y_pe
 
+    def tensors(self, which):
+        return ((which + ".x", self.x), (which + ".gain", self.gain), (which + ".bias", self.bias),
+                (which + ".y", self.y), (which + ".y_pe", self.y_pe))
+
+
+def _strides(t):
+    """Row and head stride in elements (the stride of a dimension of one is any number in torch: 0 here)."""
+    if t is None:
+        return 0, 0
+    n, h, _ = t.shape
+    a, b, _ = t.stride()
+    return a if n > 1 else 0, b if h > 1 else 0
+
 
 def dsa_head_norm_rope(q: Heads | None, k: Heads | None, rope_cos, rope_sin, seqs: Seqs, pos=None, rope="pairs",
                        rope_first=False, eps=1e-6, split=False, dtype=None, stream=None):
@@ -607,58 +638,61 @@ def dsa_head_norm_rope(q: Heads | None, k: Heads | None, rope_cos, rope_sin, seq
     tensor that is None): y [sum T, heads, D], or with ``split`` (y without the rotary dims, y_pe) as the attention
     takes them."""
     fn = "dsa_head_norm_rope"
-    both = [h for h in (q, k) if h is not None]
-    if not both:
+    if q is None and k is None:
         raise ValueError(f"{fn}: neither q nor k")
     if rope not in _ROPES:
         raise ValueError(f"{fn}: rope must be 'pairs' or 'halves', not {rope!r}")
+    both = ([] if q is None else [q]) + ([] if k is None else [k])
+    named = (("rope_cos", rope_cos), ("rope_sin", rope_sin), ("pos", pos))
+    for name, h in (("q", q), ("k", k)):
+        if h is not None:
+            named += h.tensors(name)
+    dev = _on_one_device(fn, named)
     x0 = both[0].x
-    dev = _on_one_device(fn, rope_cos=rope_cos, rope_sin=rope_sin, pos=pos, **{
-        f"{'qk'[i]}.{n}": getattr(h, n) for i, h in enumerate((q, k)) if h is not None
-        for n in ("x", "gain", "bias", "y", "y_pe")})
-    D, d_r = x0.shape[2], 2 * rope_cos.shape[1]
+    N, D, d_r = seqs.total_q, x0.shape[-1], 2 * rope_cos.shape[-1]
     for name, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)):
-        if t.dtype != torch.float32 or not t.is_contiguous() or t.shape != rope_cos.shape or t.dim() != 2:
+        if t.dtype != torch.float32 or t.dim() != 2 or t.shape != rope_cos.shape or not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous fp32 [positions, d_r / 2]")
-    _int32(fn, "pos", pos, (seqs.total_q,))
+    _int32(fn, "pos", pos, N)
     if d_r > D:
         raise ValueError(f"{fn}: {d_r} rotary dims in heads of {D}")
     split = split or any(h.y_pe is not None for h in both)
     if split and d_r == 0:
         raise ValueError(f"{fn}: no rotary dims to split off")
     y_dtype = next((h.y.dtype for h in both if h.y is not None), dtype or x0.dtype)
-    with _launching(dev, stream) as s:
+    width = D - d_r if split else D
+    with _launching(dev, stream):
         structs, results = [], []
         for h in (q, k):
             if h is None:
                 structs.append(None)
                 results.append(None)
                 continue
-            n = h.x.shape[1]
-            if h.x.dim() != 3 or h.x.shape[0] != seqs.total_q or h.x.shape[2] != D or h.x.dtype != x0.dtype:
-                raise ValueError(f"{fn}: x must be [{seqs.total_q}, heads, {D}] of {x0.dtype}")
-            for name, t in (("gain", h.gain), ("bias", h.bias)):
-                if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (D,) or not t.is_contiguous()):
-                    raise ValueError(f"{fn}: {name} must be contiguous fp32 [{D}]")
-            y = h.y if h.y is not None else torch.empty((seqs.total_q, n, D - d_r if split else D), dtype=y_dtype,
-                                                        device=dev)
-            pe = (h.y_pe if h.y_pe is not None else torch.empty((seqs.total_q, n, d_r), dtype=y_dtype, device=dev)) \
-                if split else None
-            for name, t, w in (("x", h.x, D), ("y", y, D - d_r if split else D), ("y_pe", pe, d_r)):
-                if t is not None and (tuple(t.shape) != (seqs.total_q, n, w) or (w > 1 and t.stride(2) != 1) or
-                                      (name != "x" and t.dtype != y_dtype)):
-                    raise ValueError(f"{fn}: {name} must be [{seqs.total_q}, {n}, {w}] with contiguous heads")
-            # the stride of a dimension of one is any number in torch: 0 here
-            sx, sy, sp = ([0 if t is None or t.shape[i] < 2 else t.stride(i) for i in (0, 1)] for t in (h.x, y, pe))
-            st = _abi.dsa_heads(h.x.data_ptr(), *sx, n, _NORMS[h.norm],
-                                None if h.gain is None else h.gain.data_ptr(),
-                                None if h.bias is None else h.bias.data_ptr(), y.data_ptr(), *sy,
-                                None if pe is None else pe.data_ptr(), *sp)
+            x, y, pe = h.x, h.y, h.y_pe
+            n = x.shape[1]
+            for t in (h.gain, h.bias):
+                if t is not None and (t.dtype != torch.float32 or t.shape != (D,) or not t.is_contiguous()):
+                    raise ValueError(f"{fn}: gain and bias must be contiguous fp32 [{D}]")
+            given = [("x", x, D, x0.dtype)]
+            if y is None:
+                y = x.new_empty((N, n, width), dtype=y_dtype)
+            else:
+                given.append(("y", y, width, y_dtype))
+            if split and pe is None:
+                pe = x.new_empty((N, n, d_r), dtype=y_dtype)
+            elif split:
+                given.append(("y_pe", pe, d_r, y_dtype))
+            for name, t, w, dt in given:
+                if t.shape != (N, n, w) or t.dtype != dt or (w > 1 and t.stride(2) != 1):
+                    raise ValueError(f"{fn}: {name} must be [{N}, {n}, {w}] of {dt} with contiguous heads")
+            st = _abi.dsa_heads(x.data_ptr(), *_strides(x), n, _NORMS[h.norm], _addr(h.gain), _addr(h.bias),
+                                y.data_ptr(), *_strides(y), _addr(pe), *_strides(pe))
             structs.append(ctypes.byref(st))
             results.append((y, pe) if split else y)
         _check(fn, _abi.load().dsa_head_norm_rope(
             structs[0], structs[1], _dt_of(x0.dtype), _dt_of(y_dtype), D, d_r, 1 if rope_first else 0, _ROPES[rope],
-            float(eps), _ptr(rope_cos), _ptr(rope_sin), rope_cos.shape[0], _ptr(pos), seqs.ref(), _stream(s)))
+            eps, rope_cos.data_ptr(), rope_sin.data_ptr(), rope_cos.shape[0], _addr(pos), seqs.ref(),
+            torch._C._cuda_getCurrentRawStream(dev)))
     return tuple(results)
 
 

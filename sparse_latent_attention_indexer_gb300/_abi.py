@@ -56,8 +56,8 @@ class dsa_host_io(ctypes.Structure):
 
 
 class dsa_pages(ctypes.Structure):
-    _fields_ = [("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("page_size", ctypes.c_int32),
-                ("n_pages", ctypes.c_int32)]
+    _fields_ = [("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
 
 
 class dsa_latent_cache(ctypes.Structure):

@@ -274,7 +274,8 @@ int check_latent_cache(const dsa_latent_cache *c, int d_c, int d_r) {
 int check_pages(const dsa_pages *pages, const dsa_latent_cache *c, const Batch &bt, bool whole, PageTab &pt) {
     pt = PageTab{nullptr, 0, 1, 0};
     if (!pages) return bt.total_k <= c->rows ? DSA_OK : DSA_ERR_INVALID_ARG;
-    if (pages->page_size < 16 || pages->page_size % 16 || pages->n_pages < 0 || pages->ld_table < 0)
+    if (pages->page_size < 16 || pages->page_size % 16 || pages->n_pages < 0 || pages->width < 0 ||
+        pages->ld_table < pages->width)
         return DSA_ERR_INVALID_ARG;
     if ((int64_t)pages->n_pages * pages->page_size > c->rows) return DSA_ERR_INVALID_ARG;
     int64_t most = 0;
@@ -282,7 +283,7 @@ int check_pages(const dsa_pages *pages, const dsa_latent_cache *c, const Batch &
         const int64_t T = bt.st.q_off[b + 1] - bt.st.q_off[b];
         if (T > 0) most = std::max<int64_t>(most, whole ? bt.st.k_len[b] : bt.st.start_pos[b] + T);
     }
-    if (most > pages->ld_table * pages->page_size) return DSA_ERR_INVALID_ARG;
+    if (most > pages->width * pages->page_size) return DSA_ERR_INVALID_ARG;
     if (most > 0 && (!pages->block_table || (uintptr_t)pages->block_table % 4)) return DSA_ERR_INVALID_ARG;
     pt = PageTab{pages->block_table, pages->ld_table, pages->page_size, pages->n_pages};
     return DSA_OK;
