@@ -8,14 +8,16 @@
 //   apply_rotary_emb).
 //
 // Bound by HBM: a head is read once and written once and a handful of operations
-// are done per value.  Eight lanes take a head, 16-byte vectors round robin (a
-// head of 192 bf16 values is three vectors a lane), so a norm costs three
-// shuffles, and neighbouring heads of a row share the angles through L1.  A pair
-// of the "pairs" order lies in one vector; in the "halves" order the other half's
-// vector is read too (from L1) rather than passed between lanes, because which
-// lane holds it depends on D and d_r.  Every load of a row comes before its first
-// store, so y may be x.  Widths that are no multiple of 8 (d_r: of 16) and rows off
-// 16 bytes go value by value, one warp a head.
+// are done per value.  A CTA takes heads of one row (query token), so the row's angles
+// and the gains and biases are fetched once, into shared memory.  Eight lanes take a head
+// (sixteen above 256 dims), one to four vectors of eight values each, so a norm costs
+// three shuffles; the next heads are on their way while these are turned and stored.
+// A pair of the "pairs" order lies in one vector; in the "halves" order its other value is
+// 1, 2 or 4 lanes (8: one vector) away (rotary parts of 16, 32, 64 or 128 at a multiple of
+// that).  Every load of a head comes before its first store, so y may be x.  Other widths
+// and rows off 16 bytes go value by value, one warp a head.
+#include <algorithm>
+
 #include "dsa_common.cuh"
 
 namespace dsa {
@@ -34,53 +36,44 @@ struct HeadParams {
     const float *cos, *sin;
     const int32_t *pos;
     int64_t rows;       // (query rows) * (heads of q + heads of k)
+    int per_cta;        // warps' items that a CTA of the vector path takes
     int D, d_r, at;     // at: first rotary dim
     int halves, n_pos;
     float eps;
 };
 static_assert(sizeof(HeadParams) + 256 <= 32764, "launch parameters");
 
-constexpr int LANES = 8;    // lanes of a head (vector path)
 constexpr int MAX_D = 512;
 
-struct Item {
-    const Half *t;
-    int h, r, p;  // head, query row, position (-1: no rotation)
-};
-__device__ __forceinline__ Item item_of(const HeadParams &P, int64_t i) {
-    const int all = P.t[0].n + P.t[1].n;
-    Item m;
-    m.r = (int)(i / all);
-    m.h = (int)(i - (int64_t)m.r * all);
-    m.t = &P.t[0];
-    if (m.h >= P.t[0].n) {
-        m.h -= P.t[0].n;
-        m.t = &P.t[1];
-    }
-    if (P.d_r == 0) {
-        m.p = -1;
-    } else if (P.pos) {
-        m.p = __ldg(P.pos + m.r);
-        if ((unsigned)m.p >= (unsigned)P.n_pos) m.p = -1;
-    } else {
-        m.p = row_info(P.st, m.r).p;
-    }
-    return m;
+// Position of row r (-1: no rotation).
+__device__ __forceinline__ int position(const HeadParams &P, int r) {
+    if (P.d_r == 0) return -1;
+    if (!P.pos) return row_info(P.st, r).p;
+    const int p = __ldg(P.pos + r);
+    return (unsigned)p < (unsigned)P.n_pos ? p : -1;
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 a = *(const uint4 *)p;
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Eight values as they are stored.
+template <typename T> struct Vec8;
+template <> struct Vec8<__nv_bfloat16> { uint4 a; };
+template <> struct Vec8<float> { uint4 a, b; };
+__device__ __forceinline__ void fetch(const __nv_bfloat16 *p, Vec8<__nv_bfloat16> &v) { v.a = *(const uint4 *)p; }
+__device__ __forceinline__ void fetch(const float *p, Vec8<float> &v) {
+    v.a = ((const uint4 *)p)[0];
+    v.b = ((const uint4 *)p)[1];
+}
+__device__ __forceinline__ void unpack(const Vec8<__nv_bfloat16> &s, float (&v)[8]) {
+    const uint32_t w[4] = {s.a.x, s.a.y, s.a.z, s.a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(w[i] << 16);
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 a = ((const float4 *)p)[0], b = ((const float4 *)p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void unpack(const Vec8<float> &s, float (&v)[8]) {
+    const uint32_t w[8] = {s.a.x, s.a.y, s.a.z, s.a.w, s.b.x, s.b.y, s.b.z, s.b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
 }
 template <int N>
 __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[N]) {
@@ -99,115 +92,161 @@ __device__ __forceinline__ void store(float *p, const float (&v)[N]) {
     for (int i = 0; i < N / 4; ++i) ((float4 *)p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
+template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// (x - mean) * inv * gain + bias of 8 values at dim d (mean 0, inv 1, gain 1, bias 0 where the norm has none).
-__device__ __forceinline__ void norm8(float (&v)[8], const Half &t, int d, float mean, float inv) {
-    if (t.norm == DSA_NORM_NONE) return;
-    float g[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (v[i] - mean) * inv;
-    if (t.gain) {
-        load8(t.gain + d, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= g[i];
-    }
-    if (t.bias && t.norm == DSA_NORM_LAYER) {
-        load8(t.bias + d, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += g[i];
-    }
+__device__ __forceinline__ void lds8(const float *p, float (&v)[8]) {
+    const float4 a = ((const float4 *)p)[0], b = ((const float4 *)p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// VPT: vectors of 8 values a lane holds (D <= 64 * VPT).
-template <typename TX, typename TY, int VPT>
-__global__ void __launch_bounds__(256) head_norm_kernel(const __grid_constant__ HeadParams P) {
-    const int sub = threadIdx.x & (LANES - 1);
-    const int64_t i = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
-    const bool live = i < P.rows;  // idle groups stay for the shuffles
-    const Item m = item_of(P, live ? i : 0);
-    const Half &t = *m.t;
-    const TX *x = (const TX *)t.x + m.r * t.ld_x + m.h * t.hd_x;
-    const int half = P.d_r / 2, rot_end = P.at + P.d_r;
-    float v[VPT][8], o[VPT][8];  // o: the other half's values of a rotary vector ("halves" order)
+constexpr int CTA = 128;
+
+// LANES of a head, each with VPT vectors of 8 values (D <= 8 * LANES * VPT).
+template <typename TX, typename TY, int LANES, int VPT, bool HALVES>
+__global__ void __launch_bounds__(CTA, VPT * sizeof(Vec8<TX>) <= 48 ? 6 : 4) head_norm_kernel(const __grid_constant__ HeadParams P) {
+    __shared__ __align__(16) float turn[2][MAX_D / 2];  // cos, sin of the row's position
+    __shared__ __align__(16) float aff[2][2 * MAX_D];   // q's and k's gains and biases
+    constexpr int PACK = 32 / LANES, WARPS = CTA / 32;  // heads of a warp
+    const int half = P.d_r / 2, lane = threadIdx.x & 31, sub = lane & (LANES - 1), mine = lane / LANES;
+    const int rq = (P.t[0].n + PACK - 1) / PACK, all = rq + (P.t[1].n + PACK - 1) / PACK;  // warps' items
+    const int end = min(all, (int)(blockIdx.y + 1) * P.per_cta);
+    const int r = blockIdx.x;
+    int it = blockIdx.y * P.per_cta + (threadIdx.x >> 5);
+    Vec8<TX> raw[VPT];
+    const auto load = [&](int item) {
+        const Half &t = P.t[item >= rq];
+        const int h = (item >= rq ? item - rq : item) * PACK + mine;
+        const TX *x = (const TX *)t.x + r * t.ld_x + h * t.hd_x + sub * 8;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int d = (j * LANES + sub) * 8;
-        if (d < P.D) {
-            load8(x + d, v[j]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
+        for (int j = 0; j < VPT; ++j) {
+            raw[j] = Vec8<TX>{};
+            if (h < t.n && (j * LANES + sub) * 8 < P.D) fetch(x + j * LANES * 8, raw[j]);
         }
-        if (P.halves && m.p >= 0 && d >= P.at && d < rot_end) load8(x + (d < P.at + half ? d + half : d - half), o[j]);
-    }
-    float mean = 0.0f, inv = 1.0f;
-    if (t.norm == DSA_NORM_LAYER) {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += v[j][e];
-        mean = s;
-    }
-    mean = group_sum(mean) / (float)P.D;  // every lane of the warp shuffles, whatever its head's norm
-    {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float c = (j * LANES + sub) * 8 < P.D ? v[j][e] - mean : 0.0f;
-                s = fmaf(c, c, s);
-            }
-        s = group_sum(s);
-        if (t.norm != DSA_NORM_NONE) inv = rsqrtf(s / (float)P.D + P.eps);
-    }
-    __syncwarp();  // every lane has read its values: y may be x
-    if (!live) return;
-    TY *y = (TY *)t.y + m.r * t.ld_y + m.h * t.hd_y;
-    TY *pe = t.pe ? (TY *)t.pe + m.r * t.ld_pe + m.h * t.hd_pe : y + P.at;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int d = (j * LANES + sub) * 8;
-        if (d >= P.D) continue;
-        norm8(v[j], t, d, mean, inv);
-        if (d < P.at || d >= rot_end) {
-            // with an output of their own for the rotary dims, the others close up
-            store<8>(y + (t.pe && d >= rot_end ? d - P.d_r : d), v[j]);
-            continue;
+    };
+    if (it < end) load(it);
+    const int p = position(P, r);
+    if (p >= 0)
+        for (int i = threadIdx.x; i < half; i += CTA) {
+            turn[0][i] = __ldg(P.cos + (int64_t)p * half + i);
+            turn[1][i] = __ldg(P.sin + (int64_t)p * half + i);
         }
-        const int k = d - P.at;  // dim within the rotary part
-        if (m.p < 0 && P.halves) {
-            store<8>(pe + k, v[j]);
-        } else if (P.halves) {
-            const bool second = k >= half;
-            norm8(o[j], t, second ? d - half : d + half, mean, inv);
-            float c[8], s[8];
-            load8(P.cos + (int64_t)m.p * half + (second ? k - half : k), c);
-            load8(P.sin + (int64_t)m.p * half + (second ? k - half : k), s);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] = second ? o[j][e] * s[e] + v[j][e] * c[e] : v[j][e] * c[e] - o[j][e] * s[e];
-            store<8>(pe + k, v[j]);
-        } else {
-            float4 c = make_float4(1.0f, 1.0f, 1.0f, 1.0f), s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (m.p >= 0) {
-                c = __ldg((const float4 *)(P.cos + (int64_t)m.p * half + k / 2));
-                s = __ldg((const float4 *)(P.sin + (int64_t)m.p * half + k / 2));
-            }
-            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-            float a[4], b[4];
+    for (int i = 0; i < 2; ++i) {
+        const Half &t = P.t[i];
+        for (int d = threadIdx.x; d < P.D; d += CTA) {
+            if (t.gain) aff[i][d] = __ldg(t.gain + d);
+            if (t.bias) aff[i][MAX_D + d] = __ldg(t.bias + d);
+        }
+    }
+    __syncthreads();
+    for (; it < end; it += WARPS) {  // every lane of a warp stays for the shuffles
+        const int which = it >= rq;
+        const Half &t = P.t[which];
+        const int h = (which ? it - rq : it) * PACK + mine;
+        const bool live = h < t.n;
+        float v[VPT][8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                a[e] = v[j][2 * e] * cc[e] - v[j][2 * e + 1] * ss[e];
-                b[e] = v[j][2 * e] * ss[e] + v[j][2 * e + 1] * cc[e];
+        for (int j = 0; j < VPT; ++j) unpack(raw[j], v[j]);  // zeros behind D
+        if (t.norm != DSA_NORM_NONE) {
+            float mu = 0.0f, s = 0.0f;
+            if (t.norm == DSA_NORM_LAYER) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mu += v[j][e];
+                mu = group_sum<LANES>(mu) / (float)P.D;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[j][e] = (j * LANES + sub) * 8 < P.D ? v[j][e] - mu : 0.0f;
             }
-            store<4>(pe + k / 2, a);
-            store<4>(pe + half + k / 2, b);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(v[j][e], v[j][e], s);
+            const float inv = rsqrtf(group_sum<LANES>(s) / (float)P.D + P.eps);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int d = (j * LANES + sub) * 8;
+                float g[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[j][e] *= inv;
+                if (t.gain && d < P.D) {
+                    lds8(aff[which] + d, g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[j][e] *= g[e];
+                }
+                if (t.bias && t.norm == DSA_NORM_LAYER && d < P.D) {
+                    lds8(aff[which] + MAX_D + d, g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[j][e] += g[e];
+                }
+            }
+        }
+        TY *y = (TY *)t.y + r * t.ld_y + h * t.hd_y;
+        TY *pe = t.pe ? (TY *)t.pe + r * t.ld_pe + h * t.hd_pe : y + P.at;
+        __syncwarp();  // every lane has its values, so y may be x: the next heads are others
+        if (it + WARPS < end) load(it + WARPS);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int d = (j * LANES + sub) * 8, k = d - P.at;  // dim, and dim within the rotary part
+            const bool rot = k >= 0 && k < P.d_r;
+            if constexpr (HALVES) {
+                // do the lanes' vectors j hold rotary dims?  (the same for the whole warp)
+                if (p >= 0 && j * LANES * 8 < P.at + P.d_r && (j + 1) * LANES * 8 > P.at) {
+                    const bool second = rot && k >= half;
+                    float o[8], c[8], sn[8];
+                    if (half < LANES * 8) {  // the pairs' other values lie half / 8 lanes away
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = __shfl_xor_sync(0xffffffffu, v[j][e], half / 8);
+                    } else {  // or in the next or last vector (half == 8 * LANES): both are turned at the first
+                        if (j + 1 < VPT && !second && rot) {
+                            lds8(turn[0] + k, c);
+                            lds8(turn[1] + k, sn);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float a = v[j][e], b = v[(j + 1) % VPT][e];
+                                v[j][e] = a * c[e] - b * sn[e];
+                                v[(j + 1) % VPT][e] = b * c[e] + a * sn[e];
+                            }
+                        }
+                    }
+                    if (half < LANES * 8 && rot) {
+                        lds8(turn[0] + (second ? k - half : k), c);
+                        lds8(turn[1] + (second ? k - half : k), sn);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * c[e] + (second ? o[e] : -o[e]) * sn[e];
+                    }
+                }
+            }
+            if (!live || d >= P.D) continue;
+            if (!rot) {
+                // with an output of their own for the rotary dims, the others close up
+                store<8>(y + (t.pe && k >= 0 ? d - P.d_r : d), v[j]);
+            } else if (HALVES) {
+                store<8>(pe + k, v[j]);
+            } else {
+                float4 c = make_float4(1.0f, 1.0f, 1.0f, 1.0f), sn = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (p >= 0) {
+                    c = *(const float4 *)(turn[0] + k / 2);
+                    sn = *(const float4 *)(turn[1] + k / 2);
+                }
+                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+                float a[4], b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    a[e] = v[j][2 * e] * cc[e] - v[j][2 * e + 1] * ss[e];
+                    b[e] = v[j][2 * e] * ss[e] + v[j][2 * e + 1] * cc[e];
+                }
+                store<4>(pe + k / 2, a);
+                store<4>(pe + half + k / 2, b);
+            }
         }
     }
 }
@@ -220,9 +259,10 @@ __global__ void __launch_bounds__(256) head_norm_any_kernel(const __grid_constan
     const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (i >= P.rows) return;
     float *v = rows[threadIdx.x >> 5];
-    const Item m = item_of(P, i);
-    const Half &t = *m.t;
-    const TX *x = (const TX *)t.x + m.r * t.ld_x + m.h * t.hd_x;
+    const int all = P.t[0].n + P.t[1].n, r = (int)(i / all), at = (int)(i - (int64_t)r * all);
+    const Half &t = P.t[at >= P.t[0].n];
+    const int h = at >= P.t[0].n ? at - P.t[0].n : at, p = position(P, r);
+    const TX *x = (const TX *)t.x + r * t.ld_x + h * t.hd_x;
     float s = 0.0f;
     for (int d = lane; d < P.D; d += 32) {
         v[d] = to_f32(x[d]);
@@ -244,8 +284,8 @@ __global__ void __launch_bounds__(256) head_norm_any_kernel(const __grid_constan
             v[d] = z;
         }
     __syncwarp();  // the row is read and normed: y may be x
-    TY *y = (TY *)t.y + m.r * t.ld_y + m.h * t.hd_y;
-    TY *pe = t.pe ? (TY *)t.pe + m.r * t.ld_pe + m.h * t.hd_pe : y + P.at;
+    TY *y = (TY *)t.y + r * t.ld_y + h * t.hd_y;
+    TY *pe = t.pe ? (TY *)t.pe + r * t.ld_pe + h * t.hd_pe : y + P.at;
     const int half = P.d_r / 2, rot_end = P.at + P.d_r;
     for (int d = lane; d < P.D; d += 32)
         if (d < P.at || d >= rot_end) y[t.pe && d >= rot_end ? d - P.d_r : d] = from_f32<TY>(v[d]);
@@ -253,9 +293,9 @@ __global__ void __launch_bounds__(256) head_norm_any_kernel(const __grid_constan
         const int ia = P.at + (P.halves ? k : 2 * k), ib = P.at + (P.halves ? half + k : 2 * k + 1);
         const float a = v[ia], b = v[ib];
         float c = 1.0f, sn = 0.0f;
-        if (m.p >= 0) {
-            c = __ldg(P.cos + (int64_t)m.p * half + k);
-            sn = __ldg(P.sin + (int64_t)m.p * half + k);
+        if (p >= 0) {
+            c = __ldg(P.cos + (int64_t)p * half + k);
+            sn = __ldg(P.sin + (int64_t)p * half + k);
         }
         pe[k] = from_f32<TY>(a * c - b * sn);
         pe[half + k] = from_f32<TY>(a * sn + b * c);
@@ -267,18 +307,34 @@ inline bool on(const void *p, int64_t a, int64_t b, int dtype, size_t n) {
     return (uintptr_t)p % n == 0 && a * esz(dtype) % n == 0 && b * esz(dtype) % n == 0;
 }
 
-template <typename TX, typename TY>
-cudaError_t launch_heads(const HeadParams &P, bool vec, cudaStream_t s) {
-    const int64_t per = vec ? 256 / LANES : 8;
-    const int64_t grid = (P.rows + per - 1) / per;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (!vec) head_norm_any_kernel<TX, TY><<<(unsigned)grid, 256, 0, s>>>(P);
-    else if (P.D <= 64) head_norm_kernel<TX, TY, 1><<<(unsigned)grid, 256, 0, s>>>(P);
-    else if (P.D <= 128) head_norm_kernel<TX, TY, 2><<<(unsigned)grid, 256, 0, s>>>(P);
-    else if (P.D <= 192) head_norm_kernel<TX, TY, 3><<<(unsigned)grid, 256, 0, s>>>(P);
-    else if (P.D <= 256) head_norm_kernel<TX, TY, 4><<<(unsigned)grid, 256, 0, s>>>(P);
-    else head_norm_kernel<TX, TY, 8><<<(unsigned)grid, 256, 0, s>>>(P);
+template <typename TX, typename TY, int LANES, int VPT>
+cudaError_t launch_vec(HeadParams &P, cudaStream_t s) {
+    // Few rows: a row's heads are spread over CTAs, so that about four of them come on every SM; many rows: one CTA takes
+    // them all and fetches the angles and gains once.  An item is the heads that a warp takes at once.
+    constexpr int PACK = 32 / LANES, WARPS = CTA / 32;
+    const int items = (P.t[0].n + PACK - 1) / PACK + (P.t[1].n + PACK - 1) / PACK, rounds = (items + WARPS - 1) / WARPS;
+    const int n = (int)(P.rows / (P.t[0].n + P.t[1].n));
+    const int parts = std::max(1, std::min({rounds, (4 * device_sm_count() + n - 1) / n, 65535}));
+    P.per_cta = (rounds + parts - 1) / parts * WARPS;
+    const dim3 grid(n, (items + P.per_cta - 1) / P.per_cta);
+    if (P.halves) head_norm_kernel<TX, TY, LANES, VPT, true><<<grid, CTA, 0, s>>>(P);
+    else head_norm_kernel<TX, TY, LANES, VPT, false><<<grid, CTA, 0, s>>>(P);
     return cudaGetLastError();
+}
+
+template <typename TX, typename TY>
+cudaError_t launch_heads(HeadParams &P, bool vec, cudaStream_t s) {
+    if (!vec) {
+        const int64_t grid = (P.rows + 7) / 8;
+        if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        head_norm_any_kernel<TX, TY><<<(unsigned)grid, 256, 0, s>>>(P);
+        return cudaGetLastError();
+    }
+    if (P.D <= 64) return launch_vec<TX, TY, 8, 1>(P, s);
+    if (P.D <= 128) return launch_vec<TX, TY, 8, 2>(P, s);
+    if (P.D <= 192) return launch_vec<TX, TY, 8, 3>(P, s);
+    if (P.D <= 256) return launch_vec<TX, TY, 8, 4>(P, s);
+    return launch_vec<TX, TY, 16, 4>(P, s);
 }
 
 }  // namespace
@@ -354,6 +410,8 @@ extern "C" int dsa_head_norm_rope(const dsa_heads *q, const dsa_heads *k, int x_
     P.d_r = d_r;
     P.at = rope_first ? 0 : D - d_r;
     P.halves = rope == DSA_ROPE_HALVES;
+    if (P.halves && d_r > 0)  // the other value of a pair is 1, 2, 4 or 8 lanes or one vector away
+        vec = vec && (d_r == 16 || d_r == 32 || d_r == 64 || d_r == 128) && P.at % d_r == 0;
     P.n_pos = n_pos;
     P.eps = eps;
     const cudaStream_t s = (cudaStream_t)stream;
