@@ -448,7 +448,7 @@ typedef struct dsa_pages {
 typedef struct dsa_latent_cache {
     void *kv;                     /* [rows, ld_kv]: d_c values or codes per row */
     int64_t ld_kv;                /* elements (bytes for E4M3) */
-    float *kv_scale;              /* E4M3: [rows, d_c / 128]; else NULL */
+    float *kv_scale;              /* E4M3: [rows, d_c / 128] powers of two; else NULL */
     void *k_pe;                   /* [rows, ld_pe]: d_r rotary key values per row (may lie inside kv's rows) */
     int64_t ld_pe;                /* elements */
     int32_t dtype;                /* DSA_F32, DSA_BF16 or DSA_E4M3 */
@@ -498,8 +498,9 @@ int dsa_latent_cache_read(const dsa_latent_cache *cache, int d_c, int d_r, const
  *               are ignored; T_b <= 64 mask_words); NULL: node t sees nodes 0 .. t
  *               (a chain: one token, or a prompt chunk)
  * A row that sees nothing gets out = 0, lse = -inf.  What a row does not see never
- * reaches it, whatever its bits (stale rows, Inf, NaN); visible Inf and NaN are
- * not supported.  Contiguous or paged cache (`pages`), of dtype's own type, or
+ * reaches it, whatever its bits (stale rows, Inf, NaN).  A row that sees a NaN is
+ * NaN; visible Inf and E4M3 NaN codes are not supported.  softmax_scale is finite, also times log2(e);
+ * 0 and negative values are allowed.  Contiguous or paged cache (`pages`), of dtype's own type, or
  * E4M3 with dtype DSA_BF16.
  * Two kernels: tensor cores for bf16 at d_n = 128, d_r = 64, d_c = 512, d_v = 128
  * and any H; a generic one for everything else within the limits of

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(HG * 32) tree_simt_kernel(const float *__restr
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) zmax = fmaxf(zmax, __shfl_xor_sync(0xffffffffu, zmax, off));
         const float m_new = fmaxf(m, zmax);
-        if (m_new == -INFINITY) continue;  // nothing seen yet
+        if (m_new == -INFINITY && !__any_sync(0xffffffffu, z != z)) continue;  // nothing seen yet
         const float corr = expf(m - m_new);
         const float p = (z == -INFINITY) ? 0.0f : expf(z - m_new);
         float psum = p;
@@ -133,14 +133,14 @@ __global__ void __launch_bounds__(HG * 32) tree_simt_kernel(const float *__restr
         }
     }
     if (h >= P.H) return;
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a NaN that the row sees stays one
     const int64_t rh = (int64_t)r * P.H + h;
 #pragma unroll
     for (int i = 0; i < MAX_PER_LANE; ++i) {
         const int d = lane + 32 * i;
         if (d < P.d_c) olat[rh * P.d_c + d] = o[i] * inv;
     }
-    if (lse && lane == 0) lse[rh] = l > 0.0f ? m + logf(l) : -INFINITY;
+    if (lse && lane == 0) lse[rh] = l == 0.0f ? -INFINITY : m + logf(l);
 }
 
 template <typename T, typename TC>
@@ -226,7 +226,7 @@ int dsa_tree_mla_fwd(const void *q_nope, const void *q_pe, int dtype, const dsa_
         (rc = check_pages(pages, cache, bt, false, pt)))
         return rc;
     if (dtype == DSA_F32 ? cache->dtype != DSA_F32 : cache->dtype == DSA_F32) return DSA_ERR_UNSUPPORTED;
-    if (!std::isfinite(softmax_scale)) return DSA_ERR_INVALID_ARG;
+    if (!std::isfinite(softmax_scale * 1.4426950408889634f)) return DSA_ERR_INVALID_ARG;  // in powers of two, too
     if ((int64_t)bt.total_q * H >= (int64_t(1) << 31) - 256) return DSA_ERR_UNSUPPORTED;
     if (bt.total_q == 0) return DSA_OK;
     if (!q_nope || (d_r > 0 && !q_pe) || !W_UK || !W_UV || !out) return DSA_ERR_INVALID_ARG;

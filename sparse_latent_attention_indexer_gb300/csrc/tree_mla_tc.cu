@@ -38,6 +38,7 @@
 // Waits are bounded; a timeout records its site in the device error word and
 // both CTAs drain and exit.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "tc_common.cuh"
@@ -121,7 +122,10 @@ struct TreeParams {
     const uint64_t *mask;
     int words, H;
     int oob;                     // a cache row past the last one
+    // softmax_scale log2(e) = +-scale_log2 2^k with scale_log2 in [1/2, 1): the queries carry +-2^k (exact), so that a
+    // score keeps clear of fp16's range unless its exponent does.
     float scale_log2;
+    uint32_t q_factor;           // +-2^k, twice in bf16
     long long wait_limit;
 };
 static_assert(sizeof(TreeParams) + 4 * 128 + 128 <= 32764, "launch parameters");
@@ -528,13 +532,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         const int q = warp & 3, g = (warp >> 2) - 1;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t own_lanes = lanes + (rank * 16u << 16), other_lanes = lanes + (peer * 16u << 16);
-        const float sl2 = fabsf(P.scale_log2);            // not 0; the queries carry its sign
+        const float sl2 = P.scale_log2;
         bool ok = true;
         if (n > 0) {
             // The q~ slice moves to tensor memory (A operand of QK^T): four slabs of 32 packed columns, two each of the first
             // groups; the last one puts the rotary slice of the queries into shared memory.
             const int h = q * 32 + lane;
-            const uint32_t flip = P.scale_log2 < 0.0f ? 0x80008000u : 0u;
+            const uint32_t f = P.q_factor;
             uint4 rq[4];
             if (g == G - 1) {
                 const int64_t row = seq_row0 + lrow + h;
@@ -551,10 +555,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const uint4 t4 = *(const uint4 *)(srow + ((e ^ (h & 7)) << 4));
-                    qv[4 * e] = t4.x ^ flip;
-                    qv[4 * e + 1] = t4.y ^ flip;
-                    qv[4 * e + 2] = t4.z ^ flip;
-                    qv[4 * e + 3] = t4.w ^ flip;
+                    qv[4 * e] = mul2(t4.x, f);
+                    qv[4 * e + 1] = mul2(t4.y, f);
+                    qv[4 * e + 2] = mul2(t4.z, f);
+                    qv[4 * e + 3] = mul2(t4.w, f);
                 }
                 tc::tmem_st32(lanes + COL_Q + js * 32, qv);
             }
@@ -563,7 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     *(uint4 *)(QR + h * 64 + ((e ^ ((h >> 1) & 3)) << 4)) =
-                        make_uint4(rq[e].x ^ flip, rq[e].y ^ flip, rq[e].z ^ flip, rq[e].w ^ flip);
+                        make_uint4(mul2(rq[e].x, f), mul2(rq[e].y, f), mul2(rq[e].z, f), mul2(rq[e].w, f));
                 tc::fence_proxy_async_smem();  // read by the rotary MMAs (async proxy)
             }
             tc::tc_fence_before();
@@ -812,13 +816,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             for (int i = 1; i < G; ++i) m = fmaxf(m, rs->ref[i][r]);
 #pragma unroll
             for (int i = 0; i < G; ++i)
-                if (rs->ref[i][r] != -INFINITY) sum += rs->sum[i][r] * pow2(rs->ref[i][r] - m);
-            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                sum += rs->sum[i][r] * (rs->ref[i][r] == -INFINITY ? 1.0f : pow2(rs->ref[i][r] - m));  // (no reference: 0, or NaN)
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN that the row sees stays one
             ms->inv[h] = inv;
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::map_peer(tc::smem_u32(&ms->inv[h]), peer)), "f"(inv)
                          : "memory");
             if (lrow + h < seq_rows) {
-                const float row_lse = sum > 0.0f ? (m + log2f(sum)) * LN2 : -INFINITY;
+                const float row_lse = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * LN2;
                 if (splits > 1) lpart[((int64_t)P.part0[lo] + rem) * ROWS + h] = row_lse;
                 else if (lse) lse[seq_row0 + lrow + h] = row_lse;
             }
@@ -847,7 +851,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             tc::tmem_ld32(lanes + COL_O + cc * 32, o);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = have && inv > 0.0f ? o[j] * inv : 0.0f;
+            for (int j = 0; j < 32; ++j) o[j] = have && inv != 0.0f ? o[j] * inv : 0.0f;
             if (whole) {
                 uint4 *d = (uint4 *)(srow + cc * 64);
 #pragma unroll
@@ -912,7 +916,13 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     const int64_t p0 = P.part0[b] + (nt - 1 - rt);  // partial of split 0; split s: + s * nt
     const int i = lr - rt * ROWS;
     float mxl = -INFINITY;
-    for (int s = lane; s < splits; s += 32) mxl = fmaxf(mxl, lpart[(p0 + (int64_t)s * nt) * ROWS + i]);
+    bool bad = false;  // a NaN that the row sees
+    for (int s = lane; s < splits; s += 32) {
+        const float l = lpart[(p0 + (int64_t)s * nt) * ROWS + i];
+        bad = bad || l != l;
+        mxl = fmaxf(mxl, l);
+    }
+    bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mxl = fmaxf(mxl, __shfl_xor_sync(0xffffffffu, mxl, o));
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -930,10 +940,10 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
             acc.w = fmaf(wgt, x.w, acc.w);
         }
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = bad ? NAN : sum > 0.0f ? 1.0f / sum : 0.0f;
     const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), c = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     *((uint2 *)(olat + rh * DC + quarter * 128) + lane) = make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&c);
-    if (lse && quarter == 0 && lane == 0) lse[rh] = sum > 0.0f ? mxl + logf(sum) : -INFINITY;
+    if (lse && quarter == 0 && lane == 0) lse[rh] = bad ? NAN : sum > 0.0f ? mxl + logf(sum) : -INFINITY;
 }
 
 // How the work is cut: every sequence's tokens in `splits` ranges of at most `chunk` tiles.
@@ -1050,7 +1060,11 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
     P.mask = mask;
     P.words = words;
     P.H = H;
-    P.scale_log2 = scale == 0.0f ? 1e-30f : scale * 1.4426950408889634f;  // 0: so small that every score counts alike
+    int k;
+    P.scale_log2 = std::frexp(std::fabs(scale == 0.0f ? 1e-30f : scale * 1.4426950408889634f), &k);  // 0: every score counts alike
+    const int kc = std::max(-120, std::min(120, k));
+    P.scale_log2 = std::ldexp(P.scale_log2, k - kc);
+    P.q_factor = 0x10001u * ((uint32_t)(kc + 127) << 7 | (scale < 0.0f ? 0x8000u : 0u));
     P.wait_limit = wait_limit_cycles();
     const uint64_t rows = (uint64_t)std::max<int64_t>(c->rows, 1);
     P.oob = (int)rows;
