@@ -76,19 +76,31 @@ constexpr float LN2 = 0.69314718055994530942f;
 constexpr long long kAbortQuietCycles = 1LL << 18;
 constexpr int PAIRS = 76;               // 152 SMs
 // warp 0: TMA (Q, bf16 K); 1: QK^T; 2: tensor memory, PV; 3: TMA (bf16 V); from 4 on the softmax groups of four
-// (warp % 4 = lane quarter); of an e4m3 cache eight more load
+// (warp % 4 = lane quarter); of an e4m3 cache eight more load, of a bf16 cache two more look V tiles over
 constexpr int G = 3;                    // softmax groups
 constexpr int SOFT = 4 * G;
 constexpr int FIRST_LOAD = 4 + SOFT;
-constexpr int LOADERS = 8;
+constexpr int LOADERS = 8, SCRUBBERS = 2;
 
 struct Bars {
-    uint64_t q_stage, q_ready, peer_ready, kv_full[4], kv_empty[4], raw[2], raw_free[2], s_full[NB], s_empty[NB];
-    uint64_t x_full[NB], x_free[NB];  // the other CTA's partial scores are here; it has read ours
-    uint64_t p_in[NB], p_full[NB];    // the other CTA's probabilities are here; all are, and the context is ready for them
+    // one arrival
+    uint64_t q_stage, peer_ready, qk_done, o_done, kv_empty[4], raw[2], mask_full[NB], hand[4][NB], s_full[NB];
+    uint64_t x_full[NB], p_in[NB];    // the other CTA's partial scores are here; its probabilities are
+    // a group's four warps
+    uint64_t s_empty[NB], x_free[NB]; // they (x_free: the other CTA's) have read the scores
+    uint64_t p_full[NB];              // all probabilities are here, and the context is ready for them
+    // two
     uint64_t p_free[NB];              // the PV products of both CTAs are done
-    uint64_t hand[4][NB], mask_full[NB], qk_done, o_done;
+    // as start() says
+    uint64_t kv_full[4], raw_free[2], q_ready;
+    static constexpr int ONE = 10 + 8 * NB, FOUR = ONE + 3 * NB, TWO = FOUR + NB, ALL = TWO + 7;
+
+    __device__ __forceinline__ void start(bool kv8, int lane) {
+        for (int i = lane; i < ALL; i += 32)
+            tc::mbar_init(&q_stage + i, i < ONE ? 1 : i < FOUR ? 4 : i < TWO ? 2 : i == ALL - 1 ? SOFT : kv8 ? LOADERS : 1);
+    }
 };
+static_assert(sizeof(Bars) == 8 * (Bars::TWO + 7), "every barrier is set up");
 struct Misc {
     float m_pub[G][HR];           // reference maximum that a group used, for the next tile's group
     float alpha_out[2][HR], alpha_in[2][HR];  // context factors of a tile, of this CTA's rows and of the other's
@@ -108,29 +120,35 @@ static_assert(4 * Q_BOX <= 2 * P_BYTES + 4 * X_BYTES, "the q~ slice is staged in
 constexpr int OUT_LD_F32 = 256 * 4 + 16, OUT_LD_BF16 = 256 * 2 + 16;
 static_assert(ROWS * OUT_LD_F32 <= KV_BYTES, "staged context");
 
-// Sequences in the order of the units (the longest units first).
+// A sequence's units.
+struct SeqUnits {
+    int unit0;       // first unit
+    int q0, T;       // first query row, nodes
+    int first;       // tokens before the tree
+    int at;          // contiguous caches: its first cache row; paged ones: its row of the table
+    int splits;      // ranges of its tokens
+    int part0;       // first partial context of a split sequence
+};
 struct TreeParams {
-    int n_seq;
-    int q0[DSA_MAX_SEQS];        // first query row
-    int T[DSA_MAX_SEQS];         // nodes
-    int kbase[DSA_MAX_SEQS];     // first cache row (contiguous caches)
-    int first[DSA_MAX_SEQS];     // tokens before the tree
-    int seq[DSA_MAX_SEQS];       // the caller's sequence number
-    int unit0[DSA_MAX_SEQS + 1]; // first unit
-    int part0[DSA_MAX_SEQS];     // first partial context of a split sequence
     PageTab pt;
     const uint64_t *mask;
     int words, H;
     int oob;                     // a cache row past the last one
+    int n_seq;
     // softmax_scale log2(e) = +-scale_log2 2^k with scale_log2 in [1/2, 1): the queries carry +-2^k (exact), so that a
     // score keeps clear of fp16's range unless its exponent does.
     float scale_log2;
     uint32_t q_factor;           // +-2^k, twice in bf16
     long long wait_limit;
+    SeqUnits s[DSA_MAX_SEQS];    // in the order of the units (the longest first)
 };
 static_assert(sizeof(TreeParams) + 4 * 128 + 128 <= 32764, "launch parameters");
 
-// One 16-bit pair per word: bf16 Inf and NaN become 0.
+// Two bf16 values a word: bits 15 and 31 say which are Inf or NaN (an exponent of ones carries into the sign's place).
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
+    return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+// Inf and NaN become 0.
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
     if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
     if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
@@ -230,7 +248,7 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b,
 
 template <bool KV8>
 struct Cfg {
-    static constexpr int THREADS = 32 * (FIRST_LOAD + (KV8 ? LOADERS : 0));
+    static constexpr int THREADS = 32 * (FIRST_LOAD + (KV8 ? LOADERS : SCRUBBERS));
 };
 
 template <bool KV8>
@@ -255,19 +273,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
     const int warp = __shfl_sync(FULL, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank(), peer = rank ^ 1u;
 
+    if (warp == 0) {
+        bar->start(KV8, lane);
+        if (lane == 0) {
+            *abort_flag = 0;
+            ms->never = 0;
+        }
+        tc::fence_mbar_init();
+        __syncwarp();
+    }
+    if (warp == 2) {
+        tc::tmem_alloc(&ms->tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+
     // ---- the unit: rows row0 .. of a sequence, tiles t0 .. t0 + n - 1 of its tokens ----
     const int u = (int)(blockIdx.x >> 1);
     int lo = 0, hi = P.n_seq - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (P.unit0[mid] <= u) lo = mid; else hi = mid - 1;
+        if (P.s[mid].unit0 <= u) lo = mid; else hi = mid - 1;
     }
-    const int T = P.T[lo], first = P.first[lo], b = P.seq[lo], kbase = P.kbase[lo];
+    const SeqUnits &me = P.s[lo];
+    const int T = me.T, first = me.first, at = me.at;
     const int nt = (int)(((int64_t)T * P.H + ROWS - 1) / ROWS);
-    const int splits = (P.unit0[lo + 1] - P.unit0[lo]) / nt;
-    const int rem = u - P.unit0[lo], split = rem / nt, rt = nt - 1 - (rem - split * nt);
+    const int splits = me.splits;
+    const int rem = u - me.unit0, split = rem / nt, rt = nt - 1 - (rem - split * nt);
     const int seq_rows = T * P.H;                                  // rows of the sequence
-    const int64_t seq_row0 = (int64_t)P.q0[lo] * P.H;
+    const int64_t seq_row0 = (int64_t)me.q0 * P.H;
     const int lrow = rt * ROWS;                                    // first row of the unit within the sequence
     const int node_lo = lrow / P.H, node_hi = min(T - 1, (lrow + ROWS - 1) / P.H);
     const int tokens = first + (P.mask ? T : node_hi + 1);         // tokens that some row may see
@@ -277,48 +310,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
     const int t0 = split * per;
     const int n = max(0, min((tokens + TK - 1) / TK, t0 + per) - t0);
 
-    if (threadIdx.x == 0) {
-        tc::mbar_init(&bar->q_stage, 1);
-        tc::mbar_init(&bar->q_ready, SOFT);
-        tc::mbar_init(&bar->peer_ready, 1);
-        for (int i = 0; i < 4; ++i) {
-            tc::mbar_init(&bar->kv_full[i], KV8 ? LOADERS : 1);
-            tc::mbar_init(&bar->kv_empty[i], 1);
-        }
-        for (int i = 0; i < NB; ++i) {
-            tc::mbar_init(&bar->s_full[i], 1);
-            tc::mbar_init(&bar->s_empty[i], 4);  // the group's warps have read the scores
-            tc::mbar_init(&bar->x_full[i], 1);   // armed here with what the other CTA sends
-            tc::mbar_init(&bar->x_free[i], 4);   // its warps
-            tc::mbar_init(&bar->p_in[i], 1);
-            tc::mbar_init(&bar->p_full[i], 4);
-            tc::mbar_init(&bar->p_free[i], 2);
-            for (int k = 0; k < 4; ++k) tc::mbar_init(&bar->hand[k][i], 1);
-            tc::mbar_init(&bar->mask_full[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bar->raw[i], 1);
-            tc::mbar_init(&bar->raw_free[i], LOADERS);
-        }
-        tc::mbar_init(&bar->qk_done, 1);
-        tc::mbar_init(&bar->o_done, 1);
-        *abort_flag = 0;
-        ms->never = 0;
-        tc::fence_mbar_init();
+    pdl_wait();  // the set-up so far overlapped the previous kernel; global memory only from here
+    if (threadIdx.x == 0 && n > 0) {  // the q~ slice, on its way before the CTAs have met (staged in the exchange buffers)
+        tc::mbar_arrive_expect_tx(&bar->q_stage, 4 * Q_BOX);
+        for (int j = 0; j < 4; ++j)
+            tc::tma_load_2d(Pb + j * Q_BOX, &tm_q, &bar->q_stage, rank * 256 + j * 64, (int)(seq_row0 + lrow));
     }
-    if (warp == 2) {
-        tc::tmem_alloc(&ms->tmem_slot, 512);
-        tc::tmem_relinquish();
-    }
+    __syncwarp();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     tc::cluster_sync();  // both CTAs' barriers exist before any remote arrive
     const uint32_t tmem = __shfl_sync(FULL, ms->tmem_slot, 0);
-    pdl_wait();  // the set-up above overlapped the previous kernel; global memory only from here
 
     // Cache row of token s, or -1 (behind the last token, or on no page).
-    const auto row_of = [&](int s) -> int64_t { return s < tokens ? cache_row(P.pt, b, kbase, s) : -1; };
+    const auto row_of = [&](int s) -> int64_t { return s < tokens ? cache_row(P.pt, at, at, s) : -1; };
     // Rows of a tile's four runs of 16 tokens, a run a lane: its cache row, -1 behind the last token, or the row past
     // the cache (read as zeros) where there is no page.
     const auto runs_of = [&](int t) {
@@ -341,13 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
     };
 
     if (warp == 0 && n > 0) {
-        // ---------------- TMA: the q~ slice (staged in the exchange buffers), then K of a bf16 cache, or raw codes ----------------
-        if (lane == 0) {
-            tc::mbar_arrive_expect_tx(&bar->q_stage, 4 * Q_BOX);
-            for (int j = 0; j < 4; ++j)
-                tc::tma_load_2d(Pb + j * Q_BOX, &tm_q, &bar->q_stage, rank * 256 + j * 64, (int)(seq_row0 + lrow));
-        }
-        __syncwarp();
+        // ---------------- TMA: K of a bf16 cache, or raw codes ----------------
         // Lane's copy: latents of run k (bf16: all four slabs at once where 64 tokens lie together), or rotary columns.
         const int runs = TK / run, per_run = KV8 || runs == 1 ? 1 : 4, nlat = per_run * runs;
         const bool lat = lane < nlat;
@@ -436,38 +436,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         tc::mbar_wait(&bar->o_done, 0, nv, err, 107);
         tc::mbar_wait(&bar->q_stage, 0, nv, err, 108);  // after an abort nobody else may have waited for it
     } else if (!KV8 && warp == 3 && n > 0) {
-        // ---------------- TMA: V of a bf16 cache; of tiles with hidden tokens Inf and NaN become 0 ----------------
+        // ---------------- TMA: V of a bf16 cache ----------------
         const int runs = TK / run, copies = runs == 1 ? 1 : 4 * runs;
         const int k = runs == 1 ? 0 : lane >> 2, j = runs == 1 ? 0 : lane & 3;
         int rows = runs_of(0);
-        uint32_t turn = 0;  // phase of each stage's `raw`
         for (int t = 0; t < n; ++t) {
             const int st = t & 1;
             if (!__all_sync(FULL, tc::mbar_wait(&bar->kv_empty[2 + st], ((t >> 1) & 1) ^ 1, abort_flag, err, 110, P.wait_limit))) break;
-            const bool scrub = (t0 + t + 1) * TK > safe;
-            uint64_t *full = scrub ? &bar->raw[st] : &bar->kv_full[2 + st];
             const int row = __shfl_sync(FULL, rows, (k * (run / 16)) & 3);
             const bool go = lane < copies && row >= 0;
             const int some = __popc(__ballot_sync(FULL, go));
+            uint64_t *full = (t0 + t + 1) * TK > safe ? &bar->raw[st] : &bar->kv_full[2 + st];
             if (lane == 0) tc::mbar_arrive_expect_tx(full, (uint32_t)(run * some * (runs == 1 ? 512 : 128)));
             __syncwarp();
-            uint8_t *stage = KV + 2 * STAGE + st * VSTAGE;
-            if (go) tc::tma_load_3d(stage + j * SLAB + k * run * 128, &tm_kv, full, 0, row, rank * 4 + j);
+            if (go)
+                tc::tma_load_3d(KV + 2 * STAGE + st * VSTAGE + j * SLAB + k * run * 128, &tm_kv, full, 0, row, rank * 4 + j);
             rows = runs_of(t + 1);
-            if (scrub) {
-                if (!__all_sync(FULL, tc::mbar_wait(full, (turn >> st) & 1u, abort_flag, err, 125, P.wait_limit))) break;
-                turn ^= 1u << st;
-                uint4 *p = (uint4 *)stage + lane;
-#pragma unroll 8
-                for (int i = 0; i < VSTAGE / 512; ++i) {
-                    const uint4 v = p[i * 32];
-                    const uint4 f = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
-                    if ((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) p[i * 32] = f;
-                }
-                tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar->kv_full[2 + st]);
+        }
+    } else if (!KV8 && warp >= FIRST_LOAD && n > 0) {
+        // ---------------- V tiles with hidden tokens, which are the last ones: Inf and NaN become 0 ----------------
+        const int behind = max(0, safe / TK - t0);  // tiles before them
+        for (int t = behind; t < n; ++t) {
+            const int st = t & 1;
+            const bool ok = tc::mbar_wait(&bar->raw[st], ((t - behind) >> 1) & 1, abort_flag, err, 125, P.wait_limit);
+            if (!bar_and<3, 32 * SCRUBBERS>(ok)) break;
+            // 32 tokens a step, half of the slabs a warp, from the first hidden token's on
+            uint8_t *half = KV + 2 * STAGE + st * VSTAGE + (warp - FIRST_LOAD) * 2 * SLAB;
+#pragma unroll 1
+            for (int at = (max(0, safe - (t0 + t) * TK) & ~15) * 128 + lane * 16; at < SLAB; at += 2048) {
+                uint4 v[8];
+                uint32_t bad = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = *(const uint4 *)(half + (i >> 2) * SLAB + at + (i & 3) * 512);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    bad |= not_finite2(v[i].x) | not_finite2(v[i].y) | not_finite2(v[i].z) | not_finite2(v[i].w);
+                if (bad)
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        uint4 *p = (uint4 *)(half + (i >> 2) * SLAB + at + (i & 3) * 512);
+                        *p = make_uint4(finite2(p->x), finite2(p->y), finite2(p->z), finite2(p->w));
+                    }
             }
+            tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
+            bar_and<3, 32 * SCRUBBERS>(true);
+            if (warp == FIRST_LOAD && lane == 0) tc::mbar_arrive(&bar->kv_full[2 + st]);
         }
     } else if (KV8 && warp >= FIRST_LOAD && n > 0) {
         // ---------------- loading warps (e4m3) ----------------
@@ -595,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                 const int left = node + 1 - rel;
                 see = left >= 64 ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1;
             } else if (rel + 64 > 0) {
-                const uint64_t *bits = P.mask + (int64_t)(P.q0[lo] + node) * P.words;
+                const uint64_t *bits = P.mask + (int64_t)(me.q0 + node) * P.words;
                 const int w = rel >> 6, sh = rel & 63;
                 const uint64_t w0 = w < 0 ? ~0ull : w < P.words ? __ldg(bits + w) : 0ull;
                 const uint64_t w1 = w + 1 < P.words ? __ldg(bits + w + 1) : 0ull;
@@ -823,7 +836,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                          : "memory");
             if (lrow + h < seq_rows) {
                 const float row_lse = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * LN2;
-                if (splits > 1) lpart[((int64_t)P.part0[lo] + rem) * ROWS + h] = row_lse;
+                if (splits > 1) lpart[((int64_t)me.part0 + rem) * ROWS + h] = row_lse;
                 else if (lse) lse[seq_row0 + lrow + h] = row_lse;
             }
         }
@@ -836,9 +849,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         }
     }
     tc::cluster_sync();  // both CTAs have every row's sum, and send each other nothing more
-    if (warp >= 4 && warp < 12) {  // two warps a lane quarter
+    if (warp < 16) {  // four warps a lane quarter
         // ---------------- epilogue: normalise, stage rows in the token stages, write whole rows ----------------
-        const int q = warp & 3, g = (warp >> 2) - 1, h = q * 32 + lane;
+        const int q = warp & 3, g = warp >> 2, h = q * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         const float inv = ms->inv[h];
         const bool have = n > 0 && !*abort_flag, whole = splits == 1;
@@ -846,7 +859,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         const int ld = whole ? OUT_LD_BF16 : OUT_LD_F32;
         uint8_t *srow = KV + h * ld;
 #pragma unroll 1
-        for (int cc = g * 4; cc < g * 4 + 4; ++cc) {
+        for (int cc = g * 2; cc < g * 2 + 2; ++cc) {
             float o[32];
             tc::tmem_ld32(lanes + COL_O + cc * 32, o);
             tc::tmem_ld_wait();
@@ -870,14 +883,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                 for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
         }
-        bar_and<2, 256>(true);
-        const int64_t part = whole ? 0 : (int64_t)P.part0[lo] + rem;
-        const int rows = min(ROWS, seq_rows - lrow);
-        for (int i = warp - 4; i < rows; i += 8) {
-            const uint4 *src = (const uint4 *)(KV + i * ld);
-            uint4 *dst = whole ? (uint4 *)(olat + (seq_row0 + lrow + i) * DC + rank * 256)
-                               : (uint4 *)(opart + (part * ROWS + i) * DC + rank * 256);
-            for (int c = lane; c < (whole ? 32 : 64); c += 32) dst[c] = src[c];
+        bar_and<2, 512>(true);
+        const int64_t part = whole ? 0 : (int64_t)me.part0 + rem;
+        uint4 *dst = whole ? (uint4 *)(olat + (seq_row0 + lrow) * DC + rank * 256)
+                           : (uint4 *)(opart + part * ROWS * DC + rank * 256);
+        const int ld_dst = whole ? DC / 8 : DC / 4, two = whole ? 0 : 1;  // 16-byte words of a row; log2 of a lane's
+        const int words = min(ROWS, seq_rows - lrow) << two;
+#pragma unroll 1
+        for (int i0 = warp; i0 < words; i0 += 64) {  // four loads ahead of four stores
+            uint4 v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + e * 16, row = i >> two, c = (i & two) * 32 + lane;
+                if (i < words) v[e] = *((const uint4 *)(KV + row * ld) + c);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + e * 16, row = i >> two, c = (i & two) * 32 + lane;
+                if (i < words) dst[(int64_t)row * ld_dst + c] = v[e];
+            }
         }
         tc::tc_fence_before();
     }
@@ -1044,18 +1068,12 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
     for (int i = 0; i < n; ++i) {
         const int b = order[i];
         const int64_t u = shape_of(bt, H, b).nt * plan.splits[b];
-        P.q0[i] = bt.st.q_off[b];
-        P.T[i] = bt.st.q_off[b + 1] - bt.st.q_off[b];
-        P.kbase[i] = bt.st.k_base[b];
-        P.first[i] = bt.st.start_pos[b];
-        P.seq[i] = b;
-        P.unit0[i] = (int)unit;
-        P.part0[i] = (int)part;
+        P.s[i] = SeqUnits{(int)unit, bt.st.q_off[b], bt.st.q_off[b + 1] - bt.st.q_off[b], bt.st.start_pos[b],
+                          pt.table ? b : bt.st.k_base[b], plan.splits[b], (int)part};
         J.part0[b] = (int)part;
         unit += u;
         if (plan.splits[b] > 1) part += u;
     }
-    P.unit0[n] = (int)unit;
     P.pt = pt;
     P.mask = mask;
     P.words = words;
