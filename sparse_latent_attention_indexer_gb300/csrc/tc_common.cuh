@@ -285,6 +285,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same in two halves; the first one orders nothing but what fences before it do (mbarrier inits: fence_mbar_init).
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Shared::cluster address of the same offset in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_peer(uint32_t local_addr, uint32_t rank) {
     uint32_t r;

@@ -320,7 +320,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    tc::cluster_sync();  // both CTAs' barriers exist before any remote arrive
+    // The CTAs meet: a warp that reaches into the other one first waits until that one's barriers exist; the others pass
+    // here again when their work is done.
+    const bool reaches = warp >= 4 && warp < FIRST_LOAD;
+    tc::cluster_arrive_relaxed();
     const uint32_t tmem = __shfl_sync(FULL, ms->tmem_slot, 0);
 
     // Cache row of token s, or -1 (behind the last token, or on no page).
@@ -587,8 +590,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             // Every warp has read its part of the staging: the buffers may carry scores, here and from the other CTA.
             ok = bar_and<1, 32 * SOFT>(ok);
             if (lane == 0) tc::mbar_arrive(&bar->q_ready);
+            tc::cluster_wait();
             if (threadIdx.x == 4 * 32) tc::mbar_arrive_remote(tc::map_peer(tc::smem_u32(&bar->peer_ready), peer));
             ok = ok && __all_sync(FULL, tc::mbar_wait(&bar->peer_ready, 0, abort_flag, err, 112, P.wait_limit));
+        } else {
+            tc::cluster_wait();
         }
         // A lane's waits only note a failure; the warp stops together at the end of the tile.
         const auto wait = [&](uint64_t *bars, int t, int site) {
@@ -841,6 +847,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             }
         }
     }
+    __syncwarp();
+    if (!reaches) tc::cluster_wait();
     __syncthreads();
     if (*abort_flag) {
         // Copies that nobody waits for any more land within microseconds.
