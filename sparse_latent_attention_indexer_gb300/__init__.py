@@ -533,11 +533,11 @@ def dsa_latent_cache_read(cache: LatentCache, seqs: Seqs, pages: Pages | None = 
     _int32(fn, "pos", pos, seqs.total_q)
     with _launching(dev, stream):
         if c_kv is None:
-            c_kv = cache.kv.new_empty((seqs.total_q, cache.d_c), dtype=dtype)
+            c_kv = torch.empty((seqs.total_q, cache.d_c), dtype=dtype, device=cache.kv.device)
         else:
             _rows_2d(fn, "c_kv", c_kv, cache.d_c, seqs.total_q)
         if k_pe is None:
-            k_pe = cache.kv.new_empty((seqs.total_q, cache.d_r), dtype=c_kv.dtype)
+            k_pe = torch.empty((seqs.total_q, cache.d_r), dtype=c_kv.dtype, device=c_kv.device)
         else:
             _rows_2d(fn, "k_pe", k_pe, cache.d_r, seqs.total_q)
             if k_pe.dtype != c_kv.dtype:
@@ -585,13 +585,14 @@ def dsa_tree_mla_fwd(q_nope, q_pe, cache: LatentCache, W_UK, W_UV, seqs: Seqs, s
     dt = _dt(q_nope)
     lib = _abi.load()
     with _launching(dev, stream):
+        on = q_nope.device
         if out is None:
-            out = q_nope.new_empty((N, H, d_v))
+            out = torch.empty((N, H, d_v), dtype=dtype, device=on)
         if lse is None and want_lse:
-            lse = q_nope.new_empty((N, H), dtype=torch.float32)
+            lse = torch.empty((N, H), dtype=torch.float32, device=on)
         if workspace is None:
             need = lib.dsa_tree_mla_workspace_size(dt, H, d_n, d_r, d_c, d_v, seqs.ref())
-            workspace = q_nope.new_empty(max(need, 256), dtype=torch.uint8)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=on)
         _check(fn, lib.dsa_tree_mla_fwd(
             q_nope.data_ptr(), q_pe.data_ptr() if d_r else None, dt, cache.ref(), W_UK.data_ptr(), W_UV.data_ptr(), H,
             d_n, d_r, d_c, d_v, _addr(tree_mask), words, seqs.ref(), _ref_pages(fn, pages, seqs), softmax_scale,
@@ -621,13 +622,14 @@ class Heads:
                 (which + ".y", self.y), (which + ".y_pe", self.y_pe))
 
 
-def _strides(t):
-    """Row and head stride in elements (the stride of a dimension of one is any number in torch: 0 here)."""
-    if t is None:
-        return 0, 0
-    n, h, _ = t.shape
-    a, b, _ = t.stride()
-    return a if n > 1 else 0, b if h > 1 else 0
+def _head_strides(fn, name, t, N, n, w, dtype):
+    """Row and head stride of a tensor [N, n, w] with contiguous heads (0 where there is one row, or one head)."""
+    if t.shape != (N, n, w) or t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} must be [{N}, {n}, {w}] of {dtype}")
+    a, b, c = t.stride()
+    if w > 1 and c != 1:
+        raise ValueError(f"{fn}: {name} must have contiguous heads")
+    return a if N > 1 else 0, b if n > 1 else 0
 
 
 def dsa_head_norm_rope(q: Heads | None, k: Heads | None, rope_cos, rope_sin, seqs: Seqs, pos=None, rope="pairs",
@@ -673,20 +675,20 @@ def dsa_head_norm_rope(q: Heads | None, k: Heads | None, rope_cos, rope_sin, seq
             for t in (h.gain, h.bias):
                 if t is not None and (t.dtype != torch.float32 or t.shape != (D,) or not t.is_contiguous()):
                     raise ValueError(f"{fn}: gain and bias must be contiguous fp32 [{D}]")
-            given = [("x", x, D, x0.dtype)]
+            strides = _head_strides(fn, "x", x, N, n, D, x0.dtype)
             if y is None:
-                y = x.new_empty((N, n, width), dtype=y_dtype)
+                y = torch.empty((N, n, width), dtype=y_dtype, device=x0.device)
+                strides_y = n * width, width
             else:
-                given.append(("y", y, width, y_dtype))
+                strides_y = _head_strides(fn, "y", y, N, n, width, y_dtype)
+            strides_pe = 0, 0
             if split and pe is None:
-                pe = x.new_empty((N, n, d_r), dtype=y_dtype)
+                pe = torch.empty((N, n, d_r), dtype=y_dtype, device=x0.device)
+                strides_pe = n * d_r, d_r
             elif split:
-                given.append(("y_pe", pe, d_r, y_dtype))
-            for name, t, w, dt in given:
-                if t.shape != (N, n, w) or t.dtype != dt or (w > 1 and t.stride(2) != 1):
-                    raise ValueError(f"{fn}: {name} must be [{N}, {n}, {w}] of {dt} with contiguous heads")
-            st = _abi.dsa_heads(x.data_ptr(), *_strides(x), n, _NORMS[h.norm], _addr(h.gain), _addr(h.bias),
-                                y.data_ptr(), *_strides(y), _addr(pe), *_strides(pe))
+                strides_pe = _head_strides(fn, "y_pe", pe, N, n, d_r, y_dtype)
+            st = _abi.dsa_heads(x.data_ptr(), *strides, n, _NORMS[h.norm], _addr(h.gain), _addr(h.bias), y.data_ptr(),
+                                *strides_y, _addr(pe), *strides_pe)
             structs.append(ctypes.byref(st))
             results.append((y, pe) if split else y)
         _check(fn, _abi.load().dsa_head_norm_rope(
