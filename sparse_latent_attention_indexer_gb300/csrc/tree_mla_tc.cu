@@ -75,6 +75,7 @@ constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr long long kAbortQuietCycles = 1LL << 18;
 constexpr int PAIRS = 76;               // 152 SMs
+constexpr int kMaxSplits = 76;          // of a sequence
 // warp 0: TMA (Q, bf16 K); 1: QK^T; 2: tensor memory, PV; 3: TMA (bf16 V); from 4 on the softmax groups of four
 // (warp % 4 = lane quarter); of an e4m3 cache eight more load, of a bf16 cache two more look V tiles over
 constexpr int G = 3;                    // softmax groups
@@ -930,6 +931,9 @@ struct JoinParams {
     int64_t rows;
 };
 static_assert(sizeof(JoinParams) + 128 <= 32764, "launch parameters");
+// AHEAD loads in flight a warp: eight where sequences are cut often, two where not (more warps fit: 8 sequences of 4 nodes
+// over 1000 tokens in 3 ranges take 34.9 us a call with two, 37.3 with eight; one of 16,000 tokens in 76 ranges 42 and 34).
+template <int AHEAD>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ JoinParams P,
                                                         const float *__restrict__ opart,
                                                         const float *__restrict__ lpart,
@@ -947,12 +951,16 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     const int lr = (int)(rh - (int64_t)P.st.q_off[b] * P.H), rt = lr / ROWS;
     const int64_t p0 = P.part0[b] + (nt - 1 - rt);  // partial of split 0; split s: + s * nt
     const int i = lr - rt * ROWS;
-    float mxl = -INFINITY;
+    // lane s has splits s, s + 32, ..: their weights
+    static_assert(kMaxSplits <= 96, "three splits a lane");
+    float l[3], mxl = -INFINITY;
     bool bad = false;  // a NaN that the row sees
-    for (int s = lane; s < splits; s += 32) {
-        const float l = lpart[(p0 + (int64_t)s * nt) * ROWS + i];
-        bad = bad || l != l;
-        mxl = fmaxf(mxl, l);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int s = k * 32 + lane;
+        l[k] = s < splits ? lpart[(p0 + (int64_t)s * nt) * ROWS + i] : -INFINITY;
+        bad = bad || l[k] != l[k];
+        mxl = fmaxf(mxl, l[k]);
     }
     bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
@@ -960,16 +968,28 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float sum = 0.0f;
     if (mxl != -INFINITY) {
-#pragma unroll 4
-        for (int s = 0; s < splits; ++s) {
-            const int64_t p = (p0 + (int64_t)s * nt) * ROWS + i;
-            const float wgt = expf(lpart[p] - mxl);
-            const float4 x = *((const float4 *)(opart + p * DC + quarter * 128) + lane);
-            sum += wgt;
-            acc.x = fmaf(wgt, x.x, acc.x);
-            acc.y = fmaf(wgt, x.y, acc.y);
-            acc.z = fmaf(wgt, x.z, acc.z);
-            acc.w = fmaf(wgt, x.w, acc.w);
+        const float *x = opart + (p0 * ROWS + i) * DC + quarter * 128 + lane * 4;
+        const int64_t step = (int64_t)nt * ROWS * DC;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const float w = expf(l[k] - mxl);  // 0 behind the last split
+            const int left = splits - k * 32;
+#pragma unroll 1
+            for (int s = 0; s < min(32, left); s += AHEAD, x += AHEAD * step) {
+                float4 v[AHEAD];
+#pragma unroll
+                for (int e = 0; e < AHEAD; ++e)
+                    v[e] = s + e < left ? __ldg((const float4 *)(x + e * step)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int e = 0; e < AHEAD; ++e) {
+                    const float ws = __shfl_sync(0xffffffffu, w, s + e);
+                    sum += ws;
+                    acc.x = fmaf(ws, v[e].x, acc.x);
+                    acc.y = fmaf(ws, v[e].y, acc.y);
+                    acc.z = fmaf(ws, v[e].z, acc.z);
+                    acc.w = fmaf(ws, v[e].w, acc.w);
+                }
+            }
         }
     }
     const float inv = bad ? NAN : sum > 0.0f ? 1.0f / sum : 0.0f;
@@ -993,8 +1013,9 @@ Shape shape_of(const Batch &bt, int H, int b) {
 }
 // One pair of SMs works on a unit at a time, so units come in waves of 76.  A unit costs its tiles and about
 // kUnitCost tiles to start and end.  Of the chunk sizes that fill one, two, .. waves the cheapest is
-// taken; no split at all competes with them.
-constexpr int kUnitCost = 6, kMinChunk = 4, kMaxWaves = 4, kMaxSplits = 76;
+// taken; no split at all competes with them, and saves the join: kJoinCost tiles, and kJoinSplit a split.
+constexpr int kUnitCost = 6, kMinChunk = 2, kMaxWaves = 4;
+constexpr double kJoinCost = 4.5, kJoinSplit = 0.08;
 int split_of(const Shape &s, int chunk) { return std::min(kMaxSplits, (s.tiles + chunk - 1) / chunk); }
 void make_plan(const Batch &bt, int H, Plan &plan) {
     const int B = bt.st.B;
@@ -1027,7 +1048,7 @@ void make_plan(const Batch &bt, int H, Plan &plan) {
             const int mid = (lo + hi) / 2;
             if (units(mid) <= (int64_t)w * PAIRS) hi = mid; else lo = mid + 1;
         }
-        const double c = cost(units(lo), lo);
+        const double c = cost(units(lo), lo) + kJoinCost + kJoinSplit * split_of(Shape{1, longest}, lo);
         if (c < least) {
             least = c;
             best = lo;
@@ -1136,10 +1157,11 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
     note_launch(DSA_KERNEL_TREE_TC);
     if (!plan.parts) return cudaSuccess;
     J.st = bt.st;
-    for (int b = 0; b < B; ++b) J.splits[b] = plan.splits[b];
+    int most = 0;
+    for (int b = 0; b < B; ++b) most = std::max(most, J.splits[b] = plan.splits[b]);
     J.H = H;
     J.rows = (int64_t)N * H;
-    e = launch_pdl(tree_join_kernel, dim3((unsigned)((J.rows * 4 + 7) / 8)), dim3(256), 0, s, J, (const float *)opart,
+    e = launch_pdl(most > 4 ? tree_join_kernel<8> : tree_join_kernel<2>, dim3((unsigned)((J.rows * 4 + 7) / 8)), dim3(256), 0, s, J, (const float *)opart,
                    (const float *)lpart, (__nv_bfloat16 *)olat, lse);
     if (e != cudaSuccess) return e;
     note_launch(DSA_KERNEL_TREE_COMBINE);
