@@ -14,26 +14,35 @@
 // 32c.. of every row and token.  A tile is 64 tokens.
 //   * Each CTA multiplies its columns: a partial score tile (q~ slice resident in
 //     tensor memory as the A operand, so QK^T reads only the tokens from shared
-//     memory).  CTA c finishes rows 64c .. 64c+63: the other CTA sends it its partial
-//     scores of those rows (fp16, 8 KB), it adds its own in
+//     memory).  Of each 32 rows CTA c finishes 16c .. 16c+15: the other CTA sends it
+//     its partial scores of those rows (fp16, 8 KB), it adds its own in
 //     fp32, runs the softmax and sends the probabilities (bf16, 8 KB) back, which both
 //     need for PV.  Nothing is computed twice, and a row's maximum and sum live in
 //     one place.
-//   * Eight softmax warps in two groups that take alternate tiles.  Tensor-memory
-//     lanes are rows, so in each group two warps finish the CTA's own rows (a thread
-//     a row) and two send the other rows' partial scores and then watch for the
-//     probabilities that come back.
-//   * Lazy rescaling: a row's reference maximum moves only when a tile exceeds it by
-//     more than 2^8; the factor travels with the probabilities, and both CTAs rescale
-//     their half of the context.
-//   * Tokens arrive by TMA (two copies a tile where 64 lie together); eight more warps
-//     dequantise e4m3 codes (exact in bf16) from where they landed into the stages.
+//   * Twelve softmax warps in three groups that take the tiles in turn; tensor-memory
+//     lanes are rows, so each of a group's four warps finishes 16 rows of its quarter
+//     and sends the other 16, and all four quarters of the SM share the exponentials.
+//   * Lazy rescaling: a row's reference maximum is a whole number (of powers of two) and
+//     moves only when a tile exceeds it by more than 8; the factor travels with the
+//     probabilities, and both CTAs rescale their half of the context.  A group works
+//     with the reference that it knows and corrects by a power of two (exact) if the
+//     tile before has moved it.
+//   * bf16 tokens arrive by TMA (two copies a tile where 64 lie together) in two stages
+//     as K and once more, from L2, in two as V, so that no operand waits for a softmax;
+//     of an e4m3 cache codes, rotary keys and scales arrive so, and eight more warps
+//     spread the codes (exact in bf16) into three stages that serve K and V.
 //   * A token that some row does not see may hold anything, and 0 x NaN is NaN: in the V
-//     of tiles with hidden tokens Inf and NaN become 0.  Scores of hidden tokens are
-//     replaced after the MMA.
-// Bound by shared memory and by the length of a tile's chain (score, exchange, softmax,
-// exchange) over four stages of tokens: per tile a CTA's MMAs take 1088 cycles and its
-// shared-memory traffic (MMA operands 92 KB, copies 37, scores and probabilities 64) 1.5K.
+//     of tiles with hidden tokens Inf and NaN become 0 (two warps of their own: by the
+//     loader itself 25 short trees took 1.13 ms instead of 0.69).  Scores of hidden tokens
+//     are replaced after the MMA.
+// Roundings: q~, the probabilities and the context to bf16 for the next product, half of a
+// score to fp16 (2^-11, far below q~'s 2^-8 times the scores' spread); maxima, sums and
+// the context's accumulation in fp32.
+// Bound by the length of a tile's chain (score, exchange, softmax, exchange, PV) over two
+// score buffers, which fill the tensor memory beside q~ and the context: a tile's MMAs take
+// 1088 cycles, a tile 1810 (bf16: tensor pipe 61% busy, 32 nodes over up to 32K tokens at
+// 1280 TFLOP/s) or 2750 (e4m3, where the spreading adds 70 KB of shared-memory traffic:
+// 32 x 64K decode at 880 TFLOP/s).  A unit's start and end cost about ten tiles.
 //
 // Waits are bounded; a timeout records its site in the device error word and
 // both CTAs drain and exit.
