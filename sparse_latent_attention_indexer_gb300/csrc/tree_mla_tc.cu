@@ -40,7 +40,7 @@
 // the context's accumulation in fp32.
 // Bound by the length of a tile's chain (score, exchange, softmax, exchange, PV) over two
 // score buffers, which fill the tensor memory beside q~ and the context: a tile's MMAs take
-// 1088 cycles, a tile 1810 (bf16: tensor pipe 61% busy, 32 nodes over up to 32K tokens at
+// 1088 cycles, a tile 1810 (bf16: tensor pipe 61% busy, trees of 32 nodes over up to 12K tokens at
 // 1280 TFLOP/s) or 2750 (e4m3, where the spreading adds 70 KB of shared-memory traffic:
 // 32 x 64K decode at 880 TFLOP/s).  A unit's start and end cost about ten tiles.
 //
