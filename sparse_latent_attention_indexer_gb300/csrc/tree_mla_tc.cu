@@ -38,11 +38,11 @@
 // Roundings: q~, the probabilities and the context to bf16 for the next product, half of a
 // score to fp16 (2^-11, far below q~'s 2^-8 times the scores' spread); maxima, sums and
 // the context's accumulation in fp32.
-// Bound by the length of a tile's chain (score, exchange, softmax, exchange, PV) over two
-// score buffers, which fill the tensor memory beside q~ and the context: a tile's MMAs take
-// 1088 cycles, a tile 1810 (bf16: tensor pipe 61% busy, trees of 32 nodes over up to 12K tokens at
-// 1280 TFLOP/s) or 2750 (e4m3, where the spreading adds 70 KB of shared-memory traffic:
-// 32 x 64K decode at 880 TFLOP/s).  A unit's start and end cost about ten tiles.
+// Bound by shared memory: a bf16 tile moves 219 KB through it (92 MMA operands, 68 tokens by
+// TMA, 59 partial scores and probabilities), 1711 cycles at 128 bytes a cycle of the 1810 that
+// it takes (its MMAs take 1088; trees of 32 nodes over up to 12K tokens run at 1280 TFLOP/s).
+// An e4m3 tile takes 2750: 226 KB (1766 cycles), and three stages whose way from codes to PV is
+// 8K cycles long (32 x 64K decode at 880 TFLOP/s).  A unit's start and end cost about ten tiles.
 //
 // Waits are bounded; a timeout records its site in the device error word and
 // both CTAs drain and exit.
