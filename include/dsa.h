@@ -504,7 +504,8 @@ int dsa_latent_cache_read(const dsa_latent_cache *cache, int d_c, int d_r, const
  * E4M3 with dtype DSA_BF16.
  * Two kernels: tensor cores for bf16 at d_n = 128, d_r = 64, d_c = 512, d_v = 128
  * and any H; a generic one for everything else within the limits of
- * dsa_sparse_mla_fwd (E4M3: d_c a multiple of 128).
+ * dsa_sparse_mla_fwd (E4M3: d_c a multiple of 128).  start_pos[b] + T_b < 2^31 - 256,
+ * sum T * H < 2^31 - 256.
  * All pointers 16-byte aligned (kv_scale too); workspace as in dsa_sparse_mla_fwd, its size
  * depends on the sequences (calls captured in graphs that may run at the same
  * time need workspaces of their own).

@@ -228,6 +228,8 @@ int dsa_tree_mla_fwd(const void *q_nope, const void *q_pe, int dtype, const dsa_
     if (dtype == DSA_F32 ? cache->dtype != DSA_F32 : cache->dtype == DSA_F32) return DSA_ERR_UNSUPPORTED;
     if (!std::isfinite(softmax_scale * 1.4426950408889634f)) return DSA_ERR_INVALID_ARG;  // in powers of two, too
     if ((int64_t)bt.total_q * H >= (int64_t(1) << 31) - 256) return DSA_ERR_UNSUPPORTED;
+    for (int b = 0; b < bt.st.B; ++b)  // tiles end past the last token
+        if (bt.st.start_pos[b] > 0x7fffffff - 256 - (bt.st.q_off[b + 1] - bt.st.q_off[b])) return DSA_ERR_UNSUPPORTED;
     if (bt.total_q == 0) return DSA_OK;
     if (!q_nope || (d_r > 0 && !q_pe) || !W_UK || !W_UV || !out) return DSA_ERR_INVALID_ARG;
     if (!on16(q_nope) || !on16(q_pe) || !on16(W_UK) || !on16(W_UV) || !on16(out) || (uintptr_t)lse % 4 ||

@@ -236,3 +236,11 @@ def test_structures_match_the_header(tmp_path):
         assert got[(st.__name__, "size")] == ctypes.sizeof(st)
         for f, _ in st._fields_:
             assert got[(st.__name__, f)] == getattr(st, f).offset
+
+
+def test_tree_refuses_positions_at_the_end_of_32_bits():
+    """Token numbers are counted in tiles beyond the last one."""
+    end = 2 ** 31 - 1
+    pages = _pages(page_size=1 << 20, n_pages=0, width=1 << 12, ld_table=1 << 12)
+    assert _tree(seqs=_seqs([3], [end], [end - 3]), pages=pages) == DSA_ERR_UNSUPPORTED
+    assert _tree(seqs=_seqs([3], [end], [end - 130]), pages=pages, ws=None) in (DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE)

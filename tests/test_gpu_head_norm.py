@@ -151,3 +151,25 @@ def test_graph_and_side_stream():
     got = dsa.dsa_head_norm_rope(dsa.Heads(xd), None, cd, sd, seqs, pos=pos, split=True, stream=side)[0]
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got[0], out[0]) and torch.equal(got[1], out[1])
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("rope", ["pairs", "halves"])
+@pytest.mark.parametrize("D,d_r", [(64, 64), (128, 64), (192, 64), (256, 128), (512, 64)])
+def test_heads_on_16_but_not_32_bytes(dt, rope, D, d_r):
+    """The same bits whether heads start on 32 bytes or on 16 only, for every number of lanes and vectors a head."""
+    g = torch.Generator().manual_seed(D)
+    T, n = [5, 0, 30], 9
+    seqs = dsa.Seqs([0, 5, 5, 35], [0, 5, 6, 40], [0, 1, 4])
+    cos, sin = (t.cuda() for t in tables(64, d_r))
+    x = torch.randn(35, n, D, generator=g).to(dt).cuda()
+    gain, bias = torch.randn(D, generator=g).cuda(), torch.randn(D, generator=g).cuda()
+    want, _ = dsa.dsa_head_norm_rope(dsa.Heads(x, norm="layer", gain=gain, bias=bias), None, cos, sin, seqs, rope=rope)
+    pad = 16 // x.element_size()
+    wide = torch.full((35, n, D + pad), 9.0, dtype=dt, device="cuda")
+    view = wide[:, :, pad:]
+    view.copy_(x)
+    got, _ = dsa.dsa_head_norm_rope(dsa.Heads(view, norm="layer", gain=gain, bias=bias, y=view), None, cos, sin, seqs, rope=rope)
+    assert torch.equal(got, want) and torch.all(wide[:, :, :pad] == 9)
+    check(want, x.cpu(), "layer", gain.cpu(), bias.cpu(), 1e-6, cos.cpu(), sin.cpu(), [0, 1, 2, 3, 4] + list(range(4, 34)), rope,
+          False, False, dt)

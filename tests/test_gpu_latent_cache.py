@@ -217,3 +217,26 @@ def test_graph_and_side_stream():
     got = dsa.dsa_latent_cache_read(cache, seqs, pages=pages, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got[0], out[0]) and torch.equal(got[1], out[1])
+
+
+@pytest.mark.parametrize("cache_dt", [F32, BF16, U8])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("T", [[9, 4], [3000, 4000]])
+def test_rows_on_16_but_not_32_bytes(cache_dt, dt, T):
+    """The same bytes whether rows start on 32 bytes or on 16 only; few tokens (one a warp) and many (four a warp)."""
+    bt = R.Batch(T, [3, 60], 64, seed=19)
+    x, pe = inputs(bt.N, 512, 64, dt, 20)
+    pad = 16 // x.element_size()
+    got = []
+    for extra in (0, pad):
+        wide = torch.zeros(bt.N, 576 + extra, dtype=dt, device="cuda")[:, extra:]
+        wide[:, :512], wide[:, 512:] = x.cuda(), pe.cuda()
+        kv, p, sc = make_cache(bt.rows, 512, 64, cache_dt, 21)
+        cache = dsa.LatentCache(kv, p, sc)
+        dsa.dsa_latent_cache_write(wide[:, :512], wide[:, 512:], cache, bt.seqs(), pages=bt.pages())
+        dense = torch.full((bt.N, 576 + extra), 7.0, dtype=dt, device="cuda")[:, extra:]
+        dsa.dsa_latent_cache_read(cache, bt.seqs(), pages=bt.pages(), c_kv=dense[:, :512], k_pe=dense[:, 512:])
+        got.append((bits(kv), bits(p), bits(dense.contiguous())))
+    assert all(torch.equal(u, v) for u, v in zip(*got))
+    if cache_dt != U8:
+        assert torch.equal(got[0][2], bits(torch.cat([x, pe], 1).to(cache_dt).to(dt).cuda()))

@@ -184,3 +184,21 @@ def test_waits_that_run_out_are_reported(cache_dt):
     again = c.call()
     assert torch.equal(again[0], out) and torch.equal(again[1], lse)
     assert dsa.dsa_check_device_error() == (_abi.DSA_OK, 0)
+
+
+@pytest.mark.parametrize("cache_dt", [BF16, U8])
+@pytest.mark.parametrize("generic", [False, True])
+def test_bits_of_nodes_that_are_not_there(cache_dt, generic, monkeypatch):
+    """Mask bits from the sequence's last node on, and words that no node needs, change nothing."""
+    if generic:
+        monkeypatch.setenv("DSA_FORCE_GENERIC", "1")
+    c = Case([5, 70, 64], [100, 7, 64], 16, 3, TC, BF16, cache_dt, "tree", seed=31, slack=9)
+    out, lse = c.call()
+    T = [t for t in c.bt.T for _ in range(t)]
+    words = 4
+    rows = [(v | (1 << 64 * words) - (1 << t)) for v, t in zip(c.bits, T)]
+    sign = lambda v: v - (1 << 64) if v >> 63 else v  # noqa: E731
+    mask = torch.tensor([[sign(v >> 64 * w & (1 << 64) - 1) for w in range(words)] for v in rows]).cuda()
+    got = dsa.dsa_tree_mla_fwd(c.q_nope.cuda(), c.q_pe.cuda(), c.cache(), c.W_UK.cuda(), c.W_UV.cuda(), c.bt.seqs(), c.scale,
+                               tree_mask=mask, pages=c.bt.pages())
+    assert torch.equal(got[0], out) and torch.equal(got[1], lse)
