@@ -497,11 +497,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         }
     } else if (KV8 && warp >= FIRST_LOAD && n > 0) {
         // ---------------- loading warps (e4m3) ----------------
-        // Warp w: eight tokens of the tile.  A pass takes four tokens' 128 codes of one block: 16 codes a lane, eight lanes two
-        // tokens' 64 columns of one slab, which are eight different chunks of the swizzled rows.  (Eight unrolled passes with
-        // the codes in registers, loaded a tile ahead, were slower: that loop and the softmax evict one another from the
-        // instruction cache.)
-        const int w = warp - FIRST_LOAD, slab = lane >> 4, chunk = (lane & 3) * 2, sub = (lane >> 2) & 3;
+        // Warp w: eight tokens of the tile.  A pass takes four tokens' 128 codes of one block: 16 codes a lane, eight lanes a
+        // token's 128, which are one row of 128 bytes where they landed and two slabs' 64 columns where they go; the lanes of
+        // the second slab store their second half first, so that eight lanes hit the eight chunks of the swizzled rows.  (Eight
+        // unrolled passes with the codes in registers, loaded a tile ahead, were slower: that loop and the softmax evict one
+        // another from the instruction cache.)
+        const int w = warp - FIRST_LOAD, slab = lane >> 2 & 1, chunk = (lane & 3) * 2, sub = lane >> 3;
         for (int t = 0; t < n; ++t) {
             const int st = t % NSTAGE;
             bool ok = tc::mbar_wait(&bar->raw[t & 1], (t >> 1) & 1, abort_flag, err, 109, P.wait_limit);
@@ -517,7 +518,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             // 2^120 scale is one factor while it stays in bf16's range; scales above 128 go in two.
             const uint8_t *from = raw + (w * 8 + sub) * RAW_LD + slab * 64 + (lane & 3) * 16;
             uint8_t *to = stage + slab * SLAB + (w * 8 + sub) * 128;
-            const auto load = [&](int i) { return *(const uint4 *)(from + (i >> 1) * 4 * RAW_LD + (i & 1) * 128); };
+            const auto load = [&](int i) {
+                const uint4 c = *(const uint4 *)(from + (i >> 1) * 4 * RAW_LD + (i & 1) * 128);
+                return slab ? make_uint4(c.z, c.w, c.x, c.y) : c;
+            };
             const auto pass = [&](int i, const uint4 &c, float up, auto more) {
                 const int tok = (i >> 1) * 4 + sub, x = tok & 7;
                 uint4 o[2];
@@ -529,8 +533,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                         o[e] = make_uint4(mul2(o[e].x, f), mul2(o[e].y, f), mul2(o[e].z, f), mul2(o[e].w, f));
                 }
                 uint8_t *dst = to + (i & 1) * 2 * SLAB + (i >> 1) * 512;
-                *(uint4 *)(dst + ((chunk ^ x) << 4)) = o[0];
-                *(uint4 *)(dst + (((chunk + 1) ^ x) << 4)) = o[1];
+                *(uint4 *)(dst + (((chunk + slab) ^ x) << 4)) = o[0];
+                *(uint4 *)(dst + (((chunk + 1 - slab) ^ x) << 4)) = o[1];
             };
             if (!__any_sync(FULL, sc > 128.0f)) {
                 uint4 c[4];  // the loads first: they could not pass the stores
