@@ -41,8 +41,8 @@
 // Bound by shared memory: a bf16 tile moves 219 KB through it (92 MMA operands, 68 tokens by
 // TMA, 59 partial scores and probabilities), 1711 cycles at 128 bytes a cycle of the 1810 that
 // it takes (its MMAs take 1088; trees of 32 nodes over up to 12K tokens run at 1280 TFLOP/s).
-// An e4m3 tile takes 2700: 226 KB (1766 cycles), and three stages whose way from codes to PV is
-// 8K cycles long (32 x 64K decode at 897 TFLOP/s).  A unit's start and end cost about ten tiles.
+// An e4m3 tile takes 2650: 226 KB (1766 cycles), and three stages whose way from codes to PV is
+// 8K cycles long (32 x 64K decode at 912 TFLOP/s).  A unit's start and end cost about ten tiles.
 //
 // Waits are bounded; a timeout records its site in the device error word and
 // both CTAs drain and exit.
@@ -505,27 +505,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
         const int w = warp - FIRST_LOAD, slab = lane >> 2 & 1, chunk = (lane & 3) * 2, sub = lane >> 3;
         for (int t = 0; t < n; ++t) {
             const int st = t % NSTAGE;
-            bool ok = tc::mbar_wait(&bar->raw[t & 1], (t >> 1) & 1, abort_flag, err, 109, P.wait_limit);
-            ok = tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 110, P.wait_limit) && ok;
-            if (!__all_sync(FULL, ok)) break;
-            uint8_t *stage = KV + st * STAGE;
+            if (!__all_sync(FULL, tc::mbar_wait(&bar->raw[t & 1], (t >> 1) & 1, abort_flag, err, 109, P.wait_limit))) break;
+            // Everything into registers, so that the raw codes' place is free and no load is left when the stage is.
             const uint8_t *raw = KV + NSTAGE * STAGE + (t & 1) * RAW;
+            const uint8_t *from = raw + (w * 8 + sub) * RAW_LD + slab * 64 + (lane & 3) * 16;
+            const int at = w * 512 + lane * 16;
+            uint4 c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = *(const uint4 *)(from + (i >> 1) * 4 * RAW_LD + (i & 1) * 128);
+            const uint4 rot = *(const uint4 *)(raw + TK * RAW_LD + at);
             // scale of token lane / 2 % 8, block lane % 2
             float sc = *(const float *)(raw + RAW_SCALE + (w * 8 + (lane >> 1 & 7)) * 16 + (rank * 2 + (lane & 1)) * 4);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar->raw_free[t & 1]);
+            if (!__all_sync(FULL, tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 110, P.wait_limit))) break;
+            uint8_t *stage = KV + st * STAGE;
             // A hidden token's scale may be anything: past what a finite product allows it counts as 0 (the codes
             // themselves become finite numbers, whatever they are).
             if ((t0 + t + 1) * TK > safe && !(fabsf(sc) <= 0x1p118f)) sc = 0.0f;
             // 2^120 scale is one factor while it stays in bf16's range; scales above 128 go in two.
-            const uint8_t *from = raw + (w * 8 + sub) * RAW_LD + slab * 64 + (lane & 3) * 16;
             uint8_t *to = stage + slab * SLAB + (w * 8 + sub) * 128;
-            const auto load = [&](int i) {
-                const uint4 c = *(const uint4 *)(from + (i >> 1) * 4 * RAW_LD + (i & 1) * 128);
-                return slab ? make_uint4(c.z, c.w, c.x, c.y) : c;
-            };
             const auto pass = [&](int i, const uint4 &c, float up, auto more) {
                 const int tok = (i >> 1) * 4 + sub, x = tok & 7;
                 uint4 o[2];
-                dequant16(c, bf16_pair(__shfl_sync(FULL, up, tok * 2 + (i & 1))), o);
+                dequant16(slab ? make_uint4(c.z, c.w, c.x, c.y) : c, bf16_pair(__shfl_sync(FULL, up, tok * 2 + (i & 1))), o);
                 if constexpr (decltype(more)::value) {
                     const uint32_t f = bf16_pair(__shfl_sync(FULL, sc, tok * 2 + (i & 1)));
 #pragma unroll
@@ -537,24 +540,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                 *(uint4 *)(dst + (((chunk + 1 - slab) ^ x) << 4)) = o[1];
             };
             if (!__any_sync(FULL, sc > 128.0f)) {
-                uint4 c[4];  // the loads first: they could not pass the stores
-#pragma unroll
-                for (int i = 0; i < 4; ++i) c[i] = load(i);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pass(i, c[i], 0x1p120f * sc, std::false_type());
             } else {
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) pass(i, load(i), 0x1p120f, std::true_type());
+                for (int i = 0; i < 4; ++i) {
+                    pass(i, c[0], 0x1p120f, std::true_type());
+                    c[0] = c[1];
+                    c[1] = c[2];
+                    c[2] = c[3];
+                }
             }
             // the rotary columns as they are (both sides in the same 64-byte swizzle)
-            const int at = w * 512 + lane * 16;
-            *(uint4 *)(stage + 4 * SLAB + at) = *(const uint4 *)(raw + TK * RAW_LD + at);
+            *(uint4 *)(stage + 4 * SLAB + at) = rot;
             tc::fence_proxy_async_smem();  // read by the MMAs (async proxy)
             __syncwarp();
-            if (lane == 0) {
-                tc::mbar_arrive(&bar->kv_full[st]);
-                tc::mbar_arrive(&bar->raw_free[t & 1]);
-            }
+            if (lane == 0) tc::mbar_arrive(&bar->kv_full[st]);
         }
     } else if (warp >= 4 && warp < FIRST_LOAD) {
         // ---------------- softmax groups: group g takes tiles g, g + G, .. ----------------
