@@ -41,7 +41,7 @@ struct HeadParams {
     int per_cta;        // warps' items that a CTA of the vector path takes
     int D, d_r, at;     // at: first rotary dim
     int halves, n_pos, wide;  // wide: every row starts on 32 bytes
-    float eps;
+    float eps, inv_D;
 };
 static_assert(sizeof(HeadParams) + 256 <= 32764, "launch parameters");
 
@@ -129,7 +129,7 @@ constexpr int CTA = 128;
 
 // LANES of a head, each with VPT vectors of 8 values (D <= 8 * LANES * VPT).
 template <typename TX, typename TY, int LANES, int VPT, bool HALVES>
-__global__ void __launch_bounds__(CTA, VPT * sizeof(Vec8<TX>) <= 64 ? 7 : 4) head_norm_kernel(const __grid_constant__ HeadParams P) {
+__global__ void __launch_bounds__(CTA, VPT * sizeof(Vec8<TX>) <= 32 ? 9 : VPT * sizeof(Vec8<TX>) <= 64 ? 7 : 4) head_norm_kernel(const __grid_constant__ HeadParams P) {
     __shared__ __align__(16) float turn[2][MAX_D / 2];  // cos, sin of the row's position
     __shared__ __align__(16) float aff[2][2 * MAX_D];   // q's and k's gains and biases
     constexpr int PACK = 32 / LANES, WARPS = CTA / 32;  // heads of a warp
@@ -181,17 +181,17 @@ __global__ void __launch_bounds__(CTA, VPT * sizeof(Vec8<TX>) <= 64 ? 7 : 4) hea
                 for (int j = 0; j < VPT; ++j)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) mu += v[j][e];
-                mu = group_sum<LANES>(mu) / (float)P.D;
+                mu = group_sum<LANES>(mu) * P.inv_D;
 #pragma unroll
                 for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[j][e] = (j * LANES + sub) * 8 < P.D ? v[j][e] - mu : 0.0f;
+                    for (int e = 0; e < 8; ++e) v[j][e] -= (j * LANES + sub) * 8 < P.D ? mu : 0.0f;
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s = fmaf(v[j][e], v[j][e], s);
-            const float inv = rsqrtf(group_sum<LANES>(s) / (float)P.D + P.eps);
+            const float inv = rsqrtf(fmaf(group_sum<LANES>(s), P.inv_D, P.eps));
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int d = (j * LANES + sub) * 8;
@@ -439,6 +439,7 @@ extern "C" int dsa_head_norm_rope(const dsa_heads *q, const dsa_heads *k, int x_
     P.n_pos = n_pos;
     P.wide = wide;
     P.eps = eps;
+    P.inv_D = 1.0f / (float)D;
     const cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (x_dtype == DSA_F32)
