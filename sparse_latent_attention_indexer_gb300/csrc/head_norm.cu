@@ -447,6 +447,7 @@ extern "C" int dsa_head_norm_rope(const dsa_heads *q, const dsa_heads *k, int x_
     else
         e = y_dtype == DSA_F32 ? launch_heads<__nv_bfloat16, float>(P, vec, s)
                                : launch_heads<__nv_bfloat16, __nv_bfloat16>(P, vec, s);
+    if (e != cudaSuccess) return fail_cuda(e);
     note_launch(DSA_KERNEL_HEAD_NORM);
-    return e == cudaSuccess ? DSA_OK : fail_cuda(e);
+    return DSA_OK;
 }

@@ -438,8 +438,9 @@ int dsa_latent_cache_write(const void *c_kv, int64_t ld_c, const void *k_pe, int
         return launch_write<TX, float>(P, c_kv, k_pe, cache, vec, vec_pe, s);
     };
     e = x_dtype == DSA_F32 ? go(float()) : go(__nv_bfloat16());
+    if (e != cudaSuccess) return fail_cuda(e);
     note_launch(DSA_KERNEL_CACHE_WRITE);
-    return e == cudaSuccess ? DSA_OK : fail_cuda(e);
+    return DSA_OK;
 }
 
 int dsa_latent_cache_read(const dsa_latent_cache *cache, int d_c, int d_r, const dsa_seqs *seqs, const dsa_pages *pages,
@@ -460,8 +461,9 @@ int dsa_latent_cache_read(const dsa_latent_cache *cache, int d_c, int d_r, const
         return launch_read<float, TO>(P, pos, cache, c_kv, k_pe, vec, vec_pe, s);
     };
     e = out_dtype == DSA_F32 ? go(float()) : go(__nv_bfloat16());
+    if (e != cudaSuccess) return fail_cuda(e);
     note_launch(DSA_KERNEL_CACHE_READ);
-    return e == cudaSuccess ? DSA_OK : fail_cuda(e);
+    return DSA_OK;
 }
 
 }  // extern "C"

@@ -174,7 +174,7 @@ cudaError_t launch_tree_simt(const float *qt, const void *q_pe, int dtype, const
     if (dtype == DSA_F32) e = tree_simt_typed<float, float>(P, qt, q_pe, c, N, olat, lse, s);
     else if (c->dtype == DSA_E4M3) e = tree_simt_typed<__nv_bfloat16, uint8_t>(P, qt, q_pe, c, N, olat, lse, s);
     else e = tree_simt_typed<__nv_bfloat16, __nv_bfloat16>(P, qt, q_pe, c, N, olat, lse, s);
-    note_launch(DSA_KERNEL_TREE_SIMT);
+    if (e == cudaSuccess) note_launch(DSA_KERNEL_TREE_SIMT);
     return e;
 }
 
