@@ -12,7 +12,7 @@
 // and the gains and biases are fetched once, into shared memory.  Eight lanes take a head
 // (sixteen above 256 dims), one to four vectors of eight values each, so a norm costs
 // three shuffles; the next heads are on their way while these are turned and stored:
-// 4096 rows of 129 heads of 192 in bf16 take 74 us, 5501 of 65 heads of 128 in fp32 67 us
+// 4096 rows of 129 heads of 192 in bf16 take 74 us, 5504 of 65 heads of 128 in fp32 66 us
 // (0.81 of the measured copy rate; one warp a head took 165 and 92).
 // A pair of the "pairs" order lies in one vector; in the "halves" order its other value is
 // 1, 2 or 4 lanes (8: one vector) away (rotary parts of 16, 32, 64 or 128 at a multiple of
