@@ -539,7 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                 *(uint4 *)(dst + (((chunk + slab) ^ x) << 4)) = o[0];
                 *(uint4 *)(dst + (((chunk + 1 - slab) ^ x) << 4)) = o[1];
             };
-            if (!__any_sync(FULL, sc > 128.0f)) {
+            if (!__any_sync(FULL, fabsf(sc) > 128.0f)) {  // (a scale that nobody sees may be negative)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pass(i, c[i], 0x1p120f * sc, std::false_type());
             } else {

@@ -41,7 +41,7 @@ def test_block_scales(e):
     c.check(out, lse)
 
 
-@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, 2.0 ** 127])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, 2.0 ** 127, -2.0 ** 20, -1e30, 1e30, -2.0 ** -140])
 @pytest.mark.parametrize("masks", ["tree", "chain", "odd"])
 def test_hidden_scales(bad, masks):
     """Any scale beside any code in rows that nobody sees, or that only some rows do not see."""
