@@ -306,6 +306,12 @@ __device__ __forceinline__ void bulk_copy_to_peer(uint32_t remote_dst, const voi
         "r"(smem_u32(src)), "r"(bytes), "r"(remote_bar)
         : "memory");
 }
+// 16 bytes from registers into another CTA's shared memory (16-byte aligned), counted on that CTA's mbarrier.
+__device__ __forceinline__ void st_async16(uint32_t remote_dst, float a, float b, float c, float d, uint32_t remote_bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(remote_dst),
+                 "f"(a), "f"(b), "f"(c), "f"(d), "r"(remote_bar)
+                 : "memory");
+}
 // Arrive on a barrier in another CTA of the cluster with the instruction's default semantics
 // (release at CTA scope): orders this thread's earlier accesses to its own CTA's shared memory.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t remote_bar) {

@@ -15,10 +15,11 @@
 //   * Each CTA multiplies its columns: a partial score tile (q~ slice resident in
 //     tensor memory as the A operand, so QK^T reads only the tokens from shared
 //     memory).  Of each 32 rows CTA c finishes 16c .. 16c+15: the other CTA sends it
-//     its partial scores of those rows (fp16, 8 KB), it adds its own in
-//     fp32, runs the softmax and sends the probabilities (bf16, 8 KB) back, which both
+//     its partial scores of those rows (fp32, 16 KB, from registers), it adds its own,
+//     runs the softmax and sends the probabilities (bf16, 8 KB) back, which both
 //     need for PV.  Nothing is computed twice, and a row's maximum and sum live in
-//     one place.
+//     one place.  The halves cross in fp32: a rounding would be relative to the half,
+//     and what all tokens of a half share cancels in the softmax only if it is exact.
 //   * Twelve softmax warps in three groups that take the tiles in turn; tensor-memory
 //     lanes are rows, so each of a group's four warps finishes 16 rows of its quarter
 //     and sends the other 16, and all four quarters of the SM share the exponentials.
@@ -35,14 +36,13 @@
 //     of tiles with hidden tokens Inf and NaN become 0 (two warps of their own: by the
 //     loader itself 25 short trees took 1.13 ms instead of 0.69).  Scores of hidden tokens
 //     are replaced after the MMA.
-// Roundings: q~, the probabilities and the context to bf16 for the next product, half of a
-// score to fp16 (2^-11, far below q~'s 2^-8 times the scores' spread); maxima, sums and
-// the context's accumulation in fp32.
+// Roundings: q~, the probabilities and the context to bf16, as operands of the next product (as
+// in the sparse attention); scores, maxima, sums and the context's accumulation in fp32.
 // Bound by shared memory: a bf16 tile moves 219 KB through it (92 MMA operands, 68 tokens by
-// TMA, 59 partial scores and probabilities), 1711 cycles at 128 bytes a cycle of the 1810 that
-// it takes (its MMAs take 1088; trees of 32 nodes over up to 12K tokens run at 1280 TFLOP/s).
-// An e4m3 tile takes 2650: 226 KB (1766 cycles), and three stages whose way from codes to PV is
-// 8K cycles long (32 x 64K decode at 912 TFLOP/s).  A unit's start and end cost about ten tiles.
+// TMA, 59 partial scores and probabilities), 1711 cycles at 128 bytes a cycle of the 2010 that
+// it takes (its MMAs take 1088; trees of 32 nodes over up to 12K tokens run at 1150 TFLOP/s; with the
+// halves rounded to fp16 1810 and 1270).  An e4m3 tile takes 2810: 226 KB (1766 cycles), and three
+// stages whose way from codes to PV is 8K cycles long (32 x 64K decode at 859 TFLOP/s).  A unit's start and end cost about ten tiles.
 //
 // Waits are bounded; a timeout records its site in the device error word and
 // both CTAs drain and exit.
@@ -73,7 +73,7 @@ constexpr int NSTAGE = 3;
 constexpr int RAW_LD = 256, RAW_SCALE = TK * RAW_LD + ROPE, RAW = RAW_SCALE + TK * 16;
 constexpr int KV_BYTES = std::max(2 * STAGE + 2 * VSTAGE, NSTAGE * STAGE + 2 * RAW);
 constexpr int P_BYTES = ROWS * TK * 2;  // probabilities of all rows
-constexpr int X_BYTES = HR * TK * 2;    // fp16 partial scores of half of the rows
+constexpr int X_BYTES = HR * TK * 4;    // fp32 partial scores of half of the rows
 constexpr int Q_BOX = ROWS * 128;       // 128 rows x 64 columns of q~ (staged in the exchange buffers)
 constexpr int QR_BYTES = ROWS * 64;     // rotary slice of the queries, 64-byte swizzle
 constexpr int NB = 6;                   // barriers of a kind: tile t uses number t % 6, which belongs to one group and one buffer
@@ -123,9 +123,9 @@ struct Misc {
 struct RowSums {                      // in the exchange buffers, at the end
     float sum[G][HR], ref[G][HR];     // a group's share of the row sum and its reference
 };
-constexpr int SMEM = 1024 + KV_BYTES + 2 * P_BYTES + 4 * X_BYTES + QR_BYTES + (int)sizeof(Misc);
+constexpr int SMEM = 1024 + KV_BYTES + 2 * P_BYTES + 2 * X_BYTES + QR_BYTES + (int)sizeof(Misc);
 static_assert(SMEM <= 232448, "shared memory per CTA");
-static_assert(4 * Q_BOX <= 2 * P_BYTES + 4 * X_BYTES, "the q~ slice is staged in the exchange buffers");
+static_assert(4 * Q_BOX <= 2 * P_BYTES + 2 * X_BYTES, "the q~ slice is staged in the exchange buffers");
 // The epilogue stages a CTA's 256 columns, rows 16 bytes apart from a power of two, in the token stages.
 constexpr int OUT_LD_F32 = 256 * 4 + 16, OUT_LD_BF16 = 256 * 2 + 16;
 static_assert(ROWS * OUT_LD_F32 <= KV_BYTES, "staged context");
@@ -145,8 +145,8 @@ struct TreeParams {
     int words, H;
     int oob;                     // a cache row past the last one
     int n_seq;
-    // softmax_scale log2(e) = +-scale_log2 2^k with scale_log2 in [1/2, 1): the queries carry +-2^k (exact), so that a
-    // score keeps clear of fp16's range unless its exponent does.
+    // softmax_scale log2(e) = +-scale_log2 2^k with scale_log2 in [1/2, 1): the queries carry +-2^k (exact), so that the
+    // largest product is the largest score, and products stay in fp32's range where scores do.
     float scale_log2;
     uint32_t q_factor;           // +-2^k, twice in bf16
     long long wait_limit;
@@ -272,8 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
     uint8_t *KV = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *Pb = KV + KV_BYTES;   // [t % 2] probabilities: rows x 64 tokens, 128-byte swizzle
     uint8_t *X = Pb + 2 * P_BYTES;       // [t % 2] the other CTA's partial scores of this CTA's rows
-    uint8_t *Y = X + 2 * X_BYTES;        // [t % 2] this CTA's partial scores of the other's rows, sent from here
-    uint8_t *QR = Y + 2 * X_BYTES;       // rotary slice of the queries
+    uint8_t *QR = X + 2 * X_BYTES;       // rotary slice of the queries
     Misc *ms = (Misc *)(QR + QR_BYTES);
     Bars *bar = &ms->bar;
     volatile int *abort_flag = (volatile int *)&ms->abort_flag, *nv = (volatile int *)&ms->never;
@@ -643,10 +642,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
 #pragma unroll 1
         for (int t = g; ok && t < n; t += G) {
             const int buf = t & 1;
-            uint8_t *Xw = X + buf * X_BYTES + q * 2048, *Yw = Y + buf * X_BYTES + q * 2048, *Pt = Pb + buf * P_BYTES;
+            uint8_t *Xw = X + buf * X_BYTES + q * 4096 + lane * 16, *Pt = Pb + buf * P_BYTES;
             if (lane == 0 && q == 0) {
                 tc::mbar_arrive_expect_tx(&bar->x_full[t % NB], X_BYTES);
-                tc::mbar_arrive_expect_tx(&bar->p_in[t % NB], X_BYTES + HR * 4);
+                tc::mbar_arrive_expect_tx(&bar->p_in[t % NB], P_BYTES / 2 + HR * 4);
             }
             uint64_t see_a = ~0ull, see_b = ~0ull;
             if ((t0 + t + 1) * TK > safe) {
@@ -659,8 +658,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
                 see_a &= m;
                 see_b &= m;
             }
-            // --- the other CTA's rows: partial scores in fp16, in this layout (the receiving thread has the same); the
-            // buffers are free once the other CTA has read tile t-2 ---
+            // --- the other CTA's rows: partial scores in this layout (the receiving thread has the same); the buffer there
+            // is free once the other CTA has read tile t-2 ---
             if (t >= 2) wait(bar->x_free, t - 2, 114);
             wait(bar->s_full, t, 115);
             __syncwarp();
@@ -669,19 +668,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             {
                 tmem_ld_16x64(other_lanes + COL_S + buf * TK, v);
                 tc::tmem_ld_wait();
+                const uint32_t to = tc::map_peer(tc::smem_u32(Xw), peer);
+                const uint32_t there = tc::map_peer(tc::smem_u32(&bar->x_full[t % NB]), peer);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *(uint4 *)(Yw + i * 512 + lane * 16) =
-                        make_uint4(tc::f16x2_satfinite(v[8 * i], v[8 * i + 1]), tc::f16x2_satfinite(v[8 * i + 2], v[8 * i + 3]),
-                                   tc::f16x2_satfinite(v[8 * i + 4], v[8 * i + 5]),
-                                   tc::f16x2_satfinite(v[8 * i + 6], v[8 * i + 7]));
+                for (int i = 0; i < 8; ++i)
+                    tc::st_async16(to + i * 512, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], there);
             }
-            tc::fence_proxy_async_smem();  // read by the copy (async proxy)
-            __syncwarp();
-            if (lane == 0)
-                tc::bulk_copy_to_peer(tc::map_peer(tc::smem_u32(Xw), peer), Yw, 2048,
-                                      tc::map_peer(tc::smem_u32(&bar->x_full[t % NB]), peer));
-            // --- this CTA's rows: its own half in fp32, and the other one's ---
+            // --- this CTA's rows: its own half and the other one's ---
             tmem_ld_16x64(own_lanes + COL_S + buf * TK, v);
             tc::tmem_ld_wait();
             tc::tc_fence_before();
@@ -689,14 +682,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             if (lane == 0) tc::mbar_arrive(&bar->s_empty[t % NB]);
             wait(bar->x_full, t, 116);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 x = *(const uint4 *)(Xw + i * 512 + lane * 16);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[8 * i + 2 * e] = tc::add_f16_f32((uint16_t)(xs[e] & 0xffffu), v[8 * i + 2 * e]);
-                    v[8 * i + 2 * e + 1] = tc::add_f16_f32((uint16_t)(xs[e] >> 16), v[8 * i + 2 * e + 1]);
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float4 x = *(const float4 *)(Xw + i * 512);
+                v[4 * i] += x.x;
+                v[4 * i + 1] += x.y;
+                v[4 * i + 2] += x.z;
+                v[4 * i + 3] += x.w;
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(tc::smem_u32(&bar->x_free[t % NB]), peer));
