@@ -514,15 +514,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             for (int i = 0; i < 4; ++i) c[i] = *(const uint4 *)(from + (i >> 1) * 4 * RAW_LD + (i & 1) * 128);
             const uint4 rot = *(const uint4 *)(raw + TK * RAW_LD + at);
             // scale of token lane / 2 % 8, block lane % 2
-            float sc = *(const float *)(raw + RAW_SCALE + (w * 8 + (lane >> 1 & 7)) * 16 + (rank * 2 + (lane & 1)) * 4);
+            const float sc = *(const float *)(raw + RAW_SCALE + (w * 8 + (lane >> 1 & 7)) * 16 + (rank * 2 + (lane & 1)) * 4);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bar->raw_free[t & 1]);
             if (!__all_sync(FULL, tc::mbar_wait(&bar->kv_empty[st], ((t / NSTAGE) & 1) ^ 1, abort_flag, err, 110, P.wait_limit))) break;
             uint8_t *stage = KV + st * STAGE;
-            // A hidden token's scale may be anything: past what a finite product allows it counts as 0 (the codes
-            // themselves become finite numbers, whatever they are).
-            if ((t0 + t + 1) * TK > safe && !(fabsf(sc) <= 0x1p118f)) sc = 0.0f;
-            // 2^120 scale is one factor while it stays in bf16's range; scales above 128 go in two.
+            // 2^120 scale is one factor while it stays in bf16's range; scales above 128 go in two.  A hidden token's scale
+            // may be anything (the codes themselves become finite numbers, whatever they are): where there may be such
+            // tokens, products that are not finite become 0.
+            const bool hidden = (t0 + t + 1) * TK > safe;
             uint8_t *to = stage + slab * SLAB + (w * 8 + sub) * 128;
             const auto pass = [&](int i, const uint4 &c, float up, auto more) {
                 const int tok = (i >> 1) * 4 + sub, x = tok & 7;
@@ -533,12 +533,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         o[e] = make_uint4(mul2(o[e].x, f), mul2(o[e].y, f), mul2(o[e].z, f), mul2(o[e].w, f));
+                    if (hidden)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            o[e] = make_uint4(finite2(o[e].x), finite2(o[e].y), finite2(o[e].z), finite2(o[e].w));
                 }
                 uint8_t *dst = to + (i & 1) * 2 * SLAB + (i >> 1) * 512;
                 *(uint4 *)(dst + (((chunk + slab) ^ x) << 4)) = o[0];
                 *(uint4 *)(dst + (((chunk + 1 - slab) ^ x) << 4)) = o[1];
             };
-            if (!__any_sync(FULL, fabsf(sc) > 128.0f)) {  // (a scale that nobody sees may be negative)
+            if (__all_sync(FULL, fabsf(sc) <= 128.0f)) {  // (a scale that nobody sees may be negative, or NaN)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pass(i, c[i], 0x1p120f * sc, std::false_type());
             } else {
