@@ -578,6 +578,8 @@ def dsa_tree_mla_fwd(q_nope, q_pe, cache: LatentCache, W_UK, W_UV, seqs: Seqs, s
                 not tree_mask.is_contiguous():
             raise ValueError(f"{fn}: tree_mask must be contiguous int64 or uint64 [{N}, words]")
         words = tree_mask.shape[1]
+        if words == 0 and N > 0:  # its address would be NULL, which means a chain
+            raise ValueError(f"{fn}: tree_mask has no words for {N} rows")
     if lse is not None and (lse.shape != (N, H) or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError(f"{fn}: lse must be contiguous fp32 [{N}, {H}]")
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):

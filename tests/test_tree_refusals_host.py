@@ -1,0 +1,17 @@
+"""CPU-only checks of calls of the cache, tree-attention and head-norm entry points that are refused, and of the
+batch description (see test_cache_tree_host for the others)."""
+import pytest
+import torch
+
+import sparse_latent_attention_indexer_gb300 as dsa
+
+
+def test_a_mask_without_words_is_no_chain(monkeypatch):
+    """The address of an empty tensor is NULL, which the library takes for a chain: the binding refuses it."""
+    monkeypatch.setattr(dsa, "_on_one_device", lambda fn, tensors: 0)  # host tensors stand in: nothing is launched
+    t = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    cache = dsa.LatentCache(t(8, 512), t(8, 64))
+    seqs = dsa.Seqs([0, 2], [0, 8], [6])
+    with pytest.raises(ValueError, match="no words"):
+        dsa.dsa_tree_mla_fwd(t(2, 4, 128), t(2, 4, 64), cache, t(4, 128, 512), t(4, 512, 128), seqs, 0.1,
+                             tree_mask=torch.zeros(2, 0, dtype=torch.int64))
