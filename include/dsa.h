@@ -467,7 +467,7 @@ typedef struct dsa_latent_cache {
  * overlap the cache.  Tokens that share a row (two sequences with one page)
  * leave that row unspecified.
  * Errors: DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED (d_c > 1024, d_r > 128, E4M3
- * with d_c not a multiple of 128), DSA_ERR_CUDA. */
+ * with d_c not a multiple of 128, sum T not below 2^31 - 1024), DSA_ERR_CUDA. */
 int dsa_latent_cache_write(const void *c_kv, int64_t ld_c, const void *k_pe, int64_t ld_x, int x_dtype, int d_c, int d_r,
                            const dsa_latent_cache *cache, const dsa_seqs *seqs, const dsa_pages *pages, void *stream);
 

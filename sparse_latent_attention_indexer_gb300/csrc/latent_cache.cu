@@ -364,6 +364,7 @@ int check_move(int dense_dtype, int d_c, int d_r, const dsa_latent_cache *cache,
     if ((rc = build_batch(seqs, bt))) return rc;
     if ((rc = check_pages(pages, cache, bt, whole, P.pt))) return rc;
     if (ld_c < d_c || (d_r > 0 && ld_x < d_r)) return DSA_ERR_INVALID_ARG;
+    if (bt.total_q >= 0x7fffffff - 1024) return DSA_ERR_UNSUPPORTED;  // rows are counted in 32 bits, up to a few warps past the last one
     P.st = bt.st;
     P.n = bt.total_q;
     if (P.n == 0) return DSA_OK;

@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import sparse_latent_attention_indexer_gb300 as dsa
+from sparse_latent_attention_indexer_gb300._abi import DSA_ERR_UNSUPPORTED
+from tests.test_cache_tree_host import _pages, _read, _seqs, _write
 
 
 def test_a_mask_without_words_is_no_chain(monkeypatch):
@@ -15,3 +17,13 @@ def test_a_mask_without_words_is_no_chain(monkeypatch):
     with pytest.raises(ValueError, match="no words"):
         dsa.dsa_tree_mla_fwd(t(2, 4, 128), t(2, 4, 64), cache, t(4, 128, 512), t(4, 512, 128), seqs, 0.1,
                              tree_mask=torch.zeros(2, 0, dtype=torch.int64))
+
+
+def test_rows_moved_at_the_end_of_32_bits():
+    """Sequences that share their pages may have more rows together than the cache."""
+    S = 2 ** 30 - 1
+    seqs = _seqs([S, S], [S, S], [0, 0])
+    pages = _pages(page_size=1 << 20, n_pages=0, width=1 << 11, ld_table=1 << 11)
+    for call in (_write, _read):
+        assert call(seqs=seqs, pages=pages) == DSA_ERR_UNSUPPORTED
+    assert dsa.last_launch_count() == 0
