@@ -551,7 +551,7 @@ typedef struct dsa_heads {
  * outputs overlap neither inputs nor each other.
  * Errors: DSA_ERR_INVALID_ARG (odd d_r, d_r > D, a position that start_pos gives
  * outside the tables, y_pe with d_r = 0), DSA_ERR_UNSUPPORTED (D > 512, dtype,
- * norm or rope of another kind), DSA_ERR_CUDA. */
+ * norm or rope of another kind, sum T or the heads of q and k together not below 2^31 - 1024), DSA_ERR_CUDA. */
 int dsa_head_norm_rope(const dsa_heads *q, const dsa_heads *k, int x_dtype, int y_dtype, int D, int d_r, int rope_first,
                        int rope, float eps, const float *rope_cos, const float *rope_sin, int n_pos,
                        const int32_t *pos, const dsa_seqs *seqs, void *stream);

@@ -414,6 +414,8 @@ extern "C" int dsa_head_norm_rope(const dsa_heads *q, const dsa_heads *k, int x_
               (!h.y_pe || on(h.y_pe, h.ld_pe, h.hd_pe, y_dtype, 16)) && (uintptr_t)h.gain % 16 == 0 &&
               (uintptr_t)h.bias % 16 == 0;
     }
+    // heads and rows are counted in 32 bits, up to a few warps past the last one
+    if ((int64_t)P.t[0].n + P.t[1].n >= (int64_t(1) << 31) - 1024 || bt.total_q >= 0x7fffffff - 1024) return DSA_ERR_UNSUPPORTED;
     P.rows = (int64_t)bt.total_q * ((int64_t)P.t[0].n + P.t[1].n);
     if (P.rows == 0) return DSA_OK;
     if (d_r > 0) {

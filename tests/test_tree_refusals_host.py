@@ -5,7 +5,7 @@ import torch
 
 import sparse_latent_attention_indexer_gb300 as dsa
 from sparse_latent_attention_indexer_gb300._abi import DSA_ERR_UNSUPPORTED
-from tests.test_cache_tree_host import _pages, _read, _seqs, _write
+from tests.test_cache_tree_host import _heads, _norm, _pages, _read, _seqs, _write
 
 
 def test_a_mask_without_words_is_no_chain(monkeypatch):
@@ -26,4 +26,21 @@ def test_rows_moved_at_the_end_of_32_bits():
     pages = _pages(page_size=1 << 20, n_pages=0, width=1 << 11, ld_table=1 << 11)
     for call in (_write, _read):
         assert call(seqs=seqs, pages=pages) == DSA_ERR_UNSUPPORTED
+    assert dsa.last_launch_count() == 0
+
+
+@pytest.mark.parametrize("q,k", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 30, 2 ** 30), (2 ** 31 - 1024, 0),
+                                 (1, 2 ** 31 - 1025)])
+@pytest.mark.parametrize("D,d_r", [(128, 64), (8, 0), (7, 0), (512, 64)])
+def test_head_counts_at_the_end_of_32_bits(q, k, D, d_r):
+    """The heads of q and k together are counted in 32 bits: past them the call is refused, whatever the kernel.  (Heads
+    of eight bf16 values would fit the GPU.)"""
+    over = dict(ld_x=D * (1 << 31), ld_y=D * (1 << 31), hd_x=D, hd_y=D)
+    assert _norm(q=_heads(n_heads=q, **over), k=_heads(n_heads=k, **over), D=D, d_r=d_r) == DSA_ERR_UNSUPPORTED
+    assert dsa.last_launch_count() == 0
+
+
+def test_rows_normed_at_the_end_of_32_bits():
+    S = 2 ** 30 - 1
+    assert _norm(q=_heads(n_heads=1), seqs=_seqs([S, S], [S, S], [0, 0]), n_pos=2 ** 30) == DSA_ERR_UNSUPPORTED
     assert dsa.last_launch_count() == 0
