@@ -1102,7 +1102,7 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
         order[n++] = b;
         per[b] = (shape_of(bt, H, b).tiles + plan.splits[b] - 1) / plan.splits[b];
     }
-    std::stable_sort(order, order + n, [&](int x, int y) { return per[x] > per[y]; });
+    std::sort(order, order + n, [&](int x, int y) { return per[x] != per[y] ? per[x] > per[y] : x < y; });  // (a stable sort would allocate)
     P.n_seq = n;
     int64_t unit = 0, part = 0;
     for (int i = 0; i < n; ++i) {

@@ -1,5 +1,9 @@
 """CPU-only checks of calls of the cache, tree-attention and head-norm entry points that are refused, and of the
 batch description (see test_cache_tree_host for the others)."""
+import os
+import shutil
+import subprocess
+
 import pytest
 import torch
 
@@ -44,3 +48,16 @@ def test_rows_normed_at_the_end_of_32_bits():
     S = 2 ** 30 - 1
     assert _norm(q=_heads(n_heads=1), seqs=_seqs([S, S], [S, S], [0, 0]), n_pos=2 ** 30) == DSA_ERR_UNSUPPORTED
     assert dsa.last_launch_count() == 0
+
+
+@pytest.mark.parametrize("part", ["tree_mla", "tree_mla_tc", "latent_cache", "head_norm"])
+def test_no_host_memory_is_allocated(part):
+    """The library's contract: what these parts import from C++ and C holds no allocation."""
+    obj = os.path.join(os.path.dirname(dsa.__file__), "_build", part + ".o")
+    nm = shutil.which("nm")
+    if nm is None or not os.path.exists(obj):
+        pytest.skip("no objects to look at")
+    names = subprocess.run([nm, "-u", obj], check=True, capture_output=True, text=True).stdout.split()
+    assert any("cudaLaunchKernel" in n for n in names)  # these are the imports
+    bad = [n for n in names if n.startswith(("_Znw", "_Zna")) or n in ("malloc", "calloc", "realloc", "cudaMalloc", "cudaHostAlloc")]
+    assert not bad, bad
