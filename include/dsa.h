@@ -509,7 +509,7 @@ int dsa_latent_cache_read(const dsa_latent_cache *cache, int d_c, int d_r, const
  * dsa_sparse_mla_fwd (E4M3: d_c a multiple of 128).  start_pos[b] + T_b < 2^31 - 256,
  * sum T * H < 2^31 - 256.
  * All pointers 16-byte aligned (kv_scale too); workspace as in dsa_sparse_mla_fwd, its size
- * depends on the sequences (calls captured in graphs that may run at the same
+ * depends on the sequences and the current device (calls captured in graphs that may run at the same
  * time need workspaces of their own).
  * Errors: DSA_ERR_INVALID_ARG, DSA_ERR_WORKSPACE, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA. */
 size_t dsa_tree_mla_workspace_size(int dtype, int H, int d_n, int d_r, int d_c, int d_v, const dsa_seqs *seqs);

@@ -83,7 +83,6 @@ constexpr uint32_t IDESC_PV = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, ROWS, 2
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr long long kAbortQuietCycles = 1LL << 18;
-constexpr int PAIRS = 76;               // 152 SMs
 constexpr int kMaxSplits = 76;          // of a sequence
 // warp 0: TMA (Q, bf16 K); 1: QK^T; 2: tensor memory, PV; 3: TMA (bf16 V); from 4 on the softmax groups of four
 // (warp % 4 = lane quarter); of an e4m3 cache eight more load, of a bf16 cache two more look V tiles over
@@ -1020,7 +1019,7 @@ Shape shape_of(const Batch &bt, int H, int b) {
     const int64_t T = bt.st.q_off[b + 1] - bt.st.q_off[b];
     return Shape{(T * H + ROWS - 1) / ROWS, (int)(((int64_t)bt.st.start_pos[b] + T + TK - 1) / TK)};
 }
-// One pair of SMs works on a unit at a time, so units come in waves of 76.  A unit costs its tiles and about
+// One pair of SMs works on a unit at a time, so units come in waves of half the SMs (76 on a GB300).  A unit costs its tiles and about
 // kUnitCost tiles to start and end.  Of the chunk sizes that fill one, two, .. waves the cheapest is
 // taken; no split at all competes with them, and saves the join: kJoinCost tiles, and kJoinSplit a split.
 // (On the GPU alone, with 128 heads: one token over 1000 cached whole 34.3 us, in ranges of 2 tiles 26.4; 4 nodes of each
@@ -1029,7 +1028,7 @@ constexpr int kUnitCost = 6, kMinChunk = 2, kMaxWaves = 4;
 constexpr double kJoinCost = 4.5, kJoinSplit = 0.08;
 int split_of(const Shape &s, int chunk) { return std::min(kMaxSplits, (s.tiles + chunk - 1) / chunk); }
 void make_plan(const Batch &bt, int H, Plan &plan) {
-    const int B = bt.st.B;
+    const int B = bt.st.B, pairs = std::max(1, device_sm_count() / 2);
     static thread_local Shape sh[DSA_MAX_SEQS];
     int longest = 1;
     int64_t work = 0, rows = 0;
@@ -1048,16 +1047,16 @@ void make_plan(const Batch &bt, int H, Plan &plan) {
     int best = longest;
     // many waves: the average load and half of the longest unit; few: whole waves of the longest unit
     const auto cost = [&](int64_t n, int chunk) {
-        const int64_t waves = (n + PAIRS - 1) / PAIRS;
-        if (waves > kMaxWaves) return (double)(work + n * kUnitCost) / PAIRS + 0.5 * (chunk + kUnitCost);
+        const int64_t waves = (n + pairs - 1) / pairs;
+        if (waves > kMaxWaves) return (double)(work + n * kUnitCost) / pairs + 0.5 * (chunk + kUnitCost);
         return (double)waves * (chunk + kUnitCost);
     };
     double least = cost(rows, longest);
-    for (int w = 1; w <= kMaxWaves && rows <= (int64_t)w * PAIRS; ++w) {
+    for (int w = 1; w <= kMaxWaves && rows <= (int64_t)w * pairs; ++w) {
         int lo = kMinChunk, hi = longest;  // the smallest chunk whose units fit w waves
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
-            if (units(mid) <= (int64_t)w * PAIRS) hi = mid; else lo = mid + 1;
+            if (units(mid) <= (int64_t)w * pairs) hi = mid; else lo = mid + 1;
         }
         const double c = cost(units(lo), lo) + kJoinCost + kJoinSplit * split_of(Shape{1, longest}, lo);
         if (c < least) {
