@@ -50,6 +50,7 @@ def _check(fn: str, status: int):
 
 def _int32s(values):
     """A C array of the values (through ``array``, which takes a list ten times as fast as ctypes does)."""
+    values = values if isinstance(values, list) else list(values)  # (array would take the bytes of a bytes object as memory)
     try:
         a = array.array("i", values)
     except TypeError:  # tensors of one value and other things that only int() takes

@@ -1,9 +1,11 @@
 """CPU-only checks of calls of the cache, tree-attention and head-norm entry points that are refused, and of the
 batch description (see test_cache_tree_host for the others)."""
+import array
 import os
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 import torch
 
@@ -61,3 +63,15 @@ def test_no_host_memory_is_allocated(part):
     assert any("cudaLaunchKernel" in n for n in names)  # these are the imports
     bad = [n for n in names if n.startswith(("_Znw", "_Zna")) or n in ("malloc", "calloc", "realloc", "cudaMalloc", "cudaHostAlloc")]
     assert not bad, bad
+
+
+def test_batches_of_any_sequence_of_numbers():
+    """Lists, tuples, ranges, arrays, tensors and bytes of numbers describe the same batch."""
+    want = [0, 3, 4], [0, 9, 16], [6, 6]
+    for make in (list, tuple, lambda v: array.array("q", v), np.array, lambda v: np.array(v, dtype=np.float32), torch.tensor,
+                 bytes, bytearray, lambda v: [torch.tensor(x) for x in v], lambda v: [float(x) for x in v]):
+        s = dsa.Seqs(*(make(v) for v in want))
+        assert [list(a[:n]) for a, n in ((s.struct.cu_q, 3), (s.struct.cu_k, 3), (s.struct.start_pos, 2))] == list(want)
+        assert (s.B, s.total_q, s.total_k, s.max_S) == (2, 4, 16, 9)
+    assert list(dsa.Seqs(range(5), range(0, 50, 10), [9] * 4).struct.cu_k[:5]) == [0, 10, 20, 30, 40]
+    assert dsa.Seqs(b"\0\0\0\0\0", b"\0\1\2\3\4", b"\0\0\0\0").total_k == 4  # four bytes are four numbers
