@@ -12,6 +12,7 @@ from __future__ import annotations
 import array
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -70,7 +71,7 @@ class Seqs:
         self.total_q = self._q[B]
         self.total_k = self._k[B]
 
-    @property
+    @functools.cached_property
     def max_S(self) -> int:
         k = self._k[:]
         return max((b - a for a, b in zip(k, k[1:])), default=0)

@@ -75,3 +75,9 @@ def test_batches_of_any_sequence_of_numbers():
         assert (s.B, s.total_q, s.total_k, s.max_S) == (2, 4, 16, 9)
     assert list(dsa.Seqs(range(5), range(0, 50, 10), [9] * 4).struct.cu_k[:5]) == [0, 10, 20, 30, 40]
     assert dsa.Seqs(b"\0\0\0\0\0", b"\0\1\2\3\4", b"\0\0\0\0").total_k == 4  # four bytes are four numbers
+
+
+def test_the_longest_sequence_is_looked_for_once():
+    s = dsa.Seqs([0, 1, 2], [0, 9, 16], [8, 6])
+    assert s.max_S == 9 and "max_S" in vars(s)
+    assert dsa.Seqs([0], [0], []).max_S == 0
