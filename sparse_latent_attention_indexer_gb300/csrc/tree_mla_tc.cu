@@ -939,8 +939,10 @@ struct JoinParams {
     int64_t rows;
 };
 static_assert(sizeof(JoinParams) + 128 <= 32764, "launch parameters");
-// AHEAD loads in flight a warp: eight where sequences are cut often, two where not (more warps fit: 8 sequences of 4 nodes
-// over 1000 tokens in 3 ranges take 34.9 us a call with two, 37.3 with eight; one of 16,000 tokens in 76 ranges 42 and 34).
+// AHEAD loads in flight a warp: eight where sequences are cut into 12 ranges or more, two where not (more warps fit).  Of one
+// token and 128 heads each over 4000 or 8000 tokens, with two and with eight, us a call on the GPU: 25 sequences in 3 ranges
+// 64.0 and 66.4, 15 in 5 52.3 and 53.5, 9 in 8 39.6 and 40.5, 7 in 11 50.0 and 50.2, 6 in 12 47.2 and 46.8, 4 in 18 37.0 and
+// 35.9, one in 63 35.9 and 31.1.
 template <int AHEAD>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ JoinParams P,
                                                         const float *__restrict__ opart,
@@ -1171,7 +1173,7 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
     for (int b = 0; b < B; ++b) most = std::max(most, J.splits[b] = plan.splits[b]);
     J.H = H;
     J.rows = (int64_t)N * H;
-    e = launch_pdl(most > 4 ? tree_join_kernel<8> : tree_join_kernel<2>, dim3((unsigned)((J.rows * 4 + 7) / 8)), dim3(256), 0, s, J, (const float *)opart,
+    e = launch_pdl(most >= 12 ? tree_join_kernel<8> : tree_join_kernel<2>, dim3((unsigned)((J.rows * 4 + 7) / 8)), dim3(256), 0, s, J, (const float *)opart,
                    (const float *)lpart, (__nv_bfloat16 *)olat, lse);
     if (e != cudaSuccess) return e;
     note_launch(DSA_KERNEL_TREE_COMBINE);
