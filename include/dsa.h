@@ -423,6 +423,9 @@ int dsa_forward_host(const dsa_problem *p, const dsa_seqs *seqs, const dsa_host_
  * counterpart to these four entry points): the heads' norm and rotation at a
  * draft tree's positions, the cache written (and quantised) and read back by
  * token position, and the attention of the tree's nodes over it.
+ * A call captured in a graph replays the lengths (cu_q, cu_k, start_pos) that it
+ * was captured with; everything in device memory (values, positions given as
+ * `pos`, masks, block tables, caches) is read at each replay.
  * ---------------------------------------------------------------------- */
 
 /* Where a sequence's tokens sit in a cache cut into pages of page_size rows:
@@ -505,7 +508,7 @@ int dsa_latent_cache_read(const dsa_latent_cache *cache, int d_c, int d_r, const
  * passes 2^119.  softmax_scale is finite, also times log2(e); 0 and negative values are allowed.  Contiguous or paged cache (`pages`), of dtype's own type, or
  * E4M3 with dtype DSA_BF16.
  * Two kernels: tensor cores for bf16 at d_n = 128, d_r = 64, d_c = 512, d_v = 128
- * and any H; a generic one for everything else within the limits of
+ * and H up to 256; a generic one for everything else within the limits of
  * dsa_sparse_mla_fwd (E4M3: d_c a multiple of 128).  start_pos[b] + T_b < 2^31 - 256,
  * sum T * H < 2^31 - 256.
  * All pointers 16-byte aligned (kv_scale too); workspace as in dsa_sparse_mla_fwd, its size

@@ -39,10 +39,11 @@
 // Roundings: q~, the probabilities and the context to bf16, as operands of the next product (as
 // in the sparse attention); scores, maxima, sums and the context's accumulation in fp32.
 // Bound by shared memory: a bf16 tile moves 219 KB through it (92 MMA operands, 68 tokens by
-// TMA, 59 partial scores and probabilities), 1711 cycles at 128 bytes a cycle of the 2010 that
-// it takes (its MMAs take 1088; trees of 32 nodes over up to 12K tokens run at 1150 TFLOP/s; with the
-// halves rounded to fp16 1810 and 1270).  An e4m3 tile takes 2810: 226 KB (1766 cycles), and three
-// stages whose way from codes to PV is 8K cycles long (32 x 64K decode at 859 TFLOP/s).  A unit's start and end cost about ten tiles.
+// TMA, 59 partial scores and probabilities), 1711 cycles at 128 bytes a cycle of the 2000 that
+// it takes (its MMAs take 1088; trees of 32 nodes over up to 12K tokens run at 1150 TFLOP/s; with
+// the halves rounded to fp16 1810 and 1270).  An e4m3 tile takes 2790, of which 226 KB through
+// shared memory are 1766 (32 x 64K decode at 874 TFLOP/s); what the rest waits for has not been
+// measured.  A unit's start and end take 12 us: 11 bf16 tiles, 9 e4m3 ones (76 units of 4 to 36).
 //
 // Waits are bounded; a timeout records its site in the device error word and
 // both CTAs drain and exit.
@@ -471,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KV8>::THREADS, 1
             const int st = t & 1;
             const bool ok = tc::mbar_wait(&bar->raw[st], ((t - behind) >> 1) & 1, abort_flag, err, 125, P.wait_limit);
             if (!bar_and<3, 32 * SCRUBBERS>(ok)) break;
-            // 32 tokens a step, half of the slabs a warp, from the first hidden token's on
+            // 16 tokens a step, half of the slabs a warp, from the first hidden token's on
             uint8_t *half = KV + 2 * STAGE + st * VSTAGE + (warp - FIRST_LOAD) * 2 * SLAB;
 #pragma unroll 1
             for (int at = (max(0, safe - (t0 + t) * TK) & ~15) * 128 + lane * 16; at < SLAB; at += 2048) {
@@ -1024,8 +1025,10 @@ Shape shape_of(const Batch &bt, int H, int b) {
 // One pair of SMs works on a unit at a time, so units come in waves of half the SMs (76 on a GB300).  A unit costs its tiles and about
 // kUnitCost tiles to start and end.  Of the chunk sizes that fill one, two, .. waves the cheapest is
 // taken; no split at all competes with them, and saves the join: kJoinCost tiles, and kJoinSplit a split.
-// (On the GPU alone, with 128 heads: one token over 1000 cached whole 34.3 us, in ranges of 2 tiles 26.4; 4 nodes of each
-// of 8 sequences over 300 whole 25.7, in ranges of 4 30.2; 2 nodes of each of 12 over 3600 whole 66.8, of 12 tiles 44.6.)
+// (On the GPU alone, with 128 heads: one token over 1000 cached whole 36.0 us, in ranges of 2 tiles 27.1; 4 nodes of each
+// of 8 sequences over 300 whole 26.2, in ranges of 4 32.9; 2 nodes of each of 12 over 3600 whole 77.7, of 19 tiles 53.9, of 12
+// 69.6.)  kUnitCost is the plan's own and less than what a unit's start and end take alone (9 to 11 tiles): these choices
+// come out alike with 6 and with 10.
 constexpr int kUnitCost = 6, kMinChunk = 2, kMaxWaves = 4;
 constexpr double kJoinCost = 4.5, kJoinSplit = 0.08;
 int split_of(const Shape &s, int chunk) { return std::min(kMaxSplits, (s.tiles + chunk - 1) / chunk); }
