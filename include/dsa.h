@@ -502,11 +502,13 @@ int dsa_latent_cache_read(const dsa_latent_cache *cache, int d_c, int d_r, const
  *               (a chain: one token, or a prompt chunk)
  * A row that sees nothing gets out = 0, lse = -inf.  What a row does not see never
  * reaches it, whatever its bits (stale rows, Inf, NaN).  A row that sees a NaN is
- * NaN; visible Inf, E4M3 NaN codes and E4M3 scales that are no finite power of two are not supported.
- * Scores and sums are fp32, the sums with weights of up to 2^8 before they are divided by the row sum: visible
- * latents are exact at any finite size, but may overflow in the sum where their size times the number of tokens
- * passes 2^119.  softmax_scale is finite, also times log2(e); 0 and negative values are allowed.  Contiguous or paged cache (`pages`), of dtype's own type, or
- * E4M3 with dtype DSA_BF16.
+ * NaN; visible Inf (a code times its scale too), E4M3 NaN codes and E4M3 scales that
+ * are no finite power of two are not supported.  Scores and sums are fp32, the sums
+ * with weights of up to 2^8 before they are divided by the row sum: visible latents
+ * count in full at any finite size, but may overflow in the sum where their size times
+ * the number of tokens passes 2^119.  softmax_scale is finite, also times log2(e); 0
+ * and negative values are allowed.  Contiguous or paged cache (`pages`), of dtype's
+ * own type, or E4M3 with dtype DSA_BF16.
  * Two kernels: tensor cores for bf16 at d_n = 128, d_r = 64, d_c = 512, d_v = 128
  * and H up to 256; a generic one for everything else within the limits of
  * dsa_sparse_mla_fwd (E4M3: d_c a multiple of 128).  start_pos[b] + T_b < 2^31 - 256,
