@@ -562,6 +562,102 @@ int dsa_head_norm_rope(const dsa_heads *q, const dsa_heads *k, int x_dtype, int 
                        const int32_t *pos, const dsa_seqs *seqs, void *stream);
 
 /* ------------------------------------------------------------------------
+ * From the attention's output to the next token.
+ * No reference code: the pages name the layers (nnterp deepseek_v32 printout: the
+ * Linear modules of the attention and the two norms of a block), the operators
+ * are those that every server needs between two attentions and after the last.
+ * ---------------------------------------------------------------------- */
+#define DSA_ACT_NONE      0
+#define DSA_ACT_RELU      1       /* max(v, 0) */
+#define DSA_ACT_SILU      2       /* v / (1 + exp(-v)) */
+#define DSA_ACT_GELU      3       /* v / 2 (1 + erf(v / sqrt 2)) */
+#define DSA_ACT_GELU_TANH 4       /* v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) */
+#define DSA_ACT_SIGMOID   5       /* 1 / (1 + exp(-v)): gates only */
+
+/* A linear layer, y = act(x W^T + bias) + residual, in fp32 up to one rounding to
+ * y's type.
+ *   x         [M, K] of dtype (DSA_BF16 or DSA_F32), row stride ld_x elements
+ *   W         [N, K] of dtype (nn.Linear layout), row stride ld_w
+ *   bias      [N] fp32 or NULL
+ *   residual  [M, N] of y's type, row stride ld_r, or NULL
+ *   y         out [M, N] of y_dtype (DSA_BF16 or DSA_F32), row stride ld_y; may be
+ *             residual itself (same address and stride), otherwise overlaps no input
+ * Any sizes and strides of whole elements.  bf16 rows that start on 16 bytes go to
+ * the tensor cores as they are; others, and fp32 values (as three bf16 terms each,
+ * six products of them: the error of an fp32 sum), are laid out in the workspace
+ * first.  In fp32 a product with an infinity is NaN, and terms of values below
+ * 2^-100 may be lost.
+ * The workspace size depends on all that it is given here (0 where none is needed).
+ * Errors: DSA_ERR_INVALID_ARG (null pointer, sizes below M >= 0, N, K >= 1, an
+ * address off its element, rows of an output that overlap), DSA_ERR_UNSUPPORTED
+ * (dtype, act, M, N or K not below 2^31 - 1024), DSA_ERR_WORKSPACE, DSA_ERR_CUDA. */
+size_t dsa_linear_workspace_size(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int dtype, int M, int N, int K);
+int dsa_linear(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int dtype, int M, int N, int K,
+               const float *bias, int act, const void *residual, int64_t ld_r, void *y, int64_t ld_y, int y_dtype,
+               void *workspace, size_t ws_bytes, void *stream);
+
+/* One norm of dsa_block_norm: DSA_NORM_*, gain and bias [D] fp32 (NULL: 1 and 0;
+ * the bias goes with DSA_NORM_LAYER only). */
+typedef struct dsa_norm {
+    int32_t kind;
+    const float *gain, *bias;
+} dsa_norm;
+
+/* The norms on both sides of a block with its gate and its residual, row by row:
+ *   h' = skip h + scale act(gate) norm_post(u),   y = norm_pre(h')
+ * in fp32; h' and y are each rounded once, y comes from the unrounded h'. */
+typedef struct dsa_block_norm_args {
+    int64_t rows;                 /* >= 0 */
+    int32_t D;                    /* values a row, 1 .. 16384 */
+    int32_t h_dtype, x_dtype;     /* DSA_F32 or DSA_BF16: of h and h_out; of u, gate and y */
+    const void *h;                /* [rows, D], row stride ld_h: the residual stream */
+    int64_t ld_h;
+    const void *u;                /* [rows, D], row stride ld_u: what the block gave; NULL: h' = skip h */
+    int64_t ld_u;
+    const void *gate;             /* [rows, D], row stride ld_gate (0: one row for all); NULL: 1 */
+    int64_t ld_gate;
+    int32_t gate_act;             /* DSA_ACT_NONE, DSA_ACT_SIGMOID or DSA_ACT_SILU */
+    dsa_norm post, pre;           /* of u; of h' */
+    float skip, scale, eps;       /* eps of both norms, >= 0 */
+    void *h_out;                  /* out [rows, D], row stride ld_ho, or NULL; may be h (same stride) */
+    int64_t ld_ho;
+    void *y;                      /* out [rows, D], row stride ld_y, or NULL; may be u (same stride) */
+    int64_t ld_y;
+} dsa_block_norm_args;
+/* Errors: DSA_ERR_INVALID_ARG (neither h_out nor y, gate or post norm without u, an
+ * address off its element, rows of an output that overlap, other overlaps that the
+ * addresses show), DSA_ERR_UNSUPPORTED (D > 16384, dtype, norm or gate_act of another
+ * kind), DSA_ERR_CUDA. */
+int dsa_block_norm(const dsa_block_norm_args *args, void *stream);
+
+/* The next token of every row of logits, from given random numbers.  With z_i =
+ * l_i / temperature and w_i = exp(z_i - max z), tokens in the order of falling l (equal
+ * ones by rising index):
+ *   1. the first top_k tokens are kept,
+ *   2. of these the shortest run from the start whose sum reaches top_p times theirs,
+ *   3. of these the ones with w_i >= min_p; the first one always is,
+ * and token = the lowest kept index whose running sum of kept weights (in the order of
+ * the indices) exceeds u times their whole sum.
+ *   logits       [R, V] of dtype (DSA_F32 or DSA_BF16), row stride ld; V 1 .. 262144
+ *   u            [R] fp32 in [0, 1); a value outside (or NaN) counts as the nearest inside (0)
+ *   temperature  [R] fp32; below 1e-5 (or NaN): top_k is 1.  NULL: 1
+ *   top_k        [R] int32; <= 0: no such limit.  NULL: none
+ *   top_p        [R] fp32; >= 1 or NaN: no such limit, <= 0: the first token.  NULL: none
+ *   min_p        [R] fp32; <= 0 or NaN: no such limit.  NULL: none
+ *   token        out [R] int32
+ *   logprob      out [R] fp32: ln of the token's share of the kept sum; NULL: not wanted
+ *   kept         out [R] int32: how many tokens were kept; NULL: not wanted
+ * -inf and NaN are never taken (a mask): a row of nothing else gives token -1, logprob
+ * -inf and kept 0.  Where a logit is +inf, those are the only ones, with equal weights.
+ * Sums are of whole numbers: weights in steps of 2^-45, each off by less than 2^-42, so
+ * that the order of summation is nothing and the same inputs give the same token.
+ * Errors: DSA_ERR_INVALID_ARG (null pointer, R < 0, V < 1, an address off its element),
+ * DSA_ERR_UNSUPPORTED (dtype, V > 262144), DSA_ERR_CUDA. */
+int dsa_sample(const void *logits, int64_t ld, int dtype, int R, int V, const float *u, const float *temperature,
+               const int32_t *top_k, const float *top_p, const float *min_p, int32_t *token, float *logprob,
+               int32_t *kept, void *stream);
+
+/* ------------------------------------------------------------------------
  * Status and diagnostics.
  * ---------------------------------------------------------------------- */
 /* Human-readable name of a dsa_status. */
@@ -647,6 +743,11 @@ int dsa_set_stage_events(void *const *events, int n_events);
 #define DSA_KERNEL_TREE_TC      (1u << 19)
 #define DSA_KERNEL_TREE_COMBINE (1u << 20)
 #define DSA_KERNEL_HEAD_NORM    (1u << 21)
+#define DSA_KERNEL_LINEAR       (1u << 22)
+#define DSA_KERNEL_LINEAR_LAYOUT (1u << 23)  /* x or W laid out in the workspace first */
+#define DSA_KERNEL_LINEAR_SIMT  (1u << 24)
+#define DSA_KERNEL_BLOCK_NORM   (1u << 25)
+#define DSA_KERNEL_SAMPLE       (1u << 26)
 
 #ifdef __cplusplus
 }

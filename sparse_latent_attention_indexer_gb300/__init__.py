@@ -25,7 +25,8 @@ __all__ = [
     "dsa_check_device_error", "dsa_selftest_bounded_wait", "dsa_set_wait_limit", "dsa_set_fused_topk", "dsa_kv_prologue",
     "dsa_output_proj", "dsa_sparse_mla_fwd_fp8kv", "dsa_forward_host", "last_kernels", "last_launch_count", "build",
     "Pages", "LatentCache", "Heads", "dsa_latent_cache_write", "dsa_latent_cache_read", "dsa_tree_mla_workspace_size",
-    "dsa_tree_mla_fwd", "dsa_head_norm_rope",
+    "dsa_tree_mla_fwd", "dsa_head_norm_rope", "dsa_linear_workspace_size", "dsa_linear", "Norm", "dsa_block_norm",
+    "dsa_sample",
 ]
 
 
@@ -708,3 +709,156 @@ def _dt_of(dtype: torch.dtype) -> int:
     if dtype == torch.bfloat16:
         return DSA_BF16
     raise TypeError(f"unsupported dtype {dtype}")
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# From the attention's output to the next token
+# ---------------------------------------------------------------------------------------------------------------
+_ACTS = {None: _abi.DSA_ACT_NONE, "none": _abi.DSA_ACT_NONE, "relu": _abi.DSA_ACT_RELU, "silu": _abi.DSA_ACT_SILU,
+         "gelu": _abi.DSA_ACT_GELU, "gelu_tanh": _abi.DSA_ACT_GELU_TANH}
+_GATES = {None: _abi.DSA_ACT_NONE, "none": _abi.DSA_ACT_NONE, "sigmoid": _abi.DSA_ACT_SIGMOID,
+          "silu": _abi.DSA_ACT_SILU}
+
+
+def _matrix(fn: str, name: str, t: torch.Tensor, rows, width, dtype):
+    """A 2-D tensor of the shape and type with contiguous rows; its row stride."""
+    _rows_2d(fn, name, t, width, rows)
+    if t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
+    return t.stride(0) if rows > 1 else width
+
+
+def _vector(fn: str, name: str, t, n: int, dtype):
+    if t is not None and (t.dtype != dtype or t.shape != (n,) or not t.is_contiguous()):
+        raise ValueError(f"{fn}: {name} must be contiguous {dtype} [{n}]")
+
+
+def dsa_linear_workspace_size(x: torch.Tensor, weight: torch.Tensor) -> int:
+    fn = "dsa_linear_workspace_size"
+    (M, K), N = x.shape, weight.shape[0]
+    return _abi.load().dsa_linear_workspace_size(x.data_ptr(), _matrix(fn, "x", x, M, K, x.dtype), weight.data_ptr(),
+                                                 _matrix(fn, "weight", weight, N, K, x.dtype), _dt_of(x.dtype), M, N, K)
+
+
+def dsa_linear(x, weight, bias=None, act=None, residual=None, y=None, dtype=None, workspace=None, stream=None):
+    """y = act(x weight^T + bias) + residual: x [M, K], weight [N, K] (nn.Linear layout), both bf16 or fp32, bias [N]
+    fp32, residual and y [M, N] of ``dtype`` (default: y's, the residual's or x's).  ``act``: "relu", "silu", "gelu",
+    "gelu_tanh" or None.  y may be residual.  Returns y."""
+    fn = "dsa_linear"
+    dev = _on_one_device(fn, (("x", x), ("weight", weight), ("bias", bias), ("residual", residual), ("y", y),
+                              ("workspace", workspace)))
+    if act not in _ACTS:
+        raise ValueError(f"{fn}: act must be 'relu', 'silu', 'gelu', 'gelu_tanh' or None, not {act!r}")
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError(f"{fn}: x and weight must be 2-D")
+    (M, K), N = x.shape, weight.shape[0]
+    ld_x, ld_w = _matrix(fn, "x", x, M, K, x.dtype), _matrix(fn, "weight", weight, N, K, x.dtype)
+    _vector(fn, "bias", bias, N, torch.float32)
+    if dtype is None:
+        dtype = (y if y is not None else residual if residual is not None else x).dtype
+    dt, y_dt = _dt_of(x.dtype), _dt_of(dtype)
+    ld_r = 0 if residual is None else _matrix(fn, "residual", residual, M, N, dtype)
+    ld_y = N if y is None else _matrix(fn, "y", y, M, N, dtype)
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+        raise ValueError(f"{fn}: workspace must be a contiguous uint8 tensor")
+    lib = _abi.load()
+    px, pw = x.data_ptr(), weight.data_ptr()
+    with _launching(dev, stream):
+        if y is None:
+            y = torch.empty((M, N), dtype=dtype, device=x.device)
+        if workspace is None:
+            need = lib.dsa_linear_workspace_size(px, ld_x, pw, ld_w, dt, M, N, K)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        _check(fn, lib.dsa_linear(px, ld_x, pw, ld_w, dt, M, N, K, _addr(bias), _ACTS[act], _addr(residual), ld_r,
+                                  y.data_ptr(), ld_y, y_dt, _addr(workspace),
+                                  0 if workspace is None else workspace.numel(),
+                                  torch._C._cuda_getCurrentRawStream(dev)))
+    return y
+
+
+class Norm:
+    """One norm of dsa_block_norm: kind "rms", "layer" or "none", gain and bias [D] fp32 (None: 1 and 0)."""
+
+    def __init__(self, kind="rms", gain=None, bias=None):
+        if kind not in _NORMS:
+            raise ValueError(f"Norm: kind must be 'rms', 'layer' or 'none', not {kind!r}")
+        self.kind, self.gain, self.bias = kind, gain, bias
+        self.struct = _abi.dsa_norm(_NORMS[kind], _addr(gain), _addr(bias))
+
+
+_NO_NORM = Norm("none")
+
+
+def dsa_block_norm(h, pre: Norm | None = None, u=None, post: Norm | None = None, gate=None, gate_act=None, skip=1.0,
+                   scale=1.0, eps=1e-6, h_out=None, y=None, want_h=True, want_y=True, dtype=None, stream=None):
+    """h' = skip h + scale act(gate) norm_post(u) and y = norm_pre(h') in one pass: the residual stream h [N, D], what
+    a block gave u [N, D] (None: h' = skip h), its gate [N, D] or [1, D] for all rows (``gate_act``: "sigmoid", "silu"
+    or None).  h, h_out and u, gate, y are fp32 or bf16; y's type is u's, or ``dtype``.  h_out may be h, y may be u.
+    Returns (h', y), None for one that is not wanted."""
+    fn = "dsa_block_norm"
+    pre, post = pre or _NO_NORM, post or _NO_NORM
+    dev = _on_one_device(fn, (("h", h), ("u", u), ("gate", gate), ("h_out", h_out), ("y", y),
+                              ("pre.gain", pre.gain), ("pre.bias", pre.bias), ("post.gain", post.gain),
+                              ("post.bias", post.bias)))
+    if gate_act not in _GATES:
+        raise ValueError(f"{fn}: gate_act must be 'sigmoid', 'silu' or None, not {gate_act!r}")
+    if h.dim() != 2:
+        raise ValueError(f"{fn}: h must be 2-D")
+    N, D = h.shape
+    x_dtype = next((t.dtype for t in (u, gate, y) if t is not None), dtype or h.dtype)
+    if dtype is not None and dtype != x_dtype:
+        raise ValueError(f"{fn}: dtype is {dtype} beside {x_dtype} tensors")
+    for n in (pre, post):
+        _vector(fn, "gain", n.gain, D, torch.float32)
+        _vector(fn, "bias", n.bias, D, torch.float32)
+    ld_h = _matrix(fn, "h", h, N, D, h.dtype)
+    ld_u = 0 if u is None else _matrix(fn, "u", u, N, D, x_dtype)
+    ld_g = 0
+    if gate is not None:
+        rows = 1 if gate.dim() == 2 and gate.shape[0] == 1 else N
+        ld_g = _matrix(fn, "gate", gate, rows, D, x_dtype)
+        if rows == 1 and N > 1:
+            ld_g = 0
+    ld_ho = D if h_out is None else _matrix(fn, "h_out", h_out, N, D, h.dtype)
+    ld_y = D if y is None else _matrix(fn, "y", y, N, D, x_dtype)
+    h_dt, x_dt = _dt_of(h.dtype), _dt_of(x_dtype)
+    with _launching(dev, stream):
+        if h_out is None and want_h:
+            h_out = torch.empty((N, D), dtype=h.dtype, device=h.device)
+        if y is None and want_y:
+            y = torch.empty((N, D), dtype=x_dtype, device=h.device)
+        args = _abi.dsa_block_norm_args(N, D, h_dt, x_dt, h.data_ptr(), ld_h, _addr(u), ld_u, _addr(gate), ld_g,
+                                        _GATES[gate_act], post.struct, pre.struct, skip, scale, eps, _addr(h_out),
+                                        ld_ho, _addr(y), ld_y)
+        _check(fn, _abi.load().dsa_block_norm(ctypes.byref(args), torch._C._cuda_getCurrentRawStream(dev)))
+    return h_out, y
+
+
+def dsa_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, token=None, want_logprob=True,
+               want_kept=False, stream=None):
+    """The next token of every row of logits [R, V] (fp32 or bf16) from ``uniform`` [R] fp32 in [0, 1): softmax at
+    ``temperature`` [R] fp32 (below 1e-5: the highest logit), cut to the ``top_k`` [R] int32 first tokens (<= 0: all),
+    the shortest run of them whose probability reaches ``top_p`` [R] fp32, and those of at least ``min_p`` [R] fp32
+    times the highest probability.  Returns (token [R] int32, its log-probability among the kept [R] fp32, how many
+    were kept [R] int32); None for what is not wanted.  A row of nothing but -inf and NaN gives token -1."""
+    fn = "dsa_sample"
+    dev = _on_one_device(fn, (("logits", logits), ("uniform", uniform), ("temperature", temperature), ("top_k", top_k),
+                              ("top_p", top_p), ("min_p", min_p), ("token", token)))
+    if logits.dim() != 2:
+        raise ValueError(f"{fn}: logits must be 2-D")
+    R, V = logits.shape
+    ld, dt = _matrix(fn, "logits", logits, R, V, logits.dtype), _dt_of(logits.dtype)
+    for name, t in (("uniform", uniform), ("temperature", temperature), ("top_p", top_p), ("min_p", min_p)):
+        _vector(fn, name, t, R, torch.float32)
+    _vector(fn, "top_k", top_k, R, torch.int32)
+    _vector(fn, "token", token, R, torch.int32)
+    with _launching(dev, stream):
+        if token is None:
+            token = torch.empty(R, dtype=torch.int32, device=logits.device)
+        logprob = torch.empty(R, dtype=torch.float32, device=logits.device) if want_logprob else None
+        kept = torch.empty(R, dtype=torch.int32, device=logits.device) if want_kept else None
+        _check(fn, _abi.load().dsa_sample(logits.data_ptr(), ld, dt, R, V, uniform.data_ptr(), _addr(temperature),
+                                          _addr(top_k), _addr(top_p), _addr(min_p), token.data_ptr(), _addr(logprob),
+                                          _addr(kept), torch._C._cuda_getCurrentRawStream(dev)))
+    return token, logprob, kept

@@ -17,10 +17,12 @@ KERNEL_BITS = {
     "absorb_simt": 1 << 5, "absorb_tc": 1 << 6, "mla_simt": 1 << 7, "mla_tc": 1 << 8, "combine": 1 << 9,
     "selftest": 1 << 10, "dense_idx": 1 << 11, "gemm_tc": 1 << 12, "prologue": 1 << 13,
     "indexer_topk": 1 << 14, "append": 1 << 15, "cache_write": 1 << 16, "cache_read": 1 << 17, "tree_simt": 1 << 18,
-    "tree_tc": 1 << 19, "tree_combine": 1 << 20, "head_norm": 1 << 21,
+    "tree_tc": 1 << 19, "tree_combine": 1 << 20, "head_norm": 1 << 21, "linear": 1 << 22, "linear_layout": 1 << 23,
+    "linear_simt": 1 << 24, "block_norm": 1 << 25, "sample": 1 << 26,
 }
 DSA_NORM_NONE, DSA_NORM_RMS, DSA_NORM_LAYER = range(3)
 DSA_ROPE_PAIRS, DSA_ROPE_HALVES = range(2)
+DSA_ACT_NONE, DSA_ACT_RELU, DSA_ACT_SILU, DSA_ACT_GELU, DSA_ACT_GELU_TANH, DSA_ACT_SIGMOID = range(6)
 
 
 class dsa_seqs(ctypes.Structure):
@@ -76,6 +78,21 @@ class dsa_heads(ctypes.Structure):
     ]
 
 
+class dsa_norm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("gain", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class dsa_block_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("D", ctypes.c_int32), ("h_dtype", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+        ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64), ("u", ctypes.c_void_p), ("ld_u", ctypes.c_int64),
+        ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64), ("gate_act", ctypes.c_int32),
+        ("post", dsa_norm), ("pre", dsa_norm),
+        ("skip", ctypes.c_float), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+        ("h_out", ctypes.c_void_p), ("ld_ho", ctypes.c_int64), ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
+    ]
+
+
 # (name, restype, argtypes) of every exported function
 P, I, I64, F, SZ, U32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint32
 SEQS = ctypes.POINTER(dsa_seqs)
@@ -100,6 +117,10 @@ SIGNATURES = [
     ("dsa_tree_mla_workspace_size", SZ, [I, I, I, I, I, I, SEQS]),
     ("dsa_tree_mla_fwd", I, [P, P, I, CACHE, P, P, I, I, I, I, I, P, I, SEQS, PAGES, F, P, P, P, SZ, P]),
     ("dsa_head_norm_rope", I, [HEADS, HEADS, I, I, I, I, I, I, F, P, P, I, P, SEQS, P]),
+    ("dsa_linear_workspace_size", SZ, [P, I64, P, I64, I, I, I, I]),
+    ("dsa_linear", I, [P, I64, P, I64, I, I, I, I, P, I, P, I64, P, I64, I, P, SZ, P]),
+    ("dsa_block_norm", I, [ctypes.POINTER(dsa_block_norm_args), P]),
+    ("dsa_sample", I, [P, I64, I, I, I, P, P, P, P, P, P, P, P, P]),
     ("dsa_status_string", ctypes.c_char_p, [I]),
     ("dsa_last_cuda_error", I, []),
     ("dsa_check_device_error", I, [P, ctypes.POINTER(ctypes.c_int)]),

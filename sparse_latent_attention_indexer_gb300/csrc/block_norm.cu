@@ -1,0 +1,316 @@
+// The norms on both sides of a block, fused with its gate and its residual:
+//
+//   h' = skip h + scale act(g) norm_post(u)        y = norm_pre(h')
+//
+// h is the residual stream, u what the block gave, g its gate; norm: none, RMS with gain,
+// layer with gain and bias ("DeepSeek-V3.2-Exp - Block input" page, RMSNorm excerpt,
+// float32 compute; nnterp deepseek_v32 printout).  y comes from h' before h' is rounded, so
+// the stream's type costs the next block nothing.
+//
+// Bound by HBM: every value is read once and written once.  A row lies in the registers of
+// one CTA (of one warp up to 1024 values) between its loads, which are all issued first, and
+// its stores; a thread stores where it has loaded, so h' may be h and y may be u.  A norm is one sum over the row (two for layer:
+// the mean, then the squares of what is left, so that a large mean costs no digits).
+#include <algorithm>
+
+#include "dsa_common.cuh"
+
+namespace dsa {
+namespace {
+
+struct NormParams {
+    const void *h, *u, *gate;
+    void *ho, *y;
+    const float *post_gain, *post_bias, *pre_gain, *pre_bias;
+    int64_t ld_h, ld_u, ld_g, ld_ho, ld_y, rows;
+    int D, post, pre, gate_act;
+    float skip, scale, eps;
+};
+
+constexpr int MAX_D = 16384;
+
+// W values (8, or 1 where rows are off 16 bytes) as they are stored.
+template <typename T, int W> struct Raw { T v[W]; };
+template <typename T> struct Raw<T, 8> { uint4 q[sizeof(T) / 2]; };
+
+template <typename T>
+__device__ __forceinline__ void fetch(const T *p, Raw<T, 1> &r) { r.v[0] = *p; }
+template <typename T>
+__device__ __forceinline__ void fetch(const T *p, Raw<T, 8> &r) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = ((const uint4 *)p)[i];
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T, 1> &r, float (&v)[1]) { v[0] = to_f32(r.v[0]); }
+__device__ __forceinline__ void unpack(const Raw<float, 8> &r, float (&v)[8]) {
+    const uint32_t w[8] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w, r.q[1].x, r.q[1].y, r.q[1].z, r.q[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 8> &r, float (&v)[8]) {
+    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void put(T *p, const float (&v)[1]) { *p = from_f32<T>(v[0]); }
+__device__ __forceinline__ void put(float *p, const float (&v)[8]) {
+    ((float4 *)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    ((float4 *)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *(const uint32_t *)&t;
+    }
+    *(uint4 *)p = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int W>
+__device__ __forceinline__ void load_gain(const float *p, float (&v)[W]) {
+    if constexpr (W == 8) {
+        const float4 a = __ldg((const float4 *)p), b = __ldg((const float4 *)p + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        v[0] = __ldg(p);
+    }
+}
+
+// Sum over the row's threads, the same in each.  `part` takes a value a warp and is used by no other sum.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float *part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (WARP) return v;
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < warps ? part[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Norms the row's values in place; part: two sums' worth of warps.
+template <int W, int N, bool WARP>
+__device__ __forceinline__ void norm_row(float (&v)[N][W], int kind, const float *gain, const float *bias, int D, float inv_D,
+                                         float eps, int first, int step, float *part) {
+    if (kind == DSA_NORM_NONE) return;
+    if (kind == DSA_NORM_LAYER) {
+        float mu = 0.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < W; ++e) mu += v[j][e];  // zeros behind D
+        mu = row_sum<WARP>(mu, part) * inv_D;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[j][e] -= first + j * step < D ? mu : 0.0f;
+    }
+    float q = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int e = 0; e < W; ++e) q = fmaf(v[j][e], v[j][e], q);
+    const float inv = rsqrtf(fmaf(row_sum<WARP>(q, part + 32), inv_D, eps));
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int d = first + j * step;
+        if (d >= D) continue;
+        float g[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[j][e] *= inv;
+        if (gain) {
+            load_gain<W>(gain + d, g);
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[j][e] *= g[e];
+        }
+        if (bias && kind == DSA_NORM_LAYER) {
+            load_gain<W>(bias + d, g);
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[j][e] += g[e];
+        }
+    }
+}
+
+// Vectors of W values; N of them a thread, `step` values apart.  WARP: a warp takes a row, four rows a CTA.
+template <typename TH, typename TX, int W, int N, int THREADS, bool WARP>
+__global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_constant__ NormParams P) {
+    __shared__ float part[4 * 32];
+    const int64_t r = WARP ? (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+    if (WARP && r >= P.rows) return;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int first = t * W, step = (WARP ? 32 : (int)blockDim.x) * W;
+    const float inv_D = 1.0f / (float)P.D;
+    Raw<TH, W> rh[N];
+    Raw<TX, W> ru[N], rg[N];
+    const TH *h = (const TH *)P.h + r * P.ld_h + first;
+    const TX *u = (const TX *)P.u + r * P.ld_u + first, *g = (const TX *)P.gate + r * P.ld_g + first;
+    if (P.u) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            ru[j] = Raw<TX, W>{};
+            if (first + j * step < P.D) fetch(u + j * step, ru[j]);
+        }
+        if (P.gate)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                rg[j] = Raw<TX, W>{};
+                if (first + j * step < P.D) fetch(g + j * step, rg[j]);
+            }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        rh[j] = Raw<TH, W>{};
+        if (first + j * step < P.D) fetch(h + j * step, rh[j]);
+    }
+    float v[N][W];
+    if (P.u) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) unpack(ru[j], v[j]);
+        norm_row<W, N, WARP>(v, P.post, P.post_gain, P.post_bias, P.D, inv_D, P.eps, first, step, part);
+        if (P.gate)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                float a[W];
+                unpack(rg[j], a);
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    if (P.gate_act != DSA_ACT_NONE) {
+                        const float s = 1.0f / (1.0f + expf(-a[e]));
+                        a[e] = P.gate_act == DSA_ACT_SILU ? a[e] * s : s;
+                    }
+                    v[j][e] *= a[e];
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float a[W];
+            unpack(rh[j], a);
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[j][e] = fmaf(P.scale, v[j][e], P.skip * a[e]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            unpack(rh[j], v[j]);
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[j][e] *= P.skip;
+        }
+    }
+    if (P.ho) {
+        TH *o = (TH *)P.ho + r * P.ld_ho + first;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (first + j * step < P.D) put(o + j * step, v[j]);
+    }
+    if (!P.y) return;
+    norm_row<W, N, WARP>(v, P.pre, P.pre_gain, P.pre_bias, P.D, inv_D, P.eps, first, step, part + 64);
+    TX *y = (TX *)P.y + r * P.ld_y + first;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (first + j * step < P.D) put(y + j * step, v[j]);
+}
+
+template <typename TH, typename TX, int W, int N, int THREADS, bool WARP>
+cudaError_t go(const NormParams &P, cudaStream_t s) {
+    const int vecs = (P.D + W - 1) / W, t = WARP ? THREADS : ((vecs + N - 1) / N + 31) / 32 * 32;
+    const int64_t grid = WARP ? (P.rows + THREADS / 32 - 1) / (THREADS / 32) : P.rows;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    block_norm_kernel<TH, TX, W, N, THREADS, WARP><<<(unsigned)grid, t, 0, s>>>(P);
+    return cudaGetLastError();
+}
+
+template <typename TH, typename TX>
+cudaError_t launch(const NormParams &P, bool vec, cudaStream_t s) {
+    if (!vec) {
+        if (P.D <= 256) return go<TH, TX, 1, 8, 128, true>(P, s);
+        if (P.D <= 4096) return go<TH, TX, 1, 8, 512, false>(P, s);
+        return go<TH, TX, 1, 16, 1024, false>(P, s);
+    }
+    if (P.D <= 256) return go<TH, TX, 8, 1, 128, true>(P, s);
+    if (P.D <= 1024) return go<TH, TX, 8, 4, 128, true>(P, s);
+    if (P.D <= 8192 && P.rows <= 2 * device_sm_count()) return go<TH, TX, 8, 1, 1024, false>(P, s);
+    if (P.D <= 8192) return go<TH, TX, 8, 4, 256, false>(P, s);
+    return go<TH, TX, 8, 4, 512, false>(P, s);
+}
+
+inline size_t esz(int dtype) { return dtype == DSA_F32 ? 4 : 2; }
+
+int check_norm(const dsa_norm &n) {
+    if (n.kind != DSA_NORM_NONE && n.kind != DSA_NORM_RMS && n.kind != DSA_NORM_LAYER) return DSA_ERR_UNSUPPORTED;
+    return (uintptr_t)n.gain % 4 || (uintptr_t)n.bias % 4 ? DSA_ERR_INVALID_ARG : DSA_OK;
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" int dsa_block_norm(const dsa_block_norm_args *a, void *stream) {
+    reset_trace();
+    if (!a || a->rows < 0 || a->D < 1 || !(a->eps >= 0.0f)) return DSA_ERR_INVALID_ARG;
+    if ((a->h_dtype != DSA_F32 && a->h_dtype != DSA_BF16) || (a->x_dtype != DSA_F32 && a->x_dtype != DSA_BF16) || a->D > MAX_D)
+        return DSA_ERR_UNSUPPORTED;
+    int rc = check_norm(a->post);
+    if (!rc) rc = check_norm(a->pre);
+    if (rc) return rc;
+    if (a->gate_act != DSA_ACT_NONE && a->gate_act != DSA_ACT_SIGMOID && a->gate_act != DSA_ACT_SILU) return DSA_ERR_UNSUPPORTED;
+    if (a->rows == 0) return DSA_OK;  // empty tensors have no addresses
+    if (!a->u && (a->gate || a->post.kind != DSA_NORM_NONE)) return DSA_ERR_INVALID_ARG;
+    if (!a->h_out && !a->y) return DSA_ERR_INVALID_ARG;
+    if (!a->h) return DSA_ERR_INVALID_ARG;
+    const size_t eh = esz(a->h_dtype), ex = esz(a->x_dtype);
+    struct { const void *p; int64_t ld; size_t e; bool out; } t[5] = {
+        {a->h, a->ld_h, eh, false}, {a->u, a->ld_u, ex, false}, {a->gate, a->ld_gate, ex, false}, {a->h_out, a->ld_ho, eh, true}, {a->y, a->ld_y, ex, true}};
+    bool vec = a->D % 8 == 0;
+    for (const auto &x : t) {
+        if (!x.p) continue;
+        if ((uintptr_t)x.p % x.e) return DSA_ERR_INVALID_ARG;
+        if (x.out && a->rows > 1 && x.ld < a->D) return DSA_ERR_INVALID_ARG;  // rows of an output that overlap
+        vec = vec && (uintptr_t)x.p % 16 == 0 && (a->rows <= 1 || x.ld * (int64_t)x.e % 16 == 0);
+    }
+    if (a->h_out == a->h && a->h_out && a->rows > 1 && a->ld_ho != a->ld_h) return DSA_ERR_INVALID_ARG;
+    if (a->y && a->y == a->u && a->rows > 1 && a->ld_y != a->ld_u) return DSA_ERR_INVALID_ARG;
+    if (a->y && (a->y == a->h || a->y == a->gate || a->y == a->h_out)) return DSA_ERR_INVALID_ARG;
+    if (a->h_out && (a->h_out == a->u || a->h_out == a->gate)) return DSA_ERR_INVALID_ARG;
+    for (const float *g : {a->post.gain, a->post.bias, a->pre.gain, a->pre.bias}) vec = vec && (uintptr_t)g % 16 == 0;
+    NormParams P;
+    P.h = a->h;
+    P.u = a->u;
+    P.gate = a->gate;
+    P.ho = a->h_out;
+    P.y = a->y;
+    P.post_gain = a->post.gain;
+    P.post_bias = a->post.bias;
+    P.pre_gain = a->pre.gain;
+    P.pre_bias = a->pre.bias;
+    P.ld_h = a->ld_h;
+    P.ld_u = a->ld_u;
+    P.ld_g = a->ld_gate;
+    P.ld_ho = a->ld_ho;
+    P.ld_y = a->ld_y;
+    P.rows = a->rows;
+    P.D = a->D;
+    P.post = a->post.kind;
+    P.pre = a->pre.kind;
+    P.gate_act = a->gate_act;
+    P.skip = a->skip;
+    P.scale = a->scale;
+    P.eps = a->eps;
+    const cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    if (a->h_dtype == DSA_F32)
+        e = a->x_dtype == DSA_F32 ? launch<float, float>(P, vec, s) : launch<float, __nv_bfloat16>(P, vec, s);
+    else
+        e = a->x_dtype == DSA_F32 ? launch<__nv_bfloat16, float>(P, vec, s) : launch<__nv_bfloat16, __nv_bfloat16>(P, vec, s);
+    if (e != cudaSuccess) return fail_cuda(e);
+    note_launch(DSA_KERNEL_BLOCK_NORM);
+    return DSA_OK;
+}
