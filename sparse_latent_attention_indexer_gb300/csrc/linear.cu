@@ -15,6 +15,11 @@
 // shared memory, and every CTA adds a share of it over the cluster in the order of the ranks, so
 // the same call gives the same bits; no workspace, no second launch.
 //
+// The tensor cores cut off what does not fit a running sum of 24 bits, step by step: over 448 steps
+// of 16 products (K = 7168) an fp32 result was off by 7.9e-6 of the whole, ten times what fp32
+// arithmetic loses.  Where y is fp32 (EXACT) the epilogue takes the sum over after every 8 slabs
+// (32 steps) and adds these parts to nearest in its registers.
+//
 // fp32 layers run on the same kernel: a value is the sum of three bf16 terms of 8 bits each, and
 // of the nine products of terms the six above 2^-24 of the whole are added, smallest first.
 // Rows that do not start on 16 bytes are laid out anew first (linear_layout_kernel).
@@ -33,6 +38,8 @@ constexpr int NUM_THREADS = 384;                  // 0 TMA, 1 MMA, 2 TMEM owner,
 constexpr int EPI_WARP0 = 4, EPI_THREADS = 256;
 constexpr int TURN = 2 * 32 * BF * 4;             // 32 tokens x 128 features in fp32 for each half of the epilogue
 constexpr int SMEM_MAX = 232448;
+constexpr int MAX_EXACT = 128;                     // tokens of a tile whose sums are exact
+constexpr int CHAIN = 8;                          // slabs of an exact sum's parts
 constexpr int GROUP_T = 8;                        // token tiles that share a panel of W in L2
 
 struct Epilogue {
@@ -50,6 +57,7 @@ struct LinearParams {
     int plane;            // columns from one plane to the next; 0: one plane
     int stages, stage_bytes;
     int share;            // CTAs that share a tile's K (SPLIT)
+    int chain;            // slabs that are added up in tensor memory (all, or CHAIN with EXACT)
     long long wait_limit;
 };
 
@@ -136,7 +144,7 @@ __device__ __forceinline__ void slab_at(const LinearParams &P, int i, int &xw, i
     xx = ((0x010120 >> (4 * q)) & 15) * P.plane + k;
 }
 
-template <bool SPLIT>
+template <bool SPLIT, bool EXACT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                   const __grid_constant__ LinearParams P) {
@@ -206,25 +214,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else if (warp == 1 && lane == 0) {
         // ---------------- MMA issuer ----------------
         const uint32_t idesc = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, BF, P.bt, 0, 0);
-        int st = 0, round = 0, issued = 0;
+        int st = 0, round = 0, issued = 0, n = 0;
         bool ok = true;
         for (int i = 0; ok && i < mine; ++i) {
-            const int acc = i & 1;
-            if (!(ok = tc::mbar_wait(&tempty[acc], ((i >> 1) & 1) ^ 1, abort_flag, err, 63, P.wait_limit))) break;
-            const uint32_t d = tmem + acc * MAX_BT;
-            for (int ks = s0; ks < s1; ++ks) {
-                if (!(ok = tc::mbar_wait(&full[st], round & 1, abort_flag, err, 64, P.wait_limit))) break;
-                tc::tc_fence_after();
-                const uint32_t a0 = tc::smem_u32(ring + st * P.stage_bytes), b0 = a0 + W_SLAB;
+            for (int k0 = s0; ok && k0 < s1; k0 += P.chain, ++n) {
+                const int acc = n & 1, k1 = min(s1, k0 + P.chain);
+                if (!(ok = tc::mbar_wait(&tempty[acc], ((n >> 1) & 1) ^ 1, abort_flag, err, 63, P.wait_limit))) break;
+                const uint32_t d = tmem + acc * MAX_BT;
+                for (int ks = k0; ks < k1; ++ks) {
+                    if (!(ok = tc::mbar_wait(&full[st], round & 1, abort_flag, err, 64, P.wait_limit))) break;
+                    tc::tc_fence_after();
+                    const uint32_t a0 = tc::smem_u32(ring + st * P.stage_bytes), b0 = a0 + W_SLAB;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    tc::mma_f16(d, tc::smem_desc(a0 + kk * 32, 16, 1024), tc::smem_desc(b0 + kk * 32, 16, 1024), idesc,
-                                ks != s0 || kk != 0);
-                tc::mma_commit(&empty[st]);
-                ++issued;
-                if (++st == P.stages) st = 0, ++round;
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::mma_f16(d, tc::smem_desc(a0 + kk * 32, 16, 1024), tc::smem_desc(b0 + kk * 32, 16, 1024), idesc,
+                                    ks != k0 || kk != 0);
+                    tc::mma_commit(&empty[st]);
+                    ++issued;
+                    if (++st == P.stages) st = 0, ++round;
+                }
+                if (ok) tc::mma_commit(&tfull[acc]);
             }
-            if (ok) tc::mma_commit(&tfull[acc]);
         }
         // No MMA may still be running when the tensor memory is released.
         if (issued > 0) {
@@ -236,71 +246,101 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // Warp (q, g): TMEM lanes (features) 32q .. 32q + 31, every other chunk of 32 tokens.
         const int q = warp & 3, g = (warp - EPI_WARP0) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        float *part = (float *)ring;           // SPLIT: [tokens][BF], once every load of the ring has landed and been used
+        float *mine_turn = turn + g * 32 * BF;
+        int n = 0;
         for (int i = 0; i < mine; ++i) {
-            const int acc = i & 1;
-            if (!epi_and(tc::mbar_wait(&tfull[acc], (i >> 1) & 1, abort_flag, err, 66, P.wait_limit))) break;
-            tc::tc_fence_after();
             int m0, f0;
             tile_of(P, who + i * step, m0, f0);
             const int tokens = min(P.bt, P.M - m0);
-            const int f = f0 + q * 32 + lane;
-            if (SPLIT) {
-                float *part = (float *)ring;  // [tokens][BF]: every load of the ring has landed and been used
-                for (int c = g * 32; c < tokens; c += 64) {
-                    float v[32];
-                    tc::tmem_ld32(lanes + acc * MAX_BT + c, v);
-                    tc::tmem_ld_wait();
+            const int f = f0 + q * 32 + lane, f4 = f0 + lane * 4;
+            const float b = !SPLIT && P.e.bias && f < P.N ? __ldg(P.e.bias + f) : 0.0f;
+            const bool ahead = !SPLIT && !EXACT && P.e.res && P.e.vec && f4 < P.N;  // EXACT has no registers to spare
+            const auto put = [&](int c, float (&v)[32]) {  // tokens c .. c + 31 of this thread's feature
+                if (SPLIT) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (c + j < tokens) part[(c + j) * BF + q * 32 + lane] = v[j];
+                    return;
                 }
-            } else {
-                const float b = P.e.bias && f < P.N ? __ldg(P.e.bias + f) : 0.0f;
-                float *mine_turn = turn + g * 32 * BF;
-                const int f4 = f0 + lane * 4;
-                const bool ahead = P.e.res && P.e.vec && f4 < P.N;
-                for (int c = g * 32; c < tokens; c += 64) {
-                    const int64_t row0 = m0 + c + q * 8;  // the eight tokens that this warp stores
-                    float r[8][4];
-                    if (ahead)
+                const int64_t row0 = m0 + c + q * 8;  // the eight tokens that this warp stores
+                float r[8][4];
+                if (ahead)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (row0 + j < P.M) residual4(P.e, row0 + j, f4, r[j]);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = activate(v[j] + b, P.e.act);
+                bar(2 + g, EPI_THREADS / 2);  // the last chunk has been read
+#pragma unroll
+                for (int j = 0; j < 32; ++j) mine_turn[j * BF + q * 32 + lane] = v[j];
+                bar(2 + g, EPI_THREADS / 2);
+                const int left = min(8, tokens - c - q * 8);
+                if (P.e.vec) {
+                    if (f4 < P.N)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            if (row0 + j < P.M) residual4(P.e, row0 + j, f4, r[j]);
-                    float v[32];
-                    tc::tmem_ld32(lanes + acc * MAX_BT + c, v);
-                    tc::tmem_ld_wait();
+                            if (j < left) {
+                                const float4 a = *(const float4 *)(mine_turn + (q * 8 + j) * BF + lane * 4);
+                                float o[4] = {a.x, a.y, a.z, a.w};
+                                if (EXACT && P.e.res) residual4(P.e, row0 + j, f4, r[j]);
+                                if (P.e.res)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = activate(v[j] + b, P.e.act);
-                    bar(2 + g, EPI_THREADS / 2);  // the last chunk has been read
+                                    for (int e = 0; e < 4; ++e) o[e] += r[j][e];
+                                store4(P.e, row0 + j, f4, o);
+                            }
+                } else {
+                    for (int j = 0; j < left; ++j)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) mine_turn[j * BF + q * 32 + lane] = v[j];
-                    bar(2 + g, EPI_THREADS / 2);
-                    const int n = min(8, tokens - c - q * 8);
-                    if (P.e.vec) {
-                        if (f4 < P.N)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (j < n) {
-                                    const float4 a = *(const float4 *)(mine_turn + (q * 8 + j) * BF + lane * 4);
-                                    float o[4] = {a.x, a.y, a.z, a.w};
-                                    if (ahead)
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) o[e] += r[j][e];
-                                    store4(P.e, row0 + j, f4, o);
-                                }
-                    } else {
-                        for (int j = 0; j < n; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (f0 + e * 32 + lane < P.N)
-                                    store1(P.e, row0 + j, f0 + e * 32 + lane, mine_turn[(q * 8 + j) * BF + e * 32 + lane]);
-                    }
+                        for (int e = 0; e < 4; ++e)
+                            if (f0 + e * 32 + lane < P.N)
+                                store1(P.e, row0 + j, f0 + e * 32 + lane, mine_turn[(q * 8 + j) * BF + e * 32 + lane]);
                 }
+            };
+            bool ok = true;
+            if (EXACT) {
+                float sum[MAX_EXACT / 64][32];
+#pragma unroll
+                for (int j = 0; j < MAX_EXACT / 64; ++j)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) sum[j][e] = 0.0f;
+                for (int k0 = s0; k0 < s1; k0 += P.chain, ++n) {
+                    ok = epi_and(tc::mbar_wait(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < MAX_EXACT / 64; ++j)
+                        if (j * 64 + g * 32 < tokens) {
+                            float v[32];
+                            tc::tmem_ld32(lanes + (n & 1) * MAX_BT + j * 64 + g * 32, v);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) sum[j][e] += v[e];
+                        }
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&tempty[n & 1]);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < MAX_EXACT / 64; ++j)
+                    if (j * 64 + g * 32 < tokens) put(j * 64 + g * 32, sum[j]);
+            } else {
+                ok = epi_and(tc::mbar_wait(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit));
+                if (!ok) break;
+                tc::tc_fence_after();
+                for (int c = g * 32; c < tokens; c += 64) {
+                    float v[32];
+                    tc::tmem_ld32(lanes + (n & 1) * MAX_BT + c, v);
+                    tc::tmem_ld_wait();
+                    put(c, v);
+                }
+                // every column of this accumulator has been read
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&tempty[n & 1]);
+                ++n;
             }
-            // every column of this accumulator has been read
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&tempty[acc]);
         }
     }
     __syncthreads();
@@ -504,14 +544,17 @@ cudaError_t lay_out(const void *src, int64_t ld, int dtype, int64_t rows, int K,
 cudaError_t launch_tiles(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int K, int plane, LinearParams &P,
                          cudaStream_t s) {
     const int sms = device_sm_count();
-    P.tt = (P.M + MAX_BT - 1) / MAX_BT;
+    P.slabs = (K + 63) / 64;
+    P.total = plane ? 6 * P.slabs : P.slabs;
+    const bool exact = P.e.f32 && P.total > CHAIN;
+    P.chain = exact ? CHAIN : P.total;
+    const int most = exact ? MAX_EXACT : MAX_BT;
+    P.tt = (P.M + most - 1) / most;
     P.bt = (int)up((P.M + P.tt - 1) / P.tt, 16);
     P.tt = (P.M + P.bt - 1) / P.bt;
     const int64_t tiles = (int64_t)P.tt * ((P.N + BF - 1) / BF);
     if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
     P.tiles = (int)tiles;
-    P.slabs = (K + 63) / 64;
-    P.total = plane ? 6 * P.slabs : P.slabs;
     P.plane = plane;
     P.stage_bytes = W_SLAB + P.bt * 128;
     P.wait_limit = wait_limit_cycles();
@@ -532,7 +575,8 @@ cudaError_t launch_tiles(const void *x, int64_t ld_x, const void *W, int64_t ld_
         const uint32_t box[2] = {64, (uint32_t)P.bt};
         if (!make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    auto *kernel = split ? linear_kernel<true> : linear_kernel<false>;
+    auto *kernel = split ? exact ? linear_kernel<true, true> : linear_kernel<true, false>
+                         : exact ? linear_kernel<false, true> : linear_kernel<false, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -28,6 +28,7 @@ typedef unsigned long long u64;
 constexpr int THREADS = 512, WARPS = THREADS / 32, BINS = THREADS;
 constexpr int MAX_V = 1 << 18, INDEX_BITS = 18;
 constexpr int MAX_SHARE = 8;
+constexpr int FEW = 2 * THREADS, LIST = 128;  // candidates that one CTA finishes; that a warp lists
 constexpr u64 NONE = ~0ull, ONE = 1ull << 45;
 constexpr float LN2_H = 0.693147182464599609375f, LN2_L = -1.90465429995776765e-9f;  // ln 2 as a pair
 
@@ -59,8 +60,10 @@ constexpr Roots make_roots() {
 }
 __device__ const Roots kRoots = make_roots();
 
-struct Shared {
-    u64 hist[2][BINS];
+struct alignas(16) Shared {
+    u64 hist[2][BINS];           // finish_few: the sorted candidates
+    u64 few[FEW];                // candidates of all CTAs, in the cluster's first
+    u64 list[WARPS][LIST];       // a warp's candidates, by index
     float2 root[512];
     u64 warp_sum[WARPS], warp_two[WARPS];
     u64 best, low, high, sum;    // what the other CTAs read
@@ -68,13 +71,16 @@ struct Shared {
     u64 pick_base;               // of the bin that holds the bound
     int pick_bin;
     float ch, cl, yh, yl;        // log2(e) / T, -log2(min_p)
-    int first_warp;
 };
 
 __device__ __forceinline__ u64 peer_u64(const u64 *p, int rank) {
     u64 v;
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(tc::map_peer(tc::smem_u32(p), rank)) : "memory");
     return v;
+}
+// Into the cluster's first CTA.
+__device__ __forceinline__ void push_u64(const u64 *p, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(tc::map_peer(tc::smem_u32(p), 0)), "l"(v) : "memory");
 }
 __device__ __forceinline__ int peer_int(const int *p, int rank) {
     int v;
@@ -185,70 +191,83 @@ __device__ __forceinline__ int first_bin(const Row &R, float l) {
     return x >= (float)(BINS - 1) ? BINS - 1 : (int)x;
 }
 
-// The bound of the shortest run from the start, among tokens with c <= bound, whose count (or weight) reaches a target:
-// want tokens, or the share p of what all of them weigh.  Every thread of every CTA gets the same answer.
-template <bool WEIGHT>
-__device__ u64 search(const Row &R, Shared &S, u64 bound, u64 want, float p, int &turn) {
+// A bin of a histogram: its number, what lies before it, and the whole.
+struct Pick {
+    int bin;
+    u64 base, all;
+};
+
+// Adds the cluster's histograms up and finds the bin in which the sum from `base` on reaches the target: `want`, or with
+// SHARE the share p of the whole.  Every thread of every CTA gets the same answer; no such bin (bin -1): all <= want.
+template <bool SHARE>
+__device__ Pick pick_bin(const Row &R, Shared &S, const u64 *hist, u64 base, u64 want, float p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    u64 low = 0, high = 0, base = 0, target = want;
-    int shift = 0, pick = -1;  // pick: the first level's bin, until low and high are known
-    bool first = true;
+    meet();
+    u64 mine = 0;
+    for (int r = 0; r < R.share; ++r) mine += peer_u64(&hist[tid], r);
+    u64 sum = warp_scan(mine, lane);
+    if (lane == 31) S.warp_sum[warp] = sum;
+    if (tid == 0) S.pick_bin = -1;
+    __syncthreads();
+    u64 before = base, all = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += S.warp_sum[w];
+        all += S.warp_sum[w];
+    }
+    sum += before;
+    const u64 target = SHARE ? max(part_of(p, all, true), 1ull) : want;
+    if (sum >= target && sum - mine < target) {
+        S.pick_bin = tid;
+        S.pick_base = sum - mine;
+    }
+    __syncthreads();
+    return {S.pick_bin, S.pick_base, all};
+}
+
+// First level: counts or weights of the tokens with c <= bound.
+template <bool WEIGHT>
+__device__ Pick first_level(const Row &R, Shared &S, u64 bound, u64 want, float p, int &turn) {
+    u64 *hist = S.hist[turn];
+    turn ^= 1;  // the other CTAs may still read this one after the next level's meeting; the one after clears it
+    hist[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < R.n; i += THREADS) {
+        const float l = R.l[i];
+        if (!(l > -INFINITY) || (bound != NONE && order_of(l, R.first + i) > bound)) continue;
+        if (WEIGHT) {
+            float yh, yl;
+            if (!exponent(R.top, l, R.ch, R.cl, yh, yl)) continue;
+            const u64 w = weight(yh, yl, S.root);
+            if (w) atomicAdd(&hist[first_bin(R, l)], w);
+        } else {
+            atomicAdd((unsigned *)&hist[first_bin(R, l)], 1u);
+        }
+    }
+    return pick_bin<WEIGHT>(R, S, hist, 0, want, p);
+}
+
+// From the first level's bin on to one token: the last of the shortest run whose count (or weight) reaches the target.
+template <bool WEIGHT>
+__device__ u64 refine(const Row &R, Shared &S, u64 bound, Pick at, u64 target, int &turn) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    u64 low = 0, high = NONE;
+    int shift = -1;  // -1: `at` is the first level's bin
     for (;;) {
-        u64 *hist = S.hist[turn];
-        hist[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < R.n; i += THREADS) {
-            const float l = R.l[i];
-            if (!(l > -INFINITY)) continue;
-            const u64 c = order_of(l, R.first + i);
-            if (c > bound || (!first && (c < low || c > high))) continue;
-            const int bin = first ? first_bin(R, l) : (int)((c - low) >> shift);
-            if (WEIGHT) {
-                float yh, yl;
-                if (!exponent(R.top, l, R.ch, R.cl, yh, yl)) continue;
-                const u64 w = weight(yh, yl, S.root);
-                if (w) atomicAdd(&hist[bin], w);
-            } else {
-                atomicAdd((unsigned *)&hist[bin], 1u);
-            }
-        }
-        meet();
-        u64 mine = 0;
-        for (int r = 0; r < R.share; ++r) mine += peer_u64(&hist[tid], r);
-        turn ^= 1;  // the others may still read this one; it is cleared after the next cluster_sync
-        u64 sum = warp_scan(mine, lane);
-        if (lane == 31) S.warp_sum[warp] = sum;
-        __syncthreads();
-        u64 before = base, all = 0;
-        for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) before += S.warp_sum[w];
-            all += S.warp_sum[w];
-        }
-        sum += before;
-        if (first) {
-            if (WEIGHT) target = max(part_of(p, all, true), 1ull);
-            else if (all <= want) return bound;  // the same in every thread
-        }
-        if (sum >= target && sum - mine < target) {
-            S.pick_bin = tid;
-            S.pick_base = sum - mine;
-        }
-        __syncthreads();
-        pick = S.pick_bin;
-        base = S.pick_base;
         // the least and the greatest c of the bin
         u64 lo = NONE, hi = NONE;  // hi: of ~c
         for (int i = tid; i < R.n; i += THREADS) {
             const float l = R.l[i];
             if (!(l > -INFINITY)) continue;
+            if (shift < 0 && first_bin(R, l) != at.bin) continue;
             const u64 c = order_of(l, R.first + i);
-            if (c > bound || (!first && (c < low || c > high))) continue;
-            if ((first ? first_bin(R, l) : (int)((c - low) >> shift)) != pick) continue;
+            if (c > bound || c < low || c > high) continue;
+            if (shift >= 0 && (int)((c - low) >> shift) != at.bin) continue;
             lo = min(lo, c);
             hi = min(hi, ~c);
         }
         lo = warp_min(lo);
         hi = warp_min(hi);
+        __syncthreads();
         if (lane == 0) {
             S.warp_sum[warp] = lo;
             S.warp_two[warp] = hi;
@@ -270,15 +289,122 @@ __device__ u64 search(const Row &R, Shared &S, u64 bound, u64 want, float p, int
         }
         high = ~high;
         if (low >= high) return low;
-        first = false;
         shift = max(0, 64 - __clzll((long long)(high - low)) - 9);
+        u64 *hist = S.hist[turn];
+        turn ^= 1;
+        hist[tid] = 0;
+        __syncthreads();
+        for (int i = tid; i < R.n; i += THREADS) {
+            const float l = R.l[i];
+            if (!(l > -INFINITY)) continue;
+            const u64 c = order_of(l, R.first + i);
+            if (c > bound || c < low || c > high) continue;
+            if (WEIGHT) {
+                float yh, yl;
+                if (!exponent(R.top, l, R.ch, R.cl, yh, yl)) continue;
+                const u64 w = weight(yh, yl, S.root);
+                if (w) atomicAdd(&hist[(c - low) >> shift], w);
+            } else {
+                atomicAdd((unsigned *)&hist[(c - low) >> shift], 1u);
+            }
+        }
+        at = pick_bin<false>(R, S, hist, at.base, target, 0.0f);
+    }
+}
+
+// Sum of v over the threads before this one and itself, and over all.
+__device__ __forceinline__ u64 block_scan(Shared &S, u64 v, u64 &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    v = warp_scan(v, lane);
+    __syncthreads();
+    if (lane == 31) S.warp_sum[warp] = v;
+    __syncthreads();
+    u64 before = 0;
+    all = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += S.warp_sum[w];
+        all += S.warp_sum[w];
+    }
+    return before + v;
+}
+
+__device__ __forceinline__ void write_token(const SampleParams &P, int64_t row, int token, float yh, float yl, u64 all, int kept) {
+    P.token[row] = token;
+    // both terms are of one sign: nothing cancels
+    if (P.logprob) P.logprob[row] = -(fmaf(yh, LN2_H, yl * LN2_H) + log1pf((float)(all - ONE) * (1.0f / (float)ONE)));
+    if (P.kept) P.kept[row] = kept;
+}
+
+// The end of a row whose kept tokens are among n <= FEW candidates, which lie in S.few by index: one CTA sorts them,
+// cuts the run by each rule and draws.  all: what every token weighs, where there is no top-k.
+__device__ void finish_few(const SampleParams &P, const Row &R, Shared &S, int64_t row, int n, int k, float p, float m, u64 all) {
+    const int tid = threadIdx.x;
+    u64 *sorted = S.hist[0];
+    int size = 32;
+    while (size < n) size *= 2;
+    for (int i = tid; i < size; i += THREADS) sorted[i] = i < n ? S.few[i] : NONE;
+    for (int len = 2; len <= size; len *= 2)
+        for (int d = len / 2; d > 0; d /= 2) {
+            __syncthreads();
+            if (tid < size / 2) {
+                const int i = 2 * tid - (tid & (d - 1)), j = i + d;
+                const u64 a = sorted[i], b = sorted[j];
+                if ((a > b) == ((i & len) == 0)) {
+                    sorted[i] = b;
+                    sorted[j] = a;
+                }
+            }
+        }
+    if (tid == 0) S.count = 0x7fffffff;
+    __syncthreads();
+    const int run = k > 0 ? min(k, n) : n;
+    // two neighbours a thread
+    u64 w[2] = {0, 0};
+    bool under[2] = {false, false};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = 2 * tid + e;
+        if (i >= run) continue;
+        float yh, yl;
+        const bool some = exponent(R.top, logit_of(sorted[i]), R.ch, R.cl, yh, yl);
+        if (some) w[e] = weight(yh, yl, S.root);
+        under[e] = m > 0.0f && i > 0 && !(some ? (yh - S.yh) + (yl - S.yl) <= 0.0f : yh <= S.yh);
+    }
+    u64 total, cum = block_scan(S, w[0] + w[1], total);
+    if (k <= 0) total = all;
+    const u64 target = p < 1.0f ? max(part_of(p, total, true), 1ull) : NONE;
+    int keep = run;
+    if (under[1]) keep = min(keep, 2 * tid + 1);
+    if (under[0]) keep = min(keep, 2 * tid);
+    if (cum >= target) keep = min(keep, 2 * tid + 2);
+    if (cum - w[1] >= target) keep = min(keep, 2 * tid + 1);
+    if (keep < run) atomicMin(&S.count, keep);
+    __syncthreads();
+    keep = min(run, S.count);
+    const u64 bound = sorted[keep - 1];
+    float yh[2], yl[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = 2 * tid + e;
+        w[e] = 0;
+        yh[e] = yl[e] = 0.0f;
+        if (i < n && S.few[i] <= bound && exponent(R.top, logit_of(S.few[i]), R.ch, R.cl, yh[e], yl[e])) w[e] = weight(yh[e], yl[e], S.root);
+    }
+    cum = block_scan(S, w[0] + w[1], total);
+    float u = __ldg(P.u + row);
+    u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
+    const u64 at = part_of(u, total, false);
+    if (cum > at && cum - w[0] - w[1] <= at) {
+        const int e = cum - w[1] > at ? 0 : 1;
+        write_token(P, row, (int)(S.few[2 * tid + e] & (MAX_V - 1)), yh[e], yl[e], total, keep);
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constant__ SampleParams P) {
-    extern __shared__ __align__(16) float logits[];
-    __shared__ Shared S;
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    Shared &S = *(Shared *)dynamic;
+    float *logits = (float *)(dynamic + sizeof(Shared));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)tc::cluster_rank();
     const int64_t row = blockIdx.x / P.share;
@@ -345,11 +471,61 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
         __syncthreads();
     }
 
+    const int per = ((R.n + WARPS - 1) / WARPS + 31) / 32 * 32;  // a warp's tokens follow one another
+    const int w0 = min(R.n, warp * per), w1 = min(R.n, w0 + per);
+
     // ---------------- the bound ----------------
+    // One pass finds the bin in which the run ends (top-k's, else top-p's, else min-p's own); the tokens up to
+    // that bin are candidates, and few of them are finished by one CTA.
     u64 bound = NONE;
     int turn = 0;
-    if (k > 0 && k < P.V) bound = search<false>(R, S, bound, (u64)k, 0.0f, turn);
-    if (p < 1.0f) bound = search<true>(R, S, bound, 0, p, turn);
+    const bool by_k = k > 0 && k < P.V, by_p = p < 1.0f, by_m = m > 0.0f;
+    Pick at{-1, 0, 0};
+    if (by_k) at = first_level<false>(R, S, NONE, (u64)k, 0.0f, turn);
+    else if (by_p) at = first_level<true>(R, S, NONE, 0, p, turn);
+    else if (by_m) at.bin = min(BINS - 1, (int)fminf(16.0f * LN2_H * S.yh + 2.0f, (float)(BINS - 1)));
+    if (by_k && at.all <= (u64)k) at.bin = -1;  // fewer tokens than that: no bound
+    const bool cut = at.bin >= 0;
+    if (cut) {
+        int n = 0;
+        for (int i0 = w0; i0 < w1; i0 += 32) {
+            const float l = i0 + lane < w1 ? logits[i0 + lane] : -INFINITY;
+            const bool in = l > -INFINITY && first_bin(R, l) <= at.bin;
+            const unsigned hit = __ballot_sync(0xffffffffu, in);
+            const int to = n + __popc(hit & ((1u << lane) - 1));
+            if (in && to < LIST) S.list[warp][to] = order_of(l, R.first + i0 + lane);
+            n += __popc(hit);
+        }
+        if (lane == 0) S.warp_two[warp] = (u64)n;
+        __syncthreads();
+        int before = 0, mine = 0;
+        bool over = false;
+        for (int w = 0; w < WARPS; ++w) {
+            const int c = (int)S.warp_two[w];
+            if (w < warp) before += c;
+            mine += c;
+            over |= c > LIST;
+        }
+        if (tid == 0) S.count = over ? FEW + 1 : mine;
+        meet();
+        int total = 0;
+        for (int r = 0; r < P.share; ++r) {
+            const int c = peer_int(&S.count, r);
+            if (r < rank) before += c;
+            total = min(FEW + 1, total + c);
+        }
+        if (total <= FEW) {
+            for (int i = lane; i < n; i += 32) push_u64(&S.few[before + i], S.list[warp][i]);
+            meet();
+            if (rank == 0) finish_few(P, R, S, row, total, by_k ? k : 0, p, m, at.all);
+            return;
+        }
+    }
+    if (by_k && cut) bound = refine<false>(R, S, NONE, at, (u64)k, turn);
+    if (by_p) {
+        if (by_k) at = first_level<true>(R, S, bound, 0, p, turn);
+        bound = refine<true>(R, S, bound, at, max(part_of(p, at.all, true), 1ull), turn);
+    }
 
     // ---------------- the draw ----------------
     const bool floor_on = m > 0.0f;
@@ -367,8 +543,6 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
         kept = true;
         return some ? weight(yh, yl, S.root) : 0;
     };
-    const int per = ((R.n + WARPS - 1) / WARPS + 31) / 32 * 32;  // a warp's tokens follow one another
-    const int w0 = min(R.n, warp * per), w1 = min(R.n, w0 + per);
     u64 sum = 0;
     int count = 0;
     for (int i = w0 + lane; i < w1; i += 32) {
@@ -406,23 +580,17 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     }
     float u = __ldg(P.u + row);
     u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
-    const u64 at = part_of(u, all, false);
+    const u64 goal = part_of(u, all, false);
     for (int w = 0; w < warp; ++w) before += S.warp_sum[w];
-    if (before <= at && at < before + S.warp_sum[warp]) {  // the token is this warp's
+    if (before <= goal && goal < before + S.warp_sum[warp]) {  // the token is this warp's
         for (int i0 = w0; i0 < w1; i0 += 32) {
             bool kept = false;
             float yh = 0.0f, yl = 0.0f;
             const u64 w = i0 + lane < w1 ? take(i0 + lane, kept, yh, yl) : 0;
             const u64 upto = before + warp_scan(w, lane);
-            const unsigned hit = __ballot_sync(0xffffffffu, upto > at);
+            const unsigned hit = __ballot_sync(0xffffffffu, upto > goal);
             if (hit) {
-                if (lane == __ffs(hit) - 1) {
-                    P.token[row] = R.first + i0 + lane;
-                    // both terms are of one sign: nothing cancels
-                    if (P.logprob)
-                        P.logprob[row] = -(fmaf(yh, LN2_H, yl * LN2_H) + log1pf((float)(all - ONE) * (1.0f / (float)ONE)));
-                    if (P.kept) P.kept[row] = kept_all;
-                }
+                if (lane == __ffs(hit) - 1) write_token(P, row, R.first + i0 + lane, yh, yl, all, kept_all);
                 break;
             }
             before = __shfl_sync(0xffffffffu, upto, 31);
@@ -434,8 +602,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
 template <typename T>
 cudaError_t launch(const SampleParams &P, int R, cudaStream_t s) {
     auto *kernel = sample_kernel<T>;
-    const int smem = (P.slice * 4 + 15) / 16 * 16;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_V / MAX_SHARE * 4);
+    const int smem = (int)sizeof(Shared) + P.slice * 4;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared) + MAX_V / MAX_SHARE * 4);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)R * P.share);
