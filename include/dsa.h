@@ -649,8 +649,9 @@ int dsa_block_norm(const dsa_block_norm_args *args, void *stream);
  *   kept         out [R] int32: how many tokens were kept; NULL: not wanted
  * -inf and NaN are never taken (a mask): a row of nothing else gives token -1, logprob
  * -inf and kept 0.  Where a logit is +inf, those are the only ones, with equal weights.
- * Sums are of whole numbers: weights in steps of 2^-45, each off by less than 2^-42, so
- * that the order of summation is nothing and the same inputs give the same token.
+ * Sums are of whole numbers: weights in steps of 2^-45, each off by less than 2^-40 of
+ * itself and half a step, so that the order of summation is nothing and the same inputs
+ * give the same token.  The logits' differences count as far as fp32 holds them.
  * Errors: DSA_ERR_INVALID_ARG (null pointer, R < 0, V < 1, an address off its element),
  * DSA_ERR_UNSUPPORTED (dtype, V > 262144), DSA_ERR_CUDA. */
 int dsa_sample(const void *logits, int64_t ld, int dtype, int R, int V, const float *u, const float *temperature,

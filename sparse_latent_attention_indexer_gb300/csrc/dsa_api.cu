@@ -299,7 +299,7 @@ int dsa_check_device_error(void *stream, int *site) {
     // Every kernel family keeps its own error word; all of them are read and cleared, and the
     // first one that recorded a timeout gives the site.
     int (*readers[])(int *) = {indexer_tc_read_error, absorb_tc_read_error, mla_tc_read_error, gemm_tc_read_error,
-                               tree_tc_read_error, linear_read_error, selftest_read_error};
+                               tree_tc_read_error, linear_read_error, sample_read_error, selftest_read_error};
     int result = DSA_OK;
     for (auto rd : readers) {
         int s = 0;

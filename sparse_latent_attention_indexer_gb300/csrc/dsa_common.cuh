@@ -264,6 +264,7 @@ cudaError_t launch_tree_tc(const void *qt, const void *qpe, const dsa_latent_cac
 int tree_tc_read_error(int *site);
 
 int linear_read_error(int *site);
+int sample_read_error(int *site);
 
 // Bounded-wait self-test (selftest.cu): one CTA whose first wait runs out after limit_cycles.
 cudaError_t launch_bounded_wait_selftest(long long limit_cycles, int *completed_ok, cudaStream_t s);

@@ -2,35 +2,47 @@
 // random number.
 //
 // Every rule keeps a run from the start of one order, falling logit and rising index, so a row's
-// kept set is one bound in that order, and min-p a bound on the weight.  An order of 50-bit
-// numbers stands for it: c = ~(logit as an ordered integer) << 18 | index, lower is better.
+// kept set is one bound in that order.  Whole numbers of 50 bits stand for it:
+// c = ~(logit as an ordered integer) << 18 | index, lower is better.
 //
 // Which token is drawn hangs on comparisons of sums of up to 262,144 weights, so sums are exact:
 // a weight 2^-y, y = (max - l) log2(e) / T, is a whole number of steps of 2^-45, worked out from
 // pairs of fp32 values (fp64 units are few on this GPU: 2 results a cycle an SM against 128).
-// Integer sums do not depend on their order, which lets threads, CTAs and atomics add as they come.
+// Integer sums do not depend on their order, which lets threads and CTAs add as they come.
 //
-// A cluster of up to 8 CTAs keeps a row in shared memory, so HBM is read once.  Bounds are found
-// by histograms of 512 bins (counts, or weights): first over the weight's logarithm, which spreads
-// logits evenly, then over c between the least and the greatest value left in the bin, until one
-// token is left; ties end in the index, so they need no rule of their own.  Every CTA adds up all
-// CTAs' histograms and takes the same decision.
+// A cluster of up to 8 CTAs keeps a row in shared memory (one bulk copy each), so HBM is read
+// once.  What follows the maximum is to find few candidates among many tokens:
+//   * top-k: the k-th largest of the threads' own maxima (a histogram of one value a thread) is
+//     not above the k-th largest logit, so the tokens from there on hold the run;
+//   * min-p: the tokens down to that weight;
+//   * top-p: a histogram of approximate weights in bins of 1/32 of a nat, whose sums are good to
+//     2^-15, finds the bin or two in which the run ends; a pass over exact weights gives the sum
+//     before them and the whole.
+// Up to 2048 candidates are sorted by one CTA, which cuts the run (and draws, where the candidates
+// are all there is to draw from).  More of them, as many equal logits or a top_p near 1 give, go
+// another way: histograms, of counts or exact weights, over ever narrower ranges of c until one
+// token is left; ties end in the index, so they need no rule of their own.
 #include <algorithm>
 
 #include "dsa_common.cuh"
 #include "tc_common.cuh"
 
 namespace dsa {
+
+__device__ int g_sample_error = 0;
+
 namespace {
 
 typedef unsigned long long u64;
 
-constexpr int THREADS = 512, WARPS = THREADS / 32, BINS = THREADS;
+constexpr int THREADS = 512, WARPS = THREADS / 32, BINS = 2 * THREADS;
 constexpr int MAX_V = 1 << 18, INDEX_BITS = 18;
 constexpr int MAX_SHARE = 8;
-constexpr int FEW = 2 * THREADS, LIST = 128;  // candidates that one CTA finishes; that a warp lists
+constexpr int EACH = 4, FEW = EACH * THREADS, LIST = 96;  // candidates that one CTA finishes; that a warp lists
+constexpr float PER_NAT = 32.0f;              // bins
 constexpr u64 NONE = ~0ull, ONE = 1ull << 45;
 constexpr float LN2_H = 0.693147182464599609375f, LN2_L = -1.90465429995776765e-9f;  // ln 2 as a pair
+constexpr float LOG2E = 1.44269504f;
 
 struct SampleParams {
     const void *logits;
@@ -44,7 +56,7 @@ struct SampleParams {
 
 // 2^(-j/512) as pairs of fp32 values, from the nine roots of two that make up an exponent of nine bits.
 struct Roots {
-    float hi[512], lo[512];
+    float2 at[512];
 };
 constexpr Roots make_roots() {
     constexpr double root[9] = {0.9986471128909701735881, 0.9972960560854701262576, 0.9945994234836331756524, 0.9892280131939754841291, 0.9785720620877001345091, 0.9576032806985736469363, 0.9170040432046712317435, 0.8408964152537145430311, 0.7071067811865475244008};
@@ -53,45 +65,79 @@ constexpr Roots make_roots() {
         double v = 1.0;
         for (int b = 0; b < 9; ++b)
             if (j >> b & 1) v *= root[b];
-        r.hi[j] = (float)v;
-        r.lo[j] = (float)(v - (double)r.hi[j]);
+        r.at[j].x = (float)v;
+        r.at[j].y = (float)(v - (double)r.at[j].x);
     }
     return r;
 }
 __device__ const Roots kRoots = make_roots();
 
 struct alignas(16) Shared {
-    u64 hist[2][BINS];           // finish_few: the sorted candidates
+    union {
+        u64 hist[2][BINS];       // exact sums or counts
+        unsigned rough[BINS];    // approximate ones
+        u64 sorted[FEW];         // finish_few
+    };
     u64 few[FEW];                // candidates of all CTAs, in the cluster's first
     u64 list[WARPS][LIST];       // a warp's candidates, by index
     float2 root[512];
     u64 warp_sum[WARPS], warp_two[WARPS];
-    u64 best, low, high, sum;    // what the other CTAs read
-    int count;
+    // What the other CTAs and this one have found, by rank.  A CTA may push while another still reads what the last meeting
+    // brought, so what follows within one meeting has a place of its own.
+    u64 in[2][MAX_SHARE], in_draw[MAX_SHARE], bound;
+    int in_alone[MAX_SHARE], in_count[MAX_SHARE], in_kept[MAX_SHARE], in_first[MAX_SHARE];
+    float in_top[MAX_SHARE];
+    int count, first;
     u64 pick_base;               // of the bin that holds the bound
-    int pick_bin;
+    int pick_bin, pick_to;
     float ch, cl, yh, yl;        // log2(e) / T, -log2(min_p)
+    uint64_t arrived;
+    int abort_word;
 };
 
-__device__ __forceinline__ u64 peer_u64(const u64 *p, int rank) {
-    u64 v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(tc::map_peer(tc::smem_u32(p), rank)) : "memory");
-    return v;
-}
-// Into the cluster's first CTA.
-__device__ __forceinline__ void push_u64(const u64 *p, u64 v) {
-    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(tc::map_peer(tc::smem_u32(p), 0)), "l"(v) : "memory");
-}
-__device__ __forceinline__ int peer_int(const int *p, int rank) {
-    int v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(tc::map_peer(tc::smem_u32(p), rank)) : "memory");
-    return v;
-}
-
-// Every thread of the cluster, with what they have written to shared memory.
-__device__ __forceinline__ void meet() {
+// Every thread of the cluster, with what they have written to shared memory; and the same in two halves.
+__device__ __forceinline__ void meet_arrive() {
     __syncwarp();
-    tc::cluster_sync();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void meet_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void meet() {
+    meet_arrive();
+    meet_wait();
+}
+// Remote stores are sent and forgotten (meet() makes them seen), a remote load is waited for: what every CTA needs is
+// pushed, and a histogram's loads are issued together.
+__device__ __forceinline__ void push(const u64 *p, int rank, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(tc::map_peer(tc::smem_u32(p), rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void push(const int *p, int rank, int v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(tc::map_peer(tc::smem_u32(p), rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void push(const float *p, int rank, float v) { push((const int *)p, rank, __float_as_int(v)); }
+__device__ __forceinline__ void peer2(const u64 *p, int rank, u64 &a, u64 &b) {
+    asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(tc::map_peer(tc::smem_u32(p), rank)) : "memory");
+}
+__device__ __forceinline__ void peer2(const unsigned *p, int rank, unsigned &a, unsigned &b) {
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(tc::map_peer(tc::smem_u32(p), rank)) : "memory");
+}
+// This thread's two bins of all CTAs, added up as A.
+template <typename A, typename T>
+__device__ __forceinline__ void merge(const T *hist, int share, A &one, A &two) {
+    T a[MAX_SHARE], b[MAX_SHARE];
+#pragma unroll
+    for (int r = 0; r < MAX_SHARE; ++r) {
+        a[r] = b[r] = 0;
+        if (r < share) peer2(hist + 2 * threadIdx.x, r, a[r], b[r]);
+    }
+    one = two = 0;
+#pragma unroll
+    for (int r = 0; r < MAX_SHARE; ++r) {
+        one += (A)a[r];
+        two += (A)b[r];
+    }
 }
 
 __device__ __forceinline__ u64 order_of(float l, int index) { return (u64)~ordered_key(l) << INDEX_BITS | (unsigned)index; }
@@ -100,28 +146,25 @@ __device__ __forceinline__ float logit_of(u64 c) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// y = (top - l) log2(e) / T as a pair; false where the weight is below 2^-45 and counts as nothing.
+// y = (top - l) log2(e) / T as a pair; false where the weight is below 2^-46 and counts as nothing.
 __device__ __forceinline__ bool exponent(float top, float l, float ch, float cl, float &yh, float &yl) {
     const float d = __fsub_rn(top, l), b = __fsub_rn(d, top);  // the exact difference is d + e
     const float e = __fsub_rn(__fsub_rn(top, __fsub_rn(d, b)), __fadd_rn(l, b));
     yh = __fmul_rn(d, ch);
-    if (!(d < INFINITY) || !(yh < 46.0f)) return false;
     yl = fmaf(d, cl, fmaf(e, ch, fmaf(d, ch, -yh)));
-    return true;
+    return d < INFINITY && yh < 46.0f;
 }
 // 2^-y in steps of 2^-45, y = yh + yl in [0, 46].  With k = round(512 yh), k = 512 n + j, and what is left, r (exact)
-// and yl, 2^-y = 2^-n 2^-(j/512) (1 - p + p^2/2 - p^3/6), p = (r + yl) ln 2 < 2^-10.5; every term is kept to 2^-44 or better:
-// the two large ones as integers on a grid of 2^-24 and 2^-32, the rest, below 2^-21, on one of 2^-43.
+// and yl, 2^-y = 2^-n 2^-(j/512) (1 - p + p^2/2 - p^3/6), p = (r + yl) ln 2 < 2^-10.5; every term is kept to 2^-41 or
+// better: the two large ones as integers on grids of 2^-24 and 2^-32, the rest, below 2^-18, on one of 2^-40.
 __device__ __forceinline__ u64 weight(float yh, float yl, const float2 *root) {
     const float magic = 12582912.0f;  // 1.5 2^23: adding it rounds to a whole number
     const float kf = fmaf(yh, 512.0f, magic);
     const int k = __float_as_int(kf) - __float_as_int(magic);
     const float r = fmaf(__fsub_rn(kf, magic), -1.0f / 512.0f, yh);
     const float2 t = root[k & 511];
-    const float rh = __fadd_rn(r, yl), rb = __fsub_rn(rh, r);
-    const float rl = __fadd_rn(__fsub_rn(r, __fsub_rn(rh, rb)), __fsub_rn(yl, rb));  // r + yl = rh + rl
-    const float ph = __fmul_rn(rh, LN2_H);
-    const float pl = fmaf(rl, LN2_H, fmaf(rh, LN2_L, fmaf(rh, LN2_H, -ph)));
+    const float ph = __fmul_rn(r, LN2_H);
+    const float pl = fmaf(yl, LN2_H, fmaf(r, LN2_L, fmaf(r, LN2_H, -ph)));
     const float p = ph + pl;
     const float q = p * p * fmaf(p, -1.0f / 6.0f, 0.5f);
     const float a = __fmul_rn(t.x, ph);               // the first-order term, a + b
@@ -132,13 +175,19 @@ __device__ __forceinline__ u64 weight(float yh, float yl, const float2 *root) {
     const float ra = __fadd_rn(a, ma);
     const int ia = __float_as_int(ra) - __float_as_int(ma);
     s = __fsub_rn(s, __fsub_rn(a, __fsub_rn(ra, ma)));
-    const float ms = 1.5f / 1048576.0f;               // ulp 2^-43
+    const float ms = 1.5f / 131072.0f;                // ulp 2^-40
     const int is = __float_as_int(__fadd_rn(s, ms)) - __float_as_int(ms);
     const int ih = __float_as_int(t.x) - 0x3e800000;  // t.x 2^24, t.x in (1/2, 1]
-    const long long w = ((long long)ih << 19) - ((long long)ia << 11) + is;  // in steps of 2^-43
-    const int n = k >> 9;
+    const u64 w = (u64)((long long)ih * 65536 + (is - ia * 256)) << 5;
     // to the nearest step: many small weights that are all cut off would shift the sum
-    return n <= 2 ? (u64)w << (2 - n) : ((u64)w + (1ull << (n - 3))) >> (n - 2);
+    return ((w << 1 >> (k >> 9)) + 1) >> 1;
+}
+// The weight of any logit, -inf and NaN among them.
+__device__ __forceinline__ u64 weight_of(float top, float l, float ch, float cl, const float2 *root) {
+    float yh, yl;
+    const bool some = exponent(top, l, ch, cl, yh, yl);
+    const u64 w = weight(some ? yh : 0.0f, some ? yl : 0.0f, root);
+    return some ? w : 0;
 }
 
 // floor(f w), or the next whole number where it is not whole: f in [0, 1), w < 2^63.
@@ -178,18 +227,19 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
     return v;
 }
 
+// A CTA's part of a row.
+template <typename T>
 struct Row {
-    const float *l;        // the CTA's logits
+    const T *raw;          // the logits, as they come
     int first, n;          // index of the first, how many
     int rank, share;
-    float top, ch, cl, bins;  // bins: level-1 bins per unit of logit
-};
+    float top, ch, cl, bins;  // bins: bins per unit of logit
 
-// Bin of the first level: falls with the logit, the same for equal ones.
-__device__ __forceinline__ int first_bin(const Row &R, float l) {
-    const float x = (R.top - l) * R.bins;
-    return x >= (float)(BINS - 1) ? BINS - 1 : (int)x;
-}
+    __device__ __forceinline__ float at(int i) const { return to_f32(raw[i]); }
+    // Bins fall with the logit; equal logits have equal ones.  A token is in bin b or before: x < b + 1.
+    __device__ __forceinline__ float x(float l) const { return (top - l) * bins; }
+    __device__ __forceinline__ int bin(float l) const { return (int)fminf(x(l), (float)(BINS - 1)); }
+};
 
 // A bin of a histogram: its number, what lies before it, and the whole.
 struct Pick {
@@ -198,57 +248,58 @@ struct Pick {
 };
 
 // Adds the cluster's histograms up and finds the bin in which the sum from `base` on reaches the target: `want`, or with
-// SHARE the share p of the whole.  Every thread of every CTA gets the same answer; no such bin (bin -1): all <= want.
+// SHARE the share p of the whole.  Every thread of every CTA gets the same answer; no such bin (bin -1): all < want.
 template <bool SHARE>
-__device__ Pick pick_bin(const Row &R, Shared &S, const u64 *hist, u64 base, u64 want, float p) {
+__device__ Pick pick_bin(int share, Shared &S, const u64 *hist, u64 base, u64 want, float p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     meet();
-    u64 mine = 0;
-    for (int r = 0; r < R.share; ++r) mine += peer_u64(&hist[tid], r);
-    u64 sum = warp_scan(mine, lane);
+    u64 one, two;
+    merge(hist, share, one, two);
+    u64 sum = warp_scan(one + two, lane);
     if (lane == 31) S.warp_sum[warp] = sum;
     if (tid == 0) S.pick_bin = -1;
     __syncthreads();
     u64 before = base, all = 0;
+#pragma unroll
     for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += S.warp_sum[w];
         all += S.warp_sum[w];
     }
     sum += before;
     const u64 target = SHARE ? max(part_of(p, all, true), 1ull) : want;
-    if (sum >= target && sum - mine < target) {
-        S.pick_bin = tid;
-        S.pick_base = sum - mine;
+    if (sum >= target && sum - one - two < target) {
+        const bool second = sum - two < target;
+        S.pick_bin = 2 * tid + second;
+        S.pick_base = second ? sum - two : sum - two - one;
     }
     __syncthreads();
     return {S.pick_bin, S.pick_base, all};
 }
 
-// First level: counts or weights of the tokens with c <= bound.
-template <bool WEIGHT>
-__device__ Pick first_level(const Row &R, Shared &S, u64 bound, u64 want, float p, int &turn) {
+// Counts or weights of the tokens with c <= bound over the whole range.
+template <bool WEIGHT, typename T>
+__device__ Pick first_level(const Row<T> &R, Shared &S, u64 bound, u64 want, float p, int &turn) {
     u64 *hist = S.hist[turn];
-    turn ^= 1;  // the other CTAs may still read this one after the next level's meeting; the one after clears it
-    hist[threadIdx.x] = 0;
+    turn ^= 1;  // the other CTAs may still read this one until the next level's meeting; the level after clears it
+    __syncthreads();
+    for (int b = threadIdx.x; b < BINS; b += THREADS) hist[b] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < R.n; i += THREADS) {
-        const float l = R.l[i];
+        const float l = R.at(i);
         if (!(l > -INFINITY) || (bound != NONE && order_of(l, R.first + i) > bound)) continue;
         if (WEIGHT) {
-            float yh, yl;
-            if (!exponent(R.top, l, R.ch, R.cl, yh, yl)) continue;
-            const u64 w = weight(yh, yl, S.root);
-            if (w) atomicAdd(&hist[first_bin(R, l)], w);
+            const u64 w = weight_of(R.top, l, R.ch, R.cl, S.root);
+            if (w) atomicAdd(&hist[R.bin(l)], w);
         } else {
-            atomicAdd((unsigned *)&hist[first_bin(R, l)], 1u);
+            atomicAdd((unsigned *)&hist[R.bin(l)], 1u);
         }
     }
-    return pick_bin<WEIGHT>(R, S, hist, 0, want, p);
+    return pick_bin<WEIGHT>(R.share, S, hist, 0, want, p);
 }
 
 // From the first level's bin on to one token: the last of the shortest run whose count (or weight) reaches the target.
-template <bool WEIGHT>
-__device__ u64 refine(const Row &R, Shared &S, u64 bound, Pick at, u64 target, int &turn) {
+template <bool WEIGHT, typename T>
+__device__ u64 refine(const Row<T> &R, Shared &S, u64 bound, Pick at, u64 target, int &turn) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     u64 low = 0, high = NONE;
     int shift = -1;  // -1: `at` is the first level's bin
@@ -256,9 +307,9 @@ __device__ u64 refine(const Row &R, Shared &S, u64 bound, Pick at, u64 target, i
         // the least and the greatest c of the bin
         u64 lo = NONE, hi = NONE;  // hi: of ~c
         for (int i = tid; i < R.n; i += THREADS) {
-            const float l = R.l[i];
+            const float l = R.at(i);
             if (!(l > -INFINITY)) continue;
-            if (shift < 0 && first_bin(R, l) != at.bin) continue;
+            if (shift < 0 && R.bin(l) != at.bin) continue;
             const u64 c = order_of(l, R.first + i);
             if (c > bound || c < low || c > high) continue;
             if (shift >= 0 && (int)((c - low) >> shift) != at.bin) continue;
@@ -276,43 +327,41 @@ __device__ u64 refine(const Row &R, Shared &S, u64 bound, Pick at, u64 target, i
         if (warp == 0) {
             lo = warp_min(lane < WARPS ? S.warp_sum[lane] : NONE);
             hi = warp_min(lane < WARPS ? S.warp_two[lane] : NONE);
-            if (lane == 0) {
-                S.low = lo;
-                S.high = hi;
+            if (lane < R.share) {
+                push(&S.in[0][R.rank], lane, lo);
+                push(&S.in[1][R.rank], lane, hi);
             }
         }
         meet();
         low = high = NONE;
         for (int r = 0; r < R.share; ++r) {
-            low = min(low, peer_u64(&S.low, r));
-            high = min(high, peer_u64(&S.high, r));
+            low = min(low, S.in[0][r]);
+            high = min(high, S.in[1][r]);
         }
         high = ~high;
         if (low >= high) return low;
-        shift = max(0, 64 - __clzll((long long)(high - low)) - 9);
+        shift = max(0, 64 - __clzll((long long)(high - low)) - 10);  // (high - low) >> shift < BINS
         u64 *hist = S.hist[turn];
         turn ^= 1;
-        hist[tid] = 0;
+        for (int b = tid; b < BINS; b += THREADS) hist[b] = 0;
         __syncthreads();
         for (int i = tid; i < R.n; i += THREADS) {
-            const float l = R.l[i];
+            const float l = R.at(i);
             if (!(l > -INFINITY)) continue;
             const u64 c = order_of(l, R.first + i);
             if (c > bound || c < low || c > high) continue;
             if (WEIGHT) {
-                float yh, yl;
-                if (!exponent(R.top, l, R.ch, R.cl, yh, yl)) continue;
-                const u64 w = weight(yh, yl, S.root);
+                const u64 w = weight_of(R.top, l, R.ch, R.cl, S.root);
                 if (w) atomicAdd(&hist[(c - low) >> shift], w);
             } else {
                 atomicAdd((unsigned *)&hist[(c - low) >> shift], 1u);
             }
         }
-        at = pick_bin<false>(R, S, hist, at.base, target, 0.0f);
+        at = pick_bin<false>(R.share, S, hist, at.base, target, 0.0f);
     }
 }
 
-// Sum of v over the threads before this one and itself, and over all.
+// Sum of v over the threads up to this one, and over all.
 __device__ __forceinline__ u64 block_scan(Shared &S, u64 v, u64 &all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     v = warp_scan(v, lane);
@@ -321,6 +370,7 @@ __device__ __forceinline__ u64 block_scan(Shared &S, u64 v, u64 &all) {
     __syncthreads();
     u64 before = 0;
     all = 0;
+#pragma unroll
     for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += S.warp_sum[w];
         all += S.warp_sum[w];
@@ -328,6 +378,10 @@ __device__ __forceinline__ u64 block_scan(Shared &S, u64 v, u64 &all) {
     return before + v;
 }
 
+__device__ __forceinline__ float random_of(const SampleParams &P, int64_t row) {
+    const float u = __ldg(P.u + row);
+    return u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
+}
 __device__ __forceinline__ void write_token(const SampleParams &P, int64_t row, int token, float yh, float yl, u64 all, int kept) {
     P.token[row] = token;
     // both terms are of one sign: nothing cancels
@@ -335,252 +389,515 @@ __device__ __forceinline__ void write_token(const SampleParams &P, int64_t row, 
     if (P.kept) P.kept[row] = kept;
 }
 
-// The end of a row whose kept tokens are among n <= FEW candidates, which lie in S.few by index: one CTA sorts them,
-// cuts the run by each rule and draws.  all: what every token weighs, where there is no top-k.
-__device__ void finish_few(const SampleParams &P, const Row &R, Shared &S, int64_t row, int n, int k, float p, float m, u64 all) {
+// How many tokens the CTA's warps have listed (above FEW: more than a list holds, or more than `most`), and how many of them
+// come before this warp's.
+__device__ __forceinline__ int count_listed(Shared &S, int listed, int most, int &before) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncthreads();
+    if (lane == 0) S.warp_two[warp] = (u64)listed;
+    __syncthreads();
+    const int c = lane < WARPS ? (int)S.warp_two[lane] : 0;
+    const bool over = __any_sync(0xffffffffu, c > LIST);
+    before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+    const int all = __reduce_add_sync(0xffffffffu, c);
+    __syncthreads();
+    return over || all > most ? FEW + 1 : all;
+}
+
+// Sorts n <= FEW candidates into S.sorted (best first); they lie in S.few by index, rank r's S.in_alone[r] from region r on
+// (0: one after another).
+__device__ void sort_few(Shared &S, int n, int region, int share) {
     const int tid = threadIdx.x;
-    u64 *sorted = S.hist[0];
     int size = 32;
     while (size < n) size *= 2;
-    for (int i = tid; i < size; i += THREADS) sorted[i] = i < n ? S.few[i] : NONE;
+    __syncthreads();
+    for (int i = n + tid; i < size; i += THREADS) S.sorted[i] = NONE;
+    if (region == 0) {
+        for (int i = tid; i < n; i += THREADS) S.sorted[i] = S.few[i];
+    } else {
+        for (int r = 0, to = 0; r < share; to += S.in_alone[r++])
+            for (int i = tid; i < S.in_alone[r]; i += THREADS) S.sorted[to + i] = S.few[r * region + i];
+    }
     for (int len = 2; len <= size; len *= 2)
         for (int d = len / 2; d > 0; d /= 2) {
             __syncthreads();
-            if (tid < size / 2) {
-                const int i = 2 * tid - (tid & (d - 1)), j = i + d;
-                const u64 a = sorted[i], b = sorted[j];
+            for (int t = tid; t < size / 2; t += THREADS) {
+                const int i = 2 * t - (t & (d - 1)), j = i + d;
+                const u64 a = S.sorted[i], b = S.sorted[j];
                 if ((a > b) == ((i & len) == 0)) {
-                    sorted[i] = b;
-                    sorted[j] = a;
+                    S.sorted[i] = b;
+                    S.sorted[j] = a;
                 }
             }
         }
     if (tid == 0) S.count = 0x7fffffff;
     __syncthreads();
+}
+
+// The end of a row whose kept tokens are among n <= FEW candidates, which lie in S.few by index: one CTA sorts them,
+// cuts the run by each rule and draws.  all: what every token weighs, where there is no top-k.  With regions, S.few holds
+// NONE where there is no candidate.
+template <typename T>
+__device__ void finish_few(const SampleParams &P, const Row<T> &R, Shared &S, int64_t row, int n, int region, int k, float p, float m,
+                           u64 all) {
+    const int first = EACH * threadIdx.x;  // neighbours a thread
+    sort_few(S, n, region, R.share);
     const int run = k > 0 ? min(k, n) : n;
-    // two neighbours a thread
-    u64 w[2] = {0, 0};
-    bool under[2] = {false, false};
+    u64 w[EACH], mine = 0;
+    int keep = run;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int i = 2 * tid + e;
-        if (i >= run) continue;
+    for (int e = 0; e < EACH; ++e) {
+        w[e] = 0;
+        if (first + e >= run) continue;
         float yh, yl;
-        const bool some = exponent(R.top, logit_of(sorted[i]), R.ch, R.cl, yh, yl);
+        const bool some = exponent(R.top, logit_of(S.sorted[first + e]), R.ch, R.cl, yh, yl);
         if (some) w[e] = weight(yh, yl, S.root);
-        under[e] = m > 0.0f && i > 0 && !(some ? (yh - S.yh) + (yl - S.yl) <= 0.0f : yh <= S.yh);
+        mine += w[e];
+        if (m > 0.0f && first + e > 0 && !(some ? (yh - S.yh) + (yl - S.yl) <= 0.0f : yh <= S.yh)) keep = min(keep, first + e);
     }
-    u64 total, cum = block_scan(S, w[0] + w[1], total);
+    u64 total, cum = block_scan(S, mine, total) - mine;
     if (k <= 0) total = all;
     const u64 target = p < 1.0f ? max(part_of(p, total, true), 1ull) : NONE;
-    int keep = run;
-    if (under[1]) keep = min(keep, 2 * tid + 1);
-    if (under[0]) keep = min(keep, 2 * tid);
-    if (cum >= target) keep = min(keep, 2 * tid + 2);
-    if (cum - w[1] >= target) keep = min(keep, 2 * tid + 1);
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        cum += w[e];
+        if (cum >= target) keep = min(keep, first + e + 1);
+    }
     if (keep < run) atomicMin(&S.count, keep);
     __syncthreads();
     keep = min(run, S.count);
-    const u64 bound = sorted[keep - 1];
-    float yh[2], yl[2];
+    const u64 bound = S.sorted[keep - 1];
+    float yh[EACH], yl[EACH];
+    mine = 0;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int i = 2 * tid + e;
+    for (int e = 0; e < EACH; ++e) {
+        const int i = first + e;
         w[e] = 0;
         yh[e] = yl[e] = 0.0f;
-        if (i < n && S.few[i] <= bound && exponent(R.top, logit_of(S.few[i]), R.ch, R.cl, yh[e], yl[e])) w[e] = weight(yh[e], yl[e], S.root);
+        if ((region || i < n) && S.few[i] <= bound && exponent(R.top, logit_of(S.few[i]), R.ch, R.cl, yh[e], yl[e])) w[e] = weight(yh[e], yl[e], S.root);
+        mine += w[e];
     }
-    cum = block_scan(S, w[0] + w[1], total);
-    float u = __ldg(P.u + row);
-    u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
-    const u64 at = part_of(u, total, false);
-    if (cum > at && cum - w[0] - w[1] <= at) {
-        const int e = cum - w[1] > at ? 0 : 1;
-        write_token(P, row, (int)(S.few[2 * tid + e] & (MAX_V - 1)), yh[e], yl[e], total, keep);
+    cum = block_scan(S, mine, total) - mine;
+    const u64 goal = part_of(random_of(P, row), total, false);
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        if (cum <= goal && cum + w[e] > goal) write_token(P, row, (int)(S.few[first + e] & (MAX_V - 1)), yh[e], yl[e], total, keep);
+        cum += w[e];
     }
+}
+
+// The CTA's logits into shared memory, element i at raw[i]: whole 16 bytes by one bulk copy, what lies before and after
+// them by itself.
+template <typename T>
+__device__ T *fetch_slice(Shared &S, uint8_t *room, const T *src, int n, bool &coming) {
+    const int off = (int)((uintptr_t)src & 15);
+    T *raw = (T *)(room + off);
+    const int head = min(n, (16 - off) % 16 / (int)sizeof(T)), body = (n - head) * (int)sizeof(T) / 16 * 16;
+    const int tail = head + body / (int)sizeof(T);
+    coming = body > 0;
+    if (threadIdx.x == 0) {
+        tc::mbar_init(&S.arrived, 1);
+        S.abort_word = 0;
+        tc::fence_mbar_init();
+        if (body) {
+            tc::mbar_arrive_expect_tx(&S.arrived, body);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             tc::smem_u32(raw + head)),
+                         "l"(src + head), "r"(body), "r"(tc::smem_u32(&S.arrived))
+                         : "memory");
+        }
+    }
+    if (threadIdx.x >= 32) {
+        const int i = threadIdx.x - 32;
+        if (i < head) raw[i] = src[i];
+        if (i < n - tail) raw[tail + i] = src[tail + i];
+    }
+    return raw;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constant__ SampleParams P) {
     extern __shared__ __align__(16) uint8_t dynamic[];
     Shared &S = *(Shared *)dynamic;
-    float *logits = (float *)(dynamic + sizeof(Shared));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)tc::cluster_rank();
     const int64_t row = blockIdx.x / P.share;
-    Row R;
-    R.l = logits;
+    Row<T> R;
     R.rank = rank;
     R.share = P.share;
     R.first = min(P.V, rank * P.slice);
     R.n = min(P.V, R.first + P.slice) - R.first;
+    if (rank == 0)
+        for (int i = tid; i < FEW; i += THREADS) S.few[i] = NONE;
+    meet_arrive();  // waited for before anything is pushed: the other CTAs have started
+    pdl_wait();     // the set-up above overlapped the previous kernel
+    bool coming;
+    T *raw = fetch_slice(S, dynamic + sizeof(Shared), (const T *)P.logits + row * P.ld + R.first, R.n, coming);
+    R.raw = raw;
 
     const float T_ = P.temperature ? __ldg(P.temperature + row) : 1.0f;
-    const bool greedy = !((double)T_ >= 1e-5);
     const float p = P.top_p ? __ldg(P.top_p + row) : 1.0f, m = P.min_p ? __ldg(P.min_p + row) : 0.0f;
-    const int k = greedy ? 1 : P.top_k ? __ldg(P.top_k + row) : 0;
-    if (tid == THREADS - 1 && !greedy) {
+    // the first token alone: no temperature, no share, or a weight that no other reaches
+    const bool one = !((double)T_ >= 1e-5) || p <= 0.0f || m > 1.0f;
+    const int k = one ? 1 : P.top_k ? __ldg(P.top_k + row) : 0;
+    const bool by_k = k > 0 && k < P.V, by_p = p < 1.0f, by_m = m > 0.0f;
+    if (tid == THREADS - 1 && k != 1) {
         const double c = 1.4426950408889634074 / (double)T_;
         S.ch = (float)c;
         S.cl = (float)(c - (double)S.ch);
-        const double y = m > 0.0f ? -log2((double)m) : 0.0;
+        const double y = by_m ? -log2((double)m) : 0.0;
         S.yh = (float)y;
         S.yl = (float)(y - (double)S.yh);
     }
-    for (int j = tid; j < 512; j += THREADS) S.root[j] = make_float2(kRoots.hi[j], kRoots.lo[j]);
-
-    // ---------------- the row, and the first of the order ----------------
-    const T *src = (const T *)P.logits + row * P.ld + R.first;
-    u64 best = NONE;
-#pragma unroll 8
-    for (int i = tid; i < R.n; i += THREADS) {
-        float l = to_f32(src[i]);
-        if (!(l > -INFINITY)) l = -INFINITY;  // NaN too
-        else best = min(best, order_of(l, R.first + i));
-        logits[i] = l;
-    }
-    best = warp_min(best);
-    if (lane == 0) S.warp_sum[warp] = best;
+    for (int j = tid; j < 512; j += THREADS) S.root[j] = kRoots.at[j];
+    if (tid == 0) S.first = MAX_V;
     __syncthreads();
-    if (warp == 0) {
-        best = warp_min(lane < WARPS ? S.warp_sum[lane] : NONE);
-        if (lane == 0) S.best = best;
-    }
-    meet();
-    best = NONE;
-    for (int r = 0; r < P.share; ++r) best = min(best, peer_u64(&S.best, r));
-
-    const bool none = best == NONE, one = !none && k == 1;
-    if (none || one) {  // the same in every thread of the cluster
-        if (rank == 0 && tid == 0) {
-            P.token[row] = none ? -1 : (int)(best & (MAX_V - 1));
-            if (P.logprob) P.logprob[row] = none ? -INFINITY : 0.0f;
-            if (P.kept) P.kept[row] = none ? 0 : 1;
-        }
-        meet();  // nobody leaves while the others read
-        return;
-    }
-    R.top = logit_of(best);
-    R.ch = S.ch;
-    R.cl = S.cl;
-    R.bins = 16.0f / T_;  // bins a sixteenth of a nat wide
-    if (R.top == INFINITY) {  // the infinite ones alone, as equals
-        for (int i = tid; i < R.n; i += THREADS) logits[i] = logits[i] == INFINITY ? 0.0f : -INFINITY;
-        R.top = 0.0f;
-        best = order_of(0.0f, (int)(best & (MAX_V - 1)));
-        __syncthreads();
-    }
-
+    if (coming) tc::mbar_wait(&S.arrived, 0, (volatile int *)&S.abort_word, &g_sample_error, 71);
     const int per = ((R.n + WARPS - 1) / WARPS + 31) / 32 * 32;  // a warp's tokens follow one another
     const int w0 = min(R.n, warp * per), w1 = min(R.n, w0 + per);
+    R.bins = PER_NAT / T_;
 
-    // ---------------- the bound ----------------
-    // One pass finds the bin in which the run ends (top-k's, else top-p's, else min-p's own); the tokens up to
-    // that bin are candidates, and few of them are finished by one CTA.
-    u64 bound = NONE;
-    int turn = 0;
-    const bool by_k = k > 0 && k < P.V, by_p = p < 1.0f, by_m = m > 0.0f;
-    Pick at{-1, 0, 0};
-    if (by_k) at = first_level<false>(R, S, NONE, (u64)k, 0.0f, turn);
-    else if (by_p) at = first_level<true>(R, S, NONE, 0, p, turn);
-    else if (by_m) at.bin = min(BINS - 1, (int)fminf(16.0f * LN2_H * S.yh + 2.0f, (float)(BINS - 1)));
-    if (by_k && at.all <= (u64)k) at.bin = -1;  // fewer tokens than that: no bound
-    const bool cut = at.bin >= 0;
-    if (cut) {
-        int n = 0;
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-            const float l = i0 + lane < w1 ? logits[i0 + lane] : -INFINITY;
-            const bool in = l > -INFINITY && first_bin(R, l) <= at.bin;
-            const unsigned hit = __ballot_sync(0xffffffffu, in);
-            const int to = n + __popc(hit & ((1u << lane) - 1));
-            if (in && to < LIST) S.list[warp][to] = order_of(l, R.first + i0 + lane);
-            n += __popc(hit);
-        }
-        if (lane == 0) S.warp_two[warp] = (u64)n;
+    // ---------------- the maximum ----------------
+    float mine = -INFINITY;  // of this thread's tokens; a NaN counts as nothing
+#pragma unroll 8
+    for (int i = tid; i < R.n; i += THREADS) mine = fmaxf(mine, R.at(i));
+    {
+        const u64 w = warp_min((u64)~ordered_key(mine));
+        if (lane == 0) S.warp_sum[warp] = w;
         __syncthreads();
-        int before = 0, mine = 0;
-        bool over = false;
-        for (int w = 0; w < WARPS; ++w) {
-            const int c = (int)S.warp_two[w];
-            if (w < warp) before += c;
-            mine += c;
-            over |= c > LIST;
+        const u64 b = warp_min(lane < WARPS ? S.warp_sum[lane] : NONE);
+        R.top = logit_of(b << INDEX_BITS);  // the CTA's
+    }
+
+    // The tokens of the bins up to `to` (no more than `most` of them, or the answer is above FEW), in S.list by warp; and where
+    // this warp's go among them.
+    const auto list_up_to = [&](int to, int most, int &listed, int &before) -> int {
+        listed = 0;
+        const float xt = (float)to + 1.0f;
+        for (int i0 = w0; i0 < w1; i0 += 128) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + e * 32 + lane;
+                const float l = i < w1 ? R.at(i) : -INFINITY;
+                const bool in = l > -INFINITY && (R.x(l) < xt || to == BINS - 1);
+                const unsigned hit = __ballot_sync(0xffffffffu, in);
+                if (hit == 0) continue;
+                const int at = listed + __popc(hit & ((1u << lane) - 1));
+                if (in && at < LIST) S.list[warp][at] = order_of(l, R.first + i);
+                listed += __popc(hit);
+            }
         }
-        if (tid == 0) S.count = over ? FEW + 1 : mine;
+        return count_listed(S, listed, most, before);
+    };
+    // The bin up to which at least `want` of the threads' maxima lie (the last one, if there are not so many), from their
+    // histogram over one CTA or all.
+    const auto pick_maxima = [&](u64 one_, u64 two, u64 want) -> int {
+        u64 all;
+        const u64 sum = block_scan(S, one_ + two, all);
+        if (tid == 0) S.pick_bin = BINS - 1;
+        __syncthreads();
+        if (sum >= want && sum - one_ - two < want) S.pick_bin = 2 * tid + (sum - two < want);
+        __syncthreads();
+        return S.pick_bin;
+    };
+    const auto maxima = [&]() {
+        for (int b = tid; b < BINS; b += THREADS) S.rough[b] = 0;
+        __syncthreads();
+        if (mine > -INFINITY) atomicAdd(&S.rough[R.bin(mine)], 1u);
+    };
+
+    // ---------------- a CTA's own candidates ----------------
+    // A token of the row's first k is one of its CTA's first k, and one near the row's maximum is nearer to its CTA's: with
+    // a small k, or min-p alone, the CTAs list what they have and meet once.
+    const int region = FEW / P.share;
+    const bool alone = k != 1 && ((by_k && k <= min(region * 2 / 3, THREADS / 2)) || (by_m && !by_k && !by_p));
+    if (alone) {
+        int to, listed = 0, before = 0, count = FEW + 1;
+        if (R.top < INFINITY) {
+            if (by_k) {
+                maxima();
+                __syncthreads();
+                to = pick_maxima(S.rough[2 * tid], S.rough[2 * tid + 1], (u64)k);
+            } else {
+                to = (int)fminf(PER_NAT * LN2_H * S.yh + 2.0f, (float)(BINS - 1));  // rounding moves a token by less than a bin
+            }
+            count = list_up_to(to, region, listed, before);
+        }
+        meet_wait();
+        if (tid < P.share) {
+            push(&S.in_top[rank], tid, R.top);
+            push(&S.in_alone[rank], tid, count);
+        }
+        if (count <= region)
+            for (int i = lane; i < listed; i += 32) push(&S.few[rank * region + before + i], 0, S.list[warp][i]);
         meet();
         int total = 0;
         for (int r = 0; r < P.share; ++r) {
-            const int c = peer_int(&S.count, r);
-            if (r < rank) before += c;
-            total = min(FEW + 1, total + c);
+            R.top = fmaxf(R.top, S.in_top[r]);
+            total = max(total, S.in_alone[r]);
         }
-        if (total <= FEW) {
-            for (int i = lane; i < n; i += 32) push_u64(&S.few[before + i], S.list[warp][i]);
-            meet();
-            if (rank == 0) finish_few(P, R, S, row, total, by_k ? k : 0, p, m, at.all);
+        if (total <= region && R.top > -INFINITY) {
+            if (rank == 0) {
+                total = 0;
+                for (int r = 0; r < P.share; ++r) total += S.in_alone[r];
+                R.ch = S.ch;
+                R.cl = S.cl;
+                finish_few(P, R, S, row, total, region, by_k ? k : 0, p, m, 0);
+            }
             return;
         }
+    } else {
+        meet_wait();
+        if (tid < P.share) push(&S.in_top[rank], tid, R.top);
+        meet();
+        for (int r = 0; r < P.share; ++r) R.top = fmaxf(R.top, S.in_top[r]);
     }
-    if (by_k && cut) bound = refine<false>(R, S, NONE, at, (u64)k, turn);
-    if (by_p) {
-        if (by_k) at = first_level<true>(R, S, bound, 0, p, turn);
-        bound = refine<true>(R, S, bound, at, max(part_of(p, at.all, true), 1ull), turn);
+
+    // ---------------- the first token, or none ----------------
+    if (R.top == -INFINITY || k == 1) {  // the same in every thread of the cluster
+        if (R.top > -INFINITY && mine == R.top)
+            for (int i = tid; i < R.n; i += THREADS)
+                if (R.at(i) == R.top) {
+                    atomicMin(&S.first, R.first + i);
+                    break;
+                }
+        __syncthreads();
+        if (tid == 0) push(&S.in_first[rank], 0, S.first);
+        meet();
+        if (rank == 0 && tid == 0) {
+            const bool none = R.top == -INFINITY;
+            int first = MAX_V;
+            for (int r = 0; r < P.share; ++r) first = min(first, S.in_first[r]);
+            P.token[row] = none ? -1 : first;
+            if (P.logprob) P.logprob[row] = none ? -INFINITY : 0.0f;
+            if (P.kept) P.kept[row] = none ? 0 : 1;
+        }
+        return;
+    }
+    R.ch = S.ch;
+    R.cl = S.cl;
+    if (R.top == INFINITY) {  // the infinite ones alone, as equals
+        __syncthreads();
+        for (int i = tid; i < R.n; i += THREADS) raw[i] = from_f32<T>(R.at(i) == INFINITY ? 0.0f : -INFINITY);
+        mine = mine == INFINITY ? 0.0f : -INFINITY;
+        R.top = 0.0f;
+        __syncthreads();
+    }
+
+    // ---------------- where the run ends ----------------
+    u64 bound = NONE;
+    int turn = 0;
+    // bins: the tokens before `from` are kept for certain, those behind `to` are not
+    int from = 0, to = BINS;
+    if (by_k) {
+        // as many of the threads' maxima as tokens are wanted lie in the bins up to `to`: so do as many tokens
+        maxima();
+        meet();
+        u64 one_, two;
+        merge(S.rough, P.share, one_, two);
+        to = pick_maxima(one_, two, (u64)k);
+    } else if (by_m) {
+        to = (int)fminf(PER_NAT * LN2_H * S.yh + 2.0f, (float)(BINS - 1));  // rounding moves a token by less than a bin
+    } else if (by_p) {
+        // The weight of a bin is that of its start times a sum of factors in (e^(-1/32), 1], each to 2^-17 (a CTA
+        // has at most 2^15 tokens).
+        for (int b = tid; b < BINS; b += THREADS) S.rough[b] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int i = tid; i < R.n; i += THREADS) {
+            const float l = R.at(i), x = R.x(l);
+            if (!(l > -INFINITY) || x >= (float)(BINS - 1)) continue;
+            const int b = (int)x;
+            atomicAdd(&S.rough[b], (unsigned)fmaf(65536.0f, tc::ex2_approx(((float)b - x) * (LOG2E / PER_NAT)), 0.5f));
+        }
+        meet();
+        float one_, two;
+        merge(S.rough, P.share, one_, two);
+        one_ *= tc::ex2_approx((float)(2 * tid) * (-LOG2E / PER_NAT));
+        two *= tc::ex2_approx((float)(2 * tid + 1) * (-LOG2E / PER_NAT));
+        float sum = one_ + two;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float a = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += a;
+        }
+        __syncthreads();
+        if (lane == 31) S.warp_sum[warp] = (u64)__float_as_uint(sum);
+        if (tid == 0) S.pick_bin = S.pick_to = BINS - 1;
+        __syncthreads();
+        float before = 0.0f, all = 0.0f;
+        for (int w = 0; w < WARPS; ++w) {
+            const float a = __uint_as_float((unsigned)S.warp_sum[w]);
+            if (w < warp) before += a;
+            all += a;
+        }
+        sum += before;
+        // Sums are off by less than 2^-15 of themselves: x and the bins' starts by 2^-17 (arguments near 46 in 24 bits),
+        // the factors by 2^-17; the tokens 32 nats down, left out, weigh less than 2^-28 in all.
+        const float slack = 1.0f / 16384.0f, least = p * all * (1.0f - slack), most = p * all * (1.0f + slack);
+        if (sum >= least) atomicMin(&S.pick_bin, sum - two >= least ? 2 * tid : 2 * tid + 1);
+        if (sum >= most) atomicMin(&S.pick_to, sum - two >= most ? 2 * tid : 2 * tid + 1);
+        __syncthreads();
+        from = S.pick_bin;
+        to = S.pick_to;
+    }
+
+    // ---------------- candidates, and exact sums ----------------
+    // w_all: what the warp's tokens weigh (top-p needs it of all, a draw from all of them too); w_sure: of those before `from`
+    u64 w_all = 0, w_sure = 0;
+    int sure = 0, listed = 0;
+    bool by_few = false;
+    const bool weigh = !by_k && (by_p || !by_m), list = to < BINS;
+    if (weigh) {
+        const float xt = (float)to + 1.0f;
+        for (int i0 = w0; i0 < w1; i0 += 64) {
+            float l[2];
+            u64 w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = i0 + e * 32 + lane;
+                l[e] = i < w1 ? R.at(i) : -INFINITY;
+                w[e] = weight_of(R.top, l[e], R.ch, R.cl, S.root);
+            }
+            w_all += w[0] + w[1];
+            if (!list) {
+                sure += (l[0] > -INFINITY) + (l[1] > -INFINITY);
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x = R.x(l[e]);
+                const bool live = l[e] > -INFINITY, before = live && (int)fminf(x, (float)(BINS - 1)) < from;
+                if (before) {
+                    w_sure += w[e];
+                    ++sure;
+                }
+                const bool in = live && !before && (x < xt || to == BINS - 1);
+                const unsigned hit = __ballot_sync(0xffffffffu, in);
+                const int at = listed + __popc(hit & ((1u << lane) - 1));
+                if (in && at < LIST) S.list[warp][at] = order_of(l[e], R.first + i0 + e * 32 + lane);
+                listed += __popc(hit);
+            }
+        }
+    }
+    u64 all = 0, sure_all = 0;  // of the cluster
+    if (list) {
+        const u64 a = warp_sum(w_all), b = warp_sum(w_sure);
+        int before, count = weigh ? count_listed(S, listed, FEW, before) : list_up_to(to, FEW, listed, before);
+        if (lane == 0) {
+            S.warp_sum[warp] = a;
+            S.warp_two[warp] = b;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const u64 x = warp_sum(lane < WARPS ? S.warp_sum[lane] : 0), y = warp_sum(lane < WARPS ? S.warp_two[lane] : 0);
+            if (lane < P.share) {
+                push(&S.in[0][rank], lane, x);
+                push(&S.in[1][rank], lane, y);
+                push(&S.in_count[rank], lane, count);
+            }
+        }
+        meet();
+        int total = 0;
+        for (int r = 0; r < P.share; ++r) {
+            const int c = S.in_count[r];
+            if (r < rank) before += c;
+            total += c;
+            all += S.in[0][r];
+            sure_all += S.in[1][r];
+        }
+        if (total <= FEW) {
+            for (int i = lane; i < listed; i += 32) push(&S.few[before + i], 0, S.list[warp][i]);
+            meet();
+            if (from == 0) {  // there is nothing but the candidates
+                if (rank == 0) finish_few(P, R, S, row, total, 0, by_k ? k : 0, p, m, all);
+                return;
+            }
+            if (rank == 0) {  // top-p alone: the run ends among the candidates
+                sort_few(S, total, 0, P.share);
+                u64 w[EACH], mine_ = 0, sum_all;
+#pragma unroll
+                for (int e = 0; e < EACH; ++e) {
+                    const int i = EACH * tid + e;
+                    w[e] = i < total ? weight_of(R.top, logit_of(S.sorted[i]), R.ch, R.cl, S.root) : 0;
+                    mine_ += w[e];
+                }
+                u64 cum = sure_all + block_scan(S, mine_, sum_all) - mine_;
+                const u64 target = part_of(p, all, true);
+#pragma unroll
+                for (int e = 0; e < EACH; ++e) {
+                    if (cum < target && cum + w[e] >= target)
+                        for (int r = 0; r < P.share; ++r) push(&S.bound, r, S.sorted[EACH * tid + e]);
+                    cum += w[e];
+                }
+            }
+            meet();
+            bound = S.bound;
+            u64 w = 0;
+            for (int i = lane; i < listed; i += 32)
+                if (S.list[warp][i] <= bound) {
+                    w += weight_of(R.top, logit_of(S.list[warp][i]), R.ch, R.cl, S.root);
+                    ++sure;
+                }
+            w_all = w_sure + w;  // what the warp's kept tokens weigh
+            by_few = true;
+        }
+    }
+    if (list && !by_few) {  // many candidates
+        if (by_k) {
+            const Pick at = first_level<false>(R, S, NONE, (u64)k, 0.0f, turn);
+            if (at.all > (u64)k) bound = refine<false>(R, S, NONE, at, (u64)k, turn);
+        }
+        if (by_p) {
+            const Pick at = first_level<true>(R, S, bound, 0, p, turn);
+            bound = refine<true>(R, S, bound, at, max(part_of(p, at.all, true), 1ull), turn);
+        }
     }
 
     // ---------------- the draw ----------------
-    const bool floor_on = m > 0.0f;
     const float fh = S.yh, fl = S.yl;
-    // weight of a kept token; kept: whether it is
+    // weight of a token, if it is kept
     const auto take = [&](int i, bool &kept, float &yh, float &yl) -> u64 {
-        const float l = logits[i];
-        kept = false;
-        yh = yl = 0.0f;
-        if (!(l > -INFINITY)) return 0;
-        const u64 c = order_of(l, R.first + i);
-        if (c > bound) return 0;
+        const float l = R.at(i);
+        kept = l > -INFINITY && (bound == NONE || order_of(l, R.first + i) <= bound);
         const bool some = exponent(R.top, l, R.ch, R.cl, yh, yl);
-        if (floor_on && c != best && !(some ? (yh - fh) + (yl - fl) <= 0.0f : yh <= fh)) return 0;
-        kept = true;
-        return some ? weight(yh, yl, S.root) : 0;
+        if (by_m && !(some ? (yh - fh) + (yl - fl) <= 0.0f : yh <= fh)) kept = false;
+        return kept && some ? weight(yh, yl, S.root) : 0;
     };
-    u64 sum = 0;
-    int count = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-        bool kept;
-        float yh, yl;
-        sum += take(i, kept, yh, yl);
-        count += kept;
+    if (list && !by_few) {
+        w_all = 0;
+        sure = 0;
+        for (int i = w0 + lane; i < w1; i += 32) {
+            bool kept;
+            float yh, yl;
+            w_all += take(i, kept, yh, yl);
+            sure += kept;
+        }
     }
-    sum = warp_sum(sum);
-    count = __reduce_add_sync(0xffffffffu, count);
-    __syncthreads();  // the last search's warp_sum has been read
+    const u64 sum = warp_sum(w_all);
+    const int count = __reduce_add_sync(0xffffffffu, sure);
+    __syncthreads();
     if (lane == 0) {
         S.warp_sum[warp] = sum;
         S.warp_two[warp] = (u64)count;
     }
     __syncthreads();
-    if (tid == 0) {
-        u64 all = 0;
-        int n = 0;
-        for (int w = 0; w < WARPS; ++w) {
-            all += S.warp_sum[w];
-            n += (int)S.warp_two[w];
+    if (warp == 0) {
+        const u64 x = warp_sum(lane < WARPS ? S.warp_sum[lane] : 0), n = warp_sum(lane < WARPS ? S.warp_two[lane] : 0);
+        if (lane < P.share) {
+            push(&S.in_draw[rank], lane, x);
+            push(&S.in_kept[rank], lane, (int)n);
         }
-        S.sum = all;
-        S.count = n;
     }
     meet();
-    u64 all = 0, before = 0;
+    u64 whole = 0, before = 0;
     int kept_all = 0;
     for (int r = 0; r < P.share; ++r) {
-        const u64 v = peer_u64(&S.sum, r);
-        if (r < rank) before += v;
-        all += v;
-        kept_all += peer_int(&S.count, r);
+        if (r < rank) before += S.in_draw[r];
+        whole += S.in_draw[r];
+        kept_all += S.in_kept[r];
     }
-    float u = __ldg(P.u + row);
-    u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
-    const u64 goal = part_of(u, all, false);
+    const u64 goal = part_of(random_of(P, row), whole, false);
     for (int w = 0; w < warp; ++w) before += S.warp_sum[w];
     if (before <= goal && goal < before + S.warp_sum[warp]) {  // the token is this warp's
         for (int i0 = w0; i0 < w1; i0 += 32) {
@@ -590,35 +907,51 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
             const u64 upto = before + warp_scan(w, lane);
             const unsigned hit = __ballot_sync(0xffffffffu, upto > goal);
             if (hit) {
-                if (lane == __ffs(hit) - 1) write_token(P, row, R.first + i0 + lane, yh, yl, all, kept_all);
+                if (lane == __ffs(hit) - 1) write_token(P, row, R.first + i0 + lane, yh, yl, whole, kept_all);
                 break;
             }
             before = __shfl_sync(0xffffffffu, upto, 31);
         }
     }
-    meet();  // nobody leaves while the others read
 }
 
 template <typename T>
 cudaError_t launch(const SampleParams &P, int R, cudaStream_t s) {
     auto *kernel = sample_kernel<T>;
-    const int smem = (int)sizeof(Shared) + P.slice * 4;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared) + MAX_V / MAX_SHARE * 4);
+    const int smem = (int)sizeof(Shared) + P.slice * (int)sizeof(T) + 16;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(Shared) + MAX_V / MAX_SHARE * (int)sizeof(T) + 16);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)R * P.share);
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {(unsigned)P.share, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, P);
 }
 
 }  // namespace
+
+int sample_read_error(int *site) {
+    int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_sample_error, sizeof(int));
+    if (e != cudaSuccess) return fail_cuda(e);
+    if (v) {
+        e = cudaMemcpyToSymbol(g_sample_error, &zero, sizeof(int));
+        if (e != cudaSuccess) return fail_cuda(e);
+        if (site) *site = v;
+        return DSA_ERR_TIMEOUT;
+    }
+    return DSA_OK;
+}
+
 }  // namespace dsa
 
 using namespace dsa;
