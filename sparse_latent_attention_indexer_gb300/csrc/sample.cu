@@ -38,7 +38,7 @@ typedef unsigned long long u64;
 constexpr int THREADS = 512, WARPS = THREADS / 32, BINS = 2 * THREADS;
 constexpr int MAX_V = 1 << 18, INDEX_BITS = 18;
 constexpr int MAX_SHARE = 8;
-constexpr int EACH = 4, FEW = EACH * THREADS, LIST = 96;  // candidates that one CTA finishes; that a warp lists
+constexpr int FEW = 4 * THREADS, LIST = 96;  // candidates that one CTA finishes; that a warp lists
 constexpr float PER_NAT = 32.0f;              // bins
 constexpr u64 NONE = ~0ull, ONE = 1ull << 45;
 constexpr float LN2_H = 0.693147182464599609375f, LN2_L = -1.90465429995776765e-9f;  // ln 2 as a pair
@@ -404,84 +404,141 @@ __device__ __forceinline__ int count_listed(Shared &S, int listed, int most, int
     return over || all > most ? FEW + 1 : all;
 }
 
-// Sorts n <= FEW candidates into S.sorted (best first); they lie in S.few by index, rank r's S.in_alone[r] from region r on
-// (0: one after another).
-__device__ void sort_few(Shared &S, int n, int region, int share) {
+// Candidate i < n of the cluster, by index: they lie in S.few, rank r's S.in_alone[r] from region r on (0: one after another).
+__device__ __forceinline__ u64 candidate(const Shared &S, int i, int n, int region, int share) {
+    if (i >= n) return NONE;
+    if (region == 0) return S.few[i];
+    int r = 0;
+    while (r < share - 1 && i >= S.in_alone[r]) i -= S.in_alone[r++];
+    return S.few[r * region + i];
+}
+
+// The thread's share of the candidates (E neighbours, by index) becomes that of the candidates in order, best first, NONE
+// behind them: one value a thread turns in registers as long as its partner is in its warp, more go through shared memory.
+template <int E>
+__device__ void sort_few(Shared &S, u64 (&c)[E], int n) {
     const int tid = threadIdx.x;
     int size = 32;
     while (size < n) size *= 2;
-    __syncthreads();
-    for (int i = n + tid; i < size; i += THREADS) S.sorted[i] = NONE;
-    if (region == 0) {
-        for (int i = tid; i < n; i += THREADS) S.sorted[i] = S.few[i];
+    if constexpr (E == 1) {
+        if (tid < size) {
+            for (int len = 2; len <= size; len *= 2)
+                for (int d = len / 2; d > 0; d /= 2) {
+                    u64 other;
+                    if (d >= 32) {
+                        asm volatile("bar.sync 1, %0;" ::"r"(size) : "memory");
+                        S.sorted[tid] = c[0];
+                        asm volatile("bar.sync 1, %0;" ::"r"(size) : "memory");
+                        other = S.sorted[tid ^ d];
+                    } else {
+                        other = __shfl_xor_sync(0xffffffffu, c[0], d);
+                    }
+                    const bool low = ((tid & d) == 0) == ((tid & len) == 0);  // this thread keeps the smaller one
+                    if (low ? other < c[0] : other > c[0]) c[0] = other;
+                }
+        }
     } else {
-        for (int r = 0, to = 0; r < share; to += S.in_alone[r++])
-            for (int i = tid; i < S.in_alone[r]; i += THREADS) S.sorted[to + i] = S.few[r * region + i];
-    }
-    for (int len = 2; len <= size; len *= 2)
-        for (int d = len / 2; d > 0; d /= 2) {
-            __syncthreads();
-            for (int t = tid; t < size / 2; t += THREADS) {
-                const int i = 2 * t - (t & (d - 1)), j = i + d;
-                const u64 a = S.sorted[i], b = S.sorted[j];
-                if ((a > b) == ((i & len) == 0)) {
-                    S.sorted[i] = b;
-                    S.sorted[j] = a;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) S.sorted[E * tid + e] = c[e];
+        for (int len = 2; len <= size; len *= 2)
+            for (int d = len / 2; d > 0; d /= 2) {
+                __syncthreads();
+                for (int t = tid; t < size / 2; t += THREADS) {
+                    const int i = 2 * t - (t & (d - 1)), j = i + d;
+                    const u64 a = S.sorted[i], b = S.sorted[j];
+                    if ((a > b) == ((i & len) == 0)) {
+                        S.sorted[i] = b;
+                        S.sorted[j] = a;
+                    }
                 }
             }
-        }
-    if (tid == 0) S.count = 0x7fffffff;
-    __syncthreads();
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) c[e] = S.sorted[E * tid + e];
+    }
 }
 
-// The end of a row whose kept tokens are among n <= FEW candidates, which lie in S.few by index: one CTA sorts them,
-// cuts the run by each rule and draws.  all: what every token weighs, where there is no top-k.  With regions, S.few holds
-// NONE where there is no candidate.
-template <typename T>
+// The end of a row whose kept tokens are among n <= E * THREADS candidates: one CTA sorts them, cuts the run by each rule
+// and draws.  all: what every token weighs, where there is no top-k.
+template <int E, typename T>
 __device__ void finish_few(const SampleParams &P, const Row<T> &R, Shared &S, int64_t row, int n, int region, int k, float p, float m,
                            u64 all) {
-    const int first = EACH * threadIdx.x;  // neighbours a thread
-    sort_few(S, n, region, R.share);
+    const int first = E * threadIdx.x;
+    u64 by_index[E], sorted[E], w[E], mine = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sorted[e] = by_index[e] = candidate(S, first + e, n, region, R.share);
+    if (threadIdx.x == 0) S.count = 0x7fffffff;
+    sort_few<E>(S, sorted, n);
     const int run = k > 0 ? min(k, n) : n;
-    u64 w[EACH], mine = 0;
     int keep = run;
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
+    for (int e = 0; e < E; ++e) {
         w[e] = 0;
         if (first + e >= run) continue;
         float yh, yl;
-        const bool some = exponent(R.top, logit_of(S.sorted[first + e]), R.ch, R.cl, yh, yl);
+        const bool some = exponent(R.top, logit_of(sorted[e]), R.ch, R.cl, yh, yl);
         if (some) w[e] = weight(yh, yl, S.root);
         mine += w[e];
         if (m > 0.0f && first + e > 0 && !(some ? (yh - S.yh) + (yl - S.yl) <= 0.0f : yh <= S.yh)) keep = min(keep, first + e);
     }
-    u64 total, cum = block_scan(S, mine, total) - mine;
-    if (k <= 0) total = all;
-    const u64 target = p < 1.0f ? max(part_of(p, total, true), 1ull) : NONE;
+    u64 total = all;
+    if (p < 1.0f) {
+        u64 sum, cum = block_scan(S, mine, sum) - mine;
+        if (k > 0) total = sum;
+        const u64 target = max(part_of(p, total, true), 1ull);
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-        cum += w[e];
-        if (cum >= target) keep = min(keep, first + e + 1);
+        for (int e = 0; e < E; ++e) {
+            cum += w[e];
+            if (cum >= target) keep = min(keep, first + e + 1);
+        }
+    } else {
+        __syncthreads();
     }
-    if (keep < run) atomicMin(&S.count, keep);
+    keep = __reduce_min_sync(0xffffffffu, keep);
+    if ((threadIdx.x & 31) == 0 && keep < run) atomicMin(&S.count, keep);
     __syncthreads();
     keep = min(run, S.count);
-    const u64 bound = S.sorted[keep - 1];
-    float yh[EACH], yl[EACH];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (first + e == keep - 1) S.bound = sorted[e];
+    __syncthreads();
+    const u64 bound = S.bound;
+    float yh[E], yl[E];
     mine = 0;
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-        const int i = first + e;
+    for (int e = 0; e < E; ++e) {
         w[e] = 0;
         yh[e] = yl[e] = 0.0f;
-        if ((region || i < n) && S.few[i] <= bound && exponent(R.top, logit_of(S.few[i]), R.ch, R.cl, yh[e], yl[e])) w[e] = weight(yh[e], yl[e], S.root);
+        if (by_index[e] <= bound && exponent(R.top, logit_of(by_index[e]), R.ch, R.cl, yh[e], yl[e])) w[e] = weight(yh[e], yl[e], S.root);
         mine += w[e];
     }
-    cum = block_scan(S, mine, total) - mine;
+    u64 cum = block_scan(S, mine, total) - mine;
     const u64 goal = part_of(random_of(P, row), total, false);
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-        if (cum <= goal && cum + w[e] > goal) write_token(P, row, (int)(S.few[first + e] & (MAX_V - 1)), yh[e], yl[e], total, keep);
+    for (int e = 0; e < E; ++e) {
+        if (cum <= goal && cum + w[e] > goal) write_token(P, row, (int)(by_index[e] & (MAX_V - 1)), yh[e], yl[e], total, keep);
+        cum += w[e];
+    }
+}
+
+// The last token of a run by top-p that ends among n candidates: `before` is what the tokens before them weigh.
+template <int E, typename T>
+__device__ void bound_few(const Row<T> &R, Shared &S, int n, u64 before, u64 target) {
+    u64 c[E], w[E], mine = 0, sum;
+#pragma unroll
+    for (int e = 0; e < E; ++e) c[e] = candidate(S, E * threadIdx.x + e, n, 0, R.share);
+    sort_few<E>(S, c, n);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        w[e] = c[e] != NONE ? weight_of(R.top, logit_of(c[e]), R.ch, R.cl, S.root) : 0;
+        mine += w[e];
+    }
+    u64 cum = before + block_scan(S, mine, sum) - mine;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (cum < target && cum + w[e] >= target)
+            for (int r = 0; r < R.share; ++r) push(&S.bound, r, c[e]);
         cum += w[e];
     }
 }
@@ -527,8 +584,6 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     R.share = P.share;
     R.first = min(P.V, rank * P.slice);
     R.n = min(P.V, R.first + P.slice) - R.first;
-    if (rank == 0)
-        for (int i = tid; i < FEW; i += THREADS) S.few[i] = NONE;
     meet_arrive();  // waited for before anything is pushed: the other CTAs have started
     pdl_wait();     // the set-up above overlapped the previous kernel
     bool coming;
@@ -573,18 +628,20 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     // this warp's go among them.
     const auto list_up_to = [&](int to, int most, int &listed, int &before) -> int {
         listed = 0;
-        const float xt = (float)to + 1.0f;
-        for (int i0 = w0; i0 < w1; i0 += 128) {
+        const float xt = to == BINS - 1 ? INFINITY : (float)to + 1.0f;
+        for (int i0 = w0; i0 < w1; i0 += 256) {
+            float l[8];
+            unsigned hit[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = i0 + e * 32 + lane;
-                const float l = i < w1 ? R.at(i) : -INFINITY;
-                const bool in = l > -INFINITY && (R.x(l) < xt || to == BINS - 1);
-                const unsigned hit = __ballot_sync(0xffffffffu, in);
-                if (hit == 0) continue;
-                const int at = listed + __popc(hit & ((1u << lane) - 1));
-                if (in && at < LIST) S.list[warp][at] = order_of(l, R.first + i);
-                listed += __popc(hit);
+            for (int e = 0; e < 8; ++e) l[e] = i0 + e * 32 + lane < w1 ? R.at(i0 + e * 32 + lane) : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) hit[e] = __ballot_sync(0xffffffffu, R.x(l[e]) < xt);  // false for -inf and NaN
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (hit[e] == 0) continue;
+                const int at = listed + __popc(hit[e] & ((1u << lane) - 1));
+                if ((hit[e] >> lane & 1) && at < LIST) S.list[warp][at] = order_of(l[e], R.first + i0 + e * 32 + lane);
+                listed += __popc(hit[e]);
             }
         }
         return count_listed(S, listed, most, before);
@@ -642,7 +699,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
                 for (int r = 0; r < P.share; ++r) total += S.in_alone[r];
                 R.ch = S.ch;
                 R.cl = S.cl;
-                finish_few(P, R, S, row, total, region, by_k ? k : 0, p, m, 0);
+                if (total <= THREADS) finish_few<1>(P, R, S, row, total, region, by_k ? k : 0, p, m, 0);
+                else finish_few<4>(P, R, S, row, total, region, by_k ? k : 0, p, m, 0);
             }
             return;
         }
@@ -749,33 +807,34 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     bool by_few = false;
     const bool weigh = !by_k && (by_p || !by_m), list = to < BINS;
     if (weigh) {
-        const float xt = (float)to + 1.0f;
-        for (int i0 = w0; i0 < w1; i0 += 64) {
-            float l[2];
-            u64 w[2];
+        const float xf = (float)from, xt = to >= BINS - 1 ? INFINITY : (float)to + 1.0f;
+        for (int i0 = w0; i0 < w1; i0 += 128) {
+            float l[4];
+            u64 w[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = i0 + e * 32 + lane;
-                l[e] = i < w1 ? R.at(i) : -INFINITY;
-                w[e] = weight_of(R.top, l[e], R.ch, R.cl, S.root);
-            }
-            w_all += w[0] + w[1];
+            for (int e = 0; e < 4; ++e) l[e] = i0 + e * 32 + lane < w1 ? R.at(i0 + e * 32 + lane) : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = weight_of(R.top, l[e], R.ch, R.cl, S.root);
             if (!list) {
-                sure += (l[0] > -INFINITY) + (l[1] > -INFINITY);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w_all += w[e];
+                    sure += l[e] > -INFINITY;
+                }
                 continue;
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float x = R.x(l[e]);
-                const bool live = l[e] > -INFINITY, before = live && (int)fminf(x, (float)(BINS - 1)) < from;
-                if (before) {
+            for (int e = 0; e < 4; ++e) {
+                const float x = R.x(l[e]);  // -inf and NaN are in no bin
+                w_all += w[e];
+                if (x < xf) {
                     w_sure += w[e];
                     ++sure;
                 }
-                const bool in = live && !before && (x < xt || to == BINS - 1);
-                const unsigned hit = __ballot_sync(0xffffffffu, in);
+                const unsigned hit = __ballot_sync(0xffffffffu, x >= xf && x < xt);
+                if (hit == 0) continue;
                 const int at = listed + __popc(hit & ((1u << lane) - 1));
-                if (in && at < LIST) S.list[warp][at] = order_of(l[e], R.first + i0 + e * 32 + lane);
+                if ((hit >> lane & 1) && at < LIST) S.list[warp][at] = order_of(l[e], R.first + i0 + e * 32 + lane);
                 listed += __popc(hit);
             }
         }
@@ -810,26 +869,14 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
             for (int i = lane; i < listed; i += 32) push(&S.few[before + i], 0, S.list[warp][i]);
             meet();
             if (from == 0) {  // there is nothing but the candidates
-                if (rank == 0) finish_few(P, R, S, row, total, 0, by_k ? k : 0, p, m, all);
+                if (rank == 0 && total <= THREADS) finish_few<1>(P, R, S, row, total, 0, by_k ? k : 0, p, m, all);
+                else if (rank == 0) finish_few<4>(P, R, S, row, total, 0, by_k ? k : 0, p, m, all);
                 return;
             }
             if (rank == 0) {  // top-p alone: the run ends among the candidates
-                sort_few(S, total, 0, P.share);
-                u64 w[EACH], mine_ = 0, sum_all;
-#pragma unroll
-                for (int e = 0; e < EACH; ++e) {
-                    const int i = EACH * tid + e;
-                    w[e] = i < total ? weight_of(R.top, logit_of(S.sorted[i]), R.ch, R.cl, S.root) : 0;
-                    mine_ += w[e];
-                }
-                u64 cum = sure_all + block_scan(S, mine_, sum_all) - mine_;
                 const u64 target = part_of(p, all, true);
-#pragma unroll
-                for (int e = 0; e < EACH; ++e) {
-                    if (cum < target && cum + w[e] >= target)
-                        for (int r = 0; r < P.share; ++r) push(&S.bound, r, S.sorted[EACH * tid + e]);
-                    cum += w[e];
-                }
+                if (total <= THREADS) bound_few<1>(R, S, total, sure_all, target);
+                else bound_few<4>(R, S, total, sure_all, target);
             }
             meet();
             bound = S.bound;
