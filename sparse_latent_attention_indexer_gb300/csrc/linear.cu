@@ -23,6 +23,8 @@
 // fp32 layers run on the same kernel: a value is the sum of three bf16 terms of 8 bits each, and
 // of the nine products of terms the six above 2^-24 of the whole are added, smallest first.
 // Rows that do not start on 16 bytes are laid out anew first (linear_layout_kernel).
+#include <atomic>
+
 #include "tc_common.cuh"
 
 namespace dsa {
@@ -40,6 +42,7 @@ constexpr int TURN = 2 * 32 * BF * 4;             // 32 tokens x 128 features in
 constexpr int SMEM_MAX = 232448;
 constexpr int MAX_EXACT = 128;                     // tokens of a tile whose sums are exact
 constexpr int CHAIN = 8;                          // slabs of an exact sum's parts
+constexpr int MAX_SHARE = 8;                      // CTAs that share a tile's K
 constexpr int GROUP_T = 8;                        // token tiles that share a panel of W in L2
 
 struct Epilogue {
@@ -57,6 +60,7 @@ struct LinearParams {
     int plane;            // columns from one plane to the next; 0: one plane
     int stages, stage_bytes;
     int share;            // CTAs that share a tile's K (SPLIT)
+    int acc_cols, tmem_cols;  // columns from one accumulator to the next; of tensor memory
     int chain;            // slabs that are added up in tensor memory (all, or CHAIN with EXACT)
     long long wait_limit;
 };
@@ -125,6 +129,47 @@ __device__ __forceinline__ float4 peer4(uint32_t addr) {
     return v;
 }
 
+// The producer and the MMA issuer are whole warps in convergence, of which one lane issues: what they hand to an instruction
+// then stays in uniform registers.  From a single lane's branch a slab took them 510 and 570 cycles.
+__device__ __forceinline__ void expect_if(uint32_t issue, uint64_t *bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(tc::smem_u32(bar)),
+        "r"(bytes), "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ void load_if(uint32_t issue, void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];\n\t}" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t issue, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
+        "r"(issue)
+        : "memory");
+}
+// mbar_wait for a warp in convergence: every lane has the same answer.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err, int site,
+                                          long long limit = tc::kWaitLimitCycles) {
+    const uint32_t a = tc::smem_u32(bar);
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait(a, parity))) return true;
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, tc::mbar_try_wait(a, parity))) {
+        if (__any_sync(0xffffffffu, *abort_flag)) return false;
+        if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
+            atomicCAS(err, 0, site);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 __device__ __forceinline__ void tile_of(const LinearParams &P, int u, int &m0, int &f0) {
     const int ft = (P.N + BF - 1) / BF, per_group = GROUP_T * ft;
     const int grp = u / per_group, r = u - grp * per_group;
@@ -145,7 +190,7 @@ __device__ __forceinline__ void slab_at(const LinearParams &P, int i, int &xw, i
 }
 
 template <bool SPLIT, bool EXACT>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT ? 2 : 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                   const __grid_constant__ LinearParams P) {
     extern __shared__ uint8_t smem_raw[];
@@ -164,82 +209,97 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int s0 = SPLIT ? (int)((int64_t)P.total * rank / share) : 0;
     const int s1 = SPLIT ? (int)((int64_t)P.total * (rank + 1) / share) : P.total;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < P.stages; ++i) {
-            tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], 1);
+    // One slab's loads, by the lane of `issue`.
+    const auto load = [&](uint32_t issue, int st, int ks, int m0, int f0) {
+        uint8_t *sw = ring + st * P.stage_bytes;
+        int xw, xx;
+        slab_at(P, ks, xw, xx);
+        expect_if(issue, &full[st], P.stage_bytes);
+        load_if(issue, sw, &tm_w, &full[st], xw, f0);
+        load_if(issue, sw + W_SLAB, &tm_x, &full[st], xx, m0);
+    };
+    // The producer's first loads go out before the CTA has met, while warp 2 waits for tensor memory.
+    const int ahead_slabs = mine > 0 ? min(s1 - s0, P.stages) : 0;
+    if (warp == 0) {
+        int m0, f0;
+        tile_of(P, who, m0, f0);
+        const uint32_t issue = tc::elect_one();
+        if (lane == 0) {
+            tc::prefetch_tmap(&tm_w);
+            tc::prefetch_tmap(&tm_x);
+            for (int i = 0; i < P.stages; ++i) {
+                tc::mbar_init(&full[i], 1);
+                tc::mbar_init(&empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                tc::mbar_init(&tfull[i], 1);
+                tc::mbar_init(&tempty[i], EPI_THREADS / 32);
+            }
+            tc::mbar_init(&mmadone, 1);
+            abort_word = 0;
+            never = 0;
+            tc::fence_mbar_init();
         }
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&tfull[i], 1);
-            tc::mbar_init(&tempty[i], EPI_THREADS / 32);
-        }
-        tc::mbar_init(&mmadone, 1);
-        abort_word = 0;
-        never = 0;
-        tc::fence_mbar_init();
-    }
-    if (warp == 2) {
-        tc::tmem_alloc(&tmem_slot, 2 * MAX_BT);
+        __syncwarp();
+        pdl_wait();  // the set-up above overlapped the previous kernel; global memory only from here
+        for (int j = 0; j < ahead_slabs; ++j) load(issue, j, s0 + j, m0, f0);
+    } else if (warp == 2) {
+        tc::tmem_alloc(&tmem_slot, P.tmem_cols);
         tc::tmem_relinquish();
     }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    pdl_wait();  // the set-up above overlapped the previous kernel; global memory only from here
+    if (warp != 0) pdl_wait();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ---------------- TMA producer ----------------
-        tc::prefetch_tmap(&tm_w);
-        tc::prefetch_tmap(&tm_x);
-        int it = 0, st = 0, round = 0;
+        const uint32_t issue = tc::elect_one();
+        int it = ahead_slabs, st = ahead_slabs == P.stages ? 0 : ahead_slabs, round = ahead_slabs == P.stages ? 1 : 0;
         bool ok = true;
         for (int i = 0; ok && i < mine; ++i) {
             int m0, f0;
             tile_of(P, who + i * step, m0, f0);
-            for (int ks = s0; ks < s1; ++ks, ++it) {
-                if (!(ok = tc::mbar_wait(&empty[st], (round & 1) ^ 1, abort_flag, err, 61, P.wait_limit))) break;
-                uint8_t *sw = ring + st * P.stage_bytes;
-                int xw, xx;
-                slab_at(P, ks, xw, xx);
-                tc::mbar_arrive_expect_tx(&full[st], P.stage_bytes);
-                tc::tma_load_2d(sw, &tm_w, &full[st], xw, f0);
-                tc::tma_load_2d(sw + W_SLAB, &tm_x, &full[st], xx, m0);
+            for (int ks = i > 0 ? s0 : s0 + ahead_slabs; ks < s1; ++ks, ++it) {
+                if (!(ok = wait_warp(&empty[st], (round & 1) ^ 1, abort_flag, err, 61, P.wait_limit))) break;
+                load(issue, st, ks, m0, f0);
                 if (++st == P.stages) st = 0, ++round;
             }
         }
         // Drain: nothing may still be landing in shared memory when the CTA goes on.
-        for (int j = max(0, it - P.stages); j < it; ++j)
-            tc::mbar_wait(&full[j % P.stages], (j / P.stages) & 1, nv, err, 62);
-    } else if (warp == 1 && lane == 0) {
+        for (int j = max(0, it - P.stages); j < it; ++j) wait_warp(&full[j % P.stages], (j / P.stages) & 1, nv, err, 62);
+    } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
+        const uint32_t issue = tc::elect_one();
         const uint32_t idesc = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, BF, P.bt, 0, 0);
+        const uint64_t first = tc::smem_desc(tc::smem_u32(ring), 16, 1024);
         int st = 0, round = 0, issued = 0, n = 0;
         bool ok = true;
         for (int i = 0; ok && i < mine; ++i) {
             for (int k0 = s0; ok && k0 < s1; k0 += P.chain, ++n) {
                 const int acc = n & 1, k1 = min(s1, k0 + P.chain);
-                if (!(ok = tc::mbar_wait(&tempty[acc], ((n >> 1) & 1) ^ 1, abort_flag, err, 63, P.wait_limit))) break;
-                const uint32_t d = tmem + acc * MAX_BT;
+                if (!(ok = wait_warp(&tempty[acc], ((n >> 1) & 1) ^ 1, abort_flag, err, 63, P.wait_limit))) break;
+                const uint32_t d = tmem + acc * P.acc_cols;
                 for (int ks = k0; ks < k1; ++ks) {
-                    if (!(ok = tc::mbar_wait(&full[st], round & 1, abort_flag, err, 64, P.wait_limit))) break;
+                    if (!(ok = wait_warp(&full[st], round & 1, abort_flag, err, 64, P.wait_limit))) break;
                     tc::tc_fence_after();
-                    const uint32_t a0 = tc::smem_u32(ring + st * P.stage_bytes), b0 = a0 + W_SLAB;
+                    // addresses in a descriptor count 16 bytes and stay below its 14 bits
+                    const uint64_t wd = first + (uint32_t)(st * P.stage_bytes / 16), xd = wd + W_SLAB / 16;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_f16(d, tc::smem_desc(a0 + kk * 32, 16, 1024), tc::smem_desc(b0 + kk * 32, 16, 1024), idesc,
-                                    ks != k0 || kk != 0);
-                    tc::mma_commit(&empty[st]);
+                        tc::mma_f16_if(issue, d, wd + kk * 2, xd + kk * 2, idesc, ks != k0 || kk != 0);
+                    commit_if(issue, &empty[st]);
                     ++issued;
                     if (++st == P.stages) st = 0, ++round;
                 }
-                if (ok) tc::mma_commit(&tfull[acc]);
+                if (ok) commit_if(issue, &tfull[acc]);
             }
         }
         // No MMA may still be running when the tensor memory is released.
         if (issued > 0) {
-            tc::mma_commit(&mmadone);
-            tc::mbar_wait(&mmadone, 0, nv, err, 65);
+            commit_if(issue, &mmadone);
+            wait_warp(&mmadone, 0, nv, err, 65);
         }
     } else if (warp >= EPI_WARP0) {
         // ---------------- epilogue ----------------
@@ -312,7 +372,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     for (int j = 0; j < MAX_EXACT / 64; ++j)
                         if (j * 64 + g * 32 < tokens) {
                             float v[32];
-                            tc::tmem_ld32(lanes + (n & 1) * MAX_BT + j * 64 + g * 32, v);
+                            tc::tmem_ld32(lanes + (n & 1) * P.acc_cols + j * 64 + g * 32, v);
                             tc::tmem_ld_wait();
 #pragma unroll
                             for (int e = 0; e < 32; ++e) sum[j][e] += v[e];
@@ -331,7 +391,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 tc::tc_fence_after();
                 for (int c = g * 32; c < tokens; c += 64) {
                     float v[32];
-                    tc::tmem_ld32(lanes + (n & 1) * MAX_BT + c, v);
+                    tc::tmem_ld32(lanes + (n & 1) * P.acc_cols + c, v);
                     tc::tmem_ld_wait();
                     put(c, v);
                 }
@@ -345,21 +405,34 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     __syncthreads();
     if (SPLIT) {
-        tc::cluster_sync();  // every CTA's partial tile is in its shared memory
         int m0, f0;
         tile_of(P, who, m0, f0);
+        tc::cluster_sync();  // every CTA's partial tile is in its shared memory
         const int units = min(P.bt, P.M - m0) * (BF / 4);
         const uint32_t part = tc::smem_u32(ring);
-        for (int u = rank * NUM_THREADS + (int)threadIdx.x; u < units; u += share * NUM_THREADS) {
-            const int t = u / (BF / 4), f = f0 + (u % (BF / 4)) * 4;
-            if (f >= P.N) continue;
+        // four features of a token at a time; the next one's parts are on their way while these are stored
+        const auto fetch = [&](int u, float4 (&a)[MAX_SHARE]) {
+#pragma unroll
+            for (int k = 0; k < MAX_SHARE; ++k)
+                if (k < share && u < units) a[k] = peer4(tc::map_peer(part + u * 16, k));
+        };
+        const int by = share * NUM_THREADS;
+        float4 next[MAX_SHARE];
+        int u = rank * NUM_THREADS + (int)threadIdx.x;
+        fetch(u, next);
+        for (; u < units; u += by) {
+            const int f = f0 + (u % (BF / 4)) * 4;
+            const int64_t row = m0 + u / (BF / 4);
+            const bool live = f < P.N;
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            const int64_t row = m0 + t;
-            if (P.e.res && P.e.vec) residual4(P.e, row, f, r);
-            for (int k = 0; k < share; ++k) {
-                const float4 a = peer4(tc::map_peer(part + u * 16, k));
-                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-            }
+            if (live && P.e.res && P.e.vec) residual4(P.e, row, f, r);
+#pragma unroll
+            for (int k = 0; k < MAX_SHARE; ++k)
+                if (k < share) {
+                    v[0] += next[k].x; v[1] += next[k].y; v[2] += next[k].z; v[3] += next[k].w;
+                }
+            fetch(u + by, next);
+            if (!live) continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (f + e < P.N) v[e] = activate(v[e] + (P.e.bias ? __ldg(P.e.bias + f + e) : 0.0f), P.e.act);
@@ -378,7 +451,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     if (warp == 2) {
         tc::tc_fence_after();
-        tc::tmem_dealloc(tmem, 2 * MAX_BT);
+        tc::tmem_dealloc(tmem, P.tmem_cols);
     }
 }
 
@@ -387,56 +460,115 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // bf16 terms, each the nearest to what the terms before it leave (a term that would round to
 // infinity is the largest number instead; infinities and NaN stay in the first plane).
 // ---------------------------------------------------------------------------
+struct Layout {
+    const void *src[2];       // x and W (rows 0: neither)
+    __nv_bfloat16 *dst[2];
+    int64_t ld[2], ld_dst;
+    int rows[2], K, cols;     // cols: of a plane, K up to a multiple of 8 or 64
+};
+
+// A warp takes 256 values of a row, a lane eight.
 template <bool F32>
-__global__ void __launch_bounds__(256) linear_layout_kernel(const void *src, int64_t ld, __nv_bfloat16 *dst, int64_t rows, int K,
-                                                             int cols, int64_t ld_dst) {
+__global__ void __launch_bounds__(256) linear_layout_kernel(const __grid_constant__ Layout L) {
     pdl_wait();
-    const int per = cols / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows * per) return;
-    const int64_t r = i / per;
-    const int k = (int)(i - r * per) * 8;
-    __nv_bfloat16 *d = dst + r * ld_dst + k;
+    const int lane = threadIdx.x & 31, parts = (L.cols + 255) / 256;
+    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    int64_t r = i / parts;
+    const int k = (int)(i - r * parts) * 256 + lane * 8;
+    const int which = r >= L.rows[0];
+    if (which) r -= L.rows[0];
+    if (r >= L.rows[which]) return;  // the whole warp
+    __nv_bfloat16 *d = L.dst[which] + r * L.ld_dst + k;
     if (F32) {
-        __nv_bfloat16 t[3][8];
+        if (k >= L.cols) return;
+        const float *s = (const float *)L.src[which] + r * L.ld[which] + k;
+        float v[8];
+        if (k + 8 <= L.K && (uintptr_t)s % 16 == 0) {
+            *(float4 *)v = *(const float4 *)s;
+            *(float4 *)(v + 4) = *((const float4 *)s + 1);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = k + e < L.K ? s[e] : 0.0f;
+        }
+        __align__(16) __nv_bfloat16 t[3][8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float v = k + e < K ? ((const float *)src)[r * ld + k + e] : 0.0f;
-            const bool finite = fabsf(v) < INFINITY;
+            const bool finite = fabsf(v[e]) < INFINITY;
 #pragma unroll
             for (int p = 0; p < 3; ++p) {
-                float h = __bfloat162float(__float2bfloat16_rn(v));
-                if (finite && !(fabsf(h) < INFINITY)) h = copysignf(3.38953139e38f, v);
+                float h = __bfloat162float(__float2bfloat16_rn(v[e]));
+                if (finite && !(fabsf(h) < INFINITY)) h = copysignf(3.38953139e38f, v[e]);
                 t[p][e] = __float2bfloat16_rn(h);
-                v = finite ? v - h : 0.0f;
+                v[e] = finite ? v[e] - h : 0.0f;
             }
         }
 #pragma unroll
-        for (int p = 0; p < 3; ++p) *(uint4 *)(d + (int64_t)p * cols) = *(const uint4 *)t[p];
+        for (int p = 0; p < 3; ++p) *(uint4 *)(d + (int64_t)p * L.cols) = *(const uint4 *)t[p];
     } else {
-        __align__(16) uint16_t t[8];
+        // Whole 16 bytes around the lane's eight values: its own and, where they go on there, the next lane's.  They hold
+        // at least one value of the row, so they lie in memory that is there.
+        const uintptr_t at = (uintptr_t)((const uint16_t *)L.src[which] + r * L.ld[which] + k), end = at + 2 * (int64_t)(L.K - k);
+        const uintptr_t from = at & ~(uintptr_t)15;
+        const int off = (int)(at & 15);  // the same in every lane
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (k < L.K) a = *(const uint4 *)from;
+        b.x = __shfl_down_sync(0xffffffffu, a.x, 1);
+        b.y = __shfl_down_sync(0xffffffffu, a.y, 1);
+        b.z = __shfl_down_sync(0xffffffffu, a.z, 1);
+        b.w = __shfl_down_sync(0xffffffffu, a.w, 1);
+        if (off && k < L.K && (lane == 31 || k + 8 >= L.K)) {
+            if (from + 16 < end) b = *(const uint4 *)(from + 16);
+        }
+        if (k >= L.cols) return;
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = k + e < K ? ((const uint16_t *)src)[r * ld + k + e] : (uint16_t)0;
-        *(uint4 *)d = *(const uint4 *)t;
+        for (int e = 0; e < 4; ++e) {  // two bytes at a time, off / 4 words and perhaps half a word on
+            uint32_t lo = w[e], hi = w[e + 1];
+#pragma unroll
+            for (int j = 1; j < 4; ++j)
+                if (off / 4 == j) {
+                    lo = w[e + j];
+                    hi = e + j + 1 < 8 ? w[e + j + 1] : 0;
+                }
+            o[e] = off & 2 ? __funnelshift_r(lo, hi, 16) : lo;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // nothing behind the row's end
+            if (k + 2 * e >= L.K) o[e] = 0;
+            else if (k + 2 * e + 1 >= L.K) o[e] &= 0xffffu;
+        }
+        *(uint4 *)d = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens whose rows the TMA does not take (off 16 bytes, fp32): a second pass over W to lay it
-// out would cost twice what the product does, so a warp takes four features and every token,
-// and reads W once, value by value.  SPLIT: the CTA's eight warps share K.
+// Few tokens whose rows the TMA does not take (off 16 bytes, fp32): a pass over W to lay it out would cost several times what
+// the product does, so a warp takes four features and up to 16 tokens (more tokens: more CTAs, W from L2) and reads W as it
+// is, V values at once.  SPLIT: the CTA's eight warps share K.  Bound by HBM for a token or two, then by the FMA pipes.
 // ---------------------------------------------------------------------------
 constexpr int FEW = 16;
 
-template <typename T, int MT, bool SPLIT>
+template <typename T, int V>
+__device__ __forceinline__ void read(const T *p, bool in, float (&v)[V]) {
+    if constexpr (V == 4) {
+        const float4 a = in ? *(const float4 *)p : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    } else {
+        v[0] = in ? to_f32(*p) : 0.0f;
+    }
+}
+
+template <typename T, int MT, int V, bool SPLIT>
 __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_x, const T *W, int64_t ld_w, int M, int N, int K,
                                                          const __grid_constant__ Epilogue E) {
+    constexpr int AHEAD = MT == 1 ? 8 / V : MT == 4 ? 4 / V : 2 / V + 1;  // loads of a feature in flight
     __shared__ float sums[8][4 * MT];
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int f0 = SPLIT ? (int)blockIdx.x * 4 : ((int)blockIdx.x * 8 + warp) * 4;
-    const int per = SPLIT ? ((K + 7) / 8 + 31) / 32 * 32 : K;
-    const int k0 = SPLIT ? warp * per : 0, k1 = min(K, k0 + per);
+    const int f0 = SPLIT ? (int)blockIdx.x * 4 : ((int)blockIdx.x * 8 + warp) * 4, m0 = (int)blockIdx.y * MT;
+    const int per = SPLIT ? ((K + 7) / 8 + 32 * V - 1) / (32 * V) * (32 * V) : K;
+    const int k0 = min((int64_t)K, SPLIT ? (int64_t)warp * per : 0), k1 = (int)min((int64_t)K, (int64_t)k0 + per);
     float acc[4][MT];
 #pragma unroll
     for (int a = 0; a < 4; ++a)
@@ -445,17 +577,23 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_
     const T *w[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) w[a] = W + (int64_t)min(f0 + a, N - 1) * ld_w;
-#pragma unroll 4
-    for (int k = k0 + lane; k < k1; k += 32) {
-        float wv[4];
+    for (int k = k0 + lane * V; k < k1; k += 32 * V * AHEAD) {
+        float wv[AHEAD][4][V];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) wv[a] = to_f32(w[a][k]);
+        for (int h = 0; h < AHEAD; ++h)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const float xv = m < M ? to_f32(x[m * ld_x + k]) : 0.0f;
+            for (int a = 0; a < 4; ++a) read<T, V>(w[a] + k + h * 32 * V, k + h * 32 * V < k1, wv[h][a]);
 #pragma unroll
-            for (int a = 0; a < 4; ++a) acc[a][m] = fmaf(wv[a], xv, acc[a][m]);
-        }
+        for (int h = 0; h < AHEAD; ++h)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float xv[V];
+                read<T, V>(x + (int64_t)(m0 + m) * ld_x + k + h * 32 * V, m0 + m < M && k + h * 32 * V < k1, xv);
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[a][m] = fmaf(wv[h][a][e], xv[e], acc[a][m]);
+            }
     }
 #pragma unroll
     for (int a = 0; a < 4; ++a)
@@ -469,7 +607,7 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_
     __syncthreads();
     const int count = SPLIT ? 4 * MT : 8 * 4 * MT;
     for (int i = threadIdx.x; i < count; i += 256) {
-        const int wi = i / (4 * MT), at = i % (4 * MT), m = at / 4;
+        const int wi = i / (4 * MT), at = i % (4 * MT), m = m0 + at / 4;
         const int f = SPLIT ? f0 + at % 4 : ((int)blockIdx.x * 8 + wi) * 4 + at % 4;
         if (m >= M || f >= N) continue;
         float v = sums[wi][at];
@@ -480,20 +618,21 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_
     }
 }
 
-template <typename T, int MT>
+template <typename T, int MT, int V>
 cudaError_t launch_few(const T *x, int64_t ld_x, const T *W, int64_t ld_w, int M, int N, int K, const Epilogue &E,
                        cudaStream_t s) {
-    // 32 features a CTA once that gives every SM a CTA
-    const bool split = N < 32 * device_sm_count();
-    return split ? launch_pdl(linear_few_kernel<T, MT, true>, dim3((N + 3) / 4), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E)
-                 : launch_pdl(linear_few_kernel<T, MT, false>, dim3((N + 31) / 32), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E);
+    // 32 features a CTA once that gives every SM two
+    const int groups = (M + MT - 1) / MT;
+    const bool split = (int64_t)N * groups < 64 * device_sm_count();
+    return split ? launch_pdl(linear_few_kernel<T, MT, V, true>, dim3((N + 3) / 4, groups), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E)
+                 : launch_pdl(linear_few_kernel<T, MT, V, false>, dim3((N + 31) / 32, groups), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E);
 }
-template <typename T>
+template <typename T, int V>
 cudaError_t launch_few(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int M, int N, int K, const Epilogue &E,
                        cudaStream_t s) {
-    if (M <= 1) return launch_few<T, 1>((const T *)x, ld_x, (const T *)W, ld_w, M, N, K, E, s);
-    if (M <= 4) return launch_few<T, 4>((const T *)x, ld_x, (const T *)W, ld_w, M, N, K, E, s);
-    return launch_few<T, FEW>((const T *)x, ld_x, (const T *)W, ld_w, M, N, K, E, s);
+    if (M <= 1) return launch_few<T, 1, V>((const T *)x, ld_x, (const T *)W, ld_w, M, N, K, E, s);
+    if (M <= 4) return launch_few<T, 4, V>((const T *)x, ld_x, (const T *)W, ld_w, M, N, K, E, s);
+    return launch_few<T, FEW, V>((const T *)x, ld_x, (const T *)W, ld_w, M, N, K, E, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -517,7 +656,9 @@ Plan plan(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int dtype, i
     p.planes = dtype == DSA_F32 ? 3 : 1;
     p.lay_x = dtype == DSA_F32 || !on16(x, ld_x, M, K);
     p.lay_w = dtype == DSA_F32 || !on16(W, ld_w, N, K);
-    p.few = p.lay_w && M <= FEW;
+    // 7168 to 7168, this way and laid out: fp32 1 token 34 us, 16 tokens 131 and 225, 32 tokens 349 and 232;
+    // bf16 off 16 bytes 1 token 26, 16 tokens 169 and 70
+    p.few = p.lay_w && M <= (dtype == DSA_F32 ? FEW : 4);
     p.cols = up(K, p.planes == 3 ? 64 : 8);
     p.ld = p.cols * p.planes;
     p.chunk = N;
@@ -530,15 +671,84 @@ Plan plan(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int dtype, i
     return p;
 }
 
-cudaError_t lay_out(const void *src, int64_t ld, int dtype, int64_t rows, int K, const Plan &p, void *dst, cudaStream_t s) {
-    const int64_t n = (rows * (p.cols / 8) + 255) / 256;
+cudaError_t lay_out(Layout &L, int dtype, const Plan &p, int K, cudaStream_t s) {
+    L.K = K;
+    L.cols = (int)p.cols;
+    L.ld_dst = p.ld;
+    const int64_t n = (((int64_t)L.rows[0] + L.rows[1]) * ((p.cols + 255) / 256) + 7) / 8;
+    if (n == 0) return cudaSuccess;
     if (n > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const cudaError_t e =
-        dtype == DSA_F32
-            ? launch_pdl(linear_layout_kernel<true>, dim3((unsigned)n), dim3(256), 0, s, src, ld, (__nv_bfloat16 *)dst, rows, K, (int)p.cols, p.ld)
-            : launch_pdl(linear_layout_kernel<false>, dim3((unsigned)n), dim3(256), 0, s, src, ld, (__nv_bfloat16 *)dst, rows, K, (int)p.cols, p.ld);
+    const cudaError_t e = dtype == DSA_F32 ? launch_pdl(linear_layout_kernel<true>, dim3((unsigned)n), dim3(256), 0, s, L)
+                                           : launch_pdl(linear_layout_kernel<false>, dim3((unsigned)n), dim3(256), 0, s, L);
     if (e == cudaSuccess) note_launch(DSA_KERNEL_LINEAR_LAYOUT);
     return e;
+}
+
+// How the product is cut: tokens of a tile, CTAs that share a tile's K, CTAs that an SM holds.  The one of least time by
+// what bounds a slab (64 columns of K), in SM cycles, each measured:
+//   * shared memory: the slab is written once and read by the MMAs (W once, x once), 128 bytes a cycle (256 tokens: 730
+//     cycles, of which the MMAs need 512);
+//   * 350 cycles to hand a slab on and for 16 KB of W from HBM to one SM;
+//   * HBM, 3550 bytes a cycle for all, which W passes once;
+// and what a CTA needs besides: 5000 cycles until its first slab is there and its last result stored, more for the
+// cluster to meet and add.  64 tokens, 16384 to 7168, take 44 us with two CTAs a tile and 51 with one; 300 tokens, 7168 to
+// 2112, 16 us with four and 31 with one; 777 tokens, 2048 to 5001, 20 us in tiles of 112 and 31 in tiles of 208
+// (280 tiles and 160 for 152 SMs); 512 tokens, 16384 to 7168, 99 us in 112 tiles of 256 and 119 with two CTAs a tile.
+struct Cut {
+    int bt, share, per_sm;
+};
+
+// Clusters of `share` CTAs that the device holds at once (they lie within one group of SMs each).
+int clusters_at_once(int share, int per_sm, bool exact) {
+    static std::atomic<int> known[2][3][MAX_SHARE + 1];  // per kind: the same answer whoever asks first
+    std::atomic<int> &k = known[exact][per_sm][share];
+    int n = k.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(share);
+        cfg.blockDim = dim3(NUM_THREADS);
+        cfg.dynamicSmemBytes = SMEM_MAX / per_sm - 2048;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {(unsigned)share, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        auto *kernel = exact ? linear_kernel<true, true> : linear_kernel<true, false>;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            n = std::max(1, device_sm_count() * per_sm / (2 * share));
+        }
+        k.store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+Cut cut(int M, int N, int total, bool exact, int sms) {
+    const int most = exact ? MAX_EXACT : MAX_BT, least_tt = (M + most - 1) / most;
+    const int64_t ft = ((int64_t)N + BF - 1) / BF;
+    Cut best{MAX_BT, 1, 1};
+    double least = 1e30;
+    for (int tt = least_tt; tt < least_tt + 8; ++tt) {
+        const int bt = (int)up((M + tt - 1) / tt, 16);
+        const int64_t tiles = (M + bt - 1) / bt * ft;
+        const double smem = 2 * (W_SLAB + 128.0 * bt) / 128, hbm = (double)ft * total * W_SLAB / 3550;
+        for (int share = 1; share <= MAX_SHARE && (share == 1 || total >= 4 * share); ++share)
+            for (int per_sm = 1; per_sm <= (share > 1 && !exact && bt <= 128 ? 2 : 1); ++per_sm) {
+                const int64_t room = share == 1 ? sms : clusters_at_once(share, per_sm, exact), rounds = (tiles + room - 1) / room;
+                const double slabs = (total + share - 1) / share, side = tiles * share > sms ? per_sm : 1;
+                const double work = slabs * std::max(smem * side, 350.0);
+                const double fix = share == 1 ? 5000 + 14.0 * bt : 8000 + 60.0 * bt;
+                // one CTA a tile: the end of a tile is beside the next one's product
+                const double t = std::max(hbm + fix, share == 1 ? rounds * std::max(work, 14.0 * bt) + fix : rounds * (work + fix));
+                if (t < least * 0.98) {
+                    least = t;
+                    best = {bt, share, per_sm};
+                }
+            }
+        if (bt == 16) break;
+    }
+    return best;
 }
 
 cudaError_t launch_tiles(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int K, int plane, LinearParams &P,
@@ -548,20 +758,22 @@ cudaError_t launch_tiles(const void *x, int64_t ld_x, const void *W, int64_t ld_
     P.total = plane ? 6 * P.slabs : P.slabs;
     const bool exact = P.e.f32 && P.total > CHAIN;
     P.chain = exact ? CHAIN : P.total;
-    const int most = exact ? MAX_EXACT : MAX_BT;
-    P.tt = (P.M + most - 1) / most;
-    P.bt = (int)up((P.M + P.tt - 1) / P.tt, 16);
+    const Cut c = cut(P.M, P.N, P.total, exact, sms);
+    P.bt = c.bt;
+    P.share = c.share;
     P.tt = (P.M + P.bt - 1) / P.bt;
-    const int64_t tiles = (int64_t)P.tt * ((P.N + BF - 1) / BF);
-    if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
+    const int64_t tiles = (int64_t)P.tt * (((int64_t)P.N + BF - 1) / BF);
+    if (tiles > 0x7fffffff / 8) return cudaErrorInvalidConfiguration;
     P.tiles = (int)tiles;
     P.plane = plane;
     P.stage_bytes = W_SLAB + P.bt * 128;
     P.wait_limit = wait_limit_cycles();
-    P.share = 1;
-    while (P.share < 8 && tiles * P.share * 2 <= sms && P.total >= P.share * 2 * 4) P.share *= 2;
     const bool split = P.share > 1;
-    P.stages = std::min(MAX_STAGES, (SMEM_MAX - 2048 - (split ? 0 : TURN)) / P.stage_bytes);
+    P.acc_cols = 32;
+    while (P.acc_cols < P.bt) P.acc_cols *= 2;
+    if (!split) P.acc_cols = MAX_BT;
+    P.tmem_cols = split && !exact ? P.acc_cols : 2 * P.acc_cols;
+    P.stages = std::min(MAX_STAGES, (SMEM_MAX / c.per_sm - 2048 - (split ? 0 : TURN)) / P.stage_bytes);
     const int smem = 1024 + P.stages * P.stage_bytes + (split ? 0 : TURN);
     CUtensorMap tw, tx;
     const uint64_t wide = plane ? 3 * (uint64_t)plane : (uint64_t)K;
@@ -666,27 +878,36 @@ extern "C" int dsa_linear(const void *x, int64_t ld_x, const void *W, int64_t ld
             (!residual || ((uintptr_t)residual % four == 0 && (M <= 1 || ld_r % 4 == 0)));
     cudaError_t e;
     if (p.few) {
-        e = dtype == DSA_F32 ? launch_few<float>(x, ld_x, W, ld_w, M, N, K, E, s)
-                             : launch_few<__nv_bfloat16>(x, ld_x, W, ld_w, M, N, K, E, s);
+        const bool four_in = K % 4 == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)W % 16 == 0 && (M <= 1 || ld_x % 4 == 0) &&
+                             (N <= 1 || ld_w % 4 == 0);
+        e = dtype != DSA_F32 ? launch_few<__nv_bfloat16, 1>(x, ld_x, W, ld_w, M, N, K, E, s)
+            : four_in        ? launch_few<float, 4>(x, ld_x, W, ld_w, M, N, K, E, s)
+                             : launch_few<float, 1>(x, ld_x, W, ld_w, M, N, K, E, s);
         if (e != cudaSuccess) return fail_cuda(e);
         note_launch(DSA_KERNEL_LINEAR_SIMT);
         return DSA_OK;
     }
     const int64_t rows_x = M > 1 ? ld_x : up(K, 8), rows_w = N > 1 ? ld_w : up(K, 8);
-    if (p.lay_x) {
-        e = lay_out(x, ld_x, dtype, M, K, p, workspace, s);
-        if (e != cudaSuccess) return fail_cuda(e);
-    }
     const void *xs = p.lay_x ? workspace : x;
     for (int n0 = 0; n0 < N; n0 += p.chunk) {
         const int n = std::min(p.chunk, N - n0);
         const void *ws = W;
+        Layout L{};
+        if (p.lay_x && n0 == 0) {
+            L.src[0] = x;
+            L.ld[0] = ld_x;
+            L.rows[0] = M;
+            L.dst[0] = (__nv_bfloat16 *)workspace;
+        }
         if (p.lay_w) {
             ws = (char *)workspace + p.x_bytes;
-            const char *from = (const char *)W + (int64_t)n0 * ld_w * (dtype == DSA_F32 ? 4 : 2);
-            e = lay_out(from, ld_w, dtype, n, K, p, (void *)ws, s);
-            if (e != cudaSuccess) return fail_cuda(e);
+            L.src[1] = (const char *)W + (int64_t)n0 * ld_w * (dtype == DSA_F32 ? 4 : 2);
+            L.ld[1] = ld_w;
+            L.rows[1] = n;
+            L.dst[1] = (__nv_bfloat16 *)ws;
         }
+        e = lay_out(L, dtype, p, K, s);
+        if (e != cudaSuccess) return fail_cuda(e);
         LinearParams P{};
         P.e = E;
         if (bias) P.e.bias = bias + n0;

@@ -53,7 +53,7 @@ def test_sizes(M, N, K, dt, out):
     kernels = dsa.last_kernels()
     if dt == BF16 and K % 8 == 0:
         assert kernels == {"linear"}
-    elif M <= 16 and (dt == F32 or N > 1):
+    elif M <= (16 if dt == F32 else 4) and (dt == F32 or N > 1):
         assert kernels == {"linear_simt"}
 
 

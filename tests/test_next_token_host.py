@@ -42,7 +42,8 @@ def test_linear_workspace():
     assert size(A, 64, B, 64, 1, 0, 32, 64) == 0
     assert size(A + 2, 64, B, 64, 1, 40, 32, 64) == 40 * 128
     assert size(A, 64, B, 65, 1, 40, 32, 64) == 32 * 128
-    assert size(A, 64, B, 65, 1, 16, 32, 64) == 0  # few tokens read W as it is
+    assert size(A, 64, B, 65, 1, 4, 32, 64) == 0 and size(A, 64, B, 65, 0, 16, 32, 64) == 0  # few tokens read W as it is
+    assert size(A, 64, B, 65, 1, 5, 32, 64) == 32 * 128 and size(A, 64, B, 64, 0, 17, 32, 64) == (17 * 384 + 255) // 256 * 256 + 32 * 384
     assert size(A, 33, B, 33, 1, 40, 32, 33) == 40 * 80 // 256 * 256 + (256 if 40 * 80 % 256 else 0) + 32 * 80
     assert size(A, 64, B, 64, 0, 40, 32, 64) == (40 + 32) * 384
     assert size(A, 64, B, 64, 0, 40, 1 << 20, 64) < (1 << 20) * 384  # not all of W at once
