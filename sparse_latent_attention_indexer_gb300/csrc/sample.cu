@@ -87,7 +87,7 @@ struct alignas(16) Shared {
     u64 in[2][MAX_SHARE], in_draw[MAX_SHARE], bound;
     int in_alone[MAX_SHARE], in_count[MAX_SHARE], in_kept[MAX_SHARE], in_first[MAX_SHARE];
     float in_top[MAX_SHARE];
-    int count, first;
+    int first, picked;
     u64 pick_base;               // of the bin that holds the bound
     int pick_bin, pick_to;
     float ch, cl, yh, yl;        // log2(e) / T, -log2(min_p)
@@ -459,65 +459,133 @@ __device__ void sort_few(Shared &S, u64 (&c)[E], int n) {
     }
 }
 
-// The end of a row whose kept tokens are among n <= E * THREADS candidates: one CTA sorts them, cuts the run by each rule
-// and draws.  all: what every token weighs, where there is no top-k.
+// Among one CTA's candidates (E a thread, at most `bound`): the last token of the shortest run whose count (or weight w) reaches
+// the target, which it does reach.  A histogram finds its bin, the bin's few tokens are sorted; many in one bin: all are.
+template <int E, bool WEIGHT, typename T>
+__device__ u64 select_few(const Row<T> &R, Shared &S, const u64 (&c)[E], const u64 (&w)[E], u64 bound, int n, u64 target) {
+    const int tid = threadIdx.x;
+    u64 *hist = S.hist[0], *some = &S.list[0][0], all;
+    __syncthreads();
+    for (int b = tid; b < BINS; b += THREADS) hist[b] = 0;
+    if (tid == 0) S.picked = 0;
+    __syncthreads();
+    int bin[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        bin[e] = c[e] <= bound && c[e] != NONE ? R.bin(logit_of(c[e])) : -1;
+        if (bin[e] >= 0) atomicAdd(&hist[bin[e]], WEIGHT ? w[e] : 1ull);
+    }
+    __syncthreads();
+    const u64 one = hist[2 * tid], two = hist[2 * tid + 1], sum = block_scan(S, one + two, all);
+    if (sum >= target && sum - one - two < target) {
+        const bool second = sum - two < target;
+        S.pick_bin = 2 * tid + second;
+        S.pick_base = second ? sum - two : sum - two - one;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (bin[e] == S.pick_bin) {
+            const int at = atomicAdd(&S.picked, 1);
+            if (at < WARPS * LIST) some[at] = c[e];
+        }
+    __syncthreads();
+    const int m = S.picked;
+    u64 base = S.pick_base;
+    const auto last = [&](auto &v, auto &of) {  // sorted values and their weights, base before them
+        u64 mine = 0;
+#pragma unroll
+        for (const u64 &x : of) mine += x;
+        u64 cum = base + block_scan(S, mine, all) - mine;
+        int e = 0;
+#pragma unroll
+        for (const u64 &x : of) {
+            if (cum < target && cum + x >= target) S.bound = v[e];
+            cum += x;
+            ++e;
+        }
+        __syncthreads();
+    };
+    const auto worth = [&](u64 x) { return x > bound || x == NONE ? 0ull : WEIGHT ? weight_of(R.top, logit_of(x), R.ch, R.cl, S.root) : 1ull; };
+    if (m <= THREADS) {
+        u64 v[1] = {tid < m ? some[tid] : NONE};
+        sort_few<1>(S, v, m);
+        u64 of[1] = {worth(v[0])};
+        last(v, of);
+    } else {
+        u64 v[E], of[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = c[e];
+        sort_few<E>(S, v, n);
+        base = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) of[e] = worth(v[e]);
+        last(v, of);
+    }
+    return S.bound;
+}
+
+// The end of a row whose kept tokens are among n <= E * THREADS candidates: one CTA cuts the run by each rule and draws.
+// all: what every token weighs, where there is no top-k.  E = 1 sorts them, E = 4 looks for the bounds (2048 candidates: 28 us
+// a row sorted, %SELECT% so).
 template <int E, typename T>
 __device__ void finish_few(const SampleParams &P, const Row<T> &R, Shared &S, int64_t row, int n, int region, int k, float p, float m,
                            u64 all) {
     const int first = E * threadIdx.x;
-    u64 by_index[E], sorted[E], w[E], mine = 0;
+    u64 by_index[E], w[E], mine = 0, total = all, bound = NONE;
+    float yh[E], yl[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) sorted[e] = by_index[e] = candidate(S, first + e, n, region, R.share);
-    if (threadIdx.x == 0) S.count = 0x7fffffff;
-    sort_few<E>(S, sorted, n);
-    const int run = k > 0 ? min(k, n) : n;
-    int keep = run;
+    for (int e = 0; e < E; ++e) by_index[e] = candidate(S, first + e, n, region, R.share);
+    if constexpr (E == 1) {
+        u64 sorted[1] = {by_index[0]};
+        sort_few<1>(S, sorted, n);
+        const int run = k > 0 ? min(k, n) : n;
+        if (first == run - 1) S.bound = sorted[0];
+        if (p < 1.0f) {
+            mine = first < run ? weight_of(R.top, logit_of(sorted[0]), R.ch, R.cl, S.root) : 0;
+            u64 sum, cum = block_scan(S, mine, sum);
+            if (k > 0) total = sum;
+            const u64 target = max(part_of(p, total, true), 1ull);
+            if (cum >= target && cum - mine < target) S.bound = sorted[0];
+        }
+        __syncthreads();
+        bound = S.bound;
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        w[e] = 0;
-        if (first + e >= run) continue;
-        float yh, yl;
-        const bool some = exponent(R.top, logit_of(sorted[e]), R.ch, R.cl, yh, yl);
-        if (some) w[e] = weight(yh, yl, S.root);
-        mine += w[e];
-        if (m > 0.0f && first + e > 0 && !(some ? (yh - S.yh) + (yl - S.yl) <= 0.0f : yh <= S.yh)) keep = min(keep, first + e);
+        const bool some = by_index[e] != NONE && exponent(R.top, logit_of(by_index[e]), R.ch, R.cl, yh[e], yl[e]);
+        if (!some) yh[e] = yl[e] = 0.0f;
+        w[e] = some ? weight(yh[e], yl[e], S.root) : 0;
+        // min-p after the others: a token that it drops counts towards their sums
+        if (!some && by_index[e] != NONE) yh[e] = INFINITY;
     }
-    u64 total = all;
-    if (p < 1.0f) {
-        u64 sum, cum = block_scan(S, mine, sum) - mine;
-        if (k > 0) total = sum;
-        const u64 target = max(part_of(p, total, true), 1ull);
+    if constexpr (E > 1) {
+        if (k > 0 && k < n) bound = select_few<E, false>(R, S, by_index, w, NONE, n, (u64)k);
+        if (p < 1.0f) {
+            if (k > 0) {
+                mine = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            cum += w[e];
-            if (cum >= target) keep = min(keep, first + e + 1);
+                for (int e = 0; e < E; ++e) mine += by_index[e] <= bound ? w[e] : 0;
+                block_scan(S, mine, total);
+            }
+            bound = select_few<E, true>(R, S, by_index, w, bound, n, max(part_of(p, total, true), 1ull));
         }
-    } else {
-        __syncthreads();
     }
-    keep = __reduce_min_sync(0xffffffffu, keep);
-    if ((threadIdx.x & 31) == 0 && keep < run) atomicMin(&S.count, keep);
-    __syncthreads();
-    keep = min(run, S.count);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (first + e == keep - 1) S.bound = sorted[e];
-    __syncthreads();
-    const u64 bound = S.bound;
-    float yh[E], yl[E];
+    int kept = 0;
     mine = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        w[e] = 0;
-        yh[e] = yl[e] = 0.0f;
-        if (by_index[e] <= bound && exponent(R.top, logit_of(by_index[e]), R.ch, R.cl, yh[e], yl[e])) w[e] = weight(yh[e], yl[e], S.root);
+        const bool in = by_index[e] <= bound && by_index[e] != NONE && (!(m > 0.0f) || (yh[e] - S.yh) + (yl[e] - S.yl) <= 0.0f);
+        if (!in) w[e] = 0;
+        kept += in;
         mine += w[e];
     }
-    u64 cum = block_scan(S, mine, total) - mine;
+    u64 kept_all, cum = block_scan(S, mine, total) - mine;
+    block_scan(S, (u64)kept, kept_all);
     const u64 goal = part_of(random_of(P, row), total, false);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        if (cum <= goal && cum + w[e] > goal) write_token(P, row, (int)(by_index[e] & (MAX_V - 1)), yh[e], yl[e], total, keep);
+        if (cum <= goal && cum + w[e] > goal) write_token(P, row, (int)(by_index[e] & (MAX_V - 1)), yh[e], yl[e], total, (int)kept_all);
         cum += w[e];
     }
 }
