@@ -720,24 +720,57 @@ _GATES = {None: _abi.DSA_ACT_NONE, "none": _abi.DSA_ACT_NONE, "sigmoid": _abi.DS
           "silu": _abi.DSA_ACT_SILU}
 
 
-def _matrix(fn: str, name: str, t: torch.Tensor, rows, width, dtype):
-    """A 2-D tensor of the shape and type with contiguous rows; its row stride."""
-    _rows_2d(fn, name, t, width, rows)
+def _wrong(fn: str, name: str, t, dev: int, shape, dtype):
+    """What _matrix and _vector refuse, in words."""
+    if not isinstance(t, torch.Tensor):
+        return TypeError(f"{fn}: {name} must be a tensor, not {type(t).__name__}")
+    if t.get_device() < 0:
+        return ValueError(f"{fn}: {name} must be a CUDA tensor, is on {t.device}")
+    if t.get_device() != dev:
+        return ValueError(f"{fn}: {name} is on {t.device}, other arguments on cuda:{dev}")
     if t.dtype != dtype:
-        raise ValueError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
-    return t.stride(0) if rows > 1 else width
+        return ValueError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        return ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return ValueError(f"{fn}: {name} must have contiguous rows" if t.dim() == 2 else f"{fn}: {name} must be contiguous")
 
 
-def _vector(fn: str, name: str, t, n: int, dtype):
-    if t is not None and (t.dtype != dtype or t.shape != (n,) or not t.is_contiguous()):
-        raise ValueError(f"{fn}: {name} must be contiguous {dtype} [{n}]")
+def _matrix(fn: str, name: str, t, dev: int, shape, dtype) -> int:
+    """The row stride of a tensor of this shape (2-D) and type with contiguous rows on the device."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        raise _wrong(fn, name, t, dev, shape, dtype)
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise _wrong(fn, name, t, dev, shape, dtype)
+    return ld if shape[0] > 1 else shape[1]
+
+
+def _vector(fn: str, name: str, t, dev: int, shape, dtype):
+    """The address of a contiguous tensor of this shape (1-D) and type, or None."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise _wrong(fn, name, t, dev, shape, dtype)
+    return t.data_ptr()
+
+
+def _first_of(fn: str, name: str, t, dims: int) -> int:
+    """The device of a call's first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise _wrong(fn, name, t, dev, t.shape, t.dtype)
+    if t.dim() != dims:
+        raise ValueError(f"{fn}: {name} must be {dims}-D, has shape {tuple(t.shape)}")
+    return dev
 
 
 def dsa_linear_workspace_size(x: torch.Tensor, weight: torch.Tensor) -> int:
     fn = "dsa_linear_workspace_size"
+    dev = _first_of(fn, "x", x, 2)
     (M, K), N = x.shape, weight.shape[0]
-    return _abi.load().dsa_linear_workspace_size(x.data_ptr(), _matrix(fn, "x", x, M, K, x.dtype), weight.data_ptr(),
-                                                 _matrix(fn, "weight", weight, N, K, x.dtype), _dt_of(x.dtype), M, N, K)
+    return _abi.load().dsa_linear_workspace_size(x.data_ptr(), _matrix(fn, "x", x, dev, (M, K), x.dtype),
+                                                 weight.data_ptr(), _matrix(fn, "weight", weight, dev, (N, K), x.dtype),
+                                                 _dt_of(x.dtype), M, N, K)
 
 
 def dsa_linear(x, weight, bias=None, act=None, residual=None, y=None, dtype=None, workspace=None, stream=None):
@@ -745,22 +778,21 @@ def dsa_linear(x, weight, bias=None, act=None, residual=None, y=None, dtype=None
     fp32, residual and y [M, N] of ``dtype`` (default: y's, the residual's or x's).  ``act``: "relu", "silu", "gelu",
     "gelu_tanh" or None.  y may be residual.  Returns y."""
     fn = "dsa_linear"
-    dev = _on_one_device(fn, (("x", x), ("weight", weight), ("bias", bias), ("residual", residual), ("y", y),
-                              ("workspace", workspace)))
     if act not in _ACTS:
         raise ValueError(f"{fn}: act must be 'relu', 'silu', 'gelu', 'gelu_tanh' or None, not {act!r}")
-    if x.dim() != 2 or weight.dim() != 2:
-        raise ValueError(f"{fn}: x and weight must be 2-D")
-    (M, K), N = x.shape, weight.shape[0]
-    ld_x, ld_w = _matrix(fn, "x", x, M, K, x.dtype), _matrix(fn, "weight", weight, N, K, x.dtype)
-    _vector(fn, "bias", bias, N, torch.float32)
+    dev = _first_of(fn, "x", x, 2)
+    M, K = x.shape
+    N = weight.shape[0]
+    x_dtype = x.dtype
+    ld_x, ld_w = _matrix(fn, "x", x, dev, (M, K), x_dtype), _matrix(fn, "weight", weight, dev, (N, K), x_dtype)
     if dtype is None:
         dtype = (y if y is not None else residual if residual is not None else x).dtype
-    dt, y_dt = _dt_of(x.dtype), _dt_of(dtype)
-    ld_r = 0 if residual is None else _matrix(fn, "residual", residual, M, N, dtype)
-    ld_y = N if y is None else _matrix(fn, "y", y, M, N, dtype)
-    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
-        raise ValueError(f"{fn}: workspace must be a contiguous uint8 tensor")
+    dt, y_dt = _dt_of(x_dtype), _dt_of(dtype)
+    ld_r = 0 if residual is None else _matrix(fn, "residual", residual, dev, (M, N), dtype)
+    ld_y = N if y is None else _matrix(fn, "y", y, dev, (M, N), dtype)
+    bias_ = _vector(fn, "bias", bias, dev, (N,), torch.float32)
+    if workspace is not None:
+        _vector(fn, "workspace", workspace, dev, (workspace.numel(),), torch.uint8)
     lib = _abi.load()
     px, pw = x.data_ptr(), weight.data_ptr()
     with _launching(dev, stream):
@@ -770,7 +802,7 @@ def dsa_linear(x, weight, bias=None, act=None, residual=None, y=None, dtype=None
             need = lib.dsa_linear_workspace_size(px, ld_x, pw, ld_w, dt, M, N, K)
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        _check(fn, lib.dsa_linear(px, ld_x, pw, ld_w, dt, M, N, K, _addr(bias), _ACTS[act], _addr(residual), ld_r,
+        _check(fn, lib.dsa_linear(px, ld_x, pw, ld_w, dt, M, N, K, bias_, _ACTS[act], _addr(residual), ld_r,
                                   y.data_ptr(), ld_y, y_dt, _addr(workspace),
                                   0 if workspace is None else workspace.numel(),
                                   torch._C._cuda_getCurrentRawStream(dev)))
@@ -783,11 +815,11 @@ class Norm:
     def __init__(self, kind="rms", gain=None, bias=None):
         if kind not in _NORMS:
             raise ValueError(f"Norm: kind must be 'rms', 'layer' or 'none', not {kind!r}")
-        self.kind, self.gain, self.bias = kind, gain, bias
-        self.struct = _abi.dsa_norm(_NORMS[kind], _addr(gain), _addr(bias))
+        self.kind, self.gain, self.bias = _NORMS[kind], gain, bias
 
-
-_NO_NORM = Norm("none")
+    def _struct(self, fn, name, dev, D):
+        return self.kind, _vector(fn, name + ".gain", self.gain, dev, (D,), torch.float32), \
+            _vector(fn, name + ".bias", self.bias, dev, (D,), torch.float32)
 
 
 def dsa_block_norm(h, pre: Norm | None = None, u=None, post: Norm | None = None, gate=None, gate_act=None, skip=1.0,
@@ -797,40 +829,37 @@ def dsa_block_norm(h, pre: Norm | None = None, u=None, post: Norm | None = None,
     or None).  h, h_out and u, gate, y are fp32 or bf16; y's type is u's, or ``dtype``.  h_out may be h, y may be u.
     Returns (h', y), None for one that is not wanted."""
     fn = "dsa_block_norm"
-    pre, post = pre or _NO_NORM, post or _NO_NORM
-    dev = _on_one_device(fn, (("h", h), ("u", u), ("gate", gate), ("h_out", h_out), ("y", y),
-                              ("pre.gain", pre.gain), ("pre.bias", pre.bias), ("post.gain", post.gain),
-                              ("post.bias", post.bias)))
     if gate_act not in _GATES:
         raise ValueError(f"{fn}: gate_act must be 'sigmoid', 'silu' or None, not {gate_act!r}")
-    if h.dim() != 2:
-        raise ValueError(f"{fn}: h must be 2-D")
-    N, D = h.shape
-    x_dtype = next((t.dtype for t in (u, gate, y) if t is not None), dtype or h.dtype)
+    dev = _first_of(fn, "h", h, 2)
+    N, D = shape = h.shape
+    h_dtype = h.dtype
+    x_dtype = next((t.dtype for t in (u, gate, y) if t is not None), dtype or h_dtype)
     if dtype is not None and dtype != x_dtype:
         raise ValueError(f"{fn}: dtype is {dtype} beside {x_dtype} tensors")
-    for n in (pre, post):
-        _vector(fn, "gain", n.gain, D, torch.float32)
-        _vector(fn, "bias", n.bias, D, torch.float32)
-    ld_h = _matrix(fn, "h", h, N, D, h.dtype)
-    ld_u = 0 if u is None else _matrix(fn, "u", u, N, D, x_dtype)
-    ld_g = 0
+    ld_h = _matrix(fn, "h", h, dev, shape, h_dtype)
+    ld_u = 0 if u is None else _matrix(fn, "u", u, dev, shape, x_dtype)
+    ld_g, ld_ho, ld_y = 0, D, D
     if gate is not None:
-        rows = 1 if gate.dim() == 2 and gate.shape[0] == 1 else N
-        ld_g = _matrix(fn, "gate", gate, rows, D, x_dtype)
-        if rows == 1 and N > 1:
-            ld_g = 0
-    ld_ho = D if h_out is None else _matrix(fn, "h_out", h_out, N, D, h.dtype)
-    ld_y = D if y is None else _matrix(fn, "y", y, N, D, x_dtype)
-    h_dt, x_dt = _dt_of(h.dtype), _dt_of(x_dtype)
+        if N > 1 and gate.shape == (1, D):
+            _matrix(fn, "gate", gate, dev, (1, D), x_dtype)
+        else:
+            ld_g = _matrix(fn, "gate", gate, dev, shape, x_dtype)
+    if h_out is not None:
+        ld_ho = _matrix(fn, "h_out", h_out, dev, shape, h_dtype)
+    if y is not None:
+        ld_y = _matrix(fn, "y", y, dev, shape, x_dtype)
+    post_ = (0, None, None) if post is None else post._struct(fn, "post", dev, D)
+    pre_ = (0, None, None) if pre is None else pre._struct(fn, "pre", dev, D)
+    h_dt, x_dt = _dt_of(h_dtype), _dt_of(x_dtype)
     with _launching(dev, stream):
         if h_out is None and want_h:
-            h_out = torch.empty((N, D), dtype=h.dtype, device=h.device)
+            h_out = torch.empty(shape, dtype=h_dtype, device=h.device)
         if y is None and want_y:
-            y = torch.empty((N, D), dtype=x_dtype, device=h.device)
+            y = torch.empty(shape, dtype=x_dtype, device=h.device)
         args = _abi.dsa_block_norm_args(N, D, h_dt, x_dt, h.data_ptr(), ld_h, _addr(u), ld_u, _addr(gate), ld_g,
-                                        _GATES[gate_act], post.struct, pre.struct, skip, scale, eps, _addr(h_out),
-                                        ld_ho, _addr(y), ld_y)
+                                        _GATES[gate_act], post_, pre_, skip, scale, eps, _addr(h_out), ld_ho, _addr(y),
+                                        ld_y)
         _check(fn, _abi.load().dsa_block_norm(ctypes.byref(args), torch._C._cuda_getCurrentRawStream(dev)))
     return h_out, y
 
@@ -843,22 +872,22 @@ def dsa_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=
     times the highest probability.  Returns (token [R] int32, its log-probability among the kept [R] fp32, how many
     were kept [R] int32); None for what is not wanted.  A row of nothing but -inf and NaN gives token -1."""
     fn = "dsa_sample"
-    dev = _on_one_device(fn, (("logits", logits), ("uniform", uniform), ("temperature", temperature), ("top_k", top_k),
-                              ("top_p", top_p), ("min_p", min_p), ("token", token)))
-    if logits.dim() != 2:
-        raise ValueError(f"{fn}: logits must be 2-D")
+    dev = _first_of(fn, "logits", logits, 2)
     R, V = logits.shape
-    ld, dt = _matrix(fn, "logits", logits, R, V, logits.dtype), _dt_of(logits.dtype)
-    for name, t in (("uniform", uniform), ("temperature", temperature), ("top_p", top_p), ("min_p", min_p)):
-        _vector(fn, name, t, R, torch.float32)
-    _vector(fn, "top_k", top_k, R, torch.int32)
-    _vector(fn, "token", token, R, torch.int32)
+    f32, i32, rows = torch.float32, torch.int32, (R,)
+    ld, dt = _matrix(fn, "logits", logits, dev, (R, V), logits.dtype), _dt_of(logits.dtype)
+    if uniform is None:
+        raise ValueError(f"{fn}: no uniform numbers")
+    u_, T_ = _vector(fn, "uniform", uniform, dev, rows, f32), _vector(fn, "temperature", temperature, dev, rows, f32)
+    k_, p_ = _vector(fn, "top_k", top_k, dev, rows, i32), _vector(fn, "top_p", top_p, dev, rows, f32)
+    m_, token_ = _vector(fn, "min_p", min_p, dev, rows, f32), _vector(fn, "token", token, dev, rows, i32)
     with _launching(dev, stream):
+        on = logits.device
         if token is None:
-            token = torch.empty(R, dtype=torch.int32, device=logits.device)
-        logprob = torch.empty(R, dtype=torch.float32, device=logits.device) if want_logprob else None
-        kept = torch.empty(R, dtype=torch.int32, device=logits.device) if want_kept else None
-        _check(fn, _abi.load().dsa_sample(logits.data_ptr(), ld, dt, R, V, uniform.data_ptr(), _addr(temperature),
-                                          _addr(top_k), _addr(top_p), _addr(min_p), token.data_ptr(), _addr(logprob),
+            token = torch.empty(rows, dtype=i32, device=on)
+            token_ = token.data_ptr()
+        logprob = torch.empty(rows, dtype=f32, device=on) if want_logprob else None
+        kept = torch.empty(rows, dtype=i32, device=on) if want_kept else None
+        _check(fn, _abi.load().dsa_sample(logits.data_ptr(), ld, dt, R, V, u_, T_, k_, p_, m_, token_, _addr(logprob),
                                           _addr(kept), torch._C._cuda_getCurrentRawStream(dev)))
     return token, logprob, kept
