@@ -797,11 +797,11 @@ def dsa_linear(x, weight, bias=None, act=None, residual=None, y=None, dtype=None
     px, pw = x.data_ptr(), weight.data_ptr()
     with _launching(dev, stream):
         if y is None:
-            y = torch.empty((M, N), dtype=dtype, device=x.device)
+            y = x.new_empty((M, N), dtype=dtype)
         if workspace is None:
             need = lib.dsa_linear_workspace_size(px, ld_x, pw, ld_w, dt, M, N, K)
             if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+                workspace = x.new_empty(need, dtype=torch.uint8)
         _check(fn, lib.dsa_linear(px, ld_x, pw, ld_w, dt, M, N, K, bias_, _ACTS[act], _addr(residual), ld_r,
                                   y.data_ptr(), ld_y, y_dt, _addr(workspace),
                                   0 if workspace is None else workspace.numel(),
@@ -854,9 +854,9 @@ def dsa_block_norm(h, pre: Norm | None = None, u=None, post: Norm | None = None,
     h_dt, x_dt = _dt_of(h_dtype), _dt_of(x_dtype)
     with _launching(dev, stream):
         if h_out is None and want_h:
-            h_out = torch.empty(shape, dtype=h_dtype, device=h.device)
+            h_out = h.new_empty(shape)
         if y is None and want_y:
-            y = torch.empty(shape, dtype=x_dtype, device=h.device)
+            y = h.new_empty(shape, dtype=x_dtype)
         args = _abi.dsa_block_norm_args(N, D, h_dt, x_dt, h.data_ptr(), ld_h, _addr(u), ld_u, _addr(gate), ld_g,
                                         _GATES[gate_act], post_, pre_, skip, scale, eps, _addr(h_out), ld_ho, _addr(y),
                                         ld_y)

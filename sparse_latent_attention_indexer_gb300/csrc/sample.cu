@@ -10,8 +10,8 @@
 // pairs of fp32 values (fp64 units are few on this GPU: 2 results a cycle an SM against 128).
 // Integer sums do not depend on their order, which lets threads and CTAs add as they come.
 //
-// A cluster of up to 8 CTAs keeps a row in shared memory (one bulk copy each), so HBM is read
-// once.  What follows the maximum is to find few candidates among many tokens:
+// A cluster of up to 8 CTAs shares a row, and keeps it in shared memory (one bulk copy each) or
+// finds it in L2 again, so HBM is read once.  What follows the maximum is to find few candidates among many tokens:
 //   * top-k: the k-th largest of the threads' own maxima (a histogram of one value a thread) is
 //     not above the k-th largest logit, so the tokens from there on hold the run;
 //   * min-p: the tokens down to that weight;
@@ -227,15 +227,20 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
     return v;
 }
 
-// A CTA's part of a row.
-template <typename T>
+// A CTA's part of a row, in shared memory or (not CACHED) where it lies.
+template <typename T_, bool CACHED>
 struct Row {
+    typedef T_ T;
     const T *raw;          // the logits, as they come
+    bool infinite;         // not CACHED: +inf counts as 0, all else as nothing
     int first, n;          // index of the first, how many
     int rank, share;
     float top, ch, cl, bins;  // bins: bins per unit of logit
 
-    __device__ __forceinline__ float at(int i) const { return to_f32(raw[i]); }
+    __device__ __forceinline__ float at(int i) const {
+        const float l = to_f32(raw[i]);
+        return CACHED || !infinite ? l : l == INFINITY ? 0.0f : -INFINITY;
+    }
     // Bins fall with the logit; equal logits have equal ones.  A token is in bin b or before: x < b + 1.
     __device__ __forceinline__ float x(float l) const { return (top - l) * bins; }
     __device__ __forceinline__ int bin(float l) const { return (int)fminf(x(l), (float)(BINS - 1)); }
@@ -277,8 +282,8 @@ __device__ Pick pick_bin(int share, Shared &S, const u64 *hist, u64 base, u64 wa
 }
 
 // Counts or weights of the tokens with c <= bound over the whole range.
-template <bool WEIGHT, typename T>
-__device__ Pick first_level(const Row<T> &R, Shared &S, u64 bound, u64 want, float p, int &turn) {
+template <bool WEIGHT, typename Part>
+__device__ Pick first_level(const Part &R, Shared &S, u64 bound, u64 want, float p, int &turn) {
     u64 *hist = S.hist[turn];
     turn ^= 1;  // the other CTAs may still read this one until the next level's meeting; the level after clears it
     __syncthreads();
@@ -298,8 +303,8 @@ __device__ Pick first_level(const Row<T> &R, Shared &S, u64 bound, u64 want, flo
 }
 
 // From the first level's bin on to one token: the last of the shortest run whose count (or weight) reaches the target.
-template <bool WEIGHT, typename T>
-__device__ u64 refine(const Row<T> &R, Shared &S, u64 bound, Pick at, u64 target, int &turn) {
+template <bool WEIGHT, typename Part>
+__device__ u64 refine(const Part &R, Shared &S, u64 bound, Pick at, u64 target, int &turn) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     u64 low = 0, high = NONE;
     int shift = -1;  // -1: `at` is the first level's bin
@@ -461,8 +466,8 @@ __device__ void sort_few(Shared &S, u64 (&c)[E], int n) {
 
 // Among one CTA's candidates (E a thread, at most `bound`): the last token of the shortest run whose count (or weight w) reaches
 // the target, which it does reach.  A histogram finds its bin, the bin's few tokens are sorted; many in one bin: all are.
-template <int E, bool WEIGHT, typename T>
-__device__ u64 select_few(const Row<T> &R, Shared &S, const u64 (&c)[E], const u64 (&w)[E], u64 bound, int n, u64 target) {
+template <int E, bool WEIGHT, typename Part>
+__device__ u64 select_few(const Part &R, Shared &S, const u64 (&c)[E], const u64 (&w)[E], u64 bound, int n, u64 target) {
     const int tid = threadIdx.x;
     u64 *hist = S.hist[0], *some = &S.list[0][0], all;
     __syncthreads();
@@ -528,8 +533,8 @@ __device__ u64 select_few(const Row<T> &R, Shared &S, const u64 (&c)[E], const u
 // The end of a row whose kept tokens are among n <= E * THREADS candidates: one CTA cuts the run by each rule and draws.
 // all: what every token weighs, where there is no top-k.  E = 1 sorts them, E = 4 looks for the bounds (2048 candidates: 28 us
 // a row sorted, %SELECT% so).
-template <int E, typename T>
-__device__ void finish_few(const SampleParams &P, const Row<T> &R, Shared &S, int64_t row, int n, int region, int k, float p, float m,
+template <int E, typename Part>
+__device__ void finish_few(const SampleParams &P, const Part &R, Shared &S, int64_t row, int n, int region, int k, float p, float m,
                            u64 all) {
     const int first = E * threadIdx.x;
     u64 by_index[E], w[E], mine = 0, total = all, bound = NONE;
@@ -591,8 +596,8 @@ __device__ void finish_few(const SampleParams &P, const Row<T> &R, Shared &S, in
 }
 
 // The last token of a run by top-p that ends among n candidates: `before` is what the tokens before them weigh.
-template <int E, typename T>
-__device__ void bound_few(const Row<T> &R, Shared &S, int n, u64 before, u64 target) {
+template <int E, typename Part>
+__device__ void bound_few(const Part &R, Shared &S, int n, u64 before, u64 target) {
     u64 c[E], w[E], mine = 0, sum;
 #pragma unroll
     for (int e = 0; e < E; ++e) c[e] = candidate(S, E * threadIdx.x + e, n, 0, R.share);
@@ -640,23 +645,49 @@ __device__ T *fetch_slice(Shared &S, uint8_t *room, const T *src, int n, bool &c
     return raw;
 }
 
+// This thread's maximum over its share of a CTA's logits, 16 bytes at a time: 64 KB of the CTA are on their way at once.
+__device__ __forceinline__ float max_in(const uint4 &q, float m, const float *) {
+    return fmaxf(fmaxf(fmaxf(m, __uint_as_float(q.x)), fmaxf(__uint_as_float(q.y), __uint_as_float(q.z))), __uint_as_float(q.w));
+}
+__device__ __forceinline__ float max_in(const uint4 &q, float m, const __nv_bfloat16 *) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)));
+    return m;
+}
 template <typename T>
+__device__ __forceinline__ float max_of(const T *src, int n) {
+    const int off = (int)((uintptr_t)src & 15), each = 16 / (int)sizeof(T), head = min(n, (16 - off) % 16 / (int)sizeof(T));
+    const int body = (n - head) / each, tail = head + body * each;
+    const uint4 *p = (const uint4 *)(src + head);
+    float m = -INFINITY;
+    if ((int)threadIdx.x < head) m = fmaxf(m, to_f32(src[threadIdx.x]));
+    if ((int)threadIdx.x < n - tail) m = fmaxf(m, to_f32(src[tail + threadIdx.x]));
+#pragma unroll 8
+    for (int i = threadIdx.x; i < body; i += THREADS) m = max_in(__ldg(p + i), m, (const T *)nullptr);
+    return m;
+}
+
+template <typename T, bool CACHED>
 __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constant__ SampleParams P) {
     extern __shared__ __align__(16) uint8_t dynamic[];
     Shared &S = *(Shared *)dynamic;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)tc::cluster_rank();
     const int64_t row = blockIdx.x / P.share;
-    Row<T> R;
+    Row<T, CACHED> R;
     R.rank = rank;
     R.share = P.share;
     R.first = min(P.V, rank * P.slice);
     R.n = min(P.V, R.first + P.slice) - R.first;
     meet_arrive();  // waited for before anything is pushed: the other CTAs have started
     pdl_wait();     // the set-up above overlapped the previous kernel
-    bool coming;
-    T *raw = fetch_slice(S, dynamic + sizeof(Shared), (const T *)P.logits + row * P.ld + R.first, R.n, coming);
-    R.raw = raw;
+    bool coming = false;
+    const T *src = (const T *)P.logits + row * P.ld + R.first;
+    T *raw = nullptr;
+    if constexpr (CACHED) R.raw = raw = fetch_slice(S, dynamic + sizeof(Shared), src, R.n, coming);
+    else R.raw = src;
+    R.infinite = false;
 
     const float T_ = P.temperature ? __ldg(P.temperature + row) : 1.0f;
     const float p = P.top_p ? __ldg(P.top_p + row) : 1.0f, m = P.min_p ? __ldg(P.min_p + row) : 0.0f;
@@ -682,8 +713,12 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
 
     // ---------------- the maximum ----------------
     float mine = -INFINITY;  // of this thread's tokens; a NaN counts as nothing
+    if constexpr (CACHED) {
 #pragma unroll 8
-    for (int i = tid; i < R.n; i += THREADS) mine = fmaxf(mine, R.at(i));
+        for (int i = tid; i < R.n; i += THREADS) mine = fmaxf(mine, R.at(i));
+    } else {
+        mine = max_of(src, R.n);
+    }
     {
         const u64 w = warp_min((u64)~ordered_key(mine));
         if (lane == 0) S.warp_sum[warp] = w;
@@ -691,6 +726,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
         const u64 b = warp_min(lane < WARPS ? S.warp_sum[lane] : NONE);
         R.top = logit_of(b << INDEX_BITS);  // the CTA's
     }
+    const float own_top = R.top;
 
     // The tokens of the bins up to `to` (no more than `most` of them, or the answer is above FEW), in S.list by warp; and where
     // this warp's go among them.
@@ -781,12 +817,12 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
 
     // ---------------- the first token, or none ----------------
     if (R.top == -INFINITY || k == 1) {  // the same in every thread of the cluster
-        if (R.top > -INFINITY && mine == R.top)
+        // CACHED: a thread's maximum is over the tokens that it looks through here; else the CTA's is known, not the thread's
+        if (R.top > -INFINITY && (CACHED ? mine : own_top) == R.top) {
+#pragma unroll 8
             for (int i = tid; i < R.n; i += THREADS)
-                if (R.at(i) == R.top) {
-                    atomicMin(&S.first, R.first + i);
-                    break;
-                }
+                if (R.at(i) == R.top) atomicMin(&S.first, R.first + i);
+        }
         __syncthreads();
         if (tid == 0) push(&S.in_first[rank], 0, S.first);
         meet();
@@ -804,7 +840,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     R.cl = S.cl;
     if (R.top == INFINITY) {  // the infinite ones alone, as equals
         __syncthreads();
-        for (int i = tid; i < R.n; i += THREADS) raw[i] = from_f32<T>(R.at(i) == INFINITY ? 0.0f : -INFINITY);
+        if constexpr (CACHED)
+            for (int i = tid; i < R.n; i += THREADS) raw[i] = from_f32<T>(R.at(i) == INFINITY ? 0.0f : -INFINITY);
+        else R.infinite = true;
         mine = mine == INFINITY ? 0.0f : -INFINITY;
         R.top = 0.0f;
         __syncthreads();
@@ -1030,12 +1068,12 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     }
 }
 
-template <typename T>
+template <typename T, bool CACHED>
 cudaError_t launch(const SampleParams &P, int R, cudaStream_t s) {
-    auto *kernel = sample_kernel<T>;
-    const int smem = (int)sizeof(Shared) + P.slice * (int)sizeof(T) + 16;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(Shared) + MAX_V / MAX_SHARE * (int)sizeof(T) + 16);
+    auto *kernel = sample_kernel<T, CACHED>;
+    const int most = (int)sizeof(Shared) + MAX_V / MAX_SHARE * (int)sizeof(T) + 16;
+    const int smem = (int)sizeof(Shared) + (CACHED ? P.slice * (int)sizeof(T) + 16 : 0);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)R * P.share);
@@ -1087,9 +1125,27 @@ extern "C" int dsa_sample(const void *logits, int64_t ld, int dtype, int R, int 
     P.logits = logits;
     P.ld = R > 1 ? ld : 0;
     P.V = V;
-    P.share = 1;
-    while (P.share < MAX_SHARE && V > P.share * 4096) P.share *= 2;
-    P.slice = ((V + P.share - 1) / P.share + 31) / 32 * 32;
+    // CTAs a row, and whether they keep their part of it.  A row takes some 20,000 cycles and 0.8 for a token of a CTA, one with
+    // top-p alone 25,000 and 2.7; without its part in shared memory (from L2) a fifth more for a token, but two CTAs
+    // an SM at any length.  What comes after the first rows that the SMs hold takes the average, the last rows may be slow ones.
+    // %TIMES%
+    const int item = dtype == DSA_F32 ? 4 : 2, sms = device_sm_count();
+    double least = 1e30;
+    bool cached = true;
+    for (int share = 1; share <= MAX_SHARE; share *= 2)
+        for (int keep = 1; keep >= 0; --keep) {
+            const int slice = ((V + share - 1) / share + 31) / 32 * 32;
+            if (keep && slice > MAX_V / MAX_SHARE) continue;
+            const int per_sm = !keep || (int)sizeof(Shared) + slice * item + 16 <= 113 * 1024 ? 2 : 1;
+            const double more = std::max(0.0, (double)R * share / (sms * per_sm) - 1), token = keep ? slice : 1.2 * slice;
+            const double t = more * (20000 + 0.8 * token) + 25000 + 2.7 * token;
+            if (t < least) {
+                least = t;
+                P.share = share;
+                P.slice = slice;
+                cached = keep;
+            }
+        }
     P.u = u;
     P.temperature = temperature;
     P.top_k = top_k;
@@ -1098,7 +1154,9 @@ extern "C" int dsa_sample(const void *logits, int64_t ld, int dtype, int R, int 
     P.token = token;
     P.logprob = logprob;
     P.kept = kept;
-    const cudaError_t e = dtype == DSA_F32 ? launch<float>(P, R, (cudaStream_t)stream) : launch<__nv_bfloat16>(P, R, (cudaStream_t)stream);
+    const cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = dtype == DSA_F32 ? cached ? launch<float, true>(P, R, s) : launch<float, false>(P, R, s)
+                          : cached ? launch<__nv_bfloat16, true>(P, R, s) : launch<__nv_bfloat16, false>(P, R, s);
     if (e != cudaSuccess) return fail_cuda(e);
     note_launch(DSA_KERNEL_SAMPLE);
     return DSA_OK;

@@ -204,3 +204,28 @@ def test_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(token, want.flip(0))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("n,V", [(256, 131072), (90, 262141), (700, 20011)])
+def test_large_batches(n, V, dt):
+    """Many long rows, of every kind side by side: the same rules whichever way a row's CTAs share it."""
+    g = torch.Generator(device="cuda").manual_seed(n + V)
+    x = 2 * torch.randn(n, V, generator=g, device="cuda")
+    x.scatter_add_(1, torch.randint(0, V, (n, 20), generator=g, device="cuda"), 4 + 3 * torch.rand(n, 20, generator=g, device="cuda"))
+    x[3], x[4, V - 5:], x[5] = -INF, INF, 1.5
+    x[6, : V // 3] = float("nan")
+    x[7] = torch.randint(-2, 3, (V,), generator=g, device="cuda").float()
+    x[8].masked_fill_(torch.rand(V, generator=g, device="cuda") < 0.99, -INF)
+    x = x.to(dt)
+    pick = lambda vals: [vals[i % len(vals)] for i in range(n)]  # noqa: E731
+    u = torch.rand(n, generator=g, device="cuda").tolist()
+    T, k = pick([0.0, 0.5, 0.8, 1.0, 1.3]), pick([0, 1, 20, 0, 170, 200, 0, 1000, 5000, V - 1, 0])
+    p, m = pick([1.0, 0.9, 0.5, 0.95, 0.999, 1.0, 0.8]), pick([0.0, 0.0, 0.05])
+    token, logprob, kept = dsa.dsa_sample(x, on(u), on(T), on(k, torch.int32), on(p), on(m), want_kept=True)
+    f = lambda v: float(torch.tensor(v, dtype=F32))  # noqa: E731
+    for i in list(range(60)) + list(range(60, n, 7)):
+        want = R.sample_row(x[i], f(u[i]), f(T[i]), k[i], f(p[i]), f(m[i]))
+        assert (int(token[i]), int(kept[i])) == want[::2], f"row {i}"
+        if want[1] > -INF:
+            assert abs(float(logprob[i]) - want[1]) <= 8 * 2.0 ** -24 * (abs(want[1]) + 2.0 ** -20)
