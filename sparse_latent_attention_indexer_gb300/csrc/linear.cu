@@ -544,8 +544,7 @@ __global__ void __launch_bounds__(256) linear_layout_kernel(const __grid_constan
 
 // ---------------------------------------------------------------------------
 // Few tokens whose rows the TMA does not take (off 16 bytes, fp32): a pass over W to lay it out would cost several times what
-// the product does, so a warp takes four features and up to 16 tokens (more tokens: more CTAs, W from L2) and reads W as it
-// is, V values at once.  SPLIT: the CTA's eight warps share K.  Bound by HBM for a token or two, then by the FMA pipes.
+// the product does, so a warp takes four features and every token and reads W as it is, V values at once.  SPLIT: the CTA's eight warps share K.  Bound by HBM for a token or two, then by the FMA pipes.
 // ---------------------------------------------------------------------------
 constexpr int FEW = 16;
 
@@ -566,7 +565,7 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_
     __shared__ float sums[8][4 * MT];
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int f0 = SPLIT ? (int)blockIdx.x * 4 : ((int)blockIdx.x * 8 + warp) * 4, m0 = (int)blockIdx.y * MT;
+    const int f0 = SPLIT ? (int)blockIdx.x * 4 : ((int)blockIdx.x * 8 + warp) * 4;
     const int per = SPLIT ? ((K + 7) / 8 + 32 * V - 1) / (32 * V) * (32 * V) : K;
     const int k0 = min((int64_t)K, SPLIT ? (int64_t)warp * per : 0), k1 = (int)min((int64_t)K, (int64_t)k0 + per);
     float acc[4][MT];
@@ -588,7 +587,7 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 float xv[V];
-                read<T, V>(x + (int64_t)(m0 + m) * ld_x + k + h * 32 * V, m0 + m < M && k + h * 32 * V < k1, xv);
+                read<T, V>(x + m * ld_x + k + h * 32 * V, m < M && k + h * 32 * V < k1, xv);
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -607,7 +606,7 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_
     __syncthreads();
     const int count = SPLIT ? 4 * MT : 8 * 4 * MT;
     for (int i = threadIdx.x; i < count; i += 256) {
-        const int wi = i / (4 * MT), at = i % (4 * MT), m = m0 + at / 4;
+        const int wi = i / (4 * MT), at = i % (4 * MT), m = at / 4;
         const int f = SPLIT ? f0 + at % 4 : ((int)blockIdx.x * 8 + wi) * 4 + at % 4;
         if (m >= M || f >= N) continue;
         float v = sums[wi][at];
@@ -622,10 +621,9 @@ template <typename T, int MT, int V>
 cudaError_t launch_few(const T *x, int64_t ld_x, const T *W, int64_t ld_w, int M, int N, int K, const Epilogue &E,
                        cudaStream_t s) {
     // 32 features a CTA once that gives every SM two
-    const int groups = (M + MT - 1) / MT;
-    const bool split = (int64_t)N * groups < 64 * device_sm_count();
-    return split ? launch_pdl(linear_few_kernel<T, MT, V, true>, dim3((N + 3) / 4, groups), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E)
-                 : launch_pdl(linear_few_kernel<T, MT, V, false>, dim3((N + 31) / 32, groups), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E);
+    const bool split = N < 64 * device_sm_count();
+    return split ? launch_pdl(linear_few_kernel<T, MT, V, true>, dim3((N + 3) / 4), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E)
+                 : launch_pdl(linear_few_kernel<T, MT, V, false>, dim3((N + 31) / 32), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E);
 }
 template <typename T, int V>
 cudaError_t launch_few(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int M, int N, int K, const Epilogue &E,

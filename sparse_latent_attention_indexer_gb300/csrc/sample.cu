@@ -16,7 +16,7 @@
 //     not above the k-th largest logit, so the tokens from there on hold the run;
 //   * min-p: the tokens down to that weight;
 //   * top-p: a histogram of approximate weights in bins of 1/32 of a nat, whose sums are good to
-//     2^-15, finds the bin or two in which the run ends; a pass over exact weights gives the sum
+//     2^-13, finds the bin or two in which the run ends; a pass over exact weights gives the sum
 //     before them and the whole.
 // Up to 2048 candidates are sorted by one CTA, which cuts the run (and draws, where the candidates
 // are all there is to draw from).  More of them, as many equal logits or a top_p near 1 give, go
@@ -863,8 +863,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     } else if (by_m) {
         to = (int)fminf(PER_NAT * LN2_H * S.yh + 2.0f, (float)(BINS - 1));  // rounding moves a token by less than a bin
     } else if (by_p) {
-        // The weight of a bin is that of its start times a sum of factors in (e^(-1/32), 1], each to 2^-17 (a CTA
-        // has at most 2^15 tokens).
+        // The weight of a bin is that of its start times a sum of factors in (e^(-1/32), 1], counted in
+        // steps that let all of the CTA's tokens lie in one bin.
+        const float steps = P.slice < 65536 ? 65536.0f : 8192.0f;
         for (int b = tid; b < BINS; b += THREADS) S.rough[b] = 0;
         __syncthreads();
 #pragma unroll 4
@@ -872,7 +873,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
             const float l = R.at(i), x = R.x(l);
             if (!(l > -INFINITY) || x >= (float)(BINS - 1)) continue;
             const int b = (int)x;
-            atomicAdd(&S.rough[b], (unsigned)fmaf(65536.0f, tc::ex2_approx(((float)b - x) * (LOG2E / PER_NAT)), 0.5f));
+            atomicAdd(&S.rough[b], (unsigned)fmaf(steps, tc::ex2_approx(((float)b - x) * (LOG2E / PER_NAT)), 0.5f));
         }
         meet();
         float one_, two;
@@ -896,9 +897,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
             all += a;
         }
         sum += before;
-        // Sums are off by less than 2^-15 of themselves: x and the bins' starts by 2^-17 (arguments near 46 in 24 bits),
-        // the factors by 2^-17; the tokens 32 nats down, left out, weigh less than 2^-28 in all.
-        const float slack = 1.0f / 16384.0f, least = p * all * (1.0f - slack), most = p * all * (1.0f + slack);
+        // Sums are off by less than 2^-15 of themselves, x and the bins' starts (arguments near 46 in 24 bits) by 2^-17, and by
+        // half a step a factor; the tokens 32 nats down, left out, weigh less than 2^-28 in all.
+        const float slack = 1.0f / 16384.0f + 1.0f / steps, least = p * all * (1.0f - slack), most = p * all * (1.0f + slack);
         if (sum >= least) atomicMin(&S.pick_bin, sum - two >= least ? 2 * tid : 2 * tid + 1);
         if (sum >= most) atomicMin(&S.pick_to, sum - two >= most ? 2 * tid : 2 * tid + 1);
         __syncthreads();

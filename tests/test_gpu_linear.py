@@ -192,3 +192,25 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         for _, y in graphs:
             assert torch.equal(y, want.flip(0))
+
+
+@pytest.mark.parametrize("M,N,K,out", [(64, 7168, 16384, BF16), (16, 1024, 16384, F32), (700, 4096, 8192, BF16), (300, 8000, 8192, F32)])
+def test_waits_that_run_out_are_reported(M, N, K, out):
+    """Clusters that share a tile and the persistent kernel, summed in parts or not: with a limit of 64 cycles on their waits
+    they give up, drain and leave; the device reports it, and the next call gives the same bits as before."""
+    from sparse_latent_attention_indexer_gb300 import _abi
+
+    x, w, b, _ = make(M, N, K, BF16, bias=True)
+    want = dsa.dsa_linear(x, w, bias=b, dtype=out)
+    torch.cuda.synchronize()
+    assert dsa.dsa_check_device_error()[0] == _abi.DSA_OK
+    try:
+        dsa.dsa_set_wait_limit(64)
+        dsa.dsa_linear(x, w, bias=b, dtype=out)
+        status, site = dsa.dsa_check_device_error()
+    finally:
+        dsa.dsa_set_wait_limit(0)
+    # a sum in parts waits for eight slabs at a time, which may be there within the hardware's own patience
+    assert (status == _abi.DSA_ERR_TIMEOUT and 61 <= site <= 66) or (out == F32 and status == _abi.DSA_OK)
+    assert torch.equal(dsa.dsa_linear(x, w, bias=b, dtype=out), want)
+    assert dsa.dsa_check_device_error()[0] == _abi.DSA_OK

@@ -229,3 +229,13 @@ def test_large_batches(n, V, dt):
         assert (int(token[i]), int(kept[i])) == want[::2], f"row {i}"
         if want[1] > -INF:
             assert abs(float(logprob[i]) - want[1]) <= 8 * 2.0 ** -24 * (abs(want[1]) + 2.0 ** -20)
+
+
+def test_large_batches_of_equal_logits():
+    """Long rows whose every token has the same weight: nothing that counts them may run over."""
+    n, V = 320, 262144
+    x = torch.full((n, V), -2.5, dtype=BF16, device="cuda")
+    p = [0.25, 0.5, 0.75, 0.125] * (n // 4)
+    token, logprob, kept = dsa.dsa_sample(x, on([0.5] * n), top_p=on(p), want_kept=True)
+    assert kept.tolist() == [int(V * v) for v in p] and token.tolist() == [int(V * v) // 2 for v in p]
+    assert torch.all((logprob.cpu() + torch.tensor([math.log(V * v) for v in p])).abs() < 1e-5)
