@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(256) linear_layout_kernel(const __grid_constan
 
 // ---------------------------------------------------------------------------
 // Few tokens whose rows the TMA does not take (off 16 bytes, fp32): a pass over W to lay it out would cost several times what
-// the product does, so a warp takes four features and every token and reads W as it is, V values at once.  SPLIT: the CTA's eight warps share K.  Bound by HBM for a token or two, then by the FMA pipes.
+// the product does, so a warp takes four features and up to 16 tokens (more: more CTAs, W from L2) and reads W as it is, V values at once.  SPLIT: the CTA's eight warps share K.  Bound by HBM for a token or two, then by the FMA pipes.
 // ---------------------------------------------------------------------------
 constexpr int FEW = 16;
 
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_
     __shared__ float sums[8][4 * MT];
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int f0 = SPLIT ? (int)blockIdx.x * 4 : ((int)blockIdx.x * 8 + warp) * 4;
+    const int f0 = SPLIT ? (int)blockIdx.x * 4 : ((int)blockIdx.x * 8 + warp) * 4, m0 = (int)blockIdx.y * MT;
     const int per = SPLIT ? ((K + 7) / 8 + 32 * V - 1) / (32 * V) * (32 * V) : K;
     const int k0 = min((int64_t)K, SPLIT ? (int64_t)warp * per : 0), k1 = (int)min((int64_t)K, (int64_t)k0 + per);
     float acc[4][MT];
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 float xv[V];
-                read<T, V>(x + m * ld_x + k + h * 32 * V, m < M && k + h * 32 * V < k1, xv);
+                read<T, V>(x + (int64_t)(m0 + m) * ld_x + k + h * 32 * V, m0 + m < M && k + h * 32 * V < k1, xv);
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_
     __syncthreads();
     const int count = SPLIT ? 4 * MT : 8 * 4 * MT;
     for (int i = threadIdx.x; i < count; i += 256) {
-        const int wi = i / (4 * MT), at = i % (4 * MT), m = at / 4;
+        const int wi = i / (4 * MT), at = i % (4 * MT), m = m0 + at / 4;
         const int f = SPLIT ? f0 + at % 4 : ((int)blockIdx.x * 8 + wi) * 4 + at % 4;
         if (m >= M || f >= N) continue;
         float v = sums[wi][at];
@@ -621,9 +621,10 @@ template <typename T, int MT, int V>
 cudaError_t launch_few(const T *x, int64_t ld_x, const T *W, int64_t ld_w, int M, int N, int K, const Epilogue &E,
                        cudaStream_t s) {
     // 32 features a CTA once that gives every SM two
-    const bool split = N < 64 * device_sm_count();
-    return split ? launch_pdl(linear_few_kernel<T, MT, V, true>, dim3((N + 3) / 4), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E)
-                 : launch_pdl(linear_few_kernel<T, MT, V, false>, dim3((N + 31) / 32), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E);
+    const int groups = (M + MT - 1) / MT;
+    const bool split = (int64_t)N * groups < 64 * device_sm_count();
+    return split ? launch_pdl(linear_few_kernel<T, MT, V, true>, dim3((N + 3) / 4, groups), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E)
+                 : launch_pdl(linear_few_kernel<T, MT, V, false>, dim3((N + 31) / 32, groups), dim3(256), 0, s, x, ld_x, W, ld_w, M, N, K, E);
 }
 template <typename T, int V>
 cudaError_t launch_few(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int M, int N, int K, const Epilogue &E,
@@ -655,8 +656,10 @@ Plan plan(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int dtype, i
     p.lay_x = dtype == DSA_F32 || !on16(x, ld_x, M, K);
     p.lay_w = dtype == DSA_F32 || !on16(W, ld_w, N, K);
     // 7168 to 7168, this way and laid out: fp32 1 token 34 us, 16 tokens 131 and 225, 32 tokens 349 and 232;
-    // bf16 off 16 bytes 1 token 26, 16 tokens 169 and 70
-    p.few = p.lay_w && M <= (dtype == DSA_F32 ? FEW : 4);
+    // bf16 off 16 bytes 1 token 26, 16 tokens 169 and 70.  Little work is worth no second launch: 64 tokens, 1536 to 260 in
+    // fp32, 8.3 and 12.8; 500 of them 69 and 17.5; 30 tokens, 511 to 300 in bf16, 4.7 and 6.3; 100 of them 9.4 and 6.3
+    p.few = p.lay_w && (M <= (dtype == DSA_F32 ? FEW : 4) ||
+                        (M <= 64 && (double)M * N * K <= (dtype == DSA_F32 ? 3e7 : 6e6)));
     p.cols = up(K, p.planes == 3 ? 64 : 8);
     p.ld = p.cols * p.planes;
     p.chunk = N;

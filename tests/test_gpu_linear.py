@@ -38,7 +38,7 @@ def make(M, N, K, dt, seed=0, bias=False, res=None):
 
 SIZES = [(1, 1, 1), (1, 128, 64), (1, 300, 8), (3, 129, 65), (15, 64, 1000), (16, 127, 200), (17, 1000, 7), (31, 260, 512),
          (33, 8, 2048), (64, 768, 4096), (100, 5, 63), (255, 257, 72), (256, 128, 640), (257, 131, 129), (300, 1024, 96),
-         (513, 40, 2), (1000, 136, 264)]
+         (513, 40, 2), (1000, 136, 264), (60, 1000, 1001), (5, 2500, 2999), (20, 2000, 1999)]
 
 
 @pytest.mark.parametrize("out", [BF16, F32])
@@ -53,8 +53,10 @@ def test_sizes(M, N, K, dt, out):
     kernels = dsa.last_kernels()
     if dt == BF16 and K % 8 == 0:
         assert kernels == {"linear"}
-    elif M <= (16 if dt == F32 else 4) and (dt == F32 or N > 1):
+    elif (dt == F32 or N > 1) and (M <= (16 if dt == F32 else 4) or (M <= 64 and M * N * K <= (3e7 if dt == F32 else 6e6))):
         assert kernels == {"linear_simt"}
+    elif N > 1:
+        assert kernels == {"linear", "linear_layout"}
 
 
 @pytest.mark.parametrize("act", ACTS)

@@ -26,8 +26,8 @@ def linear(**k):
     (dict(dtype=2), NOT), (dict(y_dtype=2), NOT), (dict(act=5), NOT), (dict(act=-1), NOT), (dict(ld_y=31), BAD),
     (dict(y=A), BAD), (dict(y=B), BAD), (dict(res=C, ld_r=64), BAD), (dict(ld_x=-64), BAD), (dict(ld_w=-1), BAD),
     (dict(M=2 ** 31 - 1), NOT), (dict(N=2 ** 31 - 1), NOT), (dict(K=2 ** 31 - 1), NOT), (dict(dtype=0, K=400000000), NOT),
-    (dict(M=40, ld_x=65), WORKSPACE), (dict(M=40, W=B + 2), WORKSPACE), (dict(M=40, dtype=0), WORKSPACE),
-    (dict(M=40, dtype=0, ws=D, ws_bytes=40 * 384 + 32 * 384 - 1), WORKSPACE), (dict(M=40, dtype=0, ws=D + 16, ws_bytes=1 << 30), WORKSPACE),
+    (dict(M=40, ld_x=65), WORKSPACE), (dict(M=70, W=B + 2), WORKSPACE), (dict(M=70, dtype=0), WORKSPACE),
+    (dict(M=70, dtype=0, ws=D, ws_bytes=70 * 384 + 32 * 384 - 1), WORKSPACE), (dict(M=70, dtype=0, ws=D + 16, ws_bytes=1 << 30), WORKSPACE),
     (dict(M=0), 0), (dict(M=0, x=None, W=None, y=None), 0),
 ])
 def test_linear_refusals(k, status):
@@ -38,15 +38,18 @@ def test_linear_refusals(k, status):
 def test_linear_workspace():
     """Nothing where the tensor cores take the rows as they are; a copy of x, of W (a part at a time) and both."""
     size = lambda x, ld_x, W, ld_w, dt, M, N, K: _abi.load().dsa_linear_workspace_size(x, ld_x, W, ld_w, dt, M, N, K)  # noqa: E731
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
     assert size(A, 64, B, 64, 1, 40, 32, 64) == 0
     assert size(A, 64, B, 64, 1, 0, 32, 64) == 0
     assert size(A + 2, 64, B, 64, 1, 40, 32, 64) == 40 * 128
-    assert size(A, 64, B, 65, 1, 40, 32, 64) == 32 * 128
-    assert size(A, 64, B, 65, 1, 4, 32, 64) == 0 and size(A, 64, B, 65, 0, 16, 32, 64) == 0  # few tokens read W as it is
-    assert size(A, 64, B, 65, 1, 5, 32, 64) == 32 * 128 and size(A, 64, B, 64, 0, 17, 32, 64) == (17 * 384 + 255) // 256 * 256 + 32 * 384
-    assert size(A, 33, B, 33, 1, 40, 32, 33) == 40 * 80 // 256 * 256 + (256 if 40 * 80 % 256 else 0) + 32 * 80
-    assert size(A, 64, B, 64, 0, 40, 32, 64) == (40 + 32) * 384
-    assert size(A, 64, B, 64, 0, 40, 1 << 20, 64) < (1 << 20) * 384  # not all of W at once
+    assert size(A, 64, B, 65, 1, 70, 32, 64) == 32 * 128
+    assert size(A, 33, B, 33, 1, 70, 32, 33) == up(70 * 80) + up(32 * 80)
+    assert size(A, 64, B, 64, 0, 70, 32, 64) == up(70 * 384) + 32 * 384
+    # few tokens, or little work, read W as it is
+    assert size(A, 9999, B, 9999, 1, 4, 9999, 9999) == 0 and size(A, 9999, B, 9999, 1, 5, 9999, 9999) > 0
+    assert size(A, 9999, B, 9999, 0, 16, 9999, 9999) == 0 and size(A, 9999, B, 9999, 0, 17, 9999, 9999) > 0
+    assert size(A, 64, B, 65, 1, 64, 32, 64) == 0 and size(A, 64, B, 64, 0, 64, 32, 64) == 0
+    assert size(A, 64, B, 64, 0, 70, 1 << 20, 64) < (1 << 20) * 384  # not all of W at once
     assert size(A, 64, B, 64, 2, 40, 32, 64) == 0 and size(A, 64, B, 64, 1, 40, 0, 64) == 0
 
 
