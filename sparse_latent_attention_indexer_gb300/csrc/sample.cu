@@ -246,6 +246,19 @@ struct Row {
     __device__ __forceinline__ int bin(float l) const { return (int)fminf(x(l), (float)(BINS - 1)); }
 };
 
+// Sum of v over the threads up to this one, and over all.
+__device__ __forceinline__ u64 block_scan(Shared &S, u64 v, u64 &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    v = warp_scan(v, lane);
+    __syncthreads();
+    if (lane == 31) S.warp_sum[warp] = v;
+    __syncthreads();
+    const u64 upto = warp_scan(lane < WARPS ? S.warp_sum[lane] : 0, lane);
+    const u64 before = __shfl_sync(0xffffffffu, upto, max(0, warp - 1));
+    all = __shfl_sync(0xffffffffu, upto, 31);
+    return (warp > 0 ? before : 0) + v;
+}
+
 // A bin of a histogram: its number, what lies before it, and the whole.
 struct Pick {
     int bin;
@@ -256,21 +269,13 @@ struct Pick {
 // SHARE the share p of the whole.  Every thread of every CTA gets the same answer; no such bin (bin -1): all < want.
 template <bool SHARE>
 __device__ Pick pick_bin(int share, Shared &S, const u64 *hist, u64 base, u64 want, float p) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     meet();
     u64 one, two;
     merge(hist, share, one, two);
-    u64 sum = warp_scan(one + two, lane);
-    if (lane == 31) S.warp_sum[warp] = sum;
     if (tid == 0) S.pick_bin = -1;
-    __syncthreads();
-    u64 before = base, all = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) before += S.warp_sum[w];
-        all += S.warp_sum[w];
-    }
-    sum += before;
+    u64 all;
+    const u64 sum = base + block_scan(S, one + two, all);
     const u64 target = SHARE ? max(part_of(p, all, true), 1ull) : want;
     if (sum >= target && sum - one - two < target) {
         const bool second = sum - two < target;
@@ -364,23 +369,6 @@ __device__ u64 refine(const Part &R, Shared &S, u64 bound, Pick at, u64 target, 
         }
         at = pick_bin<false>(R.share, S, hist, at.base, target, 0.0f);
     }
-}
-
-// Sum of v over the threads up to this one, and over all.
-__device__ __forceinline__ u64 block_scan(Shared &S, u64 v, u64 &all) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    v = warp_scan(v, lane);
-    __syncthreads();
-    if (lane == 31) S.warp_sum[warp] = v;
-    __syncthreads();
-    u64 before = 0;
-    all = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) before += S.warp_sum[w];
-        all += S.warp_sum[w];
-    }
-    return before + v;
 }
 
 __device__ __forceinline__ float random_of(const SampleParams &P, int64_t row) {
