@@ -467,78 +467,91 @@ struct Layout {
     int rows[2], K, cols;     // cols: of a plane, K up to a multiple of 8 or 64
 };
 
-// A warp takes 256 values of a row, a lane eight.
+// Eight fp32 values as three planes.
+__device__ __forceinline__ void split8(float (&v)[8], __nv_bfloat16 *d, int plane) {
+    __align__(16) __nv_bfloat16 t[3][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const bool finite = fabsf(v[e]) < INFINITY;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            float h = __bfloat162float(__float2bfloat16_rn(v[e]));
+            if (finite && !(fabsf(h) < INFINITY)) h = copysignf(3.38953139e38f, v[e]);
+            t[p][e] = __float2bfloat16_rn(h);
+            v[e] = finite ? v[e] - h : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) *(uint4 *)(d + (int64_t)p * plane) = *(const uint4 *)t[p];
+}
+
+// A warp takes CHUNKS times 256 values of a row, a lane eight of each; all loads before the first use.
 template <bool F32>
 __global__ void __launch_bounds__(256) linear_layout_kernel(const __grid_constant__ Layout L) {
+    constexpr int CHUNKS = F32 ? 1 : 4;
     pdl_wait();
-    const int lane = threadIdx.x & 31, parts = (L.cols + 255) / 256;
+    const int lane = threadIdx.x & 31, parts = (L.cols + CHUNKS * 256 - 1) / (CHUNKS * 256);
     const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     int64_t r = i / parts;
-    const int k = (int)(i - r * parts) * 256 + lane * 8;
+    const int k0 = (int)(i - r * parts) * (CHUNKS * 256) + lane * 8;
     const int which = r >= L.rows[0];
     if (which) r -= L.rows[0];
     if (r >= L.rows[which]) return;  // the whole warp
-    __nv_bfloat16 *d = L.dst[which] + r * L.ld_dst + k;
-    if (F32) {
-        if (k >= L.cols) return;
-        const float *s = (const float *)L.src[which] + r * L.ld[which] + k;
+    __nv_bfloat16 *d = L.dst[which] + r * L.ld_dst + k0;
+    if constexpr (F32) {
+        if (k0 >= L.cols) return;
+        const float *s = (const float *)L.src[which] + r * L.ld[which] + k0;
         float v[8];
-        if (k + 8 <= L.K && (uintptr_t)s % 16 == 0) {
-            *(float4 *)v = *(const float4 *)s;
-            *(float4 *)(v + 4) = *((const float4 *)s + 1);
+        if (k0 + 8 <= L.K && (uintptr_t)s % 16 == 0) {
+            const float4 a = *(const float4 *)s, b = *((const float4 *)s + 1);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = k + e < L.K ? s[e] : 0.0f;
+            for (int e = 0; e < 8; ++e) v[e] = k0 + e < L.K ? s[e] : 0.0f;
         }
-        __align__(16) __nv_bfloat16 t[3][8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const bool finite = fabsf(v[e]) < INFINITY;
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                float h = __bfloat162float(__float2bfloat16_rn(v[e]));
-                if (finite && !(fabsf(h) < INFINITY)) h = copysignf(3.38953139e38f, v[e]);
-                t[p][e] = __float2bfloat16_rn(h);
-                v[e] = finite ? v[e] - h : 0.0f;
-            }
-        }
-#pragma unroll
-        for (int p = 0; p < 3; ++p) *(uint4 *)(d + (int64_t)p * L.cols) = *(const uint4 *)t[p];
+        split8(v, d, L.cols);
     } else {
         // Whole 16 bytes around the lane's eight values: its own and, where they go on there, the next lane's.  They hold
         // at least one value of the row, so they lie in memory that is there.
-        const uintptr_t at = (uintptr_t)((const uint16_t *)L.src[which] + r * L.ld[which] + k), end = at + 2 * (int64_t)(L.K - k);
-        const uintptr_t from = at & ~(uintptr_t)15;
+        const uintptr_t at = (uintptr_t)((const uint16_t *)L.src[which] + r * L.ld[which] + k0);
         const int off = (int)(at & 15);  // the same in every lane
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (k < L.K) a = *(const uint4 *)from;
-        b.x = __shfl_down_sync(0xffffffffu, a.x, 1);
-        b.y = __shfl_down_sync(0xffffffffu, a.y, 1);
-        b.z = __shfl_down_sync(0xffffffffu, a.z, 1);
-        b.w = __shfl_down_sync(0xffffffffu, a.w, 1);
-        if (off && k < L.K && (lane == 31 || k + 8 >= L.K)) {
-            if (from + 16 < end) b = *(const uint4 *)(from + 16);
-        }
-        if (k >= L.cols) return;
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint32_t o[4];
+        uint4 a[CHUNKS], b[CHUNKS];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // two bytes at a time, off / 4 words and perhaps half a word on
-            uint32_t lo = w[e], hi = w[e + 1];
-#pragma unroll
-            for (int j = 1; j < 4; ++j)
-                if (off / 4 == j) {
-                    lo = w[e + j];
-                    hi = e + j + 1 < 8 ? w[e + j + 1] : 0;
-                }
-            o[e] = off & 2 ? __funnelshift_r(lo, hi, 16) : lo;
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int k = k0 + c * 256;
+            const uintptr_t from = (at & ~(uintptr_t)15) + c * 512, end = at + 2 * (int64_t)(L.K - k0);
+            a[c] = b[c] = make_uint4(0, 0, 0, 0);
+            if (k < L.K) a[c] = *(const uint4 *)from;
+            if (off && k < L.K && (lane == 31 || k + 8 >= L.K) && from + 16 < end) b[c] = *(const uint4 *)(from + 16);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // nothing behind the row's end
-            if (k + 2 * e >= L.K) o[e] = 0;
-            else if (k + 2 * e + 1 >= L.K) o[e] &= 0xffffu;
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int k = k0 + c * 256;
+            const uint4 n = make_uint4(__shfl_down_sync(0xffffffffu, a[c].x, 1), __shfl_down_sync(0xffffffffu, a[c].y, 1),
+                                       __shfl_down_sync(0xffffffffu, a[c].z, 1), __shfl_down_sync(0xffffffffu, a[c].w, 1));
+            if (!(lane == 31 || k + 8 >= L.K)) b[c] = n;
+            if (k >= L.cols) continue;
+            const uint32_t w[8] = {a[c].x, a[c].y, a[c].z, a[c].w, b[c].x, b[c].y, b[c].z, b[c].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // two bytes at a time, off / 4 words and perhaps half a word on
+                uint32_t lo = w[e], hi = w[e + 1];
+#pragma unroll
+                for (int j = 1; j < 4; ++j)
+                    if (off / 4 == j) {
+                        lo = w[e + j];
+                        hi = e + j + 1 < 8 ? w[e + j + 1] : 0;
+                    }
+                o[e] = off & 2 ? __funnelshift_r(lo, hi, 16) : lo;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // nothing behind the row's end
+                if (k + 2 * e >= L.K) o[e] = 0;
+                else if (k + 2 * e + 1 >= L.K) o[e] &= 0xffffu;
+            }
+            *(uint4 *)(d + c * 256) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *(uint4 *)d = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -676,7 +689,8 @@ cudaError_t lay_out(Layout &L, int dtype, const Plan &p, int K, cudaStream_t s) 
     L.K = K;
     L.cols = (int)p.cols;
     L.ld_dst = p.ld;
-    const int64_t n = (((int64_t)L.rows[0] + L.rows[1]) * ((p.cols + 255) / 256) + 7) / 8;
+    const int of = dtype == DSA_F32 ? 256 : 1024;  // values of a row that a warp takes
+    const int64_t n = (((int64_t)L.rows[0] + L.rows[1]) * ((p.cols + of - 1) / of) + 7) / 8;
     if (n == 0) return cudaSuccess;
     if (n > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const cudaError_t e = dtype == DSA_F32 ? launch_pdl(linear_layout_kernel<true>, dim3((unsigned)n), dim3(256), 0, s, L)
