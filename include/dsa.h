@@ -585,9 +585,10 @@ int dsa_head_norm_rope(const dsa_heads *q, const dsa_heads *k, int x_dtype, int 
  * Any sizes and strides of whole elements.  bf16 rows that start on 16 bytes go to
  * the tensor cores as they are; others, and fp32 values (as three bf16 terms each,
  * six products of them: the error of an fp32 sum), are laid out in the workspace
- * first.  In fp32 a product with an infinity is NaN, and terms of values below
- * 2^-100 may be lost.
- * The workspace size depends on all that it is given here (0 where none is needed).
+ * first, but for few tokens or little work.  In fp32 a product with an infinity may
+ * be NaN, and terms of values below 2^-100 may be lost.
+ * The workspace size depends on all that it is given here (0 where none is needed);
+ * calls that overlap need a workspace each.
  * Errors: DSA_ERR_INVALID_ARG (null pointer, sizes below M >= 0, N, K >= 1, an
  * address off its element, rows of an output that overlap), DSA_ERR_UNSUPPORTED
  * (dtype, act, M, N or K not below 2^31 - 1024), DSA_ERR_WORKSPACE, DSA_ERR_CUDA. */

@@ -7,7 +7,8 @@
 // float32 compute; nnterp deepseek_v32 printout).  y comes from h' before h' is rounded, so
 // the stream's type costs the next block nothing.
 //
-// Bound by HBM: every value is read once and written once.  A row lies in the registers of
+// Bound by HBM (8192 rows of 7168 in bf16: 74 us, 0.94 of the measured copy rate; normed twice and gated 98, 0.88; in rows
+// off 16 bytes by latency, 3001 of 2049: 21, 0.51): every value is read once and written once.  A row lies in the registers of
 // one CTA (of one warp up to 1024 values) between its loads, which are all issued first, and
 // its stores; a thread stores where it has loaded, so h' may be h and y may be u.  A norm is one sum over the row (two for layer:
 // the mean, then the squares of what is left, so that a large mean costs no digits).
