@@ -18,11 +18,14 @@
 // The tensor cores cut off what does not fit a running sum of 24 bits, step by step: over 448 steps
 // of 16 products (K = 7168) an fp32 result was off by 7.9e-6 of the whole, ten times what fp32
 // arithmetic loses.  Where y is fp32 (EXACT) the epilogue takes the sum over after every 8 slabs
-// (32 steps) and adds these parts to nearest in its registers.
+// (32 steps; fp32 layers: 4) and adds these parts to nearest in its registers.
 //
-// fp32 layers run on the same kernel: a value is the sum of three bf16 terms of 8 bits each, and
-// of the nine products of terms the six above 2^-24 of the whole are added, smallest first.
-// Rows that do not start on 16 bytes are laid out anew first (linear_layout_kernel).
+// fp32 layers run on the same kernel (PLANES = 3): a value is the sum of three bf16 terms of 8 bits
+// each, and of the nine products of terms the six above 2^-24 of the whole are added.  A stage holds
+// all planes of a slab, x's one behind the other, so that W's plane p meets x's planes 0 .. 2 - p in
+// one MMA of as many times the tokens: W is read three times instead of six (1000 tokens, 2048
+// to 5000: 189 -> 122 us).  Products of one order share an accumulator; the three are added last.
+// Rows that do not start on 16 bytes, and fp32 ones, are laid out anew first (linear_layout_kernel).
 //
 // Bound by HBM with few tokens (17 tokens, 7168 to 131,072, fp32 out: 266 to 272 us, 1.02 of the measured copy
 // rate; 64 tokens, 16384 to 7168: 43.7 us, 0.80, the rest being the start and the end of a tile), by shared memory with
@@ -39,14 +42,15 @@ __device__ int g_linear_error = 0;
 namespace {
 
 constexpr int BF = 128, MAX_BT = 256;             // features, tokens of a tile
+// Tokens of a tile: the MMA's N is that or, with three planes, three times that; less where exact sums take registers.
+constexpr int max_bt(bool exact, int planes) { return planes == 3 ? 80 : exact ? 128 : MAX_BT; }
 constexpr int W_SLAB = BF * 128;                  // 16 KB: 128 rows x 64 bf16
 constexpr int MAX_STAGES = 12;
 constexpr int NUM_THREADS = 384;                  // 0 TMA, 1 MMA, 2 TMEM owner, 3 idle, 4-11 epilogue
 constexpr int EPI_WARP0 = 4, EPI_THREADS = 256;
 constexpr int TURN = 2 * 32 * BF * 4;             // 32 tokens x 128 features in fp32 for each half of the epilogue
 constexpr int SMEM_MAX = 232448;
-constexpr int MAX_EXACT = 128;                     // tokens of a tile whose sums are exact
-constexpr int CHAIN = 8;                          // slabs of an exact sum's parts
+constexpr int chain_of(int planes) { return planes == 3 ? 4 : 8; }  // slabs of an exact sum's parts
 constexpr int MAX_SHARE = 8;                      // CTAs that share a tile's K
 constexpr int GROUP_T = 8;                        // token tiles that share a panel of W in L2
 
@@ -61,22 +65,35 @@ struct LinearParams {
     Epilogue e;
     int M, N;
     int bt, tt, tiles;    // tokens of a tile, token tiles, tiles
-    int slabs, total;     // slabs of K; of all products of planes
-    int plane;            // columns from one plane to the next; 0: one plane
+    int total;            // slabs (64 columns) of K
     int stages, stage_bytes;
     int share;            // CTAs that share a tile's K (SPLIT)
     int acc_cols, tmem_cols;  // columns from one accumulator to the next; of tensor memory
-    int chain;            // slabs that are added up in tensor memory (all, or CHAIN with EXACT)
+    int chain;            // slabs that are added up in tensor memory (all, or with EXACT a part)
     long long wait_limit;
 };
 
-__device__ __forceinline__ float activate(float v, int act) {
+template <int ACT>
+__device__ __forceinline__ float activation(float v) {
+    if (ACT == DSA_ACT_RELU) return v < 0.0f ? 0.0f : v;  // a NaN stays
+    if (ACT == DSA_ACT_SILU) return v / (1.0f + expf(-v));
+    if (ACT == DSA_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678f));
+    if (ACT == DSA_ACT_GELU_TANH) return 0.5f * v * (1.0f + tanhf(0.79788456f * fmaf(0.044715f * v * v, v, v)));
+    return v;
+}
+template <int ACT, int N>
+__device__ __forceinline__ void activation(float (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = activation<ACT>(v[j]);
+}
+// One branch for all values: a branch for each made so much code that a tile's end waited 7 us for it.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
     switch (act) {
-        case DSA_ACT_RELU: return v < 0.0f ? 0.0f : v;  // a NaN stays
-        case DSA_ACT_SILU: return v / (1.0f + expf(-v));
-        case DSA_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678f));
-        case DSA_ACT_GELU_TANH: return 0.5f * v * (1.0f + tanhf(0.79788456f * fmaf(0.044715f * v * v, v, v)));
-        default: return v;
+        case DSA_ACT_RELU: return activation<DSA_ACT_RELU>(v);
+        case DSA_ACT_SILU: return activation<DSA_ACT_SILU>(v);
+        case DSA_ACT_GELU: return activation<DSA_ACT_GELU>(v);
+        case DSA_ACT_GELU_TANH: return activation<DSA_ACT_GELU_TANH>(v);
     }
 }
 
@@ -143,13 +160,22 @@ __device__ __forceinline__ void expect_if(uint32_t issue, uint64_t *bar, uint32_
         "r"(bytes), "r"(issue)
         : "memory");
 }
+template <int PLANES>  // all planes of the rows at once
 __device__ __forceinline__ void load_if(uint32_t issue, void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-        "[%2];\n\t}" ::"r"(tc::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(issue)
-        : "memory");
+    if constexpr (PLANES == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+            "[%2];\n\t}" ::"r"(tc::smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(issue)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+            "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+            "[%2];\n\t}" ::"r"(tc::smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(0), "r"(issue)
+            : "memory");
 }
 __device__ __forceinline__ void commit_if(uint32_t issue, uint64_t *bar) {
     asm volatile(
@@ -183,19 +209,42 @@ __device__ __forceinline__ void tile_of(const LinearParams &P, int u, int &m0, i
     f0 = (r / gt) * BF;
 }
 
-// The planes of W and x whose product slab i belongs to, smallest products first, and its column.
-__device__ __forceinline__ void slab_at(const LinearParams &P, int i, int &xw, int &xx) {
-    if (P.plane == 0) {
-        xw = xx = i * 64;
-        return;
+// Eight fp32 values as three planes of bf16 terms, each the nearest to what the terms before it leave (above the largest bf16
+// number that and what is left; infinities and NaN in the first plane alone).
+constexpr float BF16_MAX = 3.38953139e38f;
+__device__ __forceinline__ void split_eight(const float (&v)[8], uint32_t (&o)[3][4]) {
+    bool large = false;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        float a = v[e], b = v[e + 1];
+        large |= !(fabsf(a) <= BF16_MAX) || !(fabsf(b) <= BF16_MAX);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            o[t][e / 2] = *(const uint32_t *)&h;
+            a -= __uint_as_float(o[t][e / 2] << 16);
+            b -= __uint_as_float(o[t][e / 2] & 0xffff0000u);
+        }
     }
-    const int q = i / P.slabs, k = (i - q * P.slabs) * 64;
-    xw = ((0x001102 >> (4 * q)) & 15) * P.plane + k;  // (2, 0) (0, 2) (1, 1) (1, 0) (0, 1) (0, 0), a digit each
-    xx = ((0x010120 >> (4 * q)) & 15) * P.plane + k;
+    if (large) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float a = v[e];
+            if (fabsf(a) <= BF16_MAX) continue;
+            const bool finite = fabsf(a) < INFINITY;
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+                const float h = t == 0 && finite ? copysignf(BF16_MAX, a) : __bfloat162float(__float2bfloat16_rn(a));
+                const uint32_t bits = __float_as_uint(h) >> 16;
+                o[t][e / 2] = e & 1 ? (o[t][e / 2] & 0xffffu) | bits << 16 : (o[t][e / 2] & 0xffff0000u) | bits;
+                a = finite ? a - h : 0.0f;
+            }
+        }
+    }
 }
 
-template <bool SPLIT, bool EXACT>
-__global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT ? 2 : 1)
+template <bool SPLIT, bool EXACT, int PLANES>
+__global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && PLANES == 1 ? 2 : 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                   const __grid_constant__ LinearParams P) {
     extern __shared__ uint8_t smem_raw[];
@@ -217,11 +266,9 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT ? 2 : 1)
     // One slab's loads, by the lane of `issue`.
     const auto load = [&](uint32_t issue, int st, int ks, int m0, int f0) {
         uint8_t *sw = ring + st * P.stage_bytes;
-        int xw, xx;
-        slab_at(P, ks, xw, xx);
         expect_if(issue, &full[st], P.stage_bytes);
-        load_if(issue, sw, &tm_w, &full[st], xw, f0);
-        load_if(issue, sw + W_SLAB, &tm_x, &full[st], xx, m0);
+        load_if<PLANES>(issue, sw, &tm_w, &full[st], ks * 64, f0);
+        load_if<PLANES>(issue, sw + PLANES * W_SLAB, &tm_x, &full[st], ks * 64, m0);
     };
     // The producer's first loads go out before the CTA has met, while warp 2 waits for tensor memory.
     const int ahead_slabs = mine > 0 ? min(s1 - s0, P.stages) : 0;
@@ -277,7 +324,9 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT ? 2 : 1)
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
         const uint32_t issue = tc::elect_one();
-        const uint32_t idesc = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, BF, P.bt, 0, 0);
+        const uint32_t idesc = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, BF, PLANES * P.bt, 0, 0);
+        const uint32_t idesc2 = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, BF, 2 * P.bt, 0, 0);
+        const uint32_t idesc1 = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, BF, P.bt, 0, 0);
         const uint64_t first = tc::smem_desc(tc::smem_u32(ring), 16, 1024);
         int st = 0, round = 0, issued = 0, n = 0;
         bool ok = true;
@@ -290,10 +339,21 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT ? 2 : 1)
                     if (!(ok = wait_warp(&full[st], round & 1, abort_flag, err, 64, P.wait_limit))) break;
                     tc::tc_fence_after();
                     // addresses in a descriptor count 16 bytes and stay below its 14 bits
-                    const uint64_t wd = first + (uint32_t)(st * P.stage_bytes / 16), xd = wd + W_SLAB / 16;
+                    const uint64_t wd = first + (uint32_t)(st * P.stage_bytes / 16), xd = wd + PLANES * W_SLAB / 16;
+                    if (PLANES == 1) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_f16_if(issue, d, wd + kk * 2, xd + kk * 2, idesc, ks != k0 || kk != 0);
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_f16_if(issue, d, wd + kk * 2, xd + kk * 2, idesc, ks != k0 || kk != 0);
+                    } else {
+                        // W's plane p times x's planes 0 .. 2 - p, which lie one behind the other: one MMA of as many times the
+                        // tokens, into the accumulators of the orders p .. 2
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                            for (int p = 0; p < PLANES; ++p)
+                                tc::mma_f16_if(issue, d + p * P.bt, wd + p * (W_SLAB / 16) + kk * 2, xd + kk * 2,
+                                               p == 0 ? idesc : p == 1 ? idesc2 : idesc1, ks != k0 || kk != 0 || p != 0);
+                    }
                     commit_if(issue, &empty[st]);
                     ++issued;
                     if (++st == P.stages) st = 0, ++round;
@@ -335,7 +395,8 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT ? 2 : 1)
                     for (int j = 0; j < 8; ++j)
                         if (row0 + j < P.M) residual4(P.e, row0 + j, f4, r[j]);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = activate(v[j] + b, P.e.act);
+                for (int j = 0; j < 32; ++j) v[j] += b;
+                activate(v, P.e.act);
                 bar(2 + g, EPI_THREADS / 2);  // the last chunk has been read
 #pragma unroll
                 for (int j = 0; j < 32; ++j) mine_turn[j * BF + q * 32 + lane] = v[j];
@@ -362,33 +423,53 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT ? 2 : 1)
                                 store1(P.e, row0 + j, f0 + e * 32 + lane, mine_turn[(q * 8 + j) * BF + e * 32 + lane]);
                 }
             };
+            const auto read = [&](int c, float (&v)[32]) {  // tokens c .. c + 31 of the accumulator
+                const uint32_t at = lanes + (n & 1) * P.acc_cols + c;
+                if constexpr (PLANES == 1) {
+                    tc::tmem_ld32(at, v);
+                    tc::tmem_ld_wait();
+                } else {
+                    float u[32];
+                    tc::tmem_ld32(at + 2 * P.bt, u);
+                    tc::tmem_ld32(at + P.bt, v);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) u[e] += v[e];
+                    tc::tmem_ld32(at, v);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] += u[e];
+                }
+            };
             bool ok = true;
             if (EXACT) {
-                float sum[MAX_EXACT / 64][32];
+                constexpr int SUMS = (max_bt(EXACT, PLANES) + 63) / 64;
+                float sum[SUMS][32];
 #pragma unroll
-                for (int j = 0; j < MAX_EXACT / 64; ++j)
+                for (int j = 0; j < SUMS; ++j)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) sum[j][e] = 0.0f;
-                for (int k0 = s0; k0 < s1; k0 += P.chain, ++n) {
+                for (int k0 = s0; ok && k0 < s1; k0 += P.chain) {
+                    // takes the next part over from tensor memory
                     ok = epi_and(tc::mbar_wait(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit));
                     if (!ok) break;
                     tc::tc_fence_after();
 #pragma unroll
-                    for (int j = 0; j < MAX_EXACT / 64; ++j)
+                    for (int j = 0; j < SUMS; ++j)
                         if (j * 64 + g * 32 < tokens) {
                             float v[32];
-                            tc::tmem_ld32(lanes + (n & 1) * P.acc_cols + j * 64 + g * 32, v);
-                            tc::tmem_ld_wait();
+                            read(j * 64 + g * 32, v);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) sum[j][e] += v[e];
                         }
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&tempty[n & 1]);
+                    ++n;
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int j = 0; j < MAX_EXACT / 64; ++j)
+                for (int j = 0; j < SUMS; ++j)
                     if (j * 64 + g * 32 < tokens) put(j * 64 + g * 32, sum[j]);
             } else {
                 ok = epi_and(tc::mbar_wait(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit));
@@ -396,8 +477,7 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT ? 2 : 1)
                 tc::tc_fence_after();
                 for (int c = g * 32; c < tokens; c += 64) {
                     float v[32];
-                    tc::tmem_ld32(lanes + (n & 1) * P.acc_cols + c, v);
-                    tc::tmem_ld_wait();
+                    read(c, v);
                     put(c, v);
                 }
                 // every column of this accumulator has been read
@@ -440,7 +520,8 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT ? 2 : 1)
             if (!live) continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (f + e < P.N) v[e] = activate(v[e] + (P.e.bias ? __ldg(P.e.bias + f + e) : 0.0f), P.e.act);
+                if (f + e < P.N) v[e] += P.e.bias ? __ldg(P.e.bias + f + e) : 0.0f;
+            activate(v, P.e.act);
             if (P.e.vec) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] += r[e];
@@ -461,9 +542,7 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT ? 2 : 1)
 }
 
 // ---------------------------------------------------------------------------
-// Rows laid out for the TMA: bf16 rows copied to rows on 16 bytes; fp32 rows as three planes of
-// bf16 terms, each the nearest to what the terms before it leave (a term that would round to
-// infinity is the largest number instead; infinities and NaN stay in the first plane).
+// Rows laid out for the TMA: bf16 rows copied to rows on 16 bytes; fp32 rows as three planes.
 // ---------------------------------------------------------------------------
 struct Layout {
     const void *src[2];       // x and W (rows 0: neither)
@@ -471,24 +550,6 @@ struct Layout {
     int64_t ld[2], ld_dst;
     int rows[2], K, cols;     // cols: of a plane, K up to a multiple of 8 or 64
 };
-
-// Eight fp32 values as three planes.
-__device__ __forceinline__ void split8(float (&v)[8], __nv_bfloat16 *d, int plane) {
-    __align__(16) __nv_bfloat16 t[3][8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const bool finite = fabsf(v[e]) < INFINITY;
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            float h = __bfloat162float(__float2bfloat16_rn(v[e]));
-            if (finite && !(fabsf(h) < INFINITY)) h = copysignf(3.38953139e38f, v[e]);
-            t[p][e] = __float2bfloat16_rn(h);
-            v[e] = finite ? v[e] - h : 0.0f;
-        }
-    }
-#pragma unroll
-    for (int p = 0; p < 3; ++p) *(uint4 *)(d + (int64_t)p * plane) = *(const uint4 *)t[p];
-}
 
 // A warp takes CHUNKS times 256 values of a row, a lane eight of each; all loads before the first use.
 template <bool F32>
@@ -515,7 +576,10 @@ __global__ void __launch_bounds__(256) linear_layout_kernel(const __grid_constan
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = k0 + e < L.K ? s[e] : 0.0f;
         }
-        split8(v, d, L.cols);
+        uint32_t o[3][4];
+        split_eight(v, o);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *(uint4 *)(d + (int64_t)p * L.cols) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
     } else {
         // Whole 16 bytes around the lane's eight values: its own and, where they go on there, the next lane's.  They hold
         // at least one value of the row, so they lie in memory that is there.
@@ -631,7 +695,9 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const T *x, int64_t ld_
         if (SPLIT)
 #pragma unroll
             for (int j = 1; j < 8; ++j) v += sums[j][at];
-        store1(E, m, f, activate(v + (E.bias ? E.bias[f] : 0.0f), E.act));
+        float o[1] = {v + (E.bias ? E.bias[f] : 0.0f)};
+        activate(o, E.act);
+        store1(E, m, f, o[0]);
     }
 }
 
@@ -656,7 +722,7 @@ cudaError_t launch_few(const void *x, int64_t ld_x, const void *W, int64_t ld_w,
 // Host
 // ---------------------------------------------------------------------------
 inline int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-// Rows that the TMA takes as they are (strides of 0 or below the row's length are laid out).
+// bf16 rows that the TMA takes as they are (strides of 0 or below the row's length are laid out).
 inline bool on16(const void *p, int64_t ld, int rows, int K) {
     return (uintptr_t)p % 16 == 0 && (rows <= 1 || (ld % 8 == 0 && ld >= K && ld < (int64_t(1) << 38)));
 }
@@ -670,23 +736,25 @@ struct Plan {
 };
 Plan plan(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int dtype, int M, int N, int K) {
     Plan p{};
-    p.planes = dtype == DSA_F32 ? 3 : 1;
-    p.lay_x = dtype == DSA_F32 || !on16(x, ld_x, M, K);
-    p.lay_w = dtype == DSA_F32 || !on16(W, ld_w, N, K);
-    // 7168 to 7168, this way and laid out: fp32 1 token 34 us, 16 tokens 131 and 225, 32 tokens 349 and 232;
-    // bf16 off 16 bytes 1 token 26, 16 tokens 169 and 70.  Little work is worth no second launch: 64 tokens, 1536 to 260 in
-    // fp32, 8.3 and 12.8; 500 of them 69 and 17.5; 30 tokens, 511 to 300 in bf16, 4.7 and 6.3; 100 of them 9.4 and 6.3
-    p.few = p.lay_w && (M <= (dtype == DSA_F32 ? FEW : 4) ||
-                        (M <= 64 && (double)M * N * K <= (dtype == DSA_F32 ? 3e7 : 6e6)));
-    p.cols = up(K, p.planes == 3 ? 64 : 8);
-    p.ld = p.cols * p.planes;
+    const bool f32 = dtype == DSA_F32, x16 = !f32 && on16(x, ld_x, M, K), w16 = !f32 && on16(W, ld_w, N, K);
+    // 7168 to 7168, this way and laid out: fp32 4 tokens 38 us and 135, 16 tokens 131 and 137 (1024 to 8192: 47 and 20);
+    // bf16 off 16 bytes 1 token 26, 16 tokens 169 and 70.  Little work is worth no second launch: 8 tokens, 4096 to 1024 in
+    // fp32, 15.2 and 15.4; 64, 1536 to 260, 8.3 and 10.1; 100, 256 to 256, 8.2 and 6.3; 30 tokens, 511 to 300 in bf16, 4.6
+    // and 6.3; 100 of them 9.4 and 6.3
+    p.few = !w16 && (M <= 4 || (M <= 64 && (double)M * N * K <= (f32 ? 3.5e7 : 6e6)));
     p.chunk = N;
-    if (p.lay_w)  // as many features as stay in L2 between the two kernels, but enough to fill the SMs
-        p.chunk = (int)std::min<int64_t>(N, std::max<int64_t>(2048, (64 << 20) / (p.ld * 2) / BF * BF));
-    if (!p.few) {
-        p.x_bytes = p.lay_x ? up((int64_t)M * p.ld * 2, 256) : 0;
-        p.w_bytes = p.lay_w ? up((int64_t)p.chunk * p.ld * 2, 256) : 0;
+    if (p.few) return p;
+    p.planes = f32 ? 3 : 1;
+    p.lay_x = !x16;
+    p.lay_w = !w16;
+    p.cols = up(K, f32 ? 64 : 8);
+    p.ld = p.cols * p.planes;
+    if (p.lay_w) {  // as many features as stay in L2 between the two kernels, but enough to fill the SMs
+        const int64_t most = std::max<int64_t>(2048, (64 << 20) / (p.ld * 2) / BF * BF), parts = (N + most - 1) / most;
+        p.chunk = (int)std::min<int64_t>(N, up((N + parts - 1) / parts, BF));
     }
+    p.x_bytes = p.lay_x ? up((int64_t)M * p.ld * 2, 256) : 0;
+    p.w_bytes = p.lay_w ? up((int64_t)p.chunk * p.ld * 2, 256) : 0;
     return p;
 }
 
@@ -707,7 +775,7 @@ cudaError_t lay_out(Layout &L, int dtype, const Plan &p, int K, cudaStream_t s) 
 // How the product is cut: tokens of a tile, CTAs that share a tile's K, CTAs that an SM holds.  The one of least time by
 // what bounds a slab (64 columns of K), in SM cycles, each measured:
 //   * shared memory: the slab is written once and read by the MMAs (W once, x once), 128 bytes a cycle (256 tokens: 730
-//     cycles, of which the MMAs need 512);
+//     cycles, of which the MMAs need 512); of planes W three times and x's six, 1488 cycles for 80 tokens;
 //   * 350 cycles to hand a slab on and for 16 KB of W from HBM to one SM;
 //   * HBM, 3550 bytes a cycle for all, which W passes once;
 // and what a CTA needs besides: 5000 cycles until its first slab is there and its last result stored, more for the
@@ -717,6 +785,12 @@ cudaError_t lay_out(Layout &L, int dtype, const Plan &p, int K, cudaStream_t s) 
 struct Cut {
     int bt, share, per_sm;
 };
+using Kernel = void (*)(CUtensorMap, CUtensorMap, LinearParams);
+template <int PLANES>
+Kernel kernel_for(bool split, bool exact) {
+    return split ? exact ? linear_kernel<true, true, PLANES> : linear_kernel<true, false, PLANES>
+                 : exact ? linear_kernel<false, true, PLANES> : linear_kernel<false, false, PLANES>;
+}
 
 // Clusters of `share` CTAs that the device holds at once (they lie within one group of SMs each).
 int clusters_at_once(int share, int per_sm, bool exact) {
@@ -733,7 +807,7 @@ int clusters_at_once(int share, int per_sm, bool exact) {
         attr[0].val.clusterDim = {(unsigned)share, 1, 1};
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        auto *kernel = exact ? linear_kernel<true, true> : linear_kernel<true, false>;
+        const Kernel kernel = kernel_for<1>(true, exact);
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
             (void)cudaGetLastError();
@@ -744,17 +818,18 @@ int clusters_at_once(int share, int per_sm, bool exact) {
     return n;
 }
 
-Cut cut(int M, int N, int total, bool exact, int sms) {
-    const int most = exact ? MAX_EXACT : MAX_BT, least_tt = (M + most - 1) / most;
+Cut cut(int M, int N, int total, bool exact, int planes, int sms) {
+    const int most = max_bt(exact, planes), least_tt = (M + most - 1) / most;
     const int64_t ft = ((int64_t)N + BF - 1) / BF;
     Cut best{MAX_BT, 1, 1};
     double least = 1e30;
     for (int tt = least_tt; tt < least_tt + 8; ++tt) {
         const int bt = (int)up((M + tt - 1) / tt, 16);
         const int64_t tiles = (M + bt - 1) / bt * ft;
-        const double smem = 2 * (W_SLAB + 128.0 * bt) / 128, hbm = (double)ft * total * W_SLAB / 3550;
-        for (int share = 1; share <= MAX_SHARE && (share == 1 || total >= 4 * share); ++share)
-            for (int per_sm = 1; per_sm <= (share > 1 && !exact && bt <= 128 ? 2 : 1); ++per_sm) {
+        const double smem = planes == 1 ? 2 * (W_SLAB + 128.0 * bt) / 128 : 768 + 9.0 * bt;
+        const double hbm = (double)ft * total * W_SLAB * planes / 3550;
+        for (int share = 1; share <= MAX_SHARE && (share == 1 || total >= (planes == 1 ? 4 : 2) * share); ++share)
+            for (int per_sm = 1; per_sm <= (share > 1 && !exact && planes == 1 && bt <= 128 ? 2 : 1); ++per_sm) {
                 const int64_t room = share == 1 ? sms : clusters_at_once(share, per_sm, exact), rounds = (tiles + room - 1) / room;
                 const double slabs = (total + share - 1) / share, side = tiles * share > sms ? per_sm : 1;
                 const double work = slabs * std::max(smem * side, 350.0);
@@ -771,44 +846,39 @@ Cut cut(int M, int N, int total, bool exact, int sms) {
     return best;
 }
 
-cudaError_t launch_tiles(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int K, int plane, LinearParams &P,
+cudaError_t launch_tiles(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int K, int64_t cols, int planes, LinearParams &P,
                          cudaStream_t s) {
     const int sms = device_sm_count();
-    P.slabs = (K + 63) / 64;
-    P.total = plane ? 6 * P.slabs : P.slabs;
-    const bool exact = P.e.f32 && P.total > CHAIN;
-    P.chain = exact ? CHAIN : P.total;
-    const Cut c = cut(P.M, P.N, P.total, exact, sms);
+    P.total = (K + 63) / 64;
+    const bool exact = P.e.f32 && P.total > chain_of(planes);
+    P.chain = exact ? chain_of(planes) : P.total;
+    const Cut c = cut(P.M, P.N, P.total, exact, planes, sms);
     P.bt = c.bt;
     P.share = c.share;
     P.tt = (P.M + P.bt - 1) / P.bt;
     const int64_t tiles = (int64_t)P.tt * (((int64_t)P.N + BF - 1) / BF);
     if (tiles > 0x7fffffff / 8) return cudaErrorInvalidConfiguration;
     P.tiles = (int)tiles;
-    P.plane = plane;
-    P.stage_bytes = W_SLAB + P.bt * 128;
+    P.stage_bytes = planes * (W_SLAB + P.bt * 128);
     P.wait_limit = wait_limit_cycles();
     const bool split = P.share > 1;
     P.acc_cols = 32;
-    while (P.acc_cols < P.bt) P.acc_cols *= 2;
+    while (P.acc_cols < (planes - 1) * P.bt + up(P.bt, 32)) P.acc_cols *= 2;
     if (!split) P.acc_cols = MAX_BT;
     P.tmem_cols = split && !exact ? P.acc_cols : 2 * P.acc_cols;
-    P.stages = std::min(MAX_STAGES, (SMEM_MAX / c.per_sm - 2048 - (split ? 0 : TURN)) / P.stage_bytes);
-    const int smem = 1024 + P.stages * P.stage_bytes + (split ? 0 : TURN);
-    CUtensorMap tw, tx;
-    const uint64_t wide = plane ? 3 * (uint64_t)plane : (uint64_t)K;
-    {
-        const uint64_t dims[2] = {wide, (uint64_t)P.N}, strides[1] = {(uint64_t)ld_w * 2};
-        const uint32_t box[2] = {64, BF};
-        if (!make_tmap(&tw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, W, dims, strides, box)) return cudaErrorInvalidValue;
-    }
-    {
-        const uint64_t dims[2] = {wide, (uint64_t)P.M}, strides[1] = {(uint64_t)ld_x * 2};
-        const uint32_t box[2] = {64, (uint32_t)P.bt};
-        if (!make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, dims, strides, box)) return cudaErrorInvalidValue;
-    }
-    auto *kernel = split ? exact ? linear_kernel<true, true> : linear_kernel<true, false>
-                         : exact ? linear_kernel<false, true> : linear_kernel<false, false>;
+    const int turn = split ? 0 : TURN, room = SMEM_MAX / c.per_sm - 2048 - turn;
+    P.stages = std::min(MAX_STAGES, room / P.stage_bytes);
+    const int smem = 1024 + P.stages * P.stage_bytes + turn;
+    CUtensorMap tw{}, tx{};
+    const int n = planes == 1 ? 2 : 3;
+    const uint64_t wide = n == 2 ? K : cols;
+    const uint64_t dims_w[3] = {wide, (uint64_t)P.N, 3}, strides_w[2] = {(uint64_t)ld_w * 2, (uint64_t)cols * 2};
+    const uint64_t dims_x[3] = {wide, (uint64_t)P.M, 3}, strides_x[2] = {(uint64_t)ld_x * 2, (uint64_t)cols * 2};
+    const uint32_t box_w[3] = {64, BF, 3}, box_x[3] = {64, (uint32_t)P.bt, 3};
+    if (!make_tmap(&tw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, W, dims_w, strides_w, box_w) ||
+        !make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, x, dims_x, strides_x, box_x))
+        return cudaErrorInvalidValue;
+    const Kernel kernel = planes == 3 ? kernel_for<3>(split, exact) : kernel_for<1>(split, exact);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -926,8 +996,10 @@ extern "C" int dsa_linear(const void *x, int64_t ld_x, const void *W, int64_t ld
             L.rows[1] = n;
             L.dst[1] = (__nv_bfloat16 *)ws;
         }
-        e = lay_out(L, dtype, p, K, s);
-        if (e != cudaSuccess) return fail_cuda(e);
+        if (p.lay_x || p.lay_w) {
+            e = lay_out(L, dtype, p, K, s);
+            if (e != cudaSuccess) return fail_cuda(e);
+        }
         LinearParams P{};
         P.e = E;
         if (bias) P.e.bias = bias + n0;
@@ -935,7 +1007,7 @@ extern "C" int dsa_linear(const void *x, int64_t ld_x, const void *W, int64_t ld
         if (residual) P.e.res = (const char *)residual + n0 * ey;
         P.M = M;
         P.N = n;
-        e = launch_tiles(xs, p.lay_x ? p.ld : rows_x, ws, p.lay_w ? p.ld : rows_w, K, p.planes == 3 ? (int)p.cols : 0, P, s);
+        e = launch_tiles(xs, p.lay_x ? p.ld : rows_x, ws, p.lay_w ? p.ld : rows_w, K, p.cols, p.planes, P, s);
         if (e != cudaSuccess) return fail_cuda(e);
     }
     return DSA_OK;

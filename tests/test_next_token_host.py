@@ -47,7 +47,7 @@ def test_linear_workspace():
     assert size(A, 64, B, 64, 0, 70, 32, 64) == up(70 * 384) + 32 * 384
     # few tokens, or little work, read W as it is
     assert size(A, 9999, B, 9999, 1, 4, 9999, 9999) == 0 and size(A, 9999, B, 9999, 1, 5, 9999, 9999) > 0
-    assert size(A, 9999, B, 9999, 0, 16, 9999, 9999) == 0 and size(A, 9999, B, 9999, 0, 17, 9999, 9999) > 0
+    assert size(A, 9999, B, 9999, 0, 4, 9999, 9999) == 0 and size(A, 9999, B, 9999, 0, 5, 9999, 9999) > 0
     assert size(A, 64, B, 65, 1, 64, 32, 64) == 0 and size(A, 64, B, 64, 0, 64, 32, 64) == 0
     assert size(A, 64, B, 64, 0, 70, 1 << 20, 64) < (1 << 20) * 384  # not all of W at once
     assert size(A, 64, B, 64, 2, 40, 32, 64) == 0 and size(A, 64, B, 64, 1, 40, 0, 64) == 0
