@@ -8,7 +8,7 @@
 // the stream's type costs the next block nothing.
 //
 // Bound by HBM (8192 rows of 7168 in bf16: 74 us, 0.94 of the measured copy rate; normed twice and gated 98, 0.88; in rows
-// off 16 bytes by latency, 3001 of 2049: 21, 0.51): every value is read once and written once.  A row lies in the registers of
+// off 16 bytes by latency, 8192 of 7167 in bf16: 123, 0.56): every value is read once and written once.  A row lies in the registers of
 // one CTA (of one warp up to 1024 values) between its loads, which are all issued first, and
 // its stores; a thread stores where it has loaded, so h' may be h and y may be u.  A norm is one sum over the row (two for layer:
 // the mean, then the squares of what is left, so that a large mean costs no digits).
@@ -25,14 +25,18 @@ struct NormParams {
     const float *post_gain, *post_bias, *pre_gain, *pre_bias;
     int64_t ld_h, ld_u, ld_g, ld_ho, ld_y, rows;
     int D, post, pre, gate_act;
+    int base;             // FLAT: which of four values the first row starts with
+    bool gate_row;        // FLAT: one gate for all rows, at an offset of its own
     float skip, scale, eps;
 };
 
 constexpr int MAX_D = 16384;
 
-// W values (8, or 1 where rows are off 16 bytes) as they are stored.
+// W values (8, 4 or 1) as they are stored.
 template <typename T, int W> struct Raw { T v[W]; };
 template <typename T> struct Raw<T, 8> { uint4 q[sizeof(T) / 2]; };
+template <> struct Raw<float, 4> { uint4 q; };
+template <> struct Raw<__nv_bfloat16, 4> { uint2 q; };
 
 template <typename T>
 __device__ __forceinline__ void fetch(const T *p, Raw<T, 1> &r) { r.v[0] = *p; }
@@ -43,6 +47,22 @@ __device__ __forceinline__ void fetch(const T *p, Raw<T, 8> &r) {
         asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r.q[i].x), "=r"(r.q[i].y), "=r"(r.q[i].z), "=r"(r.q[i].w)
                      : "l"((const uint4 *)p + i));
+}
+__device__ __forceinline__ void fetch(const float *p, Raw<float, 4> &r) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.q.x), "=r"(r.q.y), "=r"(r.q.z), "=r"(r.q.w)
+                 : "l"(p));
+}
+__device__ __forceinline__ void fetch(const __nv_bfloat16 *p, Raw<__nv_bfloat16, 4> &r) {
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.q.x), "=r"(r.q.y) : "l"(p));
+}
+__device__ __forceinline__ void unpack(const Raw<float, 4> &r, float (&v)[4]) {
+    v[0] = __uint_as_float(r.q.x); v[1] = __uint_as_float(r.q.y);
+    v[2] = __uint_as_float(r.q.z); v[3] = __uint_as_float(r.q.w);
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 4> &r, float (&v)[4]) {
+    v[0] = __uint_as_float(r.q.x << 16); v[1] = __uint_as_float(r.q.x & 0xffff0000u);
+    v[2] = __uint_as_float(r.q.y << 16); v[3] = __uint_as_float(r.q.y & 0xffff0000u);
 }
 template <typename T>
 __device__ __forceinline__ void unpack(const Raw<T, 1> &r, float (&v)[1]) { v[0] = to_f32(r.v[0]); }
@@ -74,9 +94,50 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&v)[8]) {
     }
     *(uint4 *)p = make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ void put(float *p, const float (&v)[4]) { *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&v)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *(uint2 *)p = make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&b);
+}
+// Values d .. d + 3 of a vector of D that may start anywhere: the two groups of four that they lie in, of which only one that
+// holds a value of the vector is loaded, shifted (by the same in every thread of the row).
+__device__ __forceinline__ void load_shifted(const float *p, int d, int D, float (&v)[4]) {
+    const int s = (int)((uintptr_t)(p + d) / 4 & 3);
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int at = d - s + 4 * i;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (at > -4 && at < D && (i == 0 || s != 0)) a = __ldg((const float4 *)(p + at));
+        w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 6; ++e) w[e] = s & 2 ? w[e + 2] : w[e];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = s & 1 ? w[e + 1] : w[e];
+}
+__device__ __forceinline__ void load_shifted(const __nv_bfloat16 *p, int d, int D, float (&v)[4]) {
+    const int s = (int)((uintptr_t)(p + d) / 2 & 3);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int at = d - s + 4 * i;
+        uint2 a = make_uint2(0, 0);
+        if (at > -4 && at < D && (i == 0 || s != 0)) a = __ldg((const uint2 *)(p + at));
+        w[2 * i] = a.x; w[2 * i + 1] = a.y;
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e) w[e] = s & 2 ? w[e + 1] : w[e];
+    Raw<__nv_bfloat16, 4> r;
+    r.q = make_uint2(__funnelshift_r(w[0], w[1], (s & 1) * 16), __funnelshift_r(w[1], w[2], (s & 1) * 16));
+    unpack(r, v);
+}
 template <int W>
-__device__ __forceinline__ void load_gain(const float *p, float (&v)[W]) {
-    if constexpr (W == 8) {
+__device__ __forceinline__ void load_gain(const float *p, int d, int D, float (&v)[W]) {
+    p += W == 4 ? 0 : d;
+    if constexpr (W == 4) {
+        load_shifted(p, d, D, v);
+    } else if constexpr (W == 8) {
         const float4 a = __ldg((const float4 *)p), b = __ldg((const float4 *)p + 1);
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -107,6 +168,12 @@ __device__ __forceinline__ float row_sum(float v, float *part) {
     return v;
 }
 
+// Whether value e of the vector from d on is the row's: vectors of four may hold some before or behind it.
+template <int W>
+__device__ __forceinline__ bool in_row(int d, int e, int D) {
+    return W == 4 ? (unsigned)(d + e) < (unsigned)D : d < D;
+}
+
 // Norms the row's values in place; part: two sums' worth of warps.
 template <int W, int N, bool WARP>
 __device__ __forceinline__ void norm_row(float (&v)[N][W], int kind, const float *gain, const float *bias, int D, float inv_D,
@@ -122,7 +189,7 @@ __device__ __forceinline__ void norm_row(float (&v)[N][W], int kind, const float
 #pragma unroll
         for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int e = 0; e < W; ++e) v[j][e] -= first + j * step < D ? mu : 0.0f;
+            for (int e = 0; e < W; ++e) v[j][e] -= in_row<W>(first + j * step, e, D) ? mu : 0.0f;
     }
     float q = 0.0f;
 #pragma unroll
@@ -138,32 +205,49 @@ __device__ __forceinline__ void norm_row(float (&v)[N][W], int kind, const float
 #pragma unroll
         for (int e = 0; e < W; ++e) v[j][e] *= inv;
         if (gain) {
-            load_gain<W>(gain + d, g);
+            load_gain<W>(gain, d, D, g);
 #pragma unroll
             for (int e = 0; e < W; ++e) v[j][e] *= g[e];
         }
         if (bias && kind == DSA_NORM_LAYER) {
-            load_gain<W>(bias + d, g);
+            load_gain<W>(bias, d, D, g);
 #pragma unroll
             for (int e = 0; e < W; ++e) v[j][e] += g[e];
         }
     }
 }
 
+template <int W, typename T>
+__device__ __forceinline__ void put_row(T *p, const float (&v)[W], int d, int D) {
+    if (W != 4 || (d >= 0 && d + W <= D)) {
+        if (d < D) put(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (in_row<W>(d, e, D)) p[e] = from_f32<T>(v[e]);
+    }
+}
+
 // Vectors of W values; N of them a thread, `step` values apart.  WARP: a warp takes a row.  AHEAD: a CTA takes one row after
 // the other, and the next row's loads are issued once this row's values are unpacked, so they travel while it is summed and
 // stored (8192 rows of 7168 in bf16: 82 -> 74 us, normed and gated 115 -> 98).
+// W = 4 (FLAT): rows off 16 bytes that start on the same place of four in all tensors, as rows of odd width do.  A vector is
+// four values on 16 bytes (8 of bf16), so that a row's first and last may hold values of its neighbours, which count as
+// nothing and are left as they are.
 template <typename TH, typename TX, int W, int N, int THREADS, bool WARP, bool AHEAD>
 __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_constant__ NormParams P) {
     __shared__ float parts[2][4 * 32];  // of the row and the next: a warp may be a row ahead
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int first = t * W, step = (WARP ? 32 : (int)blockDim.x) * W;
+    constexpr bool FLAT = W == 4;
+    const int step = (WARP ? 32 : (int)blockDim.x) * W;
+    const auto first_of = [&](int64_t row) { return t * W - (FLAT ? (int)(P.base + row * P.ld_h & 3) : 0); };
     const float inv_D = 1.0f / (float)P.D;
     const int64_t by = WARP ? (int64_t)gridDim.x * (THREADS / 32) : (int64_t)gridDim.x;
     int64_t r = WARP ? (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
     Raw<TH, W> rh[N];
     Raw<TX, W> ru[N], rg[N];
     const auto load = [&](int64_t row) {
+        const int first = first_of(row);
         const TH *h = (const TH *)P.h + row * P.ld_h + first;
         const TX *u = (const TX *)P.u + row * P.ld_u + first, *g = (const TX *)P.gate + row * P.ld_g + first;
         if (P.u) {
@@ -172,7 +256,7 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
                 ru[j] = Raw<TX, W>{};
                 if (first + j * step < P.D) fetch(u + j * step, ru[j]);
             }
-            if (P.gate)
+            if (P.gate && !(FLAT && P.gate_row))
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     rg[j] = Raw<TX, W>{};
@@ -189,16 +273,30 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
     for (int odd = 0; r < P.rows; r += by, odd ^= 1) {
         float *part = parts[odd];
         float v[N][W];
+        const int first = first_of(r);
+        const auto only_row = [&](float (&a)[W], int d) {
+            if (FLAT && (d < 0 || d + W > P.D))
+#pragma unroll
+                for (int e = 0; e < W; ++e) a[e] = in_row<W>(d, e, P.D) ? a[e] : 0.0f;
+        };
         if (!AHEAD) load(r);
         if (P.u) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) unpack(ru[j], v[j]);
+            for (int j = 0; j < N; ++j) {
+                unpack(ru[j], v[j]);
+                only_row(v[j], first + j * step);
+            }
             norm_row<W, N, WARP>(v, P.post, P.post_gain, P.post_bias, P.D, inv_D, P.eps, first, step, part);
             if (P.gate)
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     float a[W];
-                    unpack(rg[j], a);
+                    if constexpr (FLAT) {
+                        if (P.gate_row) load_shifted((const TX *)P.gate, first + j * step, P.D, a);
+                        else unpack(rg[j], a);
+                    } else {
+                        unpack(rg[j], a);
+                    }
 #pragma unroll
                     for (int e = 0; e < W; ++e) {
                         if (P.gate_act != DSA_ACT_NONE) {
@@ -214,11 +312,13 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
                 unpack(rh[j], a);
 #pragma unroll
                 for (int e = 0; e < W; ++e) v[j][e] = fmaf(P.scale, v[j][e], P.skip * a[e]);
+                only_row(v[j], first + j * step);  // gains and gates beside the row may be anything
             }
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 unpack(rh[j], v[j]);
+                only_row(v[j], first + j * step);
 #pragma unroll
                 for (int e = 0; e < W; ++e) v[j][e] *= P.skip;
             }
@@ -228,14 +328,14 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
             TH *o = (TH *)P.ho + r * P.ld_ho + first;
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                if (first + j * step < P.D) put(o + j * step, v[j]);
+                put_row<W>(o + j * step, v[j], first + j * step, P.D);
         }
         if (P.y) {
             norm_row<W, N, WARP>(v, P.pre, P.pre_gain, P.pre_bias, P.D, inv_D, P.eps, first, step, part + 64);
             TX *y = (TX *)P.y + r * P.ld_y + first;
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                if (first + j * step < P.D) put(y + j * step, v[j]);
+                put_row<W>(y + j * step, v[j], first + j * step, P.D);
         }
         if (!AHEAD) break;
     }
@@ -243,7 +343,7 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
 
 template <typename TH, typename TX, int W, int N, int THREADS, bool WARP, bool AHEAD>
 cudaError_t go(const NormParams &P, cudaStream_t s) {
-    const int vecs = (P.D + W - 1) / W, t = WARP ? THREADS : ((vecs + N - 1) / N + 31) / 32 * 32;
+    const int vecs = (P.D + (W == 4 ? 3 : 0) + W - 1) / W, t = WARP ? THREADS : ((vecs + N - 1) / N + 31) / 32 * 32;
     const int64_t grid = WARP ? (P.rows + THREADS / 32 - 1) / (THREADS / 32) : P.rows;
     // with loads ahead, as many CTAs as the SMs hold threads, each with rows to walk
     const int64_t most = AHEAD ? (int64_t)device_sm_count() * std::max(1, std::min(2048 / t, 32)) : 0x7fffffff;
@@ -253,7 +353,13 @@ cudaError_t go(const NormParams &P, cudaStream_t s) {
 }
 
 template <typename TH, typename TX>
-cudaError_t launch(const NormParams &P, bool vec, cudaStream_t s) {
+cudaError_t launch(const NormParams &P, bool vec, bool flat, cudaStream_t s) {
+    // 8192 rows of 7167 in bf16, four values at a time or one: 123 us and 278 (with loads ahead 119, but 199 instead of 143 where
+    // h is fp32); 3001 of 2049 16 and 23; 16384 of 201 10 and 11
+    if (flat && P.D <= 253) return go<TH, TX, 4, 2, 128, true, false>(P, s);
+    if (flat && P.D <= 509) return go<TH, TX, 4, 4, 128, true, false>(P, s);
+    if (flat && P.D <= 4093) return go<TH, TX, 4, 2, 512, false, false>(P, s);
+    if (flat && P.D <= 16381) return go<TH, TX, 4, 4, 1024, false, false>(P, s);
     if (!vec) {
         if (P.D <= 256) return go<TH, TX, 1, 8, 128, true, false>(P, s);
         if (P.D <= 4096) return go<TH, TX, 1, 8, 512, false, false>(P, s);
@@ -297,11 +403,15 @@ extern "C" int dsa_block_norm(const dsa_block_norm_args *a, void *stream) {
     const size_t eh = esz(a->h_dtype), ex = esz(a->x_dtype);
     struct { const void *p; int64_t ld; size_t e; bool out; } t[5] = {
         {a->h, a->ld_h, eh, false}, {a->u, a->ld_u, ex, false}, {a->gate, a->ld_gate, ex, false}, {a->h_out, a->ld_ho, eh, true}, {a->y, a->ld_y, ex, true}};
-    bool vec = a->D % 8 == 0;
+    bool vec = a->D % 8 == 0, flat = true;
+    const int base = (int)((uintptr_t)a->h / eh & 3);
+    const bool gate_row = a->gate && (a->rows == 1 || a->ld_gate == 0);
     for (const auto &x : t) {
         if (!x.p) continue;
         if ((uintptr_t)x.p % x.e) return DSA_ERR_INVALID_ARG;
         if (x.out && a->rows > 1 && x.ld < a->D) return DSA_ERR_INVALID_ARG;  // rows of an output that overlap
+        if (!(gate_row && x.p == a->gate))
+            flat = flat && (int)((uintptr_t)x.p / x.e & 3) == base && (a->rows == 1 || ((x.ld - a->ld_h) & 3) == 0);
         vec = vec && (uintptr_t)x.p % 16 == 0 && (a->rows <= 1 || x.ld * (int64_t)x.e % 16 == 0);
     }
     if (a->h_out == a->h && a->h_out && a->rows > 1 && a->ld_ho != a->ld_h) return DSA_ERR_INVALID_ARG;
@@ -326,6 +436,8 @@ extern "C" int dsa_block_norm(const dsa_block_norm_args *a, void *stream) {
     P.ld_y = a->ld_y;
     P.rows = a->rows;
     P.D = a->D;
+    P.base = base;
+    P.gate_row = gate_row;
     P.post = a->post.kind;
     P.pre = a->pre.kind;
     P.gate_act = a->gate_act;
@@ -335,9 +447,9 @@ extern "C" int dsa_block_norm(const dsa_block_norm_args *a, void *stream) {
     const cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (a->h_dtype == DSA_F32)
-        e = a->x_dtype == DSA_F32 ? launch<float, float>(P, vec, s) : launch<float, __nv_bfloat16>(P, vec, s);
+        e = a->x_dtype == DSA_F32 ? launch<float, float>(P, vec, !vec && flat, s) : launch<float, __nv_bfloat16>(P, vec, !vec && flat, s);
     else
-        e = a->x_dtype == DSA_F32 ? launch<__nv_bfloat16, float>(P, vec, s) : launch<__nv_bfloat16, __nv_bfloat16>(P, vec, s);
+        e = a->x_dtype == DSA_F32 ? launch<__nv_bfloat16, float>(P, vec, !vec && flat, s) : launch<__nv_bfloat16, __nv_bfloat16>(P, vec, !vec && flat, s);
     if (e != cudaSuccess) return fail_cuda(e);
     note_launch(DSA_KERNEL_BLOCK_NORM);
     return DSA_OK;

@@ -102,11 +102,37 @@ def test_strides_and_in_place(D, off):
     pre = dsa.Norm("layer")
     got = dsa.dsa_block_norm(cut(bh), pre, u=cut(bu), gate=cut(bg), h_out=cut(bh), y=cut(bu))
     assert got[0].data_ptr() == cut(bh).data_ptr() and got[1].data_ptr() == cut(bu).data_ptr()
-    want = dsa.dsa_block_norm(h, pre, u=u, gate=gate)
+    apart = [cut(torch.empty_like(bh)) for _ in range(2)]  # rows that start on the same bytes: the same sums
+    want = dsa.dsa_block_norm(cut(keep_h), pre, u=cut(keep_u), gate=cut(bg), h_out=apart[0], y=apart[1])
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     check(got, h, u, gate, None, ("none", None, None), ("layer", None, None), 1.0, 1.0, 1e-6, (BF16, BF16))
     for now, then in ((bh, keep_h), (bu, keep_u)):
         assert torch.equal(now[:, :off], then[:, :off]) and torch.equal(now[:, off + D:], then[:, off + D:])
+
+
+@pytest.mark.parametrize("h_dt,x_dt", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+@pytest.mark.parametrize("D", [1, 2, 5, 253, 254, 509, 510, 2050, 4093, 4094, 8191, 16381, 16382])
+def test_rows_that_start_off_16_bytes(D, h_dt, x_dt):
+    """All tensors alike, with NaN beside every row, gain, bias and gate row: none gets in, and what lies there stays."""
+    N = 21
+    for off in range(4):
+        h, u, gate, pg, pb, qg, qb = make(N, D, h_dt, x_dt, seed=off)
+        pad = 9 - D % 4 + off
+
+        def beside(t, at=off):
+            buf = torch.full((t.shape[0], D + pad) if t.dim() == 2 else (D + 11,), float("nan"), dtype=t.dtype, device="cuda")
+            return buf, (buf[:, at:at + D] if t.dim() == 2 else buf[at:at + D]).copy_(t)
+
+        row = beside(gate[0], 3)[1][None]
+        post, pre = ("layer", beside(pg, 1)[1], beside(pb, 2)[1]), ("rms", beside(qg, 3)[1], None)
+        for gate_, act in ((beside(gate)[1], "silu"), (row, "sigmoid"), (None, None)):
+            (bh, ch), (bu, cu) = beside(h), beside(u)
+            for outs in ((beside(torch.zeros_like(h)), beside(torch.zeros_like(u))), ((bh, ch), (bu, cu))):
+                got = dsa.dsa_block_norm(ch, dsa.Norm(*pre), u=cu, post=dsa.Norm(*post), gate=gate_, gate_act=act, skip=0.5, scale=2.0,
+                                         h_out=outs[0][1], y=outs[1][1])
+                check(got, h, u, gate_, act, post, pre, 0.5, 2.0, 1e-6, (h_dt, x_dt))
+                for buf, _ in outs:
+                    assert bool(buf[:, :off].isnan().all()) and bool(buf[:, off + D:].isnan().all())
 
 
 def test_large_means_zeros_and_nan():
