@@ -581,45 +581,37 @@ __global__ void __launch_bounds__(256) linear_layout_kernel(const __grid_constan
 #pragma unroll
         for (int p = 0; p < 3; ++p) *(uint4 *)(d + (int64_t)p * L.cols) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
     } else {
-        // Whole 16 bytes around the lane's eight values: its own and, where they go on there, the next lane's.  They hold
-        // at least one value of the row, so they lie in memory that is there.
+        // The whole 16 bytes, one or two, that the lane's eight values lie in.  Each holds a value of the row, so it lies in
+        // memory that is there.
         const uintptr_t at = (uintptr_t)((const uint16_t *)L.src[which] + r * L.ld[which] + k0);
         const int off = (int)(at & 15);  // the same in every lane
         uint4 a[CHUNKS], b[CHUNKS];
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
-            const int k = k0 + c * 256;
-            const uintptr_t from = (at & ~(uintptr_t)15) + c * 512, end = at + 2 * (int64_t)(L.K - k0);
+            const uintptr_t from = at - off + c * 512;
+            const int64_t bytes = off + 2 * (int64_t)(L.K - k0 - c * 256);  // to the row's end
             a[c] = b[c] = make_uint4(0, 0, 0, 0);
-            if (k < L.K) a[c] = *(const uint4 *)from;
-            if (off && k < L.K && (lane == 31 || k + 8 >= L.K) && from + 16 < end) b[c] = *(const uint4 *)(from + 16);
+            if (bytes > off) a[c] = *(const uint4 *)from;
+            if (off && bytes > max(off, 16)) b[c] = *(const uint4 *)(from + 16);
         }
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
             const int k = k0 + c * 256;
-            const uint4 n = make_uint4(__shfl_down_sync(0xffffffffu, a[c].x, 1), __shfl_down_sync(0xffffffffu, a[c].y, 1),
-                                       __shfl_down_sync(0xffffffffu, a[c].z, 1), __shfl_down_sync(0xffffffffu, a[c].w, 1));
-            if (!(lane == 31 || k + 8 >= L.K)) b[c] = n;
-            if (k >= L.cols) continue;
-            const uint32_t w[8] = {a[c].x, a[c].y, a[c].z, a[c].w, b[c].x, b[c].y, b[c].z, b[c].w};
-            uint32_t o[4];
+            if (k >= L.cols) break;
+            uint32_t w[8] = {a[c].x, a[c].y, a[c].z, a[c].w, b[c].x, b[c].y, b[c].z, b[c].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {  // two bytes at a time, off / 4 words and perhaps half a word on
-                uint32_t lo = w[e], hi = w[e + 1];
+            for (int e = 0; e < 6; ++e) w[e] = off & 8 ? w[e + 2] : w[e];
 #pragma unroll
-                for (int j = 1; j < 4; ++j)
-                    if (off / 4 == j) {
-                        lo = w[e + j];
-                        hi = e + j + 1 < 8 ? w[e + j + 1] : 0;
-                    }
-                o[e] = off & 2 ? __funnelshift_r(lo, hi, 16) : lo;
-            }
+            for (int e = 0; e < 5; ++e) w[e] = off & 4 ? w[e + 1] : w[e];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {  // nothing behind the row's end
-                if (k + 2 * e >= L.K) o[e] = 0;
-                else if (k + 2 * e + 1 >= L.K) o[e] &= 0xffffu;
-            }
-            *(uint4 *)(d + c * 256) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int e = 0; e < 4; ++e) w[e] = __funnelshift_r(w[e], w[e + 1], (off & 2) * 8);
+            if (k + 8 > L.K)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // nothing behind the row's end
+                    if (k + 2 * e >= L.K) w[e] = 0;
+                    else if (k + 2 * e + 1 >= L.K) w[e] &= 0xffffu;
+                }
+            *(uint4 *)(d + c * 256) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }

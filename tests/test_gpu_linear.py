@@ -102,6 +102,17 @@ def test_strides(M, dt):
         check(dsa.dsa_linear(same, w), same, w)
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", [(100, 200, 301), (130, 150, 1040), (3, 70, 77)])
+def test_rows_at_every_offset(M, N, K, dt):
+    """Rows that start anywhere within 16 bytes, with NaN beside each."""
+    x, w, _, _ = make(M, N, K, dt)
+    for off in range(9):
+        bufs = [torch.full((n, K + 10 + off % 2), float("nan"), dtype=dt, device="cuda") for n in (M, N)]
+        cx, cw = bufs[0][:, off:off + K].copy_(x), bufs[1][:, 8 - off:8 - off + K].copy_(w)
+        check(dsa.dsa_linear(cx, cw), x, w)
+
+
 @pytest.mark.parametrize("M", [1, 20, 600])
 def test_in_place_residual(M):
     x, w, b, r = make(M, 264, 192, BF16, bias=True, res=BF16)
