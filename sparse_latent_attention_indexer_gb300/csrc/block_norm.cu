@@ -149,7 +149,7 @@ __device__ __forceinline__ void load_gain(const float *p, int d, int D, float (&
 // A bf16 gate needs no more than 2^-20: full division and exponential were half of the time of a gated row.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float v) {
-    if (sizeof(T) == 4) return 1.0f / (1.0f + expf(-v));
+    if (sizeof(T) == 4) return __fdividef(1.0f, 1.0f + expf(-v));  // to 2 units in the last place
     return __fdividef(1.0f, 1.0f + __expf(-v));
 }
 

@@ -76,7 +76,9 @@ struct LinearParams {
 template <int ACT>
 __device__ __forceinline__ float activation(float v) {
     if (ACT == DSA_ACT_RELU) return v < 0.0f ? 0.0f : v;  // a NaN stays
-    if (ACT == DSA_ACT_SILU) return v / (1.0f + expf(-v));
+    // the quotient to 2 units in the last place, 0 where it is next to nothing: with full division 777 tokens, 2048 to 5000, took
+    // 32 us instead of 20
+    if (ACT == DSA_ACT_SILU) return __fdividef(v, 1.0f + expf(-v));
     if (ACT == DSA_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678f));
     if (ACT == DSA_ACT_GELU_TANH) return 0.5f * v * (1.0f + tanhf(0.79788456f * fmaf(0.044715f * v * v, v, v)));
     return v;
