@@ -370,9 +370,9 @@ cudaError_t launch(const NormParams &P, bool vec, bool flat, cudaStream_t s) {
     // few rows: as many threads a row as there are vectors (64 rows of 7168: 2.8 us, with two vectors a thread 3.9)
     if (P.D <= 8192 && P.rows <= device_sm_count()) return go<TH, TX, 8, 1, 1024, false, false>(P, s);
     // loads ahead of fp32 take registers that more threads would use, as long as two CTAs' worth of them fit: 8192 rows of 5120 in
-    // fp32 alone 145 us with and 122 without, gated at 7168 214 and 224; in an fp32 stream of bf16 blocks 4096 71 and 66, 7168
+    // fp32 alone 145 us with and 122 without, of 6144 gated 197 and 204; in an fp32 stream of bf16 blocks 4096 71 and 66, 7168
     // 114 and 128 (all bf16: 79 and 99)
-    if (P.D <= (sizeof(TX) == 4 ? 6144 : sizeof(TH) == 4 ? 5120 : 0)) return go<TH, TX, 8, 2, 1024, false, false>(P, s);
+    if (P.D <= (sizeof(TH) + sizeof(TX) > 4 ? 5120 : 0)) return go<TH, TX, 8, 2, 1024, false, false>(P, s);
     if (P.D <= 8192) return go<TH, TX, 8, 2, 512, false, true>(P, s);
     // 4096 rows of 16384: all bf16 95 us and with four vectors a thread 104; mixed 157 and 148; all fp32 with loads ahead 319
     // and without 235

@@ -27,9 +27,9 @@
 // to 5000: 189 -> 122 us).  Products of one order share an accumulator; the three are added last.
 // Rows that do not start on 16 bytes, and fp32 ones, are laid out anew first (linear_layout_kernel).
 //
-// Bound by HBM with few tokens (17 tokens, 7168 to 131,072, fp32 out: 266 to 272 us, 1.02 of the measured copy
-// rate; 64 tokens, 16384 to 7168: 43.7 us, 0.80, the rest being the start and the end of a tile), by shared memory with
-// many (4096 tokens, 16384 to 7168: 548 us, 1.76 PFLOP/s or 0.91 of the measured peak: a slab is written once and
+// Bound by HBM with few tokens (17 tokens, 7168 to 131,072, fp32 out: 267 to 272 us, 1.02 of the measured copy
+// rate; 64 tokens, 16384 to 7168: 43 us, 0.81, the rest being the start and the end of a tile), by shared memory with
+// many (4096 tokens, 16384 to 7168: 535 us, 1.80 PFLOP/s or 0.94 of the measured peak: a slab is written once and
 // read by the MMAs once, 96 KB in 730 cycles of which the MMAs need 512).
 #include <atomic>
 
