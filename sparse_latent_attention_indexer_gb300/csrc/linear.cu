@@ -20,18 +20,21 @@
 // arithmetic loses.  Where y is fp32 (EXACT) the epilogue takes the sum over after every 8 slabs
 // (32 steps; fp32 layers: 4) and adds these parts to nearest in its registers.
 //
-// fp32 layers run on the same kernel (PLANES = 3): a value is the sum of three bf16 terms of 8 bits
-// each, and of the nine products of terms the six above 2^-24 of the whole are added.  A stage holds
+// fp32 layers run on the same kernel: a value is the sum of three bf16 terms of 8 bits each (planes),
+// and of the nine products of terms the six above 2^-24 of the whole are added.  A stage holds
 // all planes of a slab, x's one behind the other, so that W's plane p meets x's planes 0 .. 2 - p in
 // one MMA of as many times the tokens: W is read three times instead of six (1000 tokens, 2048
 // to 5000: 189 -> 122 us).  Products of one order share an accumulator; the three are added last.
-// Rows that do not start on 16 bytes, and fp32 ones, are laid out anew first (linear_layout_kernel).
+// Rows that do not start on 16 bytes, and fp32 ones, are laid out anew first (linear_layout_kernel);
+// of a large fp32 W and few tokens the epilogue's warps make the planes themselves (RAW), bound by
+// shared memory, which a slab passes three times (17 tokens, 7168 to 7168: 137 -> 70 us).
 //
 // Bound by HBM with few tokens (17 tokens, 7168 to 131,072, fp32 out: 267 to 272 us, 1.02 of the measured copy
 // rate; 64 tokens, 16384 to 7168: 43 us, 0.81, the rest being the start and the end of a tile), by shared memory with
 // many (4096 tokens, 16384 to 7168: 535 us, 1.80 PFLOP/s or 0.94 of the measured peak: a slab is written once and
 // read by the MMAs once, 96 KB in 730 cycles of which the MMAs need 512).
 #include <atomic>
+#include <type_traits>
 
 #include "tc_common.cuh"
 
@@ -42,8 +45,12 @@ __device__ int g_linear_error = 0;
 namespace {
 
 constexpr int BF = 128, MAX_BT = 256;             // features, tokens of a tile
-// Tokens of a tile: the MMA's N is that or, with three planes, three times that; less where exact sums take registers.
-constexpr int max_bt(bool exact, int planes) { return planes == 3 ? 80 : exact ? 128 : MAX_BT; }
+// Where a tile's operands come from: bf16 rows by TMA; planes of fp32 rows by TMA; fp32 rows, by the epilogue's warps.
+enum { ROWS, PLANES, RAW };
+constexpr int planes_of(int src) { return src == ROWS ? 1 : 3; }
+// Tokens of a tile: the MMA's N is that or, with planes, three times that; less where exact sums take registers or rows on
+// their way shared memory.
+constexpr int max_bt(bool exact, int src) { return src == RAW ? 64 : src == PLANES ? 80 : exact ? 128 : MAX_BT; }
 constexpr int W_SLAB = BF * 128;                  // 16 KB: 128 rows x 64 bf16
 constexpr int MAX_STAGES = 12;
 constexpr int NUM_THREADS = 384;                  // 0 TMA, 1 MMA, 2 TMEM owner, 3 idle, 4-11 epilogue
@@ -65,7 +72,10 @@ struct LinearParams {
     Epilogue e;
     int M, N;
     int bt, tt, tiles;    // tokens of a tile, token tiles, tiles
-    int total;            // slabs (64 columns) of K
+    int total, K;         // slabs (64 columns) of K
+    const void *w, *x;    // RAW: the operands and their row strides
+    int64_t ld_w, ld_x;
+    int deep, raw_bytes;  // RAW: slabs that are on their way, bytes of one
     int stages, stage_bytes;
     int share;            // CTAs that share a tile's K (SPLIT)
     int acc_cols, tmem_cols;  // columns from one accumulator to the next; of tensor memory
@@ -162,9 +172,9 @@ __device__ __forceinline__ void expect_if(uint32_t issue, uint64_t *bar, uint32_
         "r"(bytes), "r"(issue)
         : "memory");
 }
-template <int PLANES>  // all planes of the rows at once
+template <int SRC>  // all planes of the rows at once
 __device__ __forceinline__ void load_if(uint32_t issue, void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
-    if constexpr (PLANES == 1)
+    if constexpr (planes_of(SRC) == 1)
         asm volatile(
             "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
             "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
@@ -245,8 +255,42 @@ __device__ __forceinline__ void split_eight(const float (&v)[8], uint32_t (&o)[3
     }
 }
 
-template <bool SPLIT, bool EXACT, int PLANES>
-__global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && PLANES == 1 ? 2 : 1)
+// ---------------------------------------------------------------------------
+// RAW: a warp copies four rows of a slab at a time to shared memory, as they are, and turns them into planes in the MMAs'
+// layout a slab or more later: eight lanes a row, eight values each.  Copied are the whole 16 bytes (chunks) that values
+// of the row lie in; each holds one, so it lies in memory that is there.
+// ---------------------------------------------------------------------------
+constexpr int RAW_ROW = 256;
+// Where chunk c of a row lies: chunks 0..7, 8..15, the even and the odd ones each pass all banks once.
+__device__ __forceinline__ int chunk_at(int c) { return (c ^ ((c >> 3) & 1)) * 16; }
+__device__ __forceinline__ void copy16_if(bool there, uint32_t dst, const char *src) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src),
+                 "r"((int)there)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// A lane's two chunks of a row's slab; bytes: from the slab's start to the row's end.
+__device__ __forceinline__ void copy_row(uint32_t dst, const char *from, int part8, int bytes) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) copy16_if((i * 8 + part8) * 16 < bytes, dst + chunk_at(i * 8 + part8), from + i * 128);
+}
+// To dst, and the further planes `plane` bytes on; left: values to the row's end.
+template <bool TAIL>
+__device__ __forceinline__ void store_eight(const uint4 &a, const uint4 &b, int left, uint8_t *dst, int plane) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = TAIL && e >= left ? 0.0f : __uint_as_float(w[e]);
+    uint32_t o[3][4];
+    split_eight(v, o);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) *(uint4 *)(dst + t * plane) = make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
+}
+
+template <bool SPLIT, bool EXACT, int SRC>
+__global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && SRC == ROWS ? 2 : 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                   const __grid_constant__ LinearParams P) {
     extern __shared__ uint8_t smem_raw[];
@@ -269,20 +313,22 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && PLANES == 1 ? 
     const auto load = [&](uint32_t issue, int st, int ks, int m0, int f0) {
         uint8_t *sw = ring + st * P.stage_bytes;
         expect_if(issue, &full[st], P.stage_bytes);
-        load_if<PLANES>(issue, sw, &tm_w, &full[st], ks * 64, f0);
-        load_if<PLANES>(issue, sw + PLANES * W_SLAB, &tm_x, &full[st], ks * 64, m0);
+        load_if<SRC>(issue, sw, &tm_w, &full[st], ks * 64, f0);
+        load_if<SRC>(issue, sw + planes_of(SRC) * W_SLAB, &tm_x, &full[st], ks * 64, m0);
     };
     // The producer's first loads go out before the CTA has met, while warp 2 waits for tensor memory.
-    const int ahead_slabs = mine > 0 ? min(s1 - s0, P.stages) : 0;
+    const int ahead_slabs = SRC != RAW && mine > 0 ? min(s1 - s0, P.stages) : 0;
     if (warp == 0) {
         int m0, f0;
         tile_of(P, who, m0, f0);
         const uint32_t issue = tc::elect_one();
         if (lane == 0) {
-            tc::prefetch_tmap(&tm_w);
-            tc::prefetch_tmap(&tm_x);
+            if (SRC != RAW) {
+                tc::prefetch_tmap(&tm_w);
+                tc::prefetch_tmap(&tm_x);
+            }
             for (int i = 0; i < P.stages; ++i) {
-                tc::mbar_init(&full[i], 1);
+                tc::mbar_init(&full[i], SRC == RAW ? EPI_THREADS / 32 : 1);
                 tc::mbar_init(&empty[i], 1);
             }
             for (int i = 0; i < 2; ++i) {
@@ -307,7 +353,7 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && PLANES == 1 ? 
     const uint32_t tmem = tmem_slot;
     if (warp != 0) pdl_wait();
 
-    if (warp == 0) {
+    if (SRC != RAW && warp == 0) {
         // ---------------- TMA producer ----------------
         const uint32_t issue = tc::elect_one();
         int it = ahead_slabs, st = ahead_slabs == P.stages ? 0 : ahead_slabs, round = ahead_slabs == P.stages ? 1 : 0;
@@ -326,7 +372,7 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && PLANES == 1 ? 
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
         const uint32_t issue = tc::elect_one();
-        const uint32_t idesc = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, BF, PLANES * P.bt, 0, 0);
+        const uint32_t idesc = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, BF, planes_of(SRC) * P.bt, 0, 0);
         const uint32_t idesc2 = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, BF, 2 * P.bt, 0, 0);
         const uint32_t idesc1 = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, BF, P.bt, 0, 0);
         const uint64_t first = tc::smem_desc(tc::smem_u32(ring), 16, 1024);
@@ -341,8 +387,8 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && PLANES == 1 ? 
                     if (!(ok = wait_warp(&full[st], round & 1, abort_flag, err, 64, P.wait_limit))) break;
                     tc::tc_fence_after();
                     // addresses in a descriptor count 16 bytes and stay below its 14 bits
-                    const uint64_t wd = first + (uint32_t)(st * P.stage_bytes / 16), xd = wd + PLANES * W_SLAB / 16;
-                    if (PLANES == 1) {
+                    const uint64_t wd = first + (uint32_t)(st * P.stage_bytes / 16), xd = wd + planes_of(SRC) * W_SLAB / 16;
+                    if (planes_of(SRC) == 1) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             tc::mma_f16_if(issue, d, wd + kk * 2, xd + kk * 2, idesc, ks != k0 || kk != 0);
@@ -352,7 +398,7 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && PLANES == 1 ? 
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                            for (int p = 0; p < PLANES; ++p)
+                            for (int p = 0; p < planes_of(SRC); ++p)
                                 tc::mma_f16_if(issue, d + p * P.bt, wd + p * (W_SLAB / 16) + kk * 2, xd + kk * 2,
                                                p == 0 ? idesc : p == 1 ? idesc2 : idesc1, ks != k0 || kk != 0 || p != 0);
                     }
@@ -375,7 +421,7 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && PLANES == 1 ? 
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         float *part = (float *)ring;           // SPLIT: [tokens][BF], once every load of the ring has landed and been used
         float *mine_turn = turn + g * 32 * BF;
-        int n = 0;
+        int n = 0, st = 0, round = 0;
         for (int i = 0; i < mine; ++i) {
             int m0, f0;
             tile_of(P, who + i * step, m0, f0);
@@ -427,7 +473,7 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && PLANES == 1 ? 
             };
             const auto read = [&](int c, float (&v)[32]) {  // tokens c .. c + 31 of the accumulator
                 const uint32_t at = lanes + (n & 1) * P.acc_cols + c;
-                if constexpr (PLANES == 1) {
+                if constexpr (planes_of(SRC) == 1) {
                     tc::tmem_ld32(at, v);
                     tc::tmem_ld_wait();
                 } else {
@@ -443,38 +489,124 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && PLANES == 1 ? 
                     for (int e = 0; e < 32; ++e) v[e] += u[e];
                 }
             };
-            bool ok = true;
+            constexpr int SUMS = EXACT ? (max_bt(EXACT, SRC) + 63) / 64 : 1;
+            float sum[SUMS][32];
+            // EXACT: takes the next part over from tensor memory, where all warps are sound.
+            const auto drain = [&](bool sound) -> bool {
+                if (!epi_and(sound && tc::mbar_wait(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit))) return false;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < SUMS; ++j)
+                    if (j * 64 + g * 32 < tokens) {
+                        float v[32];
+                        read(j * 64 + g * 32, v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) sum[j][e] += v[e];
+                    }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&tempty[n & 1]);
+                ++n;
+                return true;
+            };
             if (EXACT) {
-                constexpr int SUMS = (max_bt(EXACT, PLANES) + 63) / 64;
-                float sum[SUMS][32];
 #pragma unroll
                 for (int j = 0; j < SUMS; ++j)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) sum[j][e] = 0.0f;
-                for (int k0 = s0; ok && k0 < s1; k0 += P.chain) {
-                    // takes the next part over from tensor memory
-                    ok = epi_and(tc::mbar_wait(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit));
-                    if (!ok) break;
-                    tc::tc_fence_after();
+            }
+            int parts = (s1 - s0 + P.chain - 1) / P.chain;  // yet to be taken over
+            bool ok = true;
+            if constexpr (SRC == RAW) {
+                // Rows r0, r0 + 32 and so on.  Rows behind the last one are its, or one 32 rows before: what they give is
+                // stored nowhere.
+                constexpr int XS = (max_bt(EXACT, SRC) + 31) / 32;
+                const int r0 = (warp - EPI_WARP0) * 4 + (lane >> 3), part8 = lane & 7;  // row of the first 32, eighth of a slab
+                const int fw = min(f0 + r0, P.N - 1), mx = m0 + min(r0, tokens - 1);
+                const int last_w = (P.N - 1 - fw) / 32, last_x = (m0 + tokens - 1 - mx) / 32;
+                const char *pw[4], *px[XS];  // this lane's first chunk of each row, in the next slab to copy
 #pragma unroll
-                    for (int j = 0; j < SUMS; ++j)
-                        if (j * 64 + g * 32 < tokens) {
-                            float v[32];
-                            read(j * 64 + g * 32, v);
+                for (int j = 0; j < 4; ++j)
+                    pw[j] = (const char *)P.w + ((fw + min(j, last_w) * 32) * P.ld_w + (int64_t)s0 * 64) * 4 + part8 * 16;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) sum[j][e] += v[e];
+                for (int j = 0; j < XS; ++j)
+                    px[j] = (const char *)P.x + ((mx + min(j, last_x) * 32) * P.ld_x + (int64_t)s0 * 64) * 4 + part8 * 16;
+                uint8_t *raw = ring + P.stages * P.stage_bytes + (SPLIT ? 0 : TURN) + r0 * RAW_ROW;
+                const auto fetch = [&](int ks, int slot) {
+                    const uint32_t to = tc::smem_u32(raw) + slot * P.raw_bytes;
+                    const int bytes = ks < s1 ? min(P.K - ks * 64, 64) * 4 : 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        copy_row(to + j * 32 * RAW_ROW, pw[j], part8, bytes);
+                        pw[j] += 256;
+                    }
+#pragma unroll
+                    for (int j = 0; j < XS; ++j)
+                        if (r0 + j * 32 < P.bt) {
+                            copy_row(to + (j + 4) * 32 * RAW_ROW, px[j], part8, bytes);
+                            px[j] += 256;
                         }
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&tempty[n & 1]);
-                    ++n;
+                    copies_commit();
+                };
+                for (int d = 0; d < P.deep; ++d) fetch(s0 + d, d);
+                int slot = 0;
+                uint4 w[4][2], x[XS][2];
+                const auto store = [&](auto tail, uint8_t *to, int left) {
+                    constexpr bool TAIL = decltype(tail)::value;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) store_eight<TAIL>(w[j][0], w[j][1], left, to + j * 4096, W_SLAB);
+                    to += 3 * W_SLAB;
+#pragma unroll
+                    for (int j = 0; j < XS; ++j)
+                        if (r0 + j * 32 < P.bt) store_eight<TAIL>(x[j][0], x[j][1], left, to + j * 4096, P.bt * 128);
+                };
+                const auto take = [&](uint4 (&c)[2], const uint8_t *row) {
+                    c[0] = *(const uint4 *)(row + chunk_at(part8 * 2));
+                    c[1] = *(const uint4 *)(row + chunk_at(part8 * 2 + 1));
+                };
+                // A warp whose wait ran out goes on to where all of them meet.
+                for (int ks = s0; ks < s1; ++ks) {
+                    if (ok) {
+                        if (P.deep == 1) copies_wait<0>();
+                        else if (P.deep == 2) copies_wait<1>();
+                        else copies_wait<2>();
+                        __syncwarp();
+                        const uint8_t *rows = raw + slot * P.raw_bytes;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) take(w[j], rows + j * 32 * RAW_ROW);
+#pragma unroll
+                        for (int j = 0; j < XS; ++j)
+                            if (r0 + j * 32 < P.bt) take(x[j], rows + (j + 4) * 32 * RAW_ROW);
+                        __syncwarp();
+                        fetch(ks + P.deep, slot);
+                        if (++slot == P.deep) slot = 0;
+                        ok = wait_warp(&empty[st], (round & 1) ^ 1, abort_flag, err, 61, P.wait_limit);
+                    }
+                    if (ok) {
+                        uint8_t *to = ring + st * P.stage_bytes + ((part8 ^ (r0 & 7)) << 4) + r0 * 128;  // the 128-byte swizzle
+                        if (ks * 64 + 64 <= P.K) store(std::false_type{}, to, 64);
+                        else store(std::true_type{}, to, P.K - ks * 64 - part8 * 8);
+                        tc::fence_proxy_async_smem();  // the MMAs read what these threads wrote
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&full[st]);
+                        if (++st == P.stages) st = 0, ++round;
+                    }
+                    // the part before the one that this slab ends: its products are done or nearly so
+                    if (EXACT && (ks + 1 - s0) % P.chain == 0 && ks + 1 - s0 > P.chain) {
+                        if (!(ok = drain(ok))) break;
+                        --parts;
+                    }
                 }
+                copies_wait<0>();
+            }
+            if (EXACT) {
+                for (bool agreed = true; agreed && parts > 0; --parts) agreed = ok = drain(ok);
                 if (!ok) break;
 #pragma unroll
                 for (int j = 0; j < SUMS; ++j)
                     if (j * 64 + g * 32 < tokens) put(j * 64 + g * 32, sum[j]);
             } else {
-                ok = epi_and(tc::mbar_wait(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit));
+                ok = epi_and(ok && tc::mbar_wait(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit));
                 if (!ok) break;
                 tc::tc_fence_after();
                 for (int c = g * 32; c < tokens; c += 64) {
@@ -724,7 +856,7 @@ inline bool on16(const void *p, int64_t ld, int rows, int K) {
 // How a call goes: which operands are laid out anew, and how many features of W at once.
 struct Plan {
     bool few, lay_x, lay_w;
-    int planes, chunk;
+    int src, chunk;
     int64_t cols, ld;      // columns of a plane, row of the layout
     size_t x_bytes, w_bytes;
 };
@@ -738,11 +870,18 @@ Plan plan(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int dtype, i
     p.few = !w16 && (M <= 4 || (M <= 64 && (double)M * N * K <= (f32 ? 3.5e7 : 6e6)));
     p.chunk = N;
     if (p.few) return p;
-    p.planes = f32 ? 3 : 1;
+    p.src = f32 ? PLANES : ROWS;
+    // W read once as it is: 64 tokens, 7168 to 7168, 78 us and laid out 138 (17 tokens 70 and 137); 4096 to 2048 22 and 23,
+    // 4096 to 1024 19 and 17, 16384 to 512 45 and 32; 80 tokens, two tiles, 138 and 140
+    if (f32 && M <= max_bt(true, RAW) && N >= 2048 && (int64_t)N * K >= 1 << 23 && (uintptr_t)x % 16 == 0 && (uintptr_t)W % 16 == 0 &&
+        (M <= 1 || ld_x % 4 == 0) && (N <= 1 || ld_w % 4 == 0)) {
+        p.src = RAW;
+        return p;
+    }
     p.lay_x = !x16;
     p.lay_w = !w16;
     p.cols = up(K, f32 ? 64 : 8);
-    p.ld = p.cols * p.planes;
+    p.ld = p.cols * planes_of(p.src);
     if (p.lay_w) {  // as many features as stay in L2 between the two kernels, but enough to fill the SMs
         const int64_t most = std::max<int64_t>(2048, (64 << 20) / (p.ld * 2) / BF * BF), parts = (N + most - 1) / most;
         p.chunk = (int)std::min<int64_t>(N, up((N + parts - 1) / parts, BF));
@@ -780,10 +919,13 @@ struct Cut {
     int bt, share, per_sm;
 };
 using Kernel = void (*)(CUtensorMap, CUtensorMap, LinearParams);
-template <int PLANES>
+template <int SRC>
 Kernel kernel_for(bool split, bool exact) {
-    return split ? exact ? linear_kernel<true, true, PLANES> : linear_kernel<true, false, PLANES>
-                 : exact ? linear_kernel<false, true, PLANES> : linear_kernel<false, false, PLANES>;
+    return split ? exact ? linear_kernel<true, true, SRC> : linear_kernel<true, false, SRC>
+                 : exact ? linear_kernel<false, true, SRC> : linear_kernel<false, false, SRC>;
+}
+Kernel kernel_for(int src, bool split, bool exact) {
+    return src == RAW ? kernel_for<RAW>(split, exact) : src == PLANES ? kernel_for<PLANES>(split, exact) : kernel_for<ROWS>(split, exact);
 }
 
 // Clusters of `share` CTAs that the device holds at once (they lie within one group of SMs each).
@@ -801,7 +943,7 @@ int clusters_at_once(int share, int per_sm, bool exact) {
         attr[0].val.clusterDim = {(unsigned)share, 1, 1};
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        const Kernel kernel = kernel_for<1>(true, exact);
+        const Kernel kernel = kernel_for<ROWS>(true, exact);
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
             (void)cudaGetLastError();
@@ -812,24 +954,25 @@ int clusters_at_once(int share, int per_sm, bool exact) {
     return n;
 }
 
-Cut cut(int M, int N, int total, bool exact, int planes, int sms) {
-    const int most = max_bt(exact, planes), least_tt = (M + most - 1) / most;
+Cut cut(int M, int N, int total, bool exact, int src, int sms) {
+    const int most = max_bt(exact, src), least_tt = (M + most - 1) / most;
     const int64_t ft = ((int64_t)N + BF - 1) / BF;
     Cut best{MAX_BT, 1, 1};
     double least = 1e30;
     for (int tt = least_tt; tt < least_tt + 8; ++tt) {
         const int bt = (int)up((M + tt - 1) / tt, 16);
         const int64_t tiles = (M + bt - 1) / bt * ft;
-        const double smem = planes == 1 ? 2 * (W_SLAB + 128.0 * bt) / 128 : 768 + 9.0 * bt;
-        const double hbm = (double)ft * total * W_SLAB * planes / 3550;
-        for (int share = 1; share <= MAX_SHARE && (share == 1 || total >= (planes == 1 ? 4 : 2) * share); ++share)
-            for (int per_sm = 1; per_sm <= (share > 1 && !exact && planes == 1 && bt <= 128 ? 2 : 1); ++per_sm) {
+        const double smem = src == ROWS ? 2 * (W_SLAB + 128.0 * bt) / 128 : src == PLANES ? 768 + 9.0 * bt : 1600 + 16.0 * bt;
+        const double hbm = (double)ft * total * W_SLAB * (src == ROWS ? 1 : src == PLANES ? 3 : 2) / 3550;
+        for (int share = 1; share <= MAX_SHARE && (share == 1 || total >= (src == PLANES ? 2 : 4) * share); ++share)
+            for (int per_sm = 1; per_sm <= (share > 1 && !exact && src == ROWS && bt <= 128 ? 2 : 1); ++per_sm) {
                 const int64_t room = share == 1 ? sms : clusters_at_once(share, per_sm, exact), rounds = (tiles + room - 1) / room;
                 const double slabs = (total + share - 1) / share, side = tiles * share > sms ? per_sm : 1;
                 const double work = slabs * std::max(smem * side, 350.0);
                 const double fix = share == 1 ? 5000 + 14.0 * bt : 8000 + 60.0 * bt;
-                // one CTA a tile: the end of a tile is beside the next one's product
-                const double t = std::max(hbm + fix, share == 1 ? rounds * std::max(work, 14.0 * bt) + fix : rounds * (work + fix));
+                // one CTA a tile: the end of a tile is beside the next one's product (RAW: behind its own)
+                const double tile = src == RAW ? work + 14.0 * bt : std::max(work, 14.0 * bt);
+                const double t = std::max(hbm + fix, share == 1 ? rounds * tile + fix : rounds * (work + fix));
                 if (t < least * 0.98) {
                     least = t;
                     best = {bt, share, per_sm};
@@ -840,13 +983,18 @@ Cut cut(int M, int N, int total, bool exact, int planes, int sms) {
     return best;
 }
 
-cudaError_t launch_tiles(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int K, int64_t cols, int planes, LinearParams &P,
+cudaError_t launch_tiles(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int K, int64_t cols, int src, LinearParams &P,
                          cudaStream_t s) {
-    const int sms = device_sm_count();
+    const int sms = device_sm_count(), planes = planes_of(src);
     P.total = (K + 63) / 64;
     const bool exact = P.e.f32 && P.total > chain_of(planes);
     P.chain = exact ? chain_of(planes) : P.total;
-    const Cut c = cut(P.M, P.N, P.total, exact, planes, sms);
+    P.K = K;
+    P.x = x;
+    P.w = W;
+    P.ld_x = ld_x;
+    P.ld_w = ld_w;
+    const Cut c = cut(P.M, P.N, P.total, exact, src, sms);
     P.bt = c.bt;
     P.share = c.share;
     P.tt = (P.M + P.bt - 1) / P.bt;
@@ -861,18 +1009,24 @@ cudaError_t launch_tiles(const void *x, int64_t ld_x, const void *W, int64_t ld_
     if (!split) P.acc_cols = MAX_BT;
     P.tmem_cols = split && !exact ? P.acc_cols : 2 * P.acc_cols;
     const int turn = split ? 0 : TURN, room = SMEM_MAX / c.per_sm - 2048 - turn;
-    P.stages = std::min(MAX_STAGES, room / P.stage_bytes);
-    const int smem = 1024 + P.stages * P.stage_bytes + turn;
+    if (src == RAW) {  // two slabs for the MMAs, up to three on their way, then more for the MMAs
+        P.raw_bytes = (BF + P.bt) * RAW_ROW;
+        P.deep = std::min(3, (room - 2 * P.stage_bytes) / P.raw_bytes);
+    }
+    P.stages = std::min(MAX_STAGES, (room - P.deep * P.raw_bytes) / P.stage_bytes);
+    const int smem = 1024 + P.stages * P.stage_bytes + turn + P.deep * P.raw_bytes;
     CUtensorMap tw{}, tx{};
-    const int n = planes == 1 ? 2 : 3;
-    const uint64_t wide = n == 2 ? K : cols;
-    const uint64_t dims_w[3] = {wide, (uint64_t)P.N, 3}, strides_w[2] = {(uint64_t)ld_w * 2, (uint64_t)cols * 2};
-    const uint64_t dims_x[3] = {wide, (uint64_t)P.M, 3}, strides_x[2] = {(uint64_t)ld_x * 2, (uint64_t)cols * 2};
-    const uint32_t box_w[3] = {64, BF, 3}, box_x[3] = {64, (uint32_t)P.bt, 3};
-    if (!make_tmap(&tw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, W, dims_w, strides_w, box_w) ||
-        !make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, x, dims_x, strides_x, box_x))
-        return cudaErrorInvalidValue;
-    const Kernel kernel = planes == 3 ? kernel_for<3>(split, exact) : kernel_for<1>(split, exact);
+    if (src != RAW) {
+        const int rank = src == ROWS ? 2 : 3;
+        const uint64_t wide = src == ROWS ? K : cols;
+        const uint64_t dims_w[3] = {wide, (uint64_t)P.N, 3}, strides_w[2] = {(uint64_t)ld_w * 2, (uint64_t)cols * 2};
+        const uint64_t dims_x[3] = {wide, (uint64_t)P.M, 3}, strides_x[2] = {(uint64_t)ld_x * 2, (uint64_t)cols * 2};
+        const uint32_t box_w[3] = {64, BF, 3}, box_x[3] = {64, (uint32_t)P.bt, 3};
+        if (!make_tmap(&tw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, W, dims_w, strides_w, box_w) ||
+            !make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, x, dims_x, strides_x, box_x))
+            return cudaErrorInvalidValue;
+    }
+    const Kernel kernel = kernel_for(src, split, exact);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1001,7 +1155,7 @@ extern "C" int dsa_linear(const void *x, int64_t ld_x, const void *W, int64_t ld
         if (residual) P.e.res = (const char *)residual + n0 * ey;
         P.M = M;
         P.N = n;
-        e = launch_tiles(xs, p.lay_x ? p.ld : rows_x, ws, p.lay_w ? p.ld : rows_w, K, p.cols, p.planes, P, s);
+        e = launch_tiles(xs, p.lay_x ? p.ld : rows_x, ws, p.lay_w ? p.ld : rows_w, K, p.cols, p.src, P, s);
         if (e != cudaSuccess) return fail_cuda(e);
     }
     return DSA_OK;
