@@ -798,7 +798,8 @@ def dsa_linear(x, weight, bias=None, act=None, residual=None, y=None, dtype=None
     with _launching(dev, stream):
         if y is None:
             y = x.new_empty((M, N), dtype=dtype)
-        if workspace is None:
+        # bf16 rows on 16 bytes need none
+        if workspace is None and (dt != DSA_BF16 or (px | pw) & 15 or (ld_x | ld_w) & 7 or ld_x < K or ld_w < K):
             need = lib.dsa_linear_workspace_size(px, ld_x, pw, ld_w, dt, M, N, K)
             if need:
                 workspace = x.new_empty(need, dtype=torch.uint8)
@@ -818,8 +819,8 @@ class Norm:
         self.kind, self.gain, self.bias = _NORMS[kind], gain, bias
 
     def _struct(self, fn, name, dev, D):
-        return self.kind, _vector(fn, name + ".gain", self.gain, dev, (D,), torch.float32), \
-            _vector(fn, name + ".bias", self.bias, dev, (D,), torch.float32)
+        return self.kind, _vector(fn, name + ".gain", self.gain, dev, (D,), torch.float32) or 0, \
+            _vector(fn, name + ".bias", self.bias, dev, (D,), torch.float32) or 0
 
 
 def dsa_block_norm(h, pre: Norm | None = None, u=None, post: Norm | None = None, gate=None, gate_act=None, skip=1.0,
@@ -849,18 +850,18 @@ def dsa_block_norm(h, pre: Norm | None = None, u=None, post: Norm | None = None,
         ld_ho = _matrix(fn, "h_out", h_out, dev, shape, h_dtype)
     if y is not None:
         ld_y = _matrix(fn, "y", y, dev, shape, x_dtype)
-    post_ = (0, None, None) if post is None else post._struct(fn, "post", dev, D)
-    pre_ = (0, None, None) if pre is None else pre._struct(fn, "pre", dev, D)
+    post_ = (0, 0, 0) if post is None else post._struct(fn, "post", dev, D)
+    pre_ = (0, 0, 0) if pre is None else pre._struct(fn, "pre", dev, D)
     h_dt, x_dt = _dt_of(h_dtype), _dt_of(x_dtype)
     with _launching(dev, stream):
         if h_out is None and want_h:
             h_out = h.new_empty(shape)
         if y is None and want_y:
             y = h.new_empty(shape, dtype=x_dtype)
-        args = _abi.dsa_block_norm_args(N, D, h_dt, x_dt, h.data_ptr(), ld_h, _addr(u), ld_u, _addr(gate), ld_g,
-                                        _GATES[gate_act], post_, pre_, skip, scale, eps, _addr(h_out), ld_ho, _addr(y),
-                                        ld_y)
-        _check(fn, _abi.load().dsa_block_norm(ctypes.byref(args), torch._C._cuda_getCurrentRawStream(dev)))
+        args = _abi.block_norm_bytes.pack(N, D, h_dt, x_dt, h.data_ptr(), ld_h, _addr(u) or 0, ld_u, _addr(gate) or 0, ld_g,
+                                          _GATES[gate_act], *post_, *pre_, skip, scale, eps, _addr(h_out) or 0, ld_ho,
+                                          _addr(y) or 0, ld_y)
+        _check(fn, _abi.load().dsa_block_norm(args, torch._C._cuda_getCurrentRawStream(dev)))
     return h_out, y
 
 

@@ -53,6 +53,21 @@ def test_linear_workspace():
     assert size(A, 64, B, 64, 2, 40, 32, 64) == 0 and size(A, 64, B, 64, 1, 40, 0, 64) == 0
 
 
+def test_block_norm_bytes():
+    """The packed form is the structure's."""
+    v = list(range(1, 25))
+    flat = _abi.block_norm_bytes.pack(*v)
+    st = _abi.dsa_block_norm_args(*v[:11], _abi.dsa_norm(*v[11:14]), _abi.dsa_norm(*v[14:17]), *v[17:])
+    got = _abi.dsa_block_norm_args.from_buffer_copy(flat)
+    for name, _ in st._fields_:
+        a, b = getattr(got, name), getattr(st, name)
+        if isinstance(a, ctypes.Structure):
+            assert [getattr(a, n) for n, _ in a._fields_] == [getattr(b, n) for n, _ in a._fields_]
+        else:
+            assert a == b and a
+    assert len(flat) == ctypes.sizeof(st)
+
+
 def norm(**k):
     d = dict(rows=4, D=64, h_dtype=1, x_dtype=1, h=A, ld_h=64, u=B, ld_u=64, gate=None, ld_gate=64, gate_act=0,
              post=(0, None, None), pre=(1, None, None), skip=1.0, scale=1.0, eps=1e-6, h_out=C, ld_ho=64, y=D, ld_y=64)
