@@ -26,8 +26,8 @@
 // one MMA of as many times the tokens: W is read three times instead of six (1000 tokens, 2048
 // to 5000: 189 -> 122 us).  Products of one order share an accumulator; the three are added last.
 // Rows that do not start on 16 bytes, and fp32 ones, are laid out anew first (linear_layout_kernel);
-// of a large fp32 W and few tokens the epilogue's warps make the planes themselves (RAW), bound by
-// shared memory, which a slab passes three times (17 tokens, 7168 to 7168: 137 -> 70 us).
+// of a large fp32 W and few tokens, or of little work, the epilogue's warps make the planes themselves
+// (RAW), bound by shared memory, which a slab passes three times (17 tokens, 7168 to 7168: 134 -> 73 us).
 //
 // Bound by HBM with few tokens (17 tokens, 7168 to 131,072, fp32 out: 267 to 272 us, 1.02 of the measured copy
 // rate; 64 tokens, 16384 to 7168: 43 us, 0.81, the rest being the start and the end of a tile), by shared memory with
@@ -871,10 +871,14 @@ Plan plan(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int dtype, i
     p.chunk = N;
     if (p.few) return p;
     p.src = f32 ? PLANES : ROWS;
-    // W read once as it is: 64 tokens, 7168 to 7168, 78 us and laid out 138 (17 tokens 70 and 137); 4096 to 2048 22 and 23,
-    // 4096 to 1024 19 and 17, 16384 to 512 45 and 32; 80 tokens, two tiles, 138 and 140
-    if (f32 && M <= max_bt(true, RAW) && N >= 2048 && (int64_t)N * K >= 1 << 23 && (uintptr_t)x % 16 == 0 && (uintptr_t)W % 16 == 0 &&
-        (M <= 1 || ld_x % 4 == 0) && (N <= 1 || ld_w % 4 == 0)) {
+    // RAW: of a large W, read once: 64 tokens, 7168 to 7168, 81 us and laid out 141 (17 tokens 73 and 134); 4096 to 2048 22 and 23,
+    // 4096 to 1024 19 and 17, 16384 to 512 45 and 32; 80 tokens, two tiles, 138 and 140.  Of little work, for one launch and no
+    // workspace, which are 8 us of the host's time: 500 tokens, 1536 to 260, 15 and 12 us on the GPU; 128, 2048 to 1024, 17
+    // and 14; but 64, 7168 to 256, 22 and 15
+    const bool large = M <= max_bt(true, RAW) && N >= 2048 && (int64_t)N * K >= 1 << 23;
+    const bool little = K <= 4096 && (double)M * N * K <= 3e8;
+    if (f32 && (large || little) && (uintptr_t)x % 16 == 0 && (uintptr_t)W % 16 == 0 && (M <= 1 || ld_x % 4 == 0) &&
+        (N <= 1 || ld_w % 4 == 0)) {
         p.src = RAW;
         return p;
     }

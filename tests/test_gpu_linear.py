@@ -43,7 +43,8 @@ def make(M, N, K, dt, seed=0, bias=False, res=None):
 SIZES = [(1, 1, 1), (1, 128, 64), (1, 300, 8), (3, 129, 65), (15, 64, 1000), (16, 127, 200), (17, 1000, 7), (31, 260, 512),
          (33, 8, 2048), (64, 768, 4096), (100, 5, 63), (255, 257, 72), (256, 128, 640), (257, 131, 129), (300, 1024, 96),
          (513, 40, 2), (1000, 136, 264), (60, 1000, 1001), (40, 130, 16384), (7, 72, 20001), (5, 2500, 2999), (20, 2000, 1999),
-         (80, 500, 576), (81, 129, 257), (161, 300, 64), (400, 5200, 4100)]
+         (80, 500, 576), (81, 129, 257), (161, 300, 64), (400, 5200, 4100),
+         (1000, 520, 1040), (2000, 250, 640)]
 
 
 @pytest.mark.parametrize("out", [BF16, F32])
@@ -60,6 +61,8 @@ def test_sizes(M, N, K, dt, out):
         assert kernels == {"linear"}
     elif (dt == F32 or N > 1) and (M <= 4 or (M <= 64 and M * N * K <= (3.5e7 if dt == F32 else 6e6))):
         assert kernels == {"linear_simt"}
+    elif dt == F32 and K % 4 == 0 and K <= 4096 and M * N * K <= 3e8:
+        assert kernels == {"linear"}
     elif N > 1:
         assert kernels == {"linear", "linear_layout"}
 

@@ -26,8 +26,8 @@ def linear(**k):
     (dict(dtype=2), NOT), (dict(y_dtype=2), NOT), (dict(act=5), NOT), (dict(act=-1), NOT), (dict(ld_y=31), BAD),
     (dict(y=A), BAD), (dict(y=B), BAD), (dict(res=C, ld_r=64), BAD), (dict(ld_x=-64), BAD), (dict(ld_w=-1), BAD),
     (dict(M=2 ** 31 - 1), NOT), (dict(N=2 ** 31 - 1), NOT), (dict(K=2 ** 31 - 1), NOT), (dict(dtype=0, K=400000000), NOT),
-    (dict(M=40, ld_x=65), WORKSPACE), (dict(M=70, W=B + 2), WORKSPACE), (dict(M=70, dtype=0), WORKSPACE),
-    (dict(M=70, dtype=0, ws=D, ws_bytes=70 * 384 + 32 * 384 - 1), WORKSPACE), (dict(M=70, dtype=0, ws=D + 16, ws_bytes=1 << 30), WORKSPACE),
+    (dict(M=40, ld_x=65), WORKSPACE), (dict(M=70, W=B + 2), WORKSPACE), (dict(M=70, dtype=0, x=A + 4), WORKSPACE),
+    (dict(M=70, dtype=0, x=A + 4, ws=D, ws_bytes=70 * 384 + 32 * 384 - 1), WORKSPACE), (dict(M=70, dtype=0, x=A + 4, ws=D + 16, ws_bytes=1 << 30), WORKSPACE),
     (dict(M=0), 0), (dict(M=0, x=None, W=None, y=None), 0),
 ])
 def test_linear_refusals(k, status):
@@ -44,7 +44,10 @@ def test_linear_workspace():
     assert size(A + 2, 64, B, 64, 1, 40, 32, 64) == 40 * 128
     assert size(A, 64, B, 65, 1, 70, 32, 64) == 32 * 128
     assert size(A, 33, B, 33, 1, 70, 32, 33) == up(70 * 80) + up(32 * 80)
-    assert size(A, 64, B, 64, 0, 70, 32, 64) == up(70 * 384) + 32 * 384
+    assert size(A + 4, 64, B, 64, 0, 70, 32, 64) == up(70 * 384) + 32 * 384
+    # fp32 rows on 16 bytes: little work, and few tokens of a large W
+    assert size(A, 64, B, 64, 0, 70, 32, 64) == 0 and size(A, 9000, B, 9000, 0, 64, 9000, 9000) == 0
+    assert size(A, 9000, B, 9000, 0, 65, 9000, 9000) > 0 and size(A, 9000, B, 9000, 0, 64, 900, 9000) > 0
     # few tokens, or little work, read W as it is
     assert size(A, 9999, B, 9999, 1, 4, 9999, 9999) == 0 and size(A, 9999, B, 9999, 1, 5, 9999, 9999) > 0
     assert size(A, 9999, B, 9999, 0, 4, 9999, 9999) == 0 and size(A, 9999, B, 9999, 0, 5, 9999, 9999) > 0
