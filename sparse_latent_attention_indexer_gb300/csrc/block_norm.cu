@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
             if (first + j * step < P.D) fetch(h + j * step, rh[j]);
         }
     };
+    pdl_wait();
     if (AHEAD && r < P.rows) load(r);
     for (int odd = 0; r < P.rows; r += by, odd ^= 1) {
         float *part = parts[odd];
@@ -348,8 +349,7 @@ cudaError_t go(const NormParams &P, cudaStream_t s) {
     // with loads ahead, as many CTAs as the SMs hold threads, each with rows to walk
     const int64_t most = AHEAD ? (int64_t)device_sm_count() * std::max(1, std::min(2048 / t, 32)) : 0x7fffffff;
     if (!AHEAD && grid > most) return cudaErrorInvalidConfiguration;
-    block_norm_kernel<TH, TX, W, N, THREADS, WARP, AHEAD><<<(unsigned)std::min(grid, most), t, 0, s>>>(P);
-    return cudaGetLastError();
+    return launch_pdl(block_norm_kernel<TH, TX, W, N, THREADS, WARP, AHEAD>, dim3((unsigned)std::min(grid, most)), dim3(t), 0, s, P);
 }
 
 template <typename TH, typename TX>
