@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
             }
         }
         if (AHEAD && r + by < P.rows) load(r + by);
+        else pdl_trigger();
         if (P.ho) {
             TH *o = (TH *)P.ho + r * P.ld_ho + first;
 #pragma unroll
