@@ -27,6 +27,8 @@
 // Bound by latency for a row (131,072 logits: top-k 50 12 us, top-p 0.95 26 to 33, of which reading takes 2: meetings of
 // the cluster, barriers, code that runs once), by latency and instructions for many (256 rows: top-k 50 58 us, top-k 1000
 // 111, top-p 0.95 230 to 280, no rule 152; HBM 20).  An exact weight takes some 75 instructions, the rest of a pass 20.
+// A row's code runs once, between other kernels from cold caches: it is kept short (loops over CTAs and steps of sorting are not
+// unrolled, the end has one place), which took one row among other kernels from 28 to 18 us.
 #include <algorithm>
 
 #include "dsa_common.cuh"
@@ -350,6 +352,7 @@ __device__ u64 refine(const Part &R, Shared &S, u64 bound, Pick at, u64 target, 
         }
         meet();
         low = high = NONE;
+#pragma unroll 1
         for (int r = 0; r < R.share; ++r) {
             low = min(low, S.in[0][r]);
             high = min(high, S.in[1][r]);
@@ -408,6 +411,7 @@ __device__ __forceinline__ u64 candidate(const Shared &S, int i, int n, int regi
     if (i >= n) return NONE;
     if (region == 0) return S.few[i];
     int r = 0;
+#pragma unroll 1
     while (r < share - 1 && i >= S.in_alone[r]) i -= S.in_alone[r++];
     return S.few[r * region + i];
 }
@@ -418,10 +422,13 @@ template <int E>
 __device__ void sort_few(Shared &S, u64 (&c)[E], int n) {
     const int tid = threadIdx.x;
     int size = 32;
+#pragma unroll 1
     while (size < n) size *= 2;
     if constexpr (E == 1) {
         if (tid < size) {
+#pragma unroll 1
             for (int len = 2; len <= size; len *= 2)
+#pragma unroll 1
                 for (int d = len / 2; d > 0; d /= 2) {
                     u64 other;
                     if (d >= 32) {
@@ -440,7 +447,9 @@ __device__ void sort_few(Shared &S, u64 (&c)[E], int n) {
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < E; ++e) S.sorted[E * tid + e] = c[e];
+#pragma unroll 1
         for (int len = 2; len <= size; len *= 2)
+#pragma unroll 1
             for (int d = len / 2; d > 0; d /= 2) {
                 __syncthreads();
                 for (int t = tid; t < size / 2; t += THREADS) {
@@ -605,6 +614,7 @@ __device__ void bound_few(const Part &R, Shared &S, int n, u64 before, u64 targe
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         if (cum < target && cum + w[e] >= target)
+#pragma unroll 1
             for (int r = 0; r < R.share; ++r) push(&S.bound, r, c[e]);
         cum += w[e];
     }
@@ -770,6 +780,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     const auto list_up_to = [&](int to, int most, int &listed, int &before) -> int {
         listed = 0;
         const float xt = to == BINS - 1 ? INFINITY : (float)to + 1.0f;
+#pragma unroll 1
         for (int i0 = w0; i0 < w1; i0 += 256) {
             float l[8];
             unsigned hit[8];
@@ -808,6 +819,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     // A token of the row's first k is one of its CTA's first k, and one near the row's maximum is nearer to its CTA's: with
     // a small k, or min-p alone, the CTAs list what they have and meet once.
     const int region = FEW / P.share;
+    int n_few = -1, regions = 0;  // candidates of a row whose kept tokens are among them, and where they lie
+    u64 all_few = 0;
     const bool alone = k != 1 && ((by_k && k <= min(region * 2 / 3, THREADS / 2)) || (by_m && !by_k && !by_p));
     if (alone) {
         int to, listed = 0, before = 0, count = FEW + 1;
@@ -827,283 +840,300 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
             push(&S.in_alone[rank], tid, count);
         }
         if (count <= region)
+#pragma unroll 1
             for (int i = lane; i < listed; i += 32) push(&S.few[rank * region + before + i], 0, S.list[warp][i]);
         meet();
         int total = 0;
+#pragma unroll 1
         for (int r = 0; r < P.share; ++r) {
             R.top = fmaxf(R.top, S.in_top[r]);
             total = max(total, S.in_alone[r]);
         }
         if (total <= region && R.top > -INFINITY) {
-            if (rank == 0) {
-                total = 0;
-                for (int r = 0; r < P.share; ++r) total += S.in_alone[r];
-                R.ch = S.ch;
-                R.cl = S.cl;
-                if (total <= THREADS) finish_few<1>(P, R, S, row, total, region, by_k ? k : 0, p, m, 0);
-                else finish_few<4>(P, R, S, row, total, region, by_k ? k : 0, p, m, 0);
-            }
-            return;
+            if (rank != 0) return;
+            n_few = 0;
+#pragma unroll 1
+            for (int r = 0; r < P.share; ++r) n_few += S.in_alone[r];
+            regions = region;
         }
     } else {
         meet_wait();
         if (tid < P.share) push(&S.in_top[rank], tid, R.top);
         meet();
+#pragma unroll 1
         for (int r = 0; r < P.share; ++r) R.top = fmaxf(R.top, S.in_top[r]);
     }
 
-    // ---------------- the first token, or none ----------------
-    if (R.top == -INFINITY || k == 1) {  // the same in every thread of the cluster
-        // CACHED: a thread's maximum is over the tokens that it looks through here; else the CTA's is known, not the thread's
-        if (R.top > -INFINITY && (CACHED ? mine : own_top) == R.top) {
+    if (n_few < 0) {
+        // ---------------- the first token, or none ----------------
+        if (R.top == -INFINITY || k == 1) {  // the same in every thread of the cluster
+            // CACHED: a thread's maximum is over the tokens that it looks through here; else the CTA's is known, not the thread's
+            if (R.top > -INFINITY && (CACHED ? mine : own_top) == R.top) {
 #pragma unroll 8
-            for (int i = tid; i < R.n; i += THREADS)
-                if (R.at(i) == R.top) atomicMin(&S.first, R.first + i);
+                for (int i = tid; i < R.n; i += THREADS)
+                    if (R.at(i) == R.top) atomicMin(&S.first, R.first + i);
+            }
+            __syncthreads();
+            if (tid == 0) push(&S.in_first[rank], 0, S.first);
+            meet();
+            if (rank == 0 && tid == 0) {
+                const bool none = R.top == -INFINITY;
+                int first = MAX_V;
+#pragma unroll 1
+                for (int r = 0; r < P.share; ++r) first = min(first, S.in_first[r]);
+                P.token[row] = none ? -1 : first;
+                if (P.logprob) P.logprob[row] = none ? -INFINITY : 0.0f;
+                if (P.kept) P.kept[row] = none ? 0 : 1;
+            }
+            return;
         }
-        __syncthreads();
-        if (tid == 0) push(&S.in_first[rank], 0, S.first);
-        meet();
-        if (rank == 0 && tid == 0) {
-            const bool none = R.top == -INFINITY;
-            int first = MAX_V;
-            for (int r = 0; r < P.share; ++r) first = min(first, S.in_first[r]);
-            P.token[row] = none ? -1 : first;
-            if (P.logprob) P.logprob[row] = none ? -INFINITY : 0.0f;
-            if (P.kept) P.kept[row] = none ? 0 : 1;
+        R.ch = S.ch;
+        R.cl = S.cl;
+        if (R.top == INFINITY) {  // the infinite ones alone, as equals
+            __syncthreads();
+            if constexpr (CACHED)
+                for (int i = tid; i < R.n; i += THREADS) raw[i] = from_f32<T>(R.at(i) == INFINITY ? 0.0f : -INFINITY);
+            else R.infinite = true;
+            mine = mine == INFINITY ? 0.0f : -INFINITY;
+            R.top = 0.0f;
+            __syncthreads();
         }
-        return;
-    }
-    R.ch = S.ch;
-    R.cl = S.cl;
-    if (R.top == INFINITY) {  // the infinite ones alone, as equals
-        __syncthreads();
-        if constexpr (CACHED)
-            for (int i = tid; i < R.n; i += THREADS) raw[i] = from_f32<T>(R.at(i) == INFINITY ? 0.0f : -INFINITY);
-        else R.infinite = true;
-        mine = mine == INFINITY ? 0.0f : -INFINITY;
-        R.top = 0.0f;
-        __syncthreads();
-    }
 
-    // ---------------- where the run ends ----------------
-    u64 bound = NONE;
-    int turn = 0;
-    // bins: the tokens before `from` are kept for certain, those behind `to` are not
-    int from = 0, to = BINS;
-    if (by_k) {
-        // as many of the threads' maxima as tokens are wanted lie in the bins up to `to`: so do as many tokens
-        maxima();
-        meet();
-        u64 one_, two;
-        merge(S.rough, P.share, one_, two);
-        to = pick_maxima(one_, two, (u64)k);
-    } else if (by_m) {
-        to = (int)fminf(PER_NAT * LN2_H * S.yh + 2.0f, (float)(BINS - 1));  // rounding moves a token by less than a bin
-    } else if (by_p) {
-        // The weight of a bin is that of its start times a sum of factors in (e^(-1/32), 1], counted in
-        // steps that let all of the CTA's tokens lie in one bin.
-        const float steps = P.slice < 65536 ? 65536.0f : 8192.0f;
-        for (int b = tid; b < BINS; b += THREADS) S.rough[b] = 0;
-        __syncthreads();
+        // ---------------- where the run ends ----------------
+        u64 bound = NONE;
+        int turn = 0;
+        // bins: the tokens before `from` are kept for certain, those behind `to` are not
+        int from = 0, to = BINS;
+        if (by_k) {
+            // as many of the threads' maxima as tokens are wanted lie in the bins up to `to`: so do as many tokens
+            maxima();
+            meet();
+            u64 one_, two;
+            merge(S.rough, P.share, one_, two);
+            to = pick_maxima(one_, two, (u64)k);
+        } else if (by_m) {
+            to = (int)fminf(PER_NAT * LN2_H * S.yh + 2.0f, (float)(BINS - 1));  // rounding moves a token by less than a bin
+        } else if (by_p) {
+            // The weight of a bin is that of its start times a sum of factors in (e^(-1/32), 1], counted in
+            // steps that let all of the CTA's tokens lie in one bin.
+            const float steps = P.slice < 65536 ? 65536.0f : 8192.0f;
+            for (int b = tid; b < BINS; b += THREADS) S.rough[b] = 0;
+            __syncthreads();
 #pragma unroll 4
-        for (int i = tid; i < R.n; i += THREADS) {
-            const float l = R.at(i), x = R.x(l);
-            if (!(l > -INFINITY) || x >= (float)(BINS - 1)) continue;
-            const int b = (int)x;
-            atomicAdd(&S.rough[b], (unsigned)fmaf(steps, tc::ex2_approx(((float)b - x) * (LOG2E / PER_NAT)), 0.5f));
-        }
-        meet();
-        float one_, two;
-        merge(S.rough, P.share, one_, two);
-        one_ *= tc::ex2_approx((float)(2 * tid) * (-LOG2E / PER_NAT));
-        two *= tc::ex2_approx((float)(2 * tid + 1) * (-LOG2E / PER_NAT));
-        float sum = one_ + two;
+            for (int i = tid; i < R.n; i += THREADS) {
+                const float l = R.at(i), x = R.x(l);
+                if (!(l > -INFINITY) || x >= (float)(BINS - 1)) continue;
+                const int b = (int)x;
+                atomicAdd(&S.rough[b], (unsigned)fmaf(steps, tc::ex2_approx(((float)b - x) * (LOG2E / PER_NAT)), 0.5f));
+            }
+            meet();
+            float one_, two;
+            merge(S.rough, P.share, one_, two);
+            one_ *= tc::ex2_approx((float)(2 * tid) * (-LOG2E / PER_NAT));
+            two *= tc::ex2_approx((float)(2 * tid + 1) * (-LOG2E / PER_NAT));
+            float sum = one_ + two;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float a = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += a;
+            for (int o = 1; o < 32; o <<= 1) {
+                const float a = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += a;
+            }
+            __syncthreads();
+            if (lane == 31) S.warp_sum[warp] = (u64)__float_as_uint(sum);
+            if (tid == 0) S.pick_bin = S.pick_to = BINS - 1;
+            __syncthreads();
+            float before = 0.0f, all = 0.0f;
+#pragma unroll 1
+            for (int w = 0; w < WARPS; ++w) {
+                const float a = __uint_as_float((unsigned)S.warp_sum[w]);
+                if (w < warp) before += a;
+                all += a;
+            }
+            sum += before;
+            // Sums are off by less than 2^-15 of themselves, x and the bins' starts (arguments near 46 in 24 bits) by 2^-17, and by
+            // half a step a factor; the tokens 32 nats down, left out, weigh less than 2^-28 in all.
+            const float slack = 1.0f / 16384.0f + 1.0f / steps, least = p * all * (1.0f - slack), most = p * all * (1.0f + slack);
+            if (sum >= least) atomicMin(&S.pick_bin, sum - two >= least ? 2 * tid : 2 * tid + 1);
+            if (sum >= most) atomicMin(&S.pick_to, sum - two >= most ? 2 * tid : 2 * tid + 1);
+            __syncthreads();
+            from = S.pick_bin;
+            to = S.pick_to;
         }
-        __syncthreads();
-        if (lane == 31) S.warp_sum[warp] = (u64)__float_as_uint(sum);
-        if (tid == 0) S.pick_bin = S.pick_to = BINS - 1;
-        __syncthreads();
-        float before = 0.0f, all = 0.0f;
-        for (int w = 0; w < WARPS; ++w) {
-            const float a = __uint_as_float((unsigned)S.warp_sum[w]);
-            if (w < warp) before += a;
-            all += a;
-        }
-        sum += before;
-        // Sums are off by less than 2^-15 of themselves, x and the bins' starts (arguments near 46 in 24 bits) by 2^-17, and by
-        // half a step a factor; the tokens 32 nats down, left out, weigh less than 2^-28 in all.
-        const float slack = 1.0f / 16384.0f + 1.0f / steps, least = p * all * (1.0f - slack), most = p * all * (1.0f + slack);
-        if (sum >= least) atomicMin(&S.pick_bin, sum - two >= least ? 2 * tid : 2 * tid + 1);
-        if (sum >= most) atomicMin(&S.pick_to, sum - two >= most ? 2 * tid : 2 * tid + 1);
-        __syncthreads();
-        from = S.pick_bin;
-        to = S.pick_to;
-    }
 
-    // ---------------- candidates, and exact sums ----------------
-    // w_all: what the warp's tokens weigh (top-p needs it of all, a draw from all of them too); w_sure: of those before `from`
-    u64 w_all = 0, w_sure = 0;
-    int sure = 0, listed = 0;
-    bool by_few = false;
-    const bool weigh = !by_k && (by_p || !by_m), list = to < BINS;
-    if (weigh) {
-        const float xf = (float)from, xt = to >= BINS - 1 ? INFINITY : (float)to + 1.0f;
-        for (int i0 = w0; i0 < w1; i0 += 128) {
-            float l[4];
-            u64 w[4];
+        // ---------------- candidates, and exact sums ----------------
+        // w_all: what the warp's tokens weigh (top-p needs it of all, a draw from all of them too); w_sure: of those before `from`
+        u64 w_all = 0, w_sure = 0;
+        int sure = 0, listed = 0;
+        bool by_few = false;
+        const bool weigh = !by_k && (by_p || !by_m), list = to < BINS;
+        if (weigh) {
+            const float xf = (float)from, xt = to >= BINS - 1 ? INFINITY : (float)to + 1.0f;
+#pragma unroll 1
+            for (int i0 = w0; i0 < w1; i0 += 128) {
+                float l[4];
+                u64 w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) l[e] = i0 + e * 32 + lane < w1 ? R.at(i0 + e * 32 + lane) : -INFINITY;
+                for (int e = 0; e < 4; ++e) l[e] = i0 + e * 32 + lane < w1 ? R.at(i0 + e * 32 + lane) : -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = weight_of(R.top, l[e], R.ch, R.cl, S.root);
-            if (!list) {
+                for (int e = 0; e < 4; ++e) w[e] = weight_of(R.top, l[e], R.ch, R.cl, S.root);
+                if (!list) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w_all += w[e];
+                        sure += l[e] > -INFINITY;
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
+                    const float x = R.x(l[e]);  // -inf and NaN are in no bin
                     w_all += w[e];
-                    sure += l[e] > -INFINITY;
+                    if (x < xf) {
+                        w_sure += w[e];
+                        ++sure;
+                    }
+                    const unsigned hit = __ballot_sync(0xffffffffu, x >= xf && x < xt);
+                    if (hit == 0) continue;
+                    const int at = listed + __popc(hit & ((1u << lane) - 1));
+                    if ((hit >> lane & 1) && at < LIST) S.list[warp][at] = order_of(l[e], R.first + i0 + e * 32 + lane);
+                    listed += __popc(hit);
                 }
-                continue;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = R.x(l[e]);  // -inf and NaN are in no bin
-                w_all += w[e];
-                if (x < xf) {
-                    w_sure += w[e];
-                    ++sure;
-                }
-                const unsigned hit = __ballot_sync(0xffffffffu, x >= xf && x < xt);
-                if (hit == 0) continue;
-                const int at = listed + __popc(hit & ((1u << lane) - 1));
-                if ((hit >> lane & 1) && at < LIST) S.list[warp][at] = order_of(l[e], R.first + i0 + e * 32 + lane);
-                listed += __popc(hit);
             }
         }
-    }
-    u64 all = 0, sure_all = 0;  // of the cluster
-    if (list) {
-        const u64 a = warp_sum(w_all), b = warp_sum(w_sure);
-        int before, count = weigh ? count_listed(S, listed, FEW, before) : list_up_to(to, FEW, listed, before);
+        u64 all = 0, sure_all = 0;  // of the cluster
+        if (list) {
+            const u64 a = warp_sum(w_all), b = warp_sum(w_sure);
+            int before, count = weigh ? count_listed(S, listed, FEW, before) : list_up_to(to, FEW, listed, before);
+            if (lane == 0) {
+                S.warp_sum[warp] = a;
+                S.warp_two[warp] = b;
+            }
+            __syncthreads();
+            if (warp == 0) {
+                const u64 x = warp_sum(lane < WARPS ? S.warp_sum[lane] : 0), y = warp_sum(lane < WARPS ? S.warp_two[lane] : 0);
+                if (lane < P.share) {
+                    push(&S.in[0][rank], lane, x);
+                    push(&S.in[1][rank], lane, y);
+                    push(&S.in_count[rank], lane, count);
+                }
+            }
+            meet();
+            int total = 0;
+#pragma unroll 1
+            for (int r = 0; r < P.share; ++r) {
+                const int c = S.in_count[r];
+                if (r < rank) before += c;
+                total += c;
+                all += S.in[0][r];
+                sure_all += S.in[1][r];
+            }
+            if (total <= FEW) {
+#pragma unroll 1
+                for (int i = lane; i < listed; i += 32) push(&S.few[before + i], 0, S.list[warp][i]);
+                meet();
+                if (from == 0) {  // there is nothing but the candidates
+                    if (rank != 0) return;
+                    n_few = total;
+                    all_few = all;
+                    goto few;
+                }
+                if (rank == 0) {  // top-p alone: the run ends among the candidates
+                    const u64 target = part_of(p, all, true);
+                    if (total <= THREADS) bound_few<1>(R, S, total, sure_all, target);
+                    else bound_few<4>(R, S, total, sure_all, target);
+                }
+                meet();
+                bound = S.bound;
+                u64 w = 0;
+#pragma unroll 1
+                for (int i = lane; i < listed; i += 32)
+                    if (S.list[warp][i] <= bound) {
+                        w += weight_of(R.top, logit_of(S.list[warp][i]), R.ch, R.cl, S.root);
+                        ++sure;
+                    }
+                w_all = w_sure + w;  // what the warp's kept tokens weigh
+                by_few = true;
+            }
+        }
+        if (list && !by_few) {  // many candidates
+            if (by_k) {
+                const Pick at = first_level<false>(R, S, NONE, (u64)k, 0.0f, turn);
+                if (at.all > (u64)k) bound = refine<false>(R, S, NONE, at, (u64)k, turn);
+            }
+            if (by_p) {
+                const Pick at = first_level<true>(R, S, bound, 0, p, turn);
+                bound = refine<true>(R, S, bound, at, max(part_of(p, at.all, true), 1ull), turn);
+            }
+        }
+
+        // ---------------- the draw ----------------
+        const float fh = S.yh, fl = S.yl;
+        // weight of a token, if it is kept
+        const auto take = [&](int i, bool &kept, float &yh, float &yl) -> u64 {
+            const float l = R.at(i);
+            kept = l > -INFINITY && (bound == NONE || order_of(l, R.first + i) <= bound);
+            const bool some = exponent(R.top, l, R.ch, R.cl, yh, yl);
+            if (by_m && !(some ? (yh - fh) + (yl - fl) <= 0.0f : yh <= fh)) kept = false;
+            return kept && some ? weight(yh, yl, S.root) : 0;
+        };
+        if (list && !by_few) {
+            w_all = 0;
+            sure = 0;
+            for (int i = w0 + lane; i < w1; i += 32) {
+                bool kept;
+                float yh, yl;
+                w_all += take(i, kept, yh, yl);
+                sure += kept;
+            }
+        }
+        const u64 sum = warp_sum(w_all);
+        const int count = __reduce_add_sync(0xffffffffu, sure);
+        __syncthreads();
         if (lane == 0) {
-            S.warp_sum[warp] = a;
-            S.warp_two[warp] = b;
+            S.warp_sum[warp] = sum;
+            S.warp_two[warp] = (u64)count;
         }
         __syncthreads();
         if (warp == 0) {
-            const u64 x = warp_sum(lane < WARPS ? S.warp_sum[lane] : 0), y = warp_sum(lane < WARPS ? S.warp_two[lane] : 0);
+            const u64 x = warp_sum(lane < WARPS ? S.warp_sum[lane] : 0), n = warp_sum(lane < WARPS ? S.warp_two[lane] : 0);
             if (lane < P.share) {
-                push(&S.in[0][rank], lane, x);
-                push(&S.in[1][rank], lane, y);
-                push(&S.in_count[rank], lane, count);
+                push(&S.in_draw[rank], lane, x);
+                push(&S.in_kept[rank], lane, (int)n);
             }
         }
         meet();
-        int total = 0;
+        u64 whole = 0, before = 0;
+        int kept_all = 0;
+#pragma unroll 1
         for (int r = 0; r < P.share; ++r) {
-            const int c = S.in_count[r];
-            if (r < rank) before += c;
-            total += c;
-            all += S.in[0][r];
-            sure_all += S.in[1][r];
+            if (r < rank) before += S.in_draw[r];
+            whole += S.in_draw[r];
+            kept_all += S.in_kept[r];
         }
-        if (total <= FEW) {
-            for (int i = lane; i < listed; i += 32) push(&S.few[before + i], 0, S.list[warp][i]);
-            meet();
-            if (from == 0) {  // there is nothing but the candidates
-                if (rank == 0 && total <= THREADS) finish_few<1>(P, R, S, row, total, 0, by_k ? k : 0, p, m, all);
-                else if (rank == 0) finish_few<4>(P, R, S, row, total, 0, by_k ? k : 0, p, m, all);
-                return;
-            }
-            if (rank == 0) {  // top-p alone: the run ends among the candidates
-                const u64 target = part_of(p, all, true);
-                if (total <= THREADS) bound_few<1>(R, S, total, sure_all, target);
-                else bound_few<4>(R, S, total, sure_all, target);
-            }
-            meet();
-            bound = S.bound;
-            u64 w = 0;
-            for (int i = lane; i < listed; i += 32)
-                if (S.list[warp][i] <= bound) {
-                    w += weight_of(R.top, logit_of(S.list[warp][i]), R.ch, R.cl, S.root);
-                    ++sure;
+        const u64 goal = part_of(random_of(P, row), whole, false);
+#pragma unroll 1
+        for (int w = 0; w < warp; ++w) before += S.warp_sum[w];
+        if (before <= goal && goal < before + S.warp_sum[warp]) {  // the token is this warp's
+#pragma unroll 1
+            for (int i0 = w0; i0 < w1; i0 += 32) {
+                bool kept = false;
+                float yh = 0.0f, yl = 0.0f;
+                const u64 w = i0 + lane < w1 ? take(i0 + lane, kept, yh, yl) : 0;
+                const u64 upto = before + warp_scan(w, lane);
+                const unsigned hit = __ballot_sync(0xffffffffu, upto > goal);
+                if (hit) {
+                    if (lane == __ffs(hit) - 1) write_token(P, row, R.first + i0 + lane, yh, yl, whole, kept_all);
+                    break;
                 }
-            w_all = w_sure + w;  // what the warp's kept tokens weigh
-            by_few = true;
-        }
-    }
-    if (list && !by_few) {  // many candidates
-        if (by_k) {
-            const Pick at = first_level<false>(R, S, NONE, (u64)k, 0.0f, turn);
-            if (at.all > (u64)k) bound = refine<false>(R, S, NONE, at, (u64)k, turn);
-        }
-        if (by_p) {
-            const Pick at = first_level<true>(R, S, bound, 0, p, turn);
-            bound = refine<true>(R, S, bound, at, max(part_of(p, at.all, true), 1ull), turn);
-        }
-    }
-
-    // ---------------- the draw ----------------
-    const float fh = S.yh, fl = S.yl;
-    // weight of a token, if it is kept
-    const auto take = [&](int i, bool &kept, float &yh, float &yl) -> u64 {
-        const float l = R.at(i);
-        kept = l > -INFINITY && (bound == NONE || order_of(l, R.first + i) <= bound);
-        const bool some = exponent(R.top, l, R.ch, R.cl, yh, yl);
-        if (by_m && !(some ? (yh - fh) + (yl - fl) <= 0.0f : yh <= fh)) kept = false;
-        return kept && some ? weight(yh, yl, S.root) : 0;
-    };
-    if (list && !by_few) {
-        w_all = 0;
-        sure = 0;
-        for (int i = w0 + lane; i < w1; i += 32) {
-            bool kept;
-            float yh, yl;
-            w_all += take(i, kept, yh, yl);
-            sure += kept;
-        }
-    }
-    const u64 sum = warp_sum(w_all);
-    const int count = __reduce_add_sync(0xffffffffu, sure);
-    __syncthreads();
-    if (lane == 0) {
-        S.warp_sum[warp] = sum;
-        S.warp_two[warp] = (u64)count;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        const u64 x = warp_sum(lane < WARPS ? S.warp_sum[lane] : 0), n = warp_sum(lane < WARPS ? S.warp_two[lane] : 0);
-        if (lane < P.share) {
-            push(&S.in_draw[rank], lane, x);
-            push(&S.in_kept[rank], lane, (int)n);
-        }
-    }
-    meet();
-    u64 whole = 0, before = 0;
-    int kept_all = 0;
-    for (int r = 0; r < P.share; ++r) {
-        if (r < rank) before += S.in_draw[r];
-        whole += S.in_draw[r];
-        kept_all += S.in_kept[r];
-    }
-    const u64 goal = part_of(random_of(P, row), whole, false);
-    for (int w = 0; w < warp; ++w) before += S.warp_sum[w];
-    if (before <= goal && goal < before + S.warp_sum[warp]) {  // the token is this warp's
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-            bool kept = false;
-            float yh = 0.0f, yl = 0.0f;
-            const u64 w = i0 + lane < w1 ? take(i0 + lane, kept, yh, yl) : 0;
-            const u64 upto = before + warp_scan(w, lane);
-            const unsigned hit = __ballot_sync(0xffffffffu, upto > goal);
-            if (hit) {
-                if (lane == __ffs(hit) - 1) write_token(P, row, R.first + i0 + lane, yh, yl, whole, kept_all);
-                break;
+                before = __shfl_sync(0xffffffffu, upto, 31);
             }
-            before = __shfl_sync(0xffffffffu, upto, 31);
         }
+        return;
     }
+few:
+    R.ch = S.ch;
+    R.cl = S.cl;
+    if (n_few <= THREADS) finish_few<1>(P, R, S, row, n_few, regions, by_k ? k : 0, p, m, all_few);
+    else finish_few<4>(P, R, S, row, n_few, regions, by_k ? k : 0, p, m, all_few);
 }
 
 template <typename T, bool CACHED>
