@@ -764,10 +764,17 @@ def _first_of(fn: str, name: str, t, dims: int) -> int:
     return dev
 
 
+def _int_sizes(fn: str, *sizes: int):
+    """The C interface counts these in 32 bits; ctypes would drop the rest."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"{fn}: sizes {sizes} must be below 2^31")
+
+
 def dsa_linear_workspace_size(x: torch.Tensor, weight: torch.Tensor) -> int:
     fn = "dsa_linear_workspace_size"
     dev = _first_of(fn, "x", x, 2)
     (M, K), N = x.shape, weight.shape[0]
+    _int_sizes(fn, M, N, K)
     return _abi.load().dsa_linear_workspace_size(x.data_ptr(), _matrix(fn, "x", x, dev, (M, K), x.dtype),
                                                  weight.data_ptr(), _matrix(fn, "weight", weight, dev, (N, K), x.dtype),
                                                  _dt_of(x.dtype), M, N, K)
@@ -783,6 +790,7 @@ def dsa_linear(x, weight, bias=None, act=None, residual=None, y=None, dtype=None
     dev = _first_of(fn, "x", x, 2)
     M, K = x.shape
     N = weight.shape[0]
+    _int_sizes(fn, M, N, K)
     x_dtype = x.dtype
     ld_x, ld_w = _matrix(fn, "x", x, dev, (M, K), x_dtype), _matrix(fn, "weight", weight, dev, (N, K), x_dtype)
     if dtype is None:
@@ -834,6 +842,7 @@ def dsa_block_norm(h, pre: Norm | None = None, u=None, post: Norm | None = None,
         raise ValueError(f"{fn}: gate_act must be 'sigmoid', 'silu' or None, not {gate_act!r}")
     dev = _first_of(fn, "h", h, 2)
     N, D = shape = h.shape
+    _int_sizes(fn, D)
     h_dtype = h.dtype
     x_dtype = next((t.dtype for t in (u, gate, y) if t is not None), dtype or h_dtype)
     if dtype is not None and dtype != x_dtype:
@@ -875,6 +884,7 @@ def dsa_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=
     fn = "dsa_sample"
     dev = _first_of(fn, "logits", logits, 2)
     R, V = logits.shape
+    _int_sizes(fn, R, V)
     f32, i32, rows = torch.float32, torch.int32, (R,)
     ld, dt = _matrix(fn, "logits", logits, dev, (R, V), logits.dtype), _dt_of(logits.dtype)
     if uniform is None:

@@ -79,3 +79,17 @@ def test_end_of_step(B):
     for i, j in zip(again, want):
         assert torch.equal(i, j)
     assert not torch.equal(want[7], got[7])
+
+
+def test_sizes_that_do_not_fit_32_bits_are_refused():
+    """Views of 2^32 + 3 rows or columns (of one row's memory) would otherwise count as 3."""
+    many = 2 ** 32 + 3
+    x, w = torch.zeros(1, 8, device="cuda", dtype=BF16), torch.zeros(4, 8, device="cuda", dtype=BF16)
+    wide = torch.zeros(1, 1, device="cuda", dtype=BF16).expand(2, many)
+    for call in (lambda: dsa.dsa_linear(x.expand(many, 8), w), lambda: dsa.dsa_linear(x, w[:1].expand(many, 8)),
+                 lambda: dsa.dsa_linear_workspace_size(x.expand(many, 8), w), lambda: dsa.dsa_linear(wide, wide),
+                 lambda: dsa.dsa_sample(x.expand(many, 8), torch.zeros(3, device="cuda")),
+                 lambda: dsa.dsa_sample(wide, torch.zeros(2, device="cuda")), lambda: dsa.dsa_block_norm(wide)):
+        with pytest.raises(ValueError):
+            call()
+        torch.cuda.synchronize()
