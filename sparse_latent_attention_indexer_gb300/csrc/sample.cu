@@ -468,7 +468,7 @@ __device__ void sort_few(Shared &S, u64 (&c)[E], int n) {
 }
 
 // Among one CTA's candidates (E a thread, at most `bound`): the last token of the shortest run whose count (or weight w) reaches
-// the target, which it does reach.  A histogram finds its bin, the bin's few tokens are sorted; many in one bin: all are.
+// the target, which all of them together have to reach.  A histogram finds its bin, the bin's few tokens are sorted; many in one bin: all are.
 template <int E, bool WEIGHT, typename Part>
 __device__ u64 select_few(const Part &R, Shared &S, const u64 (&c)[E], const u64 (&w)[E], u64 bound, int n, u64 target) {
     const int tid = threadIdx.x;
@@ -570,13 +570,15 @@ __device__ void finish_few(const SampleParams &P, const Part &R, Shared &S, int6
     if constexpr (E > 1) {
         if (k > 0 && k < n) bound = select_few<E, false>(R, S, by_index, w, NONE, n, (u64)k);
         if (p < 1.0f) {
-            if (k > 0) {
-                mine = 0;
+            u64 here;
+            mine = 0;
 #pragma unroll
-                for (int e = 0; e < E; ++e) mine += by_index[e] <= bound ? w[e] : 0;
-                block_scan(S, mine, total);
-            }
-            bound = select_few<E, true>(R, S, by_index, w, bound, n, max(part_of(p, total, true), 1ull));
+            for (int e = 0; e < E; ++e) mine += by_index[e] <= bound ? w[e] : 0;
+            block_scan(S, mine, here);
+            if (k > 0) total = here;
+            const u64 target = max(part_of(p, total, true), 1ull);
+            // candidates by min-p may weigh less than that share of all tokens: then the run has them all and more
+            if (here >= target) bound = select_few<E, true>(R, S, by_index, w, bound, n, target);
         }
     }
     int kept = 0;

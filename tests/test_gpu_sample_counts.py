@@ -1,0 +1,61 @@
+"""Sampling where the kept tokens are hard to count: outputs are filled before the call, so that one which is not written
+shows, and token and count have to equal the 64-bit form's (the kernel's sums are off by less than 2^-36 of the whole)."""
+import pytest
+import torch
+
+import sparse_latent_attention_indexer_gb300 as dsa
+from sparse_latent_attention_indexer_gb300 import _abi
+from tests import next_token_reference as R
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def on(values, dt=F32):
+    return None if values is None else torch.as_tensor(values, dtype=dt, device="cuda")
+
+
+def sample(x, u, T=None, k=None, p=None, m=None):
+    """The C call, into outputs that hold something else before."""
+    n, V = x.shape
+    u, T, k, p, m = on(u), on(T), on(k, torch.int32), on(p), on(m)
+    token, kept = torch.full((n,), -77, dtype=torch.int32, device="cuda"), torch.full((n,), -78, dtype=torch.int32, device="cuda")
+    logprob = torch.full((n,), 79.0, device="cuda")
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    rc = _abi.load().dsa_sample(x.data_ptr(), x.stride(0), _abi.DSA_F32 if x.dtype == F32 else _abi.DSA_BF16, n, V, at(u), at(T), at(k),
+                                at(p), at(m), at(token), at(logprob), at(kept), torch.cuda.current_stream().cuda_stream)
+    assert rc == _abi.DSA_OK
+    return token.tolist(), logprob.tolist(), kept.tolist()
+
+
+def check(x, u, T=None, k=None, p=None, m=None, rows=None):
+    got = sample(x, u, T, k, p, m)
+    f = lambda v, i, d: d if v is None else float(torch.tensor(float(v[i]), dtype=F32))  # noqa: E731
+    for i in range(x.shape[0]) if rows is None else rows:
+        want = R.sample_row(x[i], f(u, i, 0.0), f(T, i, 1.0), 0 if k is None else int(k[i]), f(p, i, 1.0), f(m, i, 0.0))
+        assert (got[0][i], got[2][i]) == (want[0], want[2]), f"row {i}: {[g[i] for g in got]}, expected {want}"
+        assert abs(got[1][i] - want[1]) <= 8 * 2.0 ** -24 * (abs(want[1]) + 2.0 ** -20), f"row {i}: {[g[i] for g in got]}, expected {want}"
+    return got
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("n,V", [(12, 131072), (10, 6007), (300, 20011), (200, 131072), (700, 6007)])
+def test_nucleus_that_reaches_behind_min_p(n, V, dt):
+    """Without top-k: 300 to 1900 tokens pass min-p, and the run that reaches top_p of all tokens ends among them or behind
+    them.  Rows of one CTA and of several, kept in shared memory or not."""
+    g = torch.Generator(device="cuda").manual_seed(n + V)
+    x = torch.randn(n, V, generator=g, device="cuda").to(dt)
+    T = [0.9, 0.8, 1.0, 1.3]
+    rows = list(range(n)) if n <= 12 else list(range(0, n, max(1, n // 40)))
+    T, p, m, behind = [T[i % 4] for i in range(n)], [], [], 0
+    for i in range(n):
+        t = float(torch.tensor(T[i], dtype=F32))
+        l = x[i].double().sort(descending=True)[0]  # noqa: E741
+        w = ((l - l[0]) / t).exp()
+        many = 300 + i * 331 % 1600
+        m.append(float((w[many - 1] * w[many]).sqrt()) if dt == F32 else float(w[many]) * 0.999)
+        share = float(w[:many].sum() / w.sum())
+        p.append([0.999, 0.95, 0.5 + 0.5 * share, 0.5 * share, share * 0.999][i % 5])
+        behind += p[-1] > share
+    assert behind >= n // 2
+    check(x, torch.rand(n, generator=g, device="cuda").tolist(), T, None, p, m, rows)
