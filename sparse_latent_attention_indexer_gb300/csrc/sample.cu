@@ -249,9 +249,10 @@ struct Row {
         const float l = to_f32(raw[i]);
         return CACHED || !infinite ? l : l == INFINITY ? 0.0f : -INFINITY;
     }
-    // Bins fall with the logit; equal logits have equal ones.  A token is in bin b or before: x < b + 1.
-    __device__ __forceinline__ float x(float l) const { return (top - l) * bins; }
-    __device__ __forceinline__ int bin(float l) const { return (int)fminf(x(l), (float)(BINS - 1)); }
+    // Bins fall with the logit; equal logits have equal ones.  A token is in bin b or before: x < b + 1.  The last bin takes all that
+    // is further down, a mask of the type's lowest number too, whose product is infinite; -inf and NaN get there and are no tokens.
+    __device__ __forceinline__ float x(float l) const { return fminf((top - l) * bins, (float)(BINS - 1)); }
+    __device__ __forceinline__ int bin(float l) const { return (int)x(l); }
 };
 
 // Sum of v over the threads up to this one, and over all.
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     // this warp's go among them.
     const auto list_up_to = [&](int to, int most, int &listed, int &before) -> int {
         listed = 0;
-        const float xt = to == BINS - 1 ? INFINITY : (float)to + 1.0f;
+        const float xt = (float)to + 1.0f;
 #pragma unroll 1
         for (int i0 = w0; i0 < w1; i0 += 256) {
             float l[8];
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
 #pragma unroll
             for (int e = 0; e < 8; ++e) l[e] = i0 + e * 32 + lane < w1 ? R.at(i0 + e * 32 + lane) : -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) hit[e] = __ballot_sync(0xffffffffu, R.x(l[e]) < xt);  // false for -inf and NaN
+            for (int e = 0; e < 8; ++e) hit[e] = __ballot_sync(0xffffffffu, l[e] > -INFINITY && R.x(l[e]) < xt);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (hit[e] == 0) continue;
@@ -924,7 +925,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
 #pragma unroll 4
             for (int i = tid; i < R.n; i += THREADS) {
                 const float l = R.at(i), x = R.x(l);
-                if (!(l > -INFINITY) || x >= (float)(BINS - 1)) continue;
+                if (x >= (float)(BINS - 1)) continue;
                 const int b = (int)x;
                 atomicAdd(&S.rough[b], (unsigned)fmaf(steps, tc::ex2_approx(((float)b - x) * (LOG2E / PER_NAT)), 0.5f));
             }
@@ -968,7 +969,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
         bool by_few = false;
         const bool weigh = !by_k && (by_p || !by_m), list = to < BINS;
         if (weigh) {
-            const float xf = (float)from, xt = to >= BINS - 1 ? INFINITY : (float)to + 1.0f;
+            const float xf = (float)from, xt = (float)to + 1.0f;
 #pragma unroll 1
             for (int i0 = w0; i0 < w1; i0 += 128) {
                 float l[4];
@@ -987,13 +988,13 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float x = R.x(l[e]);  // -inf and NaN are in no bin
+                    const float x = R.x(l[e]);
                     w_all += w[e];
                     if (x < xf) {
                         w_sure += w[e];
                         ++sure;
                     }
-                    const unsigned hit = __ballot_sync(0xffffffffu, x >= xf && x < xt);
+                    const unsigned hit = __ballot_sync(0xffffffffu, l[e] > -INFINITY && x >= xf && x < xt);
                     if (hit == 0) continue;
                     const int at = listed + __popc(hit & ((1u << lane) - 1));
                     if ((hit >> lane & 1) && at < LIST) S.list[warp][at] = order_of(l[e], R.first + i0 + e * 32 + lane);

@@ -59,3 +59,30 @@ def test_nucleus_that_reaches_behind_min_p(n, V, dt):
         behind += p[-1] > share
     assert behind >= n // 2
     check(x, torch.rand(n, generator=g, device="cuda").tolist(), T, None, p, m, rows)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("n,V", [(10, 64), (10, 5000), (10, 131072), (300, 131072), (900, 3001)])
+def test_masks_of_finite_numbers(n, V, dt):
+    """The type's lowest number, or another far below the rest, is a token like any other: it weighs nothing and counts.
+    top_k below, at and above the number of tokens without a mask."""
+    g = torch.Generator(device="cuda").manual_seed(n * V)
+    low = [torch.finfo(dt).min, -1e30, -1e9, -1e38]
+    x = torch.empty(n, V, dtype=dt, device="cuda")
+    for i in range(n):
+        x[i] = low[i % 4]
+        at = torch.randperm(V, generator=g, device="cuda")[:40]
+        x[i, at] = (2 * torch.randn(40, generator=g, device="cuda")).to(dt)
+    u = torch.rand(n, generator=g, device="cuda").tolist()
+    T = [[1.0, 0.5, 1.0, 2.0, 1e-4][i % 5] for i in range(n)]
+    pick = lambda *v: [v[i // 4 % len(v)] for i in range(n)]  # noqa: E731
+    rows = list(range(n)) if n <= 12 else list(range(0, n, 31))
+    for k in ([50] * n, [1000] * n, pick(3, 40, 41, V - 1)):
+        got = check(x, u, T, k, None, None, rows)
+        assert all(got[2][i] == min(k[i], V) for i in range(n))
+    check(x, u, T, [50] * n, pick(0.9, 0.999, 1.0), None, rows)
+    check(x, u, T, [50] * n, None, pick(0.0, 0.01, 1e-20), rows)
+    check(x, u, T, None, pick(0.9, 0.999), None, rows)
+    check(x, u, T, None, None, pick(0.01, 1e-20, 1e-44), rows)
+    check(x, u, T, None, pick(0.9, 0.999), pick(0.01, 1e-20, 1e-44), rows)
+    assert check(x, u, T, None, None, None, rows)[2] == [V] * n
