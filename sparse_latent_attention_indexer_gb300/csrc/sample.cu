@@ -162,6 +162,8 @@ __device__ __forceinline__ bool exponent(float top, float l, float ch, float cl,
     yl = fmaf(d, cl, fmaf(e, ch, fmaf(d, ch, -yh)));
     return d < INFINITY && yh < 46.0f;
 }
+// Whether 2^-y is at least min_p, 2^-f (above fp32's range y is infinite, or not a number).
+__device__ __forceinline__ bool passes(float yh, float yl, float fh, float fl) { return (yh - fh) + (yl - fl) <= 0.0f; }
 // 2^-y in steps of 2^-45, y = yh + yl in [0, 46].  With k = round(512 yh), k = 512 n + j, and what is left, r (exact)
 // and yl, 2^-y = 2^-n 2^-(j/512) (1 - p + p^2/2 - p^3/6), p = (r + yl) ln 2 < 2^-10.5; every term is kept to 2^-41 or
 // better: the two large ones as integers on grids of 2^-24 and 2^-32, the rest, below 2^-18, on one of 2^-40.
@@ -562,11 +564,11 @@ __device__ void finish_few(const SampleParams &P, const Part &R, Shared &S, int6
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
+        yh[e] = yl[e] = 0.0f;
+        // what weighs nothing keeps its exponent, which a min-p below 2^-46 may let pass
         const bool some = by_index[e] != NONE && exponent(R.top, logit_of(by_index[e]), R.ch, R.cl, yh[e], yl[e]);
-        if (!some) yh[e] = yl[e] = 0.0f;
-        w[e] = some ? weight(yh[e], yl[e], S.root) : 0;
-        // min-p after the others: a token that it drops counts towards their sums
-        if (!some && by_index[e] != NONE) yh[e] = INFINITY;
+        w[e] = weight(some ? yh[e] : 0.0f, some ? yl[e] : 0.0f, S.root);
+        if (!some) w[e] = 0;
     }
     if constexpr (E > 1) {
         if (k > 0 && k < n) bound = select_few<E, false>(R, S, by_index, w, NONE, n, (u64)k);
@@ -586,7 +588,8 @@ __device__ void finish_few(const SampleParams &P, const Part &R, Shared &S, int6
     mine = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const bool in = by_index[e] <= bound && by_index[e] != NONE && (!(m > 0.0f) || (yh[e] - S.yh) + (yl[e] - S.yl) <= 0.0f);
+        // min-p after the others: a token that it drops counts towards their sums
+        const bool in = by_index[e] <= bound && by_index[e] != NONE && (!(m > 0.0f) || passes(yh[e], yl[e], S.yh, S.yl));
         if (!in) w[e] = 0;
         kept += in;
         mine += w[e];
@@ -1075,7 +1078,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
             const float l = R.at(i);
             kept = l > -INFINITY && (bound == NONE || order_of(l, R.first + i) <= bound);
             const bool some = exponent(R.top, l, R.ch, R.cl, yh, yl);
-            if (by_m && !(some ? (yh - fh) + (yl - fl) <= 0.0f : yh <= fh)) kept = false;
+            if (by_m && !passes(yh, yl, fh, fl)) kept = false;
             return kept && some ? weight(yh, yl, S.root) : 0;
         };
         if (list && !by_few) {

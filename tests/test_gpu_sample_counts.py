@@ -86,3 +86,22 @@ def test_masks_of_finite_numbers(n, V, dt):
     check(x, u, T, None, None, pick(0.01, 1e-20, 1e-44), rows)
     check(x, u, T, None, pick(0.9, 0.999), pick(0.01, 1e-20, 1e-44), rows)
     assert check(x, u, T, None, None, None, rows)[2] == [V] * n
+
+
+@pytest.mark.parametrize("V", [200, 1500, 20011, 131072])
+def test_min_p_below_every_weight_that_counts(V):
+    """min_p below 2^-46, where weights are too small to be drawn: their tokens are counted all the same, however many
+    candidates there are."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    n = 16
+    x = -90 * torch.rand(n, V, generator=g, device="cuda")
+    x[::2] -= 300  # most of the row far below its highest token
+    x[:, 7] = 1.0
+    x[::2, 50:150] = -60 * torch.rand(8, 100, generator=g, device="cuda")
+    u = torch.rand(n, generator=g, device="cuda").tolist()
+    m = [[1e-13, 2e-14, 1e-14, 1e-16, 1e-20, 1e-25, 1e-30, 1e-37][i // 2] for i in range(n)]
+    T = [[1.0, 0.75][i % 2] for i in range(n)]
+    check(x, u, T, None, None, m)
+    for k in (20, 120, 700, 5000):
+        check(x, u, T, [k] * n, None, m)
+    check(x, u, T, None, [0.9999] * n, m)
