@@ -146,11 +146,11 @@ __device__ __forceinline__ void load_gain(const float *p, int d, int D, float (&
     }
 }
 
-// A bf16 gate needs no more than 2^-20: full division and exponential were half of the time of a gated row.
-template <typename T>
+// Where nothing is stored in more than bf16 (2^-8), the quick exponential's 2^-16 and better do; an fp32 h' or y has all digits of
+// expf.  The quotient is good to 2 units in the last place.
+template <bool FP32>
 __device__ __forceinline__ float sigmoid(float v) {
-    if (sizeof(T) == 4) return __fdividef(1.0f, 1.0f + expf(-v));  // to 2 units in the last place
-    return __fdividef(1.0f, 1.0f + __expf(-v));
+    return __fdividef(1.0f, 1.0f + (FP32 ? expf(-v) : __expf(-v)));
 }
 
 // Sum over the row's threads, the same in each.  `part` takes a value a warp and is used by no other sum.
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
 #pragma unroll
                     for (int e = 0; e < W; ++e) {
                         if (P.gate_act != DSA_ACT_NONE) {
-                            const float s = sigmoid<TX>(a[e]);
+                            const float s = sigmoid<sizeof(TH) == 4 || sizeof(TX) == 4>(a[e]);
                             a[e] = P.gate_act == DSA_ACT_SILU ? a[e] * s : s;
                         }
                         v[j][e] *= a[e];

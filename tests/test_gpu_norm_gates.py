@@ -1,4 +1,4 @@
-"""Gates of the norms around a block that share memory with what they gate."""
+"""Gates of the norms around a block: their digits, and gates that share memory with what they gate."""
 import pytest
 import torch
 
@@ -31,3 +31,19 @@ def test_gate_that_is_the_block_output(N, D, h_dt, x_dt):
         got, _ = dsa.dsa_block_norm(h, u=one, gate=one)
         want = h.double() + one.double() ** 2
         assert float(((got.double() - want).abs() - R.U[h_dt] * want.abs() - 2.0 ** -23 * (h.double().abs() + one.double() ** 2)).max()) <= 0
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("x_dt", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 1000, 2049, 4096, 7168, 16384])
+def test_gates_of_an_fp32_stream(D, x_dt, act):
+    """h' = gate alone, in fp32 whatever the gate's type: expf is good to 1 unit of 2^-23, 1 + e to a rounding, the quotient to 2
+    units, silu's product, u's and the sum round once each: 3.5 + 1.5 units at most."""
+    gate = torch.linspace(-80, 80, 7 * D, device="cuda").reshape(7, D).to(x_dt)
+    h, u = torch.zeros(7, D, device="cuda"), torch.ones(7, D, dtype=x_dt, device="cuda")
+    for g in (gate, gate[3:4]):
+        got = dsa.dsa_block_norm(h, u=u, gate=g, gate_act=act, want_y=False)[0]
+        want = R.act(g.double(), act)
+        over = (got.double() - want).abs() / want.abs().clamp(min=2.0 ** -110)
+        assert got.dtype == F32 and got.shape == h.shape
+        assert float(over.max()) <= 5 * 2.0 ** -23, f"{float(over.max()) * 2 ** 23:.1f} units"
