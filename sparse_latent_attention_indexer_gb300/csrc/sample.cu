@@ -252,9 +252,9 @@ struct Row {
         return CACHED || !infinite ? l : l == INFINITY ? 0.0f : -INFINITY;
     }
     // Bins fall with the logit; equal logits have equal ones.  A token is in bin b or before: x < b + 1.  The last bin takes all that
-    // is further down, a mask of the type's lowest number too, whose product is infinite; -inf and NaN get there and are no tokens.
-    __device__ __forceinline__ float x(float l) const { return fminf((top - l) * bins, (float)(BINS - 1)); }
-    __device__ __forceinline__ int bin(float l) const { return (int)x(l); }
+    // is further down, a mask of the type's lowest number too, whose product is infinite like that of -inf, which is no token.
+    __device__ __forceinline__ float x(float l) const { return (top - l) * bins; }
+    __device__ __forceinline__ int bin(float l) const { return (int)fminf(x(l), (float)(BINS - 1)); }
 };
 
 // Sum of v over the threads up to this one, and over all.
@@ -471,7 +471,8 @@ __device__ void sort_few(Shared &S, u64 (&c)[E], int n) {
 }
 
 // Among one CTA's candidates (E a thread, at most `bound`): the last token of the shortest run whose count (or weight w) reaches
-// the target, which all of them together have to reach.  A histogram finds its bin, the bin's few tokens are sorted; many in one bin: all are.
+// the target, which all of them together have to reach.  A histogram finds its bin, the bin's few tokens are sorted; many in one
+// bin: all are.
 template <int E, bool WEIGHT, typename Part>
 __device__ u64 select_few(const Part &R, Shared &S, const u64 (&c)[E], const u64 (&w)[E], u64 bound, int n, u64 target) {
     const int tid = threadIdx.x;
@@ -785,7 +786,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     // this warp's go among them.
     const auto list_up_to = [&](int to, int most, int &listed, int &before) -> int {
         listed = 0;
-        const float xt = (float)to + 1.0f;
+        // up to the last bin lie all tokens: -l < INFINITY
+        const bool last = to == BINS - 1;
+        const float top = last ? 0.0f : R.top, bins = last ? 1.0f : R.bins, xt = last ? INFINITY : (float)to + 1.0f;
 #pragma unroll 1
         for (int i0 = w0; i0 < w1; i0 += 256) {
             float l[8];
@@ -793,7 +796,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
 #pragma unroll
             for (int e = 0; e < 8; ++e) l[e] = i0 + e * 32 + lane < w1 ? R.at(i0 + e * 32 + lane) : -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) hit[e] = __ballot_sync(0xffffffffu, l[e] > -INFINITY && R.x(l[e]) < xt);
+            for (int e = 0; e < 8; ++e) hit[e] = __ballot_sync(0xffffffffu, (top - l[e]) * bins < xt);  // false for -inf and NaN
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (hit[e] == 0) continue;
@@ -928,7 +931,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
 #pragma unroll 4
             for (int i = tid; i < R.n; i += THREADS) {
                 const float l = R.at(i), x = R.x(l);
-                if (x >= (float)(BINS - 1)) continue;
+                if (!(l > -INFINITY) || x >= (float)(BINS - 1)) continue;
                 const int b = (int)x;
                 atomicAdd(&S.rough[b], (unsigned)fmaf(steps, tc::ex2_approx(((float)b - x) * (LOG2E / PER_NAT)), 0.5f));
             }
@@ -972,7 +975,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
         bool by_few = false;
         const bool weigh = !by_k && (by_p || !by_m), list = to < BINS;
         if (weigh) {
-            const float xf = (float)from, xt = (float)to + 1.0f;
+            // a token beyond the last bin's finite products weighs nothing: no run by top-p ends there
+            const float xf = (float)from, xt = to >= BINS - 1 ? INFINITY : (float)to + 1.0f;
 #pragma unroll 1
             for (int i0 = w0; i0 < w1; i0 += 128) {
                 float l[4];
@@ -991,13 +995,13 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float x = R.x(l[e]);
+                    const float x = R.x(l[e]);  // -inf and NaN are in no bin
                     w_all += w[e];
                     if (x < xf) {
                         w_sure += w[e];
                         ++sure;
                     }
-                    const unsigned hit = __ballot_sync(0xffffffffu, l[e] > -INFINITY && x >= xf && x < xt);
+                    const unsigned hit = __ballot_sync(0xffffffffu, x >= xf && x < xt);
                     if (hit == 0) continue;
                     const int at = listed + __popc(hit & ((1u << lane) - 1));
                     if ((hit >> lane & 1) && at < LIST) S.list[warp][at] = order_of(l[e], R.first + i0 + e * 32 + lane);
