@@ -653,6 +653,8 @@ int dsa_block_norm(const dsa_block_norm_args *args, void *stream);
  * Sums are of whole numbers: weights in steps of 2^-45, each off by less than 2^-40 of
  * itself and half a step, so that the order of summation is nothing and the same inputs
  * give the same token.  The logits' differences count as far as fp32 holds them.
+ * A row whose logits have not arrived within the wait limit (dsa_check_device_error tells)
+ * gives what a row without a token gives.
  * Errors: DSA_ERR_INVALID_ARG (null pointer, R < 0, V < 1, an address off its element),
  * DSA_ERR_UNSUPPORTED (dtype, V > 262144), DSA_ERR_CUDA. */
 int dsa_sample(const void *logits, int64_t ld, int dtype, int R, int V, const float *u, const float *temperature,
@@ -684,9 +686,9 @@ int dsa_check_device_error(void *stream, int *site);
  * for a limit out of range. */
 int dsa_selftest_bounded_wait(int64_t limit_cycles, int *completed_ok, void *stream);
 /* Wait limit of the tensor-core kernels (no counterpart on the pages: a
- * diagnostic of this library).  Every wait of the indexer, absorption and
- * attention kernels on a barrier phase gives up after this many SM clock cycles
- * (default, and `cycles` = 0: 2^32, about two seconds), records its site in the
+ * diagnostic of this library).  Every wait of the indexer, absorption,
+ * attention, product and sampling kernels on a barrier phase gives up after this
+ * many SM clock cycles (default, and `cycles` = 0: 2^32, about two seconds), records its site in the
  * device error word, and the CTA drains its copies and MMAs already in flight
  * (those drain waits keep the default limit), frees its tensor memory and exits.
  * A short limit makes the failure path of the production kernels run without a

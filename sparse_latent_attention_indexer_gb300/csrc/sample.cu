@@ -60,6 +60,7 @@ struct SampleParams {
     const int32_t *top_k;
     int32_t *token, *kept;
     float *logprob;
+    long long wait_limit;
 };
 
 // 2^(-j/512) as pairs of fp32 values, from the nine roots of two that make up an exponent of nine bits.
@@ -100,7 +101,7 @@ struct alignas(16) Shared {
     int pick_bin, pick_to;
     float ch, cl, yh, yl;        // log2(e) / T, -log2(min_p)
     uint64_t arrived;
-    int abort_word;
+    int abort_word, never;
 };
 
 // Every thread of the cluster, with what they have written to shared memory; and the same in two halves.
@@ -638,7 +639,7 @@ __device__ T *fetch_slice(Shared &S, uint8_t *room, const T *src, int n, bool &c
     coming = body > 0;
     if (threadIdx.x == 0) {
         tc::mbar_init(&S.arrived, 1);
-        S.abort_word = 0;
+        S.abort_word = S.never = 0;
         tc::fence_mbar_init();
         if (body) {
             tc::mbar_arrive_expect_tx(&S.arrived, body);
@@ -654,6 +655,22 @@ __device__ T *fetch_slice(Shared &S, uint8_t *room, const T *src, int n, bool &c
         if (i < n - tail) raw[tail + i] = src[tail + i];
     }
     return raw;
+}
+
+// Waits for the CTA's bulk copy.  The phase is polled, not waited for by the hardware, whose patience is longer than a copy takes:
+// so a limit that is set counts.
+__device__ __forceinline__ bool wait_copy(Shared &S, volatile int *abort_flag, int site, long long limit) {
+    if (tc::mbar_test(&S.arrived, 0)) return true;
+    const long long t0 = clock64();
+    while (!tc::mbar_test(&S.arrived, 0)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > limit) {
+            atomicCAS(&g_sample_error, 0, site);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // This thread's maximum over its share of a CTA's logits, 16 bytes at a time: 64 KB of the CTA are on their way at once.
@@ -760,7 +777,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     for (int j = tid; j < 512; j += THREADS) S.root[j] = kRoots.at[j];
     if (tid == 0) S.first = MAX_V;
     __syncthreads();
-    if (coming) tc::mbar_wait(&S.arrived, 0, (volatile int *)&S.abort_word, &g_sample_error, 71);
+    if (coming) wait_copy(S, &S.abort_word, 71, P.wait_limit);
     const int per = ((R.n + WARPS - 1) / WARPS + 31) / 32 * 32;  // a warp's tokens follow one another
     const int w0 = min(R.n, warp * per), w1 = min(R.n, w0 + per);
     R.bins = PER_NAT / T_;
@@ -781,6 +798,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
         R.top = logit_of(b << INDEX_BITS);  // the CTA's
     }
     const float own_top = R.top;
+    // A wait that ran out (the barrier above has shown it to every thread): the CTA's maximum is no number, which tells the cluster
+    // when it meets; until then what lies in shared memory is taken as it is.
+    bool lost = false;
+    if constexpr (CACHED)
+        if (*(volatile int *)&S.abort_word) R.top = NAN;
 
     // The tokens of the bins up to `to` (no more than `most` of them, or the answer is above FEW), in S.list by warp; and where
     // this warp's go among them.
@@ -855,10 +877,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
         int total = 0;
 #pragma unroll 1
         for (int r = 0; r < P.share; ++r) {
+            lost |= isnan(S.in_top[r]);
             R.top = fmaxf(R.top, S.in_top[r]);
             total = max(total, S.in_alone[r]);
         }
-        if (total <= region && R.top > -INFINITY) {
+        if (total <= region && R.top > -INFINITY && !lost) {
             if (rank != 0) return;
             n_few = 0;
 #pragma unroll 1
@@ -870,7 +893,19 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
         if (tid < P.share) push(&S.in_top[rank], tid, R.top);
         meet();
 #pragma unroll 1
-        for (int r = 0; r < P.share; ++r) R.top = fmaxf(R.top, S.in_top[r]);
+        for (int r = 0; r < P.share; ++r) {
+            lost |= isnan(S.in_top[r]);
+            R.top = fmaxf(R.top, S.in_top[r]);
+        }
+    }
+    if (CACHED && lost) {  // the same in every thread of the cluster: the row has no token
+        if (coming) wait_copy(S, &S.never, 72, tc::kWaitLimitCycles);  // nothing may still be landing when the CTA leaves
+        if (rank == 0 && tid == 0) {
+            P.token[row] = -1;
+            if (P.logprob) P.logprob[row] = -INFINITY;
+            if (P.kept) P.kept[row] = 0;
+        }
+        return;
     }
 
     if (n_few < 0) {
@@ -1234,6 +1269,7 @@ extern "C" int dsa_sample(const void *logits, int64_t ld, int dtype, int R, int 
     P.token = token;
     P.logprob = logprob;
     P.kept = kept;
+    P.wait_limit = wait_limit_cycles();
     const cudaStream_t s = (cudaStream_t)stream;
     const cudaError_t e = dtype == DSA_F32 ? cached ? launch<float, true>(P, R, s) : launch<float, false>(P, R, s)
                           : cached ? launch<__nv_bfloat16, true>(P, R, s) : launch<__nv_bfloat16, false>(P, R, s);
