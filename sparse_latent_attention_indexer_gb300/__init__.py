@@ -737,7 +737,7 @@ def _wrong(fn: str, name: str, t, dev: int, shape, dtype):
 
 def _matrix(fn: str, name: str, t, dev: int, shape, dtype) -> int:
     """The row stride of a tensor of this shape (2-D) and type with contiguous rows on the device."""
-    if t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
         raise _wrong(fn, name, t, dev, shape, dtype)
     ld, one = t.stride()
     if one != 1 and shape[1] > 1:
@@ -749,13 +749,23 @@ def _vector(fn: str, name: str, t, dev: int, shape, dtype):
     """The address of a contiguous tensor of this shape (1-D) and type, or None."""
     if t is None:
         return None
-    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape or
+            not t.is_contiguous()):
         raise _wrong(fn, name, t, dev, shape, dtype)
     return t.data_ptr()
 
 
+def _tensors(fn: str, **named):
+    """Refuses what is neither a tensor nor None, before anything is asked of it."""
+    for name, t in named.items():
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise _wrong(fn, name, t, -1, None, None)
+
+
 def _first_of(fn: str, name: str, t, dims: int) -> int:
     """The device of a call's first tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise _wrong(fn, name, t, -1, None, None)
     dev = t.get_device()
     if dev < 0:
         raise _wrong(fn, name, t, dev, t.shape, t.dtype)
@@ -773,6 +783,7 @@ def _int_sizes(fn: str, *sizes: int):
 def dsa_linear_workspace_size(x: torch.Tensor, weight: torch.Tensor) -> int:
     fn = "dsa_linear_workspace_size"
     dev = _first_of(fn, "x", x, 2)
+    _first_of(fn, "weight", weight, 2)
     (M, K), N = x.shape, weight.shape[0]
     _int_sizes(fn, M, N, K)
     return _abi.load().dsa_linear_workspace_size(x.data_ptr(), _matrix(fn, "x", x, dev, (M, K), x.dtype),
@@ -788,6 +799,8 @@ def dsa_linear(x, weight, bias=None, act=None, residual=None, y=None, dtype=None
     if act not in _ACTS:
         raise ValueError(f"{fn}: act must be 'relu', 'silu', 'gelu', 'gelu_tanh' or None, not {act!r}")
     dev = _first_of(fn, "x", x, 2)
+    _first_of(fn, "weight", weight, 2)
+    _tensors(fn, residual=residual, y=y, workspace=workspace)
     M, K = x.shape
     N = weight.shape[0]
     _int_sizes(fn, M, N, K)
@@ -841,6 +854,10 @@ def dsa_block_norm(h, pre: Norm | None = None, u=None, post: Norm | None = None,
     if gate_act not in _GATES:
         raise ValueError(f"{fn}: gate_act must be 'sigmoid', 'silu' or None, not {gate_act!r}")
     dev = _first_of(fn, "h", h, 2)
+    _tensors(fn, u=u, gate=gate, y=y)
+    for name, norm in (("post", post), ("pre", pre)):
+        if norm is not None and not isinstance(norm, Norm):
+            raise TypeError(f"{fn}: {name} must be a Norm, not {type(norm).__name__}")
     N, D = shape = h.shape
     _int_sizes(fn, D)
     h_dtype = h.dtype
