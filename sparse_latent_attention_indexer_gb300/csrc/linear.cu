@@ -1161,8 +1161,8 @@ extern "C" int dsa_linear(const void *x, int64_t ld_x, const void *W, int64_t ld
     }
     const int64_t rows_x = M > 1 ? ld_x : up(K, 8), rows_w = N > 1 ? ld_w : up(K, 8);
     const void *xs = p.lay_x ? workspace : x;
-    for (int n0 = 0; n0 < N; n0 += p.chunk) {
-        const int n = std::min(p.chunk, N - n0);
+    for (int64_t n0 = 0; n0 < N; n0 += p.chunk) {  // (the sum behind the last part may pass 32 bits)
+        const int n = (int)std::min<int64_t>(p.chunk, N - n0);
         const void *ws = W;
         Layout L{};
         if (p.lay_x && n0 == 0) {
@@ -1173,7 +1173,7 @@ extern "C" int dsa_linear(const void *x, int64_t ld_x, const void *W, int64_t ld
         }
         if (p.lay_w) {
             ws = (char *)workspace + p.x_bytes;
-            L.src[1] = (const char *)W + (int64_t)n0 * ld_w * (dtype == DSA_F32 ? 4 : 2);
+            L.src[1] = (const char *)W + n0 * ld_w * (dtype == DSA_F32 ? 4 : 2);
             L.ld[1] = ld_w;
             L.rows[1] = n;
             L.dst[1] = (__nv_bfloat16 *)ws;
