@@ -994,7 +994,7 @@ Cut cut(int M, int N, int total, bool exact, int src, int sms) {
     Cut best{MAX_BT, 1, 1};
     double least = 1e30;
     for (int tt = least_tt; tt < least_tt + 8; ++tt) {
-        const int bt = (int)up((M + tt - 1) / tt, 16);
+        const int bt = (int)up(((int64_t)M + tt - 1) / tt, 16);
         const int64_t tiles = (M + bt - 1) / bt * ft;
         const double smem = src == ROWS ? 2 * (W_SLAB + 128.0 * bt) / 128 : src == PLANES ? 768 + 9.0 * bt : 1600 + 16.0 * bt;
         const double hbm = (double)ft * total * W_SLAB * (src == ROWS ? 1 : src == PLANES ? 3 : 2) / 3550;

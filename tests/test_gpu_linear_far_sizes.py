@@ -26,3 +26,12 @@ def test_features_up_to_2_31():
     y = dsa.dsa_linear(x, w)
     assert dsa.last_kernels() == {"linear", "linear_layout"}
     assert same(y, x, w)
+
+
+def test_tokens_up_to_2_31():
+    """More tokens than their number and that of their tiles add up to in 32 bits."""
+    x = torch.randint(-512, 513, (FAR, 1), dtype=torch.int16, device="cuda").bfloat16()
+    w = torch.randn(5, 1, device="cuda").bfloat16()
+    y = dsa.dsa_linear(x, w)
+    assert dsa.last_kernels() == {"linear", "linear_layout"}
+    assert same(y, x, w)
