@@ -737,9 +737,12 @@ def _wrong(fn: str, name: str, t, dev: int, shape, dtype):
 
 def _matrix(fn: str, name: str, t, dev: int, shape, dtype) -> int:
     """The row stride of a tensor of this shape (2-D) and type with contiguous rows on the device."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
-        raise _wrong(fn, name, t, dev, shape, dtype)
-    ld, one = t.stride()
+    try:
+        if t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+            raise _wrong(fn, name, t, dev, shape, dtype)
+        ld, one = t.stride()
+    except AttributeError:
+        raise _wrong(fn, name, t, dev, shape, dtype) from None
     if one != 1 and shape[1] > 1:
         raise _wrong(fn, name, t, dev, shape, dtype)
     return ld if shape[0] > 1 else shape[1]
@@ -749,17 +752,18 @@ def _vector(fn: str, name: str, t, dev: int, shape, dtype):
     """The address of a contiguous tensor of this shape (1-D) and type, or None."""
     if t is None:
         return None
-    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape or
-            not t.is_contiguous()):
-        raise _wrong(fn, name, t, dev, shape, dtype)
-    return t.data_ptr()
+    try:
+        if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise _wrong(fn, name, t, dev, shape, dtype)
+        return t.data_ptr()
+    except AttributeError:
+        raise _wrong(fn, name, t, dev, shape, dtype) from None
 
 
-def _tensors(fn: str, **named):
-    """Refuses what is neither a tensor nor None, before anything is asked of it."""
-    for name, t in named.items():
-        if t is not None and not isinstance(t, torch.Tensor):
-            raise _wrong(fn, name, t, -1, None, None)
+def _not_a_tensor(fn: str, **named):
+    """The first of these that is neither a tensor nor None, in words."""
+    return next(_wrong(fn, name, t, -1, None, None) for name, t in named.items()
+                if t is not None and not isinstance(t, torch.Tensor))
 
 
 def _first_of(fn: str, name: str, t, dims: int) -> int:
@@ -799,20 +803,27 @@ def dsa_linear(x, weight, bias=None, act=None, residual=None, y=None, dtype=None
     if act not in _ACTS:
         raise ValueError(f"{fn}: act must be 'relu', 'silu', 'gelu', 'gelu_tanh' or None, not {act!r}")
     dev = _first_of(fn, "x", x, 2)
-    _first_of(fn, "weight", weight, 2)
-    _tensors(fn, residual=residual, y=y, workspace=workspace)
     M, K = x.shape
-    N = weight.shape[0]
+    try:
+        N, _ = weight.shape
+    except (AttributeError, ValueError):
+        _first_of(fn, "weight", weight, 2)
+        raise
     _int_sizes(fn, M, N, K)
     x_dtype = x.dtype
     ld_x, ld_w = _matrix(fn, "x", x, dev, (M, K), x_dtype), _matrix(fn, "weight", weight, dev, (N, K), x_dtype)
     if dtype is None:
-        dtype = (y if y is not None else residual if residual is not None else x).dtype
+        try:
+            dtype = (y if y is not None else residual if residual is not None else x).dtype
+        except AttributeError:
+            raise _not_a_tensor(fn, y=y, residual=residual) from None
     dt, y_dt = _dt_of(x_dtype), _dt_of(dtype)
     ld_r = 0 if residual is None else _matrix(fn, "residual", residual, dev, (M, N), dtype)
     ld_y = N if y is None else _matrix(fn, "y", y, dev, (M, N), dtype)
     bias_ = _vector(fn, "bias", bias, dev, (N,), torch.float32)
     if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise _not_a_tensor(fn, workspace=workspace)
         _vector(fn, "workspace", workspace, dev, (workspace.numel(),), torch.uint8)
     lib = _abi.load()
     px, pw = x.data_ptr(), weight.data_ptr()
@@ -854,21 +865,20 @@ def dsa_block_norm(h, pre: Norm | None = None, u=None, post: Norm | None = None,
     if gate_act not in _GATES:
         raise ValueError(f"{fn}: gate_act must be 'sigmoid', 'silu' or None, not {gate_act!r}")
     dev = _first_of(fn, "h", h, 2)
-    _tensors(fn, u=u, gate=gate, y=y)
-    for name, norm in (("post", post), ("pre", pre)):
-        if norm is not None and not isinstance(norm, Norm):
-            raise TypeError(f"{fn}: {name} must be a Norm, not {type(norm).__name__}")
     N, D = shape = h.shape
     _int_sizes(fn, D)
     h_dtype = h.dtype
-    x_dtype = next((t.dtype for t in (u, gate, y) if t is not None), dtype or h_dtype)
+    try:
+        x_dtype = next((t.dtype for t in (u, gate, y) if t is not None), dtype or h_dtype)
+    except AttributeError:
+        raise _not_a_tensor(fn, u=u, gate=gate, y=y) from None
     if dtype is not None and dtype != x_dtype:
         raise ValueError(f"{fn}: dtype is {dtype} beside {x_dtype} tensors")
     ld_h = _matrix(fn, "h", h, dev, shape, h_dtype)
     ld_u = 0 if u is None else _matrix(fn, "u", u, dev, shape, x_dtype)
     ld_g, ld_ho, ld_y = 0, D, D
     if gate is not None:
-        if N > 1 and gate.shape == (1, D):
+        if N > 1 and getattr(gate, "shape", None) == (1, D):
             _matrix(fn, "gate", gate, dev, (1, D), x_dtype)
         else:
             ld_g = _matrix(fn, "gate", gate, dev, shape, x_dtype)
@@ -876,6 +886,9 @@ def dsa_block_norm(h, pre: Norm | None = None, u=None, post: Norm | None = None,
         ld_ho = _matrix(fn, "h_out", h_out, dev, shape, h_dtype)
     if y is not None:
         ld_y = _matrix(fn, "y", y, dev, shape, x_dtype)
+    for name, norm in (("post", post), ("pre", pre)):
+        if norm is not None and not isinstance(norm, Norm):
+            raise TypeError(f"{fn}: {name} must be a Norm, not {type(norm).__name__}")
     post_ = (0, 0, 0) if post is None else post._struct(fn, "post", dev, D)
     pre_ = (0, 0, 0) if pre is None else pre._struct(fn, "pre", dev, D)
     h_dt, x_dt = _dt_of(h_dtype), _dt_of(x_dtype)
