@@ -212,6 +212,22 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
 }
 
 __device__ __forceinline__ void tile_of(const LinearParams &P, int u, int &m0, int &f0) {
+// The epilogue's wait for an accumulator.  A limit that is set is polled for: the hardware's own patience is longer than a part of
+// a sum takes, so that no limit would run out.
+__device__ __forceinline__ bool wait_sum(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err, int site, long long limit) {
+    if (limit >= tc::kWaitLimitCycles) return tc::mbar_wait(bar, parity, abort_flag, err, site);
+    const long long t0 = clock64();
+    while (!tc::mbar_test(bar, parity)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > limit) {
+            atomicCAS(err, 0, site);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
     const int ft = (P.N + BF - 1) / BF, per_group = GROUP_T * ft;
     const int grp = u / per_group, r = u - grp * per_group;
     const int gt = min(GROUP_T, P.tt - grp * GROUP_T);
@@ -516,7 +532,7 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && SRC == ROWS ? 
             float sum[SUMS][32];
             // EXACT: takes the next part over from tensor memory, where all warps are sound.
             const auto drain = [&](bool sound) -> bool {
-                if (!epi_and(sound && tc::mbar_wait(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit))) return false;
+                if (!epi_and(sound && wait_sum(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit))) return false;
                 tc::tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < SUMS; ++j)
@@ -629,7 +645,7 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && SRC == ROWS ? 
                 for (int j = 0; j < SUMS; ++j)
                     if (j * 64 + g * 32 < tokens) put(j * 64 + g * 32, sum[j]);
             } else {
-                ok = epi_and(ok && tc::mbar_wait(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit));
+                ok = epi_and(ok && wait_sum(&tfull[n & 1], (n >> 1) & 1, abort_flag, err, 66, P.wait_limit));
                 if (!ok) break;
                 tc::tc_fence_after();
                 for (int c = g * 32; c < tokens; c += 64) {
