@@ -211,7 +211,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
     return true;
 }
 
-__device__ __forceinline__ void tile_of(const LinearParams &P, int u, int &m0, int &f0) {
 // The epilogue's wait for an accumulator.  A limit that is set is polled for: the hardware's own patience is longer than a part of
 // a sum takes, so that no limit would run out.
 __device__ __forceinline__ bool wait_sum(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err, int site, long long limit) {
@@ -228,6 +227,7 @@ __device__ __forceinline__ bool wait_sum(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 
+__device__ __forceinline__ void tile_of(const LinearParams &P, int u, int &m0, int &f0) {
     const int ft = (P.N + BF - 1) / BF, per_group = GROUP_T * ft;
     const int grp = u / per_group, r = u - grp * per_group;
     const int gt = min(GROUP_T, P.tt - grp * GROUP_T);
