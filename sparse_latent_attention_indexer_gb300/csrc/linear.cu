@@ -18,7 +18,8 @@
 // The tensor cores cut off what does not fit a running sum of 24 bits, step by step: over 448 steps
 // of 16 products (K = 7168) an fp32 result was off by 7.9e-6 of the whole, ten times what fp32
 // arithmetic loses.  Where y is fp32 (EXACT) the epilogue takes the sum over after every 8 slabs
-// (32 steps; fp32 layers: 4) and adds these parts to nearest in its registers.
+// (32 steps; fp32 layers: 4) and adds these parts to nearest in its registers: 4.7e-7 of the whole (fp32 layers 2.4e-7) at any K.
+// A sum of one part is as it was cut off: over K = 512 in bf16 4.7e-7, where fp32 arithmetic loses 1.6e-7.
 //
 // fp32 layers run on the same kernel: a value is the sum of three bf16 terms of 8 bits each (planes),
 // and of the nine products of terms the six above 2^-24 of the whole are added.  A stage holds
@@ -31,8 +32,8 @@
 //
 // Bound by HBM with few tokens (17 tokens, 7168 to 131,072, fp32 out: 267 to 272 us, 1.02 of the measured copy
 // rate; 64 tokens, 16384 to 7168: 43 us, 0.81, the rest being the start and the end of a tile), by shared memory with
-// many (4096 tokens, 16384 to 7168: 535 us, 1.80 PFLOP/s or 0.94 of the measured peak: a slab is written once and
-// read by the MMAs once, 96 KB in 730 cycles of which the MMAs need 512).
+// many (4096 tokens, 16384 to 7168: 535 us by itself, 1.80 PFLOP/s or 0.94 of the measured peak, and 593 to 609 call after call, when
+// power limits it: a slab is written once and read by the MMAs once, 96 KB in 730 cycles of which the MMAs need 512).
 #include <atomic>
 #include <type_traits>
 
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(NUM_THREADS, SPLIT && !EXACT && SRC == ROWS ? 
                                 store1(P.e, row0 + j, f0 + e * 32 + lane, mine_turn[(q * 8 + j) * BF + e * 32 + lane]);
                 } else {
                     // residuals before the first store, which no load passes: one after the other took 4096 tokens, 2048 to 7166,
-                    // 328 us instead of 183, and 7966, 810 to 26446 in fp32, 2799 instead of 700 to 725
+                    // 328 us instead of 183, and 7966, 810 to 26446, bf16 with residual and y in fp32, 2799 instead of 700 to 725
 #pragma unroll
                     for (int h = 0; h < 8; h += 4) {
                         if (EXACT)
@@ -919,8 +920,9 @@ Plan plan(const void *x, int64_t ld_x, const void *W, int64_t ld_w, int dtype, i
     p.src = f32 ? PLANES : ROWS;
     // RAW: of a large W, read once: 64 tokens, 7168 to 7168, 81 us and laid out 141 (17 tokens 73 and 134); 4096 to 2048 22 and 23,
     // 4096 to 1024 19 and 17, 16384 to 512 45 and 32; 80 tokens, two tiles, 138 and 140.  Of little work, for one launch and no
-    // workspace, which are 8 us of the host's time: 500 tokens, 1536 to 260, 15 and 12 us on the GPU; 128, 2048 to 1024, 17
-    // and 14; but 64, 7168 to 256, 22 and 15
+    // workspace, which are 8 us of the host's time (a call of 500 tokens, 1536 to 260, 25 -> 17 us), although the GPU takes longer,
+    // which is what counts in a graph: 500 tokens, 1536 to 260, 15 and 12 us; 128, 2048 to 1024, 17 and 14; but 64, 7168 to
+    // 256, 22 and 15
     const bool large = M <= max_bt(true, RAW) && N >= 2048 && (int64_t)N * K >= 1 << 23;
     const bool little = K <= 4096 && (double)M * N * K <= 3e8;
     if (f32 && (large || little) && (uintptr_t)x % 16 == 0 && (uintptr_t)W % 16 == 0 && (M <= 1 || ld_x % 4 == 0) &&

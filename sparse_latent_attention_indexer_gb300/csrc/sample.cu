@@ -24,11 +24,12 @@
 // another way: histograms, of counts or exact weights, over ever narrower ranges of c until one
 // token is left; ties end in the index, so they need no rule of their own.
 //
-// Bound by latency for a row (131,072 logits: top-k 50 12 us, top-p 0.95 26 to 33, of which reading takes 2: meetings of
-// the cluster, barriers, code that runs once), by latency and instructions for many (256 rows: top-k 50 58 us, top-k 1000
-// 111, top-p 0.95 230 to 280, no rule 152; HBM 20).  An exact weight takes some 75 instructions, the rest of a pass 20.
+// Bound by latency for a row (131,072 logits in fp32, replayed in a graph: highest logit 5.5 us, top-k 50 11.5, top-k 1000 19,
+// top-p 0.95 32, no rule 16, of which reading takes 2: meetings of the cluster, barriers, code that runs once), by latency and
+// instructions for many (256 rows: highest logit 43 us, top-k 50 59, top-k 1000 119, top-p 0.95 277, no rule 152; HBM 20).  An
+// exact weight takes some 75 instructions, the rest of a pass 20.
 // A row's code runs once, between other kernels from cold caches: it is kept short (loops over CTAs and steps of sorting are not
-// unrolled, the end has one place), which took one row among other kernels from 28 to 18 us.
+// unrolled, the end has one place), which took one row (settings drawn), among other kernels, from 28 to 18 us.
 #include <algorithm>
 
 #include "dsa_common.cuh"
